@@ -495,6 +495,125 @@ forge_status forge_adamw(const void* dW, forge_dtype dw_dtype, void* W,
 forge_status forge_fp8_roll_scales(forge_fp8_scales* scales, int n, float headroom,
                                    forge_stream stream);
 
+/*
+ * The operators around a linear layer's weight gradient: the RMS norm whose
+ * output is the layer's X, 8-bit forms of the layer's other two products, and
+ * clipping by the global gradient norm.
+ *
+ * The 128-block e4m3 format.  A matrix [rows, cols] is stored as e4m3 codes
+ * [rows, cols] (one byte each, the OCP "fn" encoding) and fp32 scales; value =
+ * e4m3(code) * scale.  Activations and their gradients have one scale per row
+ * and 128 columns (block_rows 1, scales [rows, ceil(cols/128)]); weights one
+ * per 128 x 128 block (block_rows 128, scales [ceil(rows/128),
+ * ceil(cols/128)]).  The last blocks may be partial.  A block whose largest
+ * magnitude is a > 0 has scale max(a / 448, 2^-126) and codes x / scale
+ * rounded to nearest even; an all-zero block has scale 0 and codes 0; a block
+ * that holds a NaN or an infinity decodes to NaN throughout.
+ */
+
+/*
+ * forge_rmsnorm: the residual's addition, the RMS norm and its 8-bit output
+ * in one pass:
+ *   h = x + residual (h = x if residual is NULL), rstd = 1 / sqrt(mean(h^2) + eps),
+ *   y = h * rstd * gain, per row of `cols` columns, in fp32.
+ *   x, residual [rows, cols] bf16; gain [cols] fp32 or bf16.
+ *   Outputs, each written if not NULL: sum [rows, cols] = h rounded to bf16
+ *   (may be the same buffer as x or residual), y [rows, cols] bf16, codes and
+ *   scales (both or neither) = y in the 128-block format with block_rows 1,
+ *   quantised from the unrounded y, rstd [rows] fp32 (forge_rmsnorm_backward
+ *   reads it).  At least one of y and codes.
+ * cols is a multiple of 8, at most 32768; eps >= 0 (FORGE_ERR_HYPER).  rows =
+ * 0 does nothing.  Pointers 16-byte aligned; apart from sum no output may
+ * overlap an input or another output.  Asynchronous on `stream`.
+ */
+forge_status forge_rmsnorm(const void* x, const void* residual, const void* gain,
+                           forge_dtype gain_dtype, void* sum, void* y, void* codes, float* scales,
+                           float* rstd, int64_t rows, int64_t cols, float eps,
+                           forge_stream stream);
+
+/*
+ * forge_rmsnorm_backward: the gradients of forge_rmsnorm.  With xh = h * rstd
+ * and u = dY * gain, in fp32:
+ *   dX = rstd * (u - xh * mean(u * xh)) + dsum,   dgain = sum over rows of dY * xh.
+ *   dY [rows, cols] bf16; h [rows, cols] bf16 (the forward pass's sum, or x
+ *   without a residual); rstd [rows] fp32 from the forward pass; dsum [rows,
+ *   cols] bf16, the gradient that reaches the sum along the residual stream,
+ *   or NULL; dX [rows, cols] bf16, the gradient of x and of the residual (may
+ *   be the same buffer as dsum); dgain [cols] fp32, overwritten, or NULL.
+ * dgain needs `workspace` (device, 16-byte aligned) of at least
+ * forge_rmsnorm_backward_workspace_bytes(rows, cols) (FORGE_ERR_SHAPE if it is
+ * smaller); it must not be used by another call until this one has run.  The
+ * rows are added in a fixed order: the same result on every run.  rows = 0
+ * writes zeros to dgain.  Otherwise the checks of forge_rmsnorm.
+ */
+forge_status forge_rmsnorm_backward(const void* dY, const void* h, const void* gain,
+                                    forge_dtype gain_dtype, const float* rstd, const void* dsum,
+                                    void* dX, float* dgain, int64_t rows, int64_t cols,
+                                    void* workspace, size_t workspace_bytes, forge_stream stream);
+size_t forge_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t cols);
+
+/*
+ * forge_quantize_b128: x [rows, cols] bf16 in the 128-block format above,
+ * block_rows 1 or 128 (FORGE_ERR_FORMAT otherwise).  cols is a multiple of 8.
+ * rows = 0 does nothing.  Asynchronous on `stream`.
+ */
+forge_status forge_quantize_b128(const void* x, void* codes, float* scales, int64_t rows,
+                                 int64_t cols, int block_rows, forge_stream stream);
+
+/*
+ * forge_linear_fp8: Y = X W^T, and forge_dgrad_fp8: dX = dY W, on the 8-bit
+ * tensor cores.  X [bt, d_in] and dY [bt, d_out] are codes with block_rows 1,
+ * W [d_out, d_in] codes with block_rows 128 (the same stored weight for both).
+ * The products of each block of 128 are summed in the tensor core; the blocks'
+ * sums are scaled and added in fp32, and the result is rounded once to
+ * FORGE_DT_BF16 (or kept, FORGE_DT_FP32).  Y [bt, d_out], dX [bt, d_in].
+ * d_in and d_out are multiples of 16; pointers 16-byte aligned; the output
+ * must not overlap an input.  bt = 0 does nothing.  The result is the same on
+ * every run.  Nothing is allocated.  Asynchronous on `stream`.
+ */
+forge_status forge_linear_fp8(const void* X, const float* x_scales, const void* W,
+                              const float* w_scales, void* Y, forge_dtype y_dtype, int64_t bt,
+                              int64_t d_in, int64_t d_out, forge_stream stream);
+forge_status forge_dgrad_fp8(const void* dY, const float* dy_scales, const void* W,
+                             const float* w_scales, void* dX, forge_dtype dx_dtype, int64_t bt,
+                             int64_t d_in, int64_t d_out, forge_stream stream);
+
+/* One gradient tensor of forge_grad_norm. */
+typedef struct {
+  const void* data;    /* device, 16-byte aligned, fp32 or bf16 (NULL if numel is 0) */
+  int64_t numel;       /* any size                                                   */
+  forge_dtype dtype;
+} forge_grad;
+
+/*
+ * forge_grad_norm: the global norm of n gradient tensors and the factor that
+ * clips them to it, left in device memory:
+ *   out[0] = sqrt(sum of g^2 over all tensors),
+ *   out[1] = min(1, max_norm / (out[0] + 1e-6)).
+ * The gradients are read once and not changed; forge_adamw_clip applies
+ * out[1] as it reads them.  Squares that would overflow or underflow fp32 are
+ * summed in fp64, so the norm is right for any finite gradients; a NaN or an
+ * infinity among them shows in out.  max_norm > 0 (FORGE_ERR_HYPER).  `grads`
+ * is host memory, read before the call returns; out is two fp32 words on the
+ * device; workspace (device, 16-byte aligned) of at least
+ * forge_grad_norm_workspace_bytes(n) (FORGE_ERR_SHAPE if smaller).  The same
+ * result on every run.  Asynchronous on `stream`.
+ */
+forge_status forge_grad_norm(const forge_grad* grads, int n, float max_norm, float* out,
+                             void* workspace, size_t workspace_bytes, forge_stream stream);
+size_t forge_grad_norm_workspace_bytes(int n);
+
+/*
+ * forge_adamw_clip: forge_adamw on the gradient dW * *coef, where coef is one
+ * fp32 word in device memory (forge_grad_norm's out + 1), read when the kernel
+ * runs.  With *coef = 1 it gives forge_adamw's bits.  dW is not changed and
+ * must not be NULL.  Otherwise the arguments and errors of forge_adamw.
+ */
+forge_status forge_adamw_clip(const void* dW, forge_dtype dw_dtype, const float* coef, void* W,
+                              forge_moment m, forge_moment v, int64_t d_in, int64_t d_out,
+                              float lr, float beta1, float beta2, float eps, float weight_decay,
+                              int64_t step, forge_moment_fmt fmt, forge_stream stream);
+
 /* Synchronises `stream`, then returns and clears the device error word of the
  * current device: FORGE_OK, FORGE_ERR_DEVICE_TIMEOUT if a kernel gave up on a
  * bounded wait since the last call, or FORGE_ERR_DEVICE_CONFIG.  FORGE_ERR_CUDA

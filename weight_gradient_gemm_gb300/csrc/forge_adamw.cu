@@ -13,8 +13,9 @@
 namespace forge {
 
 // dW formats: 0 fp32, 1 bf16, 2 no gradient (zero).
+// `gs` multiplies the gradient (1 without clipping, which changes no bit).
 template <int DW>
-__device__ __forceinline__ void load_grad8(const void* dW, int64_t i8, float (&g)[8]) {
+__device__ __forceinline__ void load_grad8(const void* dW, int64_t i8, float gs, float (&g)[8]) {
   if constexpr (DW == 0) {
     const float4* p = reinterpret_cast<const float4*>(dW) + 2 * i8;
     const float4 a = __ldcs(p), b = __ldcs(p + 1);
@@ -29,6 +30,13 @@ __device__ __forceinline__ void load_grad8(const void* dW, int64_t i8, float (&g
 #pragma unroll
     for (int k = 0; k < 8; ++k) g[k] = 0.0f;
   }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) g[k] = __fmul_rn(g[k], gs);
+}
+
+// The clipping coefficient of a step: a device word, or 1 without one.
+__device__ __forceinline__ float grad_scale(const float* coef) {
+  return coef ? __ldg(coef) : 1.0f;
 }
 
 // fp32 or bf16 moments: one thread per 8 consecutive elements.
@@ -37,12 +45,14 @@ __global__ void __launch_bounds__(256) adamw_vec8_kernel(const void* __restrict_
                                                          uint16_t* __restrict__ W,
                                                          void* __restrict__ m,
                                                          void* __restrict__ v, int64_t n8,
-                                                         const AdamWConsts h) {
+                                                         const AdamWConsts h,
+                                                         const float* __restrict__ coef) {
+  const float gs = grad_scale(coef);
   const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n8;
        i += stride) {
     float g[8], w[8], mm[8], vv[8];
-    load_grad8<DW>(dW, i, g);
+    load_grad8<DW>(dW, i, gs, g);
     uint4* wp = reinterpret_cast<uint4*>(W) + i;
     const uint4 wq = __ldcs(wp);
     const uint32_t wu[4] = {wq.x, wq.y, wq.z, wq.w};
@@ -108,7 +118,9 @@ __global__ void __launch_bounds__(256) adamw_int8_kernel(const void* __restrict_
                                                          int8_t* __restrict__ vq,
                                                          float* __restrict__ m_scale,
                                                          float* __restrict__ v_scale,
-                                                         int64_t nblocks, const AdamWConsts h) {
+                                                         int64_t nblocks, const AdamWConsts h,
+                                                         const float* __restrict__ coef) {
+  const float gs = grad_scale(coef);
   const int lane = threadIdx.x & 31;
   const int64_t warps = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
   for (int64_t b = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
@@ -124,6 +136,8 @@ __global__ void __launch_bounds__(256) adamw_int8_kernel(const void* __restrict_
     } else {
       g[0] = g[1] = g[2] = g[3] = 0.0f;
     }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) g[k] = __fmul_rn(g[k], gs);
     uint2* wp = reinterpret_cast<uint2*>(W) + e0 / 4;
     const uint2 wv = __ldcs(wp);
     w[0] = bf16_lo(wv.x); w[1] = bf16_hi(wv.x); w[2] = bf16_lo(wv.y); w[3] = bf16_hi(wv.y);
@@ -176,15 +190,17 @@ __global__ void __launch_bounds__(256) adamw_fp8_kernel(const void* __restrict__
                                                         uint8_t* __restrict__ rq,
                                                         float* __restrict__ m_words,
                                                         float* __restrict__ r_words,
-                                                        int64_t n16, const AdamWConsts h) {
+                                                        int64_t n16, const AdamWConsts h,
+                                                        const float* __restrict__ coef) {
+  const float gs = grad_scale(coef);
   const Fp8Step fm = fp8_step_of(m_words), fr = fp8_step_of(r_words);
   float amax_m = 0.0f, amax_r = 0.0f;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n16;
        i += stride) {
     float g[16], w[16], ga[8], gb[8];
-    load_grad8<DW>(dW, 2 * i, ga);
-    load_grad8<DW>(dW, 2 * i + 1, gb);
+    load_grad8<DW>(dW, 2 * i, gs, ga);
+    load_grad8<DW>(dW, 2 * i + 1, gs, gb);
 #pragma unroll
     for (int k = 0; k < 8; ++k) { g[k] = ga[k]; g[8 + k] = gb[k]; }
     uint4* wp = reinterpret_cast<uint4*>(W) + 2 * i;
@@ -230,24 +246,26 @@ cudaError_t launch_fp8_roll(float* words, int n, int stride, float headroom,
 
 template <int FMT, int DW>
 static cudaError_t launch_vec8(const void* dW, void* W, void* m, void* v, int64_t n, int grid,
-                               const AdamWConsts& h, cudaStream_t stream) {
+                               const AdamWConsts& h, const float* coef, cudaStream_t stream) {
   adamw_vec8_kernel<FMT, DW><<<grid, 256, 0, stream>>>(dW, static_cast<uint16_t*>(W), m, v, n / 8,
-                                                      h);
+                                                      h, coef);
   return cudaGetLastError();
 }
 
 template <int DW>
 static cudaError_t launch_i8(const void* dW, void* W, void* m, void* v, float* ms, float* vs,
-                             int64_t n, int grid, const AdamWConsts& h, cudaStream_t stream) {
+                             int64_t n, int grid, const AdamWConsts& h, const float* coef,
+                             cudaStream_t stream) {
   adamw_int8_kernel<DW><<<grid, 256, 0, stream>>>(dW, static_cast<uint16_t*>(W),
                                                  static_cast<int8_t*>(m), static_cast<int8_t*>(v),
-                                                 ms, vs, n / 128, h);
+                                                 ms, vs, n / 128, h, coef);
   return cudaGetLastError();
 }
 
 cudaError_t launch_adamw(const void* dW, int dw_fmt, void* W, void* m, void* v, float* m_scale,
                          float* v_scale, int64_t d_in, int64_t d_out, int fmt,
-                         const AdamWConsts& h, int num_sms, cudaStream_t stream) {
+                         const AdamWConsts& h, const float* coef, int num_sms,
+                         cudaStream_t stream) {
   const int64_t n = d_in * d_out;
   const int dw = dW == nullptr ? 2 : dw_fmt;
   if (fmt == kFmtF8) {   // n is a multiple of 64 (d_in, d_out multiples of 8)
@@ -258,9 +276,9 @@ cudaError_t launch_adamw(const void* dW, int dw_fmt, void* W, void* m, void* v, 
     auto* mp = static_cast<uint8_t*>(m);
     auto* vp = static_cast<uint8_t*>(v);
     switch (dw) {
-      case 0: adamw_fp8_kernel<0><<<grid, 256, 0, stream>>>(dW, Wp, mp, vp, m_scale, v_scale, n16, h); break;
-      case 1: adamw_fp8_kernel<1><<<grid, 256, 0, stream>>>(dW, Wp, mp, vp, m_scale, v_scale, n16, h); break;
-      default: adamw_fp8_kernel<2><<<grid, 256, 0, stream>>>(dW, Wp, mp, vp, m_scale, v_scale, n16, h); break;
+      case 0: adamw_fp8_kernel<0><<<grid, 256, 0, stream>>>(dW, Wp, mp, vp, m_scale, v_scale, n16, h, coef); break;
+      case 1: adamw_fp8_kernel<1><<<grid, 256, 0, stream>>>(dW, Wp, mp, vp, m_scale, v_scale, n16, h, coef); break;
+      default: adamw_fp8_kernel<2><<<grid, 256, 0, stream>>>(dW, Wp, mp, vp, m_scale, v_scale, n16, h, coef); break;
     }
     return cudaGetLastError();
   }
@@ -269,9 +287,9 @@ cudaError_t launch_adamw(const void* dW, int dw_fmt, void* W, void* m, void* v, 
     const int64_t want = (nb + 7) / 8;
     const int grid = static_cast<int>(want < 8LL * num_sms ? (want > 0 ? want : 1) : 8LL * num_sms);
     switch (dw) {
-      case 0: return launch_i8<0>(dW, W, m, v, m_scale, v_scale, n, grid, h, stream);
-      case 1: return launch_i8<1>(dW, W, m, v, m_scale, v_scale, n, grid, h, stream);
-      default: return launch_i8<2>(dW, W, m, v, m_scale, v_scale, n, grid, h, stream);
+      case 0: return launch_i8<0>(dW, W, m, v, m_scale, v_scale, n, grid, h, coef, stream);
+      case 1: return launch_i8<1>(dW, W, m, v, m_scale, v_scale, n, grid, h, coef, stream);
+      default: return launch_i8<2>(dW, W, m, v, m_scale, v_scale, n, grid, h, coef, stream);
     }
   }
   const int64_t n8 = n / 8;
@@ -279,15 +297,15 @@ cudaError_t launch_adamw(const void* dW, int dw_fmt, void* W, void* m, void* v, 
   const int grid = static_cast<int>(want < 8LL * num_sms ? (want > 0 ? want : 1) : 8LL * num_sms);
   if (fmt == kFmtF32) {
     switch (dw) {
-      case 0: return launch_vec8<kFmtF32, 0>(dW, W, m, v, n, grid, h, stream);
-      case 1: return launch_vec8<kFmtF32, 1>(dW, W, m, v, n, grid, h, stream);
-      default: return launch_vec8<kFmtF32, 2>(dW, W, m, v, n, grid, h, stream);
+      case 0: return launch_vec8<kFmtF32, 0>(dW, W, m, v, n, grid, h, coef, stream);
+      case 1: return launch_vec8<kFmtF32, 1>(dW, W, m, v, n, grid, h, coef, stream);
+      default: return launch_vec8<kFmtF32, 2>(dW, W, m, v, n, grid, h, coef, stream);
     }
   }
   switch (dw) {
-    case 0: return launch_vec8<kFmtBF16, 0>(dW, W, m, v, n, grid, h, stream);
-    case 1: return launch_vec8<kFmtBF16, 1>(dW, W, m, v, n, grid, h, stream);
-    default: return launch_vec8<kFmtBF16, 2>(dW, W, m, v, n, grid, h, stream);
+    case 0: return launch_vec8<kFmtBF16, 0>(dW, W, m, v, n, grid, h, coef, stream);
+    case 1: return launch_vec8<kFmtBF16, 1>(dW, W, m, v, n, grid, h, coef, stream);
+    default: return launch_vec8<kFmtBF16, 2>(dW, W, m, v, n, grid, h, coef, stream);
   }
 }
 

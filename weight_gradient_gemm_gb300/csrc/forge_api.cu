@@ -733,6 +733,35 @@ bool layers_clash(const forge_linear& a, const forge_linear& b, int64_t bt, forg
          (ns && input_overlaps_state(a.v.scale, ns, b.W, b.m, b.v, b.d_in, b.d_out, fmt));
 }
 
+// forge_adamw, with the gradient multiplied by *coef (device) unless it is null.
+forge_status adamw_run(const void* dW, forge_dtype dw_dtype, const float* coef, void* W,
+                       const forge_moment& m, const forge_moment& v, int64_t d_in, int64_t d_out,
+                       float lr, float beta1, float beta2, float eps, float weight_decay,
+                       int64_t step, forge_moment_fmt fmt, forge_stream stream) {
+  forge_status s = check_shape(0, d_in, d_out);
+  if (s != FORGE_OK) return s;
+  if (dw_dtype != FORGE_DT_FP32 && dw_dtype != FORGE_DT_BF16) return FORGE_ERR_FORMAT;
+  s = check_state(W, m, v, d_in, d_out, fmt);
+  if (s != FORGE_OK) return s;
+  if (dW && !aligned16(dW)) return FORGE_ERR_ALIGN;
+  s = check_hyper(lr, beta1, beta2, eps, weight_decay, step);
+  if (s != FORGE_OK) return s;
+  const uint64_t nbytes =
+      static_cast<uint64_t>(d_in) * d_out * (dw_dtype == FORGE_DT_FP32 ? 4 : 2);
+  if (dW && input_overlaps_state(dW, nbytes, W, m, v, d_in, d_out, fmt)) return FORGE_ERR_ALIAS;
+  if (coef && input_overlaps_state(coef, sizeof(float), W, m, v, d_in, d_out, fmt))
+    return FORGE_ERR_ALIAS;
+  DeviceInfo* d = nullptr;
+  s = device_info(&d);
+  if (s != FORGE_OK) return s;
+  const AdamWConsts h = make_consts(lr, beta1, beta2, eps, weight_decay, step);
+  return launch_adamw(dW, dw_dtype == FORGE_DT_FP32 ? 0 : 1, W, m.data, v.data, m.scale, v.scale,
+                      d_in, d_out, static_cast<int>(fmt), h, coef, d->num_sms,
+                      static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? FORGE_OK
+             : FORGE_ERR_LAUNCH;
+}
+
 int take_drop_flag() {
   std::lock_guard<std::mutex> lk(g_mu);
   const int f = g_drop_first_arrival;
@@ -741,6 +770,21 @@ int take_drop_flag() {
 }
 
 }  // namespace
+
+int host_device(HostDevice* out) {
+  DeviceInfo* d = nullptr;
+  const forge_status s = device_info(&d);
+  if (s != FORGE_OK) return s;
+  *out = HostDevice{d->num_sms, d->err_word, d->site_word, g_wait_limit_ns};
+  return FORGE_OK;
+}
+
+bool host_map(CUtensorMap* out, const void* ptr, CUtensorMapDataType dt, uint64_t inner,
+              uint64_t outer, uint64_t stride_bytes, uint32_t box_inner, uint32_t box_outer,
+              CUtensorMapSwizzle sw) {
+  return get_map(out, ptr, dt, inner, outer, stride_bytes, box_inner, box_outer, sw);
+}
+
 }  // namespace forge
 
 using namespace forge;
@@ -771,7 +815,7 @@ forge_status forge_wgrad_adamw_grouped(const forge_linear* layers, int n, int64_
     for (int i = 0; i < n; ++i) {
       const forge_linear& L = layers[i];
       if (launch_adamw(nullptr, 0, L.W, L.m.data, L.v.data, L.m.scale, L.v.scale, L.d_in,
-                       L.d_out, ifmt, h, d->num_sms, st) != cudaSuccess)
+                       L.d_out, ifmt, h, nullptr, d->num_sms, st) != cudaSuccess)
         return FORGE_ERR_LAUNCH;
     }
     return FORGE_OK;
@@ -830,7 +874,7 @@ forge_status forge_wgrad_adamw_acc_grouped(const forge_linear* layers, const flo
     for (int i = 0; i < n; ++i) {
       const forge_linear& L = layers[i];
       if (launch_adamw(B[i], 0, L.W, L.m.data, L.v.data, nullptr, nullptr, L.d_in, L.d_out,
-                       static_cast<int>(fmt), h, d->num_sms, st) != cudaSuccess)
+                       static_cast<int>(fmt), h, nullptr, d->num_sms, st) != cudaSuccess)
         return FORGE_ERR_LAUNCH;
     }
     return FORGE_OK;
@@ -1448,26 +1492,18 @@ forge_status forge_adamw(const void* dW, forge_dtype dw_dtype, void* W, forge_mo
                          forge_moment v, int64_t d_in, int64_t d_out, float lr, float beta1,
                          float beta2, float eps, float weight_decay, int64_t step,
                          forge_moment_fmt fmt, forge_stream stream) {
-  forge_status s = check_shape(0, d_in, d_out);
-  if (s != FORGE_OK) return s;
-  if (dw_dtype != FORGE_DT_FP32 && dw_dtype != FORGE_DT_BF16) return FORGE_ERR_FORMAT;
-  s = check_state(W, m, v, d_in, d_out, fmt);
-  if (s != FORGE_OK) return s;
-  if (dW && !aligned16(dW)) return FORGE_ERR_ALIGN;
-  s = check_hyper(lr, beta1, beta2, eps, weight_decay, step);
-  if (s != FORGE_OK) return s;
-  const uint64_t nbytes =
-      static_cast<uint64_t>(d_in) * d_out * (dw_dtype == FORGE_DT_FP32 ? 4 : 2);
-  if (dW && input_overlaps_state(dW, nbytes, W, m, v, d_in, d_out, fmt)) return FORGE_ERR_ALIAS;
-  DeviceInfo* d = nullptr;
-  s = device_info(&d);
-  if (s != FORGE_OK) return s;
-  const AdamWConsts h = make_consts(lr, beta1, beta2, eps, weight_decay, step);
-  return launch_adamw(dW, dw_dtype == FORGE_DT_FP32 ? 0 : 1, W, m.data, v.data, m.scale, v.scale,
-                      d_in, d_out, static_cast<int>(fmt), h, d->num_sms,
-                      static_cast<cudaStream_t>(stream)) == cudaSuccess
-             ? FORGE_OK
-             : FORGE_ERR_LAUNCH;
+  return adamw_run(dW, dw_dtype, nullptr, W, m, v, d_in, d_out, lr, beta1, beta2, eps,
+                   weight_decay, step, fmt, stream);
+}
+
+forge_status forge_adamw_clip(const void* dW, forge_dtype dw_dtype, const float* coef, void* W,
+                              forge_moment m, forge_moment v, int64_t d_in, int64_t d_out,
+                              float lr, float beta1, float beta2, float eps, float weight_decay,
+                              int64_t step, forge_moment_fmt fmt, forge_stream stream) {
+  if (!dW || !coef) return FORGE_ERR_NULL;
+  if (reinterpret_cast<uintptr_t>(coef) & 3u) return FORGE_ERR_ALIGN;
+  return adamw_run(dW, dw_dtype, coef, W, m, v, d_in, d_out, lr, beta1, beta2, eps,
+                   weight_decay, step, fmt, stream);
 }
 
 forge_status forge_device_error(forge_stream stream) {

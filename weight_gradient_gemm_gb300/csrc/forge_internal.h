@@ -178,10 +178,101 @@ cudaError_t launch_dgrad_reduce(const float* part, int splits, int cg, int bn, i
 
 cudaError_t launch_adamw(const void* dW, int dw_fmt, void* W, void* m, void* v, float* m_scale,
                          float* v_scale, int64_t d_in, int64_t d_out, int fmt,
-                         const AdamWConsts& h, int num_sms, cudaStream_t stream);
+                         const AdamWConsts& h, const float* coef, int num_sms,
+                         cudaStream_t stream);   // coef: device gradient factor, or null
 
 // fp8 moments: the scale roll between steps (see forge_fp8_roll_scales).
 cudaError_t launch_fp8_roll(float* words, int n, int stride, float headroom,
                             cudaStream_t stream);
+
+// What the host entry points outside forge_api.cu need of its state.
+struct HostDevice {
+  int num_sms;
+  int* err;              // device error word
+  int* err_site;
+  uint64_t timeout_ns;   // bounded-wait limit
+};
+// The current device (a forge_status; FORGE_ERR_ARCH off sm_103).
+int host_device(HostDevice* out);
+// A 2-D row-major tensor map, from the cache or newly encoded.
+bool host_map(CUtensorMap* out, const void* ptr, CUtensorMapDataType dt, uint64_t inner,
+              uint64_t outer, uint64_t stride_bytes, uint32_t box_inner, uint32_t box_outer,
+              CUtensorMapSwizzle sw);
+
+// The RMS norm in front of a linear layer (forge_norm.cu).  Null pointers
+// leave an input or output out.
+struct NormArgs {
+  const uint16_t* x;
+  const uint16_t* residual;
+  const void* gain;
+  int gain_bf16;
+  uint16_t* sum;
+  uint16_t* y;
+  uint8_t* codes;
+  float* scales;
+  float* rstd;
+  int64_t rows;
+  int cols;
+  float eps;
+};
+cudaError_t launch_rmsnorm(const NormArgs& a, int num_sms, cudaStream_t stream);
+
+struct NormBwdArgs {
+  const uint16_t* dy;
+  const uint16_t* h;
+  const void* gain;
+  int gain_bf16;
+  const float* rstd;
+  const uint16_t* dsum;
+  uint16_t* dx;
+  float* dgain;
+  float* part;           // [rmsnorm_bwd_blocks][cols] partial sums of dgain
+  int64_t rows;
+  int cols;
+};
+int rmsnorm_bwd_blocks(int64_t rows, int cols, int num_sms);
+cudaError_t launch_rmsnorm_bwd(const NormBwdArgs& a, int num_sms, cudaStream_t stream);
+// Widest row the norm's kernels hold in registers.
+constexpr int kNormMaxCols = 32768;
+
+// e4m3 codes and one scale per block of block_rows (1 or 128) x 128.
+cudaError_t launch_quantize_b128(const uint16_t* x, uint8_t* codes, float* scales, int64_t rows,
+                                 int64_t cols, int block_rows, int num_sms, cudaStream_t stream);
+
+// The global gradient norm (forge_gradnorm.cu).
+constexpr int kNormTensors = 256;   // tensors one launch takes
+struct GradNormArgs {
+  const void* ptr[kNormTensors];
+  int64_t numel[kNormTensors];
+  int32_t unit0[kNormTensors + 1];   // first work unit of each tensor
+  uint64_t bf16[kNormTensors / 64];  // bit i: tensor i is bf16
+  int32_t n;
+  double* part;                      // one partial sum of squares per block
+};
+constexpr int kNormUnit = 16384;     // elements per work unit
+int grad_norm_blocks(int64_t units, int num_sms);
+cudaError_t launch_grad_norm(const GradNormArgs& a, int blocks, cudaStream_t stream);
+cudaError_t launch_grad_norm_final(const double* part, int n, float max_norm, float* out,
+                                   cudaStream_t stream);
+
+// The 8-bit products of a linear layer (forge_gemm_b128.cu).
+struct B128Args {
+  CUtensorMap a, b, out;   // tokens' codes, weight codes, output
+  const float* sa;         // [m, num_kb] scales of the tokens' codes
+  const float* sw;         // scales of the weight's 128 x 128 blocks
+  int32_t m, n, num_kb;    // tokens, output columns, 128-deep steps of the reduction
+  int32_t sw_n, sw_k;      // steps in sw from one column block / reduction block to the next
+  int32_t tiles_m, tiles_n, num_tiles, group_m;
+  int32_t out_fp32;
+  int* err;
+  int* err_site;
+  uint64_t timeout_ns;
+};
+// Box heights of the operand maps and tile sizes of a configuration.
+struct B128Config {
+  int cg, bn;
+};
+cudaError_t launch_gemm_b128(const B128Config& c, bool dgrad, const B128Args& a, int num_sms,
+                             cudaStream_t stream);
 
 }  // namespace forge

@@ -68,6 +68,11 @@ class ForgeDgradItem(ctypes.Structure):
     _fields_ = [("dY", ctypes.c_void_p), ("W", ctypes.c_void_p), ("dX", ctypes.c_void_p),
                 ("d_in", ctypes.c_int64), ("d_out", ctypes.c_int64)]
 
+
+class ForgeGrad(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("numel", ctypes.c_int64), ("dtype", ctypes.c_int)]
+
+
 # forge_profile values
 PROFILES = {"auto": -1, "stream": 0, "mma": 1, "balanced": 2, "deep": 3}
 
@@ -85,6 +90,8 @@ _lib: Optional[ctypes.CDLL] = None
 def lib() -> ctypes.CDLL:
     """The loaded libforge.so (loaded once)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -162,6 +169,25 @@ def lib() -> ctypes.CDLL:
             L.forge_wgrad_adamw_acc_grouped.restype = st
             L.forge_fp8_roll_scales.argtypes = [vp, st, f32, vp]
             L.forge_fp8_roll_scales.restype = st
+            L.forge_adamw_clip.argtypes = [vp, st, vp, vp, ForgeMoment, ForgeMoment, i64, i64,
+                                           f32, f32, f32, f32, f32, i64, st, vp]
+            L.forge_adamw_clip.restype = st
+            L.forge_rmsnorm.argtypes = [vp, vp, vp, st, vp, vp, vp, vp, vp, i64, i64, f32, vp]
+            L.forge_rmsnorm.restype = st
+            L.forge_rmsnorm_backward.argtypes = [vp, vp, vp, st, vp, vp, vp, vp, i64, i64, vp, sz,
+                                                 vp]
+            L.forge_rmsnorm_backward.restype = st
+            L.forge_rmsnorm_backward_workspace_bytes.argtypes = [i64, i64]
+            L.forge_rmsnorm_backward_workspace_bytes.restype = sz
+            L.forge_quantize_b128.argtypes = [vp, vp, vp, i64, i64, st, vp]
+            L.forge_quantize_b128.restype = st
+            for name in ("forge_linear_fp8", "forge_dgrad_fp8"):
+                getattr(L, name).argtypes = [vp, vp, vp, vp, vp, st, i64, i64, i64, vp]
+                getattr(L, name).restype = st
+            L.forge_grad_norm.argtypes = [vp, st, f32, vp, vp, sz, vp]
+            L.forge_grad_norm.restype = st
+            L.forge_grad_norm_workspace_bytes.argtypes = [st]
+            L.forge_grad_norm_workspace_bytes.restype = sz
             L.forge_set_tuning.argtypes = [ctypes.POINTER(ForgeTuning)]
             L.forge_set_tuning.restype = None
             L.forge_get_tuning.argtypes = [ctypes.POINTER(ForgeTuning)]
@@ -226,7 +252,44 @@ def _want(t: Optional[torch.Tensor], name: str, shape, dtypes) -> None:
 
 _BF16 = (torch.bfloat16,)
 _F32 = (torch.float32,)
+_F8 = (torch.float8_e4m3fn,)
+_GAIN = (torch.float32, torch.bfloat16)
+_DT = {torch.float32: DT_FP32, torch.bfloat16: DT_BF16}
 _MOM = (torch.float32, torch.bfloat16, torch.int8, torch.float8_e4m3fn)
+
+
+def _matrix(t: torch.Tensor, name: str):
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    return t.shape
+
+
+def _device_of(t: torch.Tensor, name: str) -> int:
+    """The index of the CUDA device t is on, which has to be the current one."""
+    dev = t.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        _dense(t, name)
+    return dev
+
+
+def _arg(t: Optional[torch.Tensor], name: str, shape, dtypes, dev: int) -> int:
+    """The pointer of one argument after the checks of _want and _dense (dev is
+    the current device), in a single test where it passes: calls on few rows
+    take a few microseconds."""
+    if (t is None or t.shape != shape or t.dtype not in dtypes or t.get_device() != dev
+            or not t.is_contiguous()):
+        _want(t, name, shape, dtypes)
+        _dense(t, name)
+    return t.data_ptr()
+
+
+def _opt(t: Optional[torch.Tensor], name: str, shape, dtypes, dev: int) -> Optional[int]:
+    return None if t is None else _arg(t, name, shape, dtypes, dev)
+
+
+def _raw_stream(stream, dev: int) -> int:
+    """_stream, without building a Stream object for the current stream."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
 def _operands(X: torch.Tensor, dY: torch.Tensor):
@@ -465,6 +528,27 @@ def adamw(dW: Optional[torch.Tensor], W: torch.Tensor, m: torch.Tensor, v: torch
                            d_in, d_out, lr, beta1, beta2, eps, weight_decay, step, fmt,
                            _stream(stream))
     _check(st, "forge_adamw")
+
+
+def adamw_clip(dW: torch.Tensor, W: torch.Tensor, m: torch.Tensor, v: torch.Tensor,
+               clip: torch.Tensor, *, lr: float, beta1: float, beta2: float, eps: float,
+               weight_decay: float, step: int, m_scale: Optional[torch.Tensor] = None,
+               v_scale: Optional[torch.Tensor] = None, stream=None) -> None:
+    """adamw on the clipped gradient dW * clip[1], where clip is what grad_norm
+    left on the device (the norm and the coefficient, fp32 [2])."""
+    shape = _matrix(W, "W")
+    dev = _device_of(W, "W")
+    wp = _arg(W, "W", shape, _BF16, dev)
+    mp, vp = _arg(m, "m", shape, _MOM, dev), _arg(v, "v", shape, (m.dtype,), dev)
+    fmt = moment_format(m)
+    if fmt == MOM_INT8_B128 or fmt == MOM_FP8_E4M3:
+        _moments(m, v, m_scale, v_scale, *shape)
+        _on_device(m_scale=m_scale, v_scale=v_scale)
+    st = lib().forge_adamw_clip(
+        _arg(dW, "dW", shape, _GAIN, dev), _DT[dW.dtype], _arg(clip, "clip", (2,), _F32, dev) + 4,
+        wp, ForgeMoment(mp, _ptr(m_scale)), ForgeMoment(vp, _ptr(v_scale)), shape[1], shape[0], lr,
+        beta1, beta2, eps, weight_decay, step, fmt, _raw_stream(stream, dev))
+    _check(st, "forge_adamw_clip")
 
 
 def device_error(stream=None) -> int:
@@ -777,3 +861,144 @@ def linear_backward_grouped(layers, *, lr: float, beta1: float, beta2: float, ep
         arr, dx, n, bt, lr, beta1, beta2, eps, weight_decay, step, fmt, _ptr(workspace),
         0 if workspace is None else workspace.numel() * workspace.element_size(),
         _stream(stream)), "forge_linear_backward_grouped")
+
+
+# ---------------------------------------------------------------------------
+# The operators around the weight gradient: the RMS norm, the 128-block e4m3
+# format, the 8-bit products and the global gradient norm.
+# ---------------------------------------------------------------------------
+def _ceil128(n: int) -> int:
+    return (n + 127) // 128
+
+
+def alloc_b128(rows: int, cols: int, block_rows: int = 1, device="cuda"):
+    """Codes and scales of a [rows, cols] matrix in the 128-block e4m3 format
+    (block_rows 1 for activations and their gradients, 128 for weights)."""
+    if block_rows not in (1, 128):
+        raise ValueError("block_rows is 1 or 128")
+    scale_rows = rows if block_rows == 1 else _ceil128(rows)
+    return (torch.empty((rows, cols), dtype=torch.float8_e4m3fn, device=device),
+            torch.empty((scale_rows, _ceil128(cols)), dtype=torch.float32, device=device))
+
+
+def rmsnorm(x: torch.Tensor, gain: torch.Tensor, *, eps: float,
+            residual: Optional[torch.Tensor] = None, sum_out: Optional[torch.Tensor] = None,
+            y: Optional[torch.Tensor] = None, codes: Optional[torch.Tensor] = None,
+            scales: Optional[torch.Tensor] = None, rstd: Optional[torch.Tensor] = None,
+            stream=None) -> None:
+    """h = x + residual, y = h / sqrt(mean(h^2) + eps) * gain over the rows of x
+    [rows, cols] bf16.  Writes the outputs given: sum_out = h (bf16; may be x or
+    residual), y (bf16), codes and scales = y in the 128-block e4m3 format, rstd
+    [rows] fp32 for rmsnorm_backward."""
+    rows, cols = shape = _matrix(x, "x")
+    dev = _device_of(x, "x")
+    st = lib().forge_rmsnorm(
+        _arg(x, "x", shape, _BF16, dev), _opt(residual, "residual", shape, _BF16, dev),
+        _arg(gain, "gain", (cols,), _GAIN, dev), _DT[gain.dtype],
+        _opt(sum_out, "sum_out", shape, _BF16, dev), _opt(y, "y", shape, _BF16, dev),
+        _opt(codes, "codes", shape, _F8, dev),
+        _opt(scales, "scales", (rows, _ceil128(cols)), _F32, dev),
+        _opt(rstd, "rstd", (rows,), _F32, dev), rows, cols, eps, _raw_stream(stream, dev))
+    _check(st, "forge_rmsnorm")
+
+
+def rmsnorm_backward_workspace_bytes(rows: int, cols: int) -> int:
+    """Workspace bytes rmsnorm_backward needs when it writes dgain."""
+    return int(lib().forge_rmsnorm_backward_workspace_bytes(rows, cols))
+
+
+def rmsnorm_backward(dY: torch.Tensor, h: torch.Tensor, gain: torch.Tensor, rstd: torch.Tensor,
+                     dX: torch.Tensor, dgain: Optional[torch.Tensor] = None, *,
+                     dsum: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """The gradients of rmsnorm: dX [rows, cols] bf16 (of x and of the residual;
+    dsum, the gradient that reaches the sum directly, is added and may be dX) and
+    dgain [cols] fp32, from h (the forward pass's sum, or x) and rstd.  dgain
+    needs a workspace of rmsnorm_backward_workspace_bytes bytes."""
+    rows, cols = shape = _matrix(h, "h")
+    dev = _device_of(h, "h")
+    if workspace is not None:
+        _dense(workspace, "workspace")
+    st = lib().forge_rmsnorm_backward(
+        _arg(dY, "dY", shape, _BF16, dev), _arg(h, "h", shape, _BF16, dev),
+        _arg(gain, "gain", (cols,), _GAIN, dev), _DT[gain.dtype],
+        _arg(rstd, "rstd", (rows,), _F32, dev), _opt(dsum, "dsum", shape, _BF16, dev),
+        _arg(dX, "dX", shape, _BF16, dev), _opt(dgain, "dgain", (cols,), _F32, dev), rows, cols,
+        _ptr(workspace), 0 if workspace is None else workspace.nbytes, _raw_stream(stream, dev))
+    _check(st, "forge_rmsnorm_backward")
+
+
+def quantize_b128(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, *,
+                  block_rows: int = 1, stream=None) -> None:
+    """x [rows, cols] bf16 as e4m3 codes and one fp32 scale per block of
+    block_rows (1 or 128) x 128 (see alloc_b128)."""
+    rows, cols = shape = _matrix(x, "x")
+    if block_rows not in (1, 128):
+        raise ValueError("block_rows is 1 or 128")
+    dev = _device_of(x, "x")
+    scale_rows = rows if block_rows == 1 else _ceil128(rows)
+    st = lib().forge_quantize_b128(
+        _arg(x, "x", shape, _BF16, dev), _arg(codes, "codes", shape, _F8, dev),
+        _arg(scales, "scales", (scale_rows, _ceil128(cols)), _F32, dev), rows, cols, block_rows,
+        _raw_stream(stream, dev))
+    _check(st, "forge_quantize_b128")
+
+
+def _product_fp8(name, a, a_scales, W, w_scales, out, k, n, d_in, d_out, stream):
+    bt = a.shape[0]
+    dev = _device_of(W, "W")
+    fn = getattr(lib(), name)
+    st = fn(_arg(a, "X" if n == d_out else "dY", (bt, k), _F8, dev),
+            _arg(a_scales, "the tokens' scales", (bt, _ceil128(k)), _F32, dev),
+            _arg(W, "W", (d_out, d_in), _F8, dev),
+            _arg(w_scales, "w_scales", (_ceil128(d_out), _ceil128(d_in)), _F32, dev),
+            _arg(out, "the output", (bt, n), _GAIN, dev), _DT[out.dtype], bt, d_in, d_out,
+            _raw_stream(stream, dev))
+    _check(st, name)
+
+
+def linear_fp8(X: torch.Tensor, x_scales: torch.Tensor, W: torch.Tensor, w_scales: torch.Tensor,
+               Y: torch.Tensor, stream=None) -> None:
+    """Y = X W^T on the 8-bit tensor cores: X [bt, d_in] codes with block_rows 1,
+    W [d_out, d_in] codes with block_rows 128, Y [bt, d_out] bf16 or fp32."""
+    _matrix(X, "X")
+    d_out, d_in = _matrix(W, "W")
+    _product_fp8("forge_linear_fp8", X, x_scales, W, w_scales, Y, d_in, d_out, d_in, d_out, stream)
+
+
+def dgrad_fp8(dY: torch.Tensor, dy_scales: torch.Tensor, W: torch.Tensor, w_scales: torch.Tensor,
+              dX: torch.Tensor, stream=None) -> None:
+    """dX = dY W on the 8-bit tensor cores, from the same stored weight as
+    linear_fp8: dY [bt, d_out] codes with block_rows 1, dX [bt, d_in] bf16 or
+    fp32."""
+    _matrix(dY, "dY")
+    d_out, d_in = _matrix(W, "W")
+    _product_fp8("forge_dgrad_fp8", dY, dy_scales, W, w_scales, dX, d_out, d_in, d_in, d_out,
+                 stream)
+
+
+def grad_norm_workspace_bytes(n: int) -> int:
+    """Workspace bytes grad_norm needs for n tensors."""
+    return int(lib().forge_grad_norm_workspace_bytes(n))
+
+
+def grad_norm(grads, max_norm: float, out: torch.Tensor, *, workspace: torch.Tensor,
+              stream=None) -> None:
+    """out (fp32 [2], on the device) = the global norm of the gradients (fp32 or
+    bf16 tensors of any shape) and min(1, max_norm / (norm + 1e-6)), the factor
+    adamw_clip applies."""
+    n = len(grads)
+    arr = (ForgeGrad * n)()
+    dev = _device_of(out, "out")
+    for i, g in enumerate(grads):
+        if g.dtype not in _GAIN:
+            raise TypeError(f"gradient {i} has dtype {g.dtype}, expected fp32 or bf16")
+        if g.get_device() != dev or not g.is_contiguous():
+            _dense(g, f"gradient {i}")
+            raise ValueError(f"gradient {i} is on {g.device}, out on {out.device}")
+        arr[i] = (g.data_ptr(), g.numel(), _DT[g.dtype])
+    _dense(workspace, "workspace")
+    st = lib().forge_grad_norm(ctypes.addressof(arr) if n else None, n, max_norm,
+                               _arg(out, "out", (2,), _F32, dev), workspace.data_ptr(),
+                               workspace.nbytes, _raw_stream(stream, dev))
+    _check(st, "forge_grad_norm")

@@ -55,6 +55,14 @@ forge_status check_rows(int64_t rows, int64_t cols, int64_t max_cols) {
   return FORGE_OK;
 }
 
+// The products' tile: 256 x 256 on CTA pairs, or 128 x 128 on one CTA where
+// pairs would leave SMs without a tile.
+B128Config choose_b128(int64_t m, int64_t n, const forge_tuning& tune, int num_sms) {
+  int cg = (m + 255) / 256 * ((n + 255) / 256) >= num_sms / 2 ? 2 : 1;
+  if (tune.cta_group) cg = tune.cta_group;
+  return cg == 2 ? B128Config{2, 256} : B128Config{1, 128};
+}
+
 // Y = A W^T (forward) or A W (input gradient), A's codes [m, k].
 forge_status product_b128(const void* A, const float* sa, const void* W, const float* sw, void* out,
                           forge_dtype dtype, int64_t m, int64_t k, int64_t n, bool dgrad,
@@ -75,7 +83,9 @@ forge_status product_b128(const void* A, const float* sa, const void* W, const f
   HostDevice d;
   const int st = host_device(&d);
   if (st != FORGE_OK) return static_cast<forge_status>(st);
-  const B128Config cfg{1, 128};
+  forge_tuning tune;
+  forge_get_tuning(&tune);
+  const B128Config cfg = choose_b128(m, n, tune, d.num_sms);
   B128Args a;
   std::memset(&a, 0, sizeof(a));
   const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;

@@ -13,10 +13,12 @@
 // registers that hold the output tile.  Several TMEM buffers let the tensor
 // core run ahead of that.
 //
-// Warp roles (320 threads): warp 0 loads operand stages of 128 columns with
-// TMA, warp 1 issues the MMAs, warps 2-9 add up (two per TMEM lane quadrant,
-// each half of the tile's columns) and store.  Every wait is bounded, as in
-// forge_gemm.cuh.
+// Warp roles (384 threads): warp 0 loads operand stages of 128 columns with
+// TMA, warp 1 issues the MMAs, warp 2 multiplies the scales and leaves the
+// products in shared memory eight blocks ahead, warps 4-11 add up (two per
+// TMEM lane quadrant, each half of the tile's columns) and store.  The first four warps give most
+// of their registers to the other eight, whose threads hold up to 128 output
+// values.  Every wait is bounded, as in forge_gemm.cuh.
 #include <cuda_bf16.h>
 
 #include "forge_internal.h"
@@ -26,7 +28,10 @@
 namespace forge {
 namespace {
 
-constexpr int kThreads8 = 320;
+constexpr int kThreads8 = 384;
+// Registers a thread after the split: 128 x 88 + 256 x 208 = 384 x 168, what
+// the block is launched with.
+constexpr int kRegsRole = 88, kRegsEpi = 208;
 constexpr int kEpiWarps = 8;
 constexpr int kSmemMax = 232448;   // dynamic shared memory of one CTA (227 KB)
 
@@ -39,12 +44,16 @@ struct Traits8 {
   static constexpr int A_BYTES = kBM * 128;
   static constexpr int STAGE_BYTES = A_BYTES + BNL * 128;
   static constexpr int OUT_BYTES = kEpiWarps * 4096;   // one 32-row slab of 128-byte rows a warp
-  static constexpr int STAGES = 6;
+  static constexpr int STAGES = 5;
   static constexpr int NBUF = 512 / BN;                // TMEM accumulators
+  static constexpr int NWB = BN / 128;                 // weight blocks across the tile
+  static constexpr int SC_BATCH = 8;                   // 128-blocks whose scales move together
+  static constexpr int SC_BYTES = 2 * SC_BATCH * NWB * kBM * 4;
   static constexpr int NC = BN / 2;                    // columns per epilogue thread
   static constexpr int OFF_OUT = STAGES * STAGE_BYTES;
-  static constexpr int OFF_BARS = OFF_OUT + OUT_BYTES;
-  static constexpr int NUM_BARS = 2 * STAGES + 2 * NBUF + 1;
+  static constexpr int OFF_SC = OFF_OUT + OUT_BYTES;
+  static constexpr int OFF_BARS = OFF_SC + SC_BYTES;
+  static constexpr int NUM_BARS = 2 * STAGES + 2 * NBUF + 5;
   static constexpr int OFF_TMEM = OFF_BARS + 8 * NUM_BARS;
   static constexpr int SMEM_USED = OFF_TMEM + 8;
   static constexpr int SMEM_ALLOC = SMEM_USED + 1024 < kSmemMax ? SMEM_USED + 1024 : kSmemMax;
@@ -85,7 +94,10 @@ __global__ void __launch_bounds__(kThreads8, 1) gemm_b128_kernel(const __grid_co
   auto bar_empty = [&](int s) { return bars + 8u * (T::STAGES + s); };
   auto bar_tfull = [&](int b) { return bars + 8u * (2 * T::STAGES + b); };
   auto bar_tempty = [&](int b) { return bars + 8u * (2 * T::STAGES + T::NBUF + b); };
-  const uint32_t bar_drain = bars + 8u * (2 * T::STAGES + 2 * T::NBUF);
+  auto bar_sfull = [&](int b) { return bars + 8u * (2 * T::STAGES + 2 * T::NBUF + b); };
+  auto bar_sempty = [&](int b) { return bars + 8u * (2 * T::STAGES + 2 * T::NBUF + 2 + b); };
+  const uint32_t bar_drain = bars + 8u * (2 * T::STAGES + 2 * T::NBUF + 4);
+  float* scales = reinterpret_cast<float*>(gbase + T::OFF_SC);   // [2][SC_BATCH][NWB][128]
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(gbase + T::OFF_TMEM + 4);
   const WaitCtx wc{abort_flag, a.err, a.err_site, a.timeout_ns};
 
@@ -97,6 +109,10 @@ __global__ void __launch_bounds__(kThreads8, 1) gemm_b128_kernel(const __grid_co
     for (int b = 0; b < T::NBUF; ++b) {
       mbar_init(bar_tfull(b), 1);
       mbar_init(bar_tempty(b), CG * kEpiWarps);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(bar_sfull(b), 32);
+      mbar_init(bar_sempty(b), kEpiWarps);
     }
     mbar_init(bar_drain, 1);
     *abort_flag = 0u;
@@ -122,24 +138,22 @@ __global__ void __launch_bounds__(kThreads8, 1) gemm_b128_kernel(const __grid_co
   tc_fence_after_sync();
   const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(gbase + T::OFF_TMEM);
 
+  if (warp < 4) {
+  regs_dec<kRegsRole>();
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
       const uint64_t pol = l2_policy_evict_normal();
-      uint32_t cnt = 0;
-      int32_t last_armed[T::STAGES];
-#pragma unroll
-      for (int s = 0; s < T::STAGES; ++s) last_armed[s] = -1;
+      uint32_t s = 0, ph = 0;   // next stage, and its phase
+      uint32_t armed = 0;       // stages filled so far, at most STAGES
       bool ok = true;
       for (int t = unit0; ok && t < a.num_tiles; t += units) {
         int tm, tn;
         tile_of(t, a, tm, tn);
         const int ya = tm * T::TM + static_cast<int>(rank) * kBM;
         const int nb = tn * BN + static_cast<int>(rank) * T::BNL;
-        for (int k = 0; k < a.num_kb; ++k, ++cnt) {
-          const int s = cnt % T::STAGES;
-          if (!wait_stage<!kPair>(bar_empty(s), ((cnt / T::STAGES) & 1u) ^ 1u, wc,
-                                  kSiteProducerEmpty)) { ok = false; break; }
+        for (int k = 0; k < a.num_kb; ++k) {
+          if (!wait_bounded(bar_empty(s), ph ^ 1u, wc, kSiteProducerEmpty)) { ok = false; break; }
           const uint32_t dst = base + s * T::STAGE_BYTES;
           // the weight's box: [BNL rows][128 of K], or for the input gradient
           // [128 of K][128 columns] per 128 columns
@@ -166,119 +180,175 @@ __global__ void __launch_bounds__(kThreads8, 1) gemm_b128_kernel(const __grid_co
               tma_load_2d(dst + T::A_BYTES, &a.b, k * 128, nb, bar_full(s), pol);
             }
           }
-          if (leader) last_armed[s] = static_cast<int32_t>(cnt);
+          if (armed < T::STAGES) ++armed;
+          if (++s == T::STAGES) { s = 0; ph ^= 1u; }
         }
       }
-      // let every armed load land before the CTA can exit
-      for (int s = 0; s < T::STAGES; ++s)
-        if (last_armed[s] >= 0)
-          wait_bounded(bar_full(s), (static_cast<uint32_t>(last_armed[s]) / T::STAGES) & 1u, wc,
-                       kSiteDrainOperands, false);
+      // let every armed load land before the CTA can exit (a pair's loads
+      // complete on the leader's barriers)
+      for (uint32_t i = 0; leader && i < armed; ++i) {
+        if (s == 0) { s = T::STAGES; ph ^= 1u; }
+        --s;
+        wait_bounded(bar_full(s), ph, wc, kSiteDrainOperands, false);
+      }
     }
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0 && leader) {
+    // The whole warp walks the blocks, so that addresses and descriptors stay
+    // in uniform registers, and one elected lane issues.  A 128 x 128 x 128
+    // block takes the tensor core 256 cycles; everything here has to fit.
+    if (leader) {
       constexpr uint32_t idesc = make_idesc_e4m3(T::TM, BN, false, DGRAD);
-      uint32_t cnt = 0;
+      const uint64_t ad0 = make_sdesc_k_sw128(base, 1024);
+      const uint64_t bd0 = DGRAD ? make_sdesc_mn_sw128(base + T::A_BYTES, 16384, 1024)
+                                 : make_sdesc_k_sw128(base + T::A_BYTES, 1024);
+      // 32 of K further: 32 bytes K-major, 32 rows MN-major
+      constexpr uint32_t kStepA = 32 >> 4, kStepB = (DGRAD ? 4096 : 32) >> 4;
+      const bool issue = elect_one();
+      uint32_t s = 0, ph = 0, buf = 0, bph = 1;
       bool ok = true;
       for (int t = unit0; ok && t < a.num_tiles; t += units) {
-        for (int k = 0; k < a.num_kb; ++k, ++cnt) {
-          const int buf = cnt % T::NBUF;
-          if (!wait_bounded(bar_tempty(buf), ((cnt / T::NBUF) & 1u) ^ 1u, wc, kSiteMmaTmemEmpty)) {
-            ok = false;
-            break;
-          }
-          const int s = cnt % T::STAGES;
-          if (!wait_stage<!kPair>(bar_full(s), (cnt / T::STAGES) & 1u, wc, kSiteMmaFull)) {
-            ok = false;
-            break;
-          }
+#pragma unroll 1
+        for (int k = 0; k < a.num_kb; ++k) {
+          ok = wait_bounded(bar_tempty(buf), bph, wc, kSiteMmaTmemEmpty) &&
+               wait_bounded(bar_full(s), ph, wc, kSiteMmaFull);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
           tc_fence_after_sync();
           const uint32_t d = tmem_base + buf * BN;
-          const uint32_t a0 = base + s * T::STAGE_BYTES;
-          const uint32_t b0 = a0 + T::A_BYTES;
+          const uint64_t ad = ad0 + s * (T::STAGE_BYTES >> 4), bd = bd0 + s * (T::STAGE_BYTES >> 4);
+          if (issue) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {   // 32 of K: 32 bytes K-major, 32 rows MN-major
-            const uint64_t ad = make_sdesc_k_sw128(a0 + kk * 32, 1024);
-            const uint64_t bd = DGRAD ? make_sdesc_mn_sw128(b0 + kk * 4096, 16384, 1024)
-                                      : make_sdesc_k_sw128(b0 + kk * 32, 1024);
-            if constexpr (kPair) umma_e4m3_pair(d, ad, bd, idesc, kk != 0);
-            else umma_e4m3(d, ad, bd, idesc, kk != 0);
+            for (int kk = 0; kk < 4; ++kk) {
+              if constexpr (kPair) umma_e4m3_pair(d, ad + kk * kStepA, bd + kk * kStepB, idesc, kk != 0);
+              else umma_e4m3(d, ad + kk * kStepA, bd + kk * kStepB, idesc, kk != 0);
+            }
+            if constexpr (kPair) {
+              umma_commit_pair_mc(bar_empty(s), 0x3);
+              umma_commit_pair_mc(bar_tfull(buf), 0x3);
+            } else {
+              umma_commit(bar_empty(s));
+              umma_commit(bar_tfull(buf));
+            }
           }
-          if constexpr (kPair) {
-            umma_commit_pair_mc(bar_empty(s), 0x3);
-            umma_commit_pair_mc(bar_tfull(buf), 0x3);
-          } else {
-            umma_commit(bar_empty(s));
-            umma_commit(bar_tfull(buf));
-          }
+          if (++s == T::STAGES) { s = 0; ph ^= 1u; }
+          if (++buf == T::NBUF) { buf = 0; bph ^= 1u; }
         }
       }
       // every MMA issued must complete before the tensor memory is freed
-      if constexpr (kPair) umma_commit_pair_mc(bar_drain, 0x1); else umma_commit(bar_drain);
+      if (issue) {
+        if constexpr (kPair) umma_commit_pair_mc(bar_drain, 0x1); else umma_commit(bar_drain);
+      }
       wait_bounded(bar_drain, 0u, wc, kSiteDrainMma, false);
     }
     __syncwarp();
-  } else {
-    // ------------------------------------------------------------ epilogue
-    const int q = warp & 3;                       // TMEM lane quadrant this warp may read
-    const int h = (warp - 2) >> 2;                // half of the tile's columns
-    const uint32_t lane_addr = static_cast<uint32_t>(q * 32) << 16;
-    const uint32_t slab = base + T::OFF_OUT + (warp - 2) * 4096;
-    uint8_t* gslab = gbase + T::OFF_OUT + (warp - 2) * 4096;
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ scales
+    // sa[row][k] sw[column block][k] for the tile's 128 rows, a batch of
+    // blocks at a time.  (Read by the epilogue threads themselves, one block
+    // ahead, their latency bounded the whole kernel: 462 ns per block of a
+    // 128 x 128 tile.)  Rows and column blocks outside count zero.
     uint32_t cnt = 0;
     bool ok = true;
     for (int t = unit0; ok && t < a.num_tiles; t += units) {
       int tm, tn;
       tile_of(t, a, tm, tn);
+      const int row0 = tm * T::TM + static_cast<int>(rank) * kBM + lane;
+      const int wb0 = tn * T::NWB;
+      for (int k0 = 0; k0 < a.num_kb; k0 += T::SC_BATCH, ++cnt) {
+        float ra[4][T::SC_BATCH];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int row = row0 + 32 * j;
+          const float* p = a.sa + static_cast<int64_t>(row < a.m ? row : 0) * a.num_kb + k0;
+#pragma unroll
+          for (int i = 0; i < T::SC_BATCH; ++i)
+            ra[j][i] = row < a.m && k0 + i < a.num_kb ? __ldg(p + i) : 0.0f;
+        }
+        const int b = cnt & 1;
+        const bool good =
+            wait_bounded(bar_sempty(b), ((cnt >> 1) & 1u) ^ 1u, wc, kSiteLoaderEmpty);
+        if (!__all_sync(0xffffffffu, good)) { ok = false; break; }
+#pragma unroll
+        for (int i = 0; i < T::SC_BATCH; ++i)
+#pragma unroll
+          for (int w = 0; w < T::NWB; ++w) {
+            const bool in = k0 + i < a.num_kb && (wb0 + w) * 128 < a.n;
+            const float rw = in ? __ldg(a.sw + static_cast<int64_t>(wb0 + w) * a.sw_n +
+                                        static_cast<int64_t>(k0 + i) * a.sw_k)
+                                : 0.0f;
+            float* dst = scales + ((b * T::SC_BATCH + i) * T::NWB + w) * kBM + lane;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) dst[32 * j] = in ? ra[j][i] * rw : 0.0f;
+          }
+        mbar_arrive(bar_sfull(b));
+      }
+    }
+    __syncwarp();
+  }
+  } else {
+    regs_inc<kRegsEpi>();
+    // ------------------------------------------------------------ epilogue
+    const int q = warp & 3;                       // TMEM lane quadrant this warp may read
+    const int h = (warp - 4) >> 2;                // half of the tile's columns
+    const uint32_t lane_addr = static_cast<uint32_t>(q * 32) << 16;
+    const uint32_t slab = base + T::OFF_OUT + (warp - 4) * 4096;
+    uint8_t* gslab = gbase + T::OFF_OUT + (warp - 4) * 4096;
+    uint32_t buf = 0, bph = 0, sb = 0, sph = 0;
+    bool ok = true;
+    for (int t = unit0; ok && t < a.num_tiles; t += units) {
+      int tm, tn;
+      tile_of(t, a, tm, tn);
       const int row0 = tm * T::TM + static_cast<int>(rank) * kBM + q * 32;
-      const int row = row0 + lane;
       const int col0 = tn * BN + h * T::NC;
-      // this row's scales, and the weight's for this half's block of columns
-      // (a half lies within one block); rows and blocks outside count zero
-      const bool row_ok = row < a.m;
-      const float* sa = a.sa + static_cast<int64_t>(row_ok ? row : 0) * a.num_kb;
-      const bool col_ok = col0 < a.n;
-      const float* sw = a.sw + static_cast<int64_t>(col_ok ? col0 / 128 : 0) * a.sw_n;
-      const bool live = row_ok && col_ok;
       float2 acc[T::NC / 2];
 #pragma unroll
       for (int i = 0; i < T::NC / 2; ++i) acc[i] = make_float2(0.0f, 0.0f);
-      float ra = live ? __ldg(sa) : 0.0f, rw = live ? __ldg(sw) : 0.0f;
-      for (int k = 0; k < a.num_kb; ++k, ++cnt) {
-        const float2 s2 = dup2(ra * rw);
-        if (live && k + 1 < a.num_kb) {   // the next block's scales, ahead of the wait
-          ra = __ldg(sa + k + 1);
-          rw = __ldg(sw + static_cast<int64_t>(k + 1) * a.sw_k);
-        }
-        const int buf = cnt % T::NBUF;
-        const bool good = wait_bounded(bar_tfull(buf), (cnt / T::NBUF) & 1u, wc, kSiteEpiTmemFull);
-        if (!__all_sync(0xffffffffu, good)) { ok = false; break; }
-        tc_fence_after_sync();
-        const uint32_t taddr = tmem_base + lane_addr + buf * BN + h * T::NC;
+      for (int k0 = 0; ok && k0 < a.num_kb; k0 += T::SC_BATCH) {
+        const int kn = min(T::SC_BATCH, a.num_kb - k0);
+        const float* sc_row =
+            scales + (sb * T::SC_BATCH * T::NWB + h * T::NWB / 2) * kBM + q * 32 + lane;
+        ok = __all_sync(0xffffffffu, wait_bounded_inline(bar_sfull(sb), sph, wc, kSiteEpiSlotFull));
+        if (!ok) break;
+#pragma unroll 1
+        for (int k = 0; k < kn; ++k) {
+          const float sc = sc_row[k * T::NWB * kBM];
+          ok = __all_sync(0xffffffffu,
+                          wait_bounded_inline(bar_tfull(buf), bph, wc, kSiteEpiTmemFull));
+          if (!ok) break;
+          tc_fence_after_sync();
+          const uint32_t taddr = tmem_base + lane_addr + buf * BN + h * T::NC;
+          // 16 columns at a time, the next ones in flight while these are added
+          uint32_t r[2][16];
+          tmem_ld_x16(taddr, r[0]);
 #pragma unroll
-        for (int c = 0; c < T::NC / 32; ++c) {
-          uint32_t r[32];
-          tmem_ld_x32(taddr + 32 * c, r);
-          tmem_ld_wait();
-          if (c == T::NC / 32 - 1) {   // this warp has read its part of the buffer
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) {
-              if constexpr (kPair) mbar_arrive_cluster(mapa_shared(bar_tempty(buf), 0));
-              else mbar_arrive(bar_tempty(buf));
+          for (int c = 0; c < T::NC / 16; ++c) {
+            tmem_ld_wait();
+            if (c + 1 < T::NC / 16) {
+              tmem_ld_x16(taddr + 16 * (c + 1), r[(c + 1) & 1]);
+            } else {   // this warp has read its part of the buffer
+              tc_fence_before_sync();
+              __syncwarp();
+              if (lane == 0) {
+                if constexpr (kPair) mbar_arrive_cluster_relaxed(mapa_shared(bar_tempty(buf), 0));
+                else mbar_arrive(bar_tempty(buf));
+              }
             }
-          }
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            acc[c * 16 + i] = fma2(make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])),
-                                   s2, acc[c * 16 + i]);
+            for (int i = 0; i < 8; ++i)
+              fma2_loaded(acc[c * 8 + i], r[c & 1][2 * i], r[c & 1][2 * i + 1], sc);
+          }
+          if (++buf == T::NBUF) { buf = 0; bph ^= 1u; }
         }
+        if (!ok) break;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_sempty(sb));   // the batch's scales are read
+        if (++sb == 2) { sb = 0; sph ^= 1u; }
       }
       if (!ok) break;
       // store through this warp's slab: boxes of 32 rows x 128 bytes
-      if (row0 < a.m && col_ok) {
+      if (row0 < a.m && col0 < a.n) {
         if (a.out_fp32) {
 #pragma unroll
           for (int c = 0; c < T::NC / 32; ++c) {
@@ -347,25 +417,55 @@ template <int CG, int BN, bool DGRAD>
 cudaError_t launch_t(const B128Args& a, int num_sms, cudaStream_t stream) {
   using T = Traits8<CG, BN>;
   auto kern = gemm_b128_kernel<CG, BN, DGRAD>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       T::SMEM_ALLOC);
-  if (e != cudaSuccess) return e;
+  static int ready[64] = {0};        // per device: attributes set; resident pairs known
+  static int max_units[64] = {0};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const bool cached = dev >= 0 && dev < 64 && ready[dev];
+  if (!cached) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         T::SMEM_ALLOC);
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchConfig_t lc = {};
   lc.blockDim = dim3(kThreads8, 1, 1);
   lc.dynamicSmemBytes = T::SMEM_ALLOC;
   lc.stream = stream;
-  const int units = num_sms / CG;
+  cudaLaunchAttribute attr[1];
+  int units = num_sms;
+  if constexpr (CG == 2) {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    units = cached ? max_units[dev] : 0;
+    if (!cached) {
+      lc.gridDim = dim3(2 * (num_sms / 2), 1, 1);
+      cudaError_t e = cudaOccupancyMaxActiveClusters(&units, kern, &lc);
+      if (e != cudaSuccess || units <= 0) return e != cudaSuccess ? e : cudaErrorInvalidConfiguration;
+      if (dev >= 0 && dev < 64) max_units[dev] = units;
+    }
+    units = units < num_sms / 2 ? units : num_sms / 2;
+  }
+  if (!cached && dev >= 0 && dev < 64) ready[dev] = 1;
   lc.gridDim = dim3(CG * (a.num_tiles < units ? a.num_tiles : units), 1, 1);
   return cudaLaunchKernelEx(&lc, kern, a);
+}
+
+template <int CG, int BN>
+cudaError_t launch_dir(bool dgrad, const B128Args& a, int num_sms, cudaStream_t stream) {
+  return dgrad ? launch_t<CG, BN, true>(a, num_sms, stream)
+               : launch_t<CG, BN, false>(a, num_sms, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_gemm_b128(const B128Config& c, bool dgrad, const B128Args& a, int num_sms,
                              cudaStream_t stream) {
-  if (c.cg == 1 && c.bn == 128)
-    return dgrad ? launch_t<1, 128, true>(a, num_sms, stream)
-                 : launch_t<1, 128, false>(a, num_sms, stream);
+  if (c.cg == 1 && c.bn == 128) return launch_dir<1, 128>(dgrad, a, num_sms, stream);
+  if (c.cg == 2 && c.bn == 256) return launch_dir<2, 256>(dgrad, a, num_sms, stream);
   return cudaErrorInvalidValue;
 }
 

@@ -134,6 +134,17 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// True in one lane of a whole, converged warp (the same one every time).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 // ---------------------------------------------------------------------------
 // Named barriers (ids 1..15; id 0 is __syncthreads)
 // ---------------------------------------------------------------------------
@@ -152,6 +163,17 @@ __device__ __forceinline__ bool named_bar_or(uint32_t id, uint32_t nthreads, boo
       : "r"(static_cast<uint32_t>(pred)), "r"(id), "r"(nthreads)
       : "memory");
   return out != 0;
+}
+
+// Registers per thread of the calling warpgroup (four whole warps): given back
+// to, or taken from, what the block was launched with.
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // ---------------------------------------------------------------------------
@@ -287,6 +309,16 @@ __device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, uint32_t (&r)[32]) {
 __device__ __forceinline__ void tmem_ld_wait() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
+// acc += r * s on two lanes, for r just loaded from tensor memory: volatile, so
+// that it keeps its place after the tmem_ld_wait before it.
+__device__ __forceinline__ void fma2_loaded(float2& acc, uint32_t r0, uint32_t r1, float s) {
+  asm volatile(
+      "{.reg .b64 ra, rs, rc;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rs, {%4, %4};\n\tmov.b64 rc, {%0, %1};\n\t"
+      "fma.rn.f32x2 rc, ra, rs, rc;\n\tmov.b64 {%0, %1}, rc;}"
+      : "+f"(acc.x), "+f"(acc.y)
+      : "r"(r0), "r"(r1), "f"(s));
+}
 // Store 32 consecutive 32-bit columns to tensor memory (lane = thread's lane
 // within the warp's lane quadrant), and wait for this thread's stores.
 __device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t (&r)[32]) {
@@ -351,6 +383,14 @@ __device__ __forceinline__ uint32_t mapa_shared(uint32_t addr, uint32_t rank) {
 // Arrive on an mbarrier given by its shared::cluster address (any CTA).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+               : "memory");
+}
+// The same without release semantics, for a thread that has only read (its
+// loads have returned) and whose arrival publishes nothing: a release at
+// cluster scope waits for all of the thread's outstanding memory operations,
+// about 1000 cycles in the 8-bit products' epilogue.
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                : "memory");
 }
 // TMA load into this CTA's shared memory whose completion is signalled on an

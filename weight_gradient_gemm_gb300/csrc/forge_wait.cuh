@@ -31,8 +31,9 @@ enum WaitSite : int {
 // call there (frame set-up, argument moves) sits between two stages' MMAs
 // long enough for the tensor core to run dry: with the call the plain GEMM
 // main loop ran 11 % slower.
-static __device__ __noinline__ bool wait_spin(uint32_t bar, uint32_t parity, const WaitCtx& w,
-                                              int site, bool honor_abort) {
+static __device__ __forceinline__ bool wait_spin_body(uint32_t bar, uint32_t parity,
+                                                      const WaitCtx& w, int site,
+                                                      bool honor_abort) {
   const uint64_t t0 = globaltimer_ns();
   while (true) {
 #pragma unroll 1
@@ -47,10 +48,23 @@ static __device__ __noinline__ bool wait_spin(uint32_t bar, uint32_t parity, con
     }
   }
 }
+static __device__ __noinline__ bool wait_spin(uint32_t bar, uint32_t parity, const WaitCtx& w,
+                                              int site, bool honor_abort) {
+  return wait_spin_body(bar, parity, w, site, honor_abort);
+}
 __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, const WaitCtx& w,
                                              int site, bool honor_abort = true) {
   if (mbar_try_wait(bar, parity)) return true;
   return wait_spin(bar, parity, w, site, honor_abort);
+}
+
+// The same with the loop inlined, for threads that hold most of their registers
+// across the wait: a call would have to save them.
+__device__ __forceinline__ bool wait_bounded_inline(uint32_t bar, uint32_t parity,
+                                                    const WaitCtx& w, int site,
+                                                    bool honor_abort = true) {
+  if (mbar_try_wait(bar, parity)) return true;
+  return wait_spin_body(bar, parity, w, site, honor_abort);
 }
 
 // The operand-stage waits of the producer and the MMA issuer.  On one CTA

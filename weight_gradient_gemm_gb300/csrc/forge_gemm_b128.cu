@@ -45,15 +45,21 @@ struct Traits8 {
   static constexpr int STAGE_BYTES = A_BYTES + BNL * 128;
   static constexpr int OUT_BYTES = kEpiWarps * 4096;   // one 32-row slab of 128-byte rows a warp
   static constexpr int STAGES = 5;
-  static constexpr int NBUF = 512 / BN;                // TMEM accumulators
+  // The tile's accumulator is cut into pieces of 128 columns with TMEM buffers
+  // of their own, so that a piece's next product waits for the warps that read
+  // that piece only.
+  static constexpr int PIECES = BN / 128;
+  static constexpr int NBUF = 4 / PIECES;              // buffers per piece (512 columns in all)
+  static constexpr int PIECE_WARPS = kEpiWarps / PIECES;
   static constexpr int NWB = BN / 128;                 // weight blocks across the tile
   static constexpr int SC_BATCH = 8;                   // 128-blocks whose scales move together
   static constexpr int SC_BYTES = 2 * SC_BATCH * NWB * kBM * 4;
   static constexpr int NC = BN / 2;                    // columns per epilogue thread
+  static constexpr int GROUPS = NC / 64;               // runs of 64 neighbouring columns among them
   static constexpr int OFF_OUT = STAGES * STAGE_BYTES;
   static constexpr int OFF_SC = OFF_OUT + OUT_BYTES;
   static constexpr int OFF_BARS = OFF_SC + SC_BYTES;
-  static constexpr int NUM_BARS = 2 * STAGES + 2 * NBUF + 5;
+  static constexpr int NUM_BARS = 2 * STAGES + 8 + 5;
   static constexpr int OFF_TMEM = OFF_BARS + 8 * NUM_BARS;
   static constexpr int SMEM_USED = OFF_TMEM + 8;
   static constexpr int SMEM_ALLOC = SMEM_USED + 1024 < kSmemMax ? SMEM_USED + 1024 : kSmemMax;
@@ -92,11 +98,12 @@ __global__ void __launch_bounds__(kThreads8, 1) gemm_b128_kernel(const __grid_co
   const uint32_t bars = base + T::OFF_BARS;
   auto bar_full = [&](int s) { return bars + 8u * s; };
   auto bar_empty = [&](int s) { return bars + 8u * (T::STAGES + s); };
+  // b: one of the four TMEM buffers, piece * NBUF + buffer
   auto bar_tfull = [&](int b) { return bars + 8u * (2 * T::STAGES + b); };
-  auto bar_tempty = [&](int b) { return bars + 8u * (2 * T::STAGES + T::NBUF + b); };
-  auto bar_sfull = [&](int b) { return bars + 8u * (2 * T::STAGES + 2 * T::NBUF + b); };
-  auto bar_sempty = [&](int b) { return bars + 8u * (2 * T::STAGES + 2 * T::NBUF + 2 + b); };
-  const uint32_t bar_drain = bars + 8u * (2 * T::STAGES + 2 * T::NBUF + 4);
+  auto bar_tempty = [&](int b) { return bars + 8u * (2 * T::STAGES + 4 + b); };
+  auto bar_sfull = [&](int b) { return bars + 8u * (2 * T::STAGES + 8 + b); };
+  auto bar_sempty = [&](int b) { return bars + 8u * (2 * T::STAGES + 10 + b); };
+  const uint32_t bar_drain = bars + 8u * (2 * T::STAGES + 12);
   float* scales = reinterpret_cast<float*>(gbase + T::OFF_SC);   // [2][SC_BATCH][NWB][128]
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(gbase + T::OFF_TMEM + 4);
   const WaitCtx wc{abort_flag, a.err, a.err_site, a.timeout_ns};
@@ -106,9 +113,9 @@ __global__ void __launch_bounds__(kThreads8, 1) gemm_b128_kernel(const __grid_co
       mbar_init(bar_full(s), 1);
       mbar_init(bar_empty(s), 1);
     }
-    for (int b = 0; b < T::NBUF; ++b) {
+    for (int b = 0; b < 4; ++b) {
       mbar_init(bar_tfull(b), 1);
-      mbar_init(bar_tempty(b), CG * kEpiWarps);
+      mbar_init(bar_tempty(b), CG * T::PIECE_WARPS);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(bar_sfull(b), 32);
@@ -199,39 +206,47 @@ __global__ void __launch_bounds__(kThreads8, 1) gemm_b128_kernel(const __grid_co
     // in uniform registers, and one elected lane issues.  A 128 x 128 x 128
     // block takes the tensor core 256 cycles; everything here has to fit.
     if (leader) {
-      constexpr uint32_t idesc = make_idesc_e4m3(T::TM, BN, false, DGRAD);
+      constexpr uint32_t idesc = make_idesc_e4m3(T::TM, 128, false, DGRAD);
       const uint64_t ad0 = make_sdesc_k_sw128(base, 1024);
       const uint64_t bd0 = DGRAD ? make_sdesc_mn_sw128(base + T::A_BYTES, 16384, 1024)
                                  : make_sdesc_k_sw128(base + T::A_BYTES, 1024);
       // 32 of K further: 32 bytes K-major, 32 rows MN-major
       constexpr uint32_t kStepA = 32 >> 4, kStepB = (DGRAD ? 4096 : 32) >> 4;
+      // 64 of each CTA's columns further (pairs): 64 rows K-major, 64 bytes MN-major
+      constexpr uint32_t kPieceB = (DGRAD ? 64 : 8192) >> 4;
       const bool issue = elect_one();
       uint32_t s = 0, ph = 0, buf = 0, bph = 1;
       bool ok = true;
       for (int t = unit0; ok && t < a.num_tiles; t += units) {
 #pragma unroll 1
         for (int k = 0; k < a.num_kb; ++k) {
-          ok = wait_bounded(bar_tempty(buf), bph, wc, kSiteMmaTmemEmpty) &&
-               wait_bounded(bar_full(s), ph, wc, kSiteMmaFull);
-          ok = __all_sync(0xffffffffu, ok);
+          ok = __all_sync(0xffffffffu, wait_bounded(bar_full(s), ph, wc, kSiteMmaFull));
           if (!ok) break;
-          tc_fence_after_sync();
-          const uint32_t d = tmem_base + buf * BN;
           const uint64_t ad = ad0 + s * (T::STAGE_BYTES >> 4), bd = bd0 + s * (T::STAGE_BYTES >> 4);
-          if (issue) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-              if constexpr (kPair) umma_e4m3_pair(d, ad + kk * kStepA, bd + kk * kStepB, idesc, kk != 0);
-              else umma_e4m3(d, ad + kk * kStepA, bd + kk * kStepB, idesc, kk != 0);
-            }
-            if constexpr (kPair) {
-              umma_commit_pair_mc(bar_empty(s), 0x3);
-              umma_commit_pair_mc(bar_tfull(buf), 0x3);
-            } else {
-              umma_commit(bar_empty(s));
-              umma_commit(bar_tfull(buf));
+          for (int pc = 0; pc < T::PIECES; ++pc) {
+            const int b = pc * T::NBUF + buf;
+            ok = ok && __all_sync(0xffffffffu,
+                                  wait_bounded(bar_tempty(b), bph, wc, kSiteMmaTmemEmpty));
+            if (!ok) break;
+            tc_fence_after_sync();
+            if (issue) {
+              const uint32_t d = tmem_base + b * 128;
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk) {
+                const uint64_t adk = ad + kk * kStepA, bdk = bd + pc * kPieceB + kk * kStepB;
+                if constexpr (kPair) umma_e4m3_pair(d, adk, bdk, idesc, kk != 0);
+                else umma_e4m3(d, adk, bdk, idesc, kk != 0);
+              }
+              if constexpr (kPair) umma_commit_pair_mc(bar_tfull(b), 0x3);
+              else umma_commit(bar_tfull(b));
+              if (pc == T::PIECES - 1) {   // frees the stage once every MMA above has read it
+                if constexpr (kPair) umma_commit_pair_mc(bar_empty(s), 0x3);
+                else umma_commit(bar_empty(s));
+              }
             }
           }
+          if (!ok) break;
           if (++s == T::STAGES) { s = 0; ph ^= 1u; }
           if (++buf == T::NBUF) { buf = 0; bph ^= 1u; }
         }
@@ -291,34 +306,43 @@ __global__ void __launch_bounds__(kThreads8, 1) gemm_b128_kernel(const __grid_co
     regs_inc<kRegsEpi>();
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;                       // TMEM lane quadrant this warp may read
-    const int h = (warp - 4) >> 2;                // half of the tile's columns
+    const int h = (warp - 4) >> 2;                // piece (pairs), or half of the one piece
     const uint32_t lane_addr = static_cast<uint32_t>(q * 32) << 16;
     const uint32_t slab = base + T::OFF_OUT + (warp - 4) * 4096;
     uint8_t* gslab = gbase + T::OFF_OUT + (warp - 4) * 4096;
+    const uint32_t bpiece = T::PIECES == 1 ? 0 : h * T::NBUF;   // first buffer of this warp's piece
     uint32_t buf = 0, bph = 0, sb = 0, sph = 0;
     bool ok = true;
     for (int t = unit0; ok && t < a.num_tiles; t += units) {
       int tm, tn;
       tile_of(t, a, tm, tn);
       const int row0 = tm * T::TM + static_cast<int>(rank) * kBM + q * 32;
-      const int col0 = tn * BN + h * T::NC;
+      // A pair's piece holds 64 columns of each CTA's 128, so of both weight
+      // blocks: columns p * 64 and 128 + p * 64 of the tile.
+      const int col0 = tn * BN + h * 64;
       float2 acc[T::NC / 2];
 #pragma unroll
       for (int i = 0; i < T::NC / 2; ++i) acc[i] = make_float2(0.0f, 0.0f);
+      bool ready = false;   // the next accumulator has been seen complete
       for (int k0 = 0; ok && k0 < a.num_kb; k0 += T::SC_BATCH) {
         const int kn = min(T::SC_BATCH, a.num_kb - k0);
-        const float* sc_row =
-            scales + (sb * T::SC_BATCH * T::NWB + h * T::NWB / 2) * kBM + q * 32 + lane;
+        const float* sc_row = scales + sb * T::SC_BATCH * T::NWB * kBM + q * 32 + lane;
         ok = __all_sync(0xffffffffu, wait_bounded_inline(bar_sfull(sb), sph, wc, kSiteEpiSlotFull));
         if (!ok) break;
 #pragma unroll 1
         for (int k = 0; k < kn; ++k) {
-          const float sc = sc_row[k * T::NWB * kBM];
-          ok = __all_sync(0xffffffffu,
-                          wait_bounded_inline(bar_tfull(buf), bph, wc, kSiteEpiTmemFull));
-          if (!ok) break;
+          float sc[T::GROUPS];
+#pragma unroll
+          for (int g = 0; g < T::GROUPS; ++g) sc[g] = sc_row[(k * T::NWB + g) * kBM];
+          const uint32_t b = bpiece + buf;
+          if (!__all_sync(0xffffffffu, ready)) {
+            ok = __all_sync(0xffffffffu,
+                            wait_bounded_inline(bar_tfull(b), bph, wc, kSiteEpiTmemFull));
+            if (!ok) break;
+          }
           tc_fence_after_sync();
-          const uint32_t taddr = tmem_base + lane_addr + buf * BN + h * T::NC;
+          const uint32_t taddr = tmem_base + lane_addr + b * 128 + (T::PIECES == 1 ? h * 64 : 0);
+          if (++buf == T::NBUF) { buf = 0; bph ^= 1u; }
           // 16 columns at a time, the next ones in flight while these are added
           uint32_t r[2][16];
           tmem_ld_x16(taddr, r[0]);
@@ -331,15 +355,16 @@ __global__ void __launch_bounds__(kThreads8, 1) gemm_b128_kernel(const __grid_co
               tc_fence_before_sync();
               __syncwarp();
               if (lane == 0) {
-                if constexpr (kPair) mbar_arrive_cluster_relaxed(mapa_shared(bar_tempty(buf), 0));
-                else mbar_arrive(bar_tempty(buf));
+                if constexpr (kPair) mbar_arrive_cluster_relaxed(mapa_shared(bar_tempty(b), 0));
+                else mbar_arrive(bar_tempty(b));
               }
             }
+            // asked early, so that the answer is there when the loop comes round
+            if (c == T::NC / 16 - 2) ready = mbar_test_wait(bar_tfull(bpiece + buf), bph);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              fma2_loaded(acc[c * 8 + i], r[c & 1][2 * i], r[c & 1][2 * i + 1], sc);
+              fma2_loaded(acc[c * 8 + i], r[c & 1][2 * i], r[c & 1][2 * i + 1], sc[c / 4]);
           }
-          if (++buf == T::NBUF) { buf = 0; bph ^= 1u; }
         }
         if (!ok) break;
         __syncwarp();
@@ -348,44 +373,44 @@ __global__ void __launch_bounds__(kThreads8, 1) gemm_b128_kernel(const __grid_co
       }
       if (!ok) break;
       // store through this warp's slab: boxes of 32 rows x 128 bytes
-      if (row0 < a.m && col0 < a.n) {
+#pragma unroll
+      for (int g = 0; g < T::GROUPS; ++g) {
+        const int col = col0 + g * 128;
+        if (row0 >= a.m || col >= a.n) continue;
+        const float2* v = acc + g * 32;
         if (a.out_fp32) {
 #pragma unroll
-          for (int c = 0; c < T::NC / 32; ++c) {
-            if (col0 + 32 * c >= a.n) break;
+          for (int c = 0; c < 2; ++c) {
+            if (col + 32 * c >= a.n) break;
             if (lane == 0) bulk_wait_group_read<0>();
             __syncwarp();
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              const float2 x = acc[c * 16 + 2 * i], y = acc[c * 16 + 2 * i + 1];
+              const float2 x = v[c * 16 + 2 * i], y = v[c * 16 + 2 * i + 1];
               *reinterpret_cast<float4*>(gslab + sw128_off(lane, i)) = make_float4(x.x, x.y, y.x, y.y);
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-              tma_store_2d(&a.out, col0 + 32 * c, row0, slab);
+              tma_store_2d(&a.out, col + 32 * c, row0, slab);
               bulk_commit_group();
             }
           }
         } else {
+          if (lane == 0) bulk_wait_group_read<0>();
+          __syncwarp();
 #pragma unroll
-          for (int c = 0; c < T::NC / 64; ++c) {
-            if (col0 + 64 * c >= a.n) break;
-            if (lane == 0) bulk_wait_group_read<0>();
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float2* x = acc + c * 32 + 4 * i;
-              *reinterpret_cast<uint4*>(gslab + sw128_off(lane, i)) =
-                  make_uint4(pack_bf16x2(x[0].x, x[0].y), pack_bf16x2(x[1].x, x[1].y),
-                             pack_bf16x2(x[2].x, x[2].y), pack_bf16x2(x[3].x, x[3].y));
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              tma_store_2d(&a.out, col0 + 64 * c, row0, slab);
-              bulk_commit_group();
-            }
+          for (int i = 0; i < 8; ++i) {
+            const float2* x = v + 4 * i;
+            *reinterpret_cast<uint4*>(gslab + sw128_off(lane, i)) =
+                make_uint4(pack_bf16x2(x[0].x, x[0].y), pack_bf16x2(x[1].x, x[1].y),
+                           pack_bf16x2(x[2].x, x[2].y), pack_bf16x2(x[3].x, x[3].y));
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(&a.out, col, row0, slab);
+            bulk_commit_group();
           }
         }
       }

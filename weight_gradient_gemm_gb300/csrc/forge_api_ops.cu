@@ -55,12 +55,33 @@ forge_status check_rows(int64_t rows, int64_t cols, int64_t max_cols) {
   return FORGE_OK;
 }
 
-// The products' tile: 256 x 256 on CTA pairs, or 128 x 128 on one CTA where
-// pairs would leave SMs without a tile.
-B128Config choose_b128(int64_t m, int64_t n, const forge_tuning& tune, int num_sms) {
-  int cg = (m + 255) / 256 * ((n + 255) / 256) >= num_sms / 2 ? 2 : 1;
-  if (tune.cta_group) cg = tune.cta_group;
-  return cg == 2 ? B128Config{2, 256} : B128Config{1, 128};
+// The products' tile.
+// Up to 128 tokens the outputs lie along M (forge_gemm_b128_few.cu) and the
+// reduction is split over as many CTAs of a cluster as leave at most one CTA
+// an SM, with two blocks each at least: one token, 4096 -> 4096 (32 tiles),
+// takes 11.3 us unsplit, 8.8 on two CTAs, 7.5 on four and 8.6 on eight.  The
+// input gradient's tile holds 32 tokens at least: with 16, where the weight
+// lies MN-major along M, a block took 440 ns against 310.
+// Beyond, 256 x 256 on CTA pairs or 128 x 128 on single CTAs, by the waves
+// each takes and the measured cycles of a block (770 and 490): 512 tokens,
+// 4096 -> 4096, take 20.5 us on pairs and 16.5 on single CTAs, 1024 tokens
+// 20.7 and 25.0.
+B128Config choose_b128(int64_t m, int64_t n, int64_t num_kb, bool dgrad, const forge_tuning& tune,
+                       int num_sms) {
+  B128Config c{1, 128, 0, 1};
+  if (m <= 128 && tune.cta_group == 0) {
+    c.few = m <= (dgrad ? 0 : 16) ? 16 : (m <= 32 ? 32 : (m <= 64 ? 64 : 128));
+    const int64_t tiles = (n + 127) / 128;
+    while (c.splits < 8 && tiles * c.splits * 2 <= num_sms && num_kb >= 4 * c.splits) c.splits *= 2;
+    if (tune.splits) c.splits = tune.splits >= 8 ? 8 : (tune.splits >= 4 ? 4 : tune.splits >= 2 ? 2 : 1);
+    return c;
+  }
+  const int64_t pairs = num_sms / 2;
+  const int64_t tiles1 = (m + 127) / 128 * ((n + 127) / 128);
+  const int64_t tiles2 = (m + 255) / 256 * ((n + 255) / 256);
+  const int64_t t1 = (tiles1 + num_sms - 1) / num_sms * 490, t2 = (tiles2 + pairs - 1) / pairs * 770;
+  if (tune.cta_group ? tune.cta_group == 2 : t2 < t1) c.cg = 2, c.bn = 256;
+  return c;
 }
 
 // Y = A W^T (forward) or A W (input gradient), A's codes [m, k].
@@ -85,18 +106,18 @@ forge_status product_b128(const void* A, const float* sa, const void* W, const f
   if (st != FORGE_OK) return static_cast<forge_status>(st);
   forge_tuning tune;
   forge_get_tuning(&tune);
-  const B128Config cfg = choose_b128(m, n, tune, d.num_sms);
+  const B128Config cfg = choose_b128(m, n, static_cast<int64_t>(blocks128(k)), dgrad, tune, d.num_sms);
   B128Args a;
   std::memset(&a, 0, sizeof(a));
   const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   const uint32_t bnl = cfg.bn / cfg.cg;
   const bool maps =
-      host_map(&a.a, A, u8, uk, um, uk, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B) &&
+      host_map(&a.a, A, u8, uk, um, uk, 128, cfg.few ? cfg.few : 128, CU_TENSOR_MAP_SWIZZLE_128B) &&
       (dgrad ? host_map(&a.b, W, u8, un, uk, un, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B)
              : host_map(&a.b, W, u8, uk, un, uk, 128, bnl, CU_TENSOR_MAP_SWIZZLE_128B)) &&
-      host_map(&a.out, out,
+      (cfg.few || host_map(&a.out, out,
                es == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, un, um,
-               un * es, static_cast<uint32_t>(128 / es), 32, CU_TENSOR_MAP_SWIZZLE_128B);
+               un * es, static_cast<uint32_t>(128 / es), 32, CU_TENSOR_MAP_SWIZZLE_128B));
   if (!maps) return FORGE_ERR_LAUNCH;
   a.sa = sa;
   a.sw = sw;
@@ -105,17 +126,21 @@ forge_status product_b128(const void* A, const float* sa, const void* W, const f
   a.num_kb = static_cast<int32_t>(blocks128(k));
   a.sw_n = dgrad ? 1 : a.num_kb;                              // sw [d_out / 128][d_in / 128]
   a.sw_k = dgrad ? static_cast<int32_t>(blocks128(n)) : 1;
-  const int64_t tm = 128 * cfg.cg, tiles_m = (m + tm - 1) / tm, tiles_n = (n + cfg.bn - 1) / cfg.bn;
+  const int64_t tm = 128 * cfg.cg, tiles_m = cfg.few ? 1 : (m + tm - 1) / tm, tiles_n = (n + cfg.bn - 1) / cfg.bn;
   if (tiles_m * tiles_n > kMaxIndex / 2) return FORGE_ERR_SHAPE;
   a.tiles_m = static_cast<int32_t>(tiles_m);
   a.tiles_n = static_cast<int32_t>(tiles_n);
   a.num_tiles = static_cast<int32_t>(tiles_m * tiles_n);
   a.group_m = 8;
   a.out_fp32 = es == 4;
+  a.out_ptr = out;
+  a.splits = cfg.splits;
   a.err = d.err;
   a.err_site = d.err_site;
   a.timeout_ns = d.timeout_ns;
-  return status(launch_gemm_b128(cfg, dgrad, a, d.num_sms, static_cast<cudaStream_t>(stream)));
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  return status(cfg.few ? launch_gemm_b128_few(cfg.few, dgrad, a, cs)
+                        : launch_gemm_b128(cfg, dgrad, a, d.num_sms, cs));
 }
 
 }  // namespace

@@ -56,6 +56,9 @@ struct Traits8 {
   static constexpr int SC_BYTES = 2 * SC_BATCH * NWB * kBM * 4;
   static constexpr int NC = BN / 2;                    // columns per epilogue thread
   static constexpr int GROUPS = NC / 64;               // runs of 64 neighbouring columns among them
+  // columns per tensor-memory load: 32 where two of them fit beside the sums
+  // (with 128 sums they spill, and the kernel ran 19 % slower)
+  static constexpr int LD = NC == 64 ? 32 : 16;
   static constexpr int OFF_OUT = STAGES * STAGE_BYTES;
   static constexpr int OFF_SC = OFF_OUT + OUT_BYTES;
   static constexpr int OFF_BARS = OFF_SC + SC_BYTES;
@@ -111,7 +114,7 @@ __global__ void __launch_bounds__(kThreads8, 1) gemm_b128_kernel(const __grid_co
   if (threadIdx.x == 0) {
     for (int s = 0; s < T::STAGES; ++s) {
       mbar_init(bar_full(s), 1);
-      mbar_init(bar_empty(s), 1);
+      mbar_init(bar_empty(s), 2);   // both issuers
     }
     for (int b = 0; b < 4; ++b) {
       mbar_init(bar_tfull(b), 1);
@@ -121,7 +124,7 @@ __global__ void __launch_bounds__(kThreads8, 1) gemm_b128_kernel(const __grid_co
       mbar_init(bar_sfull(b), 32);
       mbar_init(bar_sempty(b), kEpiWarps);
     }
-    mbar_init(bar_drain, 1);
+    mbar_init(bar_drain, 2);
     *abort_flag = 0u;
     fence_mbarrier_init();
   }
@@ -191,20 +194,27 @@ __global__ void __launch_bounds__(kThreads8, 1) gemm_b128_kernel(const __grid_co
           if (++s == T::STAGES) { s = 0; ph ^= 1u; }
         }
       }
-      // let every armed load land before the CTA can exit (a pair's loads
-      // complete on the leader's barriers)
-      for (uint32_t i = 0; leader && i < armed; ++i) {
+      // Before the CTA can exit, every stage's last release has to arrive (on a
+      // pair the leader's MMAs signal it from afar); after a timeout, every
+      // load that is under way has to land (a pair's complete on the leader's
+      // barriers).
+      for (uint32_t i = 0; i < armed; ++i) {
         if (s == 0) { s = T::STAGES; ph ^= 1u; }
         --s;
-        wait_bounded(bar_full(s), ph, wc, kSiteDrainOperands, false);
+        const bool freed = ok && wait_bounded(bar_empty(s), ph, wc, kSiteDrainOperands);
+        if (!freed && leader) wait_bounded(bar_full(s), ph, wc, kSiteDrainOperands, false);
       }
     }
     __syncwarp();
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
-    // The whole warp walks the blocks, so that addresses and descriptors stay
-    // in uniform registers, and one elected lane issues.  A 128 x 128 x 128
-    // block takes the tensor core 256 cycles; everything here has to fit.
+  } else if (warp == 1 || warp == 3) {
+    // ------------------------------------------------------------ MMA issuers
+    // A product costs its issuing thread about 39 cycles, a commit 41 and a
+    // wait that is ready 60, so one thread's 8 products, 3 commits and 3 waits
+    // per block of a pair (634 cycles measured) would be slower than the tensor
+    // core (512).  Two warps share them: each a piece of a pair's tile, or
+    // every other block of a single CTA's.  They walk the blocks with the
+    // whole warp, so that addresses and descriptors stay in uniform registers,
+    // and one elected lane issues.
     if (leader) {
       constexpr uint32_t idesc = make_idesc_e4m3(T::TM, 128, false, DGRAD);
       const uint64_t ad0 = make_sdesc_k_sw128(base, 1024);
@@ -215,38 +225,49 @@ __global__ void __launch_bounds__(kThreads8, 1) gemm_b128_kernel(const __grid_co
       // 64 of each CTA's columns further (pairs): 64 rows K-major, 64 bytes MN-major
       constexpr uint32_t kPieceB = (DGRAD ? 64 : 8192) >> 4;
       const bool issue = elect_one();
-      uint32_t s = 0, ph = 0, buf = 0, bph = 1;
+      const uint32_t me = warp >> 1;   // issuer 0 or 1
+      const uint32_t pc = T::PIECES == 1 ? 0 : me;
+      uint32_t s = 0, ph = 0, buf = 0, bph = 1, turn = 0;
       bool ok = true;
       for (int t = unit0; ok && t < a.num_tiles; t += units) {
 #pragma unroll 1
         for (int k = 0; k < a.num_kb; ++k) {
-          ok = __all_sync(0xffffffffu, wait_bounded(bar_full(s), ph, wc, kSiteMmaFull));
+          // Both issuers wait for every block's stage and release it, also where
+          // the block is the other's: a stage goes from one to the other, and a
+          // parity wait that skipped or lagged a phase would take another for
+          // its own.  (TMEM buffers stay with one issuer: their number is even.)
+          const bool mine = T::PIECES > 1 || turn == me;
+          const uint32_t b = pc * T::NBUF + buf;
+          ok = wait_bounded(bar_full(s), ph, wc, kSiteMmaFull) &&
+               (!mine || wait_bounded(bar_tempty(b), bph, wc, kSiteMmaTmemEmpty));
+          ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          const uint64_t ad = ad0 + s * (T::STAGE_BYTES >> 4), bd = bd0 + s * (T::STAGE_BYTES >> 4);
-#pragma unroll
-          for (int pc = 0; pc < T::PIECES; ++pc) {
-            const int b = pc * T::NBUF + buf;
-            ok = ok && __all_sync(0xffffffffu,
-                                  wait_bounded(bar_tempty(b), bph, wc, kSiteMmaTmemEmpty));
-            if (!ok) break;
+          if (mine) {
             tc_fence_after_sync();
+            const uint64_t ad = ad0 + s * (T::STAGE_BYTES >> 4);
+            const uint64_t bd = bd0 + s * (T::STAGE_BYTES >> 4) + pc * kPieceB;
+            const uint32_t d = tmem_base + b * 128;
             if (issue) {
-              const uint32_t d = tmem_base + b * 128;
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk) {
-                const uint64_t adk = ad + kk * kStepA, bdk = bd + pc * kPieceB + kk * kStepB;
-                if constexpr (kPair) umma_e4m3_pair(d, adk, bdk, idesc, kk != 0);
-                else umma_e4m3(d, adk, bdk, idesc, kk != 0);
+                if constexpr (kPair)
+                  umma_e4m3_pair(d, ad + kk * kStepA, bd + kk * kStepB, idesc, kk != 0);
+                else
+                  umma_e4m3(d, ad + kk * kStepA, bd + kk * kStepB, idesc, kk != 0);
               }
-              if constexpr (kPair) umma_commit_pair_mc(bar_tfull(b), 0x3);
-              else umma_commit(bar_tfull(b));
-              if (pc == T::PIECES - 1) {   // frees the stage once every MMA above has read it
-                if constexpr (kPair) umma_commit_pair_mc(bar_empty(s), 0x3);
-                else umma_commit(bar_empty(s));
+              // the stage is free, and the piece complete, once these have run
+              if constexpr (kPair) {
+                umma_commit_pair_mc(bar_empty(s), 0x3);
+                umma_commit_pair_mc(bar_tfull(b), 0x3);
+              } else {
+                umma_commit(bar_empty(s));
+                umma_commit(bar_tfull(b));
               }
             }
+          } else if (issue) {
+            mbar_arrive(bar_empty(s));
           }
-          if (!ok) break;
+          turn ^= 1u;
           if (++s == T::STAGES) { s = 0; ph ^= 1u; }
           if (++buf == T::NBUF) { buf = 0; bph ^= 1u; }
         }
@@ -343,14 +364,14 @@ __global__ void __launch_bounds__(kThreads8, 1) gemm_b128_kernel(const __grid_co
           tc_fence_after_sync();
           const uint32_t taddr = tmem_base + lane_addr + b * 128 + (T::PIECES == 1 ? h * 64 : 0);
           if (++buf == T::NBUF) { buf = 0; bph ^= 1u; }
-          // 16 columns at a time, the next ones in flight while these are added
-          uint32_t r[2][16];
-          tmem_ld_x16(taddr, r[0]);
+          // some columns at a time, the next ones in flight while these are added
+          uint32_t r[2][T::LD];
+          tmem_ld(taddr, r[0]);
 #pragma unroll
-          for (int c = 0; c < T::NC / 16; ++c) {
+          for (int c = 0; c < T::NC / T::LD; ++c) {
             tmem_ld_wait();
-            if (c + 1 < T::NC / 16) {
-              tmem_ld_x16(taddr + 16 * (c + 1), r[(c + 1) & 1]);
+            if (c + 1 < T::NC / T::LD) {
+              tmem_ld(taddr + T::LD * (c + 1), r[(c + 1) & 1]);
             } else {   // this warp has read its part of the buffer
               tc_fence_before_sync();
               __syncwarp();
@@ -360,10 +381,11 @@ __global__ void __launch_bounds__(kThreads8, 1) gemm_b128_kernel(const __grid_co
               }
             }
             // asked early, so that the answer is there when the loop comes round
-            if (c == T::NC / 16 - 2) ready = mbar_test_wait(bar_tfull(bpiece + buf), bph);
+            if (c == T::NC / T::LD - 2) ready = mbar_test_wait(bar_tfull(bpiece + buf), bph);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              fma2_loaded(acc[c * 8 + i], r[c & 1][2 * i], r[c & 1][2 * i + 1], sc[c / 4]);
+            for (int i = 0; i < T::LD / 2; ++i)
+              fma2_loaded(acc[c * (T::LD / 2) + i], r[c & 1][2 * i], r[c & 1][2 * i + 1],
+                          sc[c * T::LD / 64]);
           }
         }
         if (!ok) break;

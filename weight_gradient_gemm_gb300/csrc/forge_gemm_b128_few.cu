@@ -1,0 +1,327 @@
+// The 8-bit products of a linear layer (see forge_gemm_b128.cu) for few tokens,
+// where reading the weight is all the time there is:
+//   out[t][o] = sum_b (sx[t][b] sw(o, b)) P_b[t][o].
+//
+// The operands change places: 128 outputs (rows of the weight, or its columns
+// for the input gradient) lie along the MMA's M and the tokens along its N, 16
+// to 128 of them, so a block's accumulator is as small as the tokens are few
+// and the weight's scale is one number per block.  To keep every SM loading,
+// the reduction is split over the CTAs of a cluster (up to 8): each walks its
+// share of the blocks, then sends slices of its partial sums to the CTAs that
+// own them, through distributed shared memory, and the owners add the shares
+// in a fixed order and store.  One launch, no workspace, the same result on
+// every run.
+//
+// Warp roles: 0 loads (TMA), 1 issues the MMAs, 2 multiplies the scales, from
+// 4 on the epilogue (the 32 outputs of a TMEM lane quadrant and up to 64
+// tokens a warp).  Every wait is bounded.
+#include <cuda_bf16.h>
+
+#include "forge_internal.h"
+#include "forge_ptx.cuh"
+#include "forge_wait.cuh"
+
+namespace forge {
+namespace {
+
+template <int NT>
+struct Few {
+  static constexpr int EPI = NT <= 64 ? 4 : 8;          // epilogue warps
+  static constexpr int THREADS = 128 + 32 * EPI;
+  static constexpr int NC = NT <= 64 ? NT : 64;         // tokens per epilogue thread
+  static constexpr int A_BYTES = kBM * 128;
+  static constexpr int STAGE_BYTES = A_BYTES + NT * 128;
+  static constexpr int STAGES = NT <= 16 ? 5 : 4;
+  static constexpr int NBUF = NT <= 32 ? 8 : (NT == 64 ? 4 : 2);   // TMEM accumulators
+  static constexpr int TMEM_COLS = NT * NBUF;           // 128 or 256: two CTAs fit an SM
+  static constexpr int SC_BATCH = 8;
+  static constexpr int SC_BYTES = 2 * SC_BATCH * NT * 4;
+  static constexpr int PART_BYTES = NT * kBM * 4;       // one tile of fp32 sums
+  // The shares arrive in a buffer of their own for few tokens; for more they
+  // take the place of the operand stages, once every CTA is done with them.
+  static constexpr bool ALIAS = NT > 32;
+  static constexpr int OFF_SC = STAGES * STAGE_BYTES;
+  static constexpr int OFF_PART = ALIAS ? 0 : OFF_SC + SC_BYTES;
+  static constexpr int OFF_BARS = OFF_SC + SC_BYTES + (ALIAS ? 0 : PART_BYTES);
+  static constexpr int NUM_BARS = 2 * STAGES + 2 * NBUF + 5;
+  static constexpr int OFF_TMEM = OFF_BARS + 8 * NUM_BARS;
+  static constexpr int SMEM_USED = OFF_TMEM + 8;
+  static constexpr int SMEM_ALLOC = SMEM_USED + 1024;
+  static_assert(!ALIAS || PART_BYTES <= STAGES * STAGE_BYTES, "shares fit the stages");
+  static_assert(NT > 64 || 2 * SMEM_ALLOC <= 228 * 1024 - 2 * 1024, "two CTAs an SM");
+};
+
+__device__ __forceinline__ void store_out(const B128Args& a, int64_t idx, float v) {
+  if (a.out_fp32) reinterpret_cast<float*>(a.out_ptr)[idx] = v;
+  else reinterpret_cast<__nv_bfloat16*>(a.out_ptr)[idx] = __float2bfloat16_rn(v);
+}
+
+template <int NT, bool DGRAD>
+__global__ void __launch_bounds__(Few<NT>::THREADS, NT <= 64 ? 2 : 1)
+    gemm_b128_few_kernel(const __grid_constant__ B128Args a) {
+  using T = Few<NT>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  // the same offset in every CTA of the cluster: remote stores use it
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* gbase = smem_raw + (base - raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int splits = a.splits;
+  const int rank = splits > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int tile = static_cast<int>(blockIdx.x) / splits;
+  const int per = (a.num_kb + splits - 1) / splits;
+  const int kb = rank * per, ke = min(a.num_kb, kb + per);   // this CTA's blocks (may be none)
+
+  const uint32_t bars = base + T::OFF_BARS;
+  auto bar_full = [&](int s) { return bars + 8u * s; };
+  auto bar_empty = [&](int s) { return bars + 8u * (T::STAGES + s); };
+  auto bar_tfull = [&](int b) { return bars + 8u * (2 * T::STAGES + b); };
+  auto bar_tempty = [&](int b) { return bars + 8u * (2 * T::STAGES + T::NBUF + b); };
+  auto bar_sfull = [&](int b) { return bars + 8u * (2 * T::STAGES + 2 * T::NBUF + b); };
+  auto bar_sempty = [&](int b) { return bars + 8u * (2 * T::STAGES + 2 * T::NBUF + 2 + b); };
+  const uint32_t bar_drain = bars + 8u * (2 * T::STAGES + 2 * T::NBUF + 4);
+  float* scales = reinterpret_cast<float*>(gbase + T::OFF_SC);   // [2][SC_BATCH][NT]
+  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(gbase + T::OFF_TMEM + 4);
+  const WaitCtx wc{abort_flag, a.err, a.err_site, a.timeout_ns};
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < T::STAGES; ++s) {
+      mbar_init(bar_full(s), 1);
+      mbar_init(bar_empty(s), 1);
+    }
+    for (int b = 0; b < T::NBUF; ++b) {
+      mbar_init(bar_tfull(b), 1);
+      mbar_init(bar_tempty(b), T::EPI);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(bar_sfull(b), 32);
+      mbar_init(bar_sempty(b), T::EPI);
+    }
+    mbar_init(bar_drain, 1);
+    *abort_flag = 0u;
+    fence_mbarrier_init();
+    tma_prefetch_desc(&a.a);
+    tma_prefetch_desc(&a.b);
+  }
+  __syncthreads();
+  if (splits > 1) cluster_arrive();   // waited for before the first remote store
+  if (warp == 1) {
+    tmem_alloc(base + T::OFF_TMEM, T::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(gbase + T::OFF_TMEM);
+
+  float2 acc[T::NC / 2];   // epilogue threads: one output, NC tokens
+  if (warp == 0) {
+    if (lane == 0) {
+      const uint64_t wpol = l2_policy_evict_normal(), xpol = l2_policy_evict_last();
+      uint32_t s = 0, ph = 0, armed = 0;
+      for (int k = kb; k < ke; ++k) {
+        if (!wait_bounded(bar_empty(s), ph ^ 1u, wc, kSiteProducerEmpty)) break;
+        const uint32_t dst = base + s * T::STAGE_BYTES;
+        mbar_arrive_expect_tx(bar_full(s), T::STAGE_BYTES);
+        tma_load_2d(dst, &a.b, DGRAD ? tile * 128 : k * 128, DGRAD ? k * 128 : tile * 128,
+                    bar_full(s), wpol);
+        tma_load_2d(dst + T::A_BYTES, &a.a, k * 128, 0, bar_full(s), xpol);
+        if (armed < T::STAGES) ++armed;
+        if (++s == T::STAGES) { s = 0; ph ^= 1u; }
+      }
+      for (uint32_t i = 0; i < armed; ++i) {   // every armed load lands
+        if (s == 0) { s = T::STAGES; ph ^= 1u; }
+        --s;
+        wait_bounded(bar_full(s), ph, wc, kSiteDrainOperands, false);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    constexpr uint32_t idesc = make_idesc_e4m3(128, NT, DGRAD, false);
+    const uint64_t ad0 = DGRAD ? make_sdesc_mn_sw128(base, 16384, 1024)
+                               : make_sdesc_k_sw128(base, 1024);
+    const uint64_t bd0 = make_sdesc_k_sw128(base + T::A_BYTES, 1024);
+    constexpr uint32_t kStepA = (DGRAD ? 4096 : 32) >> 4, kStepB = 32 >> 4;
+    const bool issue = elect_one();
+    uint32_t s = 0, ph = 0, buf = 0, bph = 1;
+#pragma unroll 1
+    for (int k = kb; k < ke; ++k) {
+      const bool ok = wait_bounded(bar_tempty(buf), bph, wc, kSiteMmaTmemEmpty) &&
+                      wait_bounded(bar_full(s), ph, wc, kSiteMmaFull);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after_sync();
+      const uint64_t ad = ad0 + s * (T::STAGE_BYTES >> 4), bd = bd0 + s * (T::STAGE_BYTES >> 4);
+      if (issue) {
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          umma_e4m3(tmem_base + buf * NT, ad + kk * kStepA, bd + kk * kStepB, idesc, kk != 0);
+        umma_commit(bar_empty(s));
+        umma_commit(bar_tfull(buf));
+      }
+      if (++s == T::STAGES) { s = 0; ph ^= 1u; }
+      if (++buf == T::NBUF) { buf = 0; bph ^= 1u; }
+    }
+    if (issue) umma_commit(bar_drain);
+    wait_bounded(bar_drain, 0u, wc, kSiteDrainMma, false);
+    __syncwarp();
+  } else if (warp == 2) {
+    // sx[t][k] sw[tile][k]; tokens past the last count zero
+    uint32_t b = 0, ph = 1;
+    for (int k0 = kb; k0 < ke; k0 += T::SC_BATCH) {
+      const bool good = wait_bounded(bar_sempty(b), ph, wc, kSiteLoaderEmpty);
+      if (!__all_sync(0xffffffffu, good)) break;
+#pragma unroll
+      for (int i = 0; i < T::SC_BATCH; ++i) {
+        const int k = k0 + i;
+        const float rw = k < ke ? __ldg(a.sw + static_cast<int64_t>(tile) * a.sw_n +
+                                        static_cast<int64_t>(k) * a.sw_k)
+                                : 0.0f;
+#pragma unroll
+        for (int t = lane; t < NT; t += 32)
+          scales[(b * T::SC_BATCH + i) * NT + t] =
+              k < ke && t < a.m ? __ldg(a.sa + static_cast<int64_t>(t) * a.num_kb + k) * rw : 0.0f;
+      }
+      mbar_arrive(bar_sfull(b));
+      if (++b == 2) { b = 0; ph ^= 1u; }
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    const int q = warp & 3, h = (warp - 4) >> 2;
+    const uint32_t tcol = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + h * T::NC;
+#pragma unroll
+    for (int i = 0; i < T::NC / 2; ++i) acc[i] = make_float2(0.0f, 0.0f);
+    uint32_t buf = 0, bph = 0, sb = 0, sph = 0;
+    bool ok = true;
+    for (int k0 = kb; ok && k0 < ke; k0 += T::SC_BATCH) {
+      const int kn = min(T::SC_BATCH, ke - k0);
+      const float* sc_row = scales + sb * T::SC_BATCH * NT + h * T::NC;
+      ok = __all_sync(0xffffffffu, wait_bounded_inline(bar_sfull(sb), sph, wc, kSiteEpiSlotFull));
+      if (!ok) break;
+#pragma unroll 1
+      for (int k = 0; k < kn; ++k) {
+        ok = __all_sync(0xffffffffu, wait_bounded_inline(bar_tfull(buf), bph, wc, kSiteEpiTmemFull));
+        if (!ok) break;
+        tc_fence_after_sync();
+#pragma unroll
+        for (int c = 0; c < T::NC / 16; ++c) {
+          uint32_t r[16];
+          tmem_ld_x16(tcol + buf * NT + 16 * c, r);
+          float4 f[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            f[i] = *reinterpret_cast<const float4*>(sc_row + k * NT + 16 * c + 4 * i);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            fma2_loaded(acc[c * 8 + 2 * i], r[4 * i], r[4 * i + 1], make_float2(f[i].x, f[i].y));
+            fma2_loaded(acc[c * 8 + 2 * i + 1], r[4 * i + 2], r[4 * i + 3],
+                        make_float2(f[i].z, f[i].w));
+          }
+        }
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_tempty(buf));
+        if (++buf == T::NBUF) { buf = 0; bph ^= 1u; }
+      }
+      if (!ok) break;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_sempty(sb));
+      if (++sb == 2) { sb = 0; sph ^= 1u; }
+    }
+  }
+
+  // ------------------------------------------------------------ join and store
+  tc_fence_before_sync();
+  if (splits == 1) {
+    __syncthreads();
+    if (warp >= 4 && !*abort_flag) {
+      const int h = (warp - 4) >> 2, o = tile * 128 + (warp & 3) * 32 + lane;
+      if (o < a.n) {
+#pragma unroll
+        for (int i = 0; i < T::NC; ++i) {
+          const int t = h * T::NC + i;
+          if (t < a.m) store_out(a, static_cast<int64_t>(t) * a.n + o, i & 1 ? acc[i / 2].y : acc[i / 2].x);
+        }
+      }
+    }
+  } else {
+    // every CTA has started; with the shares in the stages' place, every CTA's
+    // loads and MMAs are also done
+    __syncthreads();
+    cluster_wait();
+    if (T::ALIAS) cluster_sync_all();
+    const int slice = kBM / splits;   // outputs each CTA of the cluster owns (splits divides 128)
+    if (warp >= 4) {
+      const int h = (warp - 4) >> 2, o = (warp & 3) * 32 + lane;
+      // [rank of the sender][token][output of the slice]
+      const uint32_t dst =
+          mapa_shared(base + T::OFF_PART, o / slice) + 4u * ((rank * NT + h * T::NC) * slice + o % slice);
+#pragma unroll
+      for (int i = 0; i < T::NC; ++i)
+        if (h * T::NC + i < a.m) st_cluster_f32(dst + 4u * i * slice, i & 1 ? acc[i / 2].y : acc[i / 2].x);
+    }
+    cluster_sync_all();
+    if (!*abort_flag) {
+      const float* part = reinterpret_cast<const float*>(gbase + T::OFF_PART);
+      const int total = a.m * slice;
+      for (int e = threadIdx.x; e < total; e += T::THREADS) {
+        const int t = e / slice, j = e - t * slice, o = tile * 128 + rank * slice + j;
+        if (o >= a.n) continue;
+        float v = 0.0f;
+        for (int z = 0; z < splits; ++z) v += part[(z * NT + t) * slice + j];
+        store_out(a, static_cast<int64_t>(t) * a.n + o, v);
+      }
+    }
+  }
+  if (warp == 1) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem_base, T::TMEM_COLS);
+  }
+}
+
+template <int NT, bool DGRAD>
+cudaError_t launch_t(const B128Args& a, cudaStream_t stream) {
+  using T = Few<NT>;
+  auto kern = gemm_b128_few_kernel<NT, DGRAD>;
+  static int ready[64] = {0};   // per device: attributes set
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64 || !ready[dev]) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         T::SMEM_ALLOC);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) ready[dev] = 1;
+  }
+  cudaLaunchConfig_t lc = {};
+  lc.blockDim = dim3(T::THREADS, 1, 1);
+  lc.gridDim = dim3(a.num_tiles * a.splits, 1, 1);
+  lc.dynamicSmemBytes = T::SMEM_ALLOC;
+  lc.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = a.splits;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  lc.attrs = attr;
+  lc.numAttrs = a.splits > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&lc, kern, a);
+}
+
+template <int NT>
+cudaError_t launch_dir(bool dgrad, const B128Args& a, cudaStream_t stream) {
+  return dgrad ? launch_t<NT, true>(a, stream) : launch_t<NT, false>(a, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_gemm_b128_few(int nt, bool dgrad, const B128Args& a, cudaStream_t stream) {
+  switch (nt) {
+    case 16: return launch_dir<16>(dgrad, a, stream);
+    case 32: return launch_dir<32>(dgrad, a, stream);
+    case 64: return launch_dir<64>(dgrad, a, stream);
+    case 128: return launch_dir<128>(dgrad, a, stream);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace forge

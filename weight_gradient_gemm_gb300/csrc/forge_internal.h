@@ -264,15 +264,19 @@ struct B128Args {
   int32_t sw_n, sw_k;      // steps in sw from one column block / reduction block to the next
   int32_t tiles_m, tiles_n, num_tiles, group_m;
   int32_t out_fp32;
+  void* out_ptr;           // few tokens: stored without a map
+  int32_t splits;          // few tokens: CTAs (a cluster) that share a tile's reduction
   int* err;
   int* err_site;
   uint64_t timeout_ns;
 };
-// Box heights of the operand maps and tile sizes of a configuration.
 struct B128Config {
-  int cg, bn;
+  int cg, bn;     // CTAs per tile and its columns
+  int few;        // 0, or the tokens a tile holds when the outputs lie along M
+  int splits;     // few tokens: CTAs per tile
 };
 cudaError_t launch_gemm_b128(const B128Config& c, bool dgrad, const B128Args& a, int num_sms,
                              cudaStream_t stream);
+cudaError_t launch_gemm_b128_few(int nt, bool dgrad, const B128Args& a, cudaStream_t stream);
 
 }  // namespace forge

@@ -306,6 +306,8 @@ __device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, uint32_t (&r)[32]) {
         "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
 }
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld_x16(taddr, r); }
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld_x32(taddr, r); }
 __device__ __forceinline__ void tmem_ld_wait() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
@@ -318,6 +320,15 @@ __device__ __forceinline__ void fma2_loaded(float2& acc, uint32_t r0, uint32_t r
       "fma.rn.f32x2 rc, ra, rs, rc;\n\tmov.b64 {%0, %1}, rc;}"
       : "+f"(acc.x), "+f"(acc.y)
       : "r"(r0), "r"(r1), "f"(s));
+}
+// The same with a factor for each lane.
+__device__ __forceinline__ void fma2_loaded(float2& acc, uint32_t r0, uint32_t r1, float2 s) {
+  asm volatile(
+      "{.reg .b64 ra, rs, rc;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rs, {%4, %5};\n\tmov.b64 rc, {%0, %1};\n\t"
+      "fma.rn.f32x2 rc, ra, rs, rc;\n\tmov.b64 {%0, %1}, rc;}"
+      : "+f"(acc.x), "+f"(acc.y)
+      : "r"(r0), "r"(r1), "f"(s.x), "f"(s.y));
 }
 // Store 32 consecutive 32-bit columns to tensor memory (lane = thread's lane
 // within the warp's lane quadrant), and wait for this thread's stores.
@@ -373,6 +384,17 @@ __device__ __forceinline__ uint32_t cluster_count_x() {
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
                "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The two halves of cluster_sync_all.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Store to another CTA's shared memory (a shared::cluster address).
+__device__ __forceinline__ void st_cluster_f32(uint32_t cluster_addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr), "f"(v) : "memory");
 }
 // The shared::cluster address of the same shared-memory offset in CTA `rank`.
 __device__ __forceinline__ uint32_t mapa_shared(uint32_t addr, uint32_t rank) {

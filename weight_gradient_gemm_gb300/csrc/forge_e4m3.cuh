@@ -43,6 +43,13 @@ __device__ __forceinline__ float max16(float v) {
   return v;
 }
 
+// The same over aligned groups of 8 lanes.
+__device__ __forceinline__ float max8(float v) {
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
 // Eight floats times inv as eight codes (the first in the low byte).
 __device__ __forceinline__ uint2 encode8(const float (&x)[8], float inv) {
   uint32_t c[4];

@@ -13,23 +13,26 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Sum of squares of 8 values as a double: in fp32 where no square can
-// overflow or lose digits to underflow, else element by element in fp64.
-// A sum of at least 2^-100 bounds what underflowed squares could add to it
-// (8 x 2^-126) below its rounding; all-zero vectors, common in embedding
-// gradients, leave before the slow path.
-__device__ __forceinline__ double squares8(const float (&g)[8]) {
-  float s = 0.0f;
+// Sum of squares of N values as a double: in fp32 where no square can overflow
+// or lose digits to underflow, else element by element in fp64.  A sum of at
+// least 2^-100 bounds what underflowed squares could add to it (N x 2^-126)
+// below its rounding; all-zero runs, common in embedding gradients, leave
+// before the slow path.  fp64 runs at 1/64 of the fp32 rate, so a conversion
+// and an addition for every 32 values keep it out of the way.
+template <int N>
+__device__ __forceinline__ double squares(const float (&g)[N]) {
+  float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-  for (int k = 0; k < 8; ++k) s = fmaf(g[k], g[k], s);
-  if (s >= 0x1p-100f && s <= 0x1p126f) return static_cast<double>(s);
+  for (int k = 0; k < N; ++k) s[k & 3] = fmaf(g[k], g[k], s[k & 3]);
+  const float t = (s[0] + s[1]) + (s[2] + s[3]);
+  if (t >= 0x1p-100f && t <= 0x1p126f) return static_cast<double>(t);
   uint32_t any = 0;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) any |= __float_as_uint(g[k]) & 0x7FFFFFFFu;
+  for (int k = 0; k < N; ++k) any |= __float_as_uint(g[k]) & 0x7FFFFFFFu;
   double d = 0.0;
   if (any) {
-#pragma unroll 1
-    for (int k = 0; k < 8; ++k) d += static_cast<double>(g[k]) * static_cast<double>(g[k]);
+#pragma unroll
+    for (int k = 0; k < N; ++k) d += static_cast<double>(g[k]) * static_cast<double>(g[k]);
   }
   return d;
 }
@@ -46,7 +49,8 @@ __device__ __forceinline__ double block_sum(double v) {
   return v;
 }
 
-__device__ __forceinline__ void load8(const void* p, bool bf16, int64_t i8, float (&g)[8]) {
+// Values 8 i8 .. 8 i8 + 7 of a tensor.
+__device__ __forceinline__ void load8(const void* p, bool bf16, int64_t i8, float* g) {
   if (bf16) {
     const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i8);
     const uint32_t u[4] = {v.x, v.y, v.z, v.w};
@@ -74,7 +78,15 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_consta
     const int64_t left = a.numel[lo] - begin;
     const int count = static_cast<int>(left < kNormUnit ? left : kNormUnit);
     const void* p = a.ptr[lo];
-    for (int e = threadIdx.x * 8; e < count; e += kThreads * 8) {
+    // 32 values a thread at a time, in four vectors kThreads apart
+    int e = threadIdx.x * 8;
+    for (; e + 3 * kThreads * 8 + 8 <= count; e += 4 * kThreads * 8) {
+      float g[32];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) load8(p, bf16, (begin + e + j * kThreads * 8) >> 3, g + 8 * j);
+      sum += squares(g);
+    }
+    for (; e < count; e += kThreads * 8) {
       float g[8];
       if (e + 8 <= count) {
         load8(p, bf16, (begin + e) >> 3, g);
@@ -87,7 +99,7 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_consta
                         : reinterpret_cast<const float*>(p)[begin + e + k];
         }
       }
-      sum += squares8(g);
+      sum += squares(g);
     }
   }
   sum = block_sum(sum);

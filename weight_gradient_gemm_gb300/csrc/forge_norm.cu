@@ -205,29 +205,72 @@ __device__ __forceinline__ float amax8(uint4 v) {
   return max_nan(__low2float(m), __high2float(m));
 }
 
-// Blocks of 1 x 128: 16 lanes per block, 8 columns a lane.
-__global__ void __launch_bounds__(256) quantize_rows_kernel(const uint16_t* __restrict__ x,
-                                                            uint8_t* __restrict__ codes,
-                                                            float* __restrict__ scales,
-                                                            int64_t rows, int64_t cols) {
-  const int64_t nblk = (cols + kBlock - 1) / kBlock, total = rows * nblk;
-  const int sub = threadIdx.x & 15;
-  const int64_t groups = static_cast<int64_t>(gridDim.x) * 16;
-  // every lane of a warp takes the same number of trips (the shuffles)
-  for (int64_t b0 = static_cast<int64_t>(blockIdx.x) * 16 + ((threadIdx.x >> 5) << 1); b0 < total;
-       b0 += groups) {
-    const int64_t b = b0 + ((threadIdx.x >> 4) & 1);
-    const int64_t row = b / nblk, col = (b - row * nblk) * kBlock + sub * 8;
-    const bool in = b < total && col < cols;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (in) v = __ldcs(reinterpret_cast<const uint4*>(x + row * cols + col));
-    const BlockScale s = block_scale(max16(amax8(v)));
-    if (in) {
+// Blocks of 1 x 128: 8 lanes per block, two vectors of 8 columns a lane, so
+// that one reduction and one pair of divisions serve 16 of a lane's values.
+constexpr int kQuantUnroll = 4;   // blocks per lane group whose loads are in flight at once
+
+// Rows of whole blocks: the blocks of all rows follow one another, and a
+// warp's groups take 4 x kQuantUnroll neighbouring ones.
+__global__ void __launch_bounds__(256) quantize_blocks_kernel(const uint4* __restrict__ x,
+                                                              uint2* __restrict__ codes,
+                                                              float* __restrict__ scales,
+                                                              int64_t blocks) {
+  const int lane = threadIdx.x & 31, sub = lane & 7;
+  const int64_t b0 =
+      (static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5)) * (4 * kQuantUnroll) + (lane >> 3);
+  uint4 v[kQuantUnroll][2];
+#pragma unroll
+  for (int j = 0; j < kQuantUnroll; ++j) {
+    const int64_t b = b0 + 4 * j;
+    v[j][0] = v[j][1] = make_uint4(0, 0, 0, 0);
+    if (b < blocks) {
+      v[j][0] = __ldcs(x + b * 16 + sub);
+      v[j][1] = __ldcs(x + b * 16 + 8 + sub);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kQuantUnroll; ++j) {
+    const int64_t b = b0 + 4 * j;
+    const BlockScale s = block_scale(max8(max_nan(amax8(v[j][0]), amax8(v[j][1]))));
+    if (b < blocks) {
       float f[8];
-      unpack8(v, f);
-      __stcs(reinterpret_cast<uint2*>(codes + row * cols + col), encode8(f, s.inv));
+      unpack8(v[j][0], f);
+      __stcs(codes + b * 16 + sub, encode8(f, s.inv));
+      unpack8(v[j][1], f);
+      __stcs(codes + b * 16 + 8 + sub, encode8(f, s.inv));
       if (sub == 0) scales[b] = s.scale;
     }
+  }
+}
+
+// Any row length: the last block of a row may be partial.
+__global__ void __launch_bounds__(256) quantize_rows_kernel(const uint4* __restrict__ x,
+                                                            uint2* __restrict__ codes,
+                                                            float* __restrict__ scales,
+                                                            int64_t rows, int nvec) {
+  const int nblk = (nvec + 15) / 16, sub = threadIdx.x & 7;
+  const int64_t total = rows * nblk, groups = static_cast<int64_t>(gridDim.x) * 32;
+  // every lane of a warp takes the same number of trips (the shuffles)
+  for (int64_t b0 = static_cast<int64_t>(blockIdx.x) * 32 + ((threadIdx.x >> 5) << 2); b0 < total;
+       b0 += groups) {
+    const int64_t b = b0 + ((threadIdx.x >> 3) & 3);
+    const int64_t row = total <= INT32_MAX ? static_cast<int>(b) / nblk : b / nblk;
+    const int vec = static_cast<int>(b - row * nblk) * 16 + sub;
+    const bool in0 = b < total && vec < nvec, in1 = b < total && vec + 8 < nvec;
+    const int64_t at = row * nvec + vec;
+    const uint4 v0 = in0 ? __ldcs(x + at) : make_uint4(0, 0, 0, 0);
+    const uint4 v1 = in1 ? __ldcs(x + at + 8) : make_uint4(0, 0, 0, 0);
+    const BlockScale s = block_scale(max8(max_nan(amax8(v0), amax8(v1))));
+    float f[8];
+    if (in0) {
+      unpack8(v0, f);
+      __stcs(codes + at, encode8(f, s.inv));
+    }
+    if (in1) {
+      unpack8(v1, f);
+      __stcs(codes + at + 8, encode8(f, s.inv));
+    }
+    if (in0 && sub == 0) scales[b] = s.scale;
   }
 }
 
@@ -313,9 +356,17 @@ cudaError_t launch_quantize_b128(const uint16_t* x, uint8_t* codes, float* scale
                                  int64_t cols, int block_rows, int num_sms, cudaStream_t stream) {
   const int64_t nblk = (cols + kBlock - 1) / kBlock;
   if (block_rows == 1) {
-    const int64_t want = (rows * nblk + 15) / 16, most = static_cast<int64_t>(num_sms) * 8;
-    quantize_rows_kernel<<<static_cast<int>(want < most ? want : most), 256, 0, stream>>>(
-        x, codes, scales, rows, cols);
+    const uint4* xv = reinterpret_cast<const uint4*>(x);
+    uint2* cv = reinterpret_cast<uint2*>(codes);
+    const int64_t blocks = rows * nblk;
+    const int64_t grid = (blocks + 32 * kQuantUnroll - 1) / (32 * kQuantUnroll);
+    if (cols % kBlock == 0 && grid <= INT32_MAX) {
+      quantize_blocks_kernel<<<static_cast<unsigned>(grid), 256, 0, stream>>>(xv, cv, scales, blocks);
+    } else {
+      const int64_t want = (blocks + 31) / 32, most = static_cast<int64_t>(num_sms) * 8;
+      quantize_rows_kernel<<<static_cast<unsigned>(want < most ? want : most), 256, 0, stream>>>(
+          xv, cv, scales, rows, static_cast<int>(cols / 8));
+    }
   } else {
     const int64_t grid = (rows + kBlock - 1) / kBlock * nblk;
     quantize_tiles_kernel<<<static_cast<unsigned>(grid), 256, 0, stream>>>(x, codes, scales, rows,

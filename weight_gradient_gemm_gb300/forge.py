@@ -6,6 +6,7 @@ fallback: if ``libforge.so`` has not been built, every call raises.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 import re
@@ -987,18 +988,18 @@ def grad_norm(grads, max_norm: float, out: torch.Tensor, *, workspace: torch.Ten
     """out (fp32 [2], on the device) = the global norm of the gradients (fp32 or
     bf16 tensors of any shape) and min(1, max_norm / (norm + 1e-6)), the factor
     adamw_clip applies."""
-    n = len(grads)
-    arr = (ForgeGrad * n)()
     dev = _device_of(out, "out")
-    for i, g in enumerate(grads):
-        if g.dtype not in _GAIN:
-            raise TypeError(f"gradient {i} has dtype {g.dtype}, expected fp32 or bf16")
-        if g.get_device() != dev or not g.is_contiguous():
-            _dense(g, f"gradient {i}")
-            raise ValueError(f"gradient {i} is on {g.device}, out on {out.device}")
-        arr[i] = (g.data_ptr(), g.numel(), _DT[g.dtype])
+    flat = []     # forge_grad records: pointer, size, dtype (and padding)
+    for g in grads:
+        dt = _DT.get(g.dtype)
+        if dt is None or g.get_device() != dev or not g.is_contiguous():
+            if dt is None:
+                raise TypeError(f"a gradient has dtype {g.dtype}, expected fp32 or bf16")
+            _dense(g, "a gradient")
+        flat += (g.data_ptr(), g.numel(), dt)
+    arr = array.array("q", flat)
     _dense(workspace, "workspace")
-    st = lib().forge_grad_norm(ctypes.addressof(arr) if n else None, n, max_norm,
+    st = lib().forge_grad_norm(arr.buffer_info()[0] if flat else None, len(flat) // 3, max_norm,
                                _arg(out, "out", (2,), _F32, dev), workspace.data_ptr(),
                                workspace.nbytes, _raw_stream(stream, dev))
     _check(st, "forge_grad_norm")

@@ -59,7 +59,8 @@ def check_codes(codes, scales, x64, block_rows, rel, absolute):
 
 # ---------------------------------------------------------------- the norm
 NORM_SHAPES = [(1, 8), (1, 4096), (2, 136), (3, 1032), (7, 128), (65, 264), (5, 8200),
-               (3, 16392), (2, 32768), (333, 520), (1300, 64)]
+               (3, 16392), (2, 32768), (333, 520), (1300, 64), (5000, 128), (1251, 1544),
+               (640, 4096), (613, 4104), (610, 8192)]
 
 
 @pytest.mark.parametrize("rows,cols", NORM_SHAPES)

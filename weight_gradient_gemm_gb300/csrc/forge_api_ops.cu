@@ -184,6 +184,7 @@ forge_status forge_rmsnorm(const void* x, const void* residual, const void* gain
   a.rows = rows;
   a.cols = static_cast<int>(cols);
   a.eps = eps;
+  a.wait = NormWait{d.err, d.err_site, d.timeout_ns};
   return status(launch_rmsnorm(a, d.num_sms, static_cast<cudaStream_t>(stream)));
 }
 
@@ -235,6 +236,7 @@ forge_status forge_rmsnorm_backward(const void* dY, const void* h, const void* g
   a.part = static_cast<float*>(workspace);
   a.rows = rows;
   a.cols = static_cast<int>(cols);
+  a.wait = NormWait{d.err, d.err_site, d.timeout_ns};
   return status(launch_rmsnorm_bwd(a, d.num_sms, cs));
 }
 

@@ -199,6 +199,12 @@ bool host_map(CUtensorMap* out, const void* ptr, CUtensorMapDataType dt, uint64_
               uint64_t outer, uint64_t stride_bytes, uint32_t box_inner, uint32_t box_outer,
               CUtensorMapSwizzle sw);
 
+// What a norm kernel's bounded waits report to.
+struct NormWait {
+  int* err;
+  int* err_site;
+  uint64_t timeout_ns;
+};
 // The RMS norm in front of a linear layer (forge_norm.cu).  Null pointers
 // leave an input or output out.
 struct NormArgs {
@@ -214,6 +220,7 @@ struct NormArgs {
   int64_t rows;
   int cols;
   float eps;
+  NormWait wait;
 };
 cudaError_t launch_rmsnorm(const NormArgs& a, int num_sms, cudaStream_t stream);
 
@@ -229,7 +236,9 @@ struct NormBwdArgs {
   float* part;           // [rmsnorm_bwd_blocks][cols] partial sums of dgain
   int64_t rows;
   int cols;
+  NormWait wait;
 };
+// Blocks of a backward call with or without dsum: rows of `part`.
 int rmsnorm_bwd_blocks(int64_t rows, int cols, int num_sms);
 cudaError_t launch_rmsnorm_bwd(const NormBwdArgs& a, int num_sms, cudaStream_t stream);
 // Widest row the norm's kernels hold in registers.

@@ -6,23 +6,26 @@
 
 #include "forge_e4m3.cuh"
 #include "forge_internal.h"
+#include "forge_ptx.cuh"
+#include "forge_wait.cuh"
 
 namespace forge {
 namespace {
 
-// Sum of v over the block, the same in every thread and on every run.  `red`
-// holds one float per warp; a caller that reduces again passes another array
-// (or synchronises in between).
-__device__ __forceinline__ float block_sum(float v, float* red) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  const int lane = threadIdx.x & 31, nw = blockDim.x >> 5;
-  if (lane == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = lane < nw ? red[lane] : 0.0f;
+// Sum of v over a row's threads, the same in every one of them and on every
+// run: a warp, or the whole block with one float per warp in `red` (a caller
+// that reduces again passes another array, or synchronises in between).
+__device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
+}
+__device__ __forceinline__ float block_sum(float v, float* red) {
+  v = warp_sum(v);
+  const int lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+  if (lane == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  return warp_sum(lane < nw ? red[lane] : 0.0f);
 }
 
 __device__ __forceinline__ void load_gain8(const void* gain, int bf16, int v, float (&g)[8]) {
@@ -36,143 +39,389 @@ __device__ __forceinline__ void load_gain8(const void* gain, int bf16, int v, fl
   }
 }
 
+// A row's columns are cut into vectors of 8; thread t of a row's `width`
+// threads owns the vectors t, t + width, ..., so 16 neighbouring lanes hold the
+// 128 columns of a scale.  Three ways to walk the rows share the arithmetic:
+//   a warp per row (up to 1024 columns): no barrier at all;
+//   a block per row: few rows, where every row is in flight at once;
+//   persistent blocks whose rows are copied ahead into shared memory (many
+//   rows): the copies keep HBM busy through the reductions.
+
+// ---------------------------------------------------------------- forward
 //   h = x + residual;  rstd = 1 / sqrt(mean(h^2) + eps);  y = h rstd gain
 // in fp32 from the bf16 inputs (the sum is rounded only where it is stored).
-// One block per row (grid-stride); thread t owns the vectors of 8 columns t,
-// t + threads, ..., so 16 neighbouring lanes hold the 128 columns of a scale.
-template <int VPT>
-__global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormArgs a) {
-  __shared__ float red[2][32];
-  const int nvec = a.cols / 8;
-  const int nblk = (a.cols + kBlock - 1) / kBlock;
-  int parity = 0;
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, parity ^= 1) {
-    const int64_t base = row * nvec;
-    float h[VPT][8];
-    float ss = 0.0f;
+// h of one vector, and its share of the sum of squares.
+__device__ __forceinline__ float norm_h(const NormArgs& a, uint4 x, uint4 r, int64_t at,
+                                        float (&h)[8]) {
+  unpack8(x, h);
+  if (a.residual) {
+    float f[8];
+    unpack8(r, f);
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int v = threadIdx.x + i * blockDim.x;
+    for (int k = 0; k < 8; ++k) h[k] += f[k];
+  }
+  if (a.sum) __stcs(reinterpret_cast<uint4*>(a.sum) + at, pack8(h));
+  float ss = 0.0f;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) h[i][k] = 0.0f;
-      if (v < nvec) {
-        unpack8(__ldcs(reinterpret_cast<const uint4*>(a.x) + base + v), h[i]);
-        if (a.residual) {
-          float r[8];
-          unpack8(__ldcs(reinterpret_cast<const uint4*>(a.residual) + base + v), r);
+  for (int k = 0; k < 8; ++k) ss = fmaf(h[k], h[k], ss);
+  return ss;
+}
+__device__ __forceinline__ float norm_rstd(const NormArgs& a, float ss) {
+  return rsqrtf(__fdiv_rn(ss, static_cast<float>(a.cols)) + a.eps);
+}
+// One vector's outputs.  Every lane of the warp takes part (the shuffles);
+// `in` is false past the row's end.
+__device__ __forceinline__ void norm_out(const NormArgs& a, float (&h)[8], const float (&g)[8],
+                                         float rstd, int64_t row, int v, bool in) {
+  const int64_t at = row * (a.cols / 8) + v;
+  float amax = 0.0f;
+  if (in) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) h[i][k] += r[k];
-        }
-        if (a.sum) __stcs(reinterpret_cast<uint4*>(a.sum) + base + v, pack8(h[i]));
-      }
-#pragma unroll
-      for (int k = 0; k < 8; ++k) ss = fmaf(h[i][k], h[i][k], ss);
+    for (int k = 0; k < 8; ++k) {
+      h[k] = h[k] * rstd * g[k];
+      amax = max_nan(amax, fabsf(h[k]));
     }
-    ss = block_sum(ss, red[parity]);
-    const float rstd = rsqrtf(__fdiv_rn(ss, static_cast<float>(a.cols)) + a.eps);
-    if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int v = threadIdx.x + i * blockDim.x;
-      float amax = 0.0f;
-      if (v < nvec) {
-        float g[8];
-        load_gain8(a.gain, a.gain_bf16, v, g);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          h[i][k] = h[i][k] * rstd * g[k];
-          amax = max_nan(amax, fabsf(h[i][k]));
-        }
-        if (a.y) __stcs(reinterpret_cast<uint4*>(a.y) + base + v, pack8(h[i]));
-      }
-      if (a.codes) {
-        const BlockScale s = block_scale(max16(amax));
-        if (v < nvec) {
-          __stcs(reinterpret_cast<uint2*>(a.codes) + base + v, encode8(h[i], s.inv));
-          if (v % 16 == 0) a.scales[row * nblk + v / 16] = s.scale;
-        }
-      }
+    if (a.y) __stcs(reinterpret_cast<uint4*>(a.y) + at, pack8(h));
+  }
+  if (a.codes) {
+    const BlockScale s = block_scale(max16(amax));
+    if (in) {
+      __stcs(reinterpret_cast<uint2*>(a.codes) + at, encode8(h, s.inv));
+      if (v % 16 == 0) a.scales[row * ((a.cols + kBlock - 1) / kBlock) + v / 16] = s.scale;
     }
   }
 }
 
+// WARP: a warp per row; else a block per row (both grid-stride).
+template <int VPT, bool WARP>
+__global__ void __launch_bounds__(WARP ? 256 : 1024) rmsnorm_kernel(const NormArgs a) {
+  __shared__ float red[2][32];
+  const int nvec = a.cols / 8;
+  const int width = WARP ? 32 : blockDim.x, me = WARP ? threadIdx.x & 31 : threadIdx.x;
+  const int64_t first = WARP ? static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5) : blockIdx.x;
+  const int64_t step = WARP ? static_cast<int64_t>(gridDim.x) * 8 : gridDim.x;
+  int parity = 0;
+  for (int64_t row = first; row < a.rows; row += step, parity ^= 1) {
+    const int64_t base = row * nvec;
+    uint4 x[VPT], r[VPT];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int v = me + i * width;
+      x[i] = r[i] = make_uint4(0, 0, 0, 0);
+      if (v < nvec) {
+        x[i] = __ldcs(reinterpret_cast<const uint4*>(a.x) + base + v);
+        if (a.residual) r[i] = __ldcs(reinterpret_cast<const uint4*>(a.residual) + base + v);
+      }
+    }
+    float h[VPT][8], ss = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+      if (me + i * width < nvec) ss += norm_h(a, x[i], r[i], base + me + i * width, h[i]);
+    ss = WARP ? warp_sum(ss) : block_sum(ss, red[parity]);
+    const float rstd = norm_rstd(a, ss);
+    if (a.rstd && me == 0) a.rstd[row] = rstd;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int v = me + i * width;
+      float g[8];
+      if (v < nvec) load_gain8(a.gain, a.gain_bf16, v, g);
+      norm_out(a, h[i], g, rstd, row, v, v < nvec);
+    }
+  }
+}
+
+// The rows of one persistent block (blockIdx.x, + gridDim.x, ...), copied ahead
+// into a ring of `depth` slots of S rows (one of each input) by bulk copies.
+// A slot is read into registers before the row's reduction, so it is free, and
+// thread 0 refills it, as soon as the reduction's barrier is passed.  A wait
+// that runs out records its error and lets the block run on (its barriers stay
+// matched; what it writes is unspecified).
+template <int S>
+struct RowRing {
+  uint32_t smem, bars, row_bytes;
+  int depth;
+  const uint8_t* src[S];
+  int64_t rows;
+  WaitCtx wc;
+  int slot = 0;
+  uint32_t ph = 0;
+  bool ok = true;
+
+  __device__ uint32_t at(int s, int i) const { return smem + (s * S + i) * row_bytes; }
+  __device__ void fill(int s, int64_t row) const {
+    mbar_arrive_expect_tx(bars + 8u * s, S * row_bytes);
+#pragma unroll
+    for (int i = 0; i < S; ++i)
+      bulk_load(at(s, i), src[i] + row * row_bytes, row_bytes, bars + 8u * s);
+  }
+  // thread 0, before anything is read
+  __device__ void start() const {
+    for (int s = 0; s < depth; ++s) mbar_init(bars + 8u * s, 1);
+    fence_mbarrier_init();
+    int64_t row = blockIdx.x;
+    for (int s = 0; s < depth && row < rows; ++s, row += gridDim.x) fill(s, row);
+  }
+  __device__ void wait() {
+    ok = ok && wait_bounded(bars + 8u * slot, ph, wc, kSiteDrainState);
+  }
+  // after the barrier that follows the slot's last read
+  __device__ void next(int64_t row) {
+    if (threadIdx.x == 0 && ok) {
+      const int64_t ahead = row + static_cast<int64_t>(depth) * gridDim.x;
+      if (ahead < rows) fill(slot, ahead);
+    }
+    if (++slot == depth) { slot = 0; ph ^= 1u; }
+  }
+  // After a timeout: time for copies still under way to land before the block
+  // leaves its shared memory.
+  __device__ void finish() const {
+    if (ok) return;
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 200000ull) {
+    }
+  }
+};
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr));
+  return v;
+}
+// Shared memory: the ring, 16-byte aligned, then its barriers and an abort flag.
+template <int S>
+__device__ __forceinline__ RowRing<S> make_ring(uint8_t* smem, int depth, uint32_t row_bytes,
+                                                int64_t rows, const NormWait& w) {
+  RowRing<S> r;
+  r.smem = smem_u32(smem);
+  r.row_bytes = row_bytes;
+  r.depth = depth;
+  r.rows = rows;
+  r.bars = r.smem + depth * S * row_bytes;
+  r.wc = WaitCtx{reinterpret_cast<volatile uint32_t*>(smem + depth * S * row_bytes + 8 * depth), w.err,
+                 w.err_site, w.timeout_ns};
+  return r;
+}
+
+template <int VPT, bool RES>
+__global__ void __launch_bounds__(512, 2) rmsnorm_stream_kernel(const NormArgs a, int depth) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  __shared__ float red[2][32];
+  const int nvec = a.cols / 8;
+  RowRing<RES ? 2 : 1> ring =
+      make_ring<RES ? 2 : 1>(smem_raw, depth, static_cast<uint32_t>(a.cols) * 2, a.rows, a.wait);
+  ring.src[0] = reinterpret_cast<const uint8_t*>(a.x);
+  if constexpr (RES) ring.src[1] = reinterpret_cast<const uint8_t*>(a.residual);
+  if (threadIdx.x == 0) {
+    *ring.wc.abort_flag = 0u;
+    ring.start();
+  }
+  float g[VPT][8];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i)
+    if (static_cast<int>(threadIdx.x + i * blockDim.x) < nvec)
+      load_gain8(a.gain, a.gain_bf16, threadIdx.x + i * blockDim.x, g[i]);
+  __syncthreads();
+  int parity = 0;
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, parity ^= 1) {
+    ring.wait();
+    float h[VPT][8], ss = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int v = threadIdx.x + i * blockDim.x;
+      if (v < nvec) {
+        const uint4 x = lds16(ring.at(ring.slot, 0) + 16 * v);
+        const uint4 r = RES ? lds16(ring.at(ring.slot, RES ? 1 : 0) + 16 * v) : make_uint4(0, 0, 0, 0);
+        ss += norm_h(a, x, r, row * nvec + v, h[i]);
+      }
+    }
+    ss = block_sum(ss, red[parity]);
+    ring.next(row);
+    const float rstd = norm_rstd(a, ss);
+    if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int v = threadIdx.x + i * blockDim.x;
+      norm_out(a, h[i], g[i], rstd, row, v, v < nvec);
+    }
+  }
+  ring.finish();
+}
+
+// ---------------------------------------------------------------- backward
 // With xh = h rstd and u = dy gain, the gradient of y = xh gain with respect
 // to h is rstd (u - xh mean(u xh)); dsum, the gradient that reaches h along
 // the residual stream, is added.  dgain = sum over rows of dy xh: a block
 // adds its rows in registers and leaves one partial row, which
 // rmsnorm_dgain_kernel adds in a fixed order.
+// One vector's share of the row's dot product; dgain's terms are added to dg.
+__device__ __forceinline__ float bwd_dot(uint4 hv, uint4 dv, const float (&g)[8], float rstd,
+                                         float (&dg)[8]) {
+  float h[8], d[8], dot = 0.0f;
+  unpack8(hv, h);
+  unpack8(dv, d);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const float t = d[k] * (h[k] * rstd);
+    dg[k] += t;
+    dot = fmaf(t, g[k], dot);
+  }
+  return dot;
+}
+__device__ __forceinline__ void bwd_out(const NormBwdArgs& a, uint4 hv, uint4 dv, uint4 sv,
+                                        const float (&g)[8], float rstd, float c, int64_t at) {
+  float h[8], d[8], o[8];
+  unpack8(hv, h);
+  unpack8(dv, d);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) o[k] = rstd * fmaf(-c, h[k] * rstd, d[k] * g[k]);
+  if (a.dsum) {
+    float r[8];
+    unpack8(sv, r);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) o[k] += r[k];
+  }
+  __stcs(reinterpret_cast<uint4*>(a.dx) + at, pack8(o));
+}
 template <int VPT>
-__global__ void __launch_bounds__(1024) rmsnorm_bwd_kernel(const NormBwdArgs a) {
-  __shared__ float red[2][32];
+__device__ __forceinline__ void write_part(const NormBwdArgs& a, const float (&dg)[VPT][8], int me,
+                                           int width) {
   const int nvec = a.cols / 8;
+  float4* part = reinterpret_cast<float4*>(a.part) + static_cast<int64_t>(blockIdx.x) * nvec * 2;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int v = me + i * width;
+    if (v < nvec) {
+      part[2 * v] = make_float4(dg[i][0], dg[i][1], dg[i][2], dg[i][3]);
+      part[2 * v + 1] = make_float4(dg[i][4], dg[i][5], dg[i][6], dg[i][7]);
+    }
+  }
+}
+
+template <int VPT, bool WARP>
+__global__ void __launch_bounds__(WARP ? 256 : 1024) rmsnorm_bwd_kernel(const NormBwdArgs a) {
+  __shared__ float red[2][32];
+  __shared__ float4 parts[WARP ? 8 * 64 * VPT : 1];   // [warp][vector][2]
+  const int nvec = a.cols / 8;
+  const int width = WARP ? 32 : blockDim.x, me = WARP ? threadIdx.x & 31 : threadIdx.x;
+  const int64_t first = WARP ? static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5) : blockIdx.x;
+  const int64_t step = WARP ? static_cast<int64_t>(gridDim.x) * 8 : gridDim.x;
   int parity = 0;
   float dg[VPT][8];
 #pragma unroll
   for (int i = 0; i < VPT; ++i)
 #pragma unroll
     for (int k = 0; k < 8; ++k) dg[i][k] = 0.0f;
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, parity ^= 1) {
+  for (int64_t row = first; row < a.rows; row += step, parity ^= 1) {
     const int64_t base = row * nvec;
     const float rstd = __ldg(a.rstd + row);
-    uint4 hv[VPT], dv[VPT];
+    uint4 hv[VPT], dv[VPT], sv[VPT];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int v = me + i * width;
+      if (v < nvec) {
+        hv[i] = __ldcs(reinterpret_cast<const uint4*>(a.h) + base + v);
+        dv[i] = __ldcs(reinterpret_cast<const uint4*>(a.dy) + base + v);
+        if (a.dsum) sv[i] = __ldcs(reinterpret_cast<const uint4*>(a.dsum) + base + v);
+      }
+    }
+    float dot = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int v = me + i * width;
+      if (v < nvec) {
+        float g[8];
+        load_gain8(a.gain, a.gain_bf16, v, g);
+        dot += bwd_dot(hv[i], dv[i], g, rstd, dg[i]);
+      }
+    }
+    dot = WARP ? warp_sum(dot) : block_sum(dot, red[parity]);
+    const float c = __fdiv_rn(dot, static_cast<float>(a.cols));
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int v = me + i * width;
+      if (v < nvec) {
+        float g[8];
+        load_gain8(a.gain, a.gain_bf16, v, g);
+        bwd_out(a, hv[i], dv[i], sv[i], g, rstd, c, base + v);
+      }
+    }
+  }
+  if (!a.dgain) return;
+  if constexpr (WARP) {   // the block's warps join in a fixed order
+    const int warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int v = me + i * 32;
+      parts[(warp * 32 * VPT + v) * 2] = make_float4(dg[i][0], dg[i][1], dg[i][2], dg[i][3]);
+      parts[(warp * 32 * VPT + v) * 2 + 1] = make_float4(dg[i][4], dg[i][5], dg[i][6], dg[i][7]);
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < 2 * nvec; e += 256) {
+      float4 s = parts[e];
+      for (int w = 1; w < 8; ++w) {
+        const float4 p = parts[w * 64 * VPT + e];
+        s.x += p.x; s.y += p.y; s.z += p.z; s.w += p.w;
+      }
+      reinterpret_cast<float4*>(a.part)[static_cast<int64_t>(blockIdx.x) * nvec * 2 + e] = s;
+    }
+  } else {
+    write_part<VPT>(a, dg, me, width);
+  }
+}
+
+template <int VPT, bool DSUM>
+__global__ void __launch_bounds__(512, 2) rmsnorm_bwd_stream_kernel(const NormBwdArgs a, int depth) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  __shared__ float red[2][32];
+  constexpr int S = DSUM ? 3 : 2;
+  const int nvec = a.cols / 8;
+  RowRing<S> ring = make_ring<S>(smem_raw, depth, static_cast<uint32_t>(a.cols) * 2, a.rows, a.wait);
+  ring.src[0] = reinterpret_cast<const uint8_t*>(a.h);
+  ring.src[1] = reinterpret_cast<const uint8_t*>(a.dy);
+  if constexpr (DSUM) ring.src[2] = reinterpret_cast<const uint8_t*>(a.dsum);
+  if (threadIdx.x == 0) {
+    *ring.wc.abort_flag = 0u;
+    ring.start();
+  }
+  float g[VPT][8], dg[VPT][8];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    if (static_cast<int>(threadIdx.x + i * blockDim.x) < nvec)
+      load_gain8(a.gain, a.gain_bf16, threadIdx.x + i * blockDim.x, g[i]);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) dg[i][k] = 0.0f;
+  }
+  __syncthreads();
+  int parity = 0;
+  float rstd = __ldg(a.rstd + blockIdx.x);
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, parity ^= 1) {
+    const float rstd_next = row + gridDim.x < a.rows ? __ldg(a.rstd + row + gridDim.x) : 0.0f;
+    ring.wait();
+    uint4 hv[VPT], dv[VPT], sv[VPT];
     float dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = threadIdx.x + i * blockDim.x;
-      hv[i] = dv[i] = make_uint4(0, 0, 0, 0);
       if (v < nvec) {
-        hv[i] = __ldcs(reinterpret_cast<const uint4*>(a.h) + base + v);
-        dv[i] = __ldcs(reinterpret_cast<const uint4*>(a.dy) + base + v);
+        hv[i] = lds16(ring.at(ring.slot, 0) + 16 * v);
+        dv[i] = lds16(ring.at(ring.slot, 1) + 16 * v);
+        if constexpr (DSUM) sv[i] = lds16(ring.at(ring.slot, S - 1) + 16 * v);
+        dot += bwd_dot(hv[i], dv[i], g[i], rstd, dg[i]);
       }
     }
+    dot = block_sum(dot, red[parity]);
+    ring.next(row);
+    const float c = __fdiv_rn(dot, static_cast<float>(a.cols));
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = threadIdx.x + i * blockDim.x;
-      if (v < nvec) {
-        float h[8], d[8], g[8];
-        unpack8(hv[i], h);
-        unpack8(dv[i], d);
-        load_gain8(a.gain, a.gain_bf16, v, g);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float t = d[k] * (h[k] * rstd);
-          dg[i][k] += t;
-          dot = fmaf(t, g[k], dot);
-        }
-      }
+      if (v < nvec) bwd_out(a, hv[i], dv[i], sv[i], g[i], rstd, c, row * nvec + v);
     }
-    const float c = __fdiv_rn(block_sum(dot, red[parity]), static_cast<float>(a.cols));
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int v = threadIdx.x + i * blockDim.x;
-      if (v < nvec) {
-        float h[8], d[8], g[8], o[8];
-        unpack8(hv[i], h);
-        unpack8(dv[i], d);
-        load_gain8(a.gain, a.gain_bf16, v, g);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) o[k] = rstd * fmaf(-c, h[k] * rstd, d[k] * g[k]);
-        if (a.dsum) {
-          float r[8];
-          unpack8(__ldcs(reinterpret_cast<const uint4*>(a.dsum) + base + v), r);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) o[k] += r[k];
-        }
-        __stcs(reinterpret_cast<uint4*>(a.dx) + base + v, pack8(o));
-      }
-    }
+    rstd = rstd_next;
   }
-  if (a.dgain) {
-    float4* part = reinterpret_cast<float4*>(a.part) + static_cast<int64_t>(blockIdx.x) * nvec * 2;
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int v = threadIdx.x + i * blockDim.x;
-      if (v < nvec) {
-        part[2 * v] = make_float4(dg[i][0], dg[i][1], dg[i][2], dg[i][3]);
-        part[2 * v + 1] = make_float4(dg[i][4], dg[i][5], dg[i][6], dg[i][7]);
-      }
-    }
-  }
+  if (a.dgain) write_part<VPT>(a, dg, threadIdx.x, blockDim.x);
+  ring.finish();
 }
 
 // dgain[c] = sum over the blocks' partial rows: 32 columns a block, 8 runs of
@@ -317,38 +566,141 @@ int row_threads(int cols, int vpt) {
   return (t + 31) / 32 * 32;
 }
 
+// How a call walks its rows.
+enum Walk { kWalkWarp, kWalkBlock, kWalkStream };
+struct RowPlan {
+  Walk walk;
+  int vpt, threads, grid, depth, smem;   // depth, smem: the stream's ring
+};
+
+// A warp per row up to 1024 columns.  Above, the stream for rows enough to
+// fill its persistent blocks twice, while a ring of three rows fits (else a
+// block per row).
+RowPlan row_plan(int64_t rows, int cols, int streams, int num_sms) {
+  RowPlan p{kWalkBlock, 1, 0, 0, 0, 0};
+  if (cols <= 1024) {
+    p.walk = kWalkWarp;
+    p.vpt = cols <= 256 ? 1 : (cols <= 512 ? 2 : 4);
+    p.threads = 256;
+    const int64_t want = (rows + 7) / 8, most = static_cast<int64_t>(num_sms) * 4;
+    p.grid = static_cast<int>(want < most ? want : most);
+    return p;
+  }
+  const int row_bytes = cols * 2;
+  int per_sm = cols <= 2048 ? 4 : 2;
+  if (cols <= 8192) {
+    p.depth = (220 * 1024 / per_sm) / (streams * row_bytes);
+    if (p.depth < 3) {
+      per_sm = 1;
+      p.depth = (220 * 1024) / (streams * row_bytes);
+    }
+    if (p.depth > 8) p.depth = 8;
+  }
+  if (p.depth >= 3 && rows >= 2 * per_sm * num_sms) {
+    p.walk = kWalkStream;
+    p.vpt = cols <= 4096 ? 1 : 2;
+    p.threads = row_threads(cols, p.vpt);
+    p.grid = per_sm * num_sms;
+    p.smem = p.depth * (streams * row_bytes + 8) + 8;
+    return p;
+  }
+  p.vpt = cols <= 8192 ? 1 : (cols <= 16384 ? 2 : 4);
+  p.threads = row_threads(cols, p.vpt);
+  const int64_t most = static_cast<int64_t>(num_sms) * 2;
+  p.grid = static_cast<int>(rows < most ? rows : most);
+  return p;
+}
+
+// Launches a stream kernel with its ring; the attribute is set once per device.
+template <typename Kern, typename Args>
+cudaError_t launch_stream(Kern kern, int* ready, const RowPlan& p, const Args& a,
+                          cudaStream_t stream) {
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64 || !ready[dev]) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 224 * 1024);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) ready[dev] = 1;
+  }
+  kern<<<p.grid, p.threads, p.smem, stream>>>(a, p.depth);
+  return cudaGetLastError();
+}
+template <int VPT, bool RES>
+cudaError_t launch_fwd_stream(const RowPlan& p, const NormArgs& a, cudaStream_t stream) {
+  static int ready[64] = {0};
+  return launch_stream(rmsnorm_stream_kernel<VPT, RES>, ready, p, a, stream);
+}
+template <int VPT, bool DSUM>
+cudaError_t launch_bwd_stream(const RowPlan& p, const NormBwdArgs& a, cudaStream_t stream) {
+  static int ready[64] = {0};
+  return launch_stream(rmsnorm_bwd_stream_kernel<VPT, DSUM>, ready, p, a, stream);
+}
+
 }  // namespace
 
 cudaError_t launch_rmsnorm(const NormArgs& a, int num_sms, cudaStream_t stream) {
-  const int vpt = a.cols <= 8192 ? 1 : (a.cols <= 16384 ? 2 : 4);
-  const int threads = row_threads(a.cols, vpt);
-  const int64_t most = static_cast<int64_t>(num_sms) * (2048 / threads);
-  const int grid = static_cast<int>(a.rows < most ? a.rows : most);
-  switch (vpt) {
-    case 1: rmsnorm_kernel<1><<<grid, threads, 0, stream>>>(a); break;
-    case 2: rmsnorm_kernel<2><<<grid, threads, 0, stream>>>(a); break;
-    default: rmsnorm_kernel<4><<<grid, threads, 0, stream>>>(a); break;
+  const RowPlan p = row_plan(a.rows, a.cols, a.residual ? 2 : 1, num_sms);
+  if (p.walk == kWalkStream) {
+    if (p.vpt == 1)
+      return a.residual ? launch_fwd_stream<1, true>(p, a, stream)
+                        : launch_fwd_stream<1, false>(p, a, stream);
+    return a.residual ? launch_fwd_stream<2, true>(p, a, stream)
+                      : launch_fwd_stream<2, false>(p, a, stream);
+  }
+  const bool warp = p.walk == kWalkWarp;
+  switch (p.vpt) {
+    case 1:
+      if (warp) rmsnorm_kernel<1, true><<<p.grid, p.threads, 0, stream>>>(a);
+      else rmsnorm_kernel<1, false><<<p.grid, p.threads, 0, stream>>>(a);
+      break;
+    case 2:
+      if (warp) rmsnorm_kernel<2, true><<<p.grid, p.threads, 0, stream>>>(a);
+      else rmsnorm_kernel<2, false><<<p.grid, p.threads, 0, stream>>>(a);
+      break;
+    default:
+      if (warp) rmsnorm_kernel<4, true><<<p.grid, p.threads, 0, stream>>>(a);
+      else rmsnorm_kernel<4, false><<<p.grid, p.threads, 0, stream>>>(a);
+      break;
   }
   return cudaGetLastError();
 }
 
 int rmsnorm_bwd_blocks(int64_t rows, int cols, int num_sms) {
-  const int64_t most = static_cast<int64_t>(num_sms) * 2;
-  return static_cast<int>(rows < most ? rows : most);
+  // the ring of two inputs is at least as deep as that of three, so this is
+  // the larger of the two grids
+  const int a = row_plan(rows, cols, 2, num_sms).grid, b = row_plan(rows, cols, 3, num_sms).grid;
+  return a > b ? a : b;
 }
 
 cudaError_t launch_rmsnorm_bwd(const NormBwdArgs& a, int num_sms, cudaStream_t stream) {
-  const int vpt = a.cols <= 8192 ? 1 : (a.cols <= 16384 ? 2 : 4);
-  const int threads = row_threads(a.cols, vpt);
-  const int grid = rmsnorm_bwd_blocks(a.rows, a.cols, num_sms);
-  switch (vpt) {
-    case 1: rmsnorm_bwd_kernel<1><<<grid, threads, 0, stream>>>(a); break;
-    case 2: rmsnorm_bwd_kernel<2><<<grid, threads, 0, stream>>>(a); break;
-    default: rmsnorm_bwd_kernel<4><<<grid, threads, 0, stream>>>(a); break;
+  const RowPlan p = row_plan(a.rows, a.cols, a.dsum ? 3 : 2, num_sms);
+  cudaError_t e = cudaSuccess;
+  if (p.walk == kWalkStream) {
+    if (p.vpt == 1)
+      e = a.dsum ? launch_bwd_stream<1, true>(p, a, stream) : launch_bwd_stream<1, false>(p, a, stream);
+    else
+      e = a.dsum ? launch_bwd_stream<2, true>(p, a, stream) : launch_bwd_stream<2, false>(p, a, stream);
+  } else {
+    const bool warp = p.walk == kWalkWarp;
+    switch (p.vpt) {
+      case 1:
+        if (warp) rmsnorm_bwd_kernel<1, true><<<p.grid, p.threads, 0, stream>>>(a);
+        else rmsnorm_bwd_kernel<1, false><<<p.grid, p.threads, 0, stream>>>(a);
+        break;
+      case 2:
+        if (warp) rmsnorm_bwd_kernel<2, true><<<p.grid, p.threads, 0, stream>>>(a);
+        else rmsnorm_bwd_kernel<2, false><<<p.grid, p.threads, 0, stream>>>(a);
+        break;
+      default:
+        if (warp) rmsnorm_bwd_kernel<4, true><<<p.grid, p.threads, 0, stream>>>(a);
+        else rmsnorm_bwd_kernel<4, false><<<p.grid, p.threads, 0, stream>>>(a);
+        break;
+    }
+    e = cudaGetLastError();
   }
-  cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !a.dgain) return e;
-  rmsnorm_dgain_kernel<<<(a.cols + 31) / 32, 256, 0, stream>>>(a.part, grid, a.cols, a.dgain);
+  rmsnorm_dgain_kernel<<<(a.cols + 31) / 32, 256, 0, stream>>>(a.part, p.grid, a.cols, a.dgain);
   return cudaGetLastError();
 }
 

@@ -99,6 +99,16 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* m, 
       "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(bar), "l"(policy)
       : "memory");
 }
+// Untiled copy of `bytes` contiguous bytes into shared memory (addresses and
+// size multiples of 16); completion as transaction bytes on `bar`.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
 // 2-D tiled store of one box from shared memory (bulk-group completion).
 // Out-of-range parts of the box are not written.
 // The same store with an L2 eviction-priority hint (a createpolicy value).

@@ -7,6 +7,7 @@
 // each block leaves one partial sum, and a second launch adds the partials in
 // a fixed order, so the norm is the same on every run.
 #include "forge_internal.h"
+#include "forge_ptx.cuh"
 
 namespace forge {
 namespace {
@@ -109,6 +110,7 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_consta
 __global__ void __launch_bounds__(kThreads) grad_norm_final_kernel(const double* __restrict__ part,
                                                                    int n, float max_norm,
                                                                    float* __restrict__ out) {
+  grid_dependency_wait();   // launched ahead of grad_norm_kernel's end
   double s = 0.0;
   for (int i = threadIdx.x; i < n; i += kThreads) s += part[i];
   s = block_sum(s);
@@ -134,8 +136,16 @@ cudaError_t launch_grad_norm(const GradNormArgs& a, int blocks, cudaStream_t str
 
 cudaError_t launch_grad_norm_final(const double* part, int n, float max_norm, float* out,
                                    cudaStream_t stream) {
-  grad_norm_final_kernel<<<1, kThreads, 0, stream>>>(part, n, max_norm, out);
-  return cudaGetLastError();
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3(1, 1, 1);
+  lc.blockDim = dim3(kThreads, 1, 1);
+  lc.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  return cudaLaunchKernelEx(&lc, grad_norm_final_kernel, part, n, max_norm, out);
 }
 
 }  // namespace forge

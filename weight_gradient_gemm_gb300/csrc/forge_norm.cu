@@ -204,7 +204,7 @@ __device__ __forceinline__ RowRing<S> make_ring(uint8_t* smem, int depth, uint32
 }
 
 template <int VPT, bool RES>
-__global__ void __launch_bounds__(512, 2) rmsnorm_stream_kernel(const NormArgs a, int depth) {
+__global__ void __launch_bounds__(1024, 1) rmsnorm_stream_kernel(const NormArgs a, int depth) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   __shared__ float red[2][32];
   const int nvec = a.cols / 8;
@@ -216,11 +216,8 @@ __global__ void __launch_bounds__(512, 2) rmsnorm_stream_kernel(const NormArgs a
     *ring.wc.abort_flag = 0u;
     ring.start();
   }
-  float g[VPT][8];
-#pragma unroll
-  for (int i = 0; i < VPT; ++i)
-    if (static_cast<int>(threadIdx.x + i * blockDim.x) < nvec)
-      load_gain8(a.gain, a.gain_bf16, threadIdx.x + i * blockDim.x, g[i]);
+  float g[8];   // the gain of the first vector; wider rows read theirs again (L1)
+  if (static_cast<int>(threadIdx.x) < nvec) load_gain8(a.gain, a.gain_bf16, threadIdx.x, g);
   __syncthreads();
   int parity = 0;
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, parity ^= 1) {
@@ -242,7 +239,8 @@ __global__ void __launch_bounds__(512, 2) rmsnorm_stream_kernel(const NormArgs a
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = threadIdx.x + i * blockDim.x;
-      norm_out(a, h[i], g[i], rstd, row, v, v < nvec);
+      if (VPT > 1 && v < nvec) load_gain8(a.gain, a.gain_bf16, v, g);
+      norm_out(a, h[i], g, rstd, row, v, v < nvec);
     }
   }
   ring.finish();
@@ -371,7 +369,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) rmsnorm_bwd_kernel(const No
 }
 
 template <int VPT, bool DSUM>
-__global__ void __launch_bounds__(512, 2) rmsnorm_bwd_stream_kernel(const NormBwdArgs a, int depth) {
+__global__ void __launch_bounds__(1024, 1) rmsnorm_bwd_stream_kernel(const NormBwdArgs a, int depth) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   __shared__ float red[2][32];
   constexpr int S = DSUM ? 3 : 2;
@@ -384,14 +382,12 @@ __global__ void __launch_bounds__(512, 2) rmsnorm_bwd_stream_kernel(const NormBw
     *ring.wc.abort_flag = 0u;
     ring.start();
   }
-  float g[VPT][8], dg[VPT][8];
+  float g[8], dg[VPT][8];
+  if (static_cast<int>(threadIdx.x) < nvec) load_gain8(a.gain, a.gain_bf16, threadIdx.x, g);
 #pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    if (static_cast<int>(threadIdx.x + i * blockDim.x) < nvec)
-      load_gain8(a.gain, a.gain_bf16, threadIdx.x + i * blockDim.x, g[i]);
+  for (int i = 0; i < VPT; ++i)
 #pragma unroll
     for (int k = 0; k < 8; ++k) dg[i][k] = 0.0f;
-  }
   __syncthreads();
   int parity = 0;
   float rstd = __ldg(a.rstd + blockIdx.x);
@@ -407,7 +403,8 @@ __global__ void __launch_bounds__(512, 2) rmsnorm_bwd_stream_kernel(const NormBw
         hv[i] = lds16(ring.at(ring.slot, 0) + 16 * v);
         dv[i] = lds16(ring.at(ring.slot, 1) + 16 * v);
         if constexpr (DSUM) sv[i] = lds16(ring.at(ring.slot, S - 1) + 16 * v);
-        dot += bwd_dot(hv[i], dv[i], g[i], rstd, dg[i]);
+        if (VPT > 1) load_gain8(a.gain, a.gain_bf16, v, g);
+        dot += bwd_dot(hv[i], dv[i], g, rstd, dg[i]);
       }
     }
     dot = block_sum(dot, red[parity]);
@@ -416,7 +413,10 @@ __global__ void __launch_bounds__(512, 2) rmsnorm_bwd_stream_kernel(const NormBw
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = threadIdx.x + i * blockDim.x;
-      if (v < nvec) bwd_out(a, hv[i], dv[i], sv[i], g[i], rstd, c, row * nvec + v);
+      if (v < nvec) {
+        if (VPT > 1) load_gain8(a.gain, a.gain_bf16, v, g);
+        bwd_out(a, hv[i], dv[i], sv[i], g, rstd, c, row * nvec + v);
+      }
     }
     rstd = rstd_next;
   }
@@ -424,24 +424,25 @@ __global__ void __launch_bounds__(512, 2) rmsnorm_bwd_stream_kernel(const NormBw
   ring.finish();
 }
 
-// dgain[c] = sum over the blocks' partial rows: 32 columns a block, 8 runs of
-// rows side by side, added in a fixed order.
-__global__ void __launch_bounds__(256) rmsnorm_dgain_kernel(const float* __restrict__ part,
-                                                            int blocks, int cols,
-                                                            float* __restrict__ dgain) {
-  __shared__ float sum[8][32];
+// dgain[c] = sum over the blocks' partial rows: 32 columns a block, 32 runs of
+// rows side by side, added in a fixed order.  Launched ahead of the main
+// kernel's end (programmatic launch), it waits for it here.
+__global__ void __launch_bounds__(1024) rmsnorm_dgain_kernel(const float* __restrict__ part,
+                                                             int blocks, int cols,
+                                                             float* __restrict__ dgain) {
+  __shared__ float sum[32][33];
   const int lane = threadIdx.x & 31, run = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
+  grid_dependency_wait();
   float s = 0.0f;
-  if (c < cols)
-    for (int b = run; b < blocks; b += 8) s += part[static_cast<int64_t>(b) * cols + c];
+  if (c < cols) {
+#pragma unroll 8
+    for (int b = run; b < blocks; b += 32) s += __ldcg(part + static_cast<int64_t>(b) * cols + c);
+  }
   sum[run][lane] = s;
   __syncthreads();
-  if (run == 0 && c < cols) {
-#pragma unroll
-    for (int k = 1; k < 8; ++k) s += sum[k][lane];
-    dgain[c] = s;
-  }
+  s = warp_sum(sum[lane][run]);   // column `run` of the block: lane is the run of rows
+  if (lane == 0 && blockIdx.x * 32 + run < cols) dgain[blockIdx.x * 32 + run] = s;
 }
 
 // Largest magnitude of eight bf16 values; NaN if one of them is.
@@ -573,12 +574,13 @@ struct RowPlan {
   int vpt, threads, grid, depth, smem;   // depth, smem: the stream's ring
 };
 
-// A warp per row up to 1024 columns.  Above, the stream for rows enough to
-// fill its persistent blocks twice, while a ring of three rows fits (else a
-// block per row).
-RowPlan row_plan(int64_t rows, int cols, int streams, int num_sms) {
+// A warp per row up to 1024 columns (backward 512, whose registers hold two
+// gradients' sums besides).  Above, the stream for rows enough to fill its
+// persistent blocks twice, while a ring of two rows fits (else a block per
+// row).  Blocks of about 1024 threads in all share an SM.
+RowPlan row_plan(int64_t rows, int cols, int streams, bool backward, int num_sms) {
   RowPlan p{kWalkBlock, 1, 0, 0, 0, 0};
-  if (cols <= 1024) {
+  if (cols <= (backward ? 512 : 1024)) {
     p.walk = kWalkWarp;
     p.vpt = cols <= 256 ? 1 : (cols <= 512 ? 2 : 4);
     p.threads = 256;
@@ -586,27 +588,21 @@ RowPlan row_plan(int64_t rows, int cols, int streams, int num_sms) {
     p.grid = static_cast<int>(want < most ? want : most);
     return p;
   }
-  const int row_bytes = cols * 2;
-  int per_sm = cols <= 2048 ? 4 : 2;
-  if (cols <= 8192) {
-    p.depth = (220 * 1024 / per_sm) / (streams * row_bytes);
-    if (p.depth < 3) {
-      per_sm = 1;
-      p.depth = (220 * 1024) / (streams * row_bytes);
-    }
-    if (p.depth > 8) p.depth = 8;
-  }
-  if (p.depth >= 3 && rows >= 2 * per_sm * num_sms) {
-    p.walk = kWalkStream;
-    p.vpt = cols <= 4096 ? 1 : 2;
-    p.threads = row_threads(cols, p.vpt);
-    p.grid = per_sm * num_sms;
-    p.smem = p.depth * (streams * row_bytes + 8) + 8;
-    return p;
-  }
   p.vpt = cols <= 8192 ? 1 : (cols <= 16384 ? 2 : 4);
   p.threads = row_threads(cols, p.vpt);
-  const int64_t most = static_cast<int64_t>(num_sms) * 2;
+  int per_sm = 1024 / p.threads;
+  per_sm = per_sm > 8 ? 8 : per_sm;
+  const int row_bytes = streams * cols * 2;
+  p.depth = (220 * 1024 / per_sm) / row_bytes;
+  if (p.depth > 8) p.depth = 8;
+  if (p.vpt <= 2 && p.depth >= 2 && rows >= 2 * per_sm * num_sms) {
+    p.walk = kWalkStream;
+    p.grid = per_sm * num_sms;
+    p.smem = p.depth * (row_bytes + 8) + 8;
+    return p;
+  }
+  // every row in flight at once; the backward pass's sums want few blocks
+  const int64_t most = backward ? static_cast<int64_t>(num_sms) * 2 : INT32_MAX;
   p.grid = static_cast<int>(rows < most ? rows : most);
   return p;
 }
@@ -640,7 +636,7 @@ cudaError_t launch_bwd_stream(const RowPlan& p, const NormBwdArgs& a, cudaStream
 }  // namespace
 
 cudaError_t launch_rmsnorm(const NormArgs& a, int num_sms, cudaStream_t stream) {
-  const RowPlan p = row_plan(a.rows, a.cols, a.residual ? 2 : 1, num_sms);
+  const RowPlan p = row_plan(a.rows, a.cols, a.residual ? 2 : 1, false, num_sms);
   if (p.walk == kWalkStream) {
     if (p.vpt == 1)
       return a.residual ? launch_fwd_stream<1, true>(p, a, stream)
@@ -667,14 +663,14 @@ cudaError_t launch_rmsnorm(const NormArgs& a, int num_sms, cudaStream_t stream) 
 }
 
 int rmsnorm_bwd_blocks(int64_t rows, int cols, int num_sms) {
-  // the ring of two inputs is at least as deep as that of three, so this is
-  // the larger of the two grids
-  const int a = row_plan(rows, cols, 2, num_sms).grid, b = row_plan(rows, cols, 3, num_sms).grid;
+  // with and without dsum: one workspace serves both
+  const int a = row_plan(rows, cols, 2, true, num_sms).grid;
+  const int b = row_plan(rows, cols, 3, true, num_sms).grid;
   return a > b ? a : b;
 }
 
 cudaError_t launch_rmsnorm_bwd(const NormBwdArgs& a, int num_sms, cudaStream_t stream) {
-  const RowPlan p = row_plan(a.rows, a.cols, a.dsum ? 3 : 2, num_sms);
+  const RowPlan p = row_plan(a.rows, a.cols, a.dsum ? 3 : 2, true, num_sms);
   cudaError_t e = cudaSuccess;
   if (p.walk == kWalkStream) {
     if (p.vpt == 1)
@@ -683,25 +679,28 @@ cudaError_t launch_rmsnorm_bwd(const NormBwdArgs& a, int num_sms, cudaStream_t s
       e = a.dsum ? launch_bwd_stream<2, true>(p, a, stream) : launch_bwd_stream<2, false>(p, a, stream);
   } else {
     const bool warp = p.walk == kWalkWarp;
-    switch (p.vpt) {
-      case 1:
-        if (warp) rmsnorm_bwd_kernel<1, true><<<p.grid, p.threads, 0, stream>>>(a);
-        else rmsnorm_bwd_kernel<1, false><<<p.grid, p.threads, 0, stream>>>(a);
-        break;
-      case 2:
-        if (warp) rmsnorm_bwd_kernel<2, true><<<p.grid, p.threads, 0, stream>>>(a);
-        else rmsnorm_bwd_kernel<2, false><<<p.grid, p.threads, 0, stream>>>(a);
-        break;
-      default:
-        if (warp) rmsnorm_bwd_kernel<4, true><<<p.grid, p.threads, 0, stream>>>(a);
-        else rmsnorm_bwd_kernel<4, false><<<p.grid, p.threads, 0, stream>>>(a);
-        break;
+    if (warp) {
+      if (p.vpt == 1) rmsnorm_bwd_kernel<1, true><<<p.grid, p.threads, 0, stream>>>(a);
+      else rmsnorm_bwd_kernel<2, true><<<p.grid, p.threads, 0, stream>>>(a);
+    } else {
+      if (p.vpt == 1) rmsnorm_bwd_kernel<1, false><<<p.grid, p.threads, 0, stream>>>(a);
+      else if (p.vpt == 2) rmsnorm_bwd_kernel<2, false><<<p.grid, p.threads, 0, stream>>>(a);
+      else rmsnorm_bwd_kernel<4, false><<<p.grid, p.threads, 0, stream>>>(a);
     }
     e = cudaGetLastError();
   }
   if (e != cudaSuccess || !a.dgain) return e;
-  rmsnorm_dgain_kernel<<<(a.cols + 31) / 32, 256, 0, stream>>>(a.part, p.grid, a.cols, a.dgain);
-  return cudaGetLastError();
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3((a.cols + 31) / 32, 1, 1);
+  lc.blockDim = dim3(1024, 1, 1);
+  lc.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  return cudaLaunchKernelEx(&lc, rmsnorm_dgain_kernel, static_cast<const float*>(a.part), p.grid,
+                            a.cols, a.dgain);
 }
 
 cudaError_t launch_quantize_b128(const uint16_t* x, uint8_t* codes, float* scales, int64_t rows,

@@ -139,7 +139,7 @@ forge_status product_b128(const void* A, const float* sa, const void* W, const f
   a.err_site = d.err_site;
   a.timeout_ns = d.timeout_ns;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  return status(cfg.few ? launch_gemm_b128_few(cfg.few, dgrad, a, cs)
+  return status(cfg.few ? launch_gemm_b128_few(cfg.few, dgrad, a, d.num_sms, cs)
                         : launch_gemm_b128(cfg, dgrad, a, d.num_sms, cs));
 }
 

@@ -31,7 +31,10 @@ struct Few {
   static constexpr int NC = NT <= 64 ? NT : 64;         // tokens per epilogue thread
   static constexpr int A_BYTES = kBM * 128;
   static constexpr int STAGE_BYTES = A_BYTES + NT * 128;
+  // Operand stages: as many as let two CTAs share an SM, or, where the grid
+  // has no more than one CTA for each, as many as fit.
   static constexpr int STAGES = NT <= 16 ? 5 : 4;
+  static constexpr int DEEP = NT <= 16 ? 11 : (NT == 32 ? 9 : (NT == 64 ? 8 : 6));
   static constexpr int NBUF = NT <= 32 ? 8 : (NT == 64 ? 4 : 2);   // TMEM accumulators
   static constexpr int TMEM_COLS = NT * NBUF;           // 128 or 256: two CTAs fit an SM
   static constexpr int SC_BATCH = 8;
@@ -40,15 +43,18 @@ struct Few {
   // The shares arrive in a buffer of their own for few tokens; for more they
   // take the place of the operand stages, once every CTA is done with them.
   static constexpr bool ALIAS = NT > 32;
-  static constexpr int OFF_SC = STAGES * STAGE_BYTES;
-  static constexpr int OFF_PART = ALIAS ? 0 : OFF_SC + SC_BYTES;
-  static constexpr int OFF_BARS = OFF_SC + SC_BYTES + (ALIAS ? 0 : PART_BYTES);
-  static constexpr int NUM_BARS = 2 * STAGES + 2 * NBUF + 5;
-  static constexpr int OFF_TMEM = OFF_BARS + 8 * NUM_BARS;
-  static constexpr int SMEM_USED = OFF_TMEM + 8;
-  static constexpr int SMEM_ALLOC = SMEM_USED + 1024;
+  // Shared memory from a 1024-aligned base: barriers (the most there can be),
+  // abort flag, scales, shares, stages.
+  static constexpr int NUM_BARS = 2 * DEEP + 2 * NBUF + 5;
+  static constexpr int OFF_TMEM = 8 * NUM_BARS;
+  static constexpr int OFF_SC = (OFF_TMEM + 8 + 15) & ~15;
+  static constexpr int OFF_PART0 = OFF_SC + SC_BYTES;
+  static constexpr int OFF_STAGES = (OFF_PART0 + (ALIAS ? 0 : PART_BYTES) + 1023) & ~1023;
+  static constexpr int OFF_PART = ALIAS ? OFF_STAGES : OFF_PART0;
+  static constexpr int smem(int stages) { return OFF_STAGES + stages * STAGE_BYTES + 1024; }
   static_assert(!ALIAS || PART_BYTES <= STAGES * STAGE_BYTES, "shares fit the stages");
-  static_assert(NT > 64 || 2 * SMEM_ALLOC <= 228 * 1024 - 2 * 1024, "two CTAs an SM");
+  static_assert(NT > 64 || 2 * smem(STAGES) <= 228 * 1024 - 2 * 1024, "two CTAs an SM");
+  static_assert(smem(DEEP) <= 232448, "shared memory budget");
 };
 
 __device__ __forceinline__ void store_out(const B128Args& a, int64_t idx, float v) {
@@ -72,75 +78,70 @@ __global__ void __launch_bounds__(Few<NT>::THREADS, NT <= 64 ? 2 : 1)
   const int per = (a.num_kb + splits - 1) / splits;
   const int kb = rank * per, ke = min(a.num_kb, kb + per);   // this CTA's blocks (may be none)
 
-  const uint32_t bars = base + T::OFF_BARS;
+  const uint32_t stages = a.stages;
+  const uint32_t bars = base, stage0 = base + T::OFF_STAGES;
   auto bar_full = [&](int s) { return bars + 8u * s; };
-  auto bar_empty = [&](int s) { return bars + 8u * (T::STAGES + s); };
-  auto bar_tfull = [&](int b) { return bars + 8u * (2 * T::STAGES + b); };
-  auto bar_tempty = [&](int b) { return bars + 8u * (2 * T::STAGES + T::NBUF + b); };
-  auto bar_sfull = [&](int b) { return bars + 8u * (2 * T::STAGES + 2 * T::NBUF + b); };
-  auto bar_sempty = [&](int b) { return bars + 8u * (2 * T::STAGES + 2 * T::NBUF + 2 + b); };
-  const uint32_t bar_drain = bars + 8u * (2 * T::STAGES + 2 * T::NBUF + 4);
+  auto bar_empty = [&](int s) { return bars + 8u * (T::DEEP + s); };
+  auto bar_tfull = [&](int b) { return bars + 8u * (2 * T::DEEP + b); };
+  auto bar_tempty = [&](int b) { return bars + 8u * (2 * T::DEEP + T::NBUF + b); };
+  auto bar_sfull = [&](int b) { return bars + 8u * (2 * T::DEEP + 2 * T::NBUF + b); };
+  auto bar_sempty = [&](int b) { return bars + 8u * (2 * T::DEEP + 2 * T::NBUF + 2 + b); };
+  const uint32_t bar_drain = bars + 8u * (2 * T::DEEP + 2 * T::NBUF + 4);
   float* scales = reinterpret_cast<float*>(gbase + T::OFF_SC);   // [2][SC_BATCH][NT]
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(gbase + T::OFF_TMEM + 4);
   const WaitCtx wc{abort_flag, a.err, a.err_site, a.timeout_ns};
 
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < T::STAGES; ++s) {
-      mbar_init(bar_full(s), 1);
-      mbar_init(bar_empty(s), 1);
+  const uint64_t wpol = l2_policy_evict_normal(), xpol = l2_policy_evict_last();
+  auto load = [&](uint32_t s, int k) {
+    const uint32_t dst = stage0 + s * T::STAGE_BYTES;
+    mbar_arrive_expect_tx(bar_full(s), T::STAGE_BYTES);
+    tma_load_2d(dst, &a.b, DGRAD ? tile * 128 : k * 128, DGRAD ? k * 128 : tile * 128, bar_full(s),
+                wpol);
+    tma_load_2d(dst + T::A_BYTES, &a.a, k * 128, 0, bar_full(s), xpol);
+  };
+  // Warp 0 sets up the barriers, a lane each, while warp 1 takes the tensor
+  // memory; one block barrier covers both.
+  if (warp == 0) {
+    for (int i = lane; i < T::NUM_BARS; i += 32) {
+      const bool tempty = i >= 2 * T::DEEP + T::NBUF && i < 2 * T::DEEP + 2 * T::NBUF;
+      const bool sfull = i == 2 * T::DEEP + 2 * T::NBUF || i == 2 * T::DEEP + 2 * T::NBUF + 1;
+      const bool sempty = i == 2 * T::DEEP + 2 * T::NBUF + 2 || i == 2 * T::DEEP + 2 * T::NBUF + 3;
+      mbar_init(bars + 8u * i, sfull ? 32 : (tempty || sempty ? T::EPI : 1));
     }
-    for (int b = 0; b < T::NBUF; ++b) {
-      mbar_init(bar_tfull(b), 1);
-      mbar_init(bar_tempty(b), T::EPI);
-    }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(bar_sfull(b), 32);
-      mbar_init(bar_sempty(b), T::EPI);
-    }
-    mbar_init(bar_drain, 1);
-    *abort_flag = 0u;
+    if (lane == 0) *abort_flag = 0u;
     fence_mbarrier_init();
-    tma_prefetch_desc(&a.a);
-    tma_prefetch_desc(&a.b);
+  } else if (warp == 1) {
+    tmem_alloc(base + T::OFF_TMEM, T::TMEM_COLS);
+    tmem_relinquish();
+    tc_fence_before_sync();
   }
   __syncthreads();
   if (splits > 1) cluster_arrive();   // waited for before the first remote store
-  if (warp == 1) {
-    tmem_alloc(base + T::OFF_TMEM, T::TMEM_COLS);
-    tmem_relinquish();
-  }
-  tc_fence_before_sync();
-  __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(gbase + T::OFF_TMEM);
 
   float2 acc[T::NC / 2];   // epilogue threads: one output, NC tokens
   if (warp == 0) {
     if (lane == 0) {
-      const uint64_t wpol = l2_policy_evict_normal(), xpol = l2_policy_evict_last();
-      uint32_t s = 0, ph = 0, armed = 0;
+      uint32_t ps = 0, pph = 0, armed = 0;   // next stage, its phase, stages in use
       for (int k = kb; k < ke; ++k) {
-        if (!wait_bounded(bar_empty(s), ph ^ 1u, wc, kSiteProducerEmpty)) break;
-        const uint32_t dst = base + s * T::STAGE_BYTES;
-        mbar_arrive_expect_tx(bar_full(s), T::STAGE_BYTES);
-        tma_load_2d(dst, &a.b, DGRAD ? tile * 128 : k * 128, DGRAD ? k * 128 : tile * 128,
-                    bar_full(s), wpol);
-        tma_load_2d(dst + T::A_BYTES, &a.a, k * 128, 0, bar_full(s), xpol);
-        if (armed < T::STAGES) ++armed;
-        if (++s == T::STAGES) { s = 0; ph ^= 1u; }
+        if (!wait_bounded(bar_empty(ps), pph ^ 1u, wc, kSiteProducerEmpty)) break;
+        load(ps, k);
+        if (armed < stages) ++armed;
+        if (++ps == stages) { ps = 0; pph ^= 1u; }
       }
-      for (uint32_t i = 0; i < armed; ++i) {   // every armed load lands
-        if (s == 0) { s = T::STAGES; ph ^= 1u; }
-        --s;
-        wait_bounded(bar_full(s), ph, wc, kSiteDrainOperands, false);
+      for (uint32_t i = 0; i < armed; ++i) {   // the last load of every stage lands
+        if (ps == 0) { ps = stages; pph ^= 1u; }
+        --ps;
+        wait_bounded(bar_full(ps), pph, wc, kSiteDrainOperands, false);
       }
     }
     __syncwarp();
   } else if (warp == 1) {
     constexpr uint32_t idesc = make_idesc_e4m3(128, NT, DGRAD, false);
-    const uint64_t ad0 = DGRAD ? make_sdesc_mn_sw128(base, 16384, 1024)
-                               : make_sdesc_k_sw128(base, 1024);
-    const uint64_t bd0 = make_sdesc_k_sw128(base + T::A_BYTES, 1024);
+    const uint64_t ad0 = DGRAD ? make_sdesc_mn_sw128(stage0, 16384, 1024)
+                               : make_sdesc_k_sw128(stage0, 1024);
+    const uint64_t bd0 = make_sdesc_k_sw128(stage0 + T::A_BYTES, 1024);
     constexpr uint32_t kStepA = (DGRAD ? 4096 : 32) >> 4, kStepB = 32 >> 4;
     const bool issue = elect_one();
     uint32_t s = 0, ph = 0, buf = 0, bph = 1;
@@ -158,7 +159,7 @@ __global__ void __launch_bounds__(Few<NT>::THREADS, NT <= 64 ? 2 : 1)
         umma_commit(bar_empty(s));
         umma_commit(bar_tfull(buf));
       }
-      if (++s == T::STAGES) { s = 0; ph ^= 1u; }
+      if (++s == stages) { s = 0; ph ^= 1u; }
       if (++buf == T::NBUF) { buf = 0; bph ^= 1u; }
     }
     if (issue) umma_commit(bar_drain);
@@ -280,7 +281,7 @@ __global__ void __launch_bounds__(Few<NT>::THREADS, NT <= 64 ? 2 : 1)
 }
 
 template <int NT, bool DGRAD>
-cudaError_t launch_t(const B128Args& a, cudaStream_t stream) {
+cudaError_t launch_t(B128Args a, int num_sms, cudaStream_t stream) {
   using T = Few<NT>;
   auto kern = gemm_b128_few_kernel<NT, DGRAD>;
   static int ready[64] = {0};   // per device: attributes set
@@ -288,14 +289,15 @@ cudaError_t launch_t(const B128Args& a, cudaStream_t stream) {
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || !ready[dev]) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         T::SMEM_ALLOC);
+                                         T::smem(T::DEEP));
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) ready[dev] = 1;
   }
   cudaLaunchConfig_t lc = {};
   lc.blockDim = dim3(T::THREADS, 1, 1);
   lc.gridDim = dim3(a.num_tiles * a.splits, 1, 1);
-  lc.dynamicSmemBytes = T::SMEM_ALLOC;
+  a.stages = a.num_tiles * a.splits <= num_sms ? T::DEEP : T::STAGES;
+  lc.dynamicSmemBytes = T::smem(a.stages);
   lc.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -308,18 +310,19 @@ cudaError_t launch_t(const B128Args& a, cudaStream_t stream) {
 }
 
 template <int NT>
-cudaError_t launch_dir(bool dgrad, const B128Args& a, cudaStream_t stream) {
-  return dgrad ? launch_t<NT, true>(a, stream) : launch_t<NT, false>(a, stream);
+cudaError_t launch_dir(bool dgrad, const B128Args& a, int num_sms, cudaStream_t stream) {
+  return dgrad ? launch_t<NT, true>(a, num_sms, stream) : launch_t<NT, false>(a, num_sms, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_gemm_b128_few(int nt, bool dgrad, const B128Args& a, cudaStream_t stream) {
+cudaError_t launch_gemm_b128_few(int nt, bool dgrad, const B128Args& a, int num_sms,
+                                 cudaStream_t stream) {
   switch (nt) {
-    case 16: return launch_dir<16>(dgrad, a, stream);
-    case 32: return launch_dir<32>(dgrad, a, stream);
-    case 64: return launch_dir<64>(dgrad, a, stream);
-    case 128: return launch_dir<128>(dgrad, a, stream);
+    case 16: return launch_dir<16>(dgrad, a, num_sms, stream);
+    case 32: return launch_dir<32>(dgrad, a, num_sms, stream);
+    case 64: return launch_dir<64>(dgrad, a, num_sms, stream);
+    case 128: return launch_dir<128>(dgrad, a, num_sms, stream);
   }
   return cudaErrorInvalidValue;
 }

@@ -275,6 +275,7 @@ struct B128Args {
   int32_t out_fp32;
   void* out_ptr;           // few tokens: stored without a map
   int32_t splits;          // few tokens: CTAs (a cluster) that share a tile's reduction
+  int32_t stages;          // few tokens: operand stages
   int* err;
   int* err_site;
   uint64_t timeout_ns;
@@ -286,6 +287,7 @@ struct B128Config {
 };
 cudaError_t launch_gemm_b128(const B128Config& c, bool dgrad, const B128Args& a, int num_sms,
                              cudaStream_t stream);
-cudaError_t launch_gemm_b128_few(int nt, bool dgrad, const B128Args& a, cudaStream_t stream);
+cudaError_t launch_gemm_b128_few(int nt, bool dgrad, const B128Args& a, int num_sms,
+                                 cudaStream_t stream);
 
 }  // namespace forge

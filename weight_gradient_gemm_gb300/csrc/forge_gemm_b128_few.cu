@@ -13,7 +13,7 @@
 // every run.
 //
 // Warp roles: 0 loads (TMA), 1 issues the MMAs, 2 multiplies the scales, from
-// 4 on the epilogue (the 32 outputs of a TMEM lane quadrant and up to 64
+// 4 on the epilogue (the 32 outputs of a TMEM lane quadrant and up to 32
 // tokens a warp).  Every wait is bounded.
 #include <cuda_bf16.h>
 
@@ -26,17 +26,17 @@ namespace {
 
 template <int NT>
 struct Few {
-  static constexpr int EPI = NT <= 64 ? 4 : 8;          // epilogue warps
+  static constexpr int EPI = NT <= 32 ? 4 : NT / 8;     // epilogue warps
   static constexpr int THREADS = 128 + 32 * EPI;
-  static constexpr int NC = NT <= 64 ? NT : 64;         // tokens per epilogue thread
+  static constexpr int NC = NT <= 32 ? NT : 32;         // tokens per epilogue thread
   static constexpr int A_BYTES = kBM * 128;
   static constexpr int STAGE_BYTES = A_BYTES + NT * 128;
   // Operand stages: as many as let two CTAs share an SM, or, where the grid
   // has no more than one CTA for each, as many as fit.
   static constexpr int STAGES = NT <= 16 ? 5 : 4;
   static constexpr int DEEP = NT <= 16 ? 11 : (NT == 32 ? 9 : (NT == 64 ? 8 : 6));
-  static constexpr int NBUF = NT <= 32 ? 8 : (NT == 64 ? 4 : 2);   // TMEM accumulators
-  static constexpr int TMEM_COLS = NT * NBUF;           // 128 or 256: two CTAs fit an SM
+  static constexpr int NBUF = NT <= 32 ? 8 : 4;         // TMEM accumulators
+  static constexpr int TMEM_COLS = NT * NBUF;           // two CTAs fit an SM up to 64 tokens
   static constexpr int SC_BATCH = 8;
   static constexpr int SC_BYTES = 2 * SC_BATCH * NT * 4;
   static constexpr int PART_BYTES = NT * kBM * 4;       // one tile of fp32 sums
@@ -166,22 +166,31 @@ __global__ void __launch_bounds__(Few<NT>::THREADS, NT <= 64 ? 2 : 1)
     wait_bounded(bar_drain, 0u, wc, kSiteDrainMma, false);
     __syncwarp();
   } else if (warp == 2) {
-    // sx[t][k] sw[tile][k]; tokens past the last count zero
+    // sx[t][k] sw[tile][k]; tokens past the last count zero.  A batch's loads
+    // all start before any is used.
+    constexpr int PT = (NT + 31) / 32;   // tokens per lane
     uint32_t b = 0, ph = 1;
     for (int k0 = kb; k0 < ke; k0 += T::SC_BATCH) {
+      float rw[T::SC_BATCH], rx[PT][T::SC_BATCH];
+#pragma unroll
+      for (int i = 0; i < T::SC_BATCH; ++i) {
+        const int k = min(k0 + i, ke - 1);   // past the end: loaded again, not used
+        rw[i] = __ldg(a.sw + static_cast<int64_t>(tile) * a.sw_n + static_cast<int64_t>(k) * a.sw_k);
+#pragma unroll
+        for (int j = 0; j < PT; ++j) {
+          const int t = lane + 32 * j;
+          rx[j][i] = __ldg(a.sa + static_cast<int64_t>(min(t, a.m - 1)) * a.num_kb + k);
+        }
+      }
       const bool good = wait_bounded(bar_sempty(b), ph, wc, kSiteLoaderEmpty);
       if (!__all_sync(0xffffffffu, good)) break;
 #pragma unroll
-      for (int i = 0; i < T::SC_BATCH; ++i) {
-        const int k = k0 + i;
-        const float rw = k < ke ? __ldg(a.sw + static_cast<int64_t>(tile) * a.sw_n +
-                                        static_cast<int64_t>(k) * a.sw_k)
-                                : 0.0f;
+      for (int i = 0; i < T::SC_BATCH; ++i)
 #pragma unroll
-        for (int t = lane; t < NT; t += 32)
-          scales[(b * T::SC_BATCH + i) * NT + t] =
-              k < ke && t < a.m ? __ldg(a.sa + static_cast<int64_t>(t) * a.num_kb + k) * rw : 0.0f;
-      }
+        for (int j = 0; j < PT; ++j) {
+          const int t = lane + 32 * j;
+          if (t < NT) scales[(b * T::SC_BATCH + i) * NT + t] = t < a.m ? rx[j][i] * rw[i] : 0.0f;
+        }
       mbar_arrive(bar_sfull(b));
       if (++b == 2) { b = 0; ph ^= 1u; }
     }

@@ -18,7 +18,9 @@ struct Span {
   uint64_t n;
 };
 
-bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+bool aligned(const void* p, uintptr_t to) {
+  return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0;
+}
 
 bool meet(const Span& a, const Span& b) {
   if (!a.p || !b.p || a.n == 0 || b.n == 0) return false;
@@ -73,13 +75,15 @@ B128Config choose_b128(int64_t m, int64_t n, int64_t num_kb, bool dgrad, const f
     c.few = m <= (dgrad ? 0 : 16) ? 16 : (m <= 32 ? 32 : (m <= 64 ? 64 : 128));
     const int64_t tiles = (n + 127) / 128;
     while (c.splits < 8 && tiles * c.splits * 2 <= num_sms && num_kb >= 4 * c.splits) c.splits *= 2;
-    if (tune.splits) c.splits = tune.splits >= 8 ? 8 : (tune.splits >= 4 ? 4 : tune.splits >= 2 ? 2 : 1);
+    if (tune.splits)   // the cluster sizes there are: powers of two
+      c.splits = tune.splits >= 8 ? 8 : (tune.splits >= 4 ? 4 : (tune.splits >= 2 ? 2 : 1));
     return c;
   }
   const int64_t pairs = num_sms / 2;
   const int64_t tiles1 = (m + 127) / 128 * ((n + 127) / 128);
   const int64_t tiles2 = (m + 255) / 256 * ((n + 255) / 256);
-  const int64_t t1 = (tiles1 + num_sms - 1) / num_sms * 490, t2 = (tiles2 + pairs - 1) / pairs * 770;
+  const int64_t t1 = (tiles1 + num_sms - 1) / num_sms * 490;
+  const int64_t t2 = (tiles2 + pairs - 1) / pairs * 770;
   if (tune.cta_group ? tune.cta_group == 2 : t2 < t1) c.cg = 2, c.bn = 256;
   return c;
 }
@@ -106,7 +110,8 @@ forge_status product_b128(const void* A, const float* sa, const void* W, const f
   if (st != FORGE_OK) return static_cast<forge_status>(st);
   forge_tuning tune;
   forge_get_tuning(&tune);
-  const B128Config cfg = choose_b128(m, n, static_cast<int64_t>(blocks128(k)), dgrad, tune, d.num_sms);
+  const B128Config cfg =
+      choose_b128(m, n, static_cast<int64_t>(blocks128(k)), dgrad, tune, d.num_sms);
   B128Args a;
   std::memset(&a, 0, sizeof(a));
   const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
@@ -126,7 +131,8 @@ forge_status product_b128(const void* A, const float* sa, const void* W, const f
   a.num_kb = static_cast<int32_t>(blocks128(k));
   a.sw_n = dgrad ? 1 : a.num_kb;                              // sw [d_out / 128][d_in / 128]
   a.sw_k = dgrad ? static_cast<int32_t>(blocks128(n)) : 1;
-  const int64_t tm = 128 * cfg.cg, tiles_m = cfg.few ? 1 : (m + tm - 1) / tm, tiles_n = (n + cfg.bn - 1) / cfg.bn;
+  const int64_t tm = 128 * cfg.cg, tiles_m = cfg.few ? 1 : (m + tm - 1) / tm;
+  const int64_t tiles_n = (n + cfg.bn - 1) / cfg.bn;
   if (tiles_m * tiles_n > kMaxIndex / 2) return FORGE_ERR_SHAPE;
   a.tiles_m = static_cast<int32_t>(tiles_m);
   a.tiles_n = static_cast<int32_t>(tiles_n);
@@ -166,7 +172,8 @@ forge_status forge_rmsnorm(const void* x, const void* residual, const void* gain
   const Span o_r{rstd, static_cast<uint64_t>(rows) * 4};
   if (clash({o_y, o_c, o_s, o_r}, {in_x, in_r, in_g, o_sum})) return FORGE_ERR_ALIAS;
   // the sum may replace x or the residual (each element is read before it is written)
-  if (meet(o_sum, in_g) || (sum != x && meet(o_sum, in_x)) || (sum != residual && meet(o_sum, in_r)))
+  if (meet(o_sum, in_g) || (sum != x && meet(o_sum, in_x)) ||
+      (sum != residual && meet(o_sum, in_r)))
     return FORGE_ERR_ALIAS;
   HostDevice d;
   const int st = host_device(&d);
@@ -191,7 +198,8 @@ forge_status forge_rmsnorm(const void* x, const void* residual, const void* gain
 size_t forge_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t cols) {
   HostDevice d;
   if (check_rows(rows, cols, kNormMaxCols) != FORGE_OK || host_device(&d) != FORGE_OK) return 0;
-  return static_cast<size_t>(rmsnorm_bwd_blocks(rows, static_cast<int>(cols), d.num_sms)) * cols * 4;
+  const int blocks = rmsnorm_bwd_blocks(rows, static_cast<int>(cols), d.num_sms);
+  return static_cast<size_t>(blocks) * static_cast<size_t>(cols) * 4;
 }
 
 forge_status forge_rmsnorm_backward(const void* dY, const void* h, const void* gain,
@@ -222,7 +230,8 @@ forge_status forge_rmsnorm_backward(const void* dY, const void* h, const void* g
     return dgain ? status(cudaMemsetAsync(dgain, 0, static_cast<size_t>(cols) * 4, cs)) : FORGE_OK;
   if (dgain) {
     if (!workspace) return FORGE_ERR_NULL;
-    if (workspace_bytes < forge_rmsnorm_backward_workspace_bytes(rows, cols)) return FORGE_ERR_SHAPE;
+    if (workspace_bytes < forge_rmsnorm_backward_workspace_bytes(rows, cols))
+      return FORGE_ERR_SHAPE;
   }
   NormBwdArgs a;
   a.dy = static_cast<const uint16_t*>(dY);
@@ -249,7 +258,8 @@ forge_status forge_quantize_b128(const void* x, void* codes, float* scales, int6
   if (!x || !codes || !scales) return FORGE_ERR_NULL;
   if (!all_aligned16({x, codes, scales})) return FORGE_ERR_ALIGN;
   const uint64_t n = static_cast<uint64_t>(rows) * cols;
-  const uint64_t nb = (block_rows == 1 ? static_cast<uint64_t>(rows) : blocks128(rows)) * blocks128(cols);
+  const uint64_t nb =
+      (block_rows == 1 ? static_cast<uint64_t>(rows) : blocks128(rows)) * blocks128(cols);
   if (block_rows == 128 && nb > static_cast<uint64_t>(kMaxIndex)) return FORGE_ERR_SHAPE;
   if (clash({{codes, n}, {scales, nb * 4}}, {{x, 2 * n}})) return FORGE_ERR_ALIAS;
   HostDevice d;

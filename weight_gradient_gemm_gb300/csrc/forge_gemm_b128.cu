@@ -43,7 +43,12 @@ struct Traits8 {
   static constexpr int BNL = BN / CG;
   static constexpr int A_BYTES = kBM * 128;
   static constexpr int STAGE_BYTES = A_BYTES + BNL * 128;
-  static constexpr int OUT_BYTES = kEpiWarps * 4096;   // one 32-row slab of 128-byte rows a warp
+  static constexpr int NC = BN / 2;                    // columns per epilogue thread
+  static constexpr int GROUPS = NC / 64;               // runs of 64 neighbouring columns among them
+  // One slab of 32 rows x 128 bytes a warp for its output.  (Two, with four
+  // operand stages, measured the same on pairs and 19 % slower on one CTA.)
+  static constexpr int SLAB = 4096;
+  static constexpr int OUT_BYTES = kEpiWarps * SLAB;
   static constexpr int STAGES = 5;
   // The tile's accumulator is cut into pieces of 128 columns with TMEM buffers
   // of their own, so that a piece's next product waits for the warps that read
@@ -54,8 +59,6 @@ struct Traits8 {
   static constexpr int NWB = BN / 128;                 // weight blocks across the tile
   static constexpr int SC_BATCH = 8;                   // 128-blocks whose scales move together
   static constexpr int SC_BYTES = 2 * SC_BATCH * NWB * kBM * 4;
-  static constexpr int NC = BN / 2;                    // columns per epilogue thread
-  static constexpr int GROUPS = NC / 64;               // runs of 64 neighbouring columns among them
   // columns per tensor-memory load: 32 where two of them fit beside the sums
   // (with 128 sums they spill, and the kernel ran 19 % slower)
   static constexpr int LD = NC == 64 ? 32 : 16;
@@ -81,7 +84,8 @@ __device__ __forceinline__ void tile_of(int t, const B128Args& a, int& tm, int& 
 }
 
 template <int CG, int BN, bool DGRAD>
-__global__ void __launch_bounds__(kThreads8, 1) gemm_b128_kernel(const __grid_constant__ B128Args a) {
+__global__ void __launch_bounds__(kThreads8, 1)
+    gemm_b128_kernel(const __grid_constant__ B128Args a) {
   using T = Traits8<CG, BN>;
   constexpr bool kPair = CG == 2;
   extern __shared__ uint8_t smem_raw[];
@@ -149,188 +153,189 @@ __global__ void __launch_bounds__(kThreads8, 1) gemm_b128_kernel(const __grid_co
   const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(gbase + T::OFF_TMEM);
 
   if (warp < 4) {
-  regs_dec<kRegsRole>();
-  if (warp == 0) {
-    // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      const uint64_t pol = l2_policy_evict_normal();
-      uint32_t s = 0, ph = 0;   // next stage, and its phase
-      uint32_t armed = 0;       // stages filled so far, at most STAGES
+    regs_dec<kRegsRole>();
+    if (warp == 0) {
+      // ------------------------------------------------------------ producer
+      if (lane == 0) {
+        const uint64_t pol = l2_policy_evict_normal();
+        uint32_t s = 0, ph = 0;   // next stage, and its phase
+        uint32_t armed = 0;       // stages filled so far, at most STAGES
+        bool ok = true;
+        for (int t = unit0; ok && t < a.num_tiles; t += units) {
+          int tm, tn;
+          tile_of(t, a, tm, tn);
+          const int ya = tm * T::TM + static_cast<int>(rank) * kBM;
+          const int nb = tn * BN + static_cast<int>(rank) * T::BNL;
+          for (int k = 0; k < a.num_kb; ++k) {
+            if (!wait_bounded(bar_empty(s), ph ^ 1u, wc, kSiteProducerEmpty)) { ok = false; break; }
+            const uint32_t dst = base + s * T::STAGE_BYTES;
+            // the weight's box: [BNL rows][128 of K], or for the input gradient
+            // [128 of K][128 columns] per 128 columns
+            if constexpr (kPair) {
+              const uint32_t fb = mapa_shared(bar_full(s), 0);
+              if (leader) mbar_arrive_expect_tx(bar_full(s), 2 * T::STAGE_BYTES);
+              tma_load_2d_pair(dst, &a.a, k * 128, ya, fb, pol);
+              if constexpr (DGRAD) {
+#pragma unroll
+                for (int c = 0; c < T::BNL / 128; ++c)
+                  tma_load_2d_pair(dst + T::A_BYTES + c * 16384, &a.b, nb + c * 128, k * 128, fb,
+                                   pol);
+              } else {
+                tma_load_2d_pair(dst + T::A_BYTES, &a.b, k * 128, nb, fb, pol);
+              }
+            } else {
+              mbar_arrive_expect_tx(bar_full(s), T::STAGE_BYTES);
+              tma_load_2d(dst, &a.a, k * 128, ya, bar_full(s), pol);
+              if constexpr (DGRAD) {
+#pragma unroll
+                for (int c = 0; c < T::BNL / 128; ++c)
+                  tma_load_2d(dst + T::A_BYTES + c * 16384, &a.b, nb + c * 128, k * 128,
+                              bar_full(s), pol);
+              } else {
+                tma_load_2d(dst + T::A_BYTES, &a.b, k * 128, nb, bar_full(s), pol);
+              }
+            }
+            if (armed < T::STAGES) ++armed;
+            if (++s == T::STAGES) { s = 0; ph ^= 1u; }
+          }
+        }
+        // Before the CTA can exit, every stage's last release has to arrive (on a
+        // pair the leader's MMAs signal it from afar); after a timeout, every
+        // load that is under way has to land (a pair's complete on the leader's
+        // barriers).
+        for (uint32_t i = 0; i < armed; ++i) {
+          if (s == 0) { s = T::STAGES; ph ^= 1u; }
+          --s;
+          const bool freed = ok && wait_bounded(bar_empty(s), ph, wc, kSiteDrainOperands);
+          if (!freed && leader) wait_bounded(bar_full(s), ph, wc, kSiteDrainOperands, false);
+        }
+      }
+      __syncwarp();
+    } else if (warp == 1 || warp == 3) {
+      // ------------------------------------------------------------ MMA issuers
+      // A product costs its issuing thread about 39 cycles, a commit 41 and a
+      // wait that is ready 60, so one thread's 8 products, 3 commits and 3 waits
+      // per block of a pair (634 cycles measured) would be slower than the tensor
+      // core (512).  Two warps share them: each a piece of a pair's tile, or
+      // every other block of a single CTA's.  They walk the blocks with the
+      // whole warp, so that addresses and descriptors stay in uniform registers,
+      // and one elected lane issues.
+      if (leader) {
+        constexpr uint32_t idesc = make_idesc_e4m3(T::TM, 128, false, DGRAD);
+        const uint64_t ad0 = make_sdesc_k_sw128(base, 1024);
+        const uint64_t bd0 = DGRAD ? make_sdesc_mn_sw128(base + T::A_BYTES, 16384, 1024)
+                                   : make_sdesc_k_sw128(base + T::A_BYTES, 1024);
+        // 32 of K further: 32 bytes K-major, 32 rows MN-major
+        constexpr uint32_t kStepA = 32 >> 4, kStepB = (DGRAD ? 4096 : 32) >> 4;
+        // 64 of each CTA's columns further (pairs): 64 rows K-major, 64 bytes MN-major
+        constexpr uint32_t kPieceB = (DGRAD ? 64 : 8192) >> 4;
+        const bool issue = elect_one();
+        const uint32_t me = warp >> 1;   // issuer 0 or 1
+        const uint32_t pc = T::PIECES == 1 ? 0 : me;
+        uint32_t s = 0, ph = 0, buf = 0, bph = 1, turn = 0;
+        bool ok = true;
+        for (int t = unit0; ok && t < a.num_tiles; t += units) {
+#pragma unroll 1
+          for (int k = 0; k < a.num_kb; ++k) {
+            // Both issuers wait for every block's stage and release it, also where
+            // the block is the other's: a stage goes from one to the other, and a
+            // parity wait that skipped or lagged a phase would take another for
+            // its own.  (TMEM buffers stay with one issuer: their number is even.)
+            const bool mine = T::PIECES > 1 || turn == me;
+            const uint32_t b = pc * T::NBUF + buf;
+            ok = wait_bounded(bar_full(s), ph, wc, kSiteMmaFull) &&
+                 (!mine || wait_bounded(bar_tempty(b), bph, wc, kSiteMmaTmemEmpty));
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            if (mine) {
+              tc_fence_after_sync();
+              const uint64_t ad = ad0 + s * (T::STAGE_BYTES >> 4);
+              const uint64_t bd = bd0 + s * (T::STAGE_BYTES >> 4) + pc * kPieceB;
+              const uint32_t d = tmem_base + b * 128;
+              if (issue) {
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                  if constexpr (kPair)
+                    umma_e4m3_pair(d, ad + kk * kStepA, bd + kk * kStepB, idesc, kk != 0);
+                  else
+                    umma_e4m3(d, ad + kk * kStepA, bd + kk * kStepB, idesc, kk != 0);
+                }
+                // the stage is free, and the piece complete, once these have run
+                if constexpr (kPair) {
+                  umma_commit_pair_mc(bar_empty(s), 0x3);
+                  umma_commit_pair_mc(bar_tfull(b), 0x3);
+                } else {
+                  umma_commit(bar_empty(s));
+                  umma_commit(bar_tfull(b));
+                }
+              }
+            } else if (issue) {
+              mbar_arrive(bar_empty(s));
+            }
+            turn ^= 1u;
+            if (++s == T::STAGES) { s = 0; ph ^= 1u; }
+            if (++buf == T::NBUF) { buf = 0; bph ^= 1u; }
+          }
+        }
+        // every MMA issued must complete before the tensor memory is freed
+        if (issue) {
+          if constexpr (kPair) umma_commit_pair_mc(bar_drain, 0x1); else umma_commit(bar_drain);
+        }
+        wait_bounded(bar_drain, 0u, wc, kSiteDrainMma, false);
+      }
+      __syncwarp();
+    } else if (warp == 2) {
+      // ------------------------------------------------------------ scales
+      // sa[row][k] sw[column block][k] for the tile's 128 rows, a batch of
+      // blocks at a time.  (Read by the epilogue threads themselves, one block
+      // ahead, their latency bounded the whole kernel: 462 ns per block of a
+      // 128 x 128 tile.)  Rows and column blocks outside count zero.
+      uint32_t cnt = 0;
       bool ok = true;
       for (int t = unit0; ok && t < a.num_tiles; t += units) {
         int tm, tn;
         tile_of(t, a, tm, tn);
-        const int ya = tm * T::TM + static_cast<int>(rank) * kBM;
-        const int nb = tn * BN + static_cast<int>(rank) * T::BNL;
-        for (int k = 0; k < a.num_kb; ++k) {
-          if (!wait_bounded(bar_empty(s), ph ^ 1u, wc, kSiteProducerEmpty)) { ok = false; break; }
-          const uint32_t dst = base + s * T::STAGE_BYTES;
-          // the weight's box: [BNL rows][128 of K], or for the input gradient
-          // [128 of K][128 columns] per 128 columns
-          if constexpr (kPair) {
-            const uint32_t fb = mapa_shared(bar_full(s), 0);
-            if (leader) mbar_arrive_expect_tx(bar_full(s), 2 * T::STAGE_BYTES);
-            tma_load_2d_pair(dst, &a.a, k * 128, ya, fb, pol);
-            if constexpr (DGRAD) {
+        const int row0 = tm * T::TM + static_cast<int>(rank) * kBM + lane;
+        const int wb0 = tn * T::NWB;
+        for (int k0 = 0; k0 < a.num_kb; k0 += T::SC_BATCH, ++cnt) {
+          float ra[4][T::SC_BATCH];
 #pragma unroll
-              for (int c = 0; c < T::BNL / 128; ++c)
-                tma_load_2d_pair(dst + T::A_BYTES + c * 16384, &a.b, nb + c * 128, k * 128, fb, pol);
-            } else {
-              tma_load_2d_pair(dst + T::A_BYTES, &a.b, k * 128, nb, fb, pol);
-            }
-          } else {
-            mbar_arrive_expect_tx(bar_full(s), T::STAGE_BYTES);
-            tma_load_2d(dst, &a.a, k * 128, ya, bar_full(s), pol);
-            if constexpr (DGRAD) {
+          for (int j = 0; j < 4; ++j) {
+            const int row = row0 + 32 * j;
+            const float* p = a.sa + static_cast<int64_t>(row < a.m ? row : 0) * a.num_kb + k0;
 #pragma unroll
-              for (int c = 0; c < T::BNL / 128; ++c)
-                tma_load_2d(dst + T::A_BYTES + c * 16384, &a.b, nb + c * 128, k * 128, bar_full(s),
-                            pol);
-            } else {
-              tma_load_2d(dst + T::A_BYTES, &a.b, k * 128, nb, bar_full(s), pol);
-            }
+            for (int i = 0; i < T::SC_BATCH; ++i)
+              ra[j][i] = row < a.m && k0 + i < a.num_kb ? __ldg(p + i) : 0.0f;
           }
-          if (armed < T::STAGES) ++armed;
-          if (++s == T::STAGES) { s = 0; ph ^= 1u; }
-        }
-      }
-      // Before the CTA can exit, every stage's last release has to arrive (on a
-      // pair the leader's MMAs signal it from afar); after a timeout, every
-      // load that is under way has to land (a pair's complete on the leader's
-      // barriers).
-      for (uint32_t i = 0; i < armed; ++i) {
-        if (s == 0) { s = T::STAGES; ph ^= 1u; }
-        --s;
-        const bool freed = ok && wait_bounded(bar_empty(s), ph, wc, kSiteDrainOperands);
-        if (!freed && leader) wait_bounded(bar_full(s), ph, wc, kSiteDrainOperands, false);
-      }
-    }
-    __syncwarp();
-  } else if (warp == 1 || warp == 3) {
-    // ------------------------------------------------------------ MMA issuers
-    // A product costs its issuing thread about 39 cycles, a commit 41 and a
-    // wait that is ready 60, so one thread's 8 products, 3 commits and 3 waits
-    // per block of a pair (634 cycles measured) would be slower than the tensor
-    // core (512).  Two warps share them: each a piece of a pair's tile, or
-    // every other block of a single CTA's.  They walk the blocks with the
-    // whole warp, so that addresses and descriptors stay in uniform registers,
-    // and one elected lane issues.
-    if (leader) {
-      constexpr uint32_t idesc = make_idesc_e4m3(T::TM, 128, false, DGRAD);
-      const uint64_t ad0 = make_sdesc_k_sw128(base, 1024);
-      const uint64_t bd0 = DGRAD ? make_sdesc_mn_sw128(base + T::A_BYTES, 16384, 1024)
-                                 : make_sdesc_k_sw128(base + T::A_BYTES, 1024);
-      // 32 of K further: 32 bytes K-major, 32 rows MN-major
-      constexpr uint32_t kStepA = 32 >> 4, kStepB = (DGRAD ? 4096 : 32) >> 4;
-      // 64 of each CTA's columns further (pairs): 64 rows K-major, 64 bytes MN-major
-      constexpr uint32_t kPieceB = (DGRAD ? 64 : 8192) >> 4;
-      const bool issue = elect_one();
-      const uint32_t me = warp >> 1;   // issuer 0 or 1
-      const uint32_t pc = T::PIECES == 1 ? 0 : me;
-      uint32_t s = 0, ph = 0, buf = 0, bph = 1, turn = 0;
-      bool ok = true;
-      for (int t = unit0; ok && t < a.num_tiles; t += units) {
-#pragma unroll 1
-        for (int k = 0; k < a.num_kb; ++k) {
-          // Both issuers wait for every block's stage and release it, also where
-          // the block is the other's: a stage goes from one to the other, and a
-          // parity wait that skipped or lagged a phase would take another for
-          // its own.  (TMEM buffers stay with one issuer: their number is even.)
-          const bool mine = T::PIECES > 1 || turn == me;
-          const uint32_t b = pc * T::NBUF + buf;
-          ok = wait_bounded(bar_full(s), ph, wc, kSiteMmaFull) &&
-               (!mine || wait_bounded(bar_tempty(b), bph, wc, kSiteMmaTmemEmpty));
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          if (mine) {
-            tc_fence_after_sync();
-            const uint64_t ad = ad0 + s * (T::STAGE_BYTES >> 4);
-            const uint64_t bd = bd0 + s * (T::STAGE_BYTES >> 4) + pc * kPieceB;
-            const uint32_t d = tmem_base + b * 128;
-            if (issue) {
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk) {
-                if constexpr (kPair)
-                  umma_e4m3_pair(d, ad + kk * kStepA, bd + kk * kStepB, idesc, kk != 0);
-                else
-                  umma_e4m3(d, ad + kk * kStepA, bd + kk * kStepB, idesc, kk != 0);
-              }
-              // the stage is free, and the piece complete, once these have run
-              if constexpr (kPair) {
-                umma_commit_pair_mc(bar_empty(s), 0x3);
-                umma_commit_pair_mc(bar_tfull(b), 0x3);
-              } else {
-                umma_commit(bar_empty(s));
-                umma_commit(bar_tfull(b));
-              }
-            }
-          } else if (issue) {
-            mbar_arrive(bar_empty(s));
-          }
-          turn ^= 1u;
-          if (++s == T::STAGES) { s = 0; ph ^= 1u; }
-          if (++buf == T::NBUF) { buf = 0; bph ^= 1u; }
-        }
-      }
-      // every MMA issued must complete before the tensor memory is freed
-      if (issue) {
-        if constexpr (kPair) umma_commit_pair_mc(bar_drain, 0x1); else umma_commit(bar_drain);
-      }
-      wait_bounded(bar_drain, 0u, wc, kSiteDrainMma, false);
-    }
-    __syncwarp();
-  } else if (warp == 2) {
-    // ------------------------------------------------------------ scales
-    // sa[row][k] sw[column block][k] for the tile's 128 rows, a batch of
-    // blocks at a time.  (Read by the epilogue threads themselves, one block
-    // ahead, their latency bounded the whole kernel: 462 ns per block of a
-    // 128 x 128 tile.)  Rows and column blocks outside count zero.
-    uint32_t cnt = 0;
-    bool ok = true;
-    for (int t = unit0; ok && t < a.num_tiles; t += units) {
-      int tm, tn;
-      tile_of(t, a, tm, tn);
-      const int row0 = tm * T::TM + static_cast<int>(rank) * kBM + lane;
-      const int wb0 = tn * T::NWB;
-      for (int k0 = 0; k0 < a.num_kb; k0 += T::SC_BATCH, ++cnt) {
-        float ra[4][T::SC_BATCH];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int row = row0 + 32 * j;
-          const float* p = a.sa + static_cast<int64_t>(row < a.m ? row : 0) * a.num_kb + k0;
+          const int b = cnt & 1;
+          const bool good =
+              wait_bounded(bar_sempty(b), ((cnt >> 1) & 1u) ^ 1u, wc, kSiteLoaderEmpty);
+          if (!__all_sync(0xffffffffu, good)) { ok = false; break; }
 #pragma unroll
           for (int i = 0; i < T::SC_BATCH; ++i)
-            ra[j][i] = row < a.m && k0 + i < a.num_kb ? __ldg(p + i) : 0.0f;
+#pragma unroll
+            for (int w = 0; w < T::NWB; ++w) {
+              const bool in = k0 + i < a.num_kb && (wb0 + w) * 128 < a.n;
+              const float rw = in ? __ldg(a.sw + static_cast<int64_t>(wb0 + w) * a.sw_n +
+                                          static_cast<int64_t>(k0 + i) * a.sw_k)
+                                  : 0.0f;
+              float* dst = scales + ((b * T::SC_BATCH + i) * T::NWB + w) * kBM + lane;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) dst[32 * j] = in ? ra[j][i] * rw : 0.0f;
+            }
+          mbar_arrive(bar_sfull(b));
         }
-        const int b = cnt & 1;
-        const bool good =
-            wait_bounded(bar_sempty(b), ((cnt >> 1) & 1u) ^ 1u, wc, kSiteLoaderEmpty);
-        if (!__all_sync(0xffffffffu, good)) { ok = false; break; }
-#pragma unroll
-        for (int i = 0; i < T::SC_BATCH; ++i)
-#pragma unroll
-          for (int w = 0; w < T::NWB; ++w) {
-            const bool in = k0 + i < a.num_kb && (wb0 + w) * 128 < a.n;
-            const float rw = in ? __ldg(a.sw + static_cast<int64_t>(wb0 + w) * a.sw_n +
-                                        static_cast<int64_t>(k0 + i) * a.sw_k)
-                                : 0.0f;
-            float* dst = scales + ((b * T::SC_BATCH + i) * T::NWB + w) * kBM + lane;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) dst[32 * j] = in ? ra[j][i] * rw : 0.0f;
-          }
-        mbar_arrive(bar_sfull(b));
       }
+      __syncwarp();
     }
-    __syncwarp();
-  }
   } else {
     regs_inc<kRegsEpi>();
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;                       // TMEM lane quadrant this warp may read
     const int h = (warp - 4) >> 2;                // piece (pairs), or half of the one piece
     const uint32_t lane_addr = static_cast<uint32_t>(q * 32) << 16;
-    const uint32_t slab = base + T::OFF_OUT + (warp - 4) * 4096;
-    uint8_t* gslab = gbase + T::OFF_OUT + (warp - 4) * 4096;
+    const uint32_t slab = base + T::OFF_OUT + (warp - 4) * T::SLAB;
+    uint8_t* gslab = gbase + T::OFF_OUT + (warp - 4) * T::SLAB;
     const uint32_t bpiece = T::PIECES == 1 ? 0 : h * T::NBUF;   // first buffer of this warp's piece
     uint32_t buf = 0, bph = 0, sb = 0, sph = 0;
     bool ok = true;
@@ -395,32 +400,40 @@ __global__ void __launch_bounds__(kThreads8, 1) gemm_b128_kernel(const __grid_co
       }
       if (!ok) break;
       // store through this warp's slab: boxes of 32 rows x 128 bytes
+      // the slab is free once the store before has read it
+      auto claim = [&]() {
+        if (lane == 0) bulk_wait_group_read<0>();
+        __syncwarp();
+      };
+      auto send = [&](int col) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_2d(&a.out, col, row0, slab);
+          bulk_commit_group();
+        }
+      };
+      if (row0 >= a.m) continue;
 #pragma unroll
       for (int g = 0; g < T::GROUPS; ++g) {
         const int col = col0 + g * 128;
-        if (row0 >= a.m || col >= a.n) continue;
+        if (col >= a.n) continue;
         const float2* v = acc + g * 32;
         if (a.out_fp32) {
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             if (col + 32 * c >= a.n) break;
-            if (lane == 0) bulk_wait_group_read<0>();
-            __syncwarp();
+            claim();
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const float2 x = v[c * 16 + 2 * i], y = v[c * 16 + 2 * i + 1];
-              *reinterpret_cast<float4*>(gslab + sw128_off(lane, i)) = make_float4(x.x, x.y, y.x, y.y);
+              *reinterpret_cast<float4*>(gslab + sw128_off(lane, i)) =
+                  make_float4(x.x, x.y, y.x, y.y);
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              tma_store_2d(&a.out, col + 32 * c, row0, slab);
-              bulk_commit_group();
-            }
+            send(col + 32 * c);
           }
         } else {
-          if (lane == 0) bulk_wait_group_read<0>();
-          __syncwarp();
+          claim();
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const float2* x = v + 4 * i;
@@ -428,12 +441,7 @@ __global__ void __launch_bounds__(kThreads8, 1) gemm_b128_kernel(const __grid_co
                 make_uint4(pack_bf16x2(x[0].x, x[0].y), pack_bf16x2(x[1].x, x[1].y),
                            pack_bf16x2(x[2].x, x[2].y), pack_bf16x2(x[3].x, x[3].y));
           }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            tma_store_2d(&a.out, col, row0, slab);
-            bulk_commit_group();
-          }
+          send(col);
         }
       }
     }
@@ -491,7 +499,8 @@ cudaError_t launch_t(const B128Args& a, int num_sms, cudaStream_t stream) {
     if (!cached) {
       lc.gridDim = dim3(2 * (num_sms / 2), 1, 1);
       cudaError_t e = cudaOccupancyMaxActiveClusters(&units, kern, &lc);
-      if (e != cudaSuccess || units <= 0) return e != cudaSuccess ? e : cudaErrorInvalidConfiguration;
+      if (e != cudaSuccess) return e;
+      if (units <= 0) return cudaErrorInvalidConfiguration;
       if (dev >= 0 && dev < 64) max_units[dev] = units;
     }
     units = units < num_sms / 2 ? units : num_sms / 2;

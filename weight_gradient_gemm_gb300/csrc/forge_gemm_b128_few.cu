@@ -175,7 +175,8 @@ __global__ void __launch_bounds__(Few<NT>::THREADS, NT <= 64 ? 2 : 1)
 #pragma unroll
       for (int i = 0; i < T::SC_BATCH; ++i) {
         const int k = min(k0 + i, ke - 1);   // past the end: loaded again, not used
-        rw[i] = __ldg(a.sw + static_cast<int64_t>(tile) * a.sw_n + static_cast<int64_t>(k) * a.sw_k);
+        rw[i] = __ldg(a.sw + static_cast<int64_t>(tile) * a.sw_n +
+                      static_cast<int64_t>(k) * a.sw_k);
 #pragma unroll
         for (int j = 0; j < PT; ++j) {
           const int t = lane + 32 * j;
@@ -209,7 +210,8 @@ __global__ void __launch_bounds__(Few<NT>::THREADS, NT <= 64 ? 2 : 1)
       if (!ok) break;
 #pragma unroll 1
       for (int k = 0; k < kn; ++k) {
-        ok = __all_sync(0xffffffffu, wait_bounded_inline(bar_tfull(buf), bph, wc, kSiteEpiTmemFull));
+        ok = __all_sync(0xffffffffu,
+                        wait_bounded_inline(bar_tfull(buf), bph, wc, kSiteEpiTmemFull));
         if (!ok) break;
         tc_fence_after_sync();
 #pragma unroll
@@ -250,7 +252,8 @@ __global__ void __launch_bounds__(Few<NT>::THREADS, NT <= 64 ? 2 : 1)
 #pragma unroll
         for (int i = 0; i < T::NC; ++i) {
           const int t = h * T::NC + i;
-          if (t < a.m) store_out(a, static_cast<int64_t>(t) * a.n + o, i & 1 ? acc[i / 2].y : acc[i / 2].x);
+          if (t < a.m)
+            store_out(a, static_cast<int64_t>(t) * a.n + o, i & 1 ? acc[i / 2].y : acc[i / 2].x);
         }
       }
     }
@@ -264,11 +267,12 @@ __global__ void __launch_bounds__(Few<NT>::THREADS, NT <= 64 ? 2 : 1)
     if (warp >= 4) {
       const int h = (warp - 4) >> 2, o = (warp & 3) * 32 + lane;
       // [rank of the sender][token][output of the slice]
-      const uint32_t dst =
-          mapa_shared(base + T::OFF_PART, o / slice) + 4u * ((rank * NT + h * T::NC) * slice + o % slice);
+      const uint32_t dst = mapa_shared(base + T::OFF_PART, o / slice) +
+                           4u * ((rank * NT + h * T::NC) * slice + o % slice);
 #pragma unroll
       for (int i = 0; i < T::NC; ++i)
-        if (h * T::NC + i < a.m) st_cluster_f32(dst + 4u * i * slice, i & 1 ? acc[i / 2].y : acc[i / 2].x);
+        if (h * T::NC + i < a.m)
+          st_cluster_f32(dst + 4u * i * slice, i & 1 ? acc[i / 2].y : acc[i / 2].x);
     }
     cluster_sync_all();
     if (!*abort_flag) {

@@ -65,7 +65,8 @@ __device__ __forceinline__ void load8(const void* p, bool bf16, int64_t i8, floa
   }
 }
 
-__global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_constant__ GradNormArgs a) {
+__global__ void __launch_bounds__(kThreads)
+    grad_norm_kernel(const __grid_constant__ GradNormArgs a) {
   double sum = 0.0;
   const int units = a.unit0[a.n];
   for (int u = blockIdx.x; u < units; u += gridDim.x) {
@@ -118,7 +119,7 @@ __global__ void __launch_bounds__(kThreads) grad_norm_final_kernel(const double*
     const double norm = sqrt(s);
     const double c = static_cast<double>(max_norm) / (norm + 1e-6);
     out[0] = static_cast<float>(norm);
-    out[1] = c < 1.0 ? static_cast<float>(c) : (c >= 1.0 ? 1.0f : static_cast<float>(c));   // NaN stays
+    out[1] = c >= 1.0 ? 1.0f : static_cast<float>(c);   // NaN stays NaN
   }
 }
 

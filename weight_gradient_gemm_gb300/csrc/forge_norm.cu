@@ -98,7 +98,8 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) rmsnorm_kernel(const NormAr
   __shared__ float red[2][32];
   const int nvec = a.cols / 8;
   const int width = WARP ? 32 : blockDim.x, me = WARP ? threadIdx.x & 31 : threadIdx.x;
-  const int64_t first = WARP ? static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5) : blockIdx.x;
+  const int64_t first =
+      WARP ? static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5) : blockIdx.x;
   const int64_t step = WARP ? static_cast<int64_t>(gridDim.x) * 8 : gridDim.x;
   int parity = 0;
   for (int64_t row = first; row < a.rows; row += step, parity ^= 1) {
@@ -198,8 +199,9 @@ __device__ __forceinline__ RowRing<S> make_ring(uint8_t* smem, int depth, uint32
   r.depth = depth;
   r.rows = rows;
   r.bars = r.smem + depth * S * row_bytes;
-  r.wc = WaitCtx{reinterpret_cast<volatile uint32_t*>(smem + depth * S * row_bytes + 8 * depth), w.err,
-                 w.err_site, w.timeout_ns};
+  volatile uint32_t* abort_flag =
+      reinterpret_cast<volatile uint32_t*>(smem + depth * S * row_bytes + 8 * depth);
+  r.wc = WaitCtx{abort_flag, w.err, w.err_site, w.timeout_ns};
   return r;
 }
 
@@ -228,7 +230,8 @@ __global__ void __launch_bounds__(1024, 1) rmsnorm_stream_kernel(const NormArgs 
       const int v = threadIdx.x + i * blockDim.x;
       if (v < nvec) {
         const uint4 x = lds16(ring.at(ring.slot, 0) + 16 * v);
-        const uint4 r = RES ? lds16(ring.at(ring.slot, RES ? 1 : 0) + 16 * v) : make_uint4(0, 0, 0, 0);
+        uint4 r = make_uint4(0, 0, 0, 0);
+        if constexpr (RES) r = lds16(ring.at(ring.slot, 1) + 16 * v);
         ss += norm_h(a, x, r, row * nvec + v, h[i]);
       }
     }
@@ -302,7 +305,8 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) rmsnorm_bwd_kernel(const No
   __shared__ float4 parts[WARP ? 8 * 64 * VPT : 1];   // [warp][vector][2]
   const int nvec = a.cols / 8;
   const int width = WARP ? 32 : blockDim.x, me = WARP ? threadIdx.x & 31 : threadIdx.x;
-  const int64_t first = WARP ? static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5) : blockIdx.x;
+  const int64_t first =
+      WARP ? static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5) : blockIdx.x;
   const int64_t step = WARP ? static_cast<int64_t>(gridDim.x) * 8 : gridDim.x;
   int parity = 0;
   float dg[VPT][8];
@@ -369,12 +373,14 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) rmsnorm_bwd_kernel(const No
 }
 
 template <int VPT, bool DSUM>
-__global__ void __launch_bounds__(1024, 1) rmsnorm_bwd_stream_kernel(const NormBwdArgs a, int depth) {
+__global__ void __launch_bounds__(1024, 1)
+    rmsnorm_bwd_stream_kernel(const NormBwdArgs a, int depth) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   __shared__ float red[2][32];
   constexpr int S = DSUM ? 3 : 2;
   const int nvec = a.cols / 8;
-  RowRing<S> ring = make_ring<S>(smem_raw, depth, static_cast<uint32_t>(a.cols) * 2, a.rows, a.wait);
+  RowRing<S> ring =
+      make_ring<S>(smem_raw, depth, static_cast<uint32_t>(a.cols) * 2, a.rows, a.wait);
   ring.src[0] = reinterpret_cast<const uint8_t*>(a.h);
   ring.src[1] = reinterpret_cast<const uint8_t*>(a.dy);
   if constexpr (DSUM) ring.src[2] = reinterpret_cast<const uint8_t*>(a.dsum);
@@ -467,7 +473,8 @@ __global__ void __launch_bounds__(256) quantize_blocks_kernel(const uint4* __res
                                                               int64_t blocks) {
   const int lane = threadIdx.x & 31, sub = lane & 7;
   const int64_t b0 =
-      (static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5)) * (4 * kQuantUnroll) + (lane >> 3);
+      (static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5)) * (4 * kQuantUnroll) +
+      (lane >> 3);
   uint4 v[kQuantUnroll][2];
 #pragma unroll
   for (int j = 0; j < kQuantUnroll; ++j) {
@@ -674,9 +681,11 @@ cudaError_t launch_rmsnorm_bwd(const NormBwdArgs& a, int num_sms, cudaStream_t s
   cudaError_t e = cudaSuccess;
   if (p.walk == kWalkStream) {
     if (p.vpt == 1)
-      e = a.dsum ? launch_bwd_stream<1, true>(p, a, stream) : launch_bwd_stream<1, false>(p, a, stream);
+      e = a.dsum ? launch_bwd_stream<1, true>(p, a, stream)
+                 : launch_bwd_stream<1, false>(p, a, stream);
     else
-      e = a.dsum ? launch_bwd_stream<2, true>(p, a, stream) : launch_bwd_stream<2, false>(p, a, stream);
+      e = a.dsum ? launch_bwd_stream<2, true>(p, a, stream)
+                 : launch_bwd_stream<2, false>(p, a, stream);
   } else {
     const bool warp = p.walk == kWalkWarp;
     if (warp) {
@@ -712,7 +721,8 @@ cudaError_t launch_quantize_b128(const uint16_t* x, uint8_t* codes, float* scale
     const int64_t blocks = rows * nblk;
     const int64_t grid = (blocks + 32 * kQuantUnroll - 1) / (32 * kQuantUnroll);
     if (cols % kBlock == 0 && grid <= INT32_MAX) {
-      quantize_blocks_kernel<<<static_cast<unsigned>(grid), 256, 0, stream>>>(xv, cv, scales, blocks);
+      quantize_blocks_kernel<<<static_cast<unsigned>(grid), 256, 0, stream>>>(xv, cv, scales,
+                                                                              blocks);
     } else {
       const int64_t want = (blocks + 31) / 32, most = static_cast<int64_t>(num_sms) * 8;
       quantize_rows_kernel<<<static_cast<unsigned>(want < most ? want : most), 256, 0, stream>>>(

@@ -71,22 +71,43 @@ __device__ __forceinline__ float norm_rstd(const NormArgs& a, float ss) {
 }
 // One vector's outputs.  Every lane of the warp takes part (the shuffles);
 // `in` is false past the row's end.
-__device__ __forceinline__ void norm_out(const NormArgs& a, float (&h)[8], const float (&g)[8],
-                                         float rstd, int64_t row, int v, bool in) {
+__device__ __forceinline__ void norm_out(const NormArgs& a, const float (&h)[8],
+                                         const float (&g)[8], float rstd, int64_t row, int v, bool in) {
   const int64_t at = row * (a.cols / 8) + v;
-  float amax = 0.0f;
-  if (in) {
+  if (a.y && in) {
+    float y[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      h[k] = h[k] * rstd * g[k];
-      amax = max_nan(amax, fabsf(h[k]));
-    }
-    if (a.y) __stcs(reinterpret_cast<uint4*>(a.y) + at, pack8(h));
+    for (int k = 0; k < 8; ++k) y[k] = h[k] * rstd * g[k];
+    __stcs(reinterpret_cast<uint4*>(a.y) + at, pack8(y));
   }
   if (a.codes) {
-    const BlockScale s = block_scale(max16(amax));
+    // rstd is common to the row, so the codes are those of h gain, with one
+    // rounding less than y's; only the scale carries it.  Outside a range that
+    // no model's activations leave, y itself is encoded.
+    float t[8], amax = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      t[k] = in ? h[k] * g[k] : 0.0f;
+      amax = max_nan(amax, fabsf(t[k]));
+    }
+    amax = max16(amax);
+    const float top = amax * rstd;
+    BlockScale s{0.0f, 0.0f};
+    const bool usual = amax >= 0x1p-100f && amax <= 0x1p100f && top >= 0x1p-100f && top <= 0x1p100f;
+    if (__all_sync(0xffffffffu, usual)) {
+      s.scale = __fdiv_rn(top, kE4m3Max);
+      s.inv = __fdiv_rn(kE4m3Max, amax);
+    } else {
+      amax = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        t[k] = in ? h[k] * rstd * g[k] : 0.0f;
+        amax = max_nan(amax, fabsf(t[k]));
+      }
+      s = block_scale(max16(amax));
+    }
     if (in) {
-      __stcs(reinterpret_cast<uint2*>(a.codes) + at, encode8(h, s.inv));
+      __stcs(reinterpret_cast<uint2*>(a.codes) + at, encode8(t, s.inv));
       if (v % 16 == 0) a.scales[row * ((a.cols + kBlock - 1) / kBlock) + v / 16] = s.scale;
     }
   }

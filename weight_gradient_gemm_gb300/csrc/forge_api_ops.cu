@@ -61,18 +61,16 @@ forge_status check_rows(int64_t rows, int64_t cols, int64_t max_cols) {
 // Up to 128 tokens the outputs lie along M (forge_gemm_b128_few.cu) and the
 // reduction is split over as many CTAs of a cluster as leave at most one CTA
 // an SM, with two blocks each at least: one token, 4096 -> 4096 (32 tiles),
-// takes 11.3 us unsplit, 8.8 on two CTAs, 7.5 on four and 8.6 on eight.  The
-// input gradient's tile holds 32 tokens at least: with 16, where the weight
-// lies MN-major along M, a block took 440 ns against 310.
+// takes 11.0 us unsplit, 8.8 on two CTAs, 7.4 on four and 7.6 on eight.
 // Beyond, 256 x 256 on CTA pairs or 128 x 128 on single CTAs, by the waves
 // each takes and the measured cycles of a block (770 and 490): 512 tokens,
 // 4096 -> 4096, take 20.5 us on pairs and 16.5 on single CTAs, 1024 tokens
 // 20.7 and 25.0.
-B128Config choose_b128(int64_t m, int64_t n, int64_t num_kb, bool dgrad, const forge_tuning& tune,
+B128Config choose_b128(int64_t m, int64_t n, int64_t num_kb, const forge_tuning& tune,
                        int num_sms) {
   B128Config c{1, 128, 0, 1};
   if (m <= 128 && tune.cta_group == 0) {
-    c.few = m <= (dgrad ? 0 : 16) ? 16 : (m <= 32 ? 32 : (m <= 64 ? 64 : 128));
+    c.few = m <= 16 ? 16 : (m <= 32 ? 32 : (m <= 64 ? 64 : 128));
     const int64_t tiles = (n + 127) / 128;
     while (c.splits < 8 && tiles * c.splits * 2 <= num_sms && num_kb >= 4 * c.splits) c.splits *= 2;
     if (tune.splits)   // the cluster sizes there are: powers of two
@@ -111,7 +109,7 @@ forge_status product_b128(const void* A, const float* sa, const void* W, const f
   forge_tuning tune;
   forge_get_tuning(&tune);
   const B128Config cfg =
-      choose_b128(m, n, static_cast<int64_t>(blocks128(k)), dgrad, tune, d.num_sms);
+      choose_b128(m, n, static_cast<int64_t>(blocks128(k)), tune, d.num_sms);
   B128Args a;
   std::memset(&a, 0, sizeof(a));
   const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;

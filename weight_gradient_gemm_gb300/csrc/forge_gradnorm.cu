@@ -38,6 +38,7 @@ __device__ __forceinline__ double squares(const float (&g)[N]) {
   return d;
 }
 
+// The sum over the block, in every thread and in a fixed order.
 __device__ __forceinline__ double block_sum(double v) {
   __shared__ double red[kThreads / 32];
 #pragma unroll
@@ -65,8 +66,8 @@ __device__ __forceinline__ void load8(const void* p, bool bf16, int64_t i8, floa
   }
 }
 
-__global__ void __launch_bounds__(kThreads)
-    grad_norm_kernel(const __grid_constant__ GradNormArgs a) {
+// One block's share of the units, as a sum of squares (in every thread).
+__device__ __forceinline__ double units_sum(const GradNormArgs& a) {
   double sum = 0.0;
   const int units = a.unit0[a.n];
   for (int u = blockIdx.x; u < units; u += gridDim.x) {
@@ -104,7 +105,20 @@ __global__ void __launch_bounds__(kThreads)
       sum += squares(g);
     }
   }
-  sum = block_sum(sum);
+  return block_sum(sum);
+}
+
+// norm = sqrt(s) and the coefficient, from the sum of squares.
+__device__ __forceinline__ void write_norm(double s, float max_norm, float* out) {
+  const double norm = sqrt(s);
+  const double c = static_cast<double>(max_norm) / (norm + 1e-6);
+  out[0] = static_cast<float>(norm);
+  out[1] = c >= 1.0 ? 1.0f : static_cast<float>(c);   // NaN stays NaN
+}
+
+__global__ void __launch_bounds__(kThreads)
+    grad_norm_kernel(const __grid_constant__ GradNormArgs a) {
+  const double sum = units_sum(a);
   if (threadIdx.x == 0) a.part[blockIdx.x] = sum;
 }
 
@@ -115,12 +129,7 @@ __global__ void __launch_bounds__(kThreads) grad_norm_final_kernel(const double*
   double s = 0.0;
   for (int i = threadIdx.x; i < n; i += kThreads) s += part[i];
   s = block_sum(s);
-  if (threadIdx.x == 0) {
-    const double norm = sqrt(s);
-    const double c = static_cast<double>(max_norm) / (norm + 1e-6);
-    out[0] = static_cast<float>(norm);
-    out[1] = c >= 1.0 ? 1.0f : static_cast<float>(c);   // NaN stays NaN
-  }
+  if (threadIdx.x == 0) write_norm(s, max_norm, out);
 }
 
 }  // namespace

@@ -249,7 +249,7 @@ cudaError_t launch_quantize_b128(const uint16_t* x, uint8_t* codes, float* scale
                                  int64_t cols, int block_rows, int num_sms, cudaStream_t stream);
 
 // The global gradient norm (forge_gradnorm.cu).
-constexpr int kNormTensors = 256;   // tensors one launch takes
+constexpr int kNormTensors = 128;   // tensors one launch takes
 struct GradNormArgs {
   const void* ptr[kNormTensors];
   int64_t numel[kNormTensors];

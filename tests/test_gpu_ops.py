@@ -455,3 +455,59 @@ def test_operators_in_a_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(Y, want)
+
+
+def test_repeated_launches_agree():
+    # many launches back to back with cold and warm operands: every tile form
+    # of the products gives the same bits each time
+    for bt, d_in, d_out in ((1, 4096, 2048), (20, 2048, 4096), (100, 4096, 1024), (300, 4096, 1024),
+                            (1500, 2048, 2048)):
+        X, xs = random_codes(70, bt, d_in, 1)
+        W, ws = random_codes(71, d_out, d_in, 128)
+        Y = [torch.empty((bt, d_out), dtype=torch.bfloat16, device=DEV) for _ in range(40)]
+        flush = torch.empty(64 << 20, dtype=torch.float32, device=DEV)
+        for i, y in enumerate(Y):
+            if i % 8 == 0:
+                flush.fill_(float(i))
+            F.linear_fp8(X, xs, W, ws, y)
+        ok()
+        assert all(torch.equal(Y[0], y) for y in Y[1:]), (bt, d_in, d_out)
+
+
+def test_offsets_past_32_bits():
+    # more than 2^31 elements: the last rows are where a narrow offset would show
+    rows, cols = 540000, 4096
+    x = torch.zeros((rows, cols), dtype=torch.bfloat16, device=DEV)
+    tail = rand(80, (200, cols))
+    x[-200:] = tail
+    codes, scales = F.alloc_b128(rows, cols)
+    F.quantize_b128(x, codes, scales)
+    ok()
+    c2, s2 = F.alloc_b128(200, cols)
+    F.quantize_b128(tail, c2, s2)
+    assert torch.equal(codes[-200:].view(torch.uint8), c2.view(torch.uint8))
+    assert torch.equal(scales[-200:], s2) and float(scales[0].max()) == 0.0
+    gain = torch.ones(cols, device=DEV)
+    y, y2 = torch.empty_like(x), torch.empty_like(tail)
+    F.rmsnorm(x, gain, eps=1e-5, y=y)
+    F.rmsnorm(tail, gain, eps=1e-5, y=y2)
+    ok()
+    assert torch.equal(y[-200:], y2)
+    del x
+    # the product's output offsets, and the gradient norm's
+    W, ws = random_codes(81, cols, 128, 128)
+    X, xs = random_codes(82, rows, 128, 1)
+    F.linear_fp8(X, xs, W, ws, y)
+    F.linear_fp8(X[-200:].clone(), xs[-200:].clone(), W, ws, y2)
+    ok()
+    assert torch.equal(y[-200:], y2)
+    y.zero_()
+    y[-1, -1] = 3.0
+    assert f64(run_norm([y], 6.0)).tolist() == [3.0, 1.0]
+
+
+def test_example_trains():
+    from examples import fp8_layer
+    losses, norms = fp8_layer.train(steps=30, bt=256, d_in=384, d_out=640)
+    assert losses[-1] < 0.2 * losses[0], losses
+    assert all(np.isfinite(norms))

@@ -22,6 +22,7 @@
 #include <cuda_bf16.h>
 
 #include "forge_internal.h"
+#include "forge_launch.cuh"
 #include "forge_ptx.cuh"
 #include "forge_wait.cuh"
 
@@ -150,6 +151,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
+  grid_dependency_wait();
   const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(gbase + T::OFF_TMEM);
 
   if (warp < 4) {
@@ -305,7 +307,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
             const float* p = a.sa + static_cast<int64_t>(row < a.m ? row : 0) * a.num_kb + k0;
 #pragma unroll
             for (int i = 0; i < T::SC_BATCH; ++i)
-              ra[j][i] = row < a.m && k0 + i < a.num_kb ? __ldg(p + i) : 0.0f;
+              ra[j][i] = row < a.m && k0 + i < a.num_kb ? p[i] : 0.0f;
           }
           const int b = cnt & 1;
           const bool good =
@@ -316,9 +318,9 @@ __global__ void __launch_bounds__(kThreads8, 1)
 #pragma unroll
             for (int w = 0; w < T::NWB; ++w) {
               const bool in = k0 + i < a.num_kb && (wb0 + w) * 128 < a.n;
-              const float rw = in ? __ldg(a.sw + static_cast<int64_t>(wb0 + w) * a.sw_n +
-                                          static_cast<int64_t>(k0 + i) * a.sw_k)
-                                  : 0.0f;
+              const float rw = in ? a.sw[static_cast<int64_t>(wb0 + w) * a.sw_n +
+                                       static_cast<int64_t>(k0 + i) * a.sw_k]
+                                : 0.0f;
               float* dst = scales + ((b * T::SC_BATCH + i) * T::NWB + w) * kBM + lane;
 #pragma unroll
               for (int j = 0; j < 4; ++j) dst[32 * j] = in ? ra[j][i] * rw : 0.0f;
@@ -450,6 +452,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
   }
 
   // ---------------------------------------------------------------- teardown
+  grid_dependency_trigger();
   tc_fence_before_sync();
   if constexpr (kPair) {
     if (*abort_flag) {   // let copies in flight into this CTA land (see forge_gemm.cuh)
@@ -482,23 +485,22 @@ cudaError_t launch_t(const B128Args& a, int num_sms, cudaStream_t stream) {
                                          T::SMEM_ALLOC);
     if (e != cudaSuccess) return e;
   }
-  cudaLaunchConfig_t lc = {};
-  lc.blockDim = dim3(kThreads8, 1, 1);
-  lc.dynamicSmemBytes = T::SMEM_ALLOC;
-  lc.stream = stream;
-  cudaLaunchAttribute attr[1];
   int units = num_sms;
-  if constexpr (CG == 2) {
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    lc.attrs = attr;
-    lc.numAttrs = 1;
+  if constexpr (CG == 2) {   // as many pairs as can be resident
     units = cached ? max_units[dev] : 0;
     if (!cached) {
+      cudaLaunchConfig_t lc = {};
       lc.gridDim = dim3(2 * (num_sms / 2), 1, 1);
-      cudaError_t e = cudaOccupancyMaxActiveClusters(&units, kern, &lc);
+      lc.blockDim = dim3(kThreads8, 1, 1);
+      lc.dynamicSmemBytes = T::SMEM_ALLOC;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = 2;
+      attr[0].val.clusterDim.y = 1;
+      attr[0].val.clusterDim.z = 1;
+      lc.attrs = attr;
+      lc.numAttrs = 1;
+      const cudaError_t e = cudaOccupancyMaxActiveClusters(&units, kern, &lc);
       if (e != cudaSuccess) return e;
       if (units <= 0) return cudaErrorInvalidConfiguration;
       if (dev >= 0 && dev < 64) max_units[dev] = units;
@@ -506,8 +508,8 @@ cudaError_t launch_t(const B128Args& a, int num_sms, cudaStream_t stream) {
     units = units < num_sms / 2 ? units : num_sms / 2;
   }
   if (!cached && dev >= 0 && dev < 64) ready[dev] = 1;
-  lc.gridDim = dim3(CG * (a.num_tiles < units ? a.num_tiles : units), 1, 1);
-  return cudaLaunchKernelEx(&lc, kern, a);
+  return launch_chained(kern, CG * (a.num_tiles < units ? a.num_tiles : units), kThreads8,
+                        T::SMEM_ALLOC, CG == 2 ? 2 : 0, stream, a);
 }
 
 template <int CG, int BN>

@@ -18,6 +18,7 @@
 #include <cuda_bf16.h>
 
 #include "forge_internal.h"
+#include "forge_launch.cuh"
 #include "forge_ptx.cuh"
 #include "forge_wait.cuh"
 
@@ -118,6 +119,7 @@ __global__ void __launch_bounds__(Few<NT>::THREADS, NT <= 64 ? 2 : 1)
   __syncthreads();
   if (splits > 1) cluster_arrive();   // waited for before the first remote store
   tc_fence_after_sync();
+  grid_dependency_wait();
   const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(gbase + T::OFF_TMEM);
 
   float2 acc[T::NC / 2];   // epilogue threads: one output, NC tokens
@@ -175,12 +177,11 @@ __global__ void __launch_bounds__(Few<NT>::THREADS, NT <= 64 ? 2 : 1)
 #pragma unroll
       for (int i = 0; i < T::SC_BATCH; ++i) {
         const int k = min(k0 + i, ke - 1);   // past the end: loaded again, not used
-        rw[i] = __ldg(a.sw + static_cast<int64_t>(tile) * a.sw_n +
-                      static_cast<int64_t>(k) * a.sw_k);
+        rw[i] = a.sw[static_cast<int64_t>(tile) * a.sw_n + static_cast<int64_t>(k) * a.sw_k];
 #pragma unroll
         for (int j = 0; j < PT; ++j) {
           const int t = lane + 32 * j;
-          rx[j][i] = __ldg(a.sa + static_cast<int64_t>(min(t, a.m - 1)) * a.num_kb + k);
+          rx[j][i] = a.sa[static_cast<int64_t>(min(t, a.m - 1)) * a.num_kb + k];
         }
       }
       const bool good = wait_bounded(bar_sempty(b), ph, wc, kSiteLoaderEmpty);
@@ -243,6 +244,7 @@ __global__ void __launch_bounds__(Few<NT>::THREADS, NT <= 64 ? 2 : 1)
   }
 
   // ------------------------------------------------------------ join and store
+  grid_dependency_trigger();
   tc_fence_before_sync();
   if (splits == 1) {
     __syncthreads();
@@ -306,20 +308,9 @@ cudaError_t launch_t(B128Args a, int num_sms, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) ready[dev] = 1;
   }
-  cudaLaunchConfig_t lc = {};
-  lc.blockDim = dim3(T::THREADS, 1, 1);
-  lc.gridDim = dim3(a.num_tiles * a.splits, 1, 1);
   a.stages = a.num_tiles * a.splits <= num_sms ? T::DEEP : T::STAGES;
-  lc.dynamicSmemBytes = T::smem(a.stages);
-  lc.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = a.splits;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  lc.attrs = attr;
-  lc.numAttrs = a.splits > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&lc, kern, a);
+  return launch_chained(kern, a.num_tiles * a.splits, T::THREADS, T::smem(a.stages),
+                        a.splits > 1 ? a.splits : 0, stream, a);
 }
 
 template <int NT>

@@ -7,7 +7,7 @@
 // each block leaves one partial sum, and a second launch adds the partials in
 // a fixed order, so the norm is the same on every run.
 #include "forge_internal.h"
-#include "forge_ptx.cuh"
+#include "forge_launch.cuh"
 
 namespace forge {
 namespace {
@@ -54,13 +54,13 @@ __device__ __forceinline__ double block_sum(double v) {
 // Values 8 i8 .. 8 i8 + 7 of a tensor.
 __device__ __forceinline__ void load8(const void* p, bool bf16, int64_t i8, float* g) {
   if (bf16) {
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i8);
+    const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p) + i8);
     const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) { g[2 * k] = bf16_lo(u[k]); g[2 * k + 1] = bf16_hi(u[k]); }
   } else {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p) + 2 * i8);
-    const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 2 * i8 + 1);
+    const float4 a = __ldcs(reinterpret_cast<const float4*>(p) + 2 * i8);
+    const float4 b = __ldcs(reinterpret_cast<const float4*>(p) + 2 * i8 + 1);
     g[0] = a.x; g[1] = a.y; g[2] = a.z; g[3] = a.w;
     g[4] = b.x; g[5] = b.y; g[6] = b.z; g[7] = b.w;
   }
@@ -118,16 +118,18 @@ __device__ __forceinline__ void write_norm(double s, float max_norm, float* out)
 
 __global__ void __launch_bounds__(kThreads)
     grad_norm_kernel(const __grid_constant__ GradNormArgs a) {
+  grid_dependency_wait();
   const double sum = units_sum(a);
+  grid_dependency_trigger();
   if (threadIdx.x == 0) a.part[blockIdx.x] = sum;
 }
 
 __global__ void __launch_bounds__(kThreads) grad_norm_final_kernel(const double* __restrict__ part,
                                                                    int n, float max_norm,
                                                                    float* __restrict__ out) {
-  grid_dependency_wait();   // launched ahead of grad_norm_kernel's end
+  grid_dependency_wait();
   double s = 0.0;
-  for (int i = threadIdx.x; i < n; i += kThreads) s += part[i];
+  for (int i = threadIdx.x; i < n; i += kThreads) s += __ldcg(part + i);
   s = block_sum(s);
   if (threadIdx.x == 0) write_norm(s, max_norm, out);
 }
@@ -140,22 +142,12 @@ int grad_norm_blocks(int64_t units, int num_sms) {
 }
 
 cudaError_t launch_grad_norm(const GradNormArgs& a, int blocks, cudaStream_t stream) {
-  grad_norm_kernel<<<blocks, kThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_chained(grad_norm_kernel, blocks, kThreads, 0, 0, stream, a);
 }
 
 cudaError_t launch_grad_norm_final(const double* part, int n, float max_norm, float* out,
                                    cudaStream_t stream) {
-  cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3(1, 1, 1);
-  lc.blockDim = dim3(kThreads, 1, 1);
-  lc.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  lc.attrs = attr;
-  lc.numAttrs = 1;
-  return cudaLaunchKernelEx(&lc, grad_norm_final_kernel, part, n, max_norm, out);
+  return launch_chained(grad_norm_final_kernel, 1, kThreads, 0, 0, stream, part, n, max_norm, out);
 }
 
 }  // namespace forge

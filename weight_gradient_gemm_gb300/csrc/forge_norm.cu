@@ -6,6 +6,7 @@
 
 #include "forge_e4m3.cuh"
 #include "forge_internal.h"
+#include "forge_launch.cuh"
 #include "forge_ptx.cuh"
 #include "forge_wait.cuh"
 
@@ -30,10 +31,10 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
 
 __device__ __forceinline__ void load_gain8(const void* gain, int bf16, int v, float (&g)[8]) {
   if (bf16) {
-    unpack8(__ldg(reinterpret_cast<const uint4*>(gain) + v), g);
+    unpack8(reinterpret_cast<const uint4*>(gain)[v], g);
   } else {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(gain) + 2 * v);
-    const float4 b = __ldg(reinterpret_cast<const float4*>(gain) + 2 * v + 1);
+    const float4 a = reinterpret_cast<const float4*>(gain)[2 * v];
+    const float4 b = reinterpret_cast<const float4*>(gain)[2 * v + 1];
     g[0] = a.x; g[1] = a.y; g[2] = a.z; g[3] = a.w;
     g[4] = b.x; g[5] = b.y; g[6] = b.z; g[7] = b.w;
   }
@@ -123,6 +124,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) rmsnorm_kernel(const NormAr
       WARP ? static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5) : blockIdx.x;
   const int64_t step = WARP ? static_cast<int64_t>(gridDim.x) * 8 : gridDim.x;
   int parity = 0;
+  grid_dependency_wait();
   for (int64_t row = first; row < a.rows; row += step, parity ^= 1) {
     const int64_t base = row * nvec;
     uint4 x[VPT], r[VPT];
@@ -235,6 +237,7 @@ __global__ void __launch_bounds__(1024, 1) rmsnorm_stream_kernel(const NormArgs 
       make_ring<RES ? 2 : 1>(smem_raw, depth, static_cast<uint32_t>(a.cols) * 2, a.rows, a.wait);
   ring.src[0] = reinterpret_cast<const uint8_t*>(a.x);
   if constexpr (RES) ring.src[1] = reinterpret_cast<const uint8_t*>(a.residual);
+  grid_dependency_wait();
   if (threadIdx.x == 0) {
     *ring.wc.abort_flag = 0u;
     ring.start();
@@ -267,6 +270,7 @@ __global__ void __launch_bounds__(1024, 1) rmsnorm_stream_kernel(const NormArgs 
       norm_out(a, h[i], g, rstd, row, v, v < nvec);
     }
   }
+  grid_dependency_trigger();
   ring.finish();
 }
 
@@ -335,9 +339,10 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) rmsnorm_bwd_kernel(const No
   for (int i = 0; i < VPT; ++i)
 #pragma unroll
     for (int k = 0; k < 8; ++k) dg[i][k] = 0.0f;
+  grid_dependency_wait();
   for (int64_t row = first; row < a.rows; row += step, parity ^= 1) {
     const int64_t base = row * nvec;
-    const float rstd = __ldg(a.rstd + row);
+    const float rstd = __ldcg(a.rstd + row);
     uint4 hv[VPT], dv[VPT], sv[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
@@ -370,6 +375,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) rmsnorm_bwd_kernel(const No
       }
     }
   }
+  grid_dependency_trigger();
   if (!a.dgain) return;
   if constexpr (WARP) {   // the block's warps join in a fixed order
     const int warp = threadIdx.x >> 5;
@@ -405,6 +411,7 @@ __global__ void __launch_bounds__(1024, 1)
   ring.src[0] = reinterpret_cast<const uint8_t*>(a.h);
   ring.src[1] = reinterpret_cast<const uint8_t*>(a.dy);
   if constexpr (DSUM) ring.src[2] = reinterpret_cast<const uint8_t*>(a.dsum);
+  grid_dependency_wait();
   if (threadIdx.x == 0) {
     *ring.wc.abort_flag = 0u;
     ring.start();
@@ -417,9 +424,9 @@ __global__ void __launch_bounds__(1024, 1)
     for (int k = 0; k < 8; ++k) dg[i][k] = 0.0f;
   __syncthreads();
   int parity = 0;
-  float rstd = __ldg(a.rstd + blockIdx.x);
+  float rstd = __ldcg(a.rstd + blockIdx.x);
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, parity ^= 1) {
-    const float rstd_next = row + gridDim.x < a.rows ? __ldg(a.rstd + row + gridDim.x) : 0.0f;
+    const float rstd_next = row + gridDim.x < a.rows ? __ldcg(a.rstd + row + gridDim.x) : 0.0f;
     ring.wait();
     uint4 hv[VPT], dv[VPT], sv[VPT];
     float dot = 0.0f;
@@ -447,13 +454,13 @@ __global__ void __launch_bounds__(1024, 1)
     }
     rstd = rstd_next;
   }
+  grid_dependency_trigger();
   if (a.dgain) write_part<VPT>(a, dg, threadIdx.x, blockDim.x);
   ring.finish();
 }
 
 // dgain[c] = sum over the blocks' partial rows: 32 columns a block, 32 runs of
-// rows side by side, added in a fixed order.  Launched ahead of the main
-// kernel's end (programmatic launch), it waits for it here.
+// rows side by side, added in a fixed order.
 __global__ void __launch_bounds__(1024) rmsnorm_dgain_kernel(const float* __restrict__ part,
                                                              int blocks, int cols,
                                                              float* __restrict__ dgain) {
@@ -497,6 +504,7 @@ __global__ void __launch_bounds__(256) quantize_blocks_kernel(const uint4* __res
       (static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5)) * (4 * kQuantUnroll) +
       (lane >> 3);
   uint4 v[kQuantUnroll][2];
+  grid_dependency_wait();
 #pragma unroll
   for (int j = 0; j < kQuantUnroll; ++j) {
     const int64_t b = b0 + 4 * j;
@@ -528,6 +536,7 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const uint4* __restr
                                                             int64_t rows, int nvec) {
   const int nblk = (nvec + 15) / 16, sub = threadIdx.x & 7;
   const int64_t total = rows * nblk, groups = static_cast<int64_t>(gridDim.x) * 32;
+  grid_dependency_wait();
   // every lane of a warp takes the same number of trips (the shuffles)
   for (int64_t b0 = static_cast<int64_t>(blockIdx.x) * 32 + ((threadIdx.x >> 5) << 2); b0 < total;
        b0 += groups) {
@@ -564,6 +573,7 @@ __global__ void __launch_bounds__(256) quantize_tiles_kernel(const uint16_t* __r
   const int64_t row0 = br * kBlock + (threadIdx.x >> 4);
   uint4 v[8];
   float amax = 0.0f;
+  grid_dependency_wait();
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     v[i] = make_uint4(0, 0, 0, 0);
@@ -647,8 +657,7 @@ cudaError_t launch_stream(Kern kern, int* ready, const RowPlan& p, const Args& a
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) ready[dev] = 1;
   }
-  kern<<<p.grid, p.threads, p.smem, stream>>>(a, p.depth);
-  return cudaGetLastError();
+  return launch_chained(kern, p.grid, p.threads, p.smem, 0, stream, a, p.depth);
 }
 template <int VPT, bool RES>
 cudaError_t launch_fwd_stream(const RowPlan& p, const NormArgs& a, cudaStream_t stream) {
@@ -672,22 +681,12 @@ cudaError_t launch_rmsnorm(const NormArgs& a, int num_sms, cudaStream_t stream) 
     return a.residual ? launch_fwd_stream<2, true>(p, a, stream)
                       : launch_fwd_stream<2, false>(p, a, stream);
   }
-  const bool warp = p.walk == kWalkWarp;
-  switch (p.vpt) {
-    case 1:
-      if (warp) rmsnorm_kernel<1, true><<<p.grid, p.threads, 0, stream>>>(a);
-      else rmsnorm_kernel<1, false><<<p.grid, p.threads, 0, stream>>>(a);
-      break;
-    case 2:
-      if (warp) rmsnorm_kernel<2, true><<<p.grid, p.threads, 0, stream>>>(a);
-      else rmsnorm_kernel<2, false><<<p.grid, p.threads, 0, stream>>>(a);
-      break;
-    default:
-      if (warp) rmsnorm_kernel<4, true><<<p.grid, p.threads, 0, stream>>>(a);
-      else rmsnorm_kernel<4, false><<<p.grid, p.threads, 0, stream>>>(a);
-      break;
-  }
-  return cudaGetLastError();
+  auto go = [&](auto kern) { return launch_chained(kern, p.grid, p.threads, 0, 0, stream, a); };
+  if (p.walk == kWalkWarp)
+    return p.vpt == 1 ? go(rmsnorm_kernel<1, true>)
+                      : (p.vpt == 2 ? go(rmsnorm_kernel<2, true>) : go(rmsnorm_kernel<4, true>));
+  return p.vpt == 1 ? go(rmsnorm_kernel<1, false>)
+                    : (p.vpt == 2 ? go(rmsnorm_kernel<2, false>) : go(rmsnorm_kernel<4, false>));
 }
 
 int rmsnorm_bwd_blocks(int64_t rows, int cols, int num_sms) {
@@ -708,29 +707,17 @@ cudaError_t launch_rmsnorm_bwd(const NormBwdArgs& a, int num_sms, cudaStream_t s
       e = a.dsum ? launch_bwd_stream<2, true>(p, a, stream)
                  : launch_bwd_stream<2, false>(p, a, stream);
   } else {
-    const bool warp = p.walk == kWalkWarp;
-    if (warp) {
-      if (p.vpt == 1) rmsnorm_bwd_kernel<1, true><<<p.grid, p.threads, 0, stream>>>(a);
-      else rmsnorm_bwd_kernel<2, true><<<p.grid, p.threads, 0, stream>>>(a);
-    } else {
-      if (p.vpt == 1) rmsnorm_bwd_kernel<1, false><<<p.grid, p.threads, 0, stream>>>(a);
-      else if (p.vpt == 2) rmsnorm_bwd_kernel<2, false><<<p.grid, p.threads, 0, stream>>>(a);
-      else rmsnorm_bwd_kernel<4, false><<<p.grid, p.threads, 0, stream>>>(a);
-    }
-    e = cudaGetLastError();
+    auto go = [&](auto kern) { return launch_chained(kern, p.grid, p.threads, 0, 0, stream, a); };
+    if (p.walk == kWalkWarp)
+      e = p.vpt == 1 ? go(rmsnorm_bwd_kernel<1, true>) : go(rmsnorm_bwd_kernel<2, true>);
+    else
+      e = p.vpt == 1 ? go(rmsnorm_bwd_kernel<1, false>)
+                     : (p.vpt == 2 ? go(rmsnorm_bwd_kernel<2, false>)
+                                   : go(rmsnorm_bwd_kernel<4, false>));
   }
   if (e != cudaSuccess || !a.dgain) return e;
-  cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3((a.cols + 31) / 32, 1, 1);
-  lc.blockDim = dim3(1024, 1, 1);
-  lc.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  lc.attrs = attr;
-  lc.numAttrs = 1;
-  return cudaLaunchKernelEx(&lc, rmsnorm_dgain_kernel, static_cast<const float*>(a.part), p.grid,
-                            a.cols, a.dgain);
+  return launch_chained(rmsnorm_dgain_kernel, (a.cols + 31) / 32, 1024, 0, 0, stream,
+                        static_cast<const float*>(a.part), p.grid, a.cols, a.dgain);
 }
 
 cudaError_t launch_quantize_b128(const uint16_t* x, uint8_t* codes, float* scales, int64_t rows,
@@ -741,20 +728,16 @@ cudaError_t launch_quantize_b128(const uint16_t* x, uint8_t* codes, float* scale
     uint2* cv = reinterpret_cast<uint2*>(codes);
     const int64_t blocks = rows * nblk;
     const int64_t grid = (blocks + 32 * kQuantUnroll - 1) / (32 * kQuantUnroll);
-    if (cols % kBlock == 0 && grid <= INT32_MAX) {
-      quantize_blocks_kernel<<<static_cast<unsigned>(grid), 256, 0, stream>>>(xv, cv, scales,
-                                                                              blocks);
-    } else {
-      const int64_t want = (blocks + 31) / 32, most = static_cast<int64_t>(num_sms) * 8;
-      quantize_rows_kernel<<<static_cast<unsigned>(want < most ? want : most), 256, 0, stream>>>(
-          xv, cv, scales, rows, static_cast<int>(cols / 8));
-    }
-  } else {
-    const int64_t grid = (rows + kBlock - 1) / kBlock * nblk;
-    quantize_tiles_kernel<<<static_cast<unsigned>(grid), 256, 0, stream>>>(x, codes, scales, rows,
-                                                                          cols);
+    if (cols % kBlock == 0 && grid <= INT32_MAX)
+      return launch_chained(quantize_blocks_kernel, static_cast<unsigned>(grid), 256, 0, 0, stream,
+                            xv, cv, scales, blocks);
+    const int64_t want = (blocks + 31) / 32, most = static_cast<int64_t>(num_sms) * 8;
+    return launch_chained(quantize_rows_kernel, static_cast<unsigned>(want < most ? want : most),
+                          256, 0, 0, stream, xv, cv, scales, rows, static_cast<int>(cols / 8));
   }
-  return cudaGetLastError();
+  const int64_t grid = (rows + kBlock - 1) / kBlock * nblk;
+  return launch_chained(quantize_tiles_kernel, static_cast<unsigned>(grid), 256, 0, 0, stream, x,
+                        codes, scales, rows, cols);
 }
 
 }  // namespace forge

@@ -175,12 +175,6 @@ __device__ __forceinline__ bool named_bar_or(uint32_t id, uint32_t nthreads, boo
   return out != 0;
 }
 
-// In a kernel launched with programmatic stream serialization: waits until the
-// kernel before it in the stream has finished and its writes are visible.
-__device__ __forceinline__ void grid_dependency_wait() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
 // Registers per thread of the calling warpgroup (four whole warps): given back
 // to, or taken from, what the block was launched with.
 template <int N>

@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) rmsnorm_bwd_kernel(const No
   grid_dependency_wait();
   for (int64_t row = first; row < a.rows; row += step, parity ^= 1) {
     const int64_t base = row * nvec;
-    const float rstd = __ldcg(a.rstd + row);
+    const float rstd = a.rstd[row];
     uint4 hv[VPT], dv[VPT], sv[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
@@ -424,9 +424,9 @@ __global__ void __launch_bounds__(1024, 1)
     for (int k = 0; k < 8; ++k) dg[i][k] = 0.0f;
   __syncthreads();
   int parity = 0;
-  float rstd = __ldcg(a.rstd + blockIdx.x);
+  float rstd = a.rstd[blockIdx.x];
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, parity ^= 1) {
-    const float rstd_next = row + gridDim.x < a.rows ? __ldcg(a.rstd + row + gridDim.x) : 0.0f;
+    const float rstd_next = row + gridDim.x < a.rows ? a.rstd[row + gridDim.x] : 0.0f;
     ring.wait();
     uint4 hv[VPT], dv[VPT], sv[VPT];
     float dot = 0.0f;

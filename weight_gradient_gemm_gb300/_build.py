@@ -1,14 +1,18 @@
 """Builds libforge.so in-tree with nvcc for sm_103a (no CMake, no torch build).
 
 Each .cu file compiles to an object in parallel, then one shared library is
-linked with the CUDA runtime static.  Re-running is cheap: objects are rebuilt
+linked with the CUDA runtime static.  Beside it, the Python calls of the
+operators around the weight gradient (csrc/forge_call.cpp) compile to a CPython
+extension against the installed torch.  Re-running is cheap: objects are rebuilt
 only when a source or header is newer.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -16,6 +20,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libforge.so")
+CALL = os.path.join(PKG, "_forge_call.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O3",
          "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]
@@ -41,6 +46,26 @@ def _stale(out: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def build_call() -> str:
+    """The CPython extension (host code only, the machine's own compiler)."""
+    src = os.path.join(CSRC, "forge_call.cpp")
+    torch_dir = list(importlib.util.find_spec("torch").submodule_search_locations)[0]
+    if _stale(CALL, [src, os.path.join(ROOT, "include", "forge.h"),
+                     os.path.join(torch_dir, "version.py")]):
+        cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+        inc = [os.path.join(ROOT, "include"), os.path.join(torch_dir, "include"),
+               os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+               os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+        cmd = (["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall", src, "-o", CALL]
+               + [a for i in inc for a in ("-isystem" if i is not inc[0] else "-I", i)]
+               + ["-L" + os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
+                  "-lc10_cuda"])
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"g++ failed for forge_call.cpp:\n{r.stdout}\n{r.stderr}")
+    return CALL
+
+
 def build(verbose: bool = False, extra_flags=None) -> str:
     os.makedirs(BUILD, exist_ok=True)
     sources = sorted(f for f in os.listdir(CSRC) if f.endswith(".cu"))
@@ -61,7 +86,9 @@ def build(verbose: bool = False, extra_flags=None) -> str:
         return obj
 
     with ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
+        call = ex.submit(build_call)
         objs = list(ex.map(compile_one, sources))
+        call.result()
     if _stale(LIB, objs):
         cmd = [cc] + ARCH + ["-shared", "-cudart", "static", "-o", LIB] + objs
         r = subprocess.run(cmd, capture_output=True, text=True)

@@ -1,5 +1,8 @@
 """Python binding for libforge (ctypes).  Argument marshalling only: every
-step of the computation runs in the library's CUDA kernels.
+step of the computation runs in the library's CUDA kernels.  The operators
+around the weight gradient, whose calls on few rows take a few microseconds, go
+through a CPython extension first (csrc/forge_call.cpp), with the same checks;
+what it does not take goes through the checks here, which say what is wrong.
 
 PyTorch supplies device memory and the current CUDA stream.  There is no CPU
 fallback: if ``libforge.so`` has not been built, every call raises.
@@ -8,6 +11,7 @@ from __future__ import annotations
 
 import array
 import ctypes
+import importlib.util
 import os
 import re
 import threading
@@ -17,6 +21,7 @@ import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libforge.so")
+CALL_PATH = os.path.join(_HERE, "_forge_call.so")
 HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "forge.h")
 
 FORGE_OK = 0
@@ -193,8 +198,26 @@ def lib() -> ctypes.CDLL:
             L.forge_set_tuning.restype = None
             L.forge_get_tuning.argtypes = [ctypes.POINTER(ForgeTuning)]
             L.forge_get_tuning.restype = None
+            _load_call(L)
             _lib = L
         return _lib
+
+
+_call = None    # the CPython extension, once the library is loaded
+
+
+def _load_call(L: ctypes.CDLL) -> None:
+    global _call
+    if not os.path.exists(CALL_PATH):
+        raise RuntimeError(f"{CALL_PATH} is not built; run `python -c \"import __graft_entry__ as "
+                           f"g; g.build()\"` first")
+    spec = importlib.util.spec_from_file_location("_forge_call", CALL_PATH)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    mod.bind(*[ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in (
+        "forge_rmsnorm", "forge_rmsnorm_backward", "forge_quantize_b128", "forge_linear_fp8",
+        "forge_dgrad_fp8", "forge_grad_norm", "forge_adamw_clip")])
+    _call = mod
 
 
 def header_functions() -> list[str]:
@@ -286,6 +309,17 @@ def _arg(t: Optional[torch.Tensor], name: str, shape, dtypes, dev: int) -> int:
 
 def _opt(t: Optional[torch.Tensor], name: str, shape, dtypes, dev: int) -> Optional[int]:
     return None if t is None else _arg(t, name, shape, dtypes, dev)
+
+
+def _loaded():
+    """The CPython extension, loading the library if need be."""
+    lib()
+    return _call
+
+
+def _address(stream) -> Optional[int]:
+    """A stream for the extension: None is the current one."""
+    return None if stream is None else _stream(stream)
 
 
 def _raw_stream(stream, dev: int) -> int:
@@ -537,6 +571,11 @@ def adamw_clip(dW: torch.Tensor, W: torch.Tensor, m: torch.Tensor, v: torch.Tens
                v_scale: Optional[torch.Tensor] = None, stream=None) -> None:
     """adamw on the clipped gradient dW * clip[1], where clip is what grad_norm
     left on the device (the norm and the coefficient, fp32 [2])."""
+    if m_scale is None and v_scale is None:
+        st = (_call or _loaded()).adamw_clip(dW, W, m, v, clip, lr, beta1, beta2, eps,
+                                             weight_decay, step, _address(stream))
+        if st >= 0:
+            return _check(st, "forge_adamw_clip") if st else None
     shape = _matrix(W, "W")
     dev = _device_of(W, "W")
     wp = _arg(W, "W", shape, _BF16, dev)
@@ -891,6 +930,10 @@ def rmsnorm(x: torch.Tensor, gain: torch.Tensor, *, eps: float,
     [rows, cols] bf16.  Writes the outputs given: sum_out = h (bf16; may be x or
     residual), y (bf16), codes and scales = y in the 128-block e4m3 format, rstd
     [rows] fp32 for rmsnorm_backward."""
+    st = (_call or _loaded()).rmsnorm(x, gain, eps, residual, sum_out, y, codes, scales, rstd,
+                                      _address(stream))
+    if st >= 0:
+        return _check(st, "forge_rmsnorm") if st else None
     rows, cols = shape = _matrix(x, "x")
     dev = _device_of(x, "x")
     st = lib().forge_rmsnorm(
@@ -916,6 +959,10 @@ def rmsnorm_backward(dY: torch.Tensor, h: torch.Tensor, gain: torch.Tensor, rstd
     dsum, the gradient that reaches the sum directly, is added and may be dX) and
     dgain [cols] fp32, from h (the forward pass's sum, or x) and rstd.  dgain
     needs a workspace of rmsnorm_backward_workspace_bytes bytes."""
+    st = (_call or _loaded()).rmsnorm_backward(dY, h, gain, rstd, dX, dgain, dsum, workspace,
+                                               _address(stream))
+    if st >= 0:
+        return _check(st, "forge_rmsnorm_backward") if st else None
     rows, cols = shape = _matrix(h, "h")
     dev = _device_of(h, "h")
     if workspace is not None:
@@ -933,6 +980,9 @@ def quantize_b128(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, *,
                   block_rows: int = 1, stream=None) -> None:
     """x [rows, cols] bf16 as e4m3 codes and one fp32 scale per block of
     block_rows (1 or 128) x 128 (see alloc_b128)."""
+    st = (_call or _loaded()).quantize(x, codes, scales, block_rows, _address(stream))
+    if st >= 0:
+        return _check(st, "forge_quantize_b128") if st else None
     rows, cols = shape = _matrix(x, "x")
     if block_rows not in (1, 128):
         raise ValueError("block_rows is 1 or 128")
@@ -962,6 +1012,9 @@ def linear_fp8(X: torch.Tensor, x_scales: torch.Tensor, W: torch.Tensor, w_scale
                Y: torch.Tensor, stream=None) -> None:
     """Y = X W^T on the 8-bit tensor cores: X [bt, d_in] codes with block_rows 1,
     W [d_out, d_in] codes with block_rows 128, Y [bt, d_out] bf16 or fp32."""
+    st = (_call or _loaded()).linear(X, x_scales, W, w_scales, Y, _address(stream))
+    if st >= 0:
+        return _check(st, "forge_linear_fp8") if st else None
     _matrix(X, "X")
     d_out, d_in = _matrix(W, "W")
     _product_fp8("forge_linear_fp8", X, x_scales, W, w_scales, Y, d_in, d_out, d_in, d_out, stream)
@@ -972,6 +1025,9 @@ def dgrad_fp8(dY: torch.Tensor, dy_scales: torch.Tensor, W: torch.Tensor, w_scal
     """dX = dY W on the 8-bit tensor cores, from the same stored weight as
     linear_fp8: dY [bt, d_out] codes with block_rows 1, dX [bt, d_in] bf16 or
     fp32."""
+    st = (_call or _loaded()).dgrad(dY, dy_scales, W, w_scales, dX, _address(stream))
+    if st >= 0:
+        return _check(st, "forge_dgrad_fp8") if st else None
     _matrix(dY, "dY")
     d_out, d_in = _matrix(W, "W")
     _product_fp8("forge_dgrad_fp8", dY, dy_scales, W, w_scales, dX, d_out, d_in, d_in, d_out,
@@ -988,6 +1044,9 @@ def grad_norm(grads, max_norm: float, out: torch.Tensor, *, workspace: torch.Ten
     """out (fp32 [2], on the device) = the global norm of the gradients (fp32 or
     bf16 tensors of any shape) and min(1, max_norm / (norm + 1e-6)), the factor
     adamw_clip applies."""
+    st = (_call or _loaded()).grad_norm(grads, max_norm, out, workspace, _address(stream))
+    if st >= 0:
+        return _check(st, "forge_grad_norm") if st else None
     dev = _device_of(out, "out")
     flat = []     # forge_grad records: pointer, size, dtype (and padding)
     for g in grads:

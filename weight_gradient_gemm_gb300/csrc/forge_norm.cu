@@ -155,15 +155,19 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) rmsnorm_kernel(const NormAr
 }
 
 // The rows of one persistent block (blockIdx.x, + gridDim.x, ...), copied ahead
-// into a ring of `depth` slots of S rows (one of each input) by bulk copies.
-// A slot is read into registers before the row's reduction, so it is free, and
+// into a ring of two slots of S rows (one of each input) by bulk copies.  Two
+// keep HBM busy; more reads in flight only meet the stores (8191 x 4096 with a
+// residual: 44.0 us, with three slots 46.7, with six 48.7).  The inputs pass
+// through L2 as the first to leave it, which the backward pass needs most
+// (8192 x 8192 with three slots: 91.6 us, 103.3 without; with two 94).  A slot
+// is read into registers before the row's reduction, so it is free, and
 // thread 0 refills it, as soon as the reduction's barrier is passed.  A wait
 // that runs out records its error and lets the block run on (its barriers stay
 // matched; what it writes is unspecified).
+constexpr int kRing = 2;
 template <int S>
 struct RowRing {
   uint32_t smem, bars, row_bytes;
-  int depth;
   const uint8_t* src[S];
   int64_t rows;
   WaitCtx wc;
@@ -173,17 +177,18 @@ struct RowRing {
 
   __device__ uint32_t at(int s, int i) const { return smem + (s * S + i) * row_bytes; }
   __device__ void fill(int s, int64_t row) const {
+    const uint64_t policy = l2_policy_evict_first();
     mbar_arrive_expect_tx(bars + 8u * s, S * row_bytes);
 #pragma unroll
     for (int i = 0; i < S; ++i)
-      bulk_load(at(s, i), src[i] + row * row_bytes, row_bytes, bars + 8u * s);
+      bulk_load(at(s, i), src[i] + row * row_bytes, row_bytes, bars + 8u * s, policy);
   }
   // thread 0, before anything is read
   __device__ void start() const {
-    for (int s = 0; s < depth; ++s) mbar_init(bars + 8u * s, 1);
+    for (int s = 0; s < kRing; ++s) mbar_init(bars + 8u * s, 1);
     fence_mbarrier_init();
     int64_t row = blockIdx.x;
-    for (int s = 0; s < depth && row < rows; ++s, row += gridDim.x) fill(s, row);
+    for (int s = 0; s < kRing && row < rows; ++s, row += gridDim.x) fill(s, row);
   }
   __device__ void wait() {
     ok = ok && wait_bounded(bars + 8u * slot, ph, wc, kSiteDrainState);
@@ -191,10 +196,10 @@ struct RowRing {
   // after the barrier that follows the slot's last read
   __device__ void next(int64_t row) {
     if (threadIdx.x == 0 && ok) {
-      const int64_t ahead = row + static_cast<int64_t>(depth) * gridDim.x;
+      const int64_t ahead = row + static_cast<int64_t>(kRing) * gridDim.x;
       if (ahead < rows) fill(slot, ahead);
     }
-    if (++slot == depth) { slot = 0; ph ^= 1u; }
+    if (++slot == kRing) { slot = 0; ph ^= 1u; }
   }
   // After a timeout: time for copies still under way to land before the block
   // leaves its shared memory.
@@ -214,27 +219,26 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr) {
 }
 // Shared memory: the ring, 16-byte aligned, then its barriers and an abort flag.
 template <int S>
-__device__ __forceinline__ RowRing<S> make_ring(uint8_t* smem, int depth, uint32_t row_bytes,
-                                                int64_t rows, const NormWait& w) {
+__device__ __forceinline__ RowRing<S> make_ring(uint8_t* smem, uint32_t row_bytes, int64_t rows,
+                                                const NormWait& w) {
   RowRing<S> r;
   r.smem = smem_u32(smem);
   r.row_bytes = row_bytes;
-  r.depth = depth;
   r.rows = rows;
-  r.bars = r.smem + depth * S * row_bytes;
+  r.bars = r.smem + kRing * S * row_bytes;
   volatile uint32_t* abort_flag =
-      reinterpret_cast<volatile uint32_t*>(smem + depth * S * row_bytes + 8 * depth);
+      reinterpret_cast<volatile uint32_t*>(smem + kRing * S * row_bytes + 8 * kRing);
   r.wc = WaitCtx{abort_flag, w.err, w.err_site, w.timeout_ns};
   return r;
 }
 
 template <int VPT, bool RES>
-__global__ void __launch_bounds__(1024, 1) rmsnorm_stream_kernel(const NormArgs a, int depth) {
+__global__ void __launch_bounds__(1024, 1) rmsnorm_stream_kernel(const NormArgs a) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   __shared__ float red[2][32];
   const int nvec = a.cols / 8;
   RowRing<RES ? 2 : 1> ring =
-      make_ring<RES ? 2 : 1>(smem_raw, depth, static_cast<uint32_t>(a.cols) * 2, a.rows, a.wait);
+      make_ring<RES ? 2 : 1>(smem_raw, static_cast<uint32_t>(a.cols) * 2, a.rows, a.wait);
   ring.src[0] = reinterpret_cast<const uint8_t*>(a.x);
   if constexpr (RES) ring.src[1] = reinterpret_cast<const uint8_t*>(a.residual);
   grid_dependency_wait();
@@ -401,13 +405,12 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) rmsnorm_bwd_kernel(const No
 
 template <int VPT, bool DSUM>
 __global__ void __launch_bounds__(1024, 1)
-    rmsnorm_bwd_stream_kernel(const NormBwdArgs a, int depth) {
+    rmsnorm_bwd_stream_kernel(const NormBwdArgs a) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   __shared__ float red[2][32];
   constexpr int S = DSUM ? 3 : 2;
   const int nvec = a.cols / 8;
-  RowRing<S> ring =
-      make_ring<S>(smem_raw, depth, static_cast<uint32_t>(a.cols) * 2, a.rows, a.wait);
+  RowRing<S> ring = make_ring<S>(smem_raw, static_cast<uint32_t>(a.cols) * 2, a.rows, a.wait);
   ring.src[0] = reinterpret_cast<const uint8_t*>(a.h);
   ring.src[1] = reinterpret_cast<const uint8_t*>(a.dy);
   if constexpr (DSUM) ring.src[2] = reinterpret_cast<const uint8_t*>(a.dsum);
@@ -609,7 +612,7 @@ int row_threads(int cols, int vpt) {
 enum Walk { kWalkWarp, kWalkBlock, kWalkStream };
 struct RowPlan {
   Walk walk;
-  int vpt, threads, grid, depth, smem;   // depth, smem: the stream's ring
+  int vpt, threads, grid, smem;   // smem: the stream's ring
 };
 
 // A warp per row up to 1024 columns (backward 512, whose registers hold two
@@ -617,7 +620,7 @@ struct RowPlan {
 // persistent blocks twice, while a ring of two rows fits (else a block per
 // row).  Blocks of about 1024 threads in all share an SM.
 RowPlan row_plan(int64_t rows, int cols, int streams, bool backward, int num_sms) {
-  RowPlan p{kWalkBlock, 1, 0, 0, 0, 0};
+  RowPlan p{kWalkBlock, 1, 0, 0, 0};
   if (cols <= (backward ? 512 : 1024)) {
     p.walk = kWalkWarp;
     p.vpt = cols <= 256 ? 1 : (cols <= 512 ? 2 : 4);
@@ -630,13 +633,10 @@ RowPlan row_plan(int64_t rows, int cols, int streams, bool backward, int num_sms
   p.threads = row_threads(cols, p.vpt);
   int per_sm = 1024 / p.threads;
   per_sm = per_sm > 8 ? 8 : per_sm;
-  const int row_bytes = streams * cols * 2;
-  p.depth = (220 * 1024 / per_sm) / row_bytes;
-  if (p.depth > 8) p.depth = 8;
-  if (p.vpt <= 2 && p.depth >= 2 && rows >= 2 * per_sm * num_sms) {
+  p.smem = kRing * (streams * cols * 2 + 8) + 8;
+  if (p.vpt <= 2 && p.smem * per_sm <= 222 * 1024 && rows >= 2 * per_sm * num_sms) {
     p.walk = kWalkStream;
     p.grid = per_sm * num_sms;
-    p.smem = p.depth * (row_bytes + 8) + 8;
     return p;
   }
   // every row in flight at once; the backward pass's sums want few blocks
@@ -657,7 +657,7 @@ cudaError_t launch_stream(Kern kern, int* ready, const RowPlan& p, const Args& a
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) ready[dev] = 1;
   }
-  return launch_chained(kern, p.grid, p.threads, p.smem, 0, stream, a, p.depth);
+  return launch_chained(kern, p.grid, p.threads, p.smem, 0, stream, a);
 }
 template <int VPT, bool RES>
 cudaError_t launch_fwd_stream(const RowPlan& p, const NormArgs& a, cudaStream_t stream) {

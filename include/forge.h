@@ -667,11 +667,14 @@ typedef enum {
  * ignored. */
 typedef struct {
   int profile;     /* a forge_profile                                          */
-  int cta_group;   /* 0 automatic; 1 one CTA per tile; 2 a CTA pair (256 x 256) */
+  int cta_group;   /* 0 automatic; 1 one CTA per tile; 2 a CTA pair (256 x 256);
+                      for the 8-bit products both also set the tile for few tokens */
   int bn;          /* 0 automatic; 128 or 256: accumulator width on one CTA     */
   int group_m;     /* 0 automatic; 1..64 tile rows per raster group             */
   int poll_store;  /* -1 automatic; 0 or 1: store lanes poll for finished slots */
-  int splits;      /* 0 automatic; 1..8 k-ranges per tile for forge_dgrad       */
+  int splits;      /* 0 automatic; 1..8 k-ranges per tile for forge_dgrad; for
+                      the 8-bit products of up to 128 tokens the CTAs that share
+                      a tile (rounded down to 1, 2, 4 or 8)                     */
   int l2_hints;    /* -1 automatic; 0..3: bit 0 marks the optimizer state's
                       stores evict-first in L2, bit 1 its m, v loads whose rows
                       are whole 128-byte lines                                  */

@@ -6,6 +6,12 @@
 // elements so that blocks share the work evenly whatever the tensors' sizes;
 // each block leaves one partial sum, and a second launch adds the partials in
 // a fixed order, so the norm is the same on every run.
+//
+// Bound by memory: the 218 M fp32 gradients of a 4096-wide layer (872 MB) take
+// 127 us, 6.9 TB/s, a plain copy's rate; in bf16 71 us, 6.1 TB/s, of which about
+// 6 us are the two launches and their tails.  Few values cost the launches alone
+// (5.4 us for six small tensors; one launch of a single cluster, whose blocks
+// join through shared memory, took 8.2 where two took 6.8).
 #include "forge_internal.h"
 #include "forge_launch.cuh"
 

@@ -54,7 +54,7 @@ __device__ __forceinline__ void load_gain8(const void* gain, int bf16, int v, fl
 //   the same with codes and scales            50.3 us (44.6)
 //   8192 x 8192                               89.7 us (79.1)
 //   8192 x 1024 (a warp per row)              13.1 us (9.9)
-//   512 x 4096 (a block per row)               5.8 us (2.5), launch and tail
+//   512 x 4096 (a block per row)               4.6 us (2.5), launch and tail
 //   1 x 4096                                   1.9 us: the latency of a launch,
 //                                              the loads and one reduction
 // With a block per row throughout, 8191 x 4096 took 55 us: between its reads and
@@ -663,7 +663,14 @@ RowPlan row_plan(int64_t rows, int cols, int streams, bool backward, int num_sms
     p.grid = per_sm * num_sms;
     return p;
   }
-  // every row in flight at once; the backward pass's sums want few blocks
+  // Every row in flight at once: where a vector a thread leaves rows for a second
+  // wave, two vectors and half the threads (512 x 4096: 4.6 us, 5.8 with one
+  // vector; 304 rows the same, 152 rows 3.0 and 2.8).  The backward pass's sums
+  // want few blocks (1000 x 1032 with two vectors 11.0 us, 8.9 with one).
+  if (!backward && p.vpt == 1 && rows > per_sm * num_sms) {
+    p.vpt = 2;
+    p.threads = row_threads(cols, 2);
+  }
   const int64_t most = backward ? static_cast<int64_t>(num_sms) * 2 : INT32_MAX;
   p.grid = static_cast<int>(rows < most ? rows : most);
   return p;

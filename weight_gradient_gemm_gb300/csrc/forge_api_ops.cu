@@ -269,6 +269,7 @@ forge_status forge_quantize_b128(const void* x, void* codes, float* scales, int6
   if (st != FORGE_OK) return static_cast<forge_status>(st);
   return status(launch_quantize_b128(static_cast<const uint16_t*>(x), static_cast<uint8_t*>(codes),
                                      scales, rows, cols, block_rows, d.num_sms,
+                                     NormWait{d.err, d.err_site, d.timeout_ns},
                                      static_cast<cudaStream_t>(stream)));
 }
 

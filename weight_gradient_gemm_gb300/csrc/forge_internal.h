@@ -246,7 +246,8 @@ constexpr int kNormMaxCols = 32768;
 
 // e4m3 codes and one scale per block of block_rows (1 or 128) x 128.
 cudaError_t launch_quantize_b128(const uint16_t* x, uint8_t* codes, float* scales, int64_t rows,
-                                 int64_t cols, int block_rows, int num_sms, cudaStream_t stream);
+                                 int64_t cols, int block_rows, int num_sms, const NormWait& wait,
+                                 cudaStream_t stream);
 
 // The global gradient norm (forge_gradnorm.cu).
 constexpr int kNormTensors = 128;   // tensors one launch takes

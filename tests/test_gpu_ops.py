@@ -89,6 +89,12 @@ def test_rmsnorm(rows, cols, res, gain_dtype):
     check_codes(codes, scales, y64, 1, yrel, np.zeros_like(y64))
 
 
+@pytest.mark.parametrize("rows,cols", [(400, 4096), (310, 4104), (1200, 1032), (200, 8200)])
+@pytest.mark.parametrize("res", [False, True])
+def test_rmsnorm_more_rows_than_one_wave(rows, cols, res):
+    test_rmsnorm(rows, cols, res, torch.bfloat16)
+
+
 def test_rmsnorm_each_output_alone():
     x, r, gain = rand(1, (5, 392)), rand(2, (5, 392)), rand(3, (392,), 1.0, torch.float32)
     y, s, rstd = torch.empty_like(x), torch.empty_like(x), torch.empty(5, device=DEV)
@@ -216,6 +222,11 @@ def test_quantize(rows, cols, block_rows):
     ok()
     x64 = f64(x)
     check_codes(codes, scales, x64, block_rows, 0.0, np.zeros_like(x64))
+
+
+@pytest.mark.parametrize("rows,cols", [(5000, 2056), (40, 80000), (80000, 40)])
+def test_quantize_more_blocks_than_resident(rows, cols):
+    test_quantize(rows, cols, 128)
 
 
 @pytest.mark.parametrize("block_rows", [1, 128])

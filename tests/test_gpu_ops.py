@@ -172,6 +172,37 @@ def test_rmsnorm_backward(rows, cols, with_dsum, gain_dtype):
     ok()
 
 
+@pytest.mark.parametrize("rows,cols", [(1500, 1032), (800, 520), (2100, 512), (1024, 4096),
+                                       (2000, 2048), (400, 8192), (320, 16384), (305, 14336)])
+@pytest.mark.parametrize("with_dsum", [False, True])
+def test_rmsnorm_backward_between_one_wave_and_many(rows, cols, with_dsum):
+    test_rmsnorm_backward(rows, cols, with_dsum, torch.float32)
+
+
+def test_rmsnorm_backward_many_wide_rows():
+    # rows too wide for the stream and too many for one launch; dX on a few rows
+    rows, cols = 4200, 16392
+    h, dy = rand(4, (rows, cols), 2.0), rand(5, (rows, cols), 1e-2)
+    gain = 1 + rand(3, (cols,), 0.2, torch.float32)
+    rstd = (1 / torch.sqrt(h.float().square().mean(1) + 1e-5))
+    dx, dgain = torch.empty_like(h), torch.empty(cols, device=DEV)
+    ws = torch.empty(F.rmsnorm_backward_workspace_bytes(rows, cols), dtype=torch.uint8, device=DEV)
+    F.rmsnorm_backward(dy, h, gain, rstd, dx, dgain, workspace=ws)
+    ok()
+    dg64, mag = torch.zeros(cols, dtype=torch.float64, device=DEV), 0.0
+    for r in range(0, rows, 600):
+        t = dy[r:r + 600].double() * (h[r:r + 600].double() * rstd[r:r + 600, None].double())
+        dg64 += t.sum(0)
+        mag = mag + t.abs().sum(0)
+    within(f64(dgain), f64(dg64), 90 * U * f64(mag) + 1e-30)
+    pick = torch.tensor([0, 1, 303, 304, 2111, 4199], device=DEV)
+    d64, h64, g64, r64 = f64(dy[pick]), f64(h[pick]), f64(gain), f64(rstd[pick])
+    dx64, _ = R.rmsnorm_backward(d64, h64, g64, r64, None)
+    xh, u = np.abs(h64 * r64[:, None]), np.abs(d64 * g64)
+    noise = r64[:, None] * (6 * U * u + 80 * U * xh * (u * xh).mean(1, keepdims=True))
+    within(f64(dx[pick]), dx64, (BF + 2 * U) * np.abs(dx64) + noise)
+
+
 def test_rmsnorm_backward_against_differences():
     # L = sum(dy * y): its central differences in h and in the gain, in fp64
     rows, cols, eps = 3, 40, 1e-5

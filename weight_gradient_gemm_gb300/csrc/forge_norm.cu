@@ -246,7 +246,7 @@ __device__ __forceinline__ RowRing<S> make_ring(uint8_t* smem, uint32_t row_byte
 
 template <int VPT, bool RES>
 __global__ void __launch_bounds__(1024, 1) rmsnorm_stream_kernel(const NormArgs a) {
-  extern __shared__ __align__(16) uint8_t smem_raw[];
+  extern __shared__ __align__(128) uint8_t smem_raw[];
   __shared__ float red[2][32];
   const int nvec = a.cols / 8;
   RowRing<RES ? 2 : 1> ring =
@@ -293,12 +293,15 @@ __global__ void __launch_bounds__(1024, 1) rmsnorm_stream_kernel(const NormArgs 
 // ---------------------------------------------------------------- backward
 // With xh = h rstd and u = dy gain, the gradient of y = xh gain with respect
 // to h is rstd (u - xh mean(u xh)); dsum, the gradient that reaches h along
-// the residual stream, is added.  dgain = sum over rows of dy xh: a block
-// adds its rows in registers and leaves one partial row, which
-// rmsnorm_dgain_kernel adds in a fixed order.
+// the residual stream, is added.  dgain = sum over rows of dy xh, in one of two
+// ways, each in a fixed order:
+//   few rows: blocks of their own beside those of the rows read dy and h again
+//   (from L2) and add down 16 or 32 columns; one launch;
+//   many rows: a block adds its rows in registers and leaves one partial row,
+//   and rmsnorm_dgain_kernel adds those.
 // Bound by memory: 8192 x 4096 with dsum, 268 MB, 47.1 us with the second
-// launch (39.5 at the copy rate; a block per row 71).  Few rows are bound by the
-// two launches: 333 x 1032 takes 4.8 us a call.
+// launch (39.5 at the copy rate; a block per row 71); 512 x 4096 6.5 us (2.5),
+// 333 x 1032 2.6 us, 1 x 4096 1.8.
 // One vector's share of the row's dot product; dgain's terms are added to dg.
 __device__ __forceinline__ float bwd_dot(uint4 hv, uint4 dv, const float (&g)[8], float rstd,
                                          float (&dg)[8]) {
@@ -343,15 +346,74 @@ __device__ __forceinline__ void write_part(const NormBwdArgs& a, const float (&d
   }
 }
 
-template <int VPT, bool WARP>
-__global__ void __launch_bounds__(WARP ? 256 : 1024) rmsnorm_bwd_kernel(const NormBwdArgs a) {
+// dgain of 8 L columns from dy, h and rstd: L lanes hold a row's columns, every
+// run of L lanes its own rows.
+template <int L>
+__device__ __forceinline__ void dgain_columns(const NormBwdArgs& a, int cb, float (&red)[32][32]) {
+  constexpr int kBatch = 4;   // rows whose loads are in flight at once
+  const int lane = threadIdx.x & 31, sub = lane & (L - 1), runs = blockDim.x / L;
+  const int nvec = a.cols / 8, v = cb * L + sub;
+  float dg[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+  if (v < nvec) {
+    for (int64_t row = threadIdx.x / L; row < a.rows; row += kBatch * runs) {
+      uint4 hv[kBatch], dv[kBatch];
+      float rs[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int64_t r = row + j * runs;
+        hv[j] = dv[j] = make_uint4(0, 0, 0, 0);
+        rs[j] = 0.0f;
+        if (r < a.rows) {
+          hv[j] = reinterpret_cast<const uint4*>(a.h)[r * nvec + v];
+          dv[j] = reinterpret_cast<const uint4*>(a.dy)[r * nvec + v];
+          rs[j] = a.rstd[r];
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        float h[8], d[8];
+        unpack8(hv[j], h);
+        unpack8(dv[j], d);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) dg[k] += d[k] * (h[k] * rs[j]);
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+#pragma unroll
+    for (int o = L; o < 32; o <<= 1) dg[k] += __shfl_xor_sync(0xffffffffu, dg[k], o);
+    if (lane < L) red[threadIdx.x >> 5][sub * 8 + k] = dg[k];
+  }
+  __syncthreads();
+  if (threadIdx.x < 8 * L && cb * 8 * L + static_cast<int>(threadIdx.x) < a.cols) {
+    float sum = 0.0f;
+    for (int w = 0; w < (blockDim.x >> 5); ++w) sum += red[w][threadIdx.x];
+    a.dgain[cb * 8 * L + threadIdx.x] = sum;
+  }
+}
+
+// DIRECT: the first col_blocks blocks add up dgain, the others take the rows.
+template <int VPT, bool WARP, bool DIRECT>
+__global__ void __launch_bounds__(WARP ? 256 : 1024)
+    rmsnorm_bwd_kernel(const NormBwdArgs a, int col_blocks, int lanes) {
   __shared__ float red[2][32];
-  __shared__ float4 parts[WARP ? 8 * 64 * VPT : 1];   // [warp][vector][2]
+  __shared__ float4 parts[DIRECT ? 256 : (WARP ? 8 * 64 * VPT : 1)];   // [warp][vector][2]
   const int nvec = a.cols / 8;
   const int width = WARP ? 32 : blockDim.x, me = WARP ? threadIdx.x & 31 : threadIdx.x;
-  const int64_t first =
-      WARP ? static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5) : blockIdx.x;
-  const int64_t step = WARP ? static_cast<int64_t>(gridDim.x) * 8 : gridDim.x;
+  int block = blockIdx.x, blocks = gridDim.x;
+  if constexpr (DIRECT) {
+    if (block < col_blocks) {
+      grid_dependency_wait();
+      if (lanes == 4) dgain_columns<4>(a, block, reinterpret_cast<float(&)[32][32]>(parts));
+      else dgain_columns<2>(a, block, reinterpret_cast<float(&)[32][32]>(parts));
+      return;
+    }
+    block -= col_blocks;
+    blocks -= col_blocks;
+  }
+  const int64_t first = WARP ? static_cast<int64_t>(block) * 8 + (threadIdx.x >> 5) : block;
+  const int64_t step = WARP ? static_cast<int64_t>(blocks) * 8 : blocks;
   int parity = 0;
   float dg[VPT][8];
 #pragma unroll
@@ -379,7 +441,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) rmsnorm_bwd_kernel(const No
       if (v < nvec) {
         float g[8];
         load_gain8(a.gain, a.gain_bf16, v, g);
-        dot += bwd_dot(hv[i], dv[i], g, rstd, dg[i]);
+        dot += bwd_dot(hv[i], dv[i], g, rstd, dg[DIRECT ? 0 : i]);   // DIRECT: not used
       }
     }
     dot = WARP ? warp_sum(dot) : block_sum(dot, red[parity]);
@@ -395,8 +457,8 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) rmsnorm_bwd_kernel(const No
     }
   }
   grid_dependency_trigger();
-  if (!a.dgain) return;
-  if constexpr (WARP) {   // the block's warps join in a fixed order
+  if (DIRECT || !a.dgain) return;
+  if constexpr (WARP && !DIRECT) {   // the block's warps join in a fixed order
     const int warp = threadIdx.x >> 5;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
@@ -413,7 +475,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) rmsnorm_bwd_kernel(const No
       }
       reinterpret_cast<float4*>(a.part)[static_cast<int64_t>(blockIdx.x) * nvec * 2 + e] = s;
     }
-  } else {
+  } else if constexpr (!DIRECT) {
     write_part<VPT>(a, dg, me, width);
   }
 }
@@ -421,7 +483,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) rmsnorm_bwd_kernel(const No
 template <int VPT, bool DSUM>
 __global__ void __launch_bounds__(1024, 1)
     rmsnorm_bwd_stream_kernel(const NormBwdArgs a) {
-  extern __shared__ __align__(16) uint8_t smem_raw[];
+  extern __shared__ __align__(128) uint8_t smem_raw[];
   __shared__ float red[2][32];
   constexpr int S = DSUM ? 3 : 2;
   const int nvec = a.cols / 8;
@@ -667,18 +729,31 @@ enum Walk { kWalkWarp, kWalkBlock, kWalkStream };
 struct RowPlan {
   Walk walk;
   int vpt, threads, grid, smem;   // smem: the stream's ring
+  bool direct;                    // backward: dgain in the same launch
+  int lanes;                      // and the lanes that hold a row's columns there
 };
 
 // A warp per row up to 1024 columns (backward 512, whose registers hold the
 // gain's gradient besides).  Above, the stream for rows enough to fill its
 // persistent blocks twice, while a ring of two rows fits (else a block per
 // row).  Blocks of about 1024 threads in all share an SM.
+//
+// (Whether dgain is asked for changes nothing here, so dX has the same bits.)
+// The backward pass adds up dgain in the same launch while a run of lanes has at
+// most 16 rows, and in place of the stream up to 2^23 values (two rounds through
+// L2 cost less than the second launch).  With the second launch, then without:
+// 333 x 1032 5.7 and 2.6 us, 512 x 4096 9.5 and 6.5, 1024 x 4096 12.4 and 9.8,
+// 2048 x 4096 17.0 and 15.7; 2000 x 8192 28.8 and 31.2.  Up to 2048 columns
+// two lanes a row, for more column blocks (1000 x 2048: 7.0 us, 9.2 with four;
+// 2048 x 4096 16.6 and 15.7).
+constexpr int64_t kDirectValues = 1 << 23;
 RowPlan row_plan(int64_t rows, int cols, int streams, bool backward, int num_sms) {
-  RowPlan p{kWalkBlock, 1, 0, 0, 0};
+  RowPlan p{kWalkBlock, 1, 0, 0, 0, false, cols <= 2048 ? 2 : 4};
   if (cols <= (backward ? 512 : 1024)) {
     p.walk = kWalkWarp;
     p.vpt = cols <= 256 ? 1 : (cols <= 512 ? 2 : 4);
     p.threads = 256;
+    p.direct = backward && rows <= 16 * p.threads / p.lanes;
     const int64_t want = (rows + 7) / 8, most = static_cast<int64_t>(num_sms) * 4;
     p.grid = static_cast<int>(want < most ? want : most);
     return p;
@@ -687,8 +762,10 @@ RowPlan row_plan(int64_t rows, int cols, int streams, bool backward, int num_sms
   p.threads = row_threads(cols, p.vpt);
   int per_sm = 1024 / p.threads;
   per_sm = per_sm > 8 ? 8 : per_sm;
+  const int64_t direct_rows = 16 * p.threads / p.lanes;
+  p.direct = backward && rows <= direct_rows && rows * cols <= kDirectValues;
   p.smem = kRing * (streams * cols * 2 + 8) + 8;
-  if (p.vpt <= 2 && p.smem * per_sm <= 222 * 1024 && rows >= 2 * per_sm * num_sms) {
+  if (!p.direct && p.vpt <= 2 && p.smem * per_sm <= 222 * 1024 && rows >= 2 * per_sm * num_sms) {
     p.walk = kWalkStream;
     p.grid = per_sm * num_sms;
     return p;
@@ -697,11 +774,12 @@ RowPlan row_plan(int64_t rows, int cols, int streams, bool backward, int num_sms
   // wave, two vectors and half the threads (512 x 4096: 4.6 us, 5.8 with one
   // vector; 304 rows the same, 152 rows 3.0 and 2.8).  The backward pass's sums
   // want few blocks (1000 x 1032 with two vectors 11.0 us, 8.9 with one).
-  if (!backward && p.vpt == 1 && rows > per_sm * num_sms) {
+  p.direct = backward && rows <= direct_rows;
+  if ((!backward || p.direct) && p.vpt == 1 && rows > per_sm * num_sms) {
     p.vpt = 2;
     p.threads = row_threads(cols, 2);
   }
-  const int64_t most = backward ? static_cast<int64_t>(num_sms) * 2 : INT32_MAX;
+  const int64_t most = backward && !p.direct ? static_cast<int64_t>(num_sms) * 2 : INT32_MAX;
   p.grid = static_cast<int>(rows < most ? rows : most);
   return p;
 }
@@ -752,9 +830,10 @@ cudaError_t launch_rmsnorm(const NormArgs& a, int num_sms, cudaStream_t stream) 
 
 int rmsnorm_bwd_blocks(int64_t rows, int cols, int num_sms) {
   // with and without dsum: one workspace serves both
-  const int a = row_plan(rows, cols, 2, true, num_sms).grid;
-  const int b = row_plan(rows, cols, 3, true, num_sms).grid;
-  return a > b ? a : b;
+  const RowPlan a = row_plan(rows, cols, 2, true, num_sms);
+  const RowPlan b = row_plan(rows, cols, 3, true, num_sms);
+  const int na = a.direct ? 1 : a.grid, nb = b.direct ? 1 : b.grid;   // direct: none read
+  return na > nb ? na : nb;
 }
 
 cudaError_t launch_rmsnorm_bwd(const NormBwdArgs& a, int num_sms, cudaStream_t stream) {
@@ -767,14 +846,26 @@ cudaError_t launch_rmsnorm_bwd(const NormBwdArgs& a, int num_sms, cudaStream_t s
     else
       e = a.dsum ? launch_bwd_stream<2, true>(p, a, stream)
                  : launch_bwd_stream<2, false>(p, a, stream);
-  } else {
-    auto go = [&](auto kern) { return launch_chained(kern, p.grid, p.threads, 0, 0, stream, a); };
+  } else if (p.direct) {
+    const int cb = a.dgain ? (a.cols + 8 * p.lanes - 1) / (8 * p.lanes) : 0;
+    auto go = [&](auto kern) {
+      return launch_chained(kern, cb + p.grid, p.threads, 0, 0, stream, a, cb, p.lanes);
+    };
     if (p.walk == kWalkWarp)
-      e = p.vpt == 1 ? go(rmsnorm_bwd_kernel<1, true>) : go(rmsnorm_bwd_kernel<2, true>);
+      return p.vpt == 1 ? go(rmsnorm_bwd_kernel<1, true, true>)
+                        : go(rmsnorm_bwd_kernel<2, true, true>);
+    return p.vpt == 1 ? go(rmsnorm_bwd_kernel<1, false, true>)
+                      : (p.vpt == 2 ? go(rmsnorm_bwd_kernel<2, false, true>)
+                                    : go(rmsnorm_bwd_kernel<4, false, true>));
+  } else {
+    auto go = [&](auto kern) { return launch_chained(kern, p.grid, p.threads, 0, 0, stream, a, 0, 0); };
+    if (p.walk == kWalkWarp)
+      e = p.vpt == 1 ? go(rmsnorm_bwd_kernel<1, true, false>)
+                     : go(rmsnorm_bwd_kernel<2, true, false>);
     else
-      e = p.vpt == 1 ? go(rmsnorm_bwd_kernel<1, false>)
-                     : (p.vpt == 2 ? go(rmsnorm_bwd_kernel<2, false>)
-                                   : go(rmsnorm_bwd_kernel<4, false>));
+      // (rows of 8200 to 16384 columns go direct or through the stream)
+      e = p.vpt == 1 ? go(rmsnorm_bwd_kernel<1, false, false>)
+                     : go(rmsnorm_bwd_kernel<4, false, false>);
   }
   if (e != cudaSuccess || !a.dgain) return e;
   return launch_chained(rmsnorm_dgain_kernel, (a.cols + 31) / 32, 1024, 0, 0, stream,

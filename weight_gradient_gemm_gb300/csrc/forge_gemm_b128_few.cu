@@ -47,21 +47,21 @@ struct Few {
   static constexpr int SC_BATCH = 8;
   static constexpr int SC_BYTES = 2 * SC_BATCH * NT * 4;
   static constexpr int PART_BYTES = NT * kBM * 4;       // one tile of fp32 sums
-  // The shares arrive in a buffer of their own for few tokens; for more they
-  // take the place of the operand stages, once every CTA is done with them.
-  static constexpr bool ALIAS = NT > 32;
   // Shared memory from a 1024-aligned base: barriers (the most there can be),
-  // abort flag, scales, shares, stages.
+  // abort flag, scales, stages, and where the reduction is split the shares.
+  // (In the stages' place the shares would have to wait for every CTA's last
+  // load and product: a cluster barrier more.)
   static constexpr int NUM_BARS = 2 * DEEP + 2 * NBUF + 5;
   static constexpr int OFF_TMEM = 8 * NUM_BARS;
   static constexpr int OFF_SC = (OFF_TMEM + 8 + 15) & ~15;
-  static constexpr int OFF_PART0 = OFF_SC + SC_BYTES;
-  static constexpr int OFF_STAGES = (OFF_PART0 + (ALIAS ? 0 : PART_BYTES) + 1023) & ~1023;
-  static constexpr int OFF_PART = ALIAS ? OFF_STAGES : OFF_PART0;
-  static constexpr int smem(int stages) { return OFF_STAGES + stages * STAGE_BYTES + 1024; }
-  static_assert(!ALIAS || PART_BYTES <= STAGES * STAGE_BYTES, "shares fit the stages");
-  static_assert(NT > 64 || 2 * smem(STAGES) <= 228 * 1024 - 2 * 1024, "two CTAs an SM");
-  static_assert(smem(DEEP) <= 232448, "shared memory budget");
+  static constexpr int OFF_STAGES = (OFF_SC + SC_BYTES + 1023) & ~1023;
+  static constexpr int smem(int stages, bool split) {
+    return OFF_STAGES + stages * STAGE_BYTES + (split ? PART_BYTES : 0) + 1024;
+  }
+  static constexpr int SPLIT_DEEP = NT <= 32 ? DEEP : (NT == 64 ? 6 : 4);   // beside the shares
+  static_assert(NT > 64 || 2 * smem(STAGES, false) <= 228 * 1024 - 2 * 1024, "two CTAs an SM");
+  static_assert(smem(DEEP, false) <= 232448 && smem(SPLIT_DEEP, true) <= 232448,
+                "shared memory budget");
 };
 
 __device__ __forceinline__ void store_out(const B128Args& a, int64_t idx, float v) {
@@ -266,16 +266,14 @@ __global__ void __launch_bounds__(Few<NT>::THREADS, NT <= 64 ? 2 : 1)
       }
     }
   } else {
-    // every CTA has started; with the shares in the stages' place, every CTA's
-    // loads and MMAs are also done
     __syncthreads();
-    cluster_wait();
-    if (T::ALIAS) cluster_sync_all();
+    cluster_wait();   // every CTA has started
+    const uint32_t off_part = T::OFF_STAGES + a.stages * T::STAGE_BYTES;
     const int slice = kBM / splits;   // outputs each CTA of the cluster owns (splits divides 128)
     if (warp >= 4) {
       const int h = (warp - 4) >> 2, o = (warp & 3) * 32 + lane;
       // [rank of the sender][token][output of the slice]
-      const uint32_t dst = mapa_shared(base + T::OFF_PART, o / slice) +
+      const uint32_t dst = mapa_shared(base + off_part, o / slice) +
                            4u * ((rank * NT + h * T::NC) * slice + o % slice);
 #pragma unroll
       for (int i = 0; i < T::NC; ++i)
@@ -284,14 +282,25 @@ __global__ void __launch_bounds__(Few<NT>::THREADS, NT <= 64 ? 2 : 1)
     }
     cluster_sync_all();
     if (!*abort_flag) {
-      const float* part = reinterpret_cast<const float*>(gbase + T::OFF_PART);
-      const int total = a.m * slice;
+      const float* part = reinterpret_cast<const float*>(gbase + off_part);
+      // four outputs at a time: a slice is a power of two of at least 16, and an
+      // output row a multiple of 16
+      const int shift = 31 - __clz(slice >> 2), total = a.m << shift;
       for (int e = threadIdx.x; e < total; e += T::THREADS) {
-        const int t = e / slice, j = e - t * slice, o = tile * 128 + rank * slice + j;
+        const int t = e >> shift, j = (e - (t << shift)) * 4, o = tile * 128 + rank * slice + j;
         if (o >= a.n) continue;
-        float v = 0.0f;
-        for (int z = 0; z < splits; ++z) v += part[(z * NT + t) * slice + j];
-        store_out(a, static_cast<int64_t>(t) * a.n + o, v);
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int z = 0; z < splits; ++z) {
+          const float4 p = *reinterpret_cast<const float4*>(part + (z * NT + t) * slice + j);
+          v.x += p.x; v.y += p.y; v.z += p.z; v.w += p.w;
+        }
+        const int64_t idx = static_cast<int64_t>(t) * a.n + o;
+        if (a.out_fp32) {
+          *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out_ptr) + idx) = v;
+        } else {
+          *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.out_ptr) + idx) =
+              make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+        }
       }
     }
   }
@@ -310,12 +319,13 @@ cudaError_t launch_t(B128Args a, int num_sms, cudaStream_t stream) {
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || !ready[dev]) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         T::smem(T::DEEP));
+                                         232448);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) ready[dev] = 1;
   }
-  a.stages = a.num_tiles * a.splits <= num_sms ? T::DEEP : T::STAGES;
-  return launch_chained(kern, a.num_tiles * a.splits, T::THREADS, T::smem(a.stages),
+  const bool split = a.splits > 1;
+  a.stages = split ? T::SPLIT_DEEP : (a.num_tiles <= num_sms ? T::DEEP : T::STAGES);
+  return launch_chained(kern, a.num_tiles * a.splits, T::THREADS, T::smem(a.stages, split),
                         a.splits > 1 ? a.splits : 0, stream, a);
 }
 

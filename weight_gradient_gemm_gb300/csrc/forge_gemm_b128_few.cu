@@ -14,9 +14,10 @@
 //
 // Bound by the weight's bytes and, below about 10 MB, by the 3.5 us that a launch
 // takes from its first load to its last store.  4096 -> 14336 (58.7 MB, 8.7 us at
-// 6.79 TB/s): 12.3 us for one token, 12.8 for 16, 13.8 for 64, 17.5 for 128 (where
-// adding up the accumulators weighs in); 4096 -> 4096 (2.5 us): 6.1, 6.6, 9.0 and
-// 11.5; 4096 -> 1024: 4.0 for one.
+// 6.79 TB/s): 12.3 us for one token, 12.8 for 16, 14.1 for 64, 17.6 for 128, where
+// every CTA reads all the tokens again (117 MB through L2; without any adding up
+// 15.6 us); 4096 -> 4096 (2.5 us): 6.1, 6.6, 7.3 and 9.3; 4096 -> 1024: 4.0 for
+// one.
 //
 // Warp roles: 0 loads (TMA), 1 issues the MMAs, 2 multiplies the scales, from
 // 4 on the epilogue (the 32 outputs of a TMEM lane quadrant and up to 32

@@ -14,9 +14,9 @@
 //
 // Bound by the weight's bytes and, below about 10 MB, by the 3.5 us that a launch
 // takes from its first load to its last store.  4096 -> 14336 (58.7 MB, 8.7 us at
-// 6.79 TB/s): 12.3 us for one token, 12.8 for 16, 14.1 for 64, 17.6 for 128, where
+// 6.79 TB/s): 12.1 us for one token, 12.4 for 16, 14.4 for 64, 17.5 for 128, where
 // every CTA reads all the tokens again (117 MB through L2; without any adding up
-// 15.6 us); 4096 -> 4096 (2.5 us): 6.1, 6.6, 7.3 and 9.3; 4096 -> 1024: 4.0 for
+// 15.6 us); 4096 -> 4096 (2.5 us): 5.9, 6.2, 7.1 and 9.4; 4096 -> 1024: 3.8 for
 // one.
 //
 // Warp roles: 0 loads (TMA), 1 issues the MMAs, 2 multiplies the scales, from
@@ -126,6 +126,16 @@ __global__ void __launch_bounds__(Few<NT>::THREADS, NT <= 64 ? 2 : 1)
   __syncthreads();
   if (splits > 1) cluster_arrive();   // waited for before the first remote store
   tc_fence_after_sync();
+  // While the kernel before still runs, the weight's first blocks are asked for
+  // as far as L2.  (L2 is where all writes meet: were that kernel writing them,
+  // the loads after the wait would still find what it wrote.)  One token, norm,
+  // 4096 -> 14336, quantiser, 14336 -> 4096: 28.6 -> 27.9 us; of up to 128 tokens
+  // four blocks gain more than half the share (64 tokens: 32.0 and 32.6).
+  if (warp == 0 && lane == 0) {
+    const int ahead = NT <= 16 ? max(4, (ke - kb) / 2) : 4;
+    for (int k = kb; k < min(ke, kb + ahead); ++k)
+      tma_prefetch_l2_2d(&a.b, DGRAD ? tile * 128 : k * 128, DGRAD ? k * 128 : tile * 128);
+  }
   grid_dependency_wait();
   const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(gbase + T::OFF_TMEM);
 

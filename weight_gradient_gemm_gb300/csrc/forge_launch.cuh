@@ -9,7 +9,9 @@
 // its time before the wait included.)  grid_dependency_trigger() lets the next such kernel start
 // its own set-up; it comes where a block needs nothing more that a waiting
 // block could hold (its tensor memory is allocated, its loads are issued).
-// One token through a linear layer, calls back to back: 14.5 -> 12.8 us.
+// One token through a linear layer, calls back to back: 14.5 -> 12.8 us.  Small
+// norms and quantisers trigger right after their own wait (a layer's four kernels
+// on one token: 30.5 -> 28.6 us).
 #pragma once
 
 #include <cuda_runtime.h>

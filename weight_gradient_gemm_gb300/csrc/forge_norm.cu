@@ -29,6 +29,13 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
   return warp_sum(lane < nw ? red[lane] : 0.0f);
 }
 
+// Fewer blocks than SMs: the next kernel can set up beside them at once (and the
+// products for few tokens begin to read their weight).  Not for more: its blocks
+// would take places unevenly (a backward pass of 1000 x 2048 6.8 -> 11.8 us).
+__device__ __forceinline__ void early_trigger() {
+  if (gridDim.x <= 128) grid_dependency_trigger();
+}
+
 __device__ __forceinline__ void load_gain8(const void* gain, int bf16, int v, float (&g)[8]) {
   if (bf16) {
     unpack8(reinterpret_cast<const uint4*>(gain)[v], g);
@@ -137,6 +144,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) rmsnorm_kernel(const NormAr
   const int64_t step = WARP ? static_cast<int64_t>(gridDim.x) * 8 : gridDim.x;
   int parity = 0;
   grid_dependency_wait();
+  early_trigger();
   for (int64_t row = first; row < a.rows; row += step, parity ^= 1) {
     const int64_t base = row * nvec;
     uint4 x[VPT], r[VPT];
@@ -592,6 +600,7 @@ __global__ void __launch_bounds__(256) quantize_blocks_kernel(const uint4* __res
       (lane >> 3);
   uint4 v[kQuantUnroll][2];
   grid_dependency_wait();
+  early_trigger();
 #pragma unroll
   for (int j = 0; j < kQuantUnroll; ++j) {
     const int64_t b = b0 + 4 * j;
@@ -624,6 +633,7 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const uint4* __restr
   const int nblk = (nvec + 15) / 16, sub = threadIdx.x & 7;
   const int64_t total = rows * nblk, groups = static_cast<int64_t>(gridDim.x) * 32;
   grid_dependency_wait();
+  early_trigger();
   // every lane of a warp takes the same number of trips (the shuffles)
   for (int64_t b0 = static_cast<int64_t>(blockIdx.x) * 32 + ((threadIdx.x >> 5) << 2); b0 < total;
        b0 += groups) {

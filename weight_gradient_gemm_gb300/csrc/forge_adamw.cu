@@ -5,10 +5,13 @@
 // kernel", Appendix E; "store-G control" plus update, Appendix D).
 //
 // An HBM-streaming kernel: grid-stride over 16-byte vectors, loads and stores
-// marked streaming (each byte is touched once).
+// marked streaming (each byte is touched once).  Its launches are chained
+// (forge_launch.cuh): the clipped step of three small matrices and three vectors,
+// norm and coefficient included, 18.3 -> 13.0 us.
 #include <cuda_bf16.h>
 
 #include "forge_internal.h"
+#include "forge_launch.cuh"
 
 namespace forge {
 
@@ -36,7 +39,7 @@ __device__ __forceinline__ void load_grad8(const void* dW, int64_t i8, float gs,
 
 // The clipping coefficient of a step: a device word, or 1 without one.
 __device__ __forceinline__ float grad_scale(const float* coef) {
-  return coef ? __ldg(coef) : 1.0f;
+  return coef ? __ldcg(coef) : 1.0f;
 }
 
 // fp32 or bf16 moments: one thread per 8 consecutive elements.
@@ -47,6 +50,7 @@ __global__ void __launch_bounds__(256) adamw_vec8_kernel(const void* __restrict_
                                                          void* __restrict__ v, int64_t n8,
                                                          const AdamWConsts h,
                                                          const float* __restrict__ coef) {
+  grid_dependency_wait();
   const float gs = grad_scale(coef);
   const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n8;
@@ -120,6 +124,7 @@ __global__ void __launch_bounds__(256) adamw_int8_kernel(const void* __restrict_
                                                          float* __restrict__ v_scale,
                                                          int64_t nblocks, const AdamWConsts h,
                                                          const float* __restrict__ coef) {
+  grid_dependency_wait();
   const float gs = grad_scale(coef);
   const int lane = threadIdx.x & 31;
   const int64_t warps = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
@@ -192,6 +197,7 @@ __global__ void __launch_bounds__(256) adamw_fp8_kernel(const void* __restrict__
                                                         float* __restrict__ r_words,
                                                         int64_t n16, const AdamWConsts h,
                                                         const float* __restrict__ coef) {
+  grid_dependency_wait();
   const float gs = grad_scale(coef);
   const Fp8Step fm = fp8_step_of(m_words), fr = fp8_step_of(r_words);
   float amax_m = 0.0f, amax_r = 0.0f;
@@ -247,19 +253,17 @@ cudaError_t launch_fp8_roll(float* words, int n, int stride, float headroom,
 template <int FMT, int DW>
 static cudaError_t launch_vec8(const void* dW, void* W, void* m, void* v, int64_t n, int grid,
                                const AdamWConsts& h, const float* coef, cudaStream_t stream) {
-  adamw_vec8_kernel<FMT, DW><<<grid, 256, 0, stream>>>(dW, static_cast<uint16_t*>(W), m, v, n / 8,
-                                                      h, coef);
-  return cudaGetLastError();
+  return launch_chained(adamw_vec8_kernel<FMT, DW>, grid, 256, 0, 0, stream, dW,
+                        static_cast<uint16_t*>(W), m, v, n / 8, h, coef);
 }
 
 template <int DW>
 static cudaError_t launch_i8(const void* dW, void* W, void* m, void* v, float* ms, float* vs,
                              int64_t n, int grid, const AdamWConsts& h, const float* coef,
                              cudaStream_t stream) {
-  adamw_int8_kernel<DW><<<grid, 256, 0, stream>>>(dW, static_cast<uint16_t*>(W),
-                                                 static_cast<int8_t*>(m), static_cast<int8_t*>(v),
-                                                 ms, vs, n / 128, h, coef);
-  return cudaGetLastError();
+  return launch_chained(adamw_int8_kernel<DW>, grid, 256, 0, 0, stream, dW,
+                        static_cast<uint16_t*>(W), static_cast<int8_t*>(m),
+                        static_cast<int8_t*>(v), ms, vs, n / 128, h, coef);
 }
 
 cudaError_t launch_adamw(const void* dW, int dw_fmt, void* W, void* m, void* v, float* m_scale,
@@ -275,12 +279,15 @@ cudaError_t launch_adamw(const void* dW, int dw_fmt, void* W, void* m, void* v, 
     auto* Wp = static_cast<uint16_t*>(W);
     auto* mp = static_cast<uint8_t*>(m);
     auto* vp = static_cast<uint8_t*>(v);
+    auto go = [&](auto kern) {
+      return launch_chained(kern, grid, 256, 0, 0, stream, dW, Wp, mp, vp, m_scale, v_scale, n16, h,
+                            coef);
+    };
     switch (dw) {
-      case 0: adamw_fp8_kernel<0><<<grid, 256, 0, stream>>>(dW, Wp, mp, vp, m_scale, v_scale, n16, h, coef); break;
-      case 1: adamw_fp8_kernel<1><<<grid, 256, 0, stream>>>(dW, Wp, mp, vp, m_scale, v_scale, n16, h, coef); break;
-      default: adamw_fp8_kernel<2><<<grid, 256, 0, stream>>>(dW, Wp, mp, vp, m_scale, v_scale, n16, h, coef); break;
+      case 0: return go(adamw_fp8_kernel<0>);
+      case 1: return go(adamw_fp8_kernel<1>);
+      default: return go(adamw_fp8_kernel<2>);
     }
-    return cudaGetLastError();
   }
   if (fmt == kFmtI8) {
     const int64_t nb = n / 128;

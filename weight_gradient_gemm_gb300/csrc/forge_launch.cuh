@@ -1,8 +1,9 @@
 // Launches whose set-up overlaps the end of the kernel before them in the
 // stream (programmatic stream serialization).
 //
-// A kernel launched this way calls grid_dependency_wait() before it touches
-// anything in global memory; that returns once every kernel it follows has
+// A kernel launched this way calls grid_dependency_wait() before it reads or
+// writes anything in global memory (it may ask for data as far as L2, where all
+// writes meet); that returns once every kernel it follows has
 // finished and its writes are visible, so the order of results is that of an
 // ordinary launch.  (What other kernels write is read with plain or L2 loads:
 // the read-only path assumes data that does not change while the kernel runs,

@@ -556,6 +556,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_dgain_kernel(const float* __rest
   const int lane = threadIdx.x & 31, run = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   grid_dependency_wait();
+  early_trigger();
   float s = 0.0f;
   if (c < cols) {
 #pragma unroll 8

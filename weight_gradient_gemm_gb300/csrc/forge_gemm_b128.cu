@@ -104,6 +104,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* gbase = smem_raw + (base - raw);
   if (base - raw + T::SMEM_USED > T::SMEM_ALLOC) {   // uniform: nothing has started
+    grid_dependency_wait();   // the launch after this one may rely on those before it
     if (threadIdx.x == 0) atomicCAS(a.err, 0, kErrDeviceConfig);
     return;
   }

@@ -89,7 +89,8 @@ def test_rmsnorm(rows, cols, res, gain_dtype):
     check_codes(codes, scales, y64, 1, yrel, np.zeros_like(y64))
 
 
-@pytest.mark.parametrize("rows,cols", [(400, 4096), (310, 4104), (1200, 1032), (200, 8200)])
+@pytest.mark.parametrize("rows,cols", [(400, 4096), (310, 4104), (1200, 1032), (200, 8200),
+                                       (2500, 1024), (2000, 1024), (2600, 520), (1217, 768)])
 @pytest.mark.parametrize("res", [False, True])
 def test_rmsnorm_more_rows_than_one_wave(rows, cols, res):
     test_rmsnorm(rows, cols, res, torch.bfloat16)
@@ -173,7 +174,8 @@ def test_rmsnorm_backward(rows, cols, with_dsum, gain_dtype):
 
 
 @pytest.mark.parametrize("rows,cols", [(1500, 1032), (800, 520), (2100, 512), (1024, 4096),
-                                       (2000, 2048), (400, 8192), (320, 16384), (305, 14336)])
+                                       (2000, 2048), (400, 8192), (320, 16384), (305, 14336),
+                                       (2000, 1024), (1281, 1032), (769, 520), (2049, 256)])
 @pytest.mark.parametrize("with_dsum", [False, True])
 def test_rmsnorm_backward_between_one_wave_and_many(rows, cols, with_dsum):
     test_rmsnorm_backward(rows, cols, with_dsum, torch.float32)

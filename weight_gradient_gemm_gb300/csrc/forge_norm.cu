@@ -50,7 +50,7 @@ __device__ __forceinline__ void load_gain8(const void* gain, int bf16, int v, fl
 // A row's columns are cut into vectors of 8; thread t of a row's `width`
 // threads owns the vectors t, t + width, ..., so 16 neighbouring lanes hold the
 // 128 columns of a scale.  Three ways to walk the rows share the arithmetic:
-//   a warp per row (up to 1024 columns): no barrier at all;
+//   a warp per row (up to 512 columns): no barrier at all;
 //   a block per row: few rows, where every row is in flight at once;
 //   persistent blocks whose rows are copied ahead into shared memory (many
 //   rows): the copies keep HBM busy through the reductions.
@@ -60,7 +60,8 @@ __device__ __forceinline__ void load_gain8(const void* gain, int bf16, int v, fl
 //   8191 x 4096, x + residual -> sum, y       43.7 us (39.5)
 //   the same with codes and scales            50.3 us (44.6)
 //   8192 x 8192                               89.7 us (79.1)
-//   8192 x 1024 (a warp per row)              13.1 us (9.9)
+//   8192 x 1024                               12.4 us (9.9)
+//   8192 x 512 (a warp per row)                7.4 us (4.9)
 //   512 x 4096 (a block per row)               4.6 us (2.5), launch and tail
 //   1 x 4096                                   1.9 us: the latency of a launch,
 //                                              the loads and one reduction
@@ -744,10 +745,10 @@ struct RowPlan {
   int lanes;                      // and the lanes that hold a row's columns there
 };
 
-// A warp per row up to 1024 columns (backward 512, whose registers hold the
-// gain's gradient besides).  Above, the stream for rows enough to fill its
-// persistent blocks twice, while a ring of two rows fits (else a block per
-// row).  Blocks of about 1024 threads in all share an SM.
+// A warp per row up to 512 columns (8192 x 768 with codes: 14.9 us so, 11.3
+// through the stream).  Above, the stream for rows enough to fill its persistent
+// blocks twice, while a ring of two rows fits (else a block per row).  Blocks of
+// about 1024 threads in all share an SM.
 //
 // (Whether dgain is asked for changes nothing here, so dX has the same bits.)
 // The backward pass adds up dgain in the same launch while a run of lanes has at
@@ -756,13 +757,14 @@ struct RowPlan {
 // 333 x 1032 5.7 and 2.6 us, 512 x 4096 9.5 and 6.5, 1024 x 4096 12.4 and 9.8,
 // 2048 x 4096 17.0 and 15.7; 2000 x 8192 28.8 and 31.2.  Up to 2048 columns
 // two lanes a row, for more column blocks (1000 x 2048: 7.0 us, 9.2 with four;
-// 2048 x 4096 16.6 and 15.7).
+// 2048 x 4096 16.6 and 15.7).  More rows take the stream (2000 x 1024: 10.2 us,
+// 12.6 with a few blocks that read as they go).
 constexpr int64_t kDirectValues = 1 << 23;
 RowPlan row_plan(int64_t rows, int cols, int streams, bool backward, int num_sms) {
   RowPlan p{kWalkBlock, 1, 0, 0, 0, false, cols <= 2048 ? 2 : 4};
-  if (cols <= (backward ? 512 : 1024)) {
+  if (cols <= 512) {
     p.walk = kWalkWarp;
-    p.vpt = cols <= 256 ? 1 : (cols <= 512 ? 2 : 4);
+    p.vpt = cols <= 256 ? 1 : 2;
     p.threads = 256;
     p.direct = backward && rows <= 16 * p.threads / p.lanes;
     const int64_t want = (rows + 7) / 8, most = static_cast<int64_t>(num_sms) * 4;
@@ -776,15 +778,16 @@ RowPlan row_plan(int64_t rows, int cols, int streams, bool backward, int num_sms
   const int64_t direct_rows = 16 * p.threads / p.lanes;
   p.direct = backward && rows <= direct_rows && rows * cols <= kDirectValues;
   p.smem = kRing * (streams * cols * 2 + 8) + 8;
-  if (!p.direct && p.vpt <= 2 && p.smem * per_sm <= 222 * 1024 && rows >= 2 * per_sm * num_sms) {
+  const bool many = rows >= 2 * per_sm * num_sms || (backward && rows > direct_rows);
+  if (!p.direct && many && p.vpt <= 2 && p.smem * per_sm <= 222 * 1024) {
     p.walk = kWalkStream;
-    p.grid = per_sm * num_sms;
+    p.grid = static_cast<int>(rows < per_sm * num_sms ? rows : per_sm * num_sms);
     return p;
   }
   // Every row in flight at once: where a vector a thread leaves rows for a second
   // wave, two vectors and half the threads (512 x 4096: 4.6 us, 5.8 with one
-  // vector; 304 rows the same, 152 rows 3.0 and 2.8).  The backward pass's sums
-  // want few blocks (1000 x 1032 with two vectors 11.0 us, 8.9 with one).
+  // vector; 304 rows the same, 152 rows 3.0 and 2.8).  Where the backward pass
+  // leaves partial rows, few blocks.
   p.direct = backward && rows <= direct_rows;
   if ((!backward || p.direct) && p.vpt == 1 && rows > per_sm * num_sms) {
     p.vpt = 2;
@@ -833,8 +836,7 @@ cudaError_t launch_rmsnorm(const NormArgs& a, int num_sms, cudaStream_t stream) 
   }
   auto go = [&](auto kern) { return launch_chained(kern, p.grid, p.threads, 0, 0, stream, a); };
   if (p.walk == kWalkWarp)
-    return p.vpt == 1 ? go(rmsnorm_kernel<1, true>)
-                      : (p.vpt == 2 ? go(rmsnorm_kernel<2, true>) : go(rmsnorm_kernel<4, true>));
+    return p.vpt == 1 ? go(rmsnorm_kernel<1, true>) : go(rmsnorm_kernel<2, true>);
   return p.vpt == 1 ? go(rmsnorm_kernel<1, false>)
                     : (p.vpt == 2 ? go(rmsnorm_kernel<2, false>) : go(rmsnorm_kernel<4, false>));
 }
@@ -874,9 +876,7 @@ cudaError_t launch_rmsnorm_bwd(const NormBwdArgs& a, int num_sms, cudaStream_t s
       e = p.vpt == 1 ? go(rmsnorm_bwd_kernel<1, true, false>)
                      : go(rmsnorm_bwd_kernel<2, true, false>);
     else
-      // (rows of 8200 to 16384 columns go direct or through the stream)
-      e = p.vpt == 1 ? go(rmsnorm_bwd_kernel<1, false, false>)
-                     : go(rmsnorm_bwd_kernel<4, false, false>);
+      e = go(rmsnorm_bwd_kernel<4, false, false>);   // up to 16384 columns: direct or the stream
   }
   if (e != cudaSuccess || !a.dgain) return e;
   return launch_chained(rmsnorm_dgain_kernel, (a.cols + 31) / 32, 1024, 0, 0, stream,

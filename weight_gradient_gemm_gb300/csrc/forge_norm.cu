@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(1024, 1) rmsnorm_stream_kernel(const NormArgs 
 //   (from L2) and add down 16 or 32 columns; one launch;
 //   many rows: a block adds its rows in registers and leaves one partial row,
 //   and rmsnorm_dgain_kernel adds those.
-// Bound by memory: 8192 x 4096 with dsum, 268 MB, 47.1 us with the second
+// Bound by memory: 8192 x 4096 with dsum, 268 MB, 46.5 us with the second
 // launch (39.5 at the copy rate; a block per row 71); 512 x 4096 6.5 us (2.5),
 // 333 x 1032 2.6 us, 1 x 4096 1.8.
 // One vector's share of the row's dot product; dgain's terms are added to dg.
@@ -548,25 +548,35 @@ __global__ void __launch_bounds__(1024, 1)
   ring.finish();
 }
 
-// dgain[c] = sum over the blocks' partial rows: 32 columns a block, 32 runs of
-// rows side by side, added in a fixed order.
+// dgain[c] = sum over the blocks' partial rows: W columns a block, 1024 / W runs of
+// rows side by side, added in a fixed order.  16 columns up to 1024, where 32
+// leave most SMs without a block (the whole backward pass of 8192 x 1024 17.3 us
+// with 32, 16.0 with 16; of 8192 x 256 8.7 and 7.8).
+template <int W>
 __global__ void __launch_bounds__(1024) rmsnorm_dgain_kernel(const float* __restrict__ part,
                                                              int blocks, int cols,
                                                              float* __restrict__ dgain) {
-  __shared__ float sum[32][33];
-  const int lane = threadIdx.x & 31, run = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + lane;
+  constexpr int RUNS = 1024 / W;
+  __shared__ float sum[RUNS][W + 1];
+  const int col = threadIdx.x % W, run = threadIdx.x / W;
+  const int c = blockIdx.x * W + col;
   grid_dependency_wait();
   early_trigger();
   float s = 0.0f;
   if (c < cols) {
 #pragma unroll 8
-    for (int b = run; b < blocks; b += 32) s += __ldcg(part + static_cast<int64_t>(b) * cols + c);
+    for (int b = run; b < blocks; b += RUNS)
+      s += __ldcg(part + static_cast<int64_t>(b) * cols + c);
   }
-  sum[run][lane] = s;
+  sum[run][col] = s;
   __syncthreads();
-  s = warp_sum(sum[lane][run]);   // column `run` of the block: lane is the run of rows
-  if (lane == 0 && blockIdx.x * 32 + run < cols) dgain[blockIdx.x * 32 + run] = s;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;   // a warp a column
+  if (warp >= W || blockIdx.x * W + warp >= cols) return;
+  s = 0.0f;
+#pragma unroll
+  for (int r = 0; r < RUNS; r += 32) s += sum[r + lane][warp];
+  s = warp_sum(s);
+  if (lane == 0) dgain[blockIdx.x * W + warp] = s;
 }
 
 // Largest magnitude of eight bf16 values; NaN if one of them is.
@@ -879,8 +889,11 @@ cudaError_t launch_rmsnorm_bwd(const NormBwdArgs& a, int num_sms, cudaStream_t s
       e = go(rmsnorm_bwd_kernel<4, false, false>);   // up to 16384 columns: direct or the stream
   }
   if (e != cudaSuccess || !a.dgain) return e;
-  return launch_chained(rmsnorm_dgain_kernel, (a.cols + 31) / 32, 1024, 0, 0, stream,
-                        static_cast<const float*>(a.part), p.grid, a.cols, a.dgain);
+  auto join = [&](auto kern, int w) {
+    return launch_chained(kern, (a.cols + w - 1) / w, 1024, 0, 0, stream,
+                          static_cast<const float*>(a.part), p.grid, a.cols, a.dgain);
+  };
+  return a.cols <= 1024 ? join(rmsnorm_dgain_kernel<16>, 16) : join(rmsnorm_dgain_kernel<32>, 32);
 }
 
 cudaError_t launch_quantize_b128(const uint16_t* x, uint8_t* codes, float* scales, int64_t rows,

@@ -282,15 +282,17 @@ PyObject* adamw_clip(PyObject*, PyObject* const* a, Py_ssize_t n) {
     for (int i = 0; i < 5; ++i) h[i] = static_cast<float>(c.number(5 + i));
     const int64_t step = c.integer(10);
     void* st = c.stream(11);
+    const forge_moment_fmt fmt = mt == FORGE_DT_FP32 ? FORGE_MOM_FP32 : FORGE_MOM_BF16;
     return FORGE_CALL(lib.adamw_clip(g, gt, coef + 1, wp, forge_moment{m, nullptr},
                                      forge_moment{v, nullptr}, d_in, d_out, h[0], h[1], h[2], h[3],
-                                     h[4], step, mt == FORGE_DT_FP32 ? FORGE_MOM_FP32 : FORGE_MOM_BF16,
-                                     st));
+                                     h[4], step, fmt, st));
   });
 }
 
 using FastFn = PyObject* (*)(PyObject*, PyObject* const*, Py_ssize_t);
-PyCFunction fast(FastFn f) { return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)); }
+PyCFunction fast(FastFn f) {
+  return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f));
+}
 
 PyMethodDef methods[] = {{"bind", fast(bind), METH_FASTCALL, nullptr},
                          {"rmsnorm", fast(rmsnorm), METH_FASTCALL, nullptr},

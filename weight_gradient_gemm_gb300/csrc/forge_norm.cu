@@ -93,7 +93,8 @@ __device__ __forceinline__ float norm_rstd(const NormArgs& a, float ss) {
 // One vector's outputs.  Every lane of the warp takes part (the shuffles);
 // `in` is false past the row's end.
 __device__ __forceinline__ void norm_out(const NormArgs& a, const float (&h)[8],
-                                         const float (&g)[8], float rstd, int64_t row, int v, bool in) {
+                                         const float (&g)[8], float rstd, int64_t row, int v,
+                                         bool in) {
   const int64_t at = row * (a.cols / 8) + v;
   if (a.y && in) {
     float y[8];
@@ -676,8 +677,8 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const uint4* __restr
 // reduction's barrier and runs under the codes and stores.  14336 x 4096: 28.9 us,
 // 6.1 TB/s (33.2 us with loads into registers, where a CTA's loads, barrier and
 // stores follow one another; more copies in flight only meet the stores: two
-// slots, three CTAs an SM, 29.9 us); 4096 x 4096 9.6 us (11.6); 1000 x 4112 4.1.  A wait that runs out records its error and
-// lets the CTA run on, as in RowRing.
+// slots, three CTAs an SM, 29.9 us); 4096 x 4096 9.6 us (11.6); 1000 x 4112 4.1.
+// A wait that runs out records its error and lets the CTA run on, as in RowRing.
 constexpr int kTileBytes = kBlock * kBlock * 2;
 __global__ void __launch_bounds__(256)
     quantize_tiles_kernel(const __grid_constant__ CUtensorMap x, uint8_t* __restrict__ codes,
@@ -881,7 +882,9 @@ cudaError_t launch_rmsnorm_bwd(const NormBwdArgs& a, int num_sms, cudaStream_t s
                       : (p.vpt == 2 ? go(rmsnorm_bwd_kernel<2, false, true>)
                                     : go(rmsnorm_bwd_kernel<4, false, true>));
   } else {
-    auto go = [&](auto kern) { return launch_chained(kern, p.grid, p.threads, 0, 0, stream, a, 0, 0); };
+    auto go = [&](auto kern) {
+      return launch_chained(kern, p.grid, p.threads, 0, 0, stream, a, 0, 0);
+    };
     if (p.walk == kWalkWarp)
       e = p.vpt == 1 ? go(rmsnorm_bwd_kernel<1, true, false>)
                      : go(rmsnorm_bwd_kernel<2, true, false>);
@@ -916,7 +919,8 @@ cudaError_t launch_quantize_b128(const uint16_t* x, uint8_t* codes, float* scale
   if (!host_map(&map, x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, cols, rows, cols * 2, kBlock, kBlock,
                 CU_TENSOR_MAP_SWIZZLE_NONE))
     return cudaErrorInvalidValue;
-  const int64_t blocks = (rows + kBlock - 1) / kBlock * nblk, most = static_cast<int64_t>(num_sms) * 4;
+  const int64_t blocks = (rows + kBlock - 1) / kBlock * nblk;
+  const int64_t most = static_cast<int64_t>(num_sms) * 4;
   return launch_chained(quantize_tiles_kernel, static_cast<unsigned>(blocks < most ? blocks : most),
                         256, kTileBytes, 0, stream, map, codes, scales, rows, cols, blocks, wait);
 }

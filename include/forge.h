@@ -506,9 +506,13 @@ forge_status forge_fp8_roll_scales(forge_fp8_scales* scales, int n, float headro
  * and 128 columns (block_rows 1, scales [rows, ceil(cols/128)]); weights one
  * per 128 x 128 block (block_rows 128, scales [ceil(rows/128),
  * ceil(cols/128)]).  The last blocks may be partial.  A block whose largest
- * magnitude is a > 0 has scale max(a / 448, 2^-126) and codes x / scale
- * rounded to nearest even; an all-zero block has scale 0 and codes 0; a block
- * that holds a NaN or an infinity decodes to NaN throughout.
+ * magnitude is a > 0 has scale s = max(a / 448, 2^-126), stored rounded to
+ * fp32, and codes x / s rounded to nearest even; an all-zero block has scale 0
+ * and codes 0; a block that holds a NaN or an infinity decodes to NaN
+ * throughout.  forge_quantize_b128 rounds the quotient by the unrounded s, so
+ * its codes are exactly these; forge_rmsnorm's x is an fp32 result itself, and
+ * where it lies within a few 2^-24 of halfway between two codes either may be
+ * taken.
  */
 
 /*

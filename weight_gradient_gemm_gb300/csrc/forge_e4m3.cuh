@@ -61,6 +61,41 @@ __device__ __forceinline__ uint2 encode8(const float (&x)[8], float inv) {
   return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
+// The same for bf16 values of a block whose amax is bf16 too, with the codes of
+// the true quotients 448 x / amax, ties to even.  Such a quotient is a tie
+// between two codes or at least 2^-13 of itself away from one (8-bit
+// significands, ties of 5 bits), but x * inv is up to 2 ulp off and falls on
+// either side of a tie.  With 448 / amax as inv + lo the product is right to
+// 2^-40 before its rounding, and a tie comes out as the tie.  lo >= 0, so that a
+// zero keeps its sign.  Measured, without and with lo: 8192 x 14336 51.7 and
+// 51.8 us, 8192 x 4104 19.8 and 20.2, 4096 x 4096 in 128 x 128 blocks 9.9 and 10.0.
+struct QuotientScale {
+  float scale, inv, lo;
+};
+__device__ __forceinline__ QuotientScale quotient_scale(float amax) {
+  QuotientScale s{amax, amax, 0.0f};
+  if (amax > 0.0f) {
+    s.scale = fmaxf(__fdiv_rn(amax, kE4m3Max), 0x1p-126f);
+    float inv = fminf(__fdiv_rn(kE4m3Max, amax), 0x1p126f);
+    // rounded down: the remainder 448 - inv amax, exact, is not negative
+    if (fmaf(-inv, amax, kE4m3Max) < 0.0f) inv = __uint_as_float(__float_as_uint(inv) - 1u);
+    const float lo = fmaf(-inv, amax, kE4m3Max) * (inv * (1.0f / kE4m3Max));
+    s.inv = inv;
+    s.lo = inv < 0x1p126f ? lo : 0.0f;
+  }
+  return s;
+}
+__device__ __forceinline__ uint2 encode8(const float (&x)[8], const QuotientScale& s) {
+  uint32_t c[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 v = make_float2(x[2 * k], x[2 * k + 1]);
+    const float2 q = fma2(v, dup2(s.inv), mul2(v, dup2(s.lo)));
+    c[k] = float2_to_e4m3x2(q.x, q.y);
+  }
+  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+}
+
 __device__ __forceinline__ void unpack8(uint4 v, float (&f)[8]) {
   const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll

@@ -590,8 +590,8 @@ __device__ __forceinline__ float amax8(uint4 v) {
   return max_nan(__low2float(m), __high2float(m));
 }
 
-// The quantisers: per block s = amax / 448, codes = x / s rounded to e4m3.  One
-// pass; a block stays in registers between its maximum and its codes.
+// The quantisers: per block s = amax / 448, codes = 448 x / amax rounded to e4m3.
+// One pass; a block stays in registers between its maximum and its codes.
 //
 // Blocks of 1 x 128: 8 lanes per block, two vectors of 8 columns a lane, so
 // that one reduction and one pair of divisions serve 16 of a lane's values.
@@ -626,13 +626,13 @@ __global__ void __launch_bounds__(256) quantize_blocks_kernel(const uint4* __res
 #pragma unroll
   for (int j = 0; j < kQuantUnroll; ++j) {
     const int64_t b = b0 + 4 * j;
-    const BlockScale s = block_scale(max8(max_nan(amax8(v[j][0]), amax8(v[j][1]))));
+    const QuotientScale s = quotient_scale(max8(max_nan(amax8(v[j][0]), amax8(v[j][1]))));
     if (b < blocks) {
       float f[8];
       unpack8(v[j][0], f);
-      __stcs(codes + b * 16 + sub, encode8(f, s.inv));
+      __stcs(codes + b * 16 + sub, encode8(f, s));
       unpack8(v[j][1], f);
-      __stcs(codes + b * 16 + 8 + sub, encode8(f, s.inv));
+      __stcs(codes + b * 16 + 8 + sub, encode8(f, s));
       if (sub == 0) scales[b] = s.scale;
     }
   }
@@ -657,15 +657,15 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const uint4* __restr
     const int64_t at = row * nvec + vec;
     const uint4 v0 = in0 ? __ldcs(x + at) : make_uint4(0, 0, 0, 0);
     const uint4 v1 = in1 ? __ldcs(x + at + 8) : make_uint4(0, 0, 0, 0);
-    const BlockScale s = block_scale(max8(max_nan(amax8(v0), amax8(v1))));
+    const QuotientScale s = quotient_scale(max8(max_nan(amax8(v0), amax8(v1))));
     float f[8];
     if (in0) {
       unpack8(v0, f);
-      __stcs(codes + at, encode8(f, s.inv));
+      __stcs(codes + at, encode8(f, s));
     }
     if (in1) {
       unpack8(v1, f);
-      __stcs(codes + at + 8, encode8(f, s.inv));
+      __stcs(codes + at + 8, encode8(f, s));
     }
     if (in0 && sub == 0) scales[b] = s.scale;
   }
@@ -721,7 +721,7 @@ __global__ void __launch_bounds__(256)
     if (threadIdx.x == 0 && ok && b + gridDim.x < blocks) load(b + gridDim.x);
 #pragma unroll
     for (int q = 0; q < 8; ++q) amax = max_nan(amax, red[ph][q]);
-    const BlockScale s = block_scale(amax);
+    const QuotientScale s = quotient_scale(amax);
     const int64_t col = b % nblk * kBlock + (threadIdx.x & 15) * 8;
     const int64_t row0 = b / nblk * kBlock + (threadIdx.x >> 4);
 #pragma unroll
@@ -729,7 +729,7 @@ __global__ void __launch_bounds__(256)
       if (col < cols && row0 + 16 * i < rows) {
         float f[8];
         unpack8(v[i], f);
-        __stcs(reinterpret_cast<uint2*>(codes + (row0 + 16 * i) * cols + col), encode8(f, s.inv));
+        __stcs(reinterpret_cast<uint2*>(codes + (row0 + 16 * i) * cols + col), encode8(f, s));
       }
     if (threadIdx.x == 0) scales[b] = s.scale;
   }

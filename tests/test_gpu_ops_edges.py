@@ -1,5 +1,5 @@
 """The operators around the weight gradient where they can go wrong: ties between
-two codes, against their fp64 definitions (oracle/ops.py)."""
+two codes and scales far apart, against their fp64 definitions (oracle/ops.py)."""
 import numpy as np
 import pytest
 import torch
@@ -63,3 +63,76 @@ def test_quantize_rounds_every_quotient_to_the_nearest_code(block_rows, power):
         held = a < 448 * 2.0 ** -126                 # the scale is 2^-126
         bad = f64(codes) != R.e4m3_round(np.where(held, part * 2.0 ** 126, part * 448 / a))
         assert not bad.any(), int(bad.sum())
+
+
+# ---------------------------------------------------------------- products
+def product_case(seed, op, bt, d_in, d_out, codes=256):
+    """Random operands of one product: code bytes below `codes` (with both signs) and
+    scales around one; the call, and its reference from the codes and scales given."""
+    g = torch.Generator().manual_seed(seed)
+    k, n = (d_in, d_out) if op == "linear" else (d_out, d_in)
+
+    def matrix(rows, cols, block_rows):
+        c = torch.randint(0, min(codes, 128), (rows, cols), generator=g, dtype=torch.uint8)
+        c |= torch.randint(0, 2, (rows, cols), generator=g, dtype=torch.uint8) << 7
+        c[(c & 0x7F) == 0x7F] = 0x30           # no NaN
+        sr = rows if block_rows == 1 else -(-rows // 128)
+        s = torch.exp2(torch.randn((sr, -(-cols // 128)), generator=g))
+        return c.view(torch.float8_e4m3fn), s.float()
+
+    return matrix(bt, k, 1), matrix(d_out, d_in, 128), k, n
+
+
+def check(op, a, sa, w, sw, k, n, dtype=torch.float32):
+    out = torch.empty((a.shape[0], n), dtype=dtype, device=DEV)
+    call = F.linear_fp8 if op == "linear" else F.dgrad_fp8
+    call(a.to(DEV), sa.to(DEV), w.to(DEV), sw.to(DEV), out)
+    ok()
+    a64, w64 = R.dequantize(f64(a), f64(sa), 1), R.dequantize(f64(w), f64(sw), 128)
+    if op == "linear":
+        w64 = w64.T
+    a64, w64 = (torch.from_numpy(np.ascontiguousarray(t)).to(DEV) for t in (a64, w64))
+    ref, mag = a64 @ w64, a64.abs() @ w64.abs()
+    # inside a block the tensor core adds 128 exact products in groups, at most 4
+    # alignments of 2^-23 of the partial sums' magnitude and the groups' own;
+    # outside, one product and one addition per block; below 2^-126 a step is 2^-149
+    nb = -(-k // 128)
+    tol = (18 + nb) * 2.0 ** -23 * mag + (nb + 1) * 2.0 ** -149
+    if dtype == torch.bfloat16:
+        tol = tol + (2.0 ** -8 + 2.0 ** -24) * ref.abs()
+    bad = ~((out.double() - ref).abs() <= tol)
+    assert not bad.any(), (int(bad.sum()), float((out.double() - ref).abs()[bad].max()))
+    return out
+
+
+# the forms of the products: up to 16, 32, 64 and 128 tokens, with the reduction on
+# one CTA and on several, tiles of one CTA and of a pair
+FORMS = [(3, {}), (3, dict(splits=1)), (30, {}), (50, {}), (100, dict(splits=2)), (200, {}),
+         (300, dict(cg=2))]
+
+
+@pytest.mark.parametrize("op", ["linear", "dgrad"])
+@pytest.mark.parametrize("bt,how", FORMS)
+@pytest.mark.parametrize("case", ["tiny", "huge", "rising", "rising_to_huge"])
+def test_products_of_scales_outside_fp32(tune, op, bt, how, case):
+    # each scale is one the format allows, and so is the result; their product is not
+    tune(**how)
+    d_in, d_out = 2576, 2320
+    small = case in ("huge", "rising_to_huge")       # sums of 2^-10: codes below 2^-6
+    (a, sa), (w, sw), k, n = product_case(90, op, bt, d_in, d_out, 8 if small else 256)
+    if case == "tiny":          # sums up to 2^20 times 2^-140
+        sa, sw = sa * 2.0 ** -110, sw * 2.0 ** -30
+    elif case == "huge":        # times 2^127
+        sa, sw = sa * 2.0 ** 85, sw * 2.0 ** 42
+    elif case == "rising":      # empty blocks, then products on both sides of 2^-90
+        a.view(torch.uint8)[:, :3 * 128] = 0
+        sa[:, :3] = 0
+        sa[:, 3:9] *= 2.0 ** -70
+        sa[:, 9:] *= 2.0 ** -67
+        sw *= 2.0 ** -22
+    else:                       # products on both sides of 2^100
+        sa[:, :9] *= 2.0 ** 60
+        sa[:, 9:] *= 2.0 ** 63
+        sw *= 2.0 ** 39
+    out = check(op, a, sa, w, sw, k, n)
+    assert torch.isfinite(out).all() and float(out.abs().max()) > 0

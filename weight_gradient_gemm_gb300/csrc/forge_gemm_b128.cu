@@ -31,6 +31,7 @@
 // took 362), the two issuers in a fixed turn (354 for 333), waits that poll.
 #include <cuda_bf16.h>
 
+#include "forge_b128.cuh"
 #include "forge_internal.h"
 #include "forge_launch.cuh"
 #include "forge_ptx.cuh"
@@ -40,9 +41,10 @@ namespace forge {
 namespace {
 
 constexpr int kThreads8 = 384;
-// Registers a thread after the split: 128 x 88 + 256 x 208 = 384 x 168, what
-// the block is launched with.
-constexpr int kRegsRole = 88, kRegsEpi = 208;
+// Registers a thread after the split: 128 x 104 + 256 x 200 = 384 x 168, what
+// the block is launched with.  (With 88 and 208 the scales' warp has too few: 2000
+// tokens, 14336 -> 4096, 91.2 us for 89.8; with 96 and 200 90.2, 112 and 192 94.0.)
+constexpr int kRegsRole = 104, kRegsEpi = 200;
 constexpr int kEpiWarps = 8;
 constexpr int kSmemMax = 232448;   // dynamic shared memory of one CTA (227 KB)
 
@@ -78,7 +80,11 @@ struct Traits8 {
   static constexpr int OFF_BARS = OFF_SC + SC_BYTES;
   static constexpr int NUM_BARS = 2 * STAGES + 8 + 5;
   static constexpr int OFF_TMEM = OFF_BARS + 8 * NUM_BARS;
-  static constexpr int SMEM_USED = OFF_TMEM + 8;
+  // per scale batch: a word, and each token's factor and exponent (forge_b128.cuh)
+  static constexpr int OFF_WORD = OFF_TMEM + 8;
+  static constexpr int OFF_FACTOR = OFF_WORD + 8;
+  static constexpr int OFF_EXPONENT = OFF_FACTOR + 2 * kBM * 4;
+  static constexpr int SMEM_USED = OFF_EXPONENT + 2 * kBM * 4;
   static constexpr int SMEM_ALLOC = SMEM_USED + 1024 < kSmemMax ? SMEM_USED + 1024 : kSmemMax;
   static_assert(SMEM_USED <= kSmemMax, "shared memory budget exceeded");
 };
@@ -125,6 +131,9 @@ __global__ void __launch_bounds__(kThreads8, 1)
   const uint32_t bar_drain = bars + 8u * (2 * T::STAGES + 12);
   float* scales = reinterpret_cast<float*>(gbase + T::OFF_SC);   // [2][SC_BATCH][NWB][128]
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(gbase + T::OFF_TMEM + 4);
+  volatile uint32_t* words = reinterpret_cast<volatile uint32_t*>(gbase + T::OFF_WORD);
+  float* factors = reinterpret_cast<float*>(gbase + T::OFF_FACTOR);        // [2][128]
+  int* exponents = reinterpret_cast<int*>(gbase + T::OFF_EXPONENT);        // [2][128]
   const WaitCtx wc{abort_flag, a.err, a.err_site, a.timeout_ns};
 
   if (threadIdx.x == 0) {
@@ -302,7 +311,9 @@ __global__ void __launch_bounds__(kThreads8, 1)
       // sa[row][k] sw[column block][k] for the tile's 128 rows, a batch of
       // blocks at a time.  (Read by the epilogue threads themselves, one block
       // ahead, their latency bounded the whole kernel: 462 ns per block of a
-      // 128 x 128 tile.)  Rows and column blocks outside count zero.
+      // 128 x 128 tile.)  Rows and column blocks outside count zero.  The weight's
+      // scales are loaded before the wait too, a lane each (one by one after it, 16
+      // latencies follow one another: 2000 tokens, 14336 -> 4096, 89.2 us for 87.5).
       uint32_t cnt = 0;
       bool ok = true;
       for (int t = unit0; ok && t < a.num_tiles; t += units) {
@@ -310,6 +321,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
         tile_of(t, a, tm, tn);
         const int row0 = tm * T::TM + static_cast<int>(rank) * kBM + lane;
         const int wb0 = tn * T::NWB;
+        TokenExponents te;
         for (int k0 = 0; k0 < a.num_kb; k0 += T::SC_BATCH, ++cnt) {
           float ra[4][T::SC_BATCH];
 #pragma unroll
@@ -320,6 +332,21 @@ __global__ void __launch_bounds__(kThreads8, 1)
             for (int i = 0; i < T::SC_BATCH; ++i)
               ra[j][i] = row < a.m && k0 + i < a.num_kb ? p[i] : 0.0f;
           }
+          float most[4];
+          uint32_t any[4];   // whether a token has a scale other than zero
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            most[j] = 0.0f;
+            any[j] = 0u;
+#pragma unroll
+            for (int i = 0; i < T::SC_BATCH; ++i) any[j] |= __float_as_uint(ra[j][i]);
+          }
+          // a lane for each of the batch's weight blocks
+          const int lk = k0 + lane / T::NWB, lw = wb0 + lane % T::NWB;
+          const float rl = lane < T::SC_BATCH * T::NWB && lk < a.num_kb && lw * 128 < a.n
+                               ? a.sw[static_cast<int64_t>(lw) * a.sw_n +
+                                      static_cast<int64_t>(lk) * a.sw_k]
+                               : 0.0f;
           const int b = cnt & 1;
           const bool good =
               wait_bounded(bar_sempty(b), ((cnt >> 1) & 1u) ^ 1u, wc, kSiteLoaderEmpty);
@@ -328,14 +355,24 @@ __global__ void __launch_bounds__(kThreads8, 1)
           for (int i = 0; i < T::SC_BATCH; ++i)
 #pragma unroll
             for (int w = 0; w < T::NWB; ++w) {
-              const bool in = k0 + i < a.num_kb && (wb0 + w) * 128 < a.n;
-              const float rw = in ? a.sw[static_cast<int64_t>(wb0 + w) * a.sw_n +
-                                       static_cast<int64_t>(k0 + i) * a.sw_k]
-                                : 0.0f;
+              const float rw = __shfl_sync(0xffffffffu, rl, i * T::NWB + w);
               float* dst = scales + ((b * T::SC_BATCH + i) * T::NWB + w) * kBM + lane;
 #pragma unroll
-              for (int j = 0; j < 4; ++j) dst[32 * j] = in ? ra[j][i] * rw : 0.0f;
+              for (int j = 0; j < 4; ++j) {
+                const float p = ra[j][i] * rw;
+                dst[32 * j] = p;
+                most[j] = fmaxf(most[j], fabsf(p));
+              }
             }
+          bool apart = false;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) apart |= te.add(j, most[j], any[j] != 0u);
+          uint32_t word = 0u;
+          if (__any_sync(0xffffffffu, apart))
+            word = scales_apart<T::NWB, kBM, T::SC_BATCH>(
+                a, te, scales + b * T::SC_BATCH * T::NWB * kBM, factors + b * kBM,
+                exponents + b * kBM, row0, lane, wb0, k0, a.num_kb);
+          if (lane == 0) words[b] = word;
           mbar_arrive(bar_sfull(b));
         }
       }
@@ -368,6 +405,11 @@ __global__ void __launch_bounds__(kThreads8, 1)
         const float* sc_row = scales + sb * T::SC_BATCH * T::NWB * kBM + q * 32 + lane;
         ok = __all_sync(0xffffffffu, wait_bounded_inline(bar_sfull(sb), sph, wc, kSiteEpiSlotFull));
         if (!ok) break;
+        if (words[sb] & kBatchFactors) {
+          const float2 f = dup2(factors[sb * kBM + q * 32 + lane]);
+#pragma unroll
+          for (int i = 0; i < T::NC / 2; ++i) acc[i] = mul2(acc[i], f);
+        }
 #pragma unroll 1
         for (int k = 0; k < kn; ++k) {
           float sc[T::GROUPS];
@@ -407,6 +449,12 @@ __global__ void __launch_bounds__(kThreads8, 1)
           }
         }
         if (!ok) break;
+        if (k0 + T::SC_BATCH >= a.num_kb && (words[sb] & kBatchExponents)) {
+          const int e = exponents[sb * kBM + q * 32 + lane];
+#pragma unroll
+          for (int i = 0; i < T::NC / 2; ++i)
+            acc[i] = make_float2(times_pow2_64(acc[i].x, e), times_pow2_64(acc[i].y, e));
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_sempty(sb));   // the batch's scales are read
         if (++sb == 2) { sb = 0; sph ^= 1u; }

@@ -24,6 +24,7 @@
 // tokens a warp).  Every wait is bounded.
 #include <cuda_bf16.h>
 
+#include "forge_b128.cuh"
 #include "forge_internal.h"
 #include "forge_launch.cuh"
 #include "forge_ptx.cuh"
@@ -49,13 +50,17 @@ struct Few {
   static constexpr int SC_BYTES = 2 * SC_BATCH * NT * 4;
   static constexpr int PART_BYTES = NT * kBM * 4;       // one tile of fp32 sums
   // Shared memory from a 1024-aligned base: barriers (the most there can be),
-  // abort flag, scales, stages, and where the reduction is split the shares.
+  // abort flag, scales (and per batch of them a word, and each token's factor and
+  // exponent: forge_b128.cuh), stages, and where the reduction is split the shares.
   // (In the stages' place the shares would have to wait for every CTA's last
   // load and product: a cluster barrier more.)
   static constexpr int NUM_BARS = 2 * DEEP + 2 * NBUF + 5;
   static constexpr int OFF_TMEM = 8 * NUM_BARS;
-  static constexpr int OFF_SC = (OFF_TMEM + 8 + 15) & ~15;
-  static constexpr int OFF_STAGES = (OFF_SC + SC_BYTES + 1023) & ~1023;
+  static constexpr int OFF_WORD = OFF_TMEM + 8;
+  static constexpr int OFF_SC = (OFF_WORD + 8 + 15) & ~15;
+  static constexpr int OFF_FACTOR = OFF_SC + SC_BYTES;
+  static constexpr int OFF_EXPONENT = OFF_FACTOR + 2 * NT * 4;
+  static constexpr int OFF_STAGES = (OFF_EXPONENT + 2 * NT * 4 + 1023) & ~1023;
   static constexpr int smem(int stages, bool split) {
     return OFF_STAGES + stages * STAGE_BYTES + (split ? PART_BYTES : 0) + 1024;
   }
@@ -97,6 +102,9 @@ __global__ void __launch_bounds__(Few<NT>::THREADS, NT <= 64 ? 2 : 1)
   const uint32_t bar_drain = bars + 8u * (2 * T::DEEP + 2 * T::NBUF + 4);
   float* scales = reinterpret_cast<float*>(gbase + T::OFF_SC);   // [2][SC_BATCH][NT]
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(gbase + T::OFF_TMEM + 4);
+  volatile uint32_t* words = reinterpret_cast<volatile uint32_t*>(gbase + T::OFF_WORD);
+  float* factors = reinterpret_cast<float*>(gbase + T::OFF_FACTOR);     // [2][NT]
+  int* exponents = reinterpret_cast<int*>(gbase + T::OFF_EXPONENT);     // [2][NT]
   const WaitCtx wc{abort_flag, a.err, a.err_site, a.timeout_ns};
 
   const uint64_t wpol = l2_policy_evict_normal(), xpol = l2_policy_evict_last();
@@ -189,27 +197,55 @@ __global__ void __launch_bounds__(Few<NT>::THREADS, NT <= 64 ? 2 : 1)
     // all start before any is used.
     constexpr int PT = (NT + 31) / 32;   // tokens per lane
     uint32_t b = 0, ph = 1;
+    TokenExponents te;
     for (int k0 = kb; k0 < ke; k0 += T::SC_BATCH) {
-      float rw[T::SC_BATCH], rx[PT][T::SC_BATCH];
+      float rx[PT][T::SC_BATCH];
 #pragma unroll
       for (int i = 0; i < T::SC_BATCH; ++i) {
         const int k = min(k0 + i, ke - 1);   // past the end: loaded again, not used
-        rw[i] = a.sw[static_cast<int64_t>(tile) * a.sw_n + static_cast<int64_t>(k) * a.sw_k];
 #pragma unroll
         for (int j = 0; j < PT; ++j) {
           const int t = lane + 32 * j;
           rx[j][i] = a.sa[static_cast<int64_t>(min(t, a.m - 1)) * a.num_kb + k];
         }
       }
+      // a lane for each of the batch's weight blocks
+      const float rl = a.sw[static_cast<int64_t>(tile) * a.sw_n +
+                            static_cast<int64_t>(min(k0 + (lane & 7), ke - 1)) * a.sw_k];
+      float rw[T::SC_BATCH];
+#pragma unroll
+      for (int i = 0; i < T::SC_BATCH; ++i) rw[i] = __shfl_sync(0xffffffffu, rl, i);
+      // (what lies past the last token or block repeats it)
+      bool apart = false;
+#pragma unroll
+      for (int j = 0; j < PT; ++j) {
+        float most = 0.0f;
+        uint32_t any = 0u;   // whether the token has a scale other than zero
+#pragma unroll
+        for (int i = 0; i < T::SC_BATCH; ++i) {
+          any |= __float_as_uint(rx[j][i]);
+          rx[j][i] *= rw[i];
+          most = fmaxf(most, fabsf(rx[j][i]));
+        }
+        apart |= te.add(j, most, any != 0u);
+      }
       const bool good = wait_bounded(bar_sempty(b), ph, wc, kSiteLoaderEmpty);
       if (!__all_sync(0xffffffffu, good)) break;
+      uint32_t word = 0u;
+      if (__any_sync(0xffffffffu, apart)) {
+        word = scales_apart<1, NT, T::SC_BATCH>(a, te, scales + b * T::SC_BATCH * NT,
+                                                factors + b * NT, exponents + b * NT, lane, lane,
+                                                tile, k0, ke);
+      } else {
 #pragma unroll
-      for (int i = 0; i < T::SC_BATCH; ++i)
+        for (int i = 0; i < T::SC_BATCH; ++i)
 #pragma unroll
-        for (int j = 0; j < PT; ++j) {
-          const int t = lane + 32 * j;
-          if (t < NT) scales[(b * T::SC_BATCH + i) * NT + t] = t < a.m ? rx[j][i] * rw[i] : 0.0f;
-        }
+          for (int j = 0; j < PT; ++j) {
+            const int t = lane + 32 * j;
+            if (t < NT) scales[(b * T::SC_BATCH + i) * NT + t] = t < a.m ? rx[j][i] : 0.0f;
+          }
+      }
+      if (lane == 0) words[b] = word;
       mbar_arrive(bar_sfull(b));
       if (++b == 2) { b = 0; ph ^= 1u; }
     }
@@ -226,6 +262,13 @@ __global__ void __launch_bounds__(Few<NT>::THREADS, NT <= 64 ? 2 : 1)
       const float* sc_row = scales + sb * T::SC_BATCH * NT + h * T::NC;
       ok = __all_sync(0xffffffffu, wait_bounded_inline(bar_sfull(sb), sph, wc, kSiteEpiSlotFull));
       if (!ok) break;
+      if (words[sb] & kBatchFactors) {
+#pragma unroll
+        for (int i = 0; i < T::NC / 2; ++i) {
+          const float* f = factors + sb * NT + h * T::NC + 2 * i;
+          acc[i] = mul2(acc[i], make_float2(f[0], f[1]));
+        }
+      }
 #pragma unroll 1
       for (int k = 0; k < kn; ++k) {
         ok = __all_sync(0xffffffffu,
@@ -254,6 +297,13 @@ __global__ void __launch_bounds__(Few<NT>::THREADS, NT <= 64 ? 2 : 1)
         if (++buf == T::NBUF) { buf = 0; bph ^= 1u; }
       }
       if (!ok) break;
+      if (k0 + T::SC_BATCH >= ke && (words[sb] & kBatchExponents)) {
+#pragma unroll
+        for (int i = 0; i < T::NC / 2; ++i) {
+          const int* e = exponents + sb * NT + h * T::NC + 2 * i;
+          acc[i] = make_float2(times_pow2_64(acc[i].x, e[0]), times_pow2_64(acc[i].y, e[1]));
+        }
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_sempty(sb));
       if (++sb == 2) { sb = 0; sph ^= 1u; }

@@ -49,7 +49,12 @@ uint64_t blocks128(int64_t n) { return static_cast<uint64_t>((n + 127) / 128); }
 
 constexpr int64_t kMaxIndex = (1LL << 31) - 1;
 
-forge_status status(cudaError_t e) { return e == cudaSuccess ? FORGE_OK : FORGE_ERR_LAUNCH; }
+// The status of a call's launches; a failed one leaves no error behind.
+forge_status status(cudaError_t e) {
+  if (e == cudaSuccess) return FORGE_OK;
+  (void)cudaGetLastError();
+  return FORGE_ERR_LAUNCH;
+}
 
 forge_status check_rows(int64_t rows, int64_t cols, int64_t max_cols) {
   if (rows < 0 || rows > kMaxIndex || cols <= 0 || cols > max_cols || cols % 8 != 0)
@@ -341,7 +346,7 @@ forge_status forge_grad_norm(const forge_grad* grads, int n, float max_norm, flo
     a.part = part + parts;
     parts += blocks;
     const cudaError_t e = launch_grad_norm(a, blocks, cs);
-    if (e != cudaSuccess) return FORGE_ERR_LAUNCH;
+    if (e != cudaSuccess) return status(e);
   }
   return status(launch_grad_norm_final(part, parts, max_norm, out, cs));
 }

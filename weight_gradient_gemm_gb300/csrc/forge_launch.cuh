@@ -28,7 +28,8 @@ __device__ __forceinline__ void grid_dependency_trigger() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// cluster_x: CTAs per cluster (0: no clusters).
+// cluster_x: CTAs per cluster (0: no clusters).  A launch that fails answers with
+// its error and leaves none behind for the check after another launch.
 template <typename... P, typename... A>
 cudaError_t launch_chained(void (*kern)(P...), unsigned grid, unsigned block, size_t smem,
                            unsigned cluster_x, cudaStream_t stream, A&&... args) {
@@ -46,7 +47,9 @@ cudaError_t launch_chained(void (*kern)(P...), unsigned grid, unsigned block, si
   attr[1].val.clusterDim.z = 1;
   lc.attrs = attr;
   lc.numAttrs = cluster_x > 0 ? 2 : 1;
-  return cudaLaunchKernelEx(&lc, kern, std::forward<A>(args)...);
+  const cudaError_t e = cudaLaunchKernelEx(&lc, kern, std::forward<A>(args)...);
+  if (e != cudaSuccess) (void)cudaGetLastError();
+  return e;
 }
 
 }  // namespace forge

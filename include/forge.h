@@ -587,7 +587,7 @@ forge_status forge_dgrad_fp8(const void* dY, const float* dy_scales, const void*
 /* One gradient tensor of forge_grad_norm. */
 typedef struct {
   const void* data;    /* device, 16-byte aligned, fp32 or bf16 (NULL if numel is 0) */
-  int64_t numel;       /* any size                                                   */
+  int64_t numel;       /* any size; less than 2^44 - 2^21 in all tensors together     */
   forge_dtype dtype;
 } forge_grad;
 

@@ -305,10 +305,14 @@ forge_status forge_grad_norm(const forge_grad* grads, int n, float max_norm, flo
   if (!(max_norm > 0.0f)) return FORGE_ERR_HYPER;
   const Span o{out, 8}, ws{workspace, workspace_bytes};
   if (meet(o, ws)) return FORGE_ERR_ALIAS;
+  int64_t launch_units = 0;   // of the launch that takes tensor i
   for (int i = 0; i < n; ++i) {
     const forge_grad& g = grads[i];
+    if (i % kNormTensors == 0) launch_units = 0;
     if (g.dtype != FORGE_DT_FP32 && g.dtype != FORGE_DT_BF16) return FORGE_ERR_FORMAT;
     if (g.numel < 0 || g.numel > (1LL << 44)) return FORGE_ERR_SHAPE;
+    launch_units += (g.numel + kNormUnit - 1) / kNormUnit;
+    if (launch_units > kMaxIndex / 2) return FORGE_ERR_SHAPE;
     if (g.numel == 0) continue;
     if (!g.data) return FORGE_ERR_NULL;
     if (!aligned(g.data, 16)) return FORGE_ERR_ALIGN;
@@ -338,7 +342,6 @@ forge_status forge_grad_norm(const forge_grad* grads, int n, float max_norm, flo
       if (g.dtype == FORGE_DT_BF16) a.bf16[a.n >> 6] |= 1ull << (a.n & 63);
       a.unit0[a.n] = static_cast<int32_t>(units);
       units += (g.numel + kNormUnit - 1) / kNormUnit;
-      if (units > kMaxIndex / 2) return FORGE_ERR_SHAPE;
       a.unit0[++a.n] = static_cast<int32_t>(units);
     }
     if (units == 0) continue;

@@ -3,7 +3,9 @@
 Each .cu file compiles to an object in parallel, then one shared library is
 linked with the CUDA runtime static.  Beside it, the Python calls of the
 operators around the weight gradient (csrc/forge_call.cpp) compile to a CPython
-extension against the installed torch.  Re-running is cheap: objects are rebuilt
+extension against the installed torch, named for the interpreter's ABI; where
+that cannot be built the library is complete without it (forge.py calls through
+ctypes, a few microseconds slower).  Re-running is cheap: objects are rebuilt
 only when a source or header is newer.
 """
 from __future__ import annotations
@@ -13,6 +15,7 @@ import os
 import shutil
 import subprocess
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -20,7 +23,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libforge.so")
-CALL = os.path.join(PKG, "_forge_call.so")
+CALL = os.path.join(PKG, "_forge_call" + sysconfig.get_config_var("EXT_SUFFIX"))
+CXX = "g++"
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O3",
          "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]
@@ -46,24 +50,33 @@ def _stale(out: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
-def build_call() -> str:
-    """The CPython extension (host code only, the machine's own compiler)."""
-    src = os.path.join(CSRC, "forge_call.cpp")
-    torch_dir = list(importlib.util.find_spec("torch").submodule_search_locations)[0]
-    if _stale(CALL, [src, os.path.join(ROOT, "include", "forge.h"),
-                     os.path.join(torch_dir, "version.py")]):
+def build_call() -> bool:
+    """The CPython extension (host code only, the machine's own compiler); False,
+    with a warning and no file, where it does not build."""
+    try:
+        src = os.path.join(CSRC, "forge_call.cpp")
+        torch_dir = list(importlib.util.find_spec("torch").submodule_search_locations)[0]
+        if not _stale(CALL, [src, os.path.join(ROOT, "include", "forge.h"),
+                             os.path.join(torch_dir, "version.py")]):
+            return True
+        if os.path.exists(CALL):
+            os.remove(CALL)
         cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
         inc = [os.path.join(ROOT, "include"), os.path.join(torch_dir, "include"),
                os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
                os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
-        cmd = (["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall", src, "-o", CALL]
+        cmd = ([CXX, "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall", src, "-o", CALL]
                + [a for i in inc for a in ("-isystem" if i is not inc[0] else "-I", i)]
                + ["-L" + os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
                   "-lc10_cuda"])
         r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"g++ failed for forge_call.cpp:\n{r.stdout}\n{r.stderr}")
-    return CALL
+        if r.returncode == 0:
+            return True
+        why = r.stdout + r.stderr
+    except (OSError, AttributeError, RuntimeError) as e:   # no compiler, torch or headers
+        why = str(e)
+    warnings.warn(f"forge_call.cpp did not build, calls go through ctypes:\n{why}", stacklevel=2)
+    return False
 
 
 def build(verbose: bool = False, extra_flags=None) -> str:

@@ -14,6 +14,7 @@
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/version.h>
 
 #include <cstdint>
 #include <vector>
@@ -308,4 +309,10 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_forge_call", nullptr, -1, methods
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__forge_call() { return PyModule_Create(&module); }
+// The module says which torch it was compiled against; another one's tensors may
+// be laid out differently, so forge.py leaves it alone then.
+PyMODINIT_FUNC PyInit__forge_call() {
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "torch_version", TORCH_VERSION) < 0) Py_CLEAR(m);
+  return m;
+}

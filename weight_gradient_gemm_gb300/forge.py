@@ -2,7 +2,8 @@
 step of the computation runs in the library's CUDA kernels.  The operators
 around the weight gradient, whose calls on few rows take a few microseconds, go
 through a CPython extension first (csrc/forge_call.cpp), with the same checks;
-what it does not take goes through the checks here, which say what is wrong.
+what it does not take goes through the checks here, which say what is wrong.  So
+does every call where the extension is missing.
 
 PyTorch supplies device memory and the current CUDA stream.  There is no CPU
 fallback: if ``libforge.so`` has not been built, every call raises.
@@ -14,14 +15,16 @@ import ctypes
 import importlib.util
 import os
 import re
+import sysconfig
 import threading
+import warnings
 from typing import Optional
 
 import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libforge.so")
-CALL_PATH = os.path.join(_HERE, "_forge_call.so")
+CALL_PATH = os.path.join(_HERE, "_forge_call" + sysconfig.get_config_var("EXT_SUFFIX"))
 HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "forge.h")
 
 FORGE_OK = 0
@@ -203,17 +206,30 @@ def lib() -> ctypes.CDLL:
         return _lib
 
 
-_call = None    # the CPython extension, once the library is loaded
+_call = None    # the CPython extension, or _NoCall, once the library is loaded
+
+
+class _NoCall:
+    """In the extension's place: takes no call."""
+
+    def __getattr__(self, name):
+        return lambda *args: -1
 
 
 def _load_call(L: ctypes.CDLL) -> None:
     global _call
-    if not os.path.exists(CALL_PATH):
-        raise RuntimeError(f"{CALL_PATH} is not built; run `python -c \"import __graft_entry__ as "
-                           f"g; g.build()\"` first")
-    spec = importlib.util.spec_from_file_location("_forge_call", CALL_PATH)
-    mod = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(mod)
+    _call = _NoCall()
+    try:
+        spec = importlib.util.spec_from_file_location("_forge_call", CALL_PATH)
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+    except (ImportError, FileNotFoundError) as e:
+        warnings.warn(f"{CALL_PATH} is not there ({e}): the operators around the weight gradient "
+                      f"are called through ctypes, 5 us slower", stacklevel=3)
+        return
+    if mod.torch_version != torch.__version__.split("+")[0]:
+        warnings.warn(f"{CALL_PATH} was built for torch {mod.torch_version}: not used", stacklevel=3)
+        return
     mod.bind(*[ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in (
         "forge_rmsnorm", "forge_rmsnorm_backward", "forge_quantize_b128", "forge_linear_fp8",
         "forge_dgrad_fp8", "forge_grad_norm", "forge_adamw_clip")])

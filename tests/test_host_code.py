@@ -2,14 +2,17 @@
 small programs compiled against its sources, which play the CUDA runtime's part
 themselves (no device is touched)."""
 import os
+import shutil
 import subprocess
+
+import pytest
 
 from weight_gradient_gemm_gb300 import _build
 
 
-def run(tmp_path, program, runtime, objects=()):
+def run(tmp_path, program, runtime, flags=()):
     """Compiles `program` (CUDA C++) with `runtime` (C++: the runtime's functions it
-    replaces) and the objects given, and runs it."""
+    replaces) and the flags or objects given, and runs it."""
     paths = [os.path.join(tmp_path, n) for n in ("program.cu", "runtime.cpp", "program")]
     for path, text in zip(paths, (program, runtime)):
         with open(path, "w") as f:
@@ -17,7 +20,7 @@ def run(tmp_path, program, runtime, objects=()):
     lib = os.path.join(os.path.dirname(os.path.dirname(_build.nvcc())), "lib64")
     cmd = ([_build.nvcc()] + _build.ARCH + ["-O1", "-std=c++17", "--expt-relaxed-constexpr",
            "-I", os.path.join(_build.ROOT, "include"), "-I", _build.CSRC, "-cudart", "shared",
-           "-Xlinker", "-rpath," + lib, "-o", paths[2]] + paths[:2] + list(objects))
+           "-Xlinker", "-rpath," + lib, "-o", paths[2]] + paths[:2] + list(flags))
     r = subprocess.run(cmd, capture_output=True, text=True)
     assert r.returncode == 0, r.stdout + r.stderr
     r = subprocess.run([paths[2]], capture_output=True, text=True, timeout=300)
@@ -48,3 +51,63 @@ extern "C" cudaError_t cudaGetLastError() {
   return e;
 }
 """)
+
+
+# launches that the program counts; the device has 152 SMs
+RUNTIME = """
+#include <cuda_runtime_api.h>
+#include <atomic>
+std::atomic<int> launches{0}, empty{0};
+extern "C" {
+cudaError_t cudaGetDevice(int* d) { *d = 0; return cudaSuccess; }
+cudaError_t cudaGetLastError() { return cudaSuccess; }
+cudaError_t cudaFuncSetAttribute(const void*, cudaFuncAttribute, int) { return cudaSuccess; }
+cudaError_t cudaOccupancyMaxActiveClusters(int* n, const void*, const cudaLaunchConfig_t*) {
+  *n = 76;
+  return cudaSuccess;
+}
+cudaError_t cudaLaunchKernelExC(const cudaLaunchConfig_t* c, const void*, void**) {
+  ++(c->gridDim.x > 0 ? launches : empty);
+  return cudaSuccess;
+}
+}
+"""
+THREADS = """
+#include <thread>
+#include <vector>
+extern std::atomic<int> launches, empty;
+template <typename F> int on_threads(F f) {
+  std::vector<std::thread> t;
+  for (int i = 0; i < 8; ++i) t.emplace_back([&] { for (int k = 0; k < 50; ++k) f(); });
+  for (auto& x : t) x.join();
+  return launches == 400 && empty == 0 ? 0 : 1;
+}
+"""
+
+
+@pytest.mark.parametrize("source,call", [
+    ("forge_gemm_b128.cu", "forge::B128Args a = {}; a.num_tiles = 100; "
+     "forge::launch_gemm_b128({2, 256, 0, 1}, false, a, 152, nullptr);"),
+    ("forge_gemm_b128_few.cu", "forge::B128Args a = {}; a.num_tiles = 100; a.splits = 1; "
+     "forge::launch_gemm_b128_few(16, true, a, 152, nullptr);"),
+    ("forge_norm.cu", "forge::NormArgs a = {}; a.rows = 8192; a.cols = 4096; "
+     "forge::launch_rmsnorm(a, 152, nullptr);"),
+])
+def test_first_calls_from_several_threads(tmp_path, source, call):
+    # what a launch works out once per device is shared by threads: the thread
+    # sanitizer must see no race, and no launch may be without blocks
+    with open(os.path.join(tmp_path, "t.cpp"), "w") as f:
+        f.write("int main() { return 0; }")
+    if shutil.which("g++") is None or subprocess.run(
+            ["g++", "-fsanitize=thread", f.name, "-o", f.name + ".exe"], capture_output=True).returncode:
+        pytest.skip("no thread sanitizer")
+    run(tmp_path, f"""
+#include <atomic>
+#include "{source}"
+{THREADS}
+namespace forge {{
+bool host_map(CUtensorMap*, const void*, CUtensorMapDataType, uint64_t, uint64_t, uint64_t,
+              uint32_t, uint32_t, CUtensorMapSwizzle) {{ return true; }}
+}}
+int main() {{ return on_threads([] {{ {call} }}); }}
+""", RUNTIME, ["-Xcompiler", "-fsanitize=thread", "-Xptxas", "-O1"])

@@ -534,39 +534,31 @@ template <int CG, int BN, bool DGRAD>
 cudaError_t launch_t(const B128Args& a, int num_sms, cudaStream_t stream) {
   using T = Traits8<CG, BN>;
   auto kern = gemm_b128_kernel<CG, BN, DGRAD>;
-  static int ready[64] = {0};        // per device: attributes set; resident pairs known
-  static int max_units[64] = {0};
-  int dev = 0;
-  cudaGetDevice(&dev);
-  const bool cached = dev >= 0 && dev < 64 && ready[dev];
-  if (!cached) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  // the units that can be resident: CTAs, or (known to the occupancy) pairs
+  static PerDevice resident;
+  int units = 0;
+  const cudaError_t e = resident.get(&units, [&](int* n) {
+    cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          T::SMEM_ALLOC);
-    if (e != cudaSuccess) return e;
-  }
-  int units = num_sms;
-  if constexpr (CG == 2) {   // as many pairs as can be resident
-    units = cached ? max_units[dev] : 0;
-    if (!cached) {
-      cudaLaunchConfig_t lc = {};
-      lc.gridDim = dim3(2 * (num_sms / 2), 1, 1);
-      lc.blockDim = dim3(kThreads8, 1, 1);
-      lc.dynamicSmemBytes = T::SMEM_ALLOC;
-      cudaLaunchAttribute attr[1];
-      attr[0].id = cudaLaunchAttributeClusterDimension;
-      attr[0].val.clusterDim.x = 2;
-      attr[0].val.clusterDim.y = 1;
-      attr[0].val.clusterDim.z = 1;
-      lc.attrs = attr;
-      lc.numAttrs = 1;
-      const cudaError_t e = cudaOccupancyMaxActiveClusters(&units, kern, &lc);
-      if (e != cudaSuccess) return e;
-      if (units <= 0) return cudaErrorInvalidConfiguration;
-      if (dev >= 0 && dev < 64) max_units[dev] = units;
-    }
-    units = units < num_sms / 2 ? units : num_sms / 2;
-  }
-  if (!cached && dev >= 0 && dev < 64) ready[dev] = 1;
+    *n = num_sms;
+    if (CG == 1 || r != cudaSuccess) return r;
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3(2 * (num_sms / 2), 1, 1);
+    lc.blockDim = dim3(kThreads8, 1, 1);
+    lc.dynamicSmemBytes = T::SMEM_ALLOC;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    r = cudaOccupancyMaxActiveClusters(n, kern, &lc);
+    if (r == cudaSuccess && *n <= 0) r = cudaErrorInvalidConfiguration;
+    *n = *n < num_sms / 2 ? *n : num_sms / 2;
+    return r;
+  });
+  if (e != cudaSuccess) return e;
   return launch_chained(kern, CG * (a.num_tiles < units ? a.num_tiles : units), kThreads8,
                         T::SMEM_ALLOC, CG == 2 ? 2 : 0, stream, a);
 }

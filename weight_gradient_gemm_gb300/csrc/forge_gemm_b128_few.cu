@@ -375,15 +375,9 @@ template <int NT, bool DGRAD>
 cudaError_t launch_t(B128Args a, int num_sms, cudaStream_t stream) {
   using T = Few<NT>;
   auto kern = gemm_b128_few_kernel<NT, DGRAD>;
-  static int ready[64] = {0};   // per device: attributes set
-  int dev = 0;
-  cudaGetDevice(&dev);
-  if (dev < 0 || dev >= 64 || !ready[dev]) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         232448);
-    if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < 64) ready[dev] = 1;
-  }
+  static PerDevice once;
+  const cudaError_t e = allow_smem(once, kern, 232448);
+  if (e != cudaSuccess) return e;
   const bool split = a.splits > 1;
   a.stages = split ? T::SPLIT_DEEP : (a.num_tiles <= num_sms ? T::DEEP : T::STAGES);
   return launch_chained(kern, a.num_tiles * a.splits, T::THREADS, T::smem(a.stages, split),

@@ -17,6 +17,7 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <utility>
 
 namespace forge {
@@ -26,6 +27,38 @@ __device__ __forceinline__ void grid_dependency_wait() {
 }
 __device__ __forceinline__ void grid_dependency_trigger() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// A number above 0 that a launch works out once per device (attributes set, CTAs
+// that fit).  Threads whose first calls meet may both work it out.
+class PerDevice {
+ public:
+  // make(&n) answers with an error or sets n.
+  template <typename F>
+  cudaError_t get(int* n, F&& make) {
+    int dev = -1;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const bool kept = dev >= 0 && dev < kMax;
+    *n = kept ? value_[dev].load(std::memory_order_acquire) : 0;
+    if (*n > 0) return cudaSuccess;
+    e = make(n);
+    if (e == cudaSuccess && kept) value_[dev].store(*n, std::memory_order_release);
+    return e;
+  }
+
+ private:
+  static constexpr int kMax = 64;
+  std::atomic<int> value_[kMax] = {};
+};
+// The launches of `kern` may use `bytes` of dynamic shared memory.
+template <typename Kern>
+cudaError_t allow_smem(PerDevice& once, Kern kern, int bytes) {
+  int n = 0;
+  return once.get(&n, [&](int* v) {
+    *v = 1;
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  });
 }
 
 // cluster_x: CTAs per cluster (0: no clusters).  A launch that fails answers with

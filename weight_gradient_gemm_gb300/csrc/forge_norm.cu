@@ -809,29 +809,23 @@ RowPlan row_plan(int64_t rows, int cols, int streams, bool backward, int num_sms
   return p;
 }
 
-// Launches a stream kernel with its ring; the attribute is set once per device.
+// Launches a stream kernel with its ring.
 template <typename Kern, typename Args>
-cudaError_t launch_stream(Kern kern, int* ready, const RowPlan& p, const Args& a,
+cudaError_t launch_stream(Kern kern, PerDevice& once, const RowPlan& p, const Args& a,
                           cudaStream_t stream) {
-  int dev = 0;
-  cudaGetDevice(&dev);
-  if (dev < 0 || dev >= 64 || !ready[dev]) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 224 * 1024);
-    if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < 64) ready[dev] = 1;
-  }
+  const cudaError_t e = allow_smem(once, kern, 224 * 1024);
+  if (e != cudaSuccess) return e;
   return launch_chained(kern, p.grid, p.threads, p.smem, 0, stream, a);
 }
 template <int VPT, bool RES>
 cudaError_t launch_fwd_stream(const RowPlan& p, const NormArgs& a, cudaStream_t stream) {
-  static int ready[64] = {0};
-  return launch_stream(rmsnorm_stream_kernel<VPT, RES>, ready, p, a, stream);
+  static PerDevice once;
+  return launch_stream(rmsnorm_stream_kernel<VPT, RES>, once, p, a, stream);
 }
 template <int VPT, bool DSUM>
 cudaError_t launch_bwd_stream(const RowPlan& p, const NormBwdArgs& a, cudaStream_t stream) {
-  static int ready[64] = {0};
-  return launch_stream(rmsnorm_bwd_stream_kernel<VPT, DSUM>, ready, p, a, stream);
+  static PerDevice once;
+  return launch_stream(rmsnorm_bwd_stream_kernel<VPT, DSUM>, once, p, a, stream);
 }
 
 }  // namespace

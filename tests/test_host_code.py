@@ -29,14 +29,14 @@ def run(tmp_path, program, runtime, flags=()):
 
 def test_a_failed_launch_leaves_no_error_behind(tmp_path):
     # the check after another launch must not meet the error
-    run(tmp_path, """
+    run(tmp_path, r"""
 #include <cstdio>
 #include "forge_launch.cuh"
 extern cudaError_t last_error;
 __global__ void nothing(int) {}
 int main() {
   const cudaError_t e = forge::launch_chained(nothing, 1, 32, 0, 0, nullptr, 1);
-  std::printf("%d, left %d\\n", static_cast<int>(e), static_cast<int>(last_error));
+  std::printf("%d, left %d\n", static_cast<int>(e), static_cast<int>(last_error));
   return e == cudaErrorInvalidConfiguration && last_error == cudaSuccess ? 0 : 1;
 }
 """, """
@@ -51,6 +51,67 @@ extern "C" cudaError_t cudaGetLastError() {
   return e;
 }
 """)
+
+
+# the products' host side, with nothing behind it
+API = """
+#include "forge_api_ops.cu"
+namespace forge {
+int host_device(HostDevice*) { return 0; }
+bool host_map(CUtensorMap*, const void*, CUtensorMapDataType, uint64_t, uint64_t, uint64_t,
+              uint32_t, uint32_t, CUtensorMapSwizzle) { return false; }
+cudaError_t launch_rmsnorm(const NormArgs&, int, cudaStream_t) { return cudaSuccess; }
+int rmsnorm_bwd_blocks(int64_t, int, int) { return 0; }
+cudaError_t launch_rmsnorm_bwd(const NormBwdArgs&, int, cudaStream_t) { return cudaSuccess; }
+cudaError_t launch_quantize_b128(const uint16_t*, uint8_t*, float*, int64_t, int64_t, int, int,
+                                 const NormWait&, cudaStream_t) { return cudaSuccess; }
+int grad_norm_blocks(int64_t, int) { return 0; }
+cudaError_t launch_grad_norm(const GradNormArgs&, int, cudaStream_t) { return cudaSuccess; }
+cudaError_t launch_grad_norm_final(const double*, int, float, float*, cudaStream_t) {
+  return cudaSuccess;
+}
+cudaError_t launch_gemm_b128(const B128Config&, bool, const B128Args&, int, cudaStream_t) {
+  return cudaSuccess;
+}
+cudaError_t launch_gemm_b128_few(int, bool, const B128Args&, int, cudaStream_t) {
+  return cudaSuccess;
+}
+}  // namespace forge
+extern "C" void forge_get_tuning(forge_tuning*) {}
+"""
+
+
+def test_a_split_reduction_is_shared_evenly(tmp_path):
+    # every CTA of a cluster has two blocks at least, and none two more than another
+    run(tmp_path, r"""
+#include <cstdio>
+""" + API + r"""
+int main() {
+  const forge_tuning automatic = {FORGE_PROFILE_AUTO, 0, 0, 0, -1, 0, -1, -1};
+  int split = 0;
+  for (int sms : {148, 152, 160})
+    for (int n = 16; n <= 8192; n += 112)
+      for (int blocks = 1; blocks <= 400; ++blocks) {
+        const B128Config c = choose_b128(1, n, blocks, automatic, sms);
+        int least = blocks, most = 0;
+        for (int r = 0; r < c.splits; ++r) {
+          const int b = b128_first_block(r + 1, c.splits, blocks) -
+                        b128_first_block(r, c.splits, blocks);
+          least = b < least ? b : least;
+          most = b > most ? b : most;
+        }
+        if (b128_first_block(0, c.splits, blocks) != 0 ||
+            b128_first_block(c.splits, c.splits, blocks) != blocks || most - least > 1 ||
+            (c.splits > 1 && least < 2)) {
+          std::printf("%d columns, %d blocks on %d CTAs: %d to %d\n", n, blocks, c.splits, least,
+                      most);
+          return 1;
+        }
+        split += c.splits > 1;
+      }
+  return split > 0 ? 0 : 2;
+}
+""", "")
 
 
 # launches that the program counts; the device has 152 SMs

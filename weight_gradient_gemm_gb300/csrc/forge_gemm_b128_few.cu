@@ -88,8 +88,9 @@ __global__ void __launch_bounds__(Few<NT>::THREADS, NT <= 64 ? 2 : 1)
   const int splits = a.splits;
   const int rank = splits > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int tile = static_cast<int>(blockIdx.x) / splits;
-  const int per = (a.num_kb + splits - 1) / splits;
-  const int kb = rank * per, ke = min(a.num_kb, kb + per);   // this CTA's blocks (may be none)
+  // this CTA's blocks (none where more CTAs than blocks are asked for)
+  const int kb = b128_first_block(rank, splits, a.num_kb);
+  const int ke = b128_first_block(rank + 1, splits, a.num_kb);
 
   const uint32_t stages = a.stages;
   const uint32_t bars = base, stage0 = base + T::OFF_STAGES;

@@ -286,6 +286,12 @@ struct B128Config {
   int few;        // 0, or the tokens a tile holds when the outputs lie along M
   int splits;     // few tokens: CTAs per tile
 };
+// Few tokens: the first of the reduction's blocks that CTA `rank` of `splits` takes.
+// (Equal up to one: 9 blocks on 4 CTAs are 3, 2, 2 and 2, not 3, 3, 3 and none.)
+__host__ __device__ constexpr int b128_first_block(int rank, int splits, int num_kb) {
+  const int each = num_kb / splits, more = num_kb - each * splits;
+  return rank * each + (rank < more ? rank : more);
+}
 cudaError_t launch_gemm_b128(const B128Config& c, bool dgrad, const B128Args& a, int num_sms,
                              cudaStream_t stream);
 cudaError_t launch_gemm_b128_few(int nt, bool dgrad, const B128Args& a, int num_sms,

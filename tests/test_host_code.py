@@ -114,6 +114,52 @@ int main() {
 """, "")
 
 
+def test_no_memory_for_a_tensor_map_is_no_exception(tmp_path):
+    # the cache of tensor maps may not grow: the map is made all the same, and no
+    # C++ exception leaves the library (whose callers are C and Python)
+    _build.build()
+    objects = [os.path.join(_build.BUILD, o) for o in sorted(os.listdir(_build.BUILD))
+               if o.endswith(".o") and o != "forge_api.o"]
+    run(tmp_path, r"""
+#include "forge_api.cu"
+extern bool none;   // no memory to be had
+static CUresult encode(CUtensorMap* m, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                       const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
+                       CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                       CUtensorMapFloatOOBfill) {
+  m->opaque[0] = 77;
+  return CUDA_SUCCESS;
+}
+int main() {
+  forge::g_encode = encode;
+  CUtensorMap m;
+  for (int i = 0; i < 3; ++i) {
+    none = i == 1;
+    m.opaque[0] = 0;
+    try {
+      if (!forge::host_map(&m, &m + i, CU_TENSOR_MAP_DATA_TYPE_UINT8, 128, 128, 128, 128, 128,
+                           CU_TENSOR_MAP_SWIZZLE_128B) || m.opaque[0] != 77)
+        return 1;
+    } catch (...) {
+      return 2;
+    }
+  }
+  return 0;
+}
+""", """
+#include <cstdlib>
+#include <new>
+bool none = false;
+void* operator new(std::size_t n, std::align_val_t a) {   // (a tensor map is 64-byte aligned)
+  void* p = none ? nullptr : std::aligned_alloc(static_cast<std::size_t>(a), (n + 63) / 64 * 64);
+  if (!p) throw std::bad_alloc();
+  return p;
+}
+void operator delete(void* p, std::align_val_t) noexcept { std::free(p); }
+void operator delete(void* p, std::size_t, std::align_val_t) noexcept { std::free(p); }
+""", objects)
+
+
 # launches that the program counts; the device has 152 SMs
 RUNTIME = """
 #include <cuda_runtime_api.h>

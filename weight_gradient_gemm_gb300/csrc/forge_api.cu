@@ -209,7 +209,10 @@ bool get_map(CUtensorMap* out, const void* ptr, CUtensorMapDataType dt, uint64_t
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return false;
   if (g_cache.size() >= kCacheMax) g_cache.clear();
-  g_cache.emplace(key, m);
+  try {
+    g_cache.emplace(key, m);
+  } catch (...) {   // no memory to keep it: encoded again next time
+  }
   *out = m;
   return true;
 }

@@ -139,13 +139,23 @@ PyObject* guarded(PyObject* const* a, Py_ssize_t n, Py_ssize_t want, F f) {
   }
   return PyLong_FromLong(st);
 }
+// The interpreter is released while one of these lives, and taken again however
+// its block is left.
+class Released {
+ public:
+  Released() : state_(PyEval_SaveThread()) {}
+  ~Released() { PyEval_RestoreThread(state_); }
+  Released(const Released&) = delete;
+
+ private:
+  PyThreadState* state_;
+};
 // The library call, with the interpreter released.
-#define FORGE_CALL(expr)                     \
-  [&]() -> long {                            \
-    if (c.bad) return -1;                    \
-    long st_;                                \
-    Py_BEGIN_ALLOW_THREADS st_ = (expr);     \
-    Py_END_ALLOW_THREADS return st_;         \
+#define FORGE_CALL(expr)     \
+  [&]() -> long {            \
+    if (c.bad) return -1;    \
+    const Released released; \
+    return (expr);           \
   }()
 
 // bind(addresses in the order of `lib`)

@@ -12,7 +12,7 @@ from weight_gradient_gemm_gb300 import _build
 
 def run(tmp_path, program, runtime, flags=()):
     """Compiles `program` (CUDA C++) with `runtime` (C++: the runtime's functions it
-    replaces) and the flags or objects given, and runs it."""
+    replaces) and the flags or objects given, runs it and returns what it prints."""
     paths = [os.path.join(tmp_path, n) for n in ("program.cu", "runtime.cpp", "program")]
     for path, text in zip(paths, (program, runtime)):
         with open(path, "w") as f:
@@ -25,6 +25,7 @@ def run(tmp_path, program, runtime, flags=()):
     assert r.returncode == 0, r.stdout + r.stderr
     r = subprocess.run([paths[2]], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stdout + r.stderr
+    return r.stdout
 
 
 def test_a_failed_launch_leaves_no_error_behind(tmp_path):
@@ -112,6 +113,62 @@ int main() {
   return split > 0 ? 0 : 2;
 }
 """, "")
+
+
+def test_product_shapes_take_their_forms(tmp_path):
+    # tests/test_gpu_ops_forms.py is there for these forms; on 152 SMs
+    from tests.test_gpu_ops_forms import FEW, LONG
+    shapes = [(bt, k, n) for bt, k, n in LONG] + [(bt, 1040, n) for bt, n in FEW]
+    out = run(tmp_path, '#include <cstdio>\n' + API + r"""
+int main() {
+  const forge_tuning automatic = {FORGE_PROFILE_AUTO, 0, 0, 0, -1, 0, -1, -1};
+  const long shapes[][3] = {""" + ", ".join("{%d, %d, %d}" % s for s in shapes) + r"""};
+  for (const auto& s : shapes) {
+    const B128Config c = choose_b128(s[0], s[2], (s[1] + 127) / 128, automatic, 152);
+    const long tm = 128 * c.cg;
+    const long tiles = (s[0] + tm - 1) / tm * ((s[2] + c.bn - 1) / c.bn);
+    std::printf("%d %d %d %ld\n", c.cg, c.few, c.splits, tiles);
+  }
+}
+""", "")
+    plans = [tuple(map(int, line.split())) for line in out.split("\n") if line]
+    long, few = plans[:len(LONG)], plans[len(LONG):]
+    assert {p[0] for p in long} == {1, 2} and all(p[1] == 0 for p in long)
+    # by either tile, given or chosen, every CTA or pair has two or more
+    for (bt, k, n), p in zip(LONG, long):
+        assert -(-bt // 256) * -(-n // 256) > 76 and -(-bt // 128) * -(-n // 128) > 152
+    assert {p[1] for p in few} == {16, 32, 64, 128}
+    assert all(p[2] == 1 and p[3] > 152 for p in few)
+
+
+def test_norm_shapes_take_their_forms(tmp_path):
+    from tests import test_gpu_ops_forms as forms
+    warp, block, stream = 0, 1, 2
+    want = [(rows, cols, streams, False, stream, 2) for rows, cols in forms.STREAMS
+            for streams in (1, 2)]
+    want += [(rows, cols, streams, True, stream, 1 if cols <= 8192 else 2)
+             for rows, cols in forms.BACKWARD_STREAMS for streams in (2, 3)]
+    form = [(warp, 2), (block, 1), (block, 2), (block, 1), (block, 2), (block, 4), (stream, 1),
+            (stream, 2), (stream, 1)]
+    want += [(rows, cols, 2, False) + f
+             for (rows, cols), f in zip(forms.IN_PLACE, form, strict=True)]
+    out = run(tmp_path, r"""
+#include <cstdio>
+#include "forge_norm.cu"
+namespace forge {
+bool host_map(CUtensorMap*, const void*, CUtensorMapDataType, uint64_t, uint64_t, uint64_t,
+              uint32_t, uint32_t, CUtensorMapSwizzle) { return false; }
+}
+int main() {
+  const int shapes[][4] = {""" + ", ".join("{%d, %d, %d, %d}" % w[:4] for w in want) + r"""};
+  for (const auto& s : shapes) {
+    const forge::RowPlan p = forge::row_plan(s[0], s[1], s[2], s[3], 152);
+    std::printf("%d %d %d\n", p.walk, p.vpt, p.direct);
+  }
+}
+""", "", ["-Xptxas", "-O1"])
+    got = [tuple(map(int, line.split())) for line in out.split("\n") if line]
+    assert got == [w[4:] + (0,) for w in want]
 
 
 def test_no_memory_for_a_tensor_map_is_no_exception(tmp_path):
@@ -206,7 +263,8 @@ def test_first_calls_from_several_threads(tmp_path, source, call):
     with open(os.path.join(tmp_path, "t.cpp"), "w") as f:
         f.write("int main() { return 0; }")
     if shutil.which("g++") is None or subprocess.run(
-            ["g++", "-fsanitize=thread", f.name, "-o", f.name + ".exe"], capture_output=True).returncode:
+            ["g++", "-fsanitize=thread", f.name, "-o", f.name + ".exe"],
+            capture_output=True).returncode:
         pytest.skip("no thread sanitizer")
     run(tmp_path, f"""
 #include <atomic>

@@ -228,7 +228,8 @@ def _load_call(L: ctypes.CDLL) -> None:
                       f"are called through ctypes, 5 us slower", stacklevel=3)
         return
     if mod.torch_version != torch.__version__.split("+")[0]:
-        warnings.warn(f"{CALL_PATH} was built for torch {mod.torch_version}: not used", stacklevel=3)
+        warnings.warn(f"{CALL_PATH} was built for torch {mod.torch_version}: not used",
+                      stacklevel=3)
         return
     mod.bind(*[ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in (
         "forge_rmsnorm", "forge_rmsnorm_backward", "forge_quantize_b128", "forge_linear_fp8",

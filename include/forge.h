@@ -653,9 +653,11 @@ int forge_debug_timeout_site(void);
 void forge_set_wait_limit_ns(uint64_t ns);
 
 /* Testing aid for the timeout path: when enabled, the next fused or forge_wgrad
- * launch skips its first operand-load arrival, so its waits run out, the kernel
- * records FORGE_ERR_DEVICE_TIMEOUT and returns with its outputs unspecified.
- * The flag clears itself after that one launch. */
+ * launch, or the next norm, quantiser or 8-bit product (where its kernel waits on
+ * copies: norms of many rows, quantisers of 128 x 128 blocks, the products), skips
+ * its first operand-load arrival, so its waits run out, the kernel records
+ * FORGE_ERR_DEVICE_TIMEOUT and returns with its outputs unspecified.  The flag
+ * clears itself after that one launch. */
 void forge_debug_drop_first_arrival(int enable);
 
 /* Pipeline profiles: how a tensor-core kernel splits shared memory between

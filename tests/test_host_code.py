@@ -59,6 +59,7 @@ API = """
 #include "forge_api_ops.cu"
 namespace forge {
 int host_device(HostDevice*) { return 0; }
+int host_drop_flag() { return 0; }
 bool host_map(CUtensorMap*, const void*, CUtensorMapDataType, uint64_t, uint64_t, uint64_t,
               uint32_t, uint32_t, CUtensorMapSwizzle) { return false; }
 cudaError_t launch_rmsnorm(const NormArgs&, int, cudaStream_t) { return cudaSuccess; }

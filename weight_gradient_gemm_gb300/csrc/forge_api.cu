@@ -782,6 +782,8 @@ int host_device(HostDevice* out) {
   return FORGE_OK;
 }
 
+int host_drop_flag() { return take_drop_flag(); }
+
 bool host_map(CUtensorMap* out, const void* ptr, CUtensorMapDataType dt, uint64_t inner,
               uint64_t outer, uint64_t stride_bytes, uint32_t box_inner, uint32_t box_outer,
               CUtensorMapSwizzle sw) {

@@ -56,6 +56,10 @@ forge_status status(cudaError_t e) {
   return FORGE_ERR_LAUNCH;
 }
 
+NormWait norm_wait(const HostDevice& d) {
+  return NormWait{d.err, d.err_site, d.timeout_ns, host_drop_flag()};
+}
+
 forge_status check_rows(int64_t rows, int64_t cols, int64_t max_cols) {
   if (rows < 0 || rows > kMaxIndex || cols <= 0 || cols > max_cols || cols % 8 != 0)
     return FORGE_ERR_SHAPE;
@@ -151,6 +155,7 @@ forge_status product_b128(const void* A, const float* sa, const void* W, const f
   a.err = d.err;
   a.err_site = d.err_site;
   a.timeout_ns = d.timeout_ns;
+  a.drop_first_arrival = host_drop_flag();
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   return status(cfg.few ? launch_gemm_b128_few(cfg.few, dgrad, a, d.num_sms, cs)
                         : launch_gemm_b128(cfg, dgrad, a, d.num_sms, cs));
@@ -198,7 +203,7 @@ forge_status forge_rmsnorm(const void* x, const void* residual, const void* gain
   a.rows = rows;
   a.cols = static_cast<int>(cols);
   a.eps = eps;
-  a.wait = NormWait{d.err, d.err_site, d.timeout_ns};
+  a.wait = norm_wait(d);
   return status(launch_rmsnorm(a, d.num_sms, static_cast<cudaStream_t>(stream)));
 }
 
@@ -252,7 +257,7 @@ forge_status forge_rmsnorm_backward(const void* dY, const void* h, const void* g
   a.part = static_cast<float*>(workspace);
   a.rows = rows;
   a.cols = static_cast<int>(cols);
-  a.wait = NormWait{d.err, d.err_site, d.timeout_ns};
+  a.wait = norm_wait(d);
   return status(launch_rmsnorm_bwd(a, d.num_sms, cs));
 }
 
@@ -273,8 +278,7 @@ forge_status forge_quantize_b128(const void* x, void* codes, float* scales, int6
   const int st = host_device(&d);
   if (st != FORGE_OK) return static_cast<forge_status>(st);
   return status(launch_quantize_b128(static_cast<const uint16_t*>(x), static_cast<uint8_t*>(codes),
-                                     scales, rows, cols, block_rows, d.num_sms,
-                                     NormWait{d.err, d.err_site, d.timeout_ns},
+                                     scales, rows, cols, block_rows, d.num_sms, norm_wait(d),
                                      static_cast<cudaStream_t>(stream)));
 }
 

@@ -152,6 +152,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
     mbar_init(bar_drain, 2);
     *abort_flag = 0u;
     fence_mbarrier_init();
+    drop_first_arrival(a.drop_first_arrival, bar_full(0));
   }
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&a.a);

@@ -127,6 +127,7 @@ __global__ void __launch_bounds__(Few<NT>::THREADS, NT <= 64 ? 2 : 1)
     }
     if (lane == 0) *abort_flag = 0u;
     fence_mbarrier_init();
+    if (lane == 0) drop_first_arrival(a.drop_first_arrival, bar_full(0));
   } else if (warp == 1) {
     tmem_alloc(base + T::OFF_TMEM, T::TMEM_COLS);
     tmem_relinquish();

@@ -199,11 +199,15 @@ bool host_map(CUtensorMap* out, const void* ptr, CUtensorMapDataType dt, uint64_
               uint64_t outer, uint64_t stride_bytes, uint32_t box_inner, uint32_t box_outer,
               CUtensorMapSwizzle sw);
 
+// Whether the launch at hand shall drop its first arrival (the flag clears itself).
+int host_drop_flag();
+
 // What a norm kernel's bounded waits report to.
 struct NormWait {
   int* err;
   int* err_site;
   uint64_t timeout_ns;
+  int drop_first_arrival;   // testing aid
 };
 // The RMS norm in front of a linear layer (forge_norm.cu).  Null pointers
 // leave an input or output out.
@@ -277,6 +281,7 @@ struct B128Args {
   void* out_ptr;           // few tokens: stored without a map
   int32_t splits;          // few tokens: CTAs (a cluster) that share a tile's reduction
   int32_t stages;          // few tokens: operand stages
+  int32_t drop_first_arrival;   // testing aid
   int* err;
   int* err_site;
   uint64_t timeout_ns;

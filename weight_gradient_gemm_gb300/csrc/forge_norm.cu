@@ -193,6 +193,7 @@ struct RowRing {
   const uint8_t* src[S];
   int64_t rows;
   WaitCtx wc;
+  int drop;   // testing aid
   int slot = 0;
   uint32_t ph = 0;
   bool ok = true;
@@ -209,6 +210,7 @@ struct RowRing {
   __device__ void start() const {
     for (int s = 0; s < kRing; ++s) mbar_init(bars + 8u * s, 1);
     fence_mbarrier_init();
+    drop_first_arrival(drop, bars);
     int64_t row = blockIdx.x;
     for (int s = 0; s < kRing && row < rows; ++s, row += gridDim.x) fill(s, row);
   }
@@ -251,6 +253,7 @@ __device__ __forceinline__ RowRing<S> make_ring(uint8_t* smem, uint32_t row_byte
   volatile uint32_t* abort_flag =
       reinterpret_cast<volatile uint32_t*>(smem + kRing * S * row_bytes + 8 * kRing);
   r.wc = WaitCtx{abort_flag, w.err, w.err_site, w.timeout_ns};
+  r.drop = w.drop_first_arrival;
   return r;
 }
 
@@ -700,6 +703,7 @@ __global__ void __launch_bounds__(256)
     mbar_init(bar, 1);
     abort_word = 0u;
     fence_mbarrier_init();
+    drop_first_arrival(w.drop_first_arrival, bar);
   }
   grid_dependency_wait();
   if (threadIdx.x == 0) load(blockIdx.x);

@@ -67,6 +67,12 @@ __device__ __forceinline__ bool wait_bounded_inline(uint32_t bar, uint32_t parit
   return wait_spin_body(bar, parity, w, site, honor_abort);
 }
 
+// Testing aid (forge_debug_drop_first_arrival): the first phase of `bar`, just
+// initialised by this thread, waits for bytes that never come.
+__device__ __forceinline__ void drop_first_arrival(int drop, uint32_t bar) {
+  if (drop) mbar_expect_tx(bar, 16);
+}
+
 // The operand-stage waits of the producer and the MMA issuer.  On one CTA
 // they first poll with the non-blocking test (at most kSpinTests times)
 // before the bounded wait, which may suspend the thread: the hand-off of a

@@ -65,6 +65,17 @@ def test_quantize_rounds_every_quotient_to_the_nearest_code(block_rows, power):
         assert not bad.any(), int(bad.sum())
 
 
+@pytest.mark.parametrize("block_rows", [1, 128])
+def test_quantize_keeps_the_sign_of_zero(block_rows):
+    x = torch.zeros((3, 136), device=DEV)
+    x[:, 1::2] = -0.0
+    x[0, 2], x[1, 4] = 1.53125, -3.25      # 448 / amax rounded up and down
+    codes, scales = F.alloc_b128(3, 136, block_rows)
+    F.quantize_b128(x.bfloat16(), codes, scales, block_rows=block_rows)
+    ok()
+    assert torch.equal(torch.signbit(codes.float()), torch.signbit(x))
+
+
 # ---------------------------------------------------------------- products
 def product_case(seed, op, bt, d_in, d_out, codes=256):
     """Random operands of one product: code bytes below `codes` (with both signs) and

@@ -571,8 +571,8 @@ forge_status forge_quantize_b128(const void* x, void* codes, float* scales, int6
  * The products of each block of 128 are summed in the tensor core; the blocks'
  * sums are scaled and added in fp32, and the result is rounded once to
  * FORGE_DT_BF16 (or kept, FORGE_DT_FP32).  The product of a token's scale and the
- * weight's may leave fp32's range; what is lost then lies 2^35 or more below the
- * token's largest such product.  Y [bt, d_out], dX [bt, d_in].
+ * weight's may leave fp32's range: its rounding is at most 2^-30 of the token's
+ * largest such product.  Y [bt, d_out], dX [bt, d_in].
  * d_in and d_out are multiples of 16; pointers 16-byte aligned; the output
  * must not overlap an input.  bt = 0 does nothing.  The result is the same on
  * every run.  Nothing is allocated.  Asynchronous on `stream`.

@@ -135,11 +135,11 @@ def test_products_of_scales_outside_fp32(tune, op, bt, how, case):
         sa, sw = sa * 2.0 ** -110, sw * 2.0 ** -30
     elif case == "huge":        # times 2^127
         sa, sw = sa * 2.0 ** 85, sw * 2.0 ** 42
-    elif case == "rising":      # empty blocks, then products on both sides of 2^-90
+    elif case == "rising":      # empty blocks, then products on both sides of 2^-120
         a.view(torch.uint8)[:, :3 * 128] = 0
         sa[:, :3] = 0
-        sa[:, 3:9] *= 2.0 ** -70
-        sa[:, 9:] *= 2.0 ** -67
+        sa[:, 3:9] *= 2.0 ** -100
+        sa[:, 9:] *= 2.0 ** -97
         sw *= 2.0 ** -22
     else:                       # products on both sides of 2^100
         sa[:, :9] *= 2.0 ** 60

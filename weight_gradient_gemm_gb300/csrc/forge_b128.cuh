@@ -9,14 +9,16 @@
 // normally 0: its sums are kept times 2^-e, its products are formed times 2^-e, and
 // the result is multiplied by 2^e.  The warp that multiplies the scales chooses e
 // by the largest product of a batch of blocks and of those before: 0 where that
-// lies from 2^-90 to 2^100, else a multiple of 64 that brings it to 2^-32 .. 2^32.
-// Once a product has been seen e only rises, so what is lost lies 2^35 or more
-// below the token's largest product.  The epilogue's loop over blocks stays as it
-// is; only a batch that raises some e multiplies the sums once.  Measured, without
-// and with exponents: 8192 tokens, 4096 -> 14336, 332 and 335 us; 2000 tokens,
-// 14336 -> 4096, 89.2 and 89.8; one token, 4096 -> 4096, 6.13 and 6.27; 128 tokens,
-// 4096 -> 14336, 17.5 and 17.3.  (A second loop with the products in fp64 took that
-// loop's registers: 385 and 149 us for the first two.)
+// lies from 2^-120 to 2^100, else a multiple of 64 that brings it to 2^-32 .. 2^32.
+// Once a product has been seen e only rises, so a product's rounding is at most
+// 2^-30 of the token's largest (2^-150 against 2^-120).  The epilogue's loop over
+// blocks stays as it is; only a batch that raises some e multiplies the sums once.
+// Measured, without and with exponents: 8192 tokens, 4096 -> 14336, 332 and 335 us;
+// 2000 tokens, 14336 -> 4096, 89.0 and 90.0; one token, 4096 -> 4096, 6.15 and 6.28;
+// 128 tokens, 4096 -> 14336, 17.4 and 17.3.  (A second loop with the products in fp64
+// took that loop's registers: 385 and 149 us for the first two.)  Where e is not 0 the
+// scales' warp forms its products in fp64 from global memory: 2000 tokens, 4096 ->
+// 14336, with every product below 2^-120, take 1016 us for 87.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -27,7 +29,7 @@
 
 namespace forge {
 
-constexpr float kScalesLow = 0x1p-90f, kScalesHigh = 0x1p100f;
+constexpr float kScalesLow = 0x1p-120f, kScalesHigh = 0x1p100f;
 // Bits of a batch's word in shared memory: the sums take factors; some e is not 0.
 constexpr uint32_t kBatchFactors = 1u, kBatchExponents = 2u;
 

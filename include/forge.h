@@ -519,7 +519,8 @@ forge_status forge_fp8_roll_scales(forge_fp8_scales* scales, int n, float headro
  * forge_rmsnorm: the residual's addition, the RMS norm and its 8-bit output
  * in one pass:
  *   h = x + residual (h = x if residual is NULL), rstd = 1 / sqrt(mean(h^2) + eps),
- *   y = h * rstd * gain, per row of `cols` columns, in fp32.
+ *   y = h * rstd * gain, per row of `cols` columns, in fp32 (a row whose mean
+ *   square leaves fp32's range, entries above about 10^19, comes out as zeros).
  *   x, residual [rows, cols] bf16; gain [cols] fp32 or bf16.
  *   Outputs, each written if not NULL: sum [rows, cols] = h rounded to bf16
  *   (may be the same buffer as x or residual), y [rows, cols] bf16, codes and

@@ -70,12 +70,12 @@ forge_status check_rows(int64_t rows, int64_t cols, int64_t max_cols) {
 // Up to 128 tokens the outputs lie along M (forge_gemm_b128_few.cu) and the
 // reduction is split over as many CTAs of a cluster as leave at most one CTA
 // an SM, with two blocks each at least: one token, 4096 -> 4096 (32 tiles),
-// takes 9.9 us unsplit, 7.3 on two CTAs, 6.1 on four and 6.3 on eight (two CTAs
-// an SM); 4096 -> 14336 (112 tiles) 12.3 unsplit, 12.8 on two and 16.2 on four.
+// takes 10.8 us unsplit, 8.8 on two CTAs, 6.7 on four and 13.5 on eight (two
+// waves); 4096 -> 14336 (112 tiles) 13.0 unsplit, 18.1 on two and 25.4 on four.
 // Beyond, 256 x 256 on CTA pairs or 128 x 128 on single CTAs, by the waves
 // each takes and the measured cycles of a block (770 and 490): 512 tokens,
-// 4096 -> 4096, take 17.0 us on pairs and 13.5 on single CTAs, 1024 tokens
-// 18.3 and 22.5.  The tiles of the last waves stay whole: cut along the reduction
+// 4096 -> 4096, take 17.8 us on pairs and 14.2 on single CTAs, 1024 tokens
+// 19.2 and 23.2.  The tiles of the last waves stay whole: cut along the reduction
 // and shared out evenly, with the parts joined through memory, 2000 tokens,
 // 14336 -> 4096 (128 tiles on 76 pairs), took 98 us in place of 91, since pairs
 // at different depths no longer read the operands together.

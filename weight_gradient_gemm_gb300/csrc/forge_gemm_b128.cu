@@ -21,13 +21,13 @@
 // hold up to 128 output values.  Every wait is bounded, as in forge_gemm.cuh.
 //
 // What bounds it: a pair takes 720 to 770 cycles for a block of 128 whose
-// products take 512.  8192 tokens, 4096 -> 14336: 333 us (2.9 PFLOP/s; 388 in
+// products take 512.  8192 tokens, 4096 -> 14336: 335 us (2.9 PFLOP/s; 386 in
 // long runs, under the power limit) where twice the bf16 rate would take 253.
 // 294 of them stay without any work in the epilogue: with two TMEM buffers a
 // piece the tensor core waits for the hand-off to the epilogue and back.  The
 // rest is the adding up, half of the SM's issue slots.  2000 tokens, 14336 ->
 // 4096: 90 us, 128 tiles on 76 pairs, the second wave 68 % full; 512 tokens,
-// 4096 -> 4096: 13.5 us.  Tried and slower: 16 epilogue warps (405 us where 8
+// 4096 -> 4096: 13.7 us, one wave of single CTAs at 490 cycles a block.  Tried and slower: 16 epilogue warps (405 us where 8
 // took 362), the two issuers in a fixed turn (354 for 333), waits that poll.
 #include <cuda_bf16.h>
 

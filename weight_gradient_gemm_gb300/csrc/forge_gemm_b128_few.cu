@@ -14,10 +14,11 @@
 //
 // Bound by the weight's bytes and, below about 10 MB, by the 3.5 us that a launch
 // takes from its first load to its last store.  4096 -> 14336 (58.7 MB, 8.7 us at
-// 6.79 TB/s): 12.1 us for one token, 12.4 for 16, 14.4 for 64, 17.5 for 128, where
-// every CTA reads all the tokens again (117 MB through L2; without any adding up
-// 15.6 us); 4096 -> 4096 (2.5 us): 5.9, 6.2, 7.1 and 9.4; 4096 -> 1024: 3.8 for
-// one.
+// 6.79 TB/s): 12.8 us a call for one token, 13.4 for 16, 14.8 for 64, 17.3 for 128,
+// where every CTA reads all the tokens again (117 MB through L2; without any adding
+// up 2 us less); 4096 -> 4096 (2.5 us): 6.3, 6.9, 8.0 and 9.4; the input gradient
+// 14336 -> 4096: 13.4, 13.6, 14.4 and 17.9.  4096 -> 128256, with more tiles than SMs
+// and two CTAs on each (525 MB, 77.4 us): 86.6 for one token, 90.9 for 32.
 //
 // Warp roles: 0 loads (TMA), 1 issues the MMAs, 2 multiplies the scales, from
 // 4 on the epilogue (the 32 outputs of a TMEM lane quadrant and up to 32
@@ -139,8 +140,8 @@ __global__ void __launch_bounds__(Few<NT>::THREADS, NT <= 64 ? 2 : 1)
   // While the kernel before still runs, the weight's first blocks are asked for
   // as far as L2.  (L2 is where all writes meet: were that kernel writing them,
   // the loads after the wait would still find what it wrote.)  One token, norm,
-  // 4096 -> 14336, quantiser, 14336 -> 4096: 28.6 -> 27.9 us; of up to 128 tokens
-  // four blocks gain more than half the share (64 tokens: 32.0 and 32.6).
+  // 4096 -> 14336, quantiser, 14336 -> 4096: 28.1 us, 28.8 without; of up to 128
+  // tokens four blocks gain more than half the share (64 tokens: 32.0 and 32.6).
   if (warp == 0 && lane == 0) {
     const int ahead = NT <= 16 ? max(4, (ke - kb) / 2) : 4;
     for (int k = kb; k < min(ke, kb + ahead); ++k)

@@ -56,13 +56,16 @@ __device__ __forceinline__ void load_gain8(const void* gain, int bf16, int v, fl
 //   rows): the copies keep HBM busy through the reductions.
 // Memory bounds all three: a row is read once and written once.  Measured, with
 // the time of the bytes a call must move at the copy rate, 6.79 TB/s, in
-// brackets:
-//   8191 x 4096, x + residual -> sum, y       43.7 us (39.5)
-//   the same with codes and scales            50.3 us (44.6)
-//   8192 x 8192                               89.7 us (79.1)
-//   8192 x 1024                               12.4 us (9.9)
-//   8192 x 512 (a warp per row)                7.4 us (4.9)
-//   512 x 4096 (a block per row)               4.6 us (2.5), launch and tail
+// brackets (calls back to back on inputs that together are larger than L2):
+//   8191 x 4096, x + residual -> sum, y       43.6 us (39.5)
+//   the same with codes and scales            50.2 us (44.6)
+//   8192 x 8192                               88.8 us (79.1)
+//   8192 x 1024                               12.8 us (9.9)
+//   8192 x 512 (a warp per row)                7.7 us (4.9): a warp has one row in
+//                                              flight, none between its reduction
+//                                              and its stores
+//   512 x 4096 (a block per row)               5.0 us (2.5), launch and tail; 3.4
+//                                              with its inputs in L2
 //   1 x 4096                                   1.9 us: the latency of a launch,
 //                                              the loads and one reduction
 // With a block per row throughout, 8191 x 4096 took 55 us: between its reads and
@@ -312,9 +315,10 @@ __global__ void __launch_bounds__(1024, 1) rmsnorm_stream_kernel(const NormArgs 
 //   (from L2) and add down 16 or 32 columns; one launch;
 //   many rows: a block adds its rows in registers and leaves one partial row,
 //   and rmsnorm_dgain_kernel adds those.
-// Bound by memory: 8192 x 4096 with dsum, 268 MB, 46.5 us with the second
-// launch (39.5 at the copy rate; a block per row 71); 512 x 4096 6.5 us (2.5),
-// 333 x 1032 2.6 us, 1 x 4096 1.8.
+// Bound by memory: 8192 x 4096 with dsum, 268 MB, 47.2 us with the second
+// launch (39.5 at the copy rate; a block per row 71); without dsum 512 x 4096
+// 5.4 us (1.9), 2048 x 4096 14.2 (7.4), 8192 x 1024 14.8 (7.4), 333 x 1032 2.9 a
+// call, the launch.
 // One vector's share of the row's dot product; dgain's terms are added to dg.
 __device__ __forceinline__ float bwd_dot(uint4 hv, uint4 dv, const float (&g)[8], float rstd,
                                          float (&dg)[8]) {
@@ -598,7 +602,7 @@ __device__ __forceinline__ float amax8(uint4 v) {
 //
 // Blocks of 1 x 128: 8 lanes per block, two vectors of 8 columns a lane, so
 // that one reduction and one pair of divisions serve 16 of a lane's values.
-// 8192 x 14336: 52.1 us, the copy rate (100 us with 16 lanes a block, one block
+// 8192 x 14336: 51.8 us, the copy rate (100 us with 16 lanes a block, one block
 // at a time: bound by its instructions and by loads that waited for the block
 // before).  No persistent walk, no barrier: the blocks' many independent loads
 // keep HBM busy by themselves.
@@ -641,7 +645,8 @@ __global__ void __launch_bounds__(256) quantize_blocks_kernel(const uint4* __res
   }
 }
 
-// Any row length: the last block of a row may be partial.
+// Any row length: the last block of a row may be partial.  One block a lane group in
+// flight: 8192 x 4104 21.3 us (15.0 at the copy rate), 8192 x 2880 15.1 (10.5).
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const uint4* __restrict__ x,
                                                             uint2* __restrict__ codes,
                                                             float* __restrict__ scales,
@@ -677,10 +682,11 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const uint4* __restr
 // Blocks of 128 x 128: persistent CTAs, four an SM, each with one block's 32 KB
 // copied ahead by TMA (which fills zeros outside the matrix).  A block is read
 // into registers before its maximum is formed, so the next copy starts at that
-// reduction's barrier and runs under the codes and stores.  14336 x 4096: 28.9 us,
-// 6.1 TB/s (33.2 us with loads into registers, where a CTA's loads, barrier and
+// reduction's barrier and runs under the codes and stores.  14336 x 4096: 30.0 us,
+// 5.9 TB/s (33.2 us with loads into registers, where a CTA's loads, barrier and
 // stores follow one another; more copies in flight only meet the stores: two
-// slots, three CTAs an SM, 29.9 us); 4096 x 4096 9.6 us (11.6); 1000 x 4112 4.1.
+// slots, three CTAs an SM, 29.9 us where one took 28.9); 4096 x 4096 10.4 us;
+// 1000 x 4112 4.5, or 3.5 with its values in L2.
 // A wait that runs out records its error and lets the CTA run on, as in RowRing.
 constexpr int kTileBytes = kBlock * kBlock * 2;
 __global__ void __launch_bounds__(256)
@@ -800,9 +806,9 @@ RowPlan row_plan(int64_t rows, int cols, int streams, bool backward, int num_sms
     return p;
   }
   // Every row in flight at once: where a vector a thread leaves rows for a second
-  // wave, two vectors and half the threads (512 x 4096: 4.6 us, 5.8 with one
-  // vector; 304 rows the same, 152 rows 3.0 and 2.8).  Where the backward pass
-  // leaves partial rows, few blocks.
+  // wave, two vectors and half the threads (512 x 4096, inputs in L2: 3.4 us;
+  // when it was chosen 4.6, and 5.8 with one vector; 304 rows the same, 152 rows
+  // 3.0 and 2.8).  Where the backward pass leaves partial rows, few blocks.
   p.direct = backward && rows <= direct_rows;
   if ((!backward || p.direct) && p.vpt == 1 && rows > per_sm * num_sms) {
     p.vpt = 2;

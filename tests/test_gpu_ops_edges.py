@@ -76,6 +76,35 @@ def test_quantize_keeps_the_sign_of_zero(block_rows):
     assert torch.equal(torch.signbit(codes.float()), torch.signbit(x))
 
 
+# ---------------------------------------------------------------- the norm's codes
+@pytest.mark.parametrize("rows,cols", [(4096, 4096), (600, 4096), (9000, 512), (3000, 1032),
+                                       (500, 8328), (60, 32768), (20000, 136)])
+@pytest.mark.parametrize("gain", ["fp32", "bf16", "one"])
+@pytest.mark.parametrize("res", [False, True])
+def test_rmsnorm_codes(rows, cols, gain, res):
+    # rstd is common to a row: the codes are those of h gain, in fp64 exact here.  The
+    # kernel's quotients carry at most six roundings (h rstd gain, its amax, their
+    # reciprocal, the product): within 6 x 2^-24 of halfway either code may be taken
+    g = torch.Generator(device=DEV).manual_seed(rows + cols)
+    x = torch.randn((rows, cols), generator=g, device=DEV).bfloat16()
+    r = torch.randn((rows, cols), generator=g, device=DEV).bfloat16() if res else None
+    w = torch.ones(cols, device=DEV) if gain == "one" else \
+        1 + 0.2 * torch.randn(cols, generator=g, device=DEV)
+    w = w.to(torch.bfloat16 if gain == "bf16" else torch.float32)
+    codes, scales = F.alloc_b128(rows, cols)
+    F.rmsnorm(x, w, eps=1e-5, residual=r, codes=codes, scales=scales)
+    ok()
+    h = x.float() + r.float() if res else x.float()
+    y = torch.zeros((rows, -(-cols // 128) * 128), dtype=torch.float64, device=DEV)
+    y[:, :cols] = h.double() * w.double()
+    a = y.view(rows, -1, 128).abs().amax(2).repeat_interleave(128, 1)[:, :cols]
+    q = y[:, :cols] * 448 / a
+    step = torch.exp2(torch.clamp(torch.frexp(q)[1] - 1, min=-6).double() - 3)
+    got = codes.double()
+    bad = (got - q).abs() > step / 2 + q.abs() * 6 * 2.0 ** -24
+    assert not bad.any(), int(bad.sum())
+
+
 # ---------------------------------------------------------------- products
 def product_case(seed, op, bt, d_in, d_out, codes=256):
     """Random operands of one product: code bytes below `codes` (with both signs) and

@@ -1,6 +1,7 @@
 // The C ABI of libforge: argument validation, TMA descriptor encoding (cached),
 // tile configuration, launches and the device error word.
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 #include <cfloat>
 #include <cmath>
@@ -98,7 +99,7 @@ struct DeviceInfo {
 std::mutex g_mu;
 DeviceInfo g_dev[kMaxDevices];
 uint64_t g_wait_limit_ns = 2000000000ull;
-int g_drop_first_arrival = 0;
+std::atomic<int> g_drop_first_arrival{0};
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                                    const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
@@ -765,11 +766,9 @@ forge_status adamw_run(const void* dW, forge_dtype dw_dtype, const float* coef, 
              : FORGE_ERR_LAUNCH;
 }
 
+// (usually one load: calls on few rows take a few microseconds)
 int take_drop_flag() {
-  std::lock_guard<std::mutex> lk(g_mu);
-  const int f = g_drop_first_arrival;
-  g_drop_first_arrival = 0;
-  return f;
+  return g_drop_first_arrival.load(std::memory_order_relaxed) ? g_drop_first_arrival.exchange(0) : 0;
 }
 
 }  // namespace
@@ -1615,7 +1614,6 @@ void forge_set_wait_limit_ns(uint64_t ns) {
 }
 
 void forge_debug_drop_first_arrival(int enable) {
-  std::lock_guard<std::mutex> lk(g_mu);
   g_drop_first_arrival = enable ? 1 : 0;
 }
 

@@ -176,3 +176,34 @@ def test_products_of_scales_outside_fp32(tune, op, bt, how, case):
         sw *= 2.0 ** 39
     out = check(op, a, sa, w, sw, k, n)
     assert torch.isfinite(out).all() and float(out.abs().max()) > 0
+
+
+@pytest.mark.parametrize("op", ["linear", "dgrad"])
+@pytest.mark.parametrize("bt,how", FORMS)
+@pytest.mark.parametrize("zero", ["weight", "tokens", "blocks"])
+def test_products_of_zeros(tune, op, bt, how, zero):
+    # zero scales: a weight that has not left its initial zeros, masked tokens, and
+    # blocks of both that never meet another
+    tune(**how)
+    (a, sa), (w, sw), k, n = product_case(91, op, bt, 2576, 2320)
+    if zero == "weight":
+        w.view(torch.uint8).zero_()
+        sw.zero_()
+    elif zero == "tokens":
+        a.view(torch.uint8)[::2] = 0
+        sa[::2] = 0
+    else:
+        nb = sa.shape[1]
+        for b in range(nb):
+            part = a.view(torch.uint8)[:, b * 128:(b + 1) * 128]
+            if b % 2:
+                part.zero_()
+                sa[:, b] = 0
+            elif op == "linear":
+                w.view(torch.uint8)[:, b * 128:(b + 1) * 128] = 0
+                sw[:, b] = 0
+            else:
+                w.view(torch.uint8)[b * 128:(b + 1) * 128] = 0
+                sw[b] = 0
+    out = check(op, a, sa, w, sw, k, n)
+    assert bool((out[::2] == 0).all()) and (zero == "tokens" or not out.any())

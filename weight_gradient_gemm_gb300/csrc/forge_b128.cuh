@@ -39,8 +39,8 @@ struct TokenExponents {
   uint32_t e = 0u, seen = 0u;
 
   // Takes in token j's products of a batch, of which `most` is the largest; `any`:
-  // the token has a scale other than zero (its products may all be lost).  True
-  // where the batch has to go through scales_apart.
+  // it and the weight have a scale other than zero (the products may all be lost).
+  // True where the batch has to go through scales_apart.
   __device__ __forceinline__ bool add(int j, float most, bool any) {
     const uint32_t bit = 1u << j;
     if (most > kScalesHigh || (most < kScalesLow && any && !(seen & bit))) return true;

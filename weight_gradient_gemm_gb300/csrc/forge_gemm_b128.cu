@@ -27,8 +27,9 @@
 // piece the tensor core waits for the hand-off to the epilogue and back.  The
 // rest is the adding up, half of the SM's issue slots.  2000 tokens, 14336 ->
 // 4096: 90 us, 128 tiles on 76 pairs, the second wave 68 % full; 512 tokens,
-// 4096 -> 4096: 13.7 us, one wave of single CTAs at 490 cycles a block.  Tried and slower: 16 epilogue warps (405 us where 8
-// took 362), the two issuers in a fixed turn (354 for 333), waits that poll.
+// 4096 -> 4096: 13.7 us, one wave of single CTAs at 490 cycles a block.  Tried and
+// slower: 16 epilogue warps (405 us where 8 took 362), the two issuers in a fixed turn
+// (354 for 333), waits that poll.
 #include <cuda_bf16.h>
 
 #include "forge_b128.cuh"
@@ -348,6 +349,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
                                ? a.sw[static_cast<int64_t>(lw) * a.sw_n +
                                       static_cast<int64_t>(lk) * a.sw_k]
                                : 0.0f;
+          const bool any_w = __any_sync(0xffffffffu, rl != 0.0f);
           const int b = cnt & 1;
           const bool good =
               wait_bounded(bar_sempty(b), ((cnt >> 1) & 1u) ^ 1u, wc, kSiteLoaderEmpty);
@@ -367,7 +369,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
             }
           bool apart = false;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) apart |= te.add(j, most[j], any[j] != 0u);
+          for (int j = 0; j < 4; ++j) apart |= te.add(j, most[j], any_w && any[j] != 0u);
           uint32_t word = 0u;
           if (__any_sync(0xffffffffu, apart))
             word = scales_apart<T::NWB, kBM, T::SC_BATCH>(

@@ -215,6 +215,7 @@ __global__ void __launch_bounds__(Few<NT>::THREADS, NT <= 64 ? 2 : 1)
       // a lane for each of the batch's weight blocks
       const float rl = a.sw[static_cast<int64_t>(tile) * a.sw_n +
                             static_cast<int64_t>(min(k0 + (lane & 7), ke - 1)) * a.sw_k];
+      const bool any_w = __any_sync(0xffffffffu, rl != 0.0f);
       float rw[T::SC_BATCH];
 #pragma unroll
       for (int i = 0; i < T::SC_BATCH; ++i) rw[i] = __shfl_sync(0xffffffffu, rl, i);
@@ -230,7 +231,7 @@ __global__ void __launch_bounds__(Few<NT>::THREADS, NT <= 64 ? 2 : 1)
           rx[j][i] *= rw[i];
           most = fmaxf(most, fabsf(rx[j][i]));
         }
-        apart |= te.add(j, most, any != 0u);
+        apart |= te.add(j, most, any_w && any != 0u);
       }
       const bool good = wait_bounded(bar_sempty(b), ph, wc, kSiteLoaderEmpty);
       if (!__all_sync(0xffffffffu, good)) break;

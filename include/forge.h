@@ -621,6 +621,196 @@ forge_status forge_adamw_clip(const void* dW, forge_dtype dw_dtype, const float*
                               float lr, float beta1, float beta2, float eps, float weight_decay,
                               int64_t step, forge_moment_fmt fmt, forge_stream stream);
 
+/*
+ * The operators between a layer's 16-bit products: the forward product with its
+ * epilogue, the epilogue's gradient (the dY that forge_wgrad and forge_dgrad read),
+ * dropout, rotary positions, and the norm of queries and keys with the rotation.
+ */
+
+/* Activations.  In fp32; a derivative at the corner of ReLU is 0.  GELU is
+ * z (1 + erf(z / sqrt(2))) / 2, GELU_TANH z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2,
+ * SILU z / (1 + e^-z). */
+typedef enum {
+  FORGE_ACT_NONE = 0,
+  FORGE_ACT_RELU = 1,
+  FORGE_ACT_GELU = 2,
+  FORGE_ACT_GELU_TANH = 3,
+  FORGE_ACT_SILU = 4
+} forge_activation;
+
+/*
+ * Dropout from a counter-based generator.  The mask is never stored: the same call
+ * arguments give the same mask, so the backward pass forms it again.
+ * Element (r, c) of a matrix [rows, cols] is element j = i % 8 of block b = i / 8,
+ * i = r cols + c.  The block's 128 random bits are Philox4x32-10 (Salmon et al. 2011)
+ * of the counter (b mod 2^32, b / 2^32, o mod 2^32, o / 2^32) with the key (seed mod
+ * 2^32, seed / 2^32), o = offset + *counter mod 2^64; the element takes bits
+ * 16 (j % 2) .. 16 (j % 2) + 15 of word j / 2 as a number u.  With T = p 65536 rounded
+ * to the nearest whole number (ties to even, at most 65535), it becomes 0 if u < T (also
+ * where it was NaN or infinite) and is multiplied by 65536 / (65536 - T) otherwise.  Give
+ * each use its own seed or offset.  `counter` (device, 8-byte aligned, or NULL: 0) is
+ * read when the kernel runs, so that a replayed graph can draw new masks.
+ */
+typedef struct {
+  float p;                  /* in [0, 1): the share dropped; 0: no dropout               */
+  uint64_t seed, offset;
+  const uint64_t* counter;
+} forge_drop;
+
+/* What follows the product of forge_linear_bf16; all zero: nothing. */
+typedef struct {
+  const void* bias;         /* [d_out] fp32 or bf16, or NULL                             */
+  forge_dtype bias_dtype;
+  forge_activation act;
+  const void* mul;          /* [bt, d_out] bf16 (the other half of a gated pair), or NULL */
+  const void* residual;     /* [bt, d_out] bf16, or NULL                                 */
+  void* z;                  /* [bt, d_out] bf16, written: Z for the backward pass, or NULL */
+  forge_drop drop;          /* over the elements of [bt, d_out]                          */
+} forge_epilogue;
+
+/*
+ * forge_linear_bf16: the forward product of a linear layer with its epilogue,
+ *   Z = X W^T + bias,   Y = residual + drop(act(Z) * mul),
+ * accumulated and computed in fp32 and rounded once to each output (act is taken of the
+ * unrounded Z).  X [bt, d_in], W [d_out, d_in] bf16; Y [bt, d_out] bf16 or fp32.
+ * `epilogue` (host memory, read before the call returns) may be NULL.
+ * d_in, d_out multiples of 8; pointers 16-byte aligned.  Y in bf16 may be the same buffer
+ * as mul or residual; otherwise no output may overlap an input or another output.  bt = 0
+ * does nothing.  The same result on every run.  Nothing is allocated.  Asynchronous on
+ * `stream`.  FORGE_ERR_FORMAT for an unknown dtype or activation, FORGE_ERR_HYPER for p
+ * outside [0, 1).
+ */
+forge_status forge_linear_bf16(const void* X, const void* W, void* Y, forge_dtype y_dtype,
+                               const forge_epilogue* epilogue, int64_t bt, int64_t d_in,
+                               int64_t d_out, forge_stream stream);
+
+/*
+ * forge_epilogue_backward: the gradients of that epilogue, in fp32 from the stored Z:
+ *   dA = drop(dY),  dmul = dA * act(Z),  dZ = dA * mul * act'(Z),  dbias = sum over rows of dZ.
+ *   dY [rows, cols] bf16; Z [rows, cols] bf16 (may be NULL where act is FORGE_ACT_NONE and
+ *   dmul is not asked for); mul [rows, cols] bf16 or NULL (1); drop as in the forward call
+ *   (NULL: none).  Outputs, at least one, each written if not NULL: dZ, dmul [rows, cols]
+ *   bf16 (dmul only with mul), dbias [cols] fp32, of the unrounded dZ.  The residual's
+ *   gradient is dY itself.
+ * dZ and dmul may take the place of dY, Z or mul (the same buffer).  dbias needs `workspace`
+ * (device, 16-byte aligned) of at least forge_epilogue_backward_workspace_bytes(rows, cols)
+ * (FORGE_ERR_SHAPE if smaller; 0 bytes: it may be NULL), not used by another call until this
+ * one has run.  The rows are added in a fixed order: the same result on every run.  rows = 0
+ * writes zeros to dbias.  cols is a multiple of 8, rows * cols at most 2^40.  Asynchronous
+ * on `stream`.
+ */
+forge_status forge_epilogue_backward(const void* dY, const void* Z, const void* mul,
+                                     forge_activation act, const forge_drop* drop, void* dZ,
+                                     void* dmul, float* dbias, int64_t rows, int64_t cols,
+                                     void* workspace, size_t workspace_bytes,
+                                     forge_stream stream);
+size_t forge_epilogue_backward_workspace_bytes(int64_t rows, int64_t cols);
+
+/*
+ * forge_dropout: y = residual + drop(x) in fp32, rounded once to bf16.  x, y [rows, cols]
+ * bf16, residual [rows, cols] bf16 or NULL (0).  The gradient of x is the same call on y's
+ * gradient without the residual, whose gradient is y's.  y may be the same buffer as x or
+ * residual.  cols is a multiple of 8, rows * cols at most 2^40.  rows = 0 does nothing.
+ * Asynchronous on `stream`.
+ */
+forge_status forge_dropout(const void* x, const void* residual, void* y, const forge_drop* drop,
+                           int64_t rows, int64_t cols, forge_stream stream);
+
+/* Which elements of a head turn together. */
+typedef enum {
+  FORGE_ROPE_HALF = 0,         /* elements i and i + dim / 2                             */
+  FORGE_ROPE_INTERLEAVED = 1   /* elements 2 i and 2 i + 1                               */
+} forge_rope_layout;
+
+/* How a table of frequencies is stretched for contexts longer than the one trained on. */
+typedef enum {
+  FORGE_ROPE_SCALE_NONE = 0,
+  FORGE_ROPE_SCALE_LINEAR = 1,  /* every frequency divided by factor                     */
+  FORGE_ROPE_SCALE_NTK = 2,     /* theta multiplied by factor^(dim / (dim - 2))          */
+  FORGE_ROPE_SCALE_LLAMA3 = 3,  /* by the turns a pair makes over `context`: at most low,
+                                   divided by factor; at least high, kept; mixed between  */
+  FORGE_ROPE_SCALE_YARN = 4     /* mixed by the pair's index between the two that make
+                                   high and low turns; magnitude 1 + 0.1 ln(factor)       */
+} forge_rope_scale;
+typedef struct {
+  forge_rope_scale kind;
+  double factor;      /* >= 1                                                            */
+  double context;     /* LLAMA3, YARN: positions of the context trained on                */
+  double low, high;   /* LLAMA3, YARN: turns, 0 < low < high (usual: 1 and 4; 1 and 32)    */
+} forge_rope_scaling;
+
+/*
+ * forge_rope_frequencies: the table of a rotation of `dim` elements (a multiple of 8, at
+ * most 256), on the host: freqs[i], i < dim / 2, is the turns per position of pair i,
+ * theta^(-2 i / dim) / (2 pi) with the scaling applied (NULL: none), as a fraction of 2^64
+ * rounded to the nearest; *magnitude is the factor of the rotated values.  The caller
+ * copies the table to the device once.  theta > 1.
+ */
+forge_status forge_rope_frequencies(int dim, double theta, const forge_rope_scaling* scaling,
+                                    uint64_t* freqs, float* magnitude);
+
+/* A rotation.  The first `dim` elements of each head turn, the others pass. */
+typedef struct {
+  const uint64_t* freqs;      /* device [dim / 2] (see forge_rope_frequencies)             */
+  const int64_t* positions;   /* device [tokens], any values; NULL: 0, 1, 2, ...           */
+  float magnitude;            /* factor of the rotated values; finite                     */
+  int32_t dim;                /* a multiple of 8, at most head_dim                        */
+  forge_rope_layout layout;
+} forge_rotation;
+
+/* The heads of one kind (queries or keys) of a call, bf16.  Element (token, head, i) of x
+ * lies at x + token * x_token + head * x_head + i; strides in elements, not negative,
+ * multiples of 8.  Unused fields are ignored. */
+typedef struct {
+  const void* x;              /* input (forge_qk_norm_rope_backward: the forward input)    */
+  void* y;                    /* output (backward: the gradient of x)                     */
+  int64_t x_token, x_head, y_token, y_head;
+  int64_t heads;
+  const void* gain;           /* forge_qk_norm_rope and its backward pass: [head_dim]      */
+  const void* dy;             /* backward: the gradient of the rotated heads              */
+  int64_t dy_token, dy_head;
+  float* dgain;               /* backward: [head_dim] fp32, overwritten, or NULL          */
+} forge_heads;
+
+/*
+ * forge_rope: rotary positions on n (1 or 2) kinds of heads in one pass.  At position p,
+ * with the angle w = 2 pi p freqs[i] / 2^64 (formed exactly modulo a turn), pair (a, b)
+ * becomes magnitude (a cos w - b sin w, b cos w + a sin w), in fp32, rounded once.  With
+ * `inverse` the angle is -w: the gradient of the call without it.
+ * head_dim is a multiple of 8, at most 256.  Pointers of heads 16-byte aligned.  y may be
+ * the same view as its own x; otherwise no output may overlap an input or another output
+ * (interleaved views of one buffer, as queries and keys in the fused output of their
+ * projections, do not), and no element of y may lie in two places.  tokens = 0 or heads = 0
+ * does nothing.  Asynchronous on `stream`.
+ */
+forge_status forge_rope(const forge_heads* sets, int n, const forge_rotation* rot, int inverse,
+                        int64_t tokens, int64_t head_dim, forge_stream stream);
+
+/*
+ * forge_qk_norm_rope: the RMS norm of each head, then the rotation, in one pass:
+ *   m = x gain / sqrt(mean(x^2) + eps) over head_dim,   y = rotation of m,
+ * in fp32, rounded once.  gain [head_dim] fp32 or bf16 (16-byte aligned), one for the
+ * queries and one for the keys.  Otherwise as forge_rope; eps >= 0.
+ */
+forge_status forge_qk_norm_rope(const forge_heads* sets, int n, forge_dtype gain_dtype, float eps,
+                                const forge_rotation* rot, int64_t tokens, int64_t head_dim,
+                                forge_stream stream);
+
+/*
+ * forge_qk_norm_rope_backward: its gradients.  With m' the gradient dy turned back,
+ * xh = x / sqrt(mean(x^2) + eps) and u = m' gain:
+ *   y = (u - xh mean(u xh)) / sqrt(mean(x^2) + eps),  dgain = sum over tokens and heads of m' xh.
+ * y may be the same view as its own x or dy.  With a dgain, `workspace` (device, 16-byte
+ * aligned) of at least forge_qk_norm_rope_backward_workspace_bytes(head_dim), not used by
+ * another call until this one has run.  Sums in a fixed order: the same result on every
+ * run.  No tokens or heads: zeros to dgain.  Otherwise as forge_qk_norm_rope.
+ */
+forge_status forge_qk_norm_rope_backward(const forge_heads* sets, int n, forge_dtype gain_dtype,
+                                         float eps, const forge_rotation* rot, int64_t tokens,
+                                         int64_t head_dim, void* workspace, size_t workspace_bytes,
+                                         forge_stream stream);
+size_t forge_qk_norm_rope_backward_workspace_bytes(int64_t head_dim);
+
 /* Synchronises `stream`, then returns and clears the device error word of the
  * current device: FORGE_OK, FORGE_ERR_DEVICE_TIMEOUT if a kernel gave up on a
  * bounded wait since the last call, or FORGE_ERR_DEVICE_CONFIG.  FORGE_ERR_CUDA

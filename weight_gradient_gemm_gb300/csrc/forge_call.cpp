@@ -33,6 +33,12 @@ struct {
   decltype(&forge_dgrad_fp8) dgrad;
   decltype(&forge_grad_norm) grad_norm;
   decltype(&forge_adamw_clip) adamw_clip;
+  decltype(&forge_linear_bf16) linear_bf16;
+  decltype(&forge_epilogue_backward) epilogue_backward;
+  decltype(&forge_dropout) dropout;
+  decltype(&forge_rope) rope;
+  decltype(&forge_qk_norm_rope) qk_norm_rope;
+  decltype(&forge_qk_norm_rope_backward) qk_norm_rope_backward;
 } lib;
 
 // One call's view of its arguments: `bad` once a check has failed.
@@ -43,12 +49,18 @@ struct Args {
   int dev = -1;
 
   const at::Tensor* tensor(int i) {
+    const at::Tensor* t = strided(i);
+    if (t && !t->is_contiguous()) bad = true;
+    return bad ? nullptr : t;
+  }
+  // A tensor of any strides.
+  const at::Tensor* strided(int i) {
     if (bad || !THPVariable_Check(a[i])) {
       bad = true;
       return nullptr;
     }
     const at::Tensor& t = THPVariable_Unpack(a[i]);
-    if (!t.defined() || !t.is_cuda() || t.layout() != c10::kStrided || !t.is_contiguous()) {
+    if (!t.defined() || !t.is_cuda() || t.layout() != c10::kStrided) {
       bad = true;
       return nullptr;
     }
@@ -105,6 +117,11 @@ struct Args {
       bad = true;
     }
     return v;
+  }
+  // One of a few small numbers; -1 for anything far from them.
+  int choice(int i) {
+    const int64_t v = integer(i);
+    return v >= 0 && v < 256 ? static_cast<int>(v) : -1;
   }
   // None: the device's current stream; else a stream's address.
   void* stream(int i) {
@@ -164,12 +181,18 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
                  reinterpret_cast<void**>(&lib.rmsnorm_backward),
                  reinterpret_cast<void**>(&lib.quantize), reinterpret_cast<void**>(&lib.linear),
                  reinterpret_cast<void**>(&lib.dgrad), reinterpret_cast<void**>(&lib.grad_norm),
-                 reinterpret_cast<void**>(&lib.adamw_clip)};
-  if (n != 7) {
-    PyErr_SetString(PyExc_TypeError, "bind takes seven addresses");
+                 reinterpret_cast<void**>(&lib.adamw_clip),
+                 reinterpret_cast<void**>(&lib.linear_bf16),
+                 reinterpret_cast<void**>(&lib.epilogue_backward),
+                 reinterpret_cast<void**>(&lib.dropout), reinterpret_cast<void**>(&lib.rope),
+                 reinterpret_cast<void**>(&lib.qk_norm_rope),
+                 reinterpret_cast<void**>(&lib.qk_norm_rope_backward)};
+  constexpr int kFns = sizeof(fn) / sizeof(fn[0]);
+  if (n != kFns) {
+    PyErr_Format(PyExc_TypeError, "bind takes %d addresses", kFns);
     return nullptr;
   }
-  for (int i = 0; i < 7; ++i) {
+  for (int i = 0; i < kFns; ++i) {
     const unsigned long long v = PyLong_AsUnsignedLongLong(a[i]);
     if (PyErr_Occurred()) return nullptr;
     *fn[i] = reinterpret_cast<void*>(static_cast<uintptr_t>(v));
@@ -300,6 +323,194 @@ PyObject* adamw_clip(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// p, seed, offset, counter from argument i on (the words are taken modulo 2^64)
+forge_drop drop_of(Args& c, int i) {
+  forge_drop d{static_cast<float>(c.number(i)), 0, 0, nullptr};
+  d.seed = PyLong_AsUnsignedLongLongMask(c.a[i + 1]);
+  if (!PyErr_Occurred()) d.offset = PyLong_AsUnsignedLongLongMask(c.a[i + 2]);
+  if (PyErr_Occurred()) {
+    PyErr_Clear();
+    c.bad = true;
+  }
+  d.counter = static_cast<const uint64_t*>(c.opt(i + 3, 1, -1, at::kLong));
+  return d;
+}
+
+// X, W, Y, bias, act, mul, residual, Z, p, seed, offset, counter, stream
+PyObject* linear_bf16(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(a, n, 13, [](Args& c) -> long {
+    const at::Tensor *x = c.tensor(0), *w = c.tensor(1);
+    if (!x || !w || x->dim() != 2 || w->dim() != 2) return c.bad = true, -1;
+    const int64_t bt = x->size(0), d_in = x->size(1), d_out = w->size(0);
+    void *xp = c.ptr(0, bt, d_in, kBF), *wp = c.ptr(1, d_out, d_in, kBF);
+    void* y = c.ptr(2, bt, d_out, kF32, kBF);
+    const forge_dtype yt = c.dtype(2);
+    forge_epilogue e{};
+    if (c.a[3] != Py_None) {
+      e.bias = c.ptr(3, d_out, -1, kF32, kBF);
+      e.bias_dtype = c.dtype(3);
+    }
+    e.act = static_cast<forge_activation>(c.choice(4));
+    e.mul = c.opt(5, bt, d_out, kBF);
+    e.residual = c.opt(6, bt, d_out, kBF);
+    e.z = c.opt(7, bt, d_out, kBF);
+    e.drop = drop_of(c, 8);
+    void* st = c.stream(12);
+    return FORGE_CALL(lib.linear_bf16(xp, wp, y, yt, &e, bt, d_in, d_out, st));
+  });
+}
+
+// dY, dZ, Z, act, mul, dmul, dbias, p, seed, offset, counter, workspace, stream
+PyObject* epilogue_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(a, n, 13, [](Args& c) -> long {
+    const at::Tensor* t = c.tensor(0);
+    if (!t || t->dim() != 2) return c.bad = true, -1;
+    const int64_t rows = t->size(0), cols = t->size(1);
+    void *dy = c.ptr(0, rows, cols, kBF), *dz = c.opt(1, rows, cols, kBF);
+    void* z = c.opt(2, rows, cols, kBF);
+    const auto act = static_cast<forge_activation>(c.choice(3));
+    void *mul = c.opt(4, rows, cols, kBF), *dmul = c.opt(5, rows, cols, kBF);
+    float* db = static_cast<float*>(c.opt(6, cols, -1, kF32));
+    const forge_drop drop = drop_of(c, 7);
+    size_t wb;
+    void* ws = c.bytes(11, &wb);
+    void* st = c.stream(12);
+    return FORGE_CALL(
+        lib.epilogue_backward(dy, z, mul, act, &drop, dz, dmul, db, rows, cols, ws, wb, st));
+  });
+}
+
+// x, y, p, seed, offset, counter, residual, stream
+PyObject* dropout(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(a, n, 8, [](Args& c) -> long {
+    const at::Tensor* t = c.tensor(0);
+    if (!t || t->dim() != 2) return c.bad = true, -1;
+    const int64_t rows = t->size(0), cols = t->size(1);
+    void *x = c.ptr(0, rows, cols, kBF), *y = c.ptr(1, rows, cols, kBF);
+    const forge_drop drop = drop_of(c, 2);
+    void* r = c.opt(6, rows, cols, kBF);
+    void* st = c.stream(7);
+    return FORGE_CALL(lib.dropout(x, r, y, &drop, rows, cols, st));
+  });
+}
+
+// The queries (argument i) and keys (j) of a call, and where their parts are given.
+struct Heads {
+  forge_heads set[2] = {};
+  int n = 1;
+  int64_t tokens = 0, dim = 0;
+};
+// The pointer and strides of argument i, [tokens, heads, dim] with dense rows.
+void view_of(Args& c, int i, const Heads& h, int64_t heads, void** p, int64_t* token,
+             int64_t* head) {
+  const at::Tensor* t = c.strided(i);
+  if (!t) return;
+  if (t->dim() != 3 || t->size(0) != h.tokens || t->size(1) != heads || t->size(2) != h.dim ||
+      (h.dim > 1 && t->stride(2) != 1) || t->scalar_type() != kBF) {
+    c.bad = true;
+    return;
+  }
+  *p = t->data_ptr();
+  *token = t->stride(0);
+  *head = t->stride(1);
+}
+// x: the arguments of the inputs (queries, then keys), y: of the outputs.
+Heads heads_of(Args& c, int x, int y) {
+  Heads h;
+  const at::Tensor* q = c.strided(x);
+  if (!q || q->dim() != 3) {
+    c.bad = true;
+    return h;
+  }
+  h.tokens = q->size(0);
+  h.dim = q->size(2);
+  h.n = c.a[x + 1] == Py_None ? 1 : 2;
+  for (int k = 0; k < h.n && !c.bad; ++k) {
+    const at::Tensor* t = c.strided(x + k);
+    if (!t || t->dim() != 3) {
+      c.bad = true;
+      return h;
+    }
+    forge_heads& s = h.set[k];
+    s.heads = t->size(1);
+    void* xp = nullptr;
+    view_of(c, x + k, h, s.heads, &xp, &s.x_token, &s.x_head);
+    view_of(c, y + k, h, s.heads, &s.y, &s.y_token, &s.y_head);
+    s.x = xp;
+  }
+  return h;
+}
+// The gains, from argument i on, of one type.
+forge_dtype gains_of(Args& c, int i, Heads& h) {
+  h.set[0].gain = c.ptr(i, h.dim, -1, kF32, kBF);
+  const forge_dtype t = c.dtype(i);
+  const auto s = t == FORGE_DT_FP32 ? kF32 : kBF;
+  if (h.n > 1) h.set[1].gain = c.ptr(i + 1, h.dim, -1, s);
+  return t;
+}
+// freqs, positions, magnitude and layout at the arguments given.
+forge_rotation rotation_of(Args& c, int freqs, int positions, const Heads& h) {
+  forge_rotation r{};
+  const at::Tensor* f = c.tensor(freqs);
+  if (!f || f->dim() != 1 || f->size(0) > 1 << 20) {
+    c.bad = true;
+    return r;
+  }
+  r.dim = static_cast<int32_t>(2 * f->size(0));
+  r.freqs = static_cast<const uint64_t*>(c.ptr(freqs, f->size(0), -1, at::kLong));
+  r.positions = static_cast<const int64_t*>(c.opt(positions, h.tokens, -1, at::kLong));
+  r.magnitude = static_cast<float>(c.number(positions + 1));
+  r.layout = static_cast<forge_rope_layout>(c.choice(positions + 2));
+  return r;
+}
+
+// q, k, freqs, q_out, k_out, positions, magnitude, layout, inverse, stream
+PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(a, n, 10, [](Args& c) -> long {
+    const Heads h = heads_of(c, 0, 3);
+    const forge_rotation r = rotation_of(c, 2, 5, h);
+    const int inverse = PyObject_IsTrue(c.a[8]);
+    void* st = c.stream(9);
+    if (inverse < 0) return PyErr_Clear(), c.bad = true, -1;
+    return FORGE_CALL(lib.rope(h.set, h.n, &r, inverse, h.tokens, h.dim, st));
+  });
+}
+
+// q, k, q_gain, k_gain, freqs, eps, q_out, k_out, positions, magnitude, layout, stream
+PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(a, n, 12, [](Args& c) -> long {
+    Heads h = heads_of(c, 0, 6);
+    const forge_dtype gt = gains_of(c, 2, h);
+    const float eps = static_cast<float>(c.number(5));
+    const forge_rotation r = rotation_of(c, 4, 8, h);
+    void* st = c.stream(11);
+    return FORGE_CALL(lib.qk_norm_rope(h.set, h.n, gt, eps, &r, h.tokens, h.dim, st));
+  });
+}
+
+// dq, dk, q, k, q_gain, k_gain, freqs, eps, dq_out, dk_out, dq_gain, dk_gain, positions,
+// magnitude, layout, workspace, stream
+PyObject* qk_norm_rope_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(a, n, 17, [](Args& c) -> long {
+    Heads h = heads_of(c, 2, 8);
+    const forge_dtype gt = gains_of(c, 4, h);
+    for (int k = 0; k < h.n && !c.bad; ++k) {
+      forge_heads& s = h.set[k];
+      void* dy = nullptr;
+      view_of(c, k, h, s.heads, &dy, &s.dy_token, &s.dy_head);
+      s.dy = dy;
+      s.dgain = static_cast<float*>(c.opt(10 + k, h.dim, -1, kF32));
+    }
+    const float eps = static_cast<float>(c.number(7));
+    const forge_rotation r = rotation_of(c, 6, 12, h);
+    size_t wb;
+    void* ws = c.bytes(15, &wb);
+    void* st = c.stream(16);
+    return FORGE_CALL(
+        lib.qk_norm_rope_backward(h.set, h.n, gt, eps, &r, h.tokens, h.dim, ws, wb, st));
+  });
+}
+
 using FastFn = PyObject* (*)(PyObject*, PyObject* const*, Py_ssize_t);
 PyCFunction fast(FastFn f) {
   return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f));
@@ -313,6 +524,13 @@ PyMethodDef methods[] = {{"bind", fast(bind), METH_FASTCALL, nullptr},
                          {"dgrad", fast(product<true>), METH_FASTCALL, nullptr},
                          {"grad_norm", fast(grad_norm), METH_FASTCALL, nullptr},
                          {"adamw_clip", fast(adamw_clip), METH_FASTCALL, nullptr},
+                         {"linear_bf16", fast(linear_bf16), METH_FASTCALL, nullptr},
+                         {"epilogue_backward", fast(epilogue_backward), METH_FASTCALL, nullptr},
+                         {"dropout", fast(dropout), METH_FASTCALL, nullptr},
+                         {"rope", fast(rope), METH_FASTCALL, nullptr},
+                         {"qk_norm_rope", fast(qk_norm_rope), METH_FASTCALL, nullptr},
+                         {"qk_norm_rope_backward", fast(qk_norm_rope_backward), METH_FASTCALL,
+                          nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_forge_call", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};

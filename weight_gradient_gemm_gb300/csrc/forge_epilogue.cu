@@ -1,0 +1,208 @@
+// The gradient of the 16-bit product's epilogue, and dropout by itself.
+#include <cuda_bf16.h>
+
+#include "forge_internal.h"
+#include "forge_launch.cuh"
+#include "forge_layer.cuh"
+
+namespace forge {
+namespace {
+
+// ---------------------------------------------------------------- dropout
+// y = residual + drop(x), eight elements (one generator block) a thread and vector.
+// U vectors' loads are in flight at once.
+template <int U>
+__global__ void __launch_bounds__(256) dropout_kernel(const uint4* x, const uint4* residual,
+                                                      uint4* y, int64_t nvec, const DropArgs d) {
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * (256 * U) + threadIdx.x;
+  grid_dependency_wait();
+  grid_dependency_trigger();
+  uint4 xv[U], rv[U];
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    const int64_t v = first + 256 * i;
+    if (v < nvec) {
+      xv[i] = __ldcs(x + v);
+      if (residual) rv[i] = __ldcs(residual + v);
+    }
+  }
+  const uint64_t offset = drop_offset(d);
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    const int64_t v = first + 256 * i;
+    if (v < nvec) {
+      float f[8];
+      unpack8(xv[i], f);
+      if (d.threshold) drop8(f, d, offset, static_cast<uint64_t>(v));
+      if (residual) {
+        float r[8];
+        unpack8(rv[i], r);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[k] += r[k];
+      }
+      __stcs(y + v, pack8(f));
+    }
+  }
+}
+
+// ---------------------------------------------------------------- backward
+//   dA = drop(dY),  dmul = dA act(Z),  dZ = dA mul act'(Z),  dbias = sum over rows of dZ
+// in fp32 (dZ rounded only where it is stored).
+template <int ACT, bool MUL>
+__device__ __forceinline__ void bwd8(const EpiBwdArgs& a, uint4 dyv, uint4 zv, uint4 mv,
+                                     uint64_t offset, int64_t at, float (&dz)[8]) {
+  unpack8(dyv, dz);
+  if (a.drop.threshold) drop8(dz, a.drop, offset, static_cast<uint64_t>(at));
+  float z[8];
+  if (ACT != kActNone || MUL) unpack8(zv, z);
+  if constexpr (MUL) {
+    float m[8];
+    unpack8(mv, m);
+    if (a.dmul) {
+      float dm[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) dm[k] = dz[k] * act_value<ACT>(z[k]);
+      __stcs(reinterpret_cast<uint4*>(a.dmul) + at, pack8(dm));
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) dz[k] *= m[k];
+  }
+  if constexpr (ACT != kActNone) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) dz[k] *= act_slope<ACT>(z[k]);
+  }
+  if (a.dz) __stcs(reinterpret_cast<uint4*>(a.dz) + at, pack8(dz));
+}
+
+// Without dbias: vectors in memory order.
+template <int ACT, bool MUL>
+__global__ void __launch_bounds__(256) epilogue_bwd_kernel(const EpiBwdArgs a) {
+  constexpr int U = 2;
+  const int64_t nvec = a.rows * (a.cols / 8);
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * (256 * U) + threadIdx.x;
+  grid_dependency_wait();
+  grid_dependency_trigger();
+  uint4 dy[U], z[U], m[U];
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    const int64_t v = first + 256 * i;
+    dy[i] = z[i] = m[i] = make_uint4(0, 0, 0, 0);
+    if (v < nvec) {
+      dy[i] = __ldcs(reinterpret_cast<const uint4*>(a.dy) + v);
+      if (ACT != kActNone || (MUL && a.dmul)) z[i] = __ldcs(reinterpret_cast<const uint4*>(a.z) + v);
+      if (MUL) m[i] = __ldcs(reinterpret_cast<const uint4*>(a.mul) + v);
+    }
+  }
+  const uint64_t offset = drop_offset(a.drop);
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    const int64_t v = first + 256 * i;
+    float dz[8];
+    if (v < nvec) bwd8<ACT, MUL>(a, dy[i], z[i], m[i], offset, v, dz);
+  }
+}
+
+// With dbias: a block takes 128 columns and a run of rows, 16 lanes to a row; a thread
+// adds its eight columns over its rows, the block's 16 rows of sums are joined in shared
+// memory, and the block leaves one partial row (or, where it has all rows, dbias).
+constexpr int kBiasCols = 128;
+template <int ACT, bool MUL>
+__global__ void __launch_bounds__(256) epilogue_bwd_bias_kernel(const EpiBwdArgs a) {
+  constexpr int U = 2;
+  __shared__ float4 sums[16][kBiasCols / 4];
+  const int64_t nv = a.cols / 8;
+  const int64_t v = static_cast<int64_t>(blockIdx.x) * 16 + (threadIdx.x & 15);
+  const int64_t each = (a.rows + gridDim.y - 1) / gridDim.y;
+  const int64_t r0 = each * blockIdx.y, r1 = min(a.rows, r0 + each);
+  float sum[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+  grid_dependency_wait();
+  const uint64_t offset = drop_offset(a.drop);
+  if (v < nv) {
+    for (int64_t row = r0 + (threadIdx.x >> 4); row < r1; row += 16 * U) {
+      uint4 dy[U], z[U], m[U];
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int64_t at = (row + 16 * i) * nv + v;
+        dy[i] = z[i] = m[i] = make_uint4(0, 0, 0, 0);
+        if (row + 16 * i < r1) {
+          dy[i] = __ldcs(reinterpret_cast<const uint4*>(a.dy) + at);
+          if (ACT != kActNone || (MUL && a.dmul))
+            z[i] = __ldcs(reinterpret_cast<const uint4*>(a.z) + at);
+          if (MUL) m[i] = __ldcs(reinterpret_cast<const uint4*>(a.mul) + at);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+        if (row + 16 * i < r1) {
+          float dz[8];
+          bwd8<ACT, MUL>(a, dy[i], z[i], m[i], offset, (row + 16 * i) * nv + v, dz);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) sum[k] += dz[k];
+        }
+    }
+  }
+  grid_dependency_trigger();
+  sums[threadIdx.x >> 4][2 * (threadIdx.x & 15)] = make_float4(sum[0], sum[1], sum[2], sum[3]);
+  sums[threadIdx.x >> 4][2 * (threadIdx.x & 15) + 1] = make_float4(sum[4], sum[5], sum[6], sum[7]);
+  __syncthreads();
+  const int64_t col = static_cast<int64_t>(blockIdx.x) * kBiasCols + threadIdx.x;
+  if (threadIdx.x < kBiasCols && col < a.cols) {
+    float s = 0.0f;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) s += reinterpret_cast<const float*>(sums[r])[threadIdx.x];
+    if (gridDim.y == 1) a.dbias[col] = s;
+    else a.part[blockIdx.y * a.cols + col] = s;
+  }
+}
+
+template <int ACT, bool MUL>
+cudaError_t launch_t(const EpiBwdArgs& a, int num_sms, cudaStream_t stream) {
+  if (!a.dbias) {
+    const int64_t blocks = (a.rows * (a.cols / 8) + 511) / 512;
+    return launch_chained(epilogue_bwd_kernel<ACT, MUL>, static_cast<unsigned>(blocks), 256, 0, 0,
+                          stream, a);
+  }
+  const int parts = epilogue_bwd_blocks(a.rows, a.cols, num_sms);
+  const dim3 grid(static_cast<unsigned>((a.cols + kBiasCols - 1) / kBiasCols), parts, 1);
+  const cudaError_t e =
+      launch_chained_2d(epilogue_bwd_bias_kernel<ACT, MUL>, grid, 256, 0, 0, stream, a);
+  if (e != cudaSuccess || parts == 1) return e;
+  return launch_join_rows(a.part, parts, static_cast<int>(a.cols), a.dbias, stream);
+}
+
+template <bool MUL>
+cudaError_t launch_act(const EpiBwdArgs& a, int num_sms, cudaStream_t stream) {
+  switch (a.act) {
+    case kActRelu: return launch_t<kActRelu, MUL>(a, num_sms, stream);
+    case kActGelu: return launch_t<kActGelu, MUL>(a, num_sms, stream);
+    case kActGeluTanh: return launch_t<kActGeluTanh, MUL>(a, num_sms, stream);
+    case kActSilu: return launch_t<kActSilu, MUL>(a, num_sms, stream);
+    default: return launch_t<kActNone, MUL>(a, num_sms, stream);
+  }
+}
+
+}  // namespace
+
+// About six blocks an SM, each with 32 rows at least.
+int epilogue_bwd_blocks(int64_t rows, int64_t cols, int num_sms) {
+  const int64_t strips = (cols + kBiasCols - 1) / kBiasCols;
+  const int64_t most = (rows + 31) / 32, want = (static_cast<int64_t>(num_sms) * 6 + strips - 1) / strips;
+  const int64_t n = want < most ? want : most;
+  return static_cast<int>(n < 1 ? 1 : n);
+}
+
+cudaError_t launch_epilogue_bwd(const EpiBwdArgs& a, int num_sms, cudaStream_t stream) {
+  return a.mul ? launch_act<true>(a, num_sms, stream) : launch_act<false>(a, num_sms, stream);
+}
+
+cudaError_t launch_dropout(const uint16_t* x, const uint16_t* residual, uint16_t* y, int64_t rows,
+                           int64_t cols, const DropArgs& drop, cudaStream_t stream) {
+  const int64_t nvec = rows * (cols / 8);
+  const uint4 *xv = reinterpret_cast<const uint4*>(x), *rv = reinterpret_cast<const uint4*>(residual);
+  uint4* yv = reinterpret_cast<uint4*>(y);
+  const int64_t blocks = (nvec + 511) / 512;
+  return launch_chained(dropout_kernel<2>, static_cast<unsigned>(blocks), 256, 0, 0, stream, xv, rv,
+                        yv, nvec, drop);
+}
+
+}  // namespace forge

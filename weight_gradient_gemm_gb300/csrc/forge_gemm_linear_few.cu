@@ -1,0 +1,269 @@
+// The forward product of a linear layer in 16 bits (see forge_gemm_linear.cu) for few
+// tokens, where reading the weight is all the time there is.
+//
+// As in the 8-bit form (forge_gemm_b128_few.cu) the operands change places: 128
+// outputs lie along the MMA's M and the tokens along its N, 16 to 128 of them, and the
+// reduction is split over the CTAs of a cluster (up to 8), which send slices of their
+// fp32 sums to the CTAs that own them through distributed shared memory; the owners
+// add them in a fixed order, apply the epilogue and store.  One launch, no workspace,
+// the same result on every run.
+//
+// Warp roles: 0 loads (TMA), 1 issues the MMAs, from 4 on a warp takes the 32 outputs
+// of a TMEM lane quadrant and up to 32 tokens; all threads join in the end.  Every
+// wait is bounded.
+#include <cuda_bf16.h>
+
+#include "forge_internal.h"
+#include "forge_launch.cuh"
+#include "forge_layer.cuh"
+#include "forge_ptx.cuh"
+#include "forge_wait.cuh"
+
+namespace forge {
+namespace {
+
+template <int NT>
+struct FewL {
+  static constexpr int EPI = NT <= 32 ? 4 : NT / 8;     // epilogue warps
+  static constexpr int THREADS = 128 + 32 * EPI;
+  static constexpr int NC = NT <= 32 ? NT : 32;         // tokens per epilogue thread
+  static constexpr int A_BYTES = kBM * 128;
+  static constexpr int STAGE_BYTES = A_BYTES + NT * 128;
+  // Operand stages: as many as let two CTAs share an SM, or, where the grid has no
+  // more than one CTA for each, as many as fit.
+  static constexpr int STAGES = NT <= 16 ? 5 : (NT <= 32 ? 4 : 3);
+  static constexpr int DEEP = NT <= 16 ? 11 : (NT == 32 ? 9 : (NT == 64 ? 7 : 4));
+  static constexpr int TMEM_COLS = NT < 32 ? 32 : NT;
+  static constexpr int PART_BYTES = NT * kBM * 4;       // one tile of fp32 sums
+  // Shared memory from a 1024-aligned base: barriers (the most there can be), abort
+  // flag, stages, the shares.
+  static constexpr int NUM_BARS = 2 * DEEP + 1;
+  static constexpr int OFF_TMEM = 8 * NUM_BARS;
+  static constexpr int OFF_STAGES = 1024;
+  static constexpr int smem(int stages) {
+    return OFF_STAGES + stages * STAGE_BYTES + PART_BYTES + 1024;
+  }
+  static_assert(OFF_TMEM + 8 <= OFF_STAGES, "barriers");
+  static_assert(NT > 64 || 2 * smem(STAGES) <= 228 * 1024 - 2 * 1024, "two CTAs an SM");
+  static_assert(smem(DEEP) <= 232448, "shared memory budget");
+};
+
+template <int NT>
+__global__ void __launch_bounds__(FewL<NT>::THREADS, NT <= 64 ? 2 : 1)
+    gemm_linear_few_kernel(const __grid_constant__ LinearArgs a) {
+  using T = FewL<NT>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  // the same offset in every CTA of the cluster: remote stores use it
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* gbase = smem_raw + (base - raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int splits = a.splits;
+  const int rank = splits > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int tile = static_cast<int>(blockIdx.x) / splits;
+  // this CTA's steps of the reduction
+  const int kb = b128_first_block(rank, splits, a.num_kb);
+  const int ke = b128_first_block(rank + 1, splits, a.num_kb);
+
+  const uint32_t stages = a.stages;
+  const uint32_t bars = base, stage0 = base + T::OFF_STAGES;
+  auto bar_full = [&](int s) { return bars + 8u * s; };
+  auto bar_empty = [&](int s) { return bars + 8u * (T::DEEP + s); };
+  const uint32_t bar_done = bars + 8u * (2 * T::DEEP);   // all products have run
+  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(gbase + T::OFF_TMEM + 4);
+  const WaitCtx wc{abort_flag, a.err, a.err_site, a.timeout_ns};
+  const uint64_t wpol = l2_policy_evict_normal(), xpol = l2_policy_evict_last();
+
+  // Warp 0 sets up the barriers while warp 1 takes the tensor memory; one block
+  // barrier covers both.
+  if (warp == 0) {
+    for (int i = lane; i < T::NUM_BARS; i += 32) mbar_init(bars + 8u * i, 1);
+    if (lane == 0) *abort_flag = 0u;
+    fence_mbarrier_init();
+    __syncwarp();
+    if (lane == 0) drop_first_arrival(a.drop_first_arrival, bar_full(0));
+  } else if (warp == 1) {
+    tmem_alloc(base + T::OFF_TMEM, T::TMEM_COLS);
+    tmem_relinquish();
+    tc_fence_before_sync();
+  }
+  __syncthreads();
+  if (splits > 1) cluster_arrive();   // waited for before the first remote store
+  tc_fence_after_sync();
+  // While the kernel before still runs, the weight's first steps are asked for as far
+  // as L2, where all writes meet (see forge_gemm_b128_few.cu).
+  if (warp == 0 && lane == 0) {
+    const int ahead = NT <= 16 ? max(8, (ke - kb) / 2) : 8;
+    for (int k = kb; k < min(ke, kb + ahead); ++k)
+      tma_prefetch_l2_2d(&a.b, k * 64, tile * 128);
+  }
+  grid_dependency_wait();
+  const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(gbase + T::OFF_TMEM);
+
+  // The outputs that this CTA owns, eight neighbouring ones at a time: token e >> shift.
+  // The first ones' inputs are asked for now, under the reduction.
+  const int slice = kBM / splits;   // splits divides 128
+  const int shift = 31 - __clz(slice >> 3), total = a.m << shift;
+  const int64_t nv = a.n / 8;
+  auto place = [&](int e, int& t, int& j, int64_t& at) {
+    t = e >> shift;
+    j = (e - (t << shift)) * 8;
+    const int o = tile * 128 + rank * slice + j;
+    at = static_cast<int64_t>(t) * nv + o / 8;
+    return e < total && o < a.n;
+  };
+  uint4 mul0 = make_uint4(0, 0, 0, 0), res0 = mul0;
+  uint64_t offset = 0;
+  if (warp != 0 && warp != 1) {
+    int t, j;
+    int64_t at;
+    if (place(threadIdx.x, t, j, at)) {
+      if (a.e.mul) mul0 = reinterpret_cast<const uint4*>(a.e.mul)[at];
+      if (a.e.residual) res0 = reinterpret_cast<const uint4*>(a.e.residual)[at];
+    }
+  }
+
+  float acc[T::NC];   // epilogue threads: one output, NC tokens
+  if (warp == 0) {
+    if (lane == 0) {
+      uint32_t s = 0, ph = 0, armed = 0;   // next stage, its phase, stages in use
+      for (int k = kb; k < ke; ++k) {
+        if (!wait_bounded(bar_empty(s), ph ^ 1u, wc, kSiteProducerEmpty)) break;
+        const uint32_t dst = stage0 + s * T::STAGE_BYTES;
+        mbar_arrive_expect_tx(bar_full(s), T::STAGE_BYTES);
+        tma_load_2d(dst, &a.b, k * 64, tile * 128, bar_full(s), wpol);
+        tma_load_2d(dst + T::A_BYTES, &a.a, k * 64, 0, bar_full(s), xpol);
+        if (armed < stages) ++armed;
+        if (++s == stages) { s = 0; ph ^= 1u; }
+      }
+      for (uint32_t i = 0; i < armed; ++i) {   // the last load of every stage lands
+        if (s == 0) { s = stages; ph ^= 1u; }
+        --s;
+        wait_bounded(bar_full(s), ph, wc, kSiteDrainOperands, false);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    constexpr uint32_t idesc = make_idesc_bf16(128, NT, false, false);
+    const uint64_t ad0 = make_sdesc_k_sw128(stage0, 1024);
+    const uint64_t bd0 = make_sdesc_k_sw128(stage0 + T::A_BYTES, 1024);
+    const bool issue = elect_one();
+    uint32_t s = 0, ph = 0;
+#pragma unroll 1
+    for (int k = kb; k < ke; ++k) {
+      if (!__all_sync(0xffffffffu, wait_bounded(bar_full(s), ph, wc, kSiteMmaFull))) break;
+      tc_fence_after_sync();
+      const uint64_t ad = ad0 + s * (T::STAGE_BYTES >> 4), bd = bd0 + s * (T::STAGE_BYTES >> 4);
+      if (issue) {
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          umma_bf16(tmem_base, ad + 2 * kk, bd + 2 * kk, idesc, (k - kb) | kk);
+        umma_commit(bar_empty(s));
+      }
+      if (++s == stages) { s = 0; ph ^= 1u; }
+    }
+    if (issue) umma_commit(bar_done);
+    wait_bounded(bar_done, 0u, wc, kSiteDrainMma, false);
+    __syncwarp();
+  } else if (warp >= 4) {
+    const int q = warp & 3, h = (warp - 4) >> 2;
+    const uint32_t tcol = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + h * T::NC;
+    const bool ok = __all_sync(0xffffffffu, wait_bounded(bar_done, 0u, wc, kSiteEpiTmemFull));
+    if (ok && ke > kb) {   // (a CTA without steps adds nothing)
+      tc_fence_after_sync();
+#pragma unroll
+      for (int c = 0; c < T::NC / 16; ++c) {
+        uint32_t r[16];
+        tmem_ld_x16(tcol + 16 * c, r);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[16 * c + i] = __uint_as_float(r[i]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < T::NC; ++i) acc[i] = 0.0f;
+    }
+  }
+  tc_fence_before_sync();
+
+  // ------------------------------------------------------------ join and store
+  grid_dependency_trigger();
+  const uint32_t off_part = T::OFF_STAGES + stages * T::STAGE_BYTES;
+  if (splits > 1) cluster_wait();   // every CTA has started
+  if (warp >= 4) {
+    const int h = (warp - 4) >> 2, o = (warp & 3) * 32 + lane;
+    // [rank of the sender][token][output of the slice]
+    const uint32_t to = base + off_part + 4u * ((rank * NT + h * T::NC) * slice + o % slice);
+    const uint32_t dst = splits > 1 ? mapa_shared(to, o / slice) : 0u;
+    float* here = reinterpret_cast<float*>(gbase + (to - base));
+#pragma unroll
+    for (int i = 0; i < T::NC; ++i)
+      if (h * T::NC + i < a.m) {
+        if (splits > 1) st_cluster_f32(dst + 4u * i * slice, acc[i]);
+        else here[i * slice] = acc[i];
+      }
+  }
+  if (splits > 1) cluster_sync_all(); else __syncthreads();
+  if (a.e.drop.threshold) offset = drop_offset(a.e.drop);
+  if (!*abort_flag) {
+    const float* part = reinterpret_cast<const float*>(gbase + off_part);
+    for (int e = threadIdx.x; e < total; e += T::THREADS) {
+      int t, j;
+      int64_t at;
+      if (!place(e, t, j, at)) continue;
+      if (e != static_cast<int>(threadIdx.x) || warp < 2) {
+        if (a.e.mul) mul0 = reinterpret_cast<const uint4*>(a.e.mul)[at];
+        if (a.e.residual) res0 = reinterpret_cast<const uint4*>(a.e.residual)[at];
+      }
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = 0.0f;
+      for (int z = 0; z < splits; ++z) {
+        const float4* p = reinterpret_cast<const float4*>(part + (z * NT + t) * slice + j);
+        const float4 x = p[0], y = p[1];
+        v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+        v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
+      }
+      const int64_t col = tile * 128 + rank * slice + j;
+      const uint4 z = epilogue8(v, a.e, col, mul0, res0, offset, static_cast<uint64_t>(at));
+      if (a.e.z) reinterpret_cast<uint4*>(a.e.z)[at] = z;
+      if (a.e.y_fp32) {
+        float4* y = reinterpret_cast<float4*>(a.e.y) + 2 * at;
+        y[0] = make_float4(v[0], v[1], v[2], v[3]);
+        y[1] = make_float4(v[4], v[5], v[6], v[7]);
+      } else {
+        reinterpret_cast<uint4*>(a.e.y)[at] = pack8(v);
+      }
+    }
+  }
+  if (warp == 1) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem_base, T::TMEM_COLS);
+  }
+}
+
+template <int NT>
+cudaError_t launch_t(LinearArgs a, int num_sms, cudaStream_t stream) {
+  using T = FewL<NT>;
+  auto kern = gemm_linear_few_kernel<NT>;
+  static PerDevice once;
+  const cudaError_t e = allow_smem(once, kern, 232448);
+  if (e != cudaSuccess) return e;
+  a.stages = a.num_tiles * a.splits <= num_sms ? T::DEEP : T::STAGES;
+  return launch_chained(kern, a.num_tiles * a.splits, T::THREADS, T::smem(a.stages),
+                        a.splits > 1 ? a.splits : 0, stream, a);
+}
+
+}  // namespace
+
+cudaError_t launch_gemm_linear_few(int nt, const LinearArgs& a, int num_sms, cudaStream_t stream) {
+  switch (nt) {
+    case 16: return launch_t<16>(a, num_sms, stream);
+    case 32: return launch_t<32>(a, num_sms, stream);
+    case 64: return launch_t<64>(a, num_sms, stream);
+    case 128: return launch_t<128>(a, num_sms, stream);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace forge

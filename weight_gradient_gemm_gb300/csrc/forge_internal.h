@@ -302,4 +302,103 @@ cudaError_t launch_gemm_b128(const B128Config& c, bool dgrad, const B128Args& a,
 cudaError_t launch_gemm_b128_few(int nt, bool dgrad, const B128Args& a, int num_sms,
                                  cudaStream_t stream);
 
+// ---------------------------------------------------------------- between the products
+// Activations (match forge_activation).
+enum Act : int { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4 };
+template <int ACT>
+struct ActTag {
+  static constexpr int value = ACT;
+};
+
+// Dropout (see forge_layer.cuh): an element is dropped where its 16 bits are below
+// `threshold` (0: nothing is dropped).
+struct DropArgs {
+  uint32_t threshold;
+  float scale;               // 65536 / (65536 - threshold)
+  uint64_t seed, offset;
+  const uint64_t* counter;   // device word added to the offset, or null
+};
+
+// The epilogue of the 16-bit product.  Null pointers leave a part out.
+struct EpiArgs {
+  const void* bias;
+  int32_t bias_bf16, act;
+  const uint16_t* mul;
+  const uint16_t* residual;
+  uint16_t* z;
+  void* y;
+  int32_t y_fp32;
+  DropArgs drop;
+};
+
+// The 16-bit product of a linear layer (forge_gemm_linear.cu).
+struct LinearArgs {
+  CUtensorMap a, b;                 // tokens and weight
+  CUtensorMap mul, residual, z, y;  // boxes of 32 rows (many tokens; y also without them)
+  EpiArgs e;
+  int32_t m, n, num_kb;             // tokens, outputs, 64-deep steps of the reduction
+  int32_t tiles_m, tiles_n, num_tiles, group_m;
+  int32_t splits, stages;           // few tokens: CTAs that share a tile's reduction; stages
+  int32_t drop_first_arrival;       // testing aid
+  int* err;
+  int* err_site;
+  uint64_t timeout_ns;
+};
+struct LinearConfig {
+  int cg, bn;   // CTAs per tile and its columns
+  int few;      // 0, or the tokens a tile holds when the outputs lie along M
+  int splits;   // few tokens: CTAs per tile
+};
+cudaError_t launch_gemm_linear(const LinearConfig& c, const LinearArgs& a, int num_sms,
+                               cudaStream_t stream);
+cudaError_t launch_gemm_linear_few(int nt, const LinearArgs& a, int num_sms, cudaStream_t stream);
+
+// The epilogue's gradient and dropout (forge_epilogue.cu).
+struct EpiBwdArgs {
+  const uint16_t* dy;
+  const uint16_t* z;
+  const uint16_t* mul;
+  uint16_t* dz;
+  uint16_t* dmul;
+  float* dbias;
+  float* part;     // [epilogue_bwd_blocks][cols] partial sums of dbias
+  int64_t rows;
+  int64_t cols;
+  int32_t act;
+  DropArgs drop;
+};
+int epilogue_bwd_blocks(int64_t rows, int64_t cols, int num_sms);   // rows of `part`
+cudaError_t launch_epilogue_bwd(const EpiBwdArgs& a, int num_sms, cudaStream_t stream);
+cudaError_t launch_dropout(const uint16_t* x, const uint16_t* residual, uint16_t* y, int64_t rows,
+                           int64_t cols, const DropArgs& drop, cudaStream_t stream);
+// out[c] = sum over `blocks` rows of part, in a fixed order (forge_norm.cu).
+cudaError_t launch_join_rows(const float* part, int blocks, int cols, float* out,
+                             cudaStream_t stream);
+
+// Rotary positions and the norm of queries and keys (forge_rope.cu).
+struct HeadSet {
+  const uint16_t* x;     // element (token, head, i) at x + token * x_token + head * x_head + i
+  const uint16_t* dy;    // backward: gradient of the rotated heads
+  uint16_t* y;           // output (backward: gradient of x)
+  const void* gain;      // [dim], or null: rotation alone
+  float* dgain;          // backward: [dim], or null
+  int64_t x_token, x_head, dy_token, dy_head, y_token, y_head;
+  int32_t heads;
+};
+struct RopeArgs {
+  HeadSet set[2];
+  int32_t sets;
+  int32_t dim, rot, interleaved;
+  int32_t gain_bf16, inverse;
+  const uint64_t* freqs;         // [rot / 2] turns per position as fractions of 2^64
+  const int64_t* positions;      // [tokens], or null: 0, 1, ...
+  float magnitude, eps;
+  int64_t tokens;
+  float* part;                   // [qk_bwd_blocks][2][dim] partial sums of the gains' gradients
+};
+cudaError_t launch_rope(const RopeArgs& a, int num_sms, cudaStream_t stream);
+cudaError_t launch_qk_norm_rope(const RopeArgs& a, int num_sms, cudaStream_t stream);
+int qk_bwd_blocks(int num_sms);   // most rows of `part`
+cudaError_t launch_qk_norm_rope_bwd(const RopeArgs& a, int num_sms, cudaStream_t stream);
+
 }  // namespace forge

@@ -64,10 +64,10 @@ cudaError_t allow_smem(PerDevice& once, Kern kern, int bytes) {
 // cluster_x: CTAs per cluster (0: no clusters).  A launch that fails answers with
 // its error and leaves none behind for the check after another launch.
 template <typename... P, typename... A>
-cudaError_t launch_chained(void (*kern)(P...), unsigned grid, unsigned block, size_t smem,
-                           unsigned cluster_x, cudaStream_t stream, A&&... args) {
+cudaError_t launch_chained_2d(void (*kern)(P...), dim3 grid, unsigned block, size_t smem,
+                              unsigned cluster_x, cudaStream_t stream, A&&... args) {
   cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3(grid, 1, 1);
+  lc.gridDim = grid;
   lc.blockDim = dim3(block, 1, 1);
   lc.dynamicSmemBytes = smem;
   lc.stream = stream;
@@ -83,6 +83,12 @@ cudaError_t launch_chained(void (*kern)(P...), unsigned grid, unsigned block, si
   const cudaError_t e = cudaLaunchKernelEx(&lc, kern, std::forward<A>(args)...);
   if (e != cudaSuccess) (void)cudaGetLastError();
   return e;
+}
+template <typename... P, typename... A>
+cudaError_t launch_chained(void (*kern)(P...), unsigned grid, unsigned block, size_t smem,
+                           unsigned cluster_x, cudaStream_t stream, A&&... args) {
+  return launch_chained_2d(kern, dim3(grid, 1, 1), block, smem, cluster_x, stream,
+                           std::forward<A>(args)...);
 }
 
 }  // namespace forge

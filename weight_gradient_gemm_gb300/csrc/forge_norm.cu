@@ -896,11 +896,15 @@ cudaError_t launch_rmsnorm_bwd(const NormBwdArgs& a, int num_sms, cudaStream_t s
       e = go(rmsnorm_bwd_kernel<4, false, false>);   // up to 16384 columns: direct or the stream
   }
   if (e != cudaSuccess || !a.dgain) return e;
+  return launch_join_rows(a.part, p.grid, a.cols, a.dgain, stream);
+}
+
+cudaError_t launch_join_rows(const float* part, int blocks, int cols, float* out,
+                             cudaStream_t stream) {
   auto join = [&](auto kern, int w) {
-    return launch_chained(kern, (a.cols + w - 1) / w, 1024, 0, 0, stream,
-                          static_cast<const float*>(a.part), p.grid, a.cols, a.dgain);
+    return launch_chained(kern, (cols + w - 1) / w, 1024, 0, 0, stream, part, blocks, cols, out);
   };
-  return a.cols <= 1024 ? join(rmsnorm_dgain_kernel<16>, 16) : join(rmsnorm_dgain_kernel<32>, 32);
+  return cols <= 1024 ? join(rmsnorm_dgain_kernel<16>, 16) : join(rmsnorm_dgain_kernel<32>, 32);
 }
 
 cudaError_t launch_quantize_b128(const uint16_t* x, uint8_t* codes, float* scales, int64_t rows,

@@ -36,6 +36,10 @@ STATUS_NAMES = {
 }
 MOM_FP32, MOM_BF16, MOM_INT8_B128, MOM_FP8_E4M3 = 0, 1, 2, 3
 DT_FP32, DT_BF16 = 0, 1
+ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU = 0, 1, 2, 3, 4
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+(ROPE_SCALE_NONE, ROPE_SCALE_LINEAR, ROPE_SCALE_NTK, ROPE_SCALE_LLAMA3,
+ ROPE_SCALE_YARN) = 0, 1, 2, 3, 4
 
 
 class ForgeError(RuntimeError):
@@ -84,6 +88,35 @@ class ForgeGrad(ctypes.Structure):
 
 # forge_profile values
 PROFILES = {"auto": -1, "stream": 0, "mma": 1, "balanced": 2, "deep": 3}
+
+
+class ForgeDrop(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_float), ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64),
+                ("counter", ctypes.c_void_p)]
+
+
+class ForgeEpilogue(ctypes.Structure):
+    _fields_ = [("bias", ctypes.c_void_p), ("bias_dtype", ctypes.c_int), ("act", ctypes.c_int),
+                ("mul", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("z", ctypes.c_void_p),
+                ("drop", ForgeDrop)]
+
+
+class ForgeRotation(ctypes.Structure):
+    _fields_ = [("freqs", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                ("magnitude", ctypes.c_float), ("dim", ctypes.c_int32), ("layout", ctypes.c_int)]
+
+
+class ForgeHeads(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("x_token", ctypes.c_int64),
+                ("x_head", ctypes.c_int64), ("y_token", ctypes.c_int64),
+                ("y_head", ctypes.c_int64), ("heads", ctypes.c_int64), ("gain", ctypes.c_void_p),
+                ("dy", ctypes.c_void_p), ("dy_token", ctypes.c_int64),
+                ("dy_head", ctypes.c_int64), ("dgain", ctypes.c_void_p)]
+
+
+class ForgeRopeScaling(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int)] + [(k, ctypes.c_double)
+                                           for k in ("factor", "context", "low", "high")]
 
 
 class ForgeTuning(ctypes.Structure):
@@ -197,6 +230,29 @@ def lib() -> ctypes.CDLL:
             L.forge_grad_norm.restype = st
             L.forge_grad_norm_workspace_bytes.argtypes = [st]
             L.forge_grad_norm_workspace_bytes.restype = sz
+            L.forge_linear_bf16.argtypes = [vp, vp, vp, st, ctypes.POINTER(ForgeEpilogue), i64, i64,
+                                            i64, vp]
+            L.forge_linear_bf16.restype = st
+            drop = ctypes.POINTER(ForgeDrop)
+            L.forge_epilogue_backward.argtypes = [vp, vp, vp, st, drop, vp, vp, vp, i64, i64, vp,
+                                                  sz, vp]
+            L.forge_epilogue_backward.restype = st
+            L.forge_epilogue_backward_workspace_bytes.argtypes = [i64, i64]
+            L.forge_epilogue_backward_workspace_bytes.restype = sz
+            L.forge_dropout.argtypes = [vp, vp, vp, drop, i64, i64, vp]
+            L.forge_dropout.restype = st
+            sets, rot = ctypes.POINTER(ForgeHeads), ctypes.POINTER(ForgeRotation)
+            L.forge_rope.argtypes = [sets, st, rot, st, i64, i64, vp]
+            L.forge_rope.restype = st
+            L.forge_qk_norm_rope.argtypes = [sets, st, st, f32, rot, i64, i64, vp]
+            L.forge_qk_norm_rope.restype = st
+            L.forge_qk_norm_rope_backward.argtypes = [sets, st, st, f32, rot, i64, i64, vp, sz, vp]
+            L.forge_qk_norm_rope_backward.restype = st
+            L.forge_qk_norm_rope_backward_workspace_bytes.argtypes = [i64]
+            L.forge_qk_norm_rope_backward_workspace_bytes.restype = sz
+            L.forge_rope_frequencies.argtypes = [st, ctypes.c_double,
+                                                 ctypes.POINTER(ForgeRopeScaling), vp, vp]
+            L.forge_rope_frequencies.restype = st
             L.forge_set_tuning.argtypes = [ctypes.POINTER(ForgeTuning)]
             L.forge_set_tuning.restype = None
             L.forge_get_tuning.argtypes = [ctypes.POINTER(ForgeTuning)]
@@ -233,7 +289,9 @@ def _load_call(L: ctypes.CDLL) -> None:
         return
     mod.bind(*[ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in (
         "forge_rmsnorm", "forge_rmsnorm_backward", "forge_quantize_b128", "forge_linear_fp8",
-        "forge_dgrad_fp8", "forge_grad_norm", "forge_adamw_clip")])
+        "forge_dgrad_fp8", "forge_grad_norm", "forge_adamw_clip", "forge_linear_bf16",
+        "forge_epilogue_backward", "forge_dropout", "forge_rope", "forge_qk_norm_rope",
+        "forge_qk_norm_rope_backward")])
     _call = mod
 
 
@@ -1079,3 +1137,244 @@ def grad_norm(grads, max_norm: float, out: torch.Tensor, *, workspace: torch.Ten
                                _arg(out, "out", (2,), _F32, dev), workspace.data_ptr(),
                                workspace.nbytes, _raw_stream(stream, dev))
     _check(st, "forge_grad_norm")
+
+
+# ---------------------------------------------------------------------------
+# Between a layer's 16-bit products: the forward product with its epilogue, the
+# epilogue's gradient, dropout, rotary positions and the norm of queries and keys.
+# ---------------------------------------------------------------------------
+def _drop(p, seed: int, offset: int, counter: Optional[torch.Tensor], dev: int) -> ForgeDrop:
+    mask = (1 << 64) - 1
+    return ForgeDrop(p, int(seed) & mask, int(offset) & mask,
+                     _opt(counter, "counter", (1,), (torch.int64,), dev))
+
+
+def linear_bf16(X: torch.Tensor, W: torch.Tensor, Y: torch.Tensor, *,
+                bias: Optional[torch.Tensor] = None, act: int = ACT_NONE,
+                mul: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
+                Z: Optional[torch.Tensor] = None, p: float = 0.0, seed: int = 0, offset: int = 0,
+                counter: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Z = X W^T + bias, Y = residual + drop(act(Z) * mul), in fp32 and rounded once:
+    X [bt, d_in], W [d_out, d_in] bf16, bias [d_out] fp32 or bf16, mul, residual and Z
+    (written, for epilogue_backward) [bt, d_out] bf16, Y [bt, d_out] bf16 or fp32 (in bf16
+    it may be mul or residual).  drop is dropout() with p, seed, offset and counter."""
+    st = (_call or _loaded()).linear_bf16(X, W, Y, bias, act, mul, residual, Z, p, seed, offset,
+                                          counter, _address(stream))
+    if st >= 0:
+        return _check(st, "forge_linear_bf16") if st else None
+    bt, d_in = _matrix(X, "X")
+    d_out = _matrix(W, "W")[0]
+    dev = _device_of(X, "X")
+    shape = (bt, d_out)
+    e = ForgeEpilogue(_opt(bias, "bias", (d_out,), _GAIN, dev),
+                      DT_FP32 if bias is None else _DT[bias.dtype], act,
+                      _opt(mul, "mul", shape, _BF16, dev),
+                      _opt(residual, "residual", shape, _BF16, dev), _opt(Z, "Z", shape, _BF16, dev),
+                      _drop(p, seed, offset, counter, dev))
+    st = lib().forge_linear_bf16(
+        _arg(X, "X", (bt, d_in), _BF16, dev), _arg(W, "W", (d_out, d_in), _BF16, dev),
+        _arg(Y, "Y", shape, _GAIN, dev), _DT[Y.dtype], ctypes.byref(e), bt, d_in, d_out,
+        _raw_stream(stream, dev))
+    _check(st, "forge_linear_bf16")
+
+
+def epilogue_backward_workspace_bytes(rows: int, cols: int) -> int:
+    """Workspace bytes epilogue_backward needs when it writes dbias."""
+    return int(lib().forge_epilogue_backward_workspace_bytes(rows, cols))
+
+
+def epilogue_backward(dY: torch.Tensor, dZ: Optional[torch.Tensor] = None, *,
+                      Z: Optional[torch.Tensor] = None, act: int = ACT_NONE,
+                      mul: Optional[torch.Tensor] = None, dmul: Optional[torch.Tensor] = None,
+                      dbias: Optional[torch.Tensor] = None, p: float = 0.0, seed: int = 0,
+                      offset: int = 0, counter: Optional[torch.Tensor] = None,
+                      workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """The gradients of linear_bf16's epilogue from dY and Z [rows, cols] bf16: with
+    dA = drop(dY), dmul = dA act(Z), dZ = dA mul act'(Z) (both [rows, cols] bf16; they may
+    take the place of dY, Z or mul) and dbias = the sum over rows of dZ ([cols] fp32; it
+    needs a workspace of epilogue_backward_workspace_bytes bytes).  dZ goes to wgrad and
+    dgrad."""
+    st = (_call or _loaded()).epilogue_backward(dY, dZ, Z, act, mul, dmul, dbias, p, seed, offset,
+                                                counter, workspace, _address(stream))
+    if st >= 0:
+        return _check(st, "forge_epilogue_backward") if st else None
+    rows, cols = shape = _matrix(dY, "dY")
+    dev = _device_of(dY, "dY")
+    if workspace is not None:
+        _dense(workspace, "workspace")
+    drop = _drop(p, seed, offset, counter, dev)
+    st = lib().forge_epilogue_backward(
+        _arg(dY, "dY", shape, _BF16, dev), _opt(Z, "Z", shape, _BF16, dev),
+        _opt(mul, "mul", shape, _BF16, dev), act, ctypes.byref(drop),
+        _opt(dZ, "dZ", shape, _BF16, dev), _opt(dmul, "dmul", shape, _BF16, dev),
+        _opt(dbias, "dbias", (cols,), _F32, dev), rows, cols, _ptr(workspace),
+        0 if workspace is None else workspace.nbytes, _raw_stream(stream, dev))
+    _check(st, "forge_epilogue_backward")
+
+
+def dropout(x: torch.Tensor, y: torch.Tensor, *, p: float, seed: int, offset: int = 0,
+            counter: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
+            stream=None) -> None:
+    """y = residual + drop(x), all [rows, cols] bf16 (y may be x or residual): drop sets a
+    share p of the elements to zero and scales the others, by random numbers that depend on
+    the element's place, seed and offset + counter alone (counter: int64 [1] on the device,
+    read when the kernel runs, or None).  The gradient of x is the same call on y's gradient
+    without the residual."""
+    st = (_call or _loaded()).dropout(x, y, p, seed, offset, counter, residual, _address(stream))
+    if st >= 0:
+        return _check(st, "forge_dropout") if st else None
+    rows, cols = shape = _matrix(x, "x")
+    dev = _device_of(x, "x")
+    drop = _drop(p, seed, offset, counter, dev)
+    st = lib().forge_dropout(
+        _arg(x, "x", shape, _BF16, dev), _opt(residual, "residual", shape, _BF16, dev),
+        _arg(y, "y", shape, _BF16, dev), ctypes.byref(drop), rows, cols, _raw_stream(stream, dev))
+    _check(st, "forge_dropout")
+
+
+def rope_frequencies(dim: int, theta: float, *, scaling: int = ROPE_SCALE_NONE,
+                     factor: float = 1.0, context: float = 0.0, low: float = 1.0,
+                     high: float = 4.0, device="cuda"):
+    """The table that rope and qk_norm_rope take for a rotation of `dim` elements (int64
+    [dim / 2] on the device: turns per position as fractions of 2^64, modulo 2^64) and the
+    rotated values' magnitude.  scaling: one of ROPE_SCALE_*, with its factor and, for
+    LLAMA3 and YARN, the context trained on and the turns low and high between which
+    frequencies are mixed (usual: 1 and 4; YARN 1 and 32)."""
+    s = ForgeRopeScaling(scaling, factor, context, low, high)
+    table = (ctypes.c_uint64 * max(dim // 2, 1))()
+    magnitude = ctypes.c_float()
+    st = lib().forge_rope_frequencies(dim, theta, ctypes.byref(s), ctypes.addressof(table),
+                                      ctypes.addressof(magnitude))
+    _check(st, "forge_rope_frequencies")
+    signed = [v - (1 << 64) if v >> 63 else v for v in table]
+    return torch.tensor(signed, dtype=torch.int64, device=device), magnitude.value
+
+
+def _view(t: Optional[torch.Tensor], name: str, shape, dev: int):
+    """Pointer and strides of a [tokens, heads, dim] bf16 view whose rows are dense."""
+    _want(t, name, shape, _BF16)
+    if t.get_device() != dev:
+        _dense(t, name)
+    if t.shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name}'s rows must be contiguous")
+    return t.data_ptr(), t.stride(0), t.stride(1)
+
+
+def _head_sets(q, k, q_out, k_out, dev: int, gains=(None, None), grads=(None, None),
+               dgains=(None, None), names=("q", "k")):
+    if q.dim() != 3 or (k is not None and k.dim() != 3):
+        raise ValueError("heads are [tokens, heads, dim]")
+    sets = (ForgeHeads * 2)()
+    for i, (x, y) in enumerate(((q, q_out), (k, k_out))):
+        if x is None:
+            break
+        s, n = sets[i], names[i]
+        shape = (q.shape[0], x.shape[1], q.shape[2])
+        s.x, s.x_token, s.x_head = _view(x, n, shape, dev)
+        s.y, s.y_token, s.y_head = _view(y, f"{n}'s output", shape, dev)
+        s.heads = x.shape[1]
+        if gains[i] is not None or gains[0] is not None:
+            s.gain = _arg(gains[i], f"{n}_gain", (q.shape[2],), (gains[0].dtype,), dev)
+        if grads[0] is not None:
+            s.dy, s.dy_token, s.dy_head = _view(grads[i], f"d{n}", shape, dev)
+            s.dgain = _opt(dgains[i], f"d{n}_gain", (q.shape[2],), _F32, dev)
+    return sets, 1 if k is None else 2
+
+
+def _rotation(freqs, positions, magnitude, layout, tokens: int, dev: int) -> ForgeRotation:
+    if freqs.dim() != 1:
+        raise ValueError("freqs must be 1-D")
+    i64 = (torch.int64,)
+    return ForgeRotation(_arg(freqs, "freqs", tuple(freqs.shape), i64, dev),
+                         _opt(positions, "positions", (tokens,), i64, dev), magnitude,
+                         2 * freqs.shape[0], layout)
+
+
+def rope(q: torch.Tensor, k: Optional[torch.Tensor], freqs: torch.Tensor, *,
+         q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+         positions: Optional[torch.Tensor] = None, magnitude: float = 1.0,
+         layout: int = ROPE_HALF, inverse: bool = False, stream=None) -> None:
+    """Rotary positions on queries and (if given) keys [tokens, heads, dim] bf16: any
+    strides over tokens and heads (multiples of 8), rows contiguous, so views of the
+    projections' fused output serve as they are.  The first 2 len(freqs) elements of each
+    head turn (freqs and magnitude: rope_frequencies); positions int64 [tokens], None: 0, 1,
+    ...  Without outputs given it works in place.  inverse: the gradient."""
+    q_out = q if q_out is None else q_out
+    k_out = k if k_out is None else k_out
+    st = (_call or _loaded()).rope(q, k, freqs, q_out, k_out, positions, magnitude, layout,
+                                   inverse, _address(stream))
+    if st >= 0:
+        return _check(st, "forge_rope") if st else None
+    dev = _device_of(q, "q")
+    sets, n = _head_sets(q, k, q_out, k_out, dev)
+    rot = _rotation(freqs, positions, magnitude, layout, q.shape[0], dev)
+    st = lib().forge_rope(sets, n, ctypes.byref(rot), int(inverse), q.shape[0], q.shape[2],
+                          _raw_stream(stream, dev))
+    _check(st, "forge_rope")
+
+
+def _gain_dtype(q_gain) -> int:
+    if q_gain is None or q_gain.dtype not in _DT:
+        raise TypeError("q_gain is fp32 or bf16")
+    return _DT[q_gain.dtype]
+
+
+def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], q_gain: torch.Tensor,
+                 k_gain: Optional[torch.Tensor], freqs: torch.Tensor, *, eps: float,
+                 q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+                 positions: Optional[torch.Tensor] = None, magnitude: float = 1.0,
+                 layout: int = ROPE_HALF, stream=None) -> None:
+    """rope of the RMS norm of each head, x gain / sqrt(mean(x^2) + eps) over its dim, in one
+    pass; gains [dim] fp32 or bf16.  Without outputs given it works in place (the backward
+    pass needs the input)."""
+    q_out = q if q_out is None else q_out
+    k_out = k if k_out is None else k_out
+    st = (_call or _loaded()).qk_norm_rope(q, k, q_gain, k_gain, freqs, eps, q_out, k_out,
+                                           positions, magnitude, layout, _address(stream))
+    if st >= 0:
+        return _check(st, "forge_qk_norm_rope") if st else None
+    dev = _device_of(q, "q")
+    dt = _gain_dtype(q_gain)
+    sets, n = _head_sets(q, k, q_out, k_out, dev, (q_gain, k_gain))
+    rot = _rotation(freqs, positions, magnitude, layout, q.shape[0], dev)
+    st = lib().forge_qk_norm_rope(sets, n, dt, eps, ctypes.byref(rot), q.shape[0], q.shape[2],
+                                  _raw_stream(stream, dev))
+    _check(st, "forge_qk_norm_rope")
+
+
+def qk_norm_rope_backward_workspace_bytes(dim: int) -> int:
+    """Workspace bytes qk_norm_rope_backward needs when it writes the gains' gradients."""
+    return int(lib().forge_qk_norm_rope_backward_workspace_bytes(dim))
+
+
+def qk_norm_rope_backward(dq: torch.Tensor, dk: Optional[torch.Tensor], q: torch.Tensor,
+                          k: Optional[torch.Tensor], q_gain: torch.Tensor,
+                          k_gain: Optional[torch.Tensor], freqs: torch.Tensor, *, eps: float,
+                          dq_out: Optional[torch.Tensor] = None,
+                          dk_out: Optional[torch.Tensor] = None,
+                          dq_gain: Optional[torch.Tensor] = None,
+                          dk_gain: Optional[torch.Tensor] = None,
+                          positions: Optional[torch.Tensor] = None, magnitude: float = 1.0,
+                          layout: int = ROPE_HALF, workspace: Optional[torch.Tensor] = None,
+                          stream=None) -> None:
+    """The gradients of qk_norm_rope from those of its outputs (dq, dk) and its inputs (q,
+    k): dq_out and dk_out (None: in place of dq and dk) and, with a workspace of
+    qk_norm_rope_backward_workspace_bytes bytes, dq_gain and dk_gain [dim] fp32."""
+    dq_out = dq if dq_out is None else dq_out
+    dk_out = dk if dk_out is None else dk_out
+    st = (_call or _loaded()).qk_norm_rope_backward(
+        dq, dk, q, k, q_gain, k_gain, freqs, eps, dq_out, dk_out, dq_gain, dk_gain, positions,
+        magnitude, layout, workspace, _address(stream))
+    if st >= 0:
+        return _check(st, "forge_qk_norm_rope_backward") if st else None
+    dev = _device_of(q, "q")
+    dt = _gain_dtype(q_gain)
+    if workspace is not None:
+        _dense(workspace, "workspace")
+    sets, n = _head_sets(q, k, dq_out, dk_out, dev, (q_gain, k_gain), (dq, dk),
+                         (dq_gain, dk_gain))
+    rot = _rotation(freqs, positions, magnitude, layout, q.shape[0], dev)
+    st = lib().forge_qk_norm_rope_backward(
+        sets, n, dt, eps, ctypes.byref(rot), q.shape[0], q.shape[2], _ptr(workspace),
+        0 if workspace is None else workspace.nbytes, _raw_stream(stream, dev))
+    _check(st, "forge_qk_norm_rope_backward")

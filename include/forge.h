@@ -777,7 +777,7 @@ typedef struct {
  * with the angle w = 2 pi p freqs[i] / 2^64 (formed exactly modulo a turn), pair (a, b)
  * becomes magnitude (a cos w - b sin w, b cos w + a sin w), in fp32, rounded once.  With
  * `inverse` the angle is -w: the gradient of the call without it.
- * head_dim is a multiple of 8, at most 256.  Pointers of heads 16-byte aligned.  y may be
+ * head_dim is a multiple of 8, at most 256; at most 1024 heads of a kind.  Pointers of heads 16-byte aligned.  y may be
  * the same view as its own x; otherwise no output may overlap an input or another output
  * (interleaved views of one buffer, as queries and keys in the fused output of their
  * projections, do not), and no element of y may lie in two places.  tokens = 0 or heads = 0

@@ -273,7 +273,7 @@ forge_status forge_dropout(const void* x, const void* residual, void* y, const f
 namespace {
 
 constexpr int kMaxHeadDim = 256;
-constexpr int64_t kMaxHeads = 1 << 20;
+
 
 // One view [tokens, heads, dim] of a call.
 struct View {
@@ -418,6 +418,7 @@ forge_status rope_args(const forge_heads* sets, int n, const forge_rotation* rot
   a->positions = rot->positions;
   a->magnitude = rot->magnitude;
   a->eps = eps;
+  a->inv_dim = 1.0f / static_cast<float>(head_dim);
   a->tokens = used ? tokens : 0;
   return FORGE_OK;
 }
@@ -452,7 +453,7 @@ size_t forge_qk_norm_rope_backward_workspace_bytes(int64_t head_dim) {
   HostDevice d;
   if (head_dim <= 0 || head_dim > kMaxHeadDim || head_dim % 8 != 0) return 0;
   if (host_device(&d) != FORGE_OK) return 0;
-  return static_cast<size_t>(qk_bwd_blocks(d.num_sms)) * 2 * static_cast<size_t>(head_dim) * 4;
+  return static_cast<size_t>(qk_bwd_blocks(d.num_sms)) * static_cast<size_t>(head_dim) * 4;
 }
 
 forge_status forge_qk_norm_rope_backward(const forge_heads* sets, int n, forge_dtype gain_dtype,

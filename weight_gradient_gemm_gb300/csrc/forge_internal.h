@@ -376,6 +376,7 @@ cudaError_t launch_join_rows(const float* part, int blocks, int cols, float* out
                              cudaStream_t stream);
 
 // Rotary positions and the norm of queries and keys (forge_rope.cu).
+constexpr int kMaxHeads = 1024;   // of one kind
 struct HeadSet {
   const uint16_t* x;     // element (token, head, i) at x + token * x_token + head * x_head + i
   const uint16_t* dy;    // backward: gradient of the rotated heads
@@ -392,9 +393,9 @@ struct RopeArgs {
   int32_t gain_bf16, inverse;
   const uint64_t* freqs;         // [rot / 2] turns per position as fractions of 2^64
   const int64_t* positions;      // [tokens], or null: 0, 1, ...
-  float magnitude, eps;
+  float magnitude, eps, inv_dim;
   int64_t tokens;
-  float* part;                   // [qk_bwd_blocks][2][dim] partial sums of the gains' gradients
+  float* part;                   // [qk_bwd_blocks][dim] partial sums of the gains' gradients
 };
 cudaError_t launch_rope(const RopeArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_qk_norm_rope(const RopeArgs& a, int num_sms, cudaStream_t stream);

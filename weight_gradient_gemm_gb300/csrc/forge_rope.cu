@@ -4,15 +4,21 @@
 // The rotation.  Pair i of a head at position p turns by the angle 2 pi p f_i.  f_i, in
 // turns per position, is a 64-bit fraction F_i / 2^64, so p F_i modulo 2^64 is the
 // angle in fractions of a turn, exact for every position (one 64-bit integer product in
-// place of a 64-bit floating one and a reduction by pi): its upper 32 bits, as a signed
-// number, are the argument of sincospi.  Its rounding to fp32 is 2^-24 of half a turn.
+// place of a 64-bit floating one and a reduction by pi).  Its upper 32 bits give the
+// quadrant and, within it, an angle of at most pi / 4, which is all that is rounded to
+// fp32.
 //
 // The layout of the work.  A head's row is cut into vectors of VEC elements.  A lane
-// holds two of them: where pairs lie half the rotated part apart, the two vectors that
-// turn into each other; where they lie side by side, two neighbouring ones.  P lanes (a
-// power of two) hold a head, 32 / P heads a warp at a time.  A lane's pairs are the same
-// in all heads, so a warp forms the sines and cosines once for its token and walks the
-// heads of queries and keys with them; the next heads' loads are in flight meanwhile.
+// holds two of them, VEC pairs: where pairs lie half the rotated part apart, the two
+// vectors that turn into each other; where they lie side by side, two neighbouring ones,
+// whose even elements are then one half of the pairs and whose odd ones the other.  P
+// lanes (a power of two) hold a head, 32 / P heads a warp at a time: one step.
+// A block keeps to one chunk of steps of the queries' or the keys' heads and walks the
+// tokens with it, a warp a token: pointers only move on, gains and their gradients' sums
+// stay in registers, and as soon as a step's values are unpacked those STEPS steps
+// further (of this token or the next) are asked for in their place, so that loads stay
+// in flight throughout.  The warp's sines and cosines are formed once a token, each lane
+// some of them, and shared through memory of the warp's own.
 #include <cuda_bf16.h>
 
 #include "forge_e4m3.cuh"
@@ -24,26 +30,40 @@ namespace forge {
 namespace {
 
 enum RopeMode { kRope = 0, kQkNorm = 1, kQkNormBwd = 2 };
+// Steps whose loads are in flight at once, most steps of a chunk, and blocks an SM.
+constexpr int kStepsFwd = 4, kChunkFwd = 4, kBlocksFwd = 2;
+constexpr int kStepsBwd = 1, kChunkBwd = 4, kBlocksBwd = 2;
 
-// VEC bf16 values.
-template <int VEC>
-struct Raw;
-template <>
-struct Raw<8> {
-  using V = uint4;
-  static __device__ __forceinline__ V zero() { return make_uint4(0, 0, 0, 0); }
-  static __device__ __forceinline__ void unpack(V v, float (&f)[8]) { unpack8(v, f); }
-  static __device__ __forceinline__ V pack(const float (&f)[8]) { return pack8(f); }
+// Which blocks take what: the chunks of set k, `per` steps each (a multiple of the steps
+// in flight), have `blocks` blocks each, one chunk's after the other's.
+struct RopeGrid {
+  int lanes;
+  struct {
+    int chunks, per, blocks;
+  } set[2];
 };
-template <>
-struct Raw<4> {
-  using V = uint2;
-  static __device__ __forceinline__ V zero() { return make_uint2(0, 0); }
-  static __device__ __forceinline__ void unpack(V v, float (&f)[4]) {
-    f[0] = bf16_lo(v.x); f[1] = bf16_hi(v.x); f[2] = bf16_lo(v.y); f[3] = bf16_hi(v.y);
+
+// VEC bf16 values as 32-bit words.
+template <int VEC>
+struct Words {
+  using V = std::conditional_t<VEC == 8, uint4, uint2>;
+  uint32_t w[VEC / 2];
+  __device__ __forceinline__ Words() = default;
+  __device__ __forceinline__ explicit Words(V v) {
+    w[0] = v.x;
+    w[1] = v.y;
+    if constexpr (VEC == 8) {
+      w[2] = v.z;
+      w[3] = v.w;
+    }
   }
-  static __device__ __forceinline__ V pack(const float (&f)[4]) {
-    return make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
+  __device__ __forceinline__ V vec() const {
+    if constexpr (VEC == 8) return make_uint4(w[0], w[1], w[2], w[3]);
+    else return make_uint2(w[0], w[1]);
+  }
+  static __device__ __forceinline__ V zero() {
+    if constexpr (VEC == 8) return make_uint4(0, 0, 0, 0);
+    else return make_uint2(0, 0);
   }
 };
 
@@ -72,65 +92,109 @@ __device__ __forceinline__ LanePart lane_part(int u, int dim, int rot) {
   return p;
 }
 
-// Sines and cosines of the lane's VEC pairs at a position, times the magnitude.
+// The two vectors as the first and second elements of VEC pairs, two pairs a float2.
 template <int VEC, bool INTER>
-__device__ __forceinline__ void turn_of(const RopeArgs& r, const LanePart& p, int64_t pos,
-                                        float (&c)[VEC], float (&s)[VEC]) {
+__device__ __forceinline__ void to_pairs(typename Words<VEC>::V va, typename Words<VEC>::V vb,
+                                         float2 (&a)[VEC / 2], float2 (&b)[VEC / 2]) {
+  const Words<VEC> x(va), y(vb);
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) {
-    // HALF: pairs a, a + 1, ...; INTER: half of them in each vector
-    const bool in = INTER ? (i < VEC / 2 ? p.rot_a : p.rot_b) : p.rot_a;
-    const int pair = INTER ? (i < VEC / 2 ? p.a / 2 + i : p.b / 2 + i - VEC / 2) : p.a + i;
-    c[i] = 1.0f;
-    s[i] = 0.0f;
-    if (in) {
-      const uint64_t at = static_cast<uint64_t>(pos) * r.freqs[pair];
-      const float half_turns = static_cast<float>(static_cast<int32_t>(at >> 32)) * 0x1p-31f;
-      sincospif(half_turns, &s[i], &c[i]);
-      c[i] *= r.magnitude;
-      s[i] *= r.magnitude;
+  for (int i = 0; i < VEC / 2; ++i) {
+    if constexpr (INTER) {
+      const uint32_t w0 = i < VEC / 4 ? x.w[2 * i] : y.w[2 * i - VEC / 2];
+      const uint32_t w1 = i < VEC / 4 ? x.w[2 * i + 1] : y.w[2 * i + 1 - VEC / 2];
+      a[i] = make_float2(bf16_lo(w0), bf16_lo(w1));
+      b[i] = make_float2(bf16_hi(w0), bf16_hi(w1));
+    } else {
+      a[i] = make_float2(bf16_lo(x.w[i]), bf16_hi(x.w[i]));
+      b[i] = make_float2(bf16_lo(y.w[i]), bf16_hi(y.w[i]));
     }
   }
 }
-
-// (a, b) turned: by the angle, or with `back` by its opposite.
 template <int VEC, bool INTER>
-__device__ __forceinline__ void turn(const LanePart& p, const float (&c)[VEC],
-                                     const float (&s)[VEC], bool back, float (&a)[VEC],
-                                     float (&b)[VEC]) {
-  const float sign = back ? -1.0f : 1.0f;
-  if constexpr (INTER) {
+__device__ __forceinline__ void from_pairs(const float2 (&a)[VEC / 2], const float2 (&b)[VEC / 2],
+                                           typename Words<VEC>::V& va,
+                                           typename Words<VEC>::V& vb) {
+  Words<VEC> x, y;
 #pragma unroll
-    for (int i = 0; i < VEC / 2; ++i) {
-      const float sa = sign * s[i], x = a[2 * i], y = a[2 * i + 1];
-      if (p.rot_a) {
-        a[2 * i] = fmaf(x, c[i], -y * sa);
-        a[2 * i + 1] = fmaf(y, c[i], x * sa);
-      }
-      const float cb = c[i + VEC / 2], sb = sign * s[i + VEC / 2], z = b[2 * i], w = b[2 * i + 1];
-      if (p.rot_b) {
-        b[2 * i] = fmaf(z, cb, -w * sb);
-        b[2 * i + 1] = fmaf(w, cb, z * sb);
-      }
-    }
-  } else if (p.rot_a) {
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      const float si = sign * s[i], x = a[i], y = b[i];
-      a[i] = fmaf(x, c[i], -y * si);
-      b[i] = fmaf(y, c[i], x * si);
+  for (int i = 0; i < VEC / 2; ++i) {
+    if constexpr (INTER) {
+      uint32_t* w = i < VEC / 4 ? x.w + 2 * i : y.w + 2 * i - VEC / 2;
+      w[0] = pack_bf16x2(a[i].x, b[i].x);
+      w[1] = pack_bf16x2(a[i].y, b[i].y);
+    } else {
+      x.w[i] = pack_bf16x2(a[i].x, a[i].y);
+      y.w[i] = pack_bf16x2(b[i].x, b[i].y);
     }
   }
+  va = x.vec();
+  vb = y.vec();
+}
+// The element of component j (0, 1) of the first (s = 0) or second elements a[i], b[i],
+// and whether it exists.
+template <int VEC, bool INTER>
+__device__ __forceinline__ int element_of(const LanePart& p, int i, int j, int s) {
+  if (INTER) return p.a + 2 * (2 * i + j) + s;
+  return (s ? p.b : p.a) + 2 * i + j;
+}
+template <int VEC, bool INTER>
+__device__ __forceinline__ bool exists(const LanePart& p, int i, int s) {
+  return (INTER ? i < VEC / 4 : s == 0) ? p.has_a : p.has_b;
 }
 
+// Sine and cosine of 2 pi turn / 2^32.  The nearest quarter turn comes off exactly; for
+// the rest, |x| <= pi / 4, the Taylor series to x^9 and x^10 leave less than 2^-28 and
+// 2^-30.  (sincospi does the same for any argument: the backward pass of 8192 tokens
+// 53.9 us with it.)
+__device__ __forceinline__ void sin_cos(uint32_t turn, float& s, float& c) {
+  const uint32_t quarter = (turn + 0x20000000u) >> 30;
+  const float x = static_cast<float>(static_cast<int32_t>(turn - (quarter << 30))) *
+                  1.4629180792671596e-9f;   // 2 pi / 2^32
+  const float q = x * x;
+  const float sx = fmaf(fmaf(fmaf(fmaf(1.0f / 362880.0f, q, -1.0f / 5040.0f), q, 1.0f / 120.0f), q,
+                             -1.0f / 6.0f), q * x, x);
+  const float cx = fmaf(fmaf(fmaf(fmaf(fmaf(-1.0f / 3628800.0f, q, 1.0f / 40320.0f), q,
+                                       -1.0f / 720.0f), q, 1.0f / 24.0f), q, -0.5f), q, 1.0f);
+  s = quarter & 1u ? cx : sx;
+  c = quarter & 1u ? sx : cx;
+  if (quarter & 2u) s = -s;
+  if ((quarter + 1u) & 2u) c = -c;
+}
+// Those of all the head's pairs at a position, times the magnitude, into the warp's
+// tables.
+__device__ __forceinline__ void fill_turns(const RopeArgs& r, int64_t pos, int lane, float* cosine,
+                                           float* sine) {
+  for (int i = lane; i < r.rot / 2; i += 32) {
+    const uint64_t at = static_cast<uint64_t>(pos) * r.freqs[i];
+    float s, c;
+    sin_cos(static_cast<uint32_t>(at >> 32), s, c);
+    cosine[i] = c * r.magnitude;
+    sine[i] = s * r.magnitude;
+  }
+}
+// Those of the lane's VEC pairs, which follow one another.
 template <int VEC>
-__device__ __forceinline__ void load_gain(const void* gain, int bf16, int at, bool has,
-                                          float (&g)[VEC]) {
+__device__ __forceinline__ void load_turns(const float* t, float2 (&v)[VEC / 2]) {
 #pragma unroll
-  for (int i = 0; i < VEC; ++i)
-    g[i] = !has ? 0.0f
-                : (bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(gain)[at + i])
-                        : static_cast<const float*>(gain)[at + i]);
+  for (int i = 0; i < VEC / 2; i += 2) {
+    const float4 w = *reinterpret_cast<const float4*>(t + 2 * i);
+    v[i] = make_float2(w.x, w.y);
+    v[i + 1] = make_float2(w.z, w.w);
+  }
+}
+__device__ __forceinline__ float2 neg2(float2 v) { return make_float2(-v.x, -v.y); }
+// The pairs turned by the angle whose sines and cosines are c and s.
+template <int VEC>
+__device__ __forceinline__ void turn(const LanePart& p, const float2 (&c)[VEC / 2],
+                                     const float2 (&s)[VEC / 2], float2 (&a)[VEC / 2],
+                                     float2 (&b)[VEC / 2]) {
+#pragma unroll
+  for (int i = 0; i < VEC / 2; ++i) {
+    if (i < VEC / 4 ? p.rot_a : p.rot_b) {
+      const float2 x = a[i], y = b[i];
+      a[i] = fma2(neg2(s[i]), y, mul2(c[i], x));
+      b[i] = fma2(s[i], x, mul2(c[i], y));
+    }
+  }
 }
 
 // Sum over the P lanes of a head.
@@ -139,160 +203,201 @@ __device__ __forceinline__ float head_sum(float v, int lanes) {
   return v;
 }
 
-// A warp's units are the pairs (token, chunk): chunk c takes the c-th of `chunks` even
-// shares of the head groups (those of queries, then those of keys).
 template <int VEC, bool INTER, int MODE>
-__global__ void __launch_bounds__(256) rope_kernel(const RopeArgs r, int lanes, int chunks) {
-  using R = Raw<VEC>;
-  using V = typename R::V;
+__global__ void __launch_bounds__(256, MODE == kQkNormBwd ? kBlocksBwd : kBlocksFwd)
+    rope_kernel(const RopeArgs r, const RopeGrid grid) {
+  using V = typename Words<VEC>::V;
   constexpr bool kBwd = MODE == kQkNormBwd;
-  const int lane = threadIdx.x & 31;
-  const int u = lane & (lanes - 1), g = lane / lanes, groups = 32 / lanes;
+  constexpr int STEPS = kBwd ? kStepsBwd : kStepsFwd;
+  constexpr int N = VEC / 2;
+  __shared__ __align__(16) float tables[8][2][128];   // [warp][cosine, sine][pair]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int lanes = grid.lanes, u = lane & (lanes - 1), g = lane / lanes, groups = 32 / lanes;
   const LanePart p = lane_part<VEC, INTER>(u, r.dim, r.rot);
-  const int its0 = (r.set[0].heads + groups - 1) / groups;
-  const int its = its0 + (r.sets > 1 ? (r.set[1].heads + groups - 1) / groups : 0);
-  float dga[2][kBwd ? VEC : 1], dgb[2][kBwd ? VEC : 1];
-  if constexpr (kBwd) {
+  const int of0 = grid.set[0].chunks * grid.set[0].blocks;
+  const int k = static_cast<int>(blockIdx.x) >= of0;
+  const int rank = static_cast<int>(blockIdx.x) - (k ? of0 : 0);
+  const int chunk = rank / grid.set[k].blocks, sub = rank - chunk * grid.set[k].blocks;
+  const HeadSet& set = r.set[k];
+  const int per = grid.set[k].per, head0 = chunk * per * groups + g;
+  const int end = min(set.heads, (chunk + 1) * per * groups);
+
+  const int64_t walk = static_cast<int64_t>(grid.set[k].blocks) * 8;   // tokens from one to the next
+  int64_t t = static_cast<int64_t>(sub) * 8 + warp;
+  const int64_t x_step = groups * set.x_head, x_jump = walk * set.x_token - per * x_step;
+  const int64_t y_step = groups * set.y_head, y_jump = walk * set.y_token - per * y_step;
+  const int64_t dy_step = groups * set.dy_head, dy_jump = walk * set.dy_token - per * dy_step;
+  const int ab = p.b - p.a;
+  // the next load: its pointers, the token's and the lane's head
+  const uint16_t* x = set.x + t * set.x_token + head0 * set.x_head + p.a;
+  const uint16_t* dy = kBwd ? set.dy + t * set.dy_token + head0 * set.dy_head + p.a : nullptr;
+  uint16_t* y = set.y + t * set.y_token + head0 * set.y_head + p.a;
+  int64_t load_t = t;
+  int load_step = 0;
+
+  V xa[STEPS], xb[STEPS], da[kBwd ? STEPS : 1], db[kBwd ? STEPS : 1];
+  auto load = [&](int j) {
+    const bool in = load_t < r.tokens && head0 + load_step * groups < end;
+    xa[j] = xb[j] = Words<VEC>::zero();
+    if (in && p.has_a) xa[j] = __ldcs(reinterpret_cast<const V*>(x));
+    if (in && p.has_b) xb[j] = __ldcs(reinterpret_cast<const V*>(x + ab));
+    x += x_step;
+    if constexpr (kBwd) {
+      da[j] = db[j] = Words<VEC>::zero();
+      if (in && p.has_a) da[j] = __ldcs(reinterpret_cast<const V*>(dy));
+      if (in && p.has_b) db[j] = __ldcs(reinterpret_cast<const V*>(dy + ab));
+      dy += dy_step;
+    }
+    if (++load_step == per) {
+      load_step = 0;
+      load_t += walk;
+      x += x_jump;
+      if constexpr (kBwd) dy += dy_jump;
+    }
+  };
+  float2 ga[N], gb[N], dga[N], dgb[N];
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) dga[k][i] = dgb[k][i] = 0.0f;
-  }
+  for (int i = 0; i < N; ++i) ga[i] = gb[i] = dga[i] = dgb[i] = make_float2(0.0f, 0.0f);
   grid_dependency_wait();
-  const int64_t units = r.tokens * chunks;
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * 8;
-  for (int64_t unit = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); unit < units;
-       unit += warps) {
-    const int64_t t = chunks == 1 ? unit : unit / chunks;
-    const int chunk = static_cast<int>(unit - t * chunks);
-    const int first = static_cast<int>(static_cast<int64_t>(its) * chunk / chunks);
-    const int last = static_cast<int>(static_cast<int64_t>(its) * (chunk + 1) / chunks);
-    const int64_t pos = r.positions ? r.positions[t] : t;
-    float c[VEC], s[VEC];
-    turn_of<VEC, INTER>(r, p, pos, c, s);
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const HeadSet& set = r.set[k];
-      const int from = k == 0 ? first : max(first - its0, 0);
-      const int to = k == 0 ? min(last, its0) : last - its0;
-      if (from >= to) continue;
-      float ga[VEC], gb[VEC];
-      if constexpr (MODE != kRope) {
-        load_gain<VEC>(set.gain, r.gain_bf16, p.a, p.has_a, ga);
-        load_gain<VEC>(set.gain, r.gain_bf16, p.b, p.has_b, gb);
+  for (int j = 0; j < STEPS; ++j) load(j);
+  int64_t pos = t < r.tokens ? (r.positions ? r.positions[t] : t) : 0;
+  if constexpr (MODE != kRope) {
+    auto gain = [&](int i, int j, int s) {
+      if (!exists<VEC, INTER>(p, i, s)) return 0.0f;
+      const int e = element_of<VEC, INTER>(p, i, j, s);
+      return r.gain_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(set.gain)[e])
+                         : static_cast<const float*>(set.gain)[e];
+    };
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      ga[i] = make_float2(gain(i, 0, 0), gain(i, 1, 0));
+      gb[i] = make_float2(gain(i, 0, 1), gain(i, 1, 1));
+    }
+  }
+  float *cosine = tables[warp][0], *sine = tables[warp][1];
+#pragma unroll 1
+  for (; t < r.tokens; t += walk) {
+    __syncwarp();
+    fill_turns(r, pos, lane, cosine, sine);
+    __syncwarp();
+    if (t + walk < r.tokens) pos = r.positions ? r.positions[t + walk] : t + walk;
+    float2 c[N], s[N];
+    auto turns = [&]() {   // the lane's pairs, VEC from VEC u on
+      if (!p.rot_a) return;
+      load_turns<VEC>(cosine + VEC * u, c);
+      load_turns<VEC>(sine + VEC * u, s);
+      if (kBwd || r.inverse) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) s[i] = neg2(s[i]);
       }
-      const uint16_t* x = set.x + t * set.x_token;
-      const uint16_t* dy = kBwd ? set.dy + t * set.dy_token : nullptr;
-      V xa, xb, da, db;
-      auto load = [&](int it) {
-        const int head = it * groups + g;
-        const bool in = it < to && head < set.heads;
-        xa = xb = da = db = R::zero();
-        const uint16_t* row = x + head * set.x_head;
-        if (in && p.has_a) xa = __ldcs(reinterpret_cast<const V*>(row + p.a));
-        if (in && p.has_b) xb = __ldcs(reinterpret_cast<const V*>(row + p.b));
-        if constexpr (kBwd) {
-          const uint16_t* drow = dy + head * set.dy_head;
-          if (in && p.has_a) da = __ldcs(reinterpret_cast<const V*>(drow + p.a));
-          if (in && p.has_b) db = __ldcs(reinterpret_cast<const V*>(drow + p.b));
-        }
-      };
-      load(from);
-      for (int it = from; it < to; ++it) {
-        const int head = it * groups + g;
-        float a[VEC], b[VEC], na[VEC], nb[VEC];
-        R::unpack(xa, a);
-        R::unpack(xb, b);
-        if constexpr (kBwd) {
-          R::unpack(da, na);
-          R::unpack(db, nb);
-        }
-        load(it + 1);
+    };
+    if constexpr (!kBwd) turns();
+#pragma unroll 1
+    for (int step = 0; step < per; step += STEPS) {
+#pragma unroll
+      for (int j = 0; j < STEPS; ++j) {
+        float2 a[N], b[N], na[N], nb[N];
+        to_pairs<VEC, INTER>(xa[j], xb[j], a, b);
+        if constexpr (kBwd) to_pairs<VEC, INTER>(da[j], db[j], na, nb);
+        load(j);
         if constexpr (MODE != kRope) {
-          float ss = 0.0f;
+          float2 sq = make_float2(0.0f, 0.0f);
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) ss = fmaf(a[i], a[i], fmaf(b[i], b[i], ss));
-          ss = head_sum(ss, lanes);
-          const float rstd = rsqrtf(__fdiv_rn(ss, static_cast<float>(r.dim)) + r.eps);
+          for (int i = 0; i < N; ++i) sq = fma2(b[i], b[i], fma2(a[i], a[i], sq));
+          const float rstd = rsqrtf(head_sum(sq.x + sq.y, lanes) * r.inv_dim + r.eps);
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) {
-            a[i] *= rstd;
-            b[i] *= rstd;
+          for (int i = 0; i < N; ++i) {
+            a[i] = mul2(a[i], dup2(rstd));
+            b[i] = mul2(b[i], dup2(rstd));
           }
           if constexpr (kBwd) {
-            turn<VEC, INTER>(p, c, s, true, na, nb);   // the gradient of the normed head
-            float dot = 0.0f;
+            turns();                      // (again: registers are short)
+            turn<VEC>(p, c, s, na, nb);   // the gradient of the normed head
+            float2 dots = make_float2(0.0f, 0.0f);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-              const float ta = na[i] * a[i], tb = nb[i] * b[i];
-              dga[k][i] += ta;
-              dgb[k][i] += tb;
-              dot = fmaf(ta, ga[i], fmaf(tb, gb[i], dot));
+            for (int i = 0; i < N; ++i) {
+              dga[i] = fma2(na[i], a[i], dga[i]);
+              dgb[i] = fma2(nb[i], b[i], dgb[i]);
+              na[i] = mul2(na[i], ga[i]);
+              nb[i] = mul2(nb[i], gb[i]);
+              dots = fma2(nb[i], b[i], fma2(na[i], a[i], dots));
             }
-            dot = __fdiv_rn(head_sum(dot, lanes), static_cast<float>(r.dim));
+            const float dot = head_sum(dots.x + dots.y, lanes) * r.inv_dim;
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-              a[i] = rstd * fmaf(-dot, a[i], na[i] * ga[i]);
-              b[i] = rstd * fmaf(-dot, b[i], nb[i] * gb[i]);
+            for (int i = 0; i < N; ++i) {
+              a[i] = mul2(dup2(rstd), fma2(dup2(-dot), a[i], na[i]));
+              b[i] = mul2(dup2(rstd), fma2(dup2(-dot), b[i], nb[i]));
             }
           } else {
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-              a[i] *= ga[i];
-              b[i] *= gb[i];
+            for (int i = 0; i < N; ++i) {
+              a[i] = mul2(a[i], ga[i]);
+              b[i] = mul2(b[i], gb[i]);
             }
           }
         }
-        if constexpr (!kBwd) turn<VEC, INTER>(p, c, s, r.inverse, a, b);
-        uint16_t* row = set.y + t * set.y_token + head * set.y_head;
-        if (head < set.heads) {
-          if (p.has_a) __stcs(reinterpret_cast<V*>(row + p.a), R::pack(a));
-          if (p.has_b) __stcs(reinterpret_cast<V*>(row + p.b), R::pack(b));
-        }
+        if constexpr (!kBwd) turn<VEC>(p, c, s, a, b);
+        V va, vb;
+        from_pairs<VEC, INTER>(a, b, va, vb);
+        const bool in = head0 + (step + j) * groups < end;
+        if (in && p.has_a) __stcs(reinterpret_cast<V*>(y), va);
+        if (in && p.has_b) __stcs(reinterpret_cast<V*>(y + ab), vb);
+        y += y_step;
       }
     }
+    y += y_jump;
   }
   grid_dependency_trigger();
   if constexpr (kBwd) {
-    // The gains' gradients: the head groups of a warp, then the block's warps, each in a
+    // The gain's gradient: the head groups of a warp, then the block's warps, each in a
     // fixed order; the block leaves one partial row, or the result where it is alone.
-    if (!r.set[0].dgain && !r.set[1].dgain) return;
-    __shared__ float sum[8][512];   // [warp][set][element]
-    const int warp = threadIdx.x >> 5;
+    if (!set.dgain) return;
+    __shared__ float sum[8][256];   // [warp][element]
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        for (int o = 16; o >= lanes; o >>= 1) {
-          dga[k][i] += __shfl_xor_sync(0xffffffffu, dga[k][i], o);
-          dgb[k][i] += __shfl_xor_sync(0xffffffffu, dgb[k][i], o);
-        }
-        if (g == 0 && p.has_a) sum[warp][k * r.dim + p.a + i] = dga[k][i];
-        if (g == 0 && p.has_b) sum[warp][k * r.dim + p.b + i] = dgb[k][i];
+    for (int i = 0; i < N; ++i) {
+      for (int o = 16; o >= lanes; o >>= 1) {
+        dga[i].x += __shfl_xor_sync(0xffffffffu, dga[i].x, o);
+        dga[i].y += __shfl_xor_sync(0xffffffffu, dga[i].y, o);
+        dgb[i].x += __shfl_xor_sync(0xffffffffu, dgb[i].x, o);
+        dgb[i].y += __shfl_xor_sync(0xffffffffu, dgb[i].y, o);
       }
+      if (g == 0 && exists<VEC, INTER>(p, i, 0)) {
+        sum[warp][element_of<VEC, INTER>(p, i, 0, 0)] = dga[i].x;
+        sum[warp][element_of<VEC, INTER>(p, i, 1, 0)] = dga[i].y;
+      }
+      if (g == 0 && exists<VEC, INTER>(p, i, 1)) {
+        sum[warp][element_of<VEC, INTER>(p, i, 0, 1)] = dgb[i].x;
+        sum[warp][element_of<VEC, INTER>(p, i, 1, 1)] = dgb[i].y;
+      }
+    }
     __syncthreads();
-    for (int e = threadIdx.x; e < 2 * r.dim; e += 256) {
+    if (static_cast<int>(threadIdx.x) < r.dim) {
       float v = 0.0f;
 #pragma unroll
-      for (int w = 0; w < 8; ++w) v += sum[w][e];
-      const int k = e >= r.dim;
-      if (gridDim.x > 1) r.part[static_cast<int64_t>(blockIdx.x) * 2 * r.dim + e] = v;
-      else if (r.set[k].dgain) r.set[k].dgain[e - k * r.dim] = v;
+      for (int w = 0; w < 8; ++w) v += sum[w][threadIdx.x];
+      const bool alone = grid.set[k].chunks * grid.set[k].blocks == 1;
+      (alone ? set.dgain : r.part + static_cast<int64_t>(blockIdx.x) * r.dim)[threadIdx.x] = v;
     }
   }
 }
 
-// The partial rows of `blocks` blocks: 16 columns a block, 64 runs of rows side by side.
-__global__ void __launch_bounds__(1024) qk_dgain_kernel(const float* part, int blocks, int dim,
-                                                        float* dq_gain, float* dk_gain) {
+// The partial rows of each set: 16 columns a block, 64 runs of rows side by side.
+__global__ void __launch_bounds__(1024) qk_dgain_kernel(const float* part, int rows0, int rows1,
+                                                        int dim, float* dq_gain, float* dk_gain) {
   __shared__ float sum[64][17];
   const int col = threadIdx.x & 15, run = threadIdx.x >> 4;
-  const int e = blockIdx.x * 16 + col;
+  const int c = blockIdx.x * 16 + col, k = blockIdx.y;
+  const int first = k ? rows0 : 0, rows = k ? rows1 : rows0;
+  float* out = k ? dk_gain : dq_gain;
   grid_dependency_wait();
   grid_dependency_trigger();
+  if (!out || rows <= 1) return;   // (one row: written where it belongs)
   float s = 0.0f;
-  if (e < 2 * dim)
-    for (int b = run; b < blocks; b += 64) s += __ldcg(part + static_cast<int64_t>(b) * 2 * dim + e);
+  if (c < dim) {
+#pragma unroll 4
+    for (int b = run; b < rows; b += 64) s += __ldcg(part + static_cast<int64_t>(first + b) * dim + c);
+  }
   sum[run][col] = s;
   __syncthreads();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;   // a warp a column
@@ -300,14 +405,13 @@ __global__ void __launch_bounds__(1024) qk_dgain_kernel(const float* part, int b
   s = sum[lane][warp] + sum[lane + 32][warp];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  const int at = blockIdx.x * 16 + warp;
-  if (lane != 0 || at >= 2 * dim) return;
-  float* out = at < dim ? dq_gain : dk_gain;
-  if (out) out[at < dim ? at : at - dim] = s;
+  if (lane == 0 && blockIdx.x * 16 + warp < dim) out[blockIdx.x * 16 + warp] = s;
 }
 
 struct RopePlan {
-  int vec, lanes, chunks, grid;
+  int vec;
+  RopeGrid grid;
+  int blocks(int k) const { return grid.set[k].chunks * grid.set[k].blocks; }
 };
 int round_up_pow2(int n) {
   int p = 1;
@@ -315,58 +419,75 @@ int round_up_pow2(int n) {
   return p;
 }
 // Vectors of eight, or of four where half the rotated part is no multiple of eight.
-// Chunks: a warp a token where the tokens fill the GPU (16 warps an SM), else as many
-// warps a token as there are head groups.
-RopePlan rope_plan(int64_t tokens, int heads0, int heads1, int dim, int rot, bool interleaved,
-                   bool backward, int num_sms) {
+// As many blocks as are resident at once, shared among the chunks by their steps (and
+// two for a token's sines and cosines), or one a chunk and eight tokens where there are
+// fewer.
+RopePlan rope_plan(const RopeArgs& a, bool backward, int num_sms) {
   RopePlan p;
-  p.vec = interleaved || rot % 16 == 0 ? 8 : 4;
-  const int turning = rot / (2 * p.vec), rest = dim - rot;
-  const int need = interleaved ? (dim + 15) / 16
-                               : turning + (rest + 2 * p.vec - 1) / (2 * p.vec);
-  p.lanes = round_up_pow2(need);
-  const int groups = 32 / p.lanes;
-  const int its = (heads0 + groups - 1) / groups + (heads1 + groups - 1) / groups;
-  const int64_t target = static_cast<int64_t>(num_sms) * 16;
-  int64_t chunks = (target + tokens - 1) / tokens;
-  p.chunks = static_cast<int>(chunks < its ? chunks : its);
-  const int64_t blocks = (tokens * p.chunks + 7) / 8;
-  const int64_t most = static_cast<int64_t>(num_sms) * (backward ? 2 : 4);
-  p.grid = static_cast<int>(blocks < most ? blocks : most);
+  p.vec = a.interleaved || a.rot % 16 == 0 ? 8 : 4;
+  const int turning = a.rot / (2 * p.vec), rest = a.dim - a.rot;
+  const int need = a.interleaved ? (a.dim + 15) / 16
+                                 : turning + (rest + 2 * p.vec - 1) / (2 * p.vec);
+  p.grid.lanes = round_up_pow2(need);
+  const int groups = 32 / p.grid.lanes;
+  const int flight = backward ? kStepsBwd : kStepsFwd;
+  const int64_t cap = static_cast<int64_t>(num_sms) * (backward ? kBlocksBwd : kBlocksFwd);
+  const int64_t full = (a.tokens + 7) / 8;
+  // few tokens: shorter chunks, for more blocks
+  int most = backward ? kChunkBwd : kChunkFwd;
+  auto chunks_of = [&](int k) {
+    const int steps = (a.set[k].heads + groups - 1) / groups;
+    return (steps + most - 1) / most;
+  };
+  while (most > flight && full * (chunks_of(0) + chunks_of(1)) * 2 <= cap) most /= 2;
+  int64_t weight = 0;
+  for (int k = 0; k < 2; ++k) {
+    auto& s = p.grid.set[k];
+    const int steps = (a.set[k].heads + groups - 1) / groups;
+    s.chunks = chunks_of(k);
+    s.per = s.chunks ? ((steps + s.chunks - 1) / s.chunks + flight - 1) / flight * flight : 0;
+    if (s.per) s.chunks = (steps + s.per - 1) / s.per;
+    weight += static_cast<int64_t>(s.chunks) * (s.per + 2);
+  }
+  for (int k = 0; k < 2; ++k) {
+    auto& s = p.grid.set[k];
+    int64_t n = s.chunks ? cap * (s.per + 2) / weight : 1;
+    n = n < full ? n : full;
+    s.blocks = static_cast<int>(n > 1 ? n : 1);
+  }
   return p;
 }
 
 template <int MODE>
 cudaError_t launch_mode(const RopeArgs& a, const RopePlan& p, cudaStream_t stream) {
   auto go = [&](auto kern) {
-    return launch_chained(kern, p.grid, 256, 0, 0, stream, a, p.lanes, p.chunks);
+    return launch_chained(kern, p.blocks(0) + p.blocks(1), 256, 0, 0, stream, a, p.grid);
   };
   if (a.interleaved) return go(rope_kernel<8, true, MODE>);
   return p.vec == 8 ? go(rope_kernel<8, false, MODE>) : go(rope_kernel<4, false, MODE>);
-}
-RopePlan plan_of(const RopeArgs& a, bool backward, int num_sms) {
-  return rope_plan(a.tokens, a.set[0].heads, a.sets > 1 ? a.set[1].heads : 0, a.dim, a.rot,
-                   a.interleaved != 0, backward, num_sms);
 }
 
 }  // namespace
 
 cudaError_t launch_rope(const RopeArgs& a, int num_sms, cudaStream_t stream) {
-  return launch_mode<kRope>(a, plan_of(a, false, num_sms), stream);
+  return launch_mode<kRope>(a, rope_plan(a, false, num_sms), stream);
 }
 cudaError_t launch_qk_norm_rope(const RopeArgs& a, int num_sms, cudaStream_t stream) {
-  return launch_mode<kQkNorm>(a, plan_of(a, false, num_sms), stream);
+  return launch_mode<kQkNorm>(a, rope_plan(a, false, num_sms), stream);
 }
 
-int qk_bwd_blocks(int num_sms) { return 2 * num_sms; }
+// A block a chunk at least: kMaxHeads heads of each kind, one a step where they are widest.
+int qk_bwd_blocks(int num_sms) { return kBlocksBwd * num_sms + 2 * (kMaxHeads / kStepsBwd); }
 
 cudaError_t launch_qk_norm_rope_bwd(const RopeArgs& a, int num_sms, cudaStream_t stream) {
-  const RopePlan p = plan_of(a, true, num_sms);
+  const RopePlan p = rope_plan(a, true, num_sms);
   const cudaError_t e = launch_mode<kQkNormBwd>(a, p, stream);
-  float* k_gain = a.sets > 1 ? a.set[1].dgain : nullptr;
-  if (e != cudaSuccess || p.grid == 1 || (!a.set[0].dgain && !k_gain)) return e;
-  return launch_chained(qk_dgain_kernel, (2 * a.dim + 15) / 16, 1024, 0, 0, stream,
-                        static_cast<const float*>(a.part), p.grid, a.dim, a.set[0].dgain, k_gain);
+  if (e != cudaSuccess) return e;
+  const bool join = (a.set[0].dgain && p.blocks(0) > 1) || (a.set[1].dgain && p.blocks(1) > 1);
+  if (!join) return e;
+  return launch_chained_2d(qk_dgain_kernel, dim3((a.dim + 15) / 16, 2, 1), 1024, 0, 0, stream,
+                           static_cast<const float*>(a.part), p.blocks(0), p.blocks(1), a.dim,
+                           a.set[0].dgain, a.set[1].dgain);
 }
 
 }  // namespace forge

@@ -150,11 +150,13 @@ def test_linear(bt, d_in, d_out, name):
 
 @pytest.mark.parametrize("bt,d_in,d_out", [(1, 64, 8), (40, 200, 328), (300, 136, 1040),
                                            (700, 1024, 1160), (2100, 72, 2600), (1, 8, 40000)])
-@pytest.mark.parametrize("cg", [1, 2])
+@pytest.mark.parametrize("bn,splits", [(0, 1), (128, 1), (256, 1), (0, 2), (128, 4), (256, 2),
+                                       (256, 4)])
 @pytest.mark.parametrize("name", ["plain", "all", "all_fp32"])
-def test_linear_by_tile(bt, d_in, d_out, cg, name, tune):
-    """Both tiles, also where the other would be taken, with several tiles a CTA."""
-    tune(cg=cg)
+def test_linear_by_tile(bt, d_in, d_out, bn, splits, name, tune):
+    """The many-token forms by tile and split, also of reductions with fewer steps than
+    pairs, with several tiles a pair."""
+    tune(cg=2, bn=bn, splits=splits)
     c = linear_case(bt, d_in, d_out, **EPILOGUES[name])
     call_linear(c)
     check_linear(c)
@@ -169,6 +171,16 @@ def test_linear_by_splits(bt, splits, tune):
         c = linear_case(bt, d_in, d_out, **EPILOGUES["all"])
         call_linear(c)
         check_linear(c)
+
+
+@pytest.mark.parametrize("bt,d_out", [(2000, 4096), (1000, 4800), (2000, 3400), (1500, 5000),
+                                      (520, 88), (2300, 2200)])
+@pytest.mark.parametrize("name", ["all", "fp32", "gate"])
+def test_linear_by_tile_width(bt, d_out, name):
+    """Sizes that take tiles of other widths (the rule counts waves)."""
+    c = linear_case(bt, 136, d_out, **EPILOGUES[name])
+    call_linear(c)
+    check_linear(c)
 
 
 def test_linear_few_tokens_more_tiles_than_sms():

@@ -77,28 +77,40 @@ forge_status drop_args(const forge_drop* d, DropArgs* out) {
 Span counter_span(const DropArgs& d) { return Span{d.counter, 8}; }
 
 // ---------------------------------------------------------------- the product
-// The tile: up to 128 tokens the outputs lie along M (forge_gemm_linear_few.cu) and the
+// The tile.  Up to 128 tokens the outputs lie along M (forge_gemm_linear_few.cu) and the
 // reduction is split over as many CTAs of a cluster as leave at most one CTA an SM, with
-// four steps each at least.  Beyond, 256 x 256 on CTA pairs or 128 x 128 on single CTAs,
-// by the waves each takes.
+// four steps each at least.  Beyond, pairs with 256 tokens and bn outputs, by a count of
+// cycles: a step of 64 takes as long as its operands need at the 64 bytes a cycle that an
+// SM loads, 256 + bn (for bn = 256 as long as its products); the tiles of persistent pairs
+// go in waves, those of a split reduction all at once, with an exchange of sums at the end;
+// the last tile's epilogue follows the products.
 LinearConfig choose_linear(int64_t m, int64_t n, int64_t num_kb, const forge_tuning& tune,
-                           int num_sms) {
-  LinearConfig c{1, 128, 0, 1};
+                           int num_sms, const int (&clusters)[3]) {
   if (m <= 128 && tune.cta_group == 0) {
-    c.few = m <= 16 ? 16 : (m <= 32 ? 32 : (m <= 64 ? 64 : 128));
+    LinearConfig c{m <= 16 ? 16 : (m <= 32 ? 32 : (m <= 64 ? 64 : 128)), 128, 1};
     const int64_t tiles = (n + 127) / 128;
     while (c.splits < 8 && tiles * c.splits * 2 <= num_sms && num_kb >= 8 * c.splits) c.splits *= 2;
     if (tune.splits)   // the cluster sizes there are: powers of two
       c.splits = tune.splits >= 8 ? 8 : (tune.splits >= 4 ? 4 : (tune.splits >= 2 ? 2 : 1));
     return c;
   }
-  const int64_t pairs = num_sms / 2;
-  const int64_t tiles1 = (m + 127) / 128 * ((n + 127) / 128);
-  const int64_t tiles2 = (m + 255) / 256 * ((n + 255) / 256);
-  const int64_t t1 = (tiles1 + num_sms - 1) / num_sms * 300;
-  const int64_t t2 = (tiles2 + pairs - 1) / pairs * 530;
-  if (tune.cta_group ? tune.cta_group == 2 : t2 < t1) c.cg = 2, c.bn = 256;
-  return c;
+  const int64_t pairs = clusters[0], tiles_m = (m + 255) / 256;
+  LinearConfig best{0, 256, 1};
+  int64_t least = INT64_MAX;
+  for (int splits = 1; splits <= 4; splits *= 2)
+    for (int bn = 256; bn >= 64; bn -= 32) {
+      if (tune.splits && splits != (tune.splits >= 4 ? 4 : (tune.splits >= 2 ? 2 : 1))) continue;
+      if (tune.bn && bn != tune.bn) continue;
+      if (bn % (16 * splits) != 0) continue;   // eight columns a warp at least
+      const int64_t tiles = tiles_m * ((n + bn - 1) / bn);
+      if (splits > 1 && tiles > clusters[splits / 2] && !tune.splits) continue;
+      const int64_t steps = (num_kb + splits - 1) / splits;
+      const int64_t waves = splits > 1 ? 1 : (tiles + pairs - 1) / pairs;
+      int64_t cost = waves * steps * (256 + bn) + 24 * bn / splits;
+      if (splits > 1) cost += 3000;
+      if (cost < least) least = cost, best = LinearConfig{0, bn, splits};
+    }
+  return best;
 }
 
 }  // namespace
@@ -140,25 +152,21 @@ forge_status forge_linear_bf16(const void* X, const void* W, void* Y, forge_dtyp
   forge_tuning tune;
   forge_get_tuning(&tune);
   const int64_t num_kb = (d_in + 63) / 64;
-  const LinearConfig cfg = choose_linear(bt, d_out, num_kb, tune, d.num_sms);
-  const int64_t tm = 128 * cfg.cg, tiles_m = cfg.few ? 1 : (bt + tm - 1) / tm;
+  int clusters[3] = {0, 0, 0};   // of one, two and four pairs
+  if (bt > 128 || tune.cta_group != 0)
+    for (int i = 0; i < 3; ++i) {
+      const cudaError_t r = linear_clusters(1 << i, d.num_sms, &clusters[i]);
+      if (r != cudaSuccess) return status(r);
+    }
+  const LinearConfig cfg = choose_linear(bt, d_out, num_kb, tune, d.num_sms, clusters);
+  const int64_t tiles_m = cfg.few ? 1 : (bt + 255) / 256;
   const int64_t tiles_n = (d_out + cfg.bn - 1) / cfg.bn;
   if (tiles_m * tiles_n > kMaxIndex / 8) return FORGE_ERR_SHAPE;
   const CUtensorMapDataType b16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
-  const uint32_t rows_a = cfg.few ? cfg.few : 128, rows_b = cfg.few ? 128 : cfg.bn / cfg.cg;
-  auto box = [&](CUtensorMap* map, const void* p, bool f32) {
-    return host_map(map, p, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : b16, n, m, n * (f32 ? 4 : 2),
-                    f32 ? 32 : 64, 32, sw);
-  };
+  const uint32_t rows_a = cfg.few ? cfg.few : 128, rows_b = cfg.few ? 128 : cfg.bn / 2;
   bool maps = host_map(&a.a, X, b16, k, m, k * 2, 64, rows_a, sw) &&
               host_map(&a.b, W, b16, k, n, k * 2, 64, rows_b, sw);
-  if (!cfg.few) {
-    maps = maps && box(&a.y, Y, es == 4);
-    if (e.mul) maps = maps && box(&a.mul, e.mul, false);
-    if (e.residual) maps = maps && box(&a.residual, e.residual, false);
-    if (e.z) maps = maps && box(&a.z, e.z, false);
-  }
   if (!maps) return FORGE_ERR_LAUNCH;
   a.e.bias = e.bias;
   a.e.bias_bf16 = e.bias && e.bias_dtype == FORGE_DT_BF16;
@@ -175,6 +183,9 @@ forge_status forge_linear_bf16(const void* X, const void* W, void* Y, forge_dtyp
   a.tiles_n = static_cast<int32_t>(tiles_n);
   a.num_tiles = static_cast<int32_t>(tiles_m * tiles_n);
   a.group_m = 8;
+  a.bn = cfg.bn;
+  a.wide = d_out % 16 == 0 && aligned(Y, 32) && aligned(e.mul, 32) && aligned(e.residual, 32) &&
+           aligned(e.z, 32);
   a.splits = cfg.splits;
   a.err = d.err;
   a.err_site = d.err_site;
@@ -182,7 +193,7 @@ forge_status forge_linear_bf16(const void* X, const void* W, void* Y, forge_dtyp
   a.drop_first_arrival = host_drop_flag();
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   return status(cfg.few ? launch_gemm_linear_few(cfg.few, a, d.num_sms, cs)
-                        : launch_gemm_linear(cfg, a, d.num_sms, cs));
+                        : launch_gemm_linear(a, d.num_sms, cs));
 }
 
 size_t forge_epilogue_backward_workspace_bytes(int64_t rows, int64_t cols) {

@@ -1,15 +1,23 @@
 // The forward product of a linear layer in 16 bits with its epilogue:
 //   Z = X W^T + bias,   Y = residual + drop(act(Z) * mul).
-// X [m, k] and W [n, k] are both K-major; a tile's whole reduction stays in tensor
-// memory (fp32), and the epilogue works on it while the next tile's products run in
-// the other accumulator.
+// X [m, k] and W [n, k] are both K-major.  A pair of CTAs computes a tile of 256 tokens
+// x BN outputs (BN a multiple of 32 up to 256), 128 tokens each, from its own tokens and
+// half of the weight's rows each; the tile's whole reduction stays in tensor memory
+// (fp32).
 //
-// Warp roles (384 threads): warp 0 loads operand stages 64 deep with TMA, warp 1
-// issues the MMAs, warps 4-11 are the epilogue (two per TMEM lane quadrant, each half
-// of the tile's columns).  An epilogue warp works on boxes of 32 rows x 64 columns:
-// residual and mul come into its two slabs of shared memory by TMA, ahead of the
-// accumulator, and Y and Z leave from the same slabs, whose every 16 bytes one thread
-// reads before it writes them.  Every wait is bounded, as in forge_gemm.cuh.
+// Two forms.  Many tiles: persistent pairs with two accumulators each, so that the
+// epilogue works on one tile while the next tile's products run.  Few tiles: the
+// reduction of a tile is split over the S pairs of a cluster, which send each other
+// parts of their sums through distributed shared memory (into the operand stages, done
+// with by then); each pair adds up BN / S columns in a fixed order and applies the
+// epilogue to them.  The same result on every run, no workspace.
+//
+// Warp roles (384 threads): warp 0 loads operand stages 64 deep with TMA, warp 1 issues
+// the MMAs, warps 4-11 are the epilogue (two per TMEM lane quadrant): a lane holds a
+// token's row, 32 columns at a time.  residual and mul of the next 32 columns are loaded
+// into registers ahead of the arithmetic, and Y and Z stored from registers, a sector
+// or more a lane: shared memory is left to the operands.  Every wait is bounded, as in
+// forge_gemm.cuh.
 #include <cuda_bf16.h>
 
 #include "forge_internal.h"
@@ -25,26 +33,20 @@ constexpr int kThreadsL = 384;
 constexpr int kEpiWarpsL = 8;
 constexpr int kSmemMaxL = 232448;   // dynamic shared memory of one CTA (227 KB)
 
-// CG CTAs compute a (128 CG) x BN tile; a CTA loads its 128 rows of X and BN / CG
-// rows of W per stage.
-template <int CG, int BN>
-struct TraitsL {
-  static constexpr int TM = kBM * CG;
-  static constexpr int BNL = BN / CG;
+// Shared memory from a 1024-aligned base: operand stages (128 tokens' and up to 128
+// outputs' rows of 64), barriers.
+struct SmemL {
   static constexpr int A_BYTES = kBM * 128;
-  static constexpr int STAGE_BYTES = A_BYTES + BNL * 128;
-  static constexpr int SLAB = 4096;                      // 32 rows x 128 bytes
-  static constexpr int OUT_BYTES = kEpiWarpsL * 2 * SLAB;
-  static constexpr int STAGES = 5;
-  static constexpr int GROUPS = BN / 128;                // boxes of 64 columns per epilogue warp
-  static constexpr int TMEM_COLS = 2 * BN;               // two accumulators
-  static constexpr int OFF_OUT = STAGES * STAGE_BYTES;
-  static constexpr int OFF_BARS = OFF_OUT + OUT_BYTES;
-  static constexpr int NUM_BARS = 2 * STAGES + 4 + 1 + kEpiWarpsL;
+  static constexpr int STAGE_BYTES = 2 * A_BYTES;
+  static constexpr int STAGES = 7;
+  static constexpr int OFF_BARS = STAGES * STAGE_BYTES;
+  static constexpr int NUM_BARS = 2 * STAGES + 5;
   static constexpr int OFF_TMEM = OFF_BARS + 8 * NUM_BARS;
-  static constexpr int SMEM_USED = OFF_TMEM + 8;
-  static constexpr int SMEM_ALLOC = SMEM_USED + 1024 < kSmemMaxL ? SMEM_USED + 1024 : kSmemMaxL;
-  static_assert(SMEM_USED <= kSmemMaxL, "shared memory budget exceeded");
+  static constexpr int USED = OFF_TMEM + 8;
+  static constexpr int ALLOC = USED + 1024 < kSmemMaxL ? USED + 1024 : kSmemMaxL;
+  static_assert(USED <= kSmemMaxL, "shared memory budget exceeded");
+  // the split form's shares: three quarters of a CTA's 128 x 256 sums at most
+  static_assert(kBM * 256 * 4 * 3 / 4 <= OFF_BARS, "shares");
 };
 
 // Tile order: groups of group_m tile rows, column by column inside a group, so that
@@ -58,25 +60,113 @@ __device__ __forceinline__ void tile_of(int t, const LinearArgs& a, int& tm, int
   tm = m0 + r - tn * gm;
 }
 
-template <int CG, int BN>
+// What an epilogue lane needs of residual, mul and bias for up to 32 columns of its row.
+struct Ahead {
+  uint4 res[4], mul[4];
+  float bias;   // lane l: that of column l
+};
+// 32 bytes (a sector) at once where everything is aligned to them, else 16.
+__device__ __forceinline__ void load32(const uint16_t* p, bool wide, bool second, uint4& x,
+                                       uint4& y) {
+  if (wide) {
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w), "=r"(y.x), "=r"(y.y), "=r"(y.z),
+                   "=r"(y.w)
+                 : "l"(p));
+  } else {
+    x = reinterpret_cast<const uint4*>(p)[0];
+    if (second) y = reinterpret_cast<const uint4*>(p)[1];
+  }
+}
+__device__ __forceinline__ void store32(void* p, bool wide, bool second, uint4 x, uint4 y) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x.x),
+                 "r"(x.y), "r"(x.z), "r"(x.w), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w)
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(p)[0] = x;
+    if (second) reinterpret_cast<uint4*>(p)[1] = y;
+  }
+}
+__device__ __forceinline__ void ask(const LinearArgs& a, int row, int col, int lane, Ahead& in) {
+  if (row < a.m) {
+    const int64_t at = static_cast<int64_t>(row) * a.n + col;
+    const bool wide = a.wide && col % 16 == 0;
+#pragma unroll
+    for (int c = 0; c < 4; c += 2) {
+      if (col + 8 * c >= a.n) break;
+      const bool second = col + 8 * c + 8 < a.n;
+      if (a.e.residual)
+        load32(a.e.residual + at + 8 * c, wide, second, in.res[c], in.res[c + 1]);
+      if (a.e.mul) load32(a.e.mul + at + 8 * c, wide, second, in.mul[c], in.mul[c + 1]);
+    }
+  }
+  if (a.e.bias && col + lane < a.n)
+    in.bias = a.e.bias_bf16
+                  ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.e.bias)[col + lane])
+                  : static_cast<const float*>(a.e.bias)[col + lane];
+}
+// The epilogue of 16 columns, from the c-th eight of the 32 on, and their stores.
+template <int ACT>
+__device__ __forceinline__ void finish16(float (&v)[2][8], const LinearArgs& a, const Ahead& in,
+                                         int c, int row, int col, uint64_t offset, bool last) {
+  uint4 z[2];
+  const uint64_t block = static_cast<uint64_t>(row) * (a.n / 8) + col / 8;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (a.e.bias) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[i][k] += __shfl_sync(0xffffffffu, in.bias, 8 * (c + i) + k);
+    }
+    z[i] = epilogue8<ACT>(v[i], a.e, in.mul[c + i], in.res[c + i], offset, block + i);
+  }
+  if (row < a.m && col < a.n) {
+    const bool second = !last && col + 8 < a.n, wide = a.wide && second && col % 16 == 0;
+    const int64_t at = static_cast<int64_t>(row) * a.n + col;
+    if (a.e.z) store32(a.e.z + at, wide, second, z[0], z[1]);
+    if (a.e.y_fp32) {
+      float* y = static_cast<float*>(a.e.y) + at;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (i == 0 || second)
+          store32(y + 8 * i, a.wide, true,
+                  make_uint4(__float_as_uint(v[i][0]), __float_as_uint(v[i][1]),
+                             __float_as_uint(v[i][2]), __float_as_uint(v[i][3])),
+                  make_uint4(__float_as_uint(v[i][4]), __float_as_uint(v[i][5]),
+                             __float_as_uint(v[i][6]), __float_as_uint(v[i][7])));
+    } else {
+      store32(static_cast<uint16_t*>(a.e.y) + at, wide, second, pack8(v[0]), pack8(v[1]));
+    }
+  }
+  __syncwarp();
+}
+
+template <bool SPLIT, int ACT>
 __global__ void __launch_bounds__(kThreadsL, 1)
     gemm_linear_kernel(const __grid_constant__ LinearArgs a) {
-  using T = TraitsL<CG, BN>;
-  constexpr bool kPair = CG == 2;
+  using T = SmemL;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* gbase = smem_raw + (base - raw);
-  if (base - raw + T::SMEM_USED > T::SMEM_ALLOC) {   // uniform: nothing has started
+  if (base - raw + T::USED > T::ALLOC) {   // uniform: nothing has started
     grid_dependency_wait();   // the launch after this one may rely on those before it
     if (threadIdx.x == 0) atomicCAS(a.err, 0, kErrDeviceConfig);
     return;
   }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = kPair ? cluster_ctarank() : 0u;
+  const uint32_t crank = cluster_ctarank();
+  const uint32_t rank = crank & 1u;                    // in the pair
+  const uint32_t lead = crank & ~1u;                   // the pair's leader in the cluster
+  const int share = SPLIT ? static_cast<int>(crank >> 1) : 0;
   const bool leader = rank == 0;
-  const int unit0 = kPair ? static_cast<int>(cluster_id_x()) : static_cast<int>(blockIdx.x);
-  const int units = kPair ? static_cast<int>(cluster_count_x()) : static_cast<int>(gridDim.x);
+  const int unit0 = static_cast<int>(cluster_id_x());
+  const int units = static_cast<int>(cluster_count_x());
+  // this pair's steps of the reduction
+  const int kb = SPLIT ? b128_first_block(share, a.splits, a.num_kb) : 0;
+  const int ke = SPLIT ? b128_first_block(share + 1, a.splits, a.num_kb) : a.num_kb;
+  const int bn = a.bn, bnl = bn / 2;
+  const uint32_t tx = 2 * (T::A_BYTES + bnl * 128);   // both CTAs' bytes a stage
 
   const uint32_t bars = base + T::OFF_BARS;
   auto bar_full = [&](int s) { return bars + 8u * s; };
@@ -84,7 +174,6 @@ __global__ void __launch_bounds__(kThreadsL, 1)
   auto bar_tfull = [&](int b) { return bars + 8u * (2 * T::STAGES + b); };
   auto bar_tempty = [&](int b) { return bars + 8u * (2 * T::STAGES + 2 + b); };
   const uint32_t bar_drain = bars + 8u * (2 * T::STAGES + 4);
-  auto bar_in = [&](int w) { return bars + 8u * (2 * T::STAGES + 5 + w); };
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(gbase + T::OFF_TMEM + 4);
   const WaitCtx wc{abort_flag, a.err, a.err_site, a.timeout_ns};
 
@@ -95,10 +184,9 @@ __global__ void __launch_bounds__(kThreadsL, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(bar_tfull(b), 1);
-      mbar_init(bar_tempty(b), CG * kEpiWarpsL);
+      mbar_init(bar_tempty(b), 2 * kEpiWarpsL);
     }
     mbar_init(bar_drain, 1);
-    for (int w = 0; w < kEpiWarpsL; ++w) mbar_init(bar_in(w), 1);
     *abort_flag = 0u;
     fence_mbarrier_init();
     drop_first_arrival(a.drop_first_arrival, bar_full(0));
@@ -106,17 +194,11 @@ __global__ void __launch_bounds__(kThreadsL, 1)
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&a.a);
     tma_prefetch_desc(&a.b);
-    tma_prefetch_desc(&a.y);
   }
-  if constexpr (kPair) cluster_sync_all(); else __syncthreads();
+  cluster_sync_all();
   if (warp == 1) {
-    if constexpr (kPair) {
-      tmem_alloc_pair(base + T::OFF_TMEM, T::TMEM_COLS);
-      tmem_relinquish_pair();
-    } else {
-      tmem_alloc(base + T::OFF_TMEM, T::TMEM_COLS);
-      tmem_relinquish();
-    }
+    tmem_alloc_pair(base + T::OFF_TMEM, 512);
+    tmem_relinquish_pair();
   }
   tc_fence_before_sync();
   __syncthreads();
@@ -124,310 +206,293 @@ __global__ void __launch_bounds__(kThreadsL, 1)
   grid_dependency_wait();
   const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(gbase + T::OFF_TMEM);
 
-  if (warp < 4) {
-    if (warp == 0) {
-      // ------------------------------------------------------------ producer
-      if (lane == 0) {
-        const uint64_t pol = l2_policy_evict_normal();
-        uint32_t s = 0, ph = 0;   // next stage, and its phase
-        uint32_t armed = 0;       // stages filled so far, at most STAGES
-        bool ok = true;
-        for (int t = unit0; ok && t < a.num_tiles; t += units) {
-          int tm, tn;
-          tile_of(t, a, tm, tn);
-          const int ya = tm * T::TM + static_cast<int>(rank) * kBM;
-          const int yb = tn * BN + static_cast<int>(rank) * T::BNL;
-          for (int k = 0; k < a.num_kb; ++k) {
-            if (!wait_bounded(bar_empty(s), ph ^ 1u, wc, kSiteProducerEmpty)) { ok = false; break; }
-            const uint32_t dst = base + s * T::STAGE_BYTES;
-            if constexpr (kPair) {
-              const uint32_t fb = mapa_shared(bar_full(s), 0);
-              if (leader) mbar_arrive_expect_tx(bar_full(s), 2 * T::STAGE_BYTES);
-              tma_load_2d_pair(dst, &a.a, k * 64, ya, fb, pol);
-              tma_load_2d_pair(dst + T::A_BYTES, &a.b, k * 64, yb, fb, pol);
-            } else {
-              mbar_arrive_expect_tx(bar_full(s), T::STAGE_BYTES);
-              tma_load_2d(dst, &a.a, k * 64, ya, bar_full(s), pol);
-              tma_load_2d(dst + T::A_BYTES, &a.b, k * 64, yb, bar_full(s), pol);
-            }
-            if (armed < T::STAGES) ++armed;
-            if (++s == T::STAGES) { s = 0; ph ^= 1u; }
-          }
-        }
-        // Before the CTA can exit, every stage's last release has to arrive (on a pair
-        // the leader's MMAs signal it from afar); after a timeout, every load that is
-        // under way has to land (a pair's complete on the leader's barriers).
-        for (uint32_t i = 0; i < armed; ++i) {
-          if (s == 0) { s = T::STAGES; ph ^= 1u; }
-          --s;
-          const bool freed = ok && wait_bounded(bar_empty(s), ph, wc, kSiteDrainOperands);
-          if (!freed && leader) wait_bounded(bar_full(s), ph, wc, kSiteDrainOperands, false);
+  // the epilogue warps: TMEM lane quadrant, half of the columns
+  const int q = warp & 3, h = warp >= 4 ? (warp - 4) >> 2 : 0;
+  const uint32_t lane_addr = static_cast<uint32_t>(q * 32) << 16;
+  const uint64_t offset = a.e.drop.threshold ? drop_offset(a.e.drop) : 0;
+  Ahead in;
+
+  if (warp == 0) {
+    // -------------------------------------------------------------- producer
+    if (lane == 0) {
+      const uint64_t pol = l2_policy_evict_normal();
+      uint32_t s = 0, ph = 0;   // next stage, and its phase
+      uint32_t armed = 0;       // stages filled so far, at most STAGES
+      bool ok = true;
+      for (int t = unit0; ok && t < a.num_tiles; t += units) {
+        int tm, tn;
+        tile_of(t, a, tm, tn);
+        const int ya = tm * 2 * kBM + static_cast<int>(rank) * kBM;
+        const int yb = tn * bn + static_cast<int>(rank) * bnl;
+        for (int k = kb; k < ke; ++k) {
+          if (!wait_bounded(bar_empty(s), ph ^ 1u, wc, kSiteProducerEmpty)) { ok = false; break; }
+          const uint32_t dst = base + s * T::STAGE_BYTES;
+          const uint32_t fb = mapa_shared(bar_full(s), lead);
+          if (leader) mbar_arrive_expect_tx(bar_full(s), tx);
+          tma_load_2d_pair(dst, &a.a, k * 64, ya, fb, pol);
+          tma_load_2d_pair(dst + T::A_BYTES, &a.b, k * 64, yb, fb, pol);
+          if (armed < T::STAGES) ++armed;
+          if (++s == T::STAGES) { s = 0; ph ^= 1u; }
         }
       }
-      __syncwarp();
-    } else if (warp == 1) {
-      // ------------------------------------------------------------ MMA issuer
-      // The whole warp walks the stages, so that addresses and descriptors stay in
-      // uniform registers, and one elected lane issues.
-      if (leader) {
-        constexpr uint32_t idesc = make_idesc_bf16(T::TM, BN, false, false);
-        const uint64_t ad0 = make_sdesc_k_sw128(base, 1024);
-        const uint64_t bd0 = make_sdesc_k_sw128(base + T::A_BYTES, 1024);
-        const bool issue = elect_one();
-        uint32_t s = 0, ph = 0, buf = 0, bph = 1;
-        bool ok = true;
-        for (int t = unit0; ok && t < a.num_tiles; t += units) {
-          ok = __all_sync(0xffffffffu,
-                          wait_bounded(bar_tempty(buf), bph, wc, kSiteMmaTmemEmpty));
+      // Before the CTA can exit, every stage's last release has to arrive (the leader's
+      // MMAs signal it from afar); after a timeout, every load that is under way has to
+      // land (they complete on the leader's barriers).
+      for (uint32_t i = 0; i < armed; ++i) {
+        if (s == 0) { s = T::STAGES; ph ^= 1u; }
+        --s;
+        const bool freed = ok && wait_bounded(bar_empty(s), ph, wc, kSiteDrainOperands);
+        if (!freed && leader) wait_bounded(bar_full(s), ph, wc, kSiteDrainOperands, false);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // -------------------------------------------------------------- MMA issuer
+    // The whole warp walks the stages, so that addresses and descriptors stay in
+    // uniform registers, and one elected lane issues.
+    if (leader) {
+      const uint32_t idesc = make_idesc_bf16(2 * kBM, bn, false, false);
+      const uint64_t ad0 = make_sdesc_k_sw128(base, 1024);
+      const uint64_t bd0 = make_sdesc_k_sw128(base + T::A_BYTES, 1024);
+      const uint16_t both = static_cast<uint16_t>(3u << lead);
+      const bool issue = elect_one();
+      uint32_t s = 0, ph = 0, buf = 0, bph = 1;
+      bool ok = true;
+      for (int t = unit0; ok && t < a.num_tiles; t += units) {
+        ok = __all_sync(0xffffffffu, wait_bounded(bar_tempty(buf), bph, wc, kSiteMmaTmemEmpty));
+        if (!ok) break;
+        tc_fence_after_sync();
+        const uint32_t d = tmem_base + buf * 256;
+#pragma unroll 1
+        for (int k = kb; k < ke; ++k) {
+          ok = __all_sync(0xffffffffu, wait_bounded(bar_full(s), ph, wc, kSiteMmaFull));
           if (!ok) break;
           tc_fence_after_sync();
-          const uint32_t d = tmem_base + buf * BN;
-#pragma unroll 1
-          for (int k = 0; k < a.num_kb; ++k) {
-            ok = __all_sync(0xffffffffu, wait_bounded(bar_full(s), ph, wc, kSiteMmaFull));
-            if (!ok) break;
-            tc_fence_after_sync();
-            const uint64_t ad = ad0 + s * (T::STAGE_BYTES >> 4);
-            const uint64_t bd = bd0 + s * (T::STAGE_BYTES >> 4);
-            if (issue) {
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk) {   // 16 of K: 32 bytes
-                if constexpr (kPair)
-                  umma_bf16_pair(d, ad + 2 * kk, bd + 2 * kk, idesc, (k | kk) != 0);
-                else
-                  umma_bf16(d, ad + 2 * kk, bd + 2 * kk, idesc, (k | kk) != 0);
-              }
-              if constexpr (kPair) umma_commit_pair_mc(bar_empty(s), 0x3);
-              else umma_commit(bar_empty(s));
-            }
-            if (++s == T::STAGES) { s = 0; ph ^= 1u; }
-          }
-          if (!ok) break;
+          const uint64_t ad = ad0 + s * (T::STAGE_BYTES >> 4);
+          const uint64_t bd = bd0 + s * (T::STAGE_BYTES >> 4);
           if (issue) {
-            if constexpr (kPair) umma_commit_pair_mc(bar_tfull(buf), 0x3);
-            else umma_commit(bar_tfull(buf));
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)   // 16 of K: 32 bytes
+              umma_bf16_pair(d, ad + 2 * kk, bd + 2 * kk, idesc, ((k - kb) | kk) != 0);
+            umma_commit_pair_mc(bar_empty(s), both);
           }
-          if (++buf == 2) { buf = 0; bph ^= 1u; }
+          if (++s == T::STAGES) { s = 0; ph ^= 1u; }
         }
-        // every MMA issued must complete before the tensor memory is freed
-        if (issue) {
-          if constexpr (kPair) umma_commit_pair_mc(bar_drain, 0x1); else umma_commit(bar_drain);
-        }
-        wait_bounded(bar_drain, 0u, wc, kSiteDrainMma, false);
+        if (!ok) break;
+        if (issue) umma_commit_pair_mc(bar_tfull(buf), both);
+        if (++buf == 2) { buf = 0; bph ^= 1u; }
       }
-      __syncwarp();
+      // every MMA issued must complete before the tensor memory is freed
+      if (issue) umma_commit_pair_mc(bar_drain, static_cast<uint16_t>(1u << lead));
+      wait_bounded(bar_drain, 0u, wc, kSiteDrainMma, false);
     }
-  } else {
-    // ------------------------------------------------------------ epilogue
-    const int q = warp & 3;                       // TMEM lane quadrant this warp may read
-    const int h = (warp - 4) >> 2;                // half of the tile's columns
-    const uint32_t lane_addr = static_cast<uint32_t>(q * 32) << 16;
-    const uint32_t slab_y = base + T::OFF_OUT + (warp - 4) * 2 * T::SLAB;
-    const uint32_t slab_z = slab_y + T::SLAB;
-    uint8_t* gy = gbase + T::OFF_OUT + (warp - 4) * 2 * T::SLAB;
-    uint8_t* gz = gy + T::SLAB;
-    const uint32_t bin = bar_in(warp - 4);
-    const uint64_t pol = l2_policy_evict_first();
-    const bool loads = a.e.mul || a.e.residual;
-    const uint32_t in_bytes = (a.e.mul ? T::SLAB : 0) + (a.e.residual ? T::SLAB : 0);
-    const uint64_t offset = drop_offset(a.e.drop);
-    const int64_t nv = a.n / 8;
-
-    // The boxes of this warp in order: group g of tile t.  (Those outside the matrix
-    // are passed over by loads, arithmetic and stores alike.)
-    auto place = [&](int t, int g, int& row0, int& col) {
+    __syncwarp();
+  } else if (!SPLIT && warp >= 4) {
+    // -------------------------------------------------------------- epilogue
+    // the warp's boxes of 32 columns in a tile
+    const int boxes = (bn / 32 + 1 - h) / 2, box0 = h * ((bn / 32 + 1) / 2);
+    auto place = [&](int t, int b, int& row0, int& col) {
       int tm, tn;
       tile_of(t, a, tm, tn);
-      row0 = tm * T::TM + static_cast<int>(rank) * kBM + q * 32;
-      col = tn * BN + h * (BN / 2) + g * 64;
-      return row0 < a.m && col < a.n;
+      row0 = tm * 2 * kBM + static_cast<int>(rank) * kBM + q * 32;
+      col = tn * bn + (box0 + b) * 32;
     };
-    auto next = [&](int& t, int& g) {
-      if (++g == T::GROUPS) { g = 0; t += units; }
-    };
-    // loads the inputs of the next box there is from (t, g) on
-    auto ask = [&](int t, int g) {
+    uint32_t buf = 0, bph = 0;
+    bool ok = true;
+    {
       int row0, col;
-      while (t < a.num_tiles && !place(t, g, row0, col)) next(t, g);
-      if (t >= a.num_tiles) return false;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(bin, in_bytes);
-        if (a.e.residual) tma_load_2d(slab_y, &a.residual, col, row0, bin, pol);
-        if (a.e.mul) tma_load_2d(slab_z, &a.mul, col, row0, bin, pol);
+      if (unit0 < a.num_tiles) {
+        place(unit0, 0, row0, col);
+        ask(a, row0 + lane, col, lane, in);
       }
-      return true;
-    };
-    uint32_t buf = 0, bph = 0, iph = 0;
-    bool ok = true, asked = loads && ask(unit0, 0);
+    }
     for (int t = unit0; ok && t < a.num_tiles; t += units) {
       ok = __all_sync(0xffffffffu,
                       wait_bounded_inline(bar_tfull(buf), bph, wc, kSiteEpiTmemFull));
       if (!ok) break;
       tc_fence_after_sync();
-      auto release = [&]() {   // this warp has read its part of the accumulator
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) {
-          if constexpr (kPair) mbar_arrive_cluster_relaxed(mapa_shared(bar_tempty(buf), 0));
-          else mbar_arrive(bar_tempty(buf));
-        }
-      };
 #pragma unroll 1
-      for (int g = 0; g < T::GROUPS; ++g) {
-        const bool last = g == T::GROUPS - 1;
+      for (int b = 0; b < boxes; ++b) {
         int row0, col;
-        if (!place(t, g, row0, col)) {
-          if (last) release();
-          continue;
-        }
-        if (loads) {
-          ok = __all_sync(0xffffffffu, wait_bounded_inline(bin, iph, wc, kSiteEpiSlotFull));
-          if (!ok) break;
-          asked = false;
-          iph ^= 1u;
-        } else {   // the slabs are free once the stores before have read them
-          if (lane == 0) bulk_wait_group_read<0>();
-          __syncwarp();
-        }
-        const uint32_t taddr = tmem_base + lane_addr + buf * BN + h * (BN / 2) + g * 64;
-        const uint64_t block0 = static_cast<uint64_t>(row0 + lane) * nv + col / 8;
-        // an fp32 box holds half the columns, in the place of all the residual's
-        uint4 later[4];
-        if (a.e.y_fp32 && a.e.residual) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            later[c] = *reinterpret_cast<const uint4*>(gy + sw128_off(lane, 4 + c));
-        }
-#pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          uint32_t r[32];
-          tmem_ld_x32(taddr + 32 * half, r);
-          tmem_ld_wait();
-          if (last && half == 1) release();
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int cc = 4 * half + c;
-            float v[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(r[8 * c + k]);
-            const uint32_t at = sw128_off(lane, cc);
-            uint4 mul = make_uint4(0, 0, 0, 0), res = mul;
-            if (a.e.mul) mul = *reinterpret_cast<const uint4*>(gz + at);
-            if (a.e.residual)
-              res = a.e.y_fp32 && half == 1 ? later[c] : *reinterpret_cast<const uint4*>(gy + at);
-            // columns past the last: the bias is not read there
-            const int64_t bc = col + 8 * cc < a.n ? col + 8 * cc : 0;
-            const uint4 z = epilogue8(v, a.e, bc, mul, res, offset, block0 + cc);
-            if (a.e.z) *reinterpret_cast<uint4*>(gz + at) = z;
-            if (!a.e.y_fp32) {
-              *reinterpret_cast<uint4*>(gy + at) = pack8(v);
-            } else {
-#pragma unroll
-              for (int k = 0; k < 8; ++k) r[8 * c + k] = __float_as_uint(v[k]);
-            }
-          }
-          if (a.e.y_fp32 && col + 32 * half < a.n) {   // a box of 32 columns
-            if (half == 1) {
-              if (lane == 0) bulk_wait_group_read<0>();
-              __syncwarp();
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              *reinterpret_cast<uint4*>(gy + sw128_off(lane, i)) =
-                  make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              tma_store_2d(&a.y, col + 32 * half, row0, slab_y);
-              bulk_commit_group();
-            }
+        place(t, b, row0, col);
+        const bool there = row0 < a.m && col < a.n;   // the same in all lanes
+        uint32_t r[32];
+        tmem_ld_x32(tmem_base + lane_addr + buf * 256 + (box0 + b) * 32, r);
+        const Ahead now = in;
+        {   // the next box's inputs
+          const bool wrap = b + 1 == boxes;
+          const int nt = wrap ? t + units : t;
+          int nrow, ncol;
+          if (nt < a.num_tiles) {
+            place(nt, wrap ? 0 : b + 1, nrow, ncol);
+            ask(a, nrow + lane, ncol, lane, in);
           }
         }
-        if (!a.e.y_fp32 || a.e.z) {
-          fence_proxy_async_smem();
+        tmem_ld_wait();
+        if (b == boxes - 1) {   // this warp has read its part of the accumulator
+          tc_fence_before_sync();
           __syncwarp();
-          if (lane == 0) {
-            if (!a.e.y_fp32) tma_store_2d(&a.y, col, row0, slab_y);
-            if (a.e.z) tma_store_2d(&a.z, col, row0, slab_z);
-            bulk_commit_group();
-          }
+          if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(bar_tempty(buf), lead));
         }
-        if (loads) {
-          if (lane == 0) bulk_wait_group_read<0>();
-          __syncwarp();
-          int nt = t, ng = g;
-          next(nt, ng);
-          asked = ask(nt, ng);
+        if (!there) continue;
+#pragma unroll
+        for (int c = 0; c < 4; c += 2) {
+          float v[2][8];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) v[k / 8][k % 8] = __uint_as_float(r[8 * c + k]);
+          finish16<ACT>(v, a, now, c, row0 + lane, col + 8 * c, offset, false);
         }
       }
       if (!ok) break;
       if (++buf == 2) { buf = 0; bph ^= 1u; }
     }
-    if (asked) wait_bounded(bin, iph, wc, kSiteDrainState, false);   // after a timeout
-    if (lane == 0) bulk_wait_group<0>();
     __syncwarp();
+  }
+
+  if constexpr (SPLIT) {
+    // -------------------------------------------------------------- join and store
+    // Columns of the tile: share z's are those from z bn / S on, half a warp's each.  A
+    // share's sums lie in shared memory as [four columns][row], 16 bytes a row.
+    const int width = bn / a.splits, half = width / 2;
+    int tm, tn;
+    tile_of(unit0, a, tm, tn);
+    const int row = tm * 2 * kBM + static_cast<int>(rank) * kBM + q * 32 + lane;
+    const int col0 = tn * bn + share * width + h * half;
+    // this pair's sums of eight columns (none: it had no steps)
+    auto sums8 = [&](int c, float (&v)[8]) {
+      tmem_ld_x8(tmem_base + lane_addr + c, reinterpret_cast<uint32_t(&)[8]>(v));
+      tmem_ld_wait();
+      if (ke <= kb) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = 0.0f;
+      }
+    };
+    bool ok = true;
+    if (warp >= 4) {
+      ask(a, row, col0, lane, in);
+      ok = __all_sync(0xffffffffu, wait_bounded(bar_tfull(0), 0u, wc, kSiteEpiTmemFull));
+      tc_fence_after_sync();
+    }
+    tc_fence_before_sync();
+    cluster_sync_all();   // every CTA's products have run: its stages are free
+    tc_fence_after_sync();
+    if (warp >= 4) {
+      const uint32_t me = base + static_cast<uint32_t>(q * 32 + lane) * 16;
+      for (int d = 1; d < a.splits; ++d) {
+        const int z = (share + d) % a.splits;
+        // among the shares that z receives this one is the (share - z - 1)-th modulo S
+        const int slot = (share - z - 1 + a.splits) % a.splits;
+        const uint32_t dst = mapa_shared(me + (slot * width + h * half) / 4 * (kBM * 16),
+                                         2 * z + rank);
+        for (int c = 0; c < half; c += 8) {
+          float v[8];
+          sums8(z * width + h * half + c, v);
+          st_cluster_f32x4(dst + c / 4 * (kBM * 16), v[0], v[1], v[2], v[3]);
+          st_cluster_f32x4(dst + (c / 4 + 1) * (kBM * 16), v[4], v[5], v[6], v[7]);
+        }
+      }
+    }
+    cluster_sync_all();
+    if (warp >= 4 && ok && !*abort_flag) {
+      const float* part = reinterpret_cast<const float*>(gbase) + (q * 32 + lane) * 4;
+      for (int c0 = 0; c0 < half; c0 += 32) {
+        if (c0 > 0) ask(a, row, col0 + c0, lane, in);
+#pragma unroll
+        for (int c = 0; c < 4; c += 2) {
+          const int cc = c0 + 8 * c;
+          if (cc >= half) break;
+          float v[2][8];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if (i == 1 && cc + 8 >= half) break;   // the half's last eight columns
+            sums8(share * width + h * half + cc + 8 * i, v[i]);
+            for (int slot = 0; slot + 1 < a.splits; ++slot) {
+              const float* p = part + (slot * width + h * half + cc + 8 * i) / 4 * (kBM * 4);
+              const float4 x = *reinterpret_cast<const float4*>(p);
+              const float4 y = *reinterpret_cast<const float4*>(p + kBM * 4);
+              v[i][0] += x.x; v[i][1] += x.y; v[i][2] += x.z; v[i][3] += x.w;
+              v[i][4] += y.x; v[i][5] += y.y; v[i][6] += y.z; v[i][7] += y.w;
+            }
+          }
+          finish16<ACT>(v, a, in, c, row, col0 + cc, offset, cc + 8 >= half);
+        }
+      }
+    }
   }
 
   // ---------------------------------------------------------------- teardown
   grid_dependency_trigger();
   tc_fence_before_sync();
-  if constexpr (kPair) {
-    if (*abort_flag) {   // let copies in flight into this CTA land (see forge_gemm.cuh)
-      const uint64_t t0 = globaltimer_ns();
-      while (globaltimer_ns() - t0 < 200000ull) {
-      }
+  if (*abort_flag) {   // let copies in flight into this CTA land (see forge_gemm.cuh)
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 200000ull) {
     }
-    cluster_sync_all();
-  } else {
-    __syncthreads();
   }
+  cluster_sync_all();
   if (warp == 1) {
     tc_fence_after_sync();
-    if constexpr (kPair) tmem_dealloc_pair(tmem_base, T::TMEM_COLS);
-    else tmem_dealloc(tmem_base, T::TMEM_COLS);
+    tmem_dealloc_pair(tmem_base, 512);
   }
 }
 
-template <int CG, int BN>
-cudaError_t launch_t(const LinearArgs& a, int num_sms, cudaStream_t stream) {
-  using T = TraitsL<CG, BN>;
-  auto kern = gemm_linear_kernel<CG, BN>;
-  // the units that can be resident: CTAs, or (known to the occupancy) pairs
-  static PerDevice resident;
-  int units = 0;
-  const cudaError_t e = resident.get(&units, [&](int* n) {
-    cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         T::SMEM_ALLOC);
-    *n = num_sms;
-    if (CG == 1 || r != cudaSuccess) return r;
+// The clusters of 2 S CTAs that can be resident at once.
+template <bool SPLIT, int ACT>
+cudaError_t resident(int splits, int num_sms, int* n) {
+  static PerDevice kept[3];
+  return kept[splits == 1 ? 0 : (splits == 2 ? 1 : 2)].get(n, [&](int* v) {
+    cudaError_t r = cudaFuncSetAttribute(gemm_linear_kernel<SPLIT, ACT>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, SmemL::ALLOC);
+    if (r != cudaSuccess) return r;
+    const unsigned size = 2u * splits;
     cudaLaunchConfig_t lc = {};
-    lc.gridDim = dim3(2 * (num_sms / 2), 1, 1);
+    lc.gridDim = dim3(num_sms / size * size, 1, 1);
     lc.blockDim = dim3(kThreadsL, 1, 1);
-    lc.dynamicSmemBytes = T::SMEM_ALLOC;
+    lc.dynamicSmemBytes = SmemL::ALLOC;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.x = size;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     lc.attrs = attr;
     lc.numAttrs = 1;
-    r = cudaOccupancyMaxActiveClusters(n, kern, &lc);
-    if (r == cudaSuccess && *n <= 0) r = cudaErrorInvalidConfiguration;
-    *n = *n < num_sms / 2 ? *n : num_sms / 2;
+    r = cudaOccupancyMaxActiveClusters(v, gemm_linear_kernel<SPLIT, ACT>, &lc);
+    if (r == cudaSuccess && *v <= 0) r = cudaErrorInvalidConfiguration;
+    *v = *v < num_sms / static_cast<int>(size) ? *v : num_sms / static_cast<int>(size);
     return r;
   });
+}
+
+template <int ACT>
+cudaError_t launch_act(const LinearArgs& a, int num_sms, cudaStream_t stream) {
+  int units = 0;
+  if (a.splits > 1) {
+    const cudaError_t e = resident<true, ACT>(a.splits, num_sms, &units);
+    if (e != cudaSuccess) return e;
+    return launch_chained(gemm_linear_kernel<true, ACT>, 2 * a.splits * a.num_tiles, kThreadsL,
+                          SmemL::ALLOC, 2 * a.splits, stream, a);
+  }
+  const cudaError_t e = resident<false, ACT>(1, num_sms, &units);
   if (e != cudaSuccess) return e;
-  return launch_chained(kern, CG * (a.num_tiles < units ? a.num_tiles : units), kThreadsL,
-                        T::SMEM_ALLOC, CG == 2 ? 2 : 0, stream, a);
+  return launch_chained(gemm_linear_kernel<false, ACT>,
+                        2 * (a.num_tiles < units ? a.num_tiles : units), kThreadsL, SmemL::ALLOC, 2,
+                        stream, a);
 }
 
 }  // namespace
 
-cudaError_t launch_gemm_linear(const LinearConfig& c, const LinearArgs& a, int num_sms,
-                               cudaStream_t stream) {
-  if (c.cg == 1 && c.bn == 128) return launch_t<1, 128>(a, num_sms, stream);
-  if (c.cg == 2 && c.bn == 256) return launch_t<2, 256>(a, num_sms, stream);
-  return cudaErrorInvalidValue;
+cudaError_t linear_clusters(int splits, int num_sms, int* n) {
+  return splits == 1 ? resident<false, kActNone>(1, num_sms, n)
+                     : resident<true, kActNone>(splits, num_sms, n);
+}
+
+cudaError_t launch_gemm_linear(const LinearArgs& a, int num_sms, cudaStream_t stream) {
+  switch (a.e.act) {
+    case kActRelu: return launch_act<kActRelu>(a, num_sms, stream);
+    case kActGelu: return launch_act<kActGelu>(a, num_sms, stream);
+    case kActGeluTanh: return launch_act<kActGeluTanh>(a, num_sms, stream);
+    case kActSilu: return launch_act<kActSilu>(a, num_sms, stream);
+    default: return launch_act<kActNone>(a, num_sms, stream);
+  }
 }
 
 }  // namespace forge

@@ -224,8 +224,16 @@ __global__ void __launch_bounds__(FewL<NT>::THREADS, NT <= 64 ? 2 : 1)
         v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
         v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
       }
-      const int64_t col = tile * 128 + rank * slice + j;
-      const uint4 z = epilogue8(v, a.e, col, mul0, res0, offset, static_cast<uint64_t>(at));
+      if (a.e.bias) {
+        float b[8];
+        load_bias8(a.e.bias, a.e.bias_bf16, tile * 128 + rank * slice + j, b);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] += b[k];
+      }
+      uint4 z;
+      with_act(a.e.act, [&](auto act) {
+        z = epilogue8<decltype(act)::value>(v, a.e, mul0, res0, offset, static_cast<uint64_t>(at));
+      });
       if (a.e.z) reinterpret_cast<uint4*>(a.e.z)[at] = z;
       if (a.e.y_fp32) {
         float4* y = reinterpret_cast<float4*>(a.e.y) + 2 * at;

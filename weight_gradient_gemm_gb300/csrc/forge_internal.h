@@ -333,24 +333,27 @@ struct EpiArgs {
 
 // The 16-bit product of a linear layer (forge_gemm_linear.cu).
 struct LinearArgs {
-  CUtensorMap a, b;                 // tokens and weight
-  CUtensorMap mul, residual, z, y;  // boxes of 32 rows (many tokens; y also without them)
+  CUtensorMap a, b;         // operands: tokens and weight
   EpiArgs e;
-  int32_t m, n, num_kb;             // tokens, outputs, 64-deep steps of the reduction
+  int32_t m, n, num_kb;     // tokens, outputs, 64-deep steps of the reduction
   int32_t tiles_m, tiles_n, num_tiles, group_m;
-  int32_t splits, stages;           // few tokens: CTAs that share a tile's reduction; stages
+  int32_t bn;               // outputs of a pair's tile: a multiple of 32, at most 256
+  int32_t splits;           // pairs (few tokens: CTAs) of a cluster that share a tile's reduction
+  int32_t stages;           // few tokens: operand stages
+  int32_t wide;             // every row of the epilogue's matrices starts on 32 bytes
   int32_t drop_first_arrival;       // testing aid
   int* err;
   int* err_site;
   uint64_t timeout_ns;
 };
 struct LinearConfig {
-  int cg, bn;   // CTAs per tile and its columns
   int few;      // 0, or the tokens a tile holds when the outputs lie along M
-  int splits;   // few tokens: CTAs per tile
+  int bn;       // a pair's outputs (few tokens: 128)
+  int splits;   // pairs, or with few tokens CTAs, per tile
 };
-cudaError_t launch_gemm_linear(const LinearConfig& c, const LinearArgs& a, int num_sms,
-                               cudaStream_t stream);
+// The clusters of `splits` pairs that can be resident at once.
+cudaError_t linear_clusters(int splits, int num_sms, int* n);
+cudaError_t launch_gemm_linear(const LinearArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_gemm_linear_few(int nt, const LinearArgs& a, int num_sms, cudaStream_t stream);
 
 // The epilogue's gradient and dropout (forge_epilogue.cu).

@@ -24,6 +24,26 @@ constexpr float kGeluB = 0.044715f;
 constexpr float kInvSqrt2 = 0.7071067811865476f;
 constexpr float kInvSqrt2Pi = 0.3989422804014327f;
 
+// The normal distribution function, (1 + erf(z / sqrt 2)) / 2 = erfc(-z / sqrt 2) / 2.
+// erfc by the Chebyshev fit of Press et al., "Numerical Recipes" (erfcc): t e^(P(t) - x^2)
+// with t = 1 / (1 + x / 2), its relative error below 1.2 10^-7 for all x >= 0, so that the
+// tail below zero keeps its digits.  Without branches: in the product's epilogue erfcf
+// cost 8192 tokens, 4096 -> 14336, 35 us.
+__device__ __forceinline__ float normal_cdf(float z) {
+  const float x = fabsf(z) * kInvSqrt2;
+  const float t = __fdividef(1.0f, fmaf(0.5f, x, 1.0f));
+  float p = fmaf(t, 0.17087277f, -0.82215223f);
+  p = fmaf(t, p, 1.48851587f);
+  p = fmaf(t, p, -1.13520398f);
+  p = fmaf(t, p, 0.27886807f);
+  p = fmaf(t, p, -0.18628806f);
+  p = fmaf(t, p, 0.09678418f);
+  p = fmaf(t, p, 0.37409196f);
+  p = fmaf(t, p, 1.00002368f);
+  p = fmaf(t, p, -1.26551223f);
+  const float tail = 0.5f * t * __expf(fmaf(-x, x, p));
+  return z > 0.0f ? 1.0f - tail : tail;
+}
 // tanh(u) as 2 sigmoid(2u) - 1, so that z (1 + tanh u) / 2 = z sigmoid(2u).
 __device__ __forceinline__ float gelu_arg(float z) {
   return 2.0f * kGeluC * fmaf(kGeluB * z * z, z, z);
@@ -39,8 +59,7 @@ __device__ __forceinline__ float act_value(float z) {
   if constexpr (ACT == kActRelu) return z < 0.0f ? 0.0f : z;   // NaN stays NaN
   if constexpr (ACT == kActNone) return z;
   z = hold_low(z);
-  // 1 + erf(x) as erfc(-x), which keeps its digits where z is far below zero
-  if constexpr (ACT == kActGelu) return 0.5f * z * erfcf(-kInvSqrt2 * z);
+  if constexpr (ACT == kActGelu) return z * normal_cdf(z);
   if constexpr (ACT == kActGeluTanh) return z * sigmoid(gelu_arg(z));
   return z * sigmoid(z);   // kActSilu
 }
@@ -49,7 +68,7 @@ __device__ __forceinline__ float act_slope(float z) {
   if constexpr (ACT == kActRelu) return z > 0.0f ? 1.0f : (z <= 0.0f ? 0.0f : z);
   if constexpr (ACT == kActGelu) {
     const float h = hold(z);
-    return fmaf(h * kInvSqrt2Pi, __expf(-0.5f * h * h), 0.5f * erfcf(-kInvSqrt2 * h));
+    return fmaf(h * kInvSqrt2Pi, __expf(-0.5f * h * h), normal_cdf(h));
   }
   if constexpr (ACT == kActGeluTanh) {
     const float h = hold(z), s = sigmoid(gelu_arg(h));
@@ -122,24 +141,18 @@ __device__ __forceinline__ void load_bias8(const void* bias, int bf16, int64_t c
     b[4] = y.x; b[5] = y.y; b[6] = y.z; b[7] = y.w;
   }
 }
-// z = v + bias; returns it packed (for the stored pre-activation).  v becomes
-// residual + drop(act(z) mul).  mul, residual: eight bf16 values, read where the call
-// has them; block: the elements' dropout block.
-__device__ __forceinline__ uint4 epilogue8(float (&v)[8], const EpiArgs& e, int64_t col, uint4 mul,
+// With z (the bias is in it): returns it packed, for the stored pre-activation, and
+// makes it residual + drop(act(z) mul).  mul, residual: eight bf16 values, read where the
+// call has them; block: the elements' dropout block.
+template <int ACT>
+__device__ __forceinline__ uint4 epilogue8(float (&v)[8], const EpiArgs& e, uint4 mul,
                                            uint4 residual, uint64_t offset, uint64_t block) {
-  if (e.bias) {
-    float b[8];
-    load_bias8(e.bias, e.bias_bf16, col, b);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] += b[k];
-  }
   uint4 z = make_uint4(0, 0, 0, 0);
   if (e.z) z = pack8(v);
-  if (e.act != kActNone)
-    with_act(e.act, [&](auto t) {
+  if constexpr (ACT != kActNone) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = act_value<decltype(t)::value>(v[k]);
-    });
+    for (int k = 0; k < 8; ++k) v[k] = act_value<ACT>(v[k]);
+  }
   if (e.mul) {
     float m[8];
     unpack8(mul, m);

@@ -182,7 +182,7 @@ forge_status forge_linear_bf16(const void* X, const void* W, void* Y, forge_dtyp
   a.tiles_m = static_cast<int32_t>(tiles_m);
   a.tiles_n = static_cast<int32_t>(tiles_n);
   a.num_tiles = static_cast<int32_t>(tiles_m * tiles_n);
-  a.group_m = 8;
+  a.group_m = tune.group_m ? tune.group_m : 16;
   a.bn = cfg.bn;
   a.wide = d_out % 16 == 0 && aligned(Y, 32) && aligned(e.mul, 32) && aligned(e.residual, 32) &&
            aligned(e.z, 32);
@@ -200,8 +200,8 @@ size_t forge_epilogue_backward_workspace_bytes(int64_t rows, int64_t cols) {
   HostDevice d;
   if (rows < 0 || rows > kMaxIndex || cols <= 0 || cols > kMaxIndex || cols % 8 != 0) return 0;
   if (host_device(&d) != FORGE_OK) return 0;
-  const int parts = epilogue_bwd_blocks(rows, cols, d.num_sms);
-  return parts == 1 ? 0 : static_cast<size_t>(parts) * static_cast<size_t>(cols) * 4;
+  return static_cast<size_t>(epilogue_bwd_rows(rows, cols, d.num_sms)) *
+         static_cast<size_t>(cols) * 4;
 }
 
 forge_status forge_epilogue_backward(const void* dY, const void* Z, const void* mul,

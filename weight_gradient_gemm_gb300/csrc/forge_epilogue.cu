@@ -4,6 +4,7 @@
 #include "forge_internal.h"
 #include "forge_launch.cuh"
 #include "forge_layer.cuh"
+#include "forge_ptx.cuh"
 
 namespace forge {
 namespace {
@@ -103,17 +104,21 @@ __global__ void __launch_bounds__(256) epilogue_bwd_kernel(const EpiBwdArgs a) {
 }
 
 // With dbias: a block takes 128 columns and a run of rows, 16 lanes to a row; a thread
-// adds its eight columns over its rows, the block's 16 rows of sums are joined in shared
-// memory, and the block leaves one partial row (or, where it has all rows, dbias).
-constexpr int kBiasCols = 128;
+// adds its eight columns over its rows, and the block's 16 rows of sums are joined in
+// shared memory.  Up to eight runs of rows are the blocks of a cluster, whose first adds
+// up the others' sums through distributed shared memory: one launch.  More leave a partial
+// row each for a second one.
+constexpr int kBiasCols = 128, kBiasCluster = 8;
 template <int ACT, bool MUL>
-__global__ void __launch_bounds__(256) epilogue_bwd_bias_kernel(const EpiBwdArgs a) {
-  constexpr int U = 2;
+__global__ void __launch_bounds__(256) epilogue_bwd_bias_kernel(const EpiBwdArgs a, int parts, int cluster) {
+  constexpr int U = MUL ? 2 : 4;   // rows whose loads are in flight at once
   __shared__ float4 sums[16][kBiasCols / 4];
+  __shared__ float joined[kBiasCols];
   const int64_t nv = a.cols / 8;
-  const int64_t v = static_cast<int64_t>(blockIdx.x) * 16 + (threadIdx.x & 15);
-  const int64_t each = (a.rows + gridDim.y - 1) / gridDim.y;
-  const int64_t r0 = each * blockIdx.y, r1 = min(a.rows, r0 + each);
+  const int strip = static_cast<int>(blockIdx.x) / parts, part = blockIdx.x - strip * parts;
+  const int64_t v = static_cast<int64_t>(strip) * 16 + (threadIdx.x & 15);
+  const int64_t each = (a.rows + parts - 1) / parts;
+  const int64_t r0 = each * part, r1 = min(a.rows, r0 + each);
   float sum[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
   grid_dependency_wait();
   const uint64_t offset = drop_offset(a.drop);
@@ -145,14 +150,35 @@ __global__ void __launch_bounds__(256) epilogue_bwd_bias_kernel(const EpiBwdArgs
   sums[threadIdx.x >> 4][2 * (threadIdx.x & 15)] = make_float4(sum[0], sum[1], sum[2], sum[3]);
   sums[threadIdx.x >> 4][2 * (threadIdx.x & 15) + 1] = make_float4(sum[4], sum[5], sum[6], sum[7]);
   __syncthreads();
-  const int64_t col = static_cast<int64_t>(blockIdx.x) * kBiasCols + threadIdx.x;
-  if (threadIdx.x < kBiasCols && col < a.cols) {
-    float s = 0.0f;
+  const int64_t col = static_cast<int64_t>(strip) * kBiasCols + threadIdx.x;
+  float s = 0.0f;
+  if (threadIdx.x < kBiasCols) {
 #pragma unroll
     for (int r = 0; r < 16; ++r) s += reinterpret_cast<const float*>(sums[r])[threadIdx.x];
-    if (gridDim.y == 1) a.dbias[col] = s;
-    else a.part[blockIdx.y * a.cols + col] = s;
   }
+  if (cluster) {   // its rank is `part`
+    if (threadIdx.x < kBiasCols) joined[threadIdx.x] = s;
+    cluster_sync_all();
+    if (part == 0 && threadIdx.x < kBiasCols) {
+      const uint32_t at = smem_u32(joined + threadIdx.x);
+      for (int r = 1; r < parts; ++r) s += ld_cluster_f32(mapa_shared(at, r));
+    }
+    cluster_sync_all();   // no block leaves before its sums are read
+  }
+  if (threadIdx.x < kBiasCols && col < a.cols) {
+    if (!cluster && parts > 1) a.part[part * a.cols + col] = s;
+    else if (part == 0) a.dbias[col] = s;
+  }
+}
+
+// Runs of rows: about six blocks an SM, each with 32 rows at least; where that makes few
+// more than a cluster holds, as many as it holds.
+int bias_parts(int64_t rows, int64_t cols, int num_sms) {
+  const int64_t strips = (cols + kBiasCols - 1) / kBiasCols, blocks = 6LL * num_sms;
+  const int64_t most = (rows + 31) / 32, want = (blocks + strips - 1) / strips;
+  const int64_t n = want < most ? want : most;
+  if (n > kBiasCluster && n <= 2 * kBiasCluster) return kBiasCluster;
+  return static_cast<int>(n < 1 ? 1 : n);
 }
 
 template <int ACT, bool MUL>
@@ -162,11 +188,13 @@ cudaError_t launch_t(const EpiBwdArgs& a, int num_sms, cudaStream_t stream) {
     return launch_chained(epilogue_bwd_kernel<ACT, MUL>, static_cast<unsigned>(blocks), 256, 0, 0,
                           stream, a);
   }
-  const int parts = epilogue_bwd_blocks(a.rows, a.cols, num_sms);
-  const dim3 grid(static_cast<unsigned>((a.cols + kBiasCols - 1) / kBiasCols), parts, 1);
+  const int parts = bias_parts(a.rows, a.cols, num_sms);
+  const int64_t strips = (a.cols + kBiasCols - 1) / kBiasCols;
+  const bool cluster = parts > 1 && parts <= kBiasCluster;
   const cudaError_t e =
-      launch_chained_2d(epilogue_bwd_bias_kernel<ACT, MUL>, grid, 256, 0, 0, stream, a);
-  if (e != cudaSuccess || parts == 1) return e;
+      launch_chained(epilogue_bwd_bias_kernel<ACT, MUL>, static_cast<unsigned>(strips * parts), 256,
+                     0, cluster ? parts : 0, stream, a, parts, static_cast<int>(cluster));
+  if (e != cudaSuccess || parts == 1 || cluster) return e;
   return launch_join_rows(a.part, parts, static_cast<int>(a.cols), a.dbias, stream);
 }
 
@@ -183,12 +211,9 @@ cudaError_t launch_act(const EpiBwdArgs& a, int num_sms, cudaStream_t stream) {
 
 }  // namespace
 
-// About six blocks an SM, each with 32 rows at least.
-int epilogue_bwd_blocks(int64_t rows, int64_t cols, int num_sms) {
-  const int64_t strips = (cols + kBiasCols - 1) / kBiasCols;
-  const int64_t most = (rows + 31) / 32, want = (static_cast<int64_t>(num_sms) * 6 + strips - 1) / strips;
-  const int64_t n = want < most ? want : most;
-  return static_cast<int>(n < 1 ? 1 : n);
+int epilogue_bwd_rows(int64_t rows, int64_t cols, int num_sms) {
+  const int parts = bias_parts(rows, cols, num_sms);
+  return parts > kBiasCluster ? parts : 0;
 }
 
 cudaError_t launch_epilogue_bwd(const EpiBwdArgs& a, int num_sms, cudaStream_t stream) {

@@ -31,19 +31,18 @@ struct FewL {
   static constexpr int STAGE_BYTES = A_BYTES + NT * 128;
   // Operand stages: as many as let two CTAs share an SM, or, where the grid has no
   // more than one CTA for each, as many as fit.
-  static constexpr int STAGES = NT <= 16 ? 5 : (NT <= 32 ? 4 : 3);
-  static constexpr int DEEP = NT <= 16 ? 11 : (NT == 32 ? 9 : (NT == 64 ? 7 : 4));
+  static constexpr int STAGES = NT <= 16 ? 6 : (NT == 32 ? 5 : 4);
+  static constexpr int DEEP = NT <= 16 ? 12 : (NT == 32 ? 11 : (NT == 64 ? 9 : 7));
   static constexpr int TMEM_COLS = NT < 32 ? 32 : NT;
-  static constexpr int PART_BYTES = NT * kBM * 4;       // one tile of fp32 sums
   // Shared memory from a 1024-aligned base: barriers (the most there can be), abort
-  // flag, stages, the shares.
+  // flag, stages.  The shares, one tile of fp32 sums, take the stages' place once the
+  // products of all the cluster's CTAs have run.
   static constexpr int NUM_BARS = 2 * DEEP + 1;
   static constexpr int OFF_TMEM = 8 * NUM_BARS;
   static constexpr int OFF_STAGES = 1024;
-  static constexpr int smem(int stages) {
-    return OFF_STAGES + stages * STAGE_BYTES + PART_BYTES + 1024;
-  }
+  static constexpr int smem(int stages) { return OFF_STAGES + stages * STAGE_BYTES + 1024; }
   static_assert(OFF_TMEM + 8 <= OFF_STAGES, "barriers");
+  static_assert(NT * kBM * 4 <= STAGES * STAGE_BYTES, "shares");
   static_assert(NT > 64 || 2 * smem(STAGES) <= 228 * 1024 - 2 * 1024, "two CTAs an SM");
   static_assert(smem(DEEP) <= 232448, "shared memory budget");
 };
@@ -88,7 +87,6 @@ __global__ void __launch_bounds__(FewL<NT>::THREADS, NT <= 64 ? 2 : 1)
     tc_fence_before_sync();
   }
   __syncthreads();
-  if (splits > 1) cluster_arrive();   // waited for before the first remote store
   tc_fence_after_sync();
   // While the kernel before still runs, the weight's first steps are asked for as far
   // as L2, where all writes meet (see forge_gemm_b128_few.cu).
@@ -188,8 +186,9 @@ __global__ void __launch_bounds__(FewL<NT>::THREADS, NT <= 64 ? 2 : 1)
 
   // ------------------------------------------------------------ join and store
   grid_dependency_trigger();
-  const uint32_t off_part = T::OFF_STAGES + stages * T::STAGE_BYTES;
-  if (splits > 1) cluster_wait();   // every CTA has started
+  constexpr uint32_t off_part = T::OFF_STAGES;
+  // every CTA's products have run and its loads have landed (warps 0 and 1 waited)
+  if (splits > 1) cluster_sync_all(); else __syncthreads();
   if (warp >= 4) {
     const int h = (warp - 4) >> 2, o = (warp & 3) * 32 + lane;
     // [rank of the sender][token][output of the slice]

@@ -364,13 +364,13 @@ struct EpiBwdArgs {
   uint16_t* dz;
   uint16_t* dmul;
   float* dbias;
-  float* part;     // [epilogue_bwd_blocks][cols] partial sums of dbias
+  float* part;     // [epilogue_bwd_rows][cols] partial sums of dbias
   int64_t rows;
   int64_t cols;
   int32_t act;
   DropArgs drop;
 };
-int epilogue_bwd_blocks(int64_t rows, int64_t cols, int num_sms);   // rows of `part`
+int epilogue_bwd_rows(int64_t rows, int64_t cols, int num_sms);   // rows of `part`, 0: none
 cudaError_t launch_epilogue_bwd(const EpiBwdArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_dropout(const uint16_t* x, const uint16_t* residual, uint16_t* y, int64_t rows,
                            int64_t cols, const DropArgs& drop, cudaStream_t stream);

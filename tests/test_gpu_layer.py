@@ -150,13 +150,13 @@ def test_linear(bt, d_in, d_out, name):
 
 @pytest.mark.parametrize("bt,d_in,d_out", [(1, 64, 8), (40, 200, 328), (300, 136, 1040),
                                            (700, 1024, 1160), (2100, 72, 2600), (1, 8, 40000)])
-@pytest.mark.parametrize("bn,splits", [(0, 1), (128, 1), (256, 1), (0, 2), (128, 4), (256, 2),
-                                       (256, 4)])
+@pytest.mark.parametrize("cg,bn,splits", [(1, 0, 1), (1, 0, 2), (1, 0, 8), (2, 0, 0), (2, 128, 0),
+                                          (2, 256, 0)])
 @pytest.mark.parametrize("name", ["plain", "all", "all_fp32"])
-def test_linear_by_tile(bt, d_in, d_out, bn, splits, name, tune):
-    """The many-token forms by tile and split, also of reductions with fewer steps than
-    pairs, with several tiles a pair."""
-    tune(cg=2, bn=bn, splits=splits)
+def test_linear_by_tile(bt, d_in, d_out, cg, bn, splits, name, tune):
+    """Both forms, also where the other would be taken, by tile and split, also of
+    reductions with fewer steps than CTAs, with several tiles a pair."""
+    tune(cg=cg, bn=bn, splits=splits)
     c = linear_case(bt, d_in, d_out, **EPILOGUES[name])
     call_linear(c)
     check_linear(c)

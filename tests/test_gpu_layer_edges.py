@@ -222,8 +222,8 @@ def test_heads_leave_the_rest_alone(dim, rot):
 
 @pytest.mark.parametrize("bt,d_in,d_out,how", [
     (3, 4104, 264, {}), (100, 1032, 520, {}), (3, 264, 40000, {}),            # few tokens
-    (700, 520, 2056, dict(splits=1)), (3000, 264, 2600, dict(splits=1)),      # pairs
-    (300, 4104, 520, dict(splits=2)), (200, 4104, 264, dict(splits=4))])      # split reductions
+    (300, 4104, 520, dict(cg=1, splits=4)), (700, 264, 2056, dict(cg=1, splits=1)),
+    (700, 520, 2056, dict(cg=2)), (3000, 264, 2600, dict(cg=2))])             # pairs
 def test_linear_waits_run_out(bt, d_in, d_out, how, tune):
     """The first copy waits for bytes that never come: the kernel records the timeout and
     returns, the context stays usable, and what lies beside the outputs is not touched."""

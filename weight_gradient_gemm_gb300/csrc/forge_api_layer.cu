@@ -77,39 +77,40 @@ forge_status drop_args(const forge_drop* d, DropArgs* out) {
 Span counter_span(const DropArgs& d) { return Span{d.counter, 8}; }
 
 // ---------------------------------------------------------------- the product
-// The tile.  Up to 128 tokens the outputs lie along M (forge_gemm_linear_few.cu) and the
-// reduction is split over as many CTAs of a cluster as leave at most one CTA an SM, with
-// four steps each at least.  Beyond, pairs with 256 tokens and bn outputs, by a count of
-// cycles: a step of 64 takes as long as its operands need at the 64 bytes a cycle that an
-// SM loads, 256 + bn (for bn = 256 as long as its products); the tiles of persistent pairs
-// go in waves, those of a split reduction all at once, with an exchange of sums at the end;
-// the last tile's epilogue follows the products.
+// The tile, by a count of cycles.
+//   Single CTAs with 128 outputs along M and up to 128 tokens (forge_gemm_linear_few.cu):
+//   a step of 64 of the reduction takes 512 cycles with 128 tokens, what its operands need
+//   at the 64 bytes a cycle that an SM loads.  The reduction is split over a cluster as
+//   long as its CTAs are all resident at once (`clusters`: of 1, 2, 4 and 8) and have two
+//   steps each.  What follows takes 6000 cycles on one CTA, 5000 on two that share the
+//   epilogue, 4000 on more.
+//   Pairs with 256 tokens and bn outputs: 370 + 5 bn / 8 cycles a step (measured; 530 for
+//   bn = 256, whose products take 512), tiles in waves, the last tile's epilogue after them.
+// 333 tokens, 1032 -> 520, 7.3 us on single CTAs and 8.1 on pairs; 300, 4096 -> 1024, 9.7
+// and 17.9; 512, 4096 -> 14336, 62 and 40; 150, 4096 -> 14336, 48.6 and 26.8.
+// Up to 128 tokens the pairs' form would leave half of its rows empty (128 tokens, 4096 ->
+// 14336, 23.5 us and 30), and the weight's bytes need every SM: the largest split there is.
 LinearConfig choose_linear(int64_t m, int64_t n, int64_t num_kb, const forge_tuning& tune,
-                           int num_sms, const int (&clusters)[3]) {
-  if (m <= 128 && tune.cta_group == 0) {
-    LinearConfig c{m <= 16 ? 16 : (m <= 32 ? 32 : (m <= 64 ? 64 : 128)), 128, 1};
-    const int64_t tiles = (n + 127) / 128;
-    while (c.splits < 8 && tiles * c.splits * 2 <= num_sms && num_kb >= 8 * c.splits) c.splits *= 2;
-    if (tune.splits)   // the cluster sizes there are: powers of two
-      c.splits = tune.splits >= 8 ? 8 : (tune.splits >= 4 ? 4 : (tune.splits >= 2 ? 2 : 1));
-    return c;
+                           int num_sms, const int (&clusters)[4]) {
+  const int nt = m <= 16 ? 16 : (m <= 32 ? 32 : (m <= 64 ? 64 : 128));
+  const int64_t tiles = (n + 127) / 128 * ((m + 127) / 128);
+  LinearConfig best{nt, 128, 1};
+  int64_t least = (tiles + num_sms - 1) / num_sms * num_kb * 512 + 6000;
+  for (int i = 1; i <= 3; ++i) {
+    const int splits = 1 << i;
+    if (tune.splits ? splits > tune.splits : tiles > clusters[i] || num_kb < 2 * splits) continue;
+    const int64_t cost = (num_kb + splits - 1) / splits * 512 + (splits > 2 ? 4000 : 5000);
+    if (tune.splits || m <= 128 || cost < least) least = cost, best.splits = splits;
   }
-  const int64_t pairs = clusters[0], tiles_m = (m + 255) / 256;
-  LinearConfig best{0, 256, 1};
-  int64_t least = INT64_MAX;
-  for (int splits = 1; splits <= 4; splits *= 2)
-    for (int bn = 256; bn >= 64; bn -= 32) {
-      if (tune.splits && splits != (tune.splits >= 4 ? 4 : (tune.splits >= 2 ? 2 : 1))) continue;
-      if (tune.bn && bn != tune.bn) continue;
-      if (bn % (16 * splits) != 0) continue;   // eight columns a warp at least
-      const int64_t tiles = tiles_m * ((n + bn - 1) / bn);
-      if (splits > 1 && tiles > clusters[splits / 2] && !tune.splits) continue;
-      const int64_t steps = (num_kb + splits - 1) / splits;
-      const int64_t waves = splits > 1 ? 1 : (tiles + pairs - 1) / pairs;
-      int64_t cost = waves * steps * (256 + bn) + 24 * bn / splits;
-      if (splits > 1) cost += 3000;
-      if (cost < least) least = cost, best = LinearConfig{0, bn, splits};
-    }
+  if (tune.cta_group == 1 || (m <= 128 && tune.cta_group == 0)) return best;
+  if (tune.cta_group == 2) least = INT64_MAX;
+  const int64_t pairs = num_sms / 2, tiles_m = (m + 255) / 256;
+  for (int bn = 256; bn >= 64; bn -= 32) {
+    if (tune.bn && bn != tune.bn) continue;
+    const int64_t waves = (tiles_m * ((n + bn - 1) / bn) + pairs - 1) / pairs;
+    const int64_t cost = waves * num_kb * (370 + 5 * bn / 8) + 24 * bn + 1500;
+    if (cost < least) least = cost, best = LinearConfig{0, bn, 1};
+  }
   return best;
 }
 
@@ -152,14 +153,14 @@ forge_status forge_linear_bf16(const void* X, const void* W, void* Y, forge_dtyp
   forge_tuning tune;
   forge_get_tuning(&tune);
   const int64_t num_kb = (d_in + 63) / 64;
-  int clusters[3] = {0, 0, 0};   // of one, two and four pairs
-  if (bt > 128 || tune.cta_group != 0)
-    for (int i = 0; i < 3; ++i) {
-      const cudaError_t r = linear_clusters(1 << i, d.num_sms, &clusters[i]);
-      if (r != cudaSuccess) return status(r);
-    }
+  int clusters[4];
+  const int nt = bt <= 16 ? 16 : (bt <= 32 ? 32 : (bt <= 64 ? 64 : 128));
+  for (int i = 0; i < 4; ++i) {
+    const cudaError_t r = linear_few_clusters(nt, 1 << i, d.num_sms, &clusters[i]);
+    if (r != cudaSuccess) return status(r);
+  }
   const LinearConfig cfg = choose_linear(bt, d_out, num_kb, tune, d.num_sms, clusters);
-  const int64_t tiles_m = cfg.few ? 1 : (bt + 255) / 256;
+  const int64_t rows = cfg.few ? cfg.few : 256, tiles_m = (bt + rows - 1) / rows;
   const int64_t tiles_n = (d_out + cfg.bn - 1) / cfg.bn;
   if (tiles_m * tiles_n > kMaxIndex / 8) return FORGE_ERR_SHAPE;
   const CUtensorMapDataType b16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;

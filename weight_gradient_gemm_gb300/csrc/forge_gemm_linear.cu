@@ -3,14 +3,8 @@
 // X [m, k] and W [n, k] are both K-major.  A pair of CTAs computes a tile of 256 tokens
 // x BN outputs (BN a multiple of 32 up to 256), 128 tokens each, from its own tokens and
 // half of the weight's rows each; the tile's whole reduction stays in tensor memory
-// (fp32).
-//
-// Two forms.  Many tiles: persistent pairs with two accumulators each, so that the
-// epilogue works on one tile while the next tile's products run.  Few tiles: the
-// reduction of a tile is split over the S pairs of a cluster, which send each other
-// parts of their sums through distributed shared memory (into the operand stages, done
-// with by then); each pair adds up BN / S columns in a fixed order and applies the
-// epilogue to them.  The same result on every run, no workspace.
+// (fp32).  Pairs are persistent and have two accumulators each, so that the epilogue
+// works on one tile while the next tile's products run.
 //
 // Warp roles (384 threads): warp 0 loads operand stages 64 deep with TMA, warp 1 issues
 // the MMAs, warps 4-11 are the epilogue (two per TMEM lane quadrant): a lane holds a
@@ -45,8 +39,6 @@ struct SmemL {
   static constexpr int USED = OFF_TMEM + 8;
   static constexpr int ALLOC = USED + 1024 < kSmemMaxL ? USED + 1024 : kSmemMaxL;
   static_assert(USED <= kSmemMaxL, "shared memory budget exceeded");
-  // the split form's shares: three quarters of a CTA's 128 x 256 sums at most
-  static_assert(kBM * 256 * 4 * 3 / 4 <= OFF_BARS, "shares");
 };
 
 // Tile order: groups of group_m tile rows, column by column inside a group, so that
@@ -91,14 +83,13 @@ __device__ __forceinline__ void store32(void* p, bool wide, bool second, uint4 x
 __device__ __forceinline__ void ask(const LinearArgs& a, int row, int col, int lane, Ahead& in) {
   if (row < a.m) {
     const int64_t at = static_cast<int64_t>(row) * a.n + col;
-    const bool wide = a.wide && col % 16 == 0;
 #pragma unroll
     for (int c = 0; c < 4; c += 2) {
       if (col + 8 * c >= a.n) break;
       const bool second = col + 8 * c + 8 < a.n;
       if (a.e.residual)
-        load32(a.e.residual + at + 8 * c, wide, second, in.res[c], in.res[c + 1]);
-      if (a.e.mul) load32(a.e.mul + at + 8 * c, wide, second, in.mul[c], in.mul[c + 1]);
+        load32(a.e.residual + at + 8 * c, a.wide, second, in.res[c], in.res[c + 1]);
+      if (a.e.mul) load32(a.e.mul + at + 8 * c, a.wide, second, in.mul[c], in.mul[c + 1]);
     }
   }
   if (a.e.bias && col + lane < a.n)
@@ -109,7 +100,7 @@ __device__ __forceinline__ void ask(const LinearArgs& a, int row, int col, int l
 // The epilogue of 16 columns, from the c-th eight of the 32 on, and their stores.
 template <int ACT>
 __device__ __forceinline__ void finish16(float (&v)[2][8], const LinearArgs& a, const Ahead& in,
-                                         int c, int row, int col, uint64_t offset, bool last) {
+                                         int c, int row, int col, uint64_t offset) {
   uint4 z[2];
   const uint64_t block = static_cast<uint64_t>(row) * (a.n / 8) + col / 8;
 #pragma unroll
@@ -121,7 +112,7 @@ __device__ __forceinline__ void finish16(float (&v)[2][8], const LinearArgs& a, 
     z[i] = epilogue8<ACT>(v[i], a.e, in.mul[c + i], in.res[c + i], offset, block + i);
   }
   if (row < a.m && col < a.n) {
-    const bool second = !last && col + 8 < a.n, wide = a.wide && second && col % 16 == 0;
+    const bool second = col + 8 < a.n, wide = a.wide && second;
     const int64_t at = static_cast<int64_t>(row) * a.n + col;
     if (a.e.z) store32(a.e.z + at, wide, second, z[0], z[1]);
     if (a.e.y_fp32) {
@@ -141,7 +132,7 @@ __device__ __forceinline__ void finish16(float (&v)[2][8], const LinearArgs& a, 
   __syncwarp();
 }
 
-template <bool SPLIT, int ACT>
+template <int ACT>
 __global__ void __launch_bounds__(kThreadsL, 1)
     gemm_linear_kernel(const __grid_constant__ LinearArgs a) {
   using T = SmemL;
@@ -155,16 +146,10 @@ __global__ void __launch_bounds__(kThreadsL, 1)
     return;
   }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t crank = cluster_ctarank();
-  const uint32_t rank = crank & 1u;                    // in the pair
-  const uint32_t lead = crank & ~1u;                   // the pair's leader in the cluster
-  const int share = SPLIT ? static_cast<int>(crank >> 1) : 0;
+  const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
   const int unit0 = static_cast<int>(cluster_id_x());
   const int units = static_cast<int>(cluster_count_x());
-  // this pair's steps of the reduction
-  const int kb = SPLIT ? b128_first_block(share, a.splits, a.num_kb) : 0;
-  const int ke = SPLIT ? b128_first_block(share + 1, a.splits, a.num_kb) : a.num_kb;
   const int bn = a.bn, bnl = bn / 2;
   const uint32_t tx = 2 * (T::A_BYTES + bnl * 128);   // both CTAs' bytes a stage
 
@@ -215,7 +200,9 @@ __global__ void __launch_bounds__(kThreadsL, 1)
   if (warp == 0) {
     // -------------------------------------------------------------- producer
     if (lane == 0) {
-      const uint64_t pol = l2_policy_evict_normal();
+      // Last to leave L2: other pairs read the same operands.  (8192 tokens, 4096 ->
+      // 14336, 472 us, as evict-normal 484; 4096 tokens, 4096 -> 4096, 73.4 and 78.6.)
+      const uint64_t pol = l2_policy_evict_last();
       uint32_t s = 0, ph = 0;   // next stage, and its phase
       uint32_t armed = 0;       // stages filled so far, at most STAGES
       bool ok = true;
@@ -224,10 +211,10 @@ __global__ void __launch_bounds__(kThreadsL, 1)
         tile_of(t, a, tm, tn);
         const int ya = tm * 2 * kBM + static_cast<int>(rank) * kBM;
         const int yb = tn * bn + static_cast<int>(rank) * bnl;
-        for (int k = kb; k < ke; ++k) {
+        for (int k = 0; k < a.num_kb; ++k) {
           if (!wait_bounded(bar_empty(s), ph ^ 1u, wc, kSiteProducerEmpty)) { ok = false; break; }
           const uint32_t dst = base + s * T::STAGE_BYTES;
-          const uint32_t fb = mapa_shared(bar_full(s), lead);
+          const uint32_t fb = mapa_shared(bar_full(s), 0);
           if (leader) mbar_arrive_expect_tx(bar_full(s), tx);
           tma_load_2d_pair(dst, &a.a, k * 64, ya, fb, pol);
           tma_load_2d_pair(dst + T::A_BYTES, &a.b, k * 64, yb, fb, pol);
@@ -254,7 +241,6 @@ __global__ void __launch_bounds__(kThreadsL, 1)
       const uint32_t idesc = make_idesc_bf16(2 * kBM, bn, false, false);
       const uint64_t ad0 = make_sdesc_k_sw128(base, 1024);
       const uint64_t bd0 = make_sdesc_k_sw128(base + T::A_BYTES, 1024);
-      const uint16_t both = static_cast<uint16_t>(3u << lead);
       const bool issue = elect_one();
       uint32_t s = 0, ph = 0, buf = 0, bph = 1;
       bool ok = true;
@@ -264,7 +250,7 @@ __global__ void __launch_bounds__(kThreadsL, 1)
         tc_fence_after_sync();
         const uint32_t d = tmem_base + buf * 256;
 #pragma unroll 1
-        for (int k = kb; k < ke; ++k) {
+        for (int k = 0; k < a.num_kb; ++k) {
           ok = __all_sync(0xffffffffu, wait_bounded(bar_full(s), ph, wc, kSiteMmaFull));
           if (!ok) break;
           tc_fence_after_sync();
@@ -273,21 +259,21 @@ __global__ void __launch_bounds__(kThreadsL, 1)
           if (issue) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)   // 16 of K: 32 bytes
-              umma_bf16_pair(d, ad + 2 * kk, bd + 2 * kk, idesc, ((k - kb) | kk) != 0);
-            umma_commit_pair_mc(bar_empty(s), both);
+              umma_bf16_pair(d, ad + 2 * kk, bd + 2 * kk, idesc, (k | kk) != 0);
+            umma_commit_pair_mc(bar_empty(s), 0x3);
           }
           if (++s == T::STAGES) { s = 0; ph ^= 1u; }
         }
         if (!ok) break;
-        if (issue) umma_commit_pair_mc(bar_tfull(buf), both);
+        if (issue) umma_commit_pair_mc(bar_tfull(buf), 0x3);
         if (++buf == 2) { buf = 0; bph ^= 1u; }
       }
       // every MMA issued must complete before the tensor memory is freed
-      if (issue) umma_commit_pair_mc(bar_drain, static_cast<uint16_t>(1u << lead));
+      if (issue) umma_commit_pair_mc(bar_drain, 0x1);
       wait_bounded(bar_drain, 0u, wc, kSiteDrainMma, false);
     }
     __syncwarp();
-  } else if (!SPLIT && warp >= 4) {
+  } else if (warp >= 4) {
     // -------------------------------------------------------------- epilogue
     // the warp's boxes of 32 columns in a tile
     const int boxes = (bn / 32 + 1 - h) / 2, box0 = h * ((bn / 32 + 1) / 2);
@@ -332,7 +318,7 @@ __global__ void __launch_bounds__(kThreadsL, 1)
         if (b == boxes - 1) {   // this warp has read its part of the accumulator
           tc_fence_before_sync();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(bar_tempty(buf), lead));
+          if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(bar_tempty(buf), 0));
         }
         if (!there) continue;
 #pragma unroll
@@ -340,84 +326,13 @@ __global__ void __launch_bounds__(kThreadsL, 1)
           float v[2][8];
 #pragma unroll
           for (int k = 0; k < 16; ++k) v[k / 8][k % 8] = __uint_as_float(r[8 * c + k]);
-          finish16<ACT>(v, a, now, c, row0 + lane, col + 8 * c, offset, false);
+          finish16<ACT>(v, a, now, c, row0 + lane, col + 8 * c, offset);
         }
       }
       if (!ok) break;
       if (++buf == 2) { buf = 0; bph ^= 1u; }
     }
     __syncwarp();
-  }
-
-  if constexpr (SPLIT) {
-    // -------------------------------------------------------------- join and store
-    // Columns of the tile: share z's are those from z bn / S on, half a warp's each.  A
-    // share's sums lie in shared memory as [four columns][row], 16 bytes a row.
-    const int width = bn / a.splits, half = width / 2;
-    int tm, tn;
-    tile_of(unit0, a, tm, tn);
-    const int row = tm * 2 * kBM + static_cast<int>(rank) * kBM + q * 32 + lane;
-    const int col0 = tn * bn + share * width + h * half;
-    // this pair's sums of eight columns (none: it had no steps)
-    auto sums8 = [&](int c, float (&v)[8]) {
-      tmem_ld_x8(tmem_base + lane_addr + c, reinterpret_cast<uint32_t(&)[8]>(v));
-      tmem_ld_wait();
-      if (ke <= kb) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = 0.0f;
-      }
-    };
-    bool ok = true;
-    if (warp >= 4) {
-      ask(a, row, col0, lane, in);
-      ok = __all_sync(0xffffffffu, wait_bounded(bar_tfull(0), 0u, wc, kSiteEpiTmemFull));
-      tc_fence_after_sync();
-    }
-    tc_fence_before_sync();
-    cluster_sync_all();   // every CTA's products have run: its stages are free
-    tc_fence_after_sync();
-    if (warp >= 4) {
-      const uint32_t me = base + static_cast<uint32_t>(q * 32 + lane) * 16;
-      for (int d = 1; d < a.splits; ++d) {
-        const int z = (share + d) % a.splits;
-        // among the shares that z receives this one is the (share - z - 1)-th modulo S
-        const int slot = (share - z - 1 + a.splits) % a.splits;
-        const uint32_t dst = mapa_shared(me + (slot * width + h * half) / 4 * (kBM * 16),
-                                         2 * z + rank);
-        for (int c = 0; c < half; c += 8) {
-          float v[8];
-          sums8(z * width + h * half + c, v);
-          st_cluster_f32x4(dst + c / 4 * (kBM * 16), v[0], v[1], v[2], v[3]);
-          st_cluster_f32x4(dst + (c / 4 + 1) * (kBM * 16), v[4], v[5], v[6], v[7]);
-        }
-      }
-    }
-    cluster_sync_all();
-    if (warp >= 4 && ok && !*abort_flag) {
-      const float* part = reinterpret_cast<const float*>(gbase) + (q * 32 + lane) * 4;
-      for (int c0 = 0; c0 < half; c0 += 32) {
-        if (c0 > 0) ask(a, row, col0 + c0, lane, in);
-#pragma unroll
-        for (int c = 0; c < 4; c += 2) {
-          const int cc = c0 + 8 * c;
-          if (cc >= half) break;
-          float v[2][8];
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            if (i == 1 && cc + 8 >= half) break;   // the half's last eight columns
-            sums8(share * width + h * half + cc + 8 * i, v[i]);
-            for (int slot = 0; slot + 1 < a.splits; ++slot) {
-              const float* p = part + (slot * width + h * half + cc + 8 * i) / 4 * (kBM * 4);
-              const float4 x = *reinterpret_cast<const float4*>(p);
-              const float4 y = *reinterpret_cast<const float4*>(p + kBM * 4);
-              v[i][0] += x.x; v[i][1] += x.y; v[i][2] += x.z; v[i][3] += x.w;
-              v[i][4] += y.x; v[i][5] += y.y; v[i][6] += y.z; v[i][7] += y.w;
-            }
-          }
-          finish16<ACT>(v, a, in, c, row, col0 + cc, offset, cc + 8 >= half);
-        }
-      }
-    }
   }
 
   // ---------------------------------------------------------------- teardown
@@ -435,29 +350,28 @@ __global__ void __launch_bounds__(kThreadsL, 1)
   }
 }
 
-// The clusters of 2 S CTAs that can be resident at once.
-template <bool SPLIT, int ACT>
-cudaError_t resident(int splits, int num_sms, int* n) {
-  static PerDevice kept[3];
-  return kept[splits == 1 ? 0 : (splits == 2 ? 1 : 2)].get(n, [&](int* v) {
-    cudaError_t r = cudaFuncSetAttribute(gemm_linear_kernel<SPLIT, ACT>,
+// The pairs that can be resident at once.
+template <int ACT>
+cudaError_t resident(int num_sms, int* n) {
+  static PerDevice kept;
+  return kept.get(n, [&](int* v) {
+    cudaError_t r = cudaFuncSetAttribute(gemm_linear_kernel<ACT>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, SmemL::ALLOC);
     if (r != cudaSuccess) return r;
-    const unsigned size = 2u * splits;
     cudaLaunchConfig_t lc = {};
-    lc.gridDim = dim3(num_sms / size * size, 1, 1);
+    lc.gridDim = dim3(2 * (num_sms / 2), 1, 1);
     lc.blockDim = dim3(kThreadsL, 1, 1);
     lc.dynamicSmemBytes = SmemL::ALLOC;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = size;
+    attr[0].val.clusterDim.x = 2;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     lc.attrs = attr;
     lc.numAttrs = 1;
-    r = cudaOccupancyMaxActiveClusters(v, gemm_linear_kernel<SPLIT, ACT>, &lc);
+    r = cudaOccupancyMaxActiveClusters(v, gemm_linear_kernel<ACT>, &lc);
     if (r == cudaSuccess && *v <= 0) r = cudaErrorInvalidConfiguration;
-    *v = *v < num_sms / static_cast<int>(size) ? *v : num_sms / static_cast<int>(size);
+    *v = *v < num_sms / 2 ? *v : num_sms / 2;
     return r;
   });
 }
@@ -465,25 +379,13 @@ cudaError_t resident(int splits, int num_sms, int* n) {
 template <int ACT>
 cudaError_t launch_act(const LinearArgs& a, int num_sms, cudaStream_t stream) {
   int units = 0;
-  if (a.splits > 1) {
-    const cudaError_t e = resident<true, ACT>(a.splits, num_sms, &units);
-    if (e != cudaSuccess) return e;
-    return launch_chained(gemm_linear_kernel<true, ACT>, 2 * a.splits * a.num_tiles, kThreadsL,
-                          SmemL::ALLOC, 2 * a.splits, stream, a);
-  }
-  const cudaError_t e = resident<false, ACT>(1, num_sms, &units);
+  const cudaError_t e = resident<ACT>(num_sms, &units);
   if (e != cudaSuccess) return e;
-  return launch_chained(gemm_linear_kernel<false, ACT>,
-                        2 * (a.num_tiles < units ? a.num_tiles : units), kThreadsL, SmemL::ALLOC, 2,
-                        stream, a);
+  return launch_chained(gemm_linear_kernel<ACT>, 2 * (a.num_tiles < units ? a.num_tiles : units),
+                        kThreadsL, SmemL::ALLOC, 2, stream, a);
 }
 
 }  // namespace
-
-cudaError_t linear_clusters(int splits, int num_sms, int* n) {
-  return splits == 1 ? resident<false, kActNone>(1, num_sms, n)
-                     : resident<true, kActNone>(splits, num_sms, n);
-}
 
 cudaError_t launch_gemm_linear(const LinearArgs& a, int num_sms, cudaStream_t stream) {
   switch (a.e.act) {

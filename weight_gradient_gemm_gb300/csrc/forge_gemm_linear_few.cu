@@ -2,8 +2,8 @@
 // tokens, where reading the weight is all the time there is.
 //
 // As in the 8-bit form (forge_gemm_b128_few.cu) the operands change places: 128
-// outputs lie along the MMA's M and the tokens along its N, 16 to 128 of them, and the
-// reduction is split over the CTAs of a cluster (up to 8), which send slices of their
+// outputs lie along the MMA's M and the tokens along its N, 16 to 128 of them (more
+// tokens: several tiles of 128), and the reduction is split over the CTAs of a cluster (up to 8), which send slices of their
 // fp32 sums to the CTAs that own them through distributed shared memory; the owners
 // add them in a fixed order, apply the epilogue and store.  One launch, no workspace,
 // the same result on every run.
@@ -59,7 +59,9 @@ __global__ void __launch_bounds__(FewL<NT>::THREADS, NT <= 64 ? 2 : 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int splits = a.splits;
   const int rank = splits > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-  const int tile = static_cast<int>(blockIdx.x) / splits;
+  const int unit = static_cast<int>(blockIdx.x) / splits;
+  const int tile = unit / a.tiles_m, t0 = (unit - tile * a.tiles_m) * NT;   // outputs, first token
+  const int m = min(a.m - t0, NT);
   // this CTA's steps of the reduction
   const int kb = b128_first_block(rank, splits, a.num_kb);
   const int ke = b128_first_block(rank + 1, splits, a.num_kb);
@@ -71,7 +73,10 @@ __global__ void __launch_bounds__(FewL<NT>::THREADS, NT <= 64 ? 2 : 1)
   const uint32_t bar_done = bars + 8u * (2 * T::DEEP);   // all products have run
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(gbase + T::OFF_TMEM + 4);
   const WaitCtx wc{abort_flag, a.err, a.err_site, a.timeout_ns};
-  const uint64_t wpol = l2_policy_evict_normal(), xpol = l2_policy_evict_last();
+  // A weight that is read once passes through L2 as the first to leave it (one token,
+  // 4096 -> 14336, 19.9 us; as evict-normal 22.7).
+  const uint64_t wpol = a.tiles_m > 1 ? l2_policy_evict_last() : l2_policy_evict_first();
+  const uint64_t xpol = l2_policy_evict_last();
 
   // Warp 0 sets up the barriers while warp 1 takes the tensor memory; one block
   // barrier covers both.
@@ -89,11 +94,10 @@ __global__ void __launch_bounds__(FewL<NT>::THREADS, NT <= 64 ? 2 : 1)
   __syncthreads();
   tc_fence_after_sync();
   // While the kernel before still runs, the weight's first steps are asked for as far
-  // as L2, where all writes meet (see forge_gemm_b128_few.cu).
+  // as L2, where all writes meet (see forge_gemm_b128_few.cu): calls back to back on one
+  // token, 4096 -> 14336, 19.2 us with 16 steps ahead, 20.7 with eight, 21.6 with none.
   if (warp == 0 && lane == 0) {
-    const int ahead = NT <= 16 ? max(8, (ke - kb) / 2) : 8;
-    for (int k = kb; k < min(ke, kb + ahead); ++k)
-      tma_prefetch_l2_2d(&a.b, k * 64, tile * 128);
+    for (int k = kb; k < min(ke, kb + 16); ++k) tma_prefetch_l2_2d(&a.b, k * 64, tile * 128);
   }
   grid_dependency_wait();
   const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(gbase + T::OFF_TMEM);
@@ -101,13 +105,13 @@ __global__ void __launch_bounds__(FewL<NT>::THREADS, NT <= 64 ? 2 : 1)
   // The outputs that this CTA owns, eight neighbouring ones at a time: token e >> shift.
   // The first ones' inputs are asked for now, under the reduction.
   const int slice = kBM / splits;   // splits divides 128
-  const int shift = 31 - __clz(slice >> 3), total = a.m << shift;
+  const int shift = 31 - __clz(slice >> 3), total = m << shift;
   const int64_t nv = a.n / 8;
   auto place = [&](int e, int& t, int& j, int64_t& at) {
     t = e >> shift;
     j = (e - (t << shift)) * 8;
     const int o = tile * 128 + rank * slice + j;
-    at = static_cast<int64_t>(t) * nv + o / 8;
+    at = static_cast<int64_t>(t0 + t) * nv + o / 8;
     return e < total && o < a.n;
   };
   uint4 mul0 = make_uint4(0, 0, 0, 0), res0 = mul0;
@@ -130,7 +134,7 @@ __global__ void __launch_bounds__(FewL<NT>::THREADS, NT <= 64 ? 2 : 1)
         const uint32_t dst = stage0 + s * T::STAGE_BYTES;
         mbar_arrive_expect_tx(bar_full(s), T::STAGE_BYTES);
         tma_load_2d(dst, &a.b, k * 64, tile * 128, bar_full(s), wpol);
-        tma_load_2d(dst + T::A_BYTES, &a.a, k * 64, 0, bar_full(s), xpol);
+        tma_load_2d(dst + T::A_BYTES, &a.a, k * 64, t0, bar_full(s), xpol);
         if (armed < stages) ++armed;
         if (++s == stages) { s = 0; ph ^= 1u; }
       }
@@ -197,7 +201,7 @@ __global__ void __launch_bounds__(FewL<NT>::THREADS, NT <= 64 ? 2 : 1)
     float* here = reinterpret_cast<float*>(gbase + (to - base));
 #pragma unroll
     for (int i = 0; i < T::NC; ++i)
-      if (h * T::NC + i < a.m) {
+      if (h * T::NC + i < m) {
         if (splits > 1) st_cluster_f32(dst + 4u * i * slice, acc[i]);
         else here[i * slice] = acc[i];
       }
@@ -249,19 +253,60 @@ __global__ void __launch_bounds__(FewL<NT>::THREADS, NT <= 64 ? 2 : 1)
   }
 }
 
+// The clusters of `splits` CTAs that can be resident at once with as many stages as fit.
+template <int NT>
+cudaError_t resident(int splits, int num_sms, int* n) {
+  using T = FewL<NT>;
+  static PerDevice kept[4];
+  auto kern = gemm_linear_few_kernel<NT>;
+  return kept[splits == 1 ? 0 : (splits == 2 ? 1 : (splits == 4 ? 2 : 3))].get(n, [&](int* v) {
+    cudaError_t r =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
+    *v = num_sms;
+    if (splits == 1 || r != cudaSuccess) return r;
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3(num_sms / splits * splits, 1, 1);
+    lc.blockDim = dim3(T::THREADS, 1, 1);
+    lc.dynamicSmemBytes = T::smem(T::DEEP);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = splits;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    r = cudaOccupancyMaxActiveClusters(v, kern, &lc);
+    if (r == cudaSuccess && *v <= 0) r = cudaErrorInvalidConfiguration;
+    return r;
+  });
+}
+
 template <int NT>
 cudaError_t launch_t(LinearArgs a, int num_sms, cudaStream_t stream) {
   using T = FewL<NT>;
-  auto kern = gemm_linear_few_kernel<NT>;
-  static PerDevice once;
-  const cudaError_t e = allow_smem(once, kern, 232448);
+  int clusters = 0;
+  const cudaError_t e = resident<NT>(a.splits, num_sms, &clusters);
   if (e != cudaSuccess) return e;
-  a.stages = a.num_tiles * a.splits <= num_sms ? T::DEEP : T::STAGES;
-  return launch_chained(kern, a.num_tiles * a.splits, T::THREADS, T::smem(a.stages),
-                        a.splits > 1 ? a.splits : 0, stream, a);
+  const int steps = (a.num_kb + a.splits - 1) / a.splits;
+  a.stages = a.num_tiles <= clusters ? T::DEEP : T::STAGES;
+  if (steps < a.stages) a.stages = steps < 2 ? 2 : steps;
+  // (the shares take the stages' place)
+  while (a.stages * T::STAGE_BYTES < NT * kBM * 4) ++a.stages;
+  return launch_chained(gemm_linear_few_kernel<NT>, a.num_tiles * a.splits, T::THREADS,
+                        T::smem(a.stages), a.splits > 1 ? a.splits : 0, stream, a);
 }
 
 }  // namespace
+
+cudaError_t linear_few_clusters(int nt, int splits, int num_sms, int* n) {
+  switch (nt) {
+    case 16: return resident<16>(splits, num_sms, n);
+    case 32: return resident<32>(splits, num_sms, n);
+    case 64: return resident<64>(splits, num_sms, n);
+    case 128: return resident<128>(splits, num_sms, n);
+  }
+  return cudaErrorInvalidValue;
+}
 
 cudaError_t launch_gemm_linear_few(int nt, const LinearArgs& a, int num_sms, cudaStream_t stream) {
   switch (nt) {

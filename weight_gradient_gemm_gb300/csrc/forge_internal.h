@@ -338,8 +338,8 @@ struct LinearArgs {
   int32_t m, n, num_kb;     // tokens, outputs, 64-deep steps of the reduction
   int32_t tiles_m, tiles_n, num_tiles, group_m;
   int32_t bn;               // outputs of a pair's tile: a multiple of 32, at most 256
-  int32_t splits;           // pairs (few tokens: CTAs) of a cluster that share a tile's reduction
-  int32_t stages;           // few tokens: operand stages
+  int32_t splits;           // single CTAs: those of a cluster, which share a tile's reduction
+  int32_t stages;           // single CTAs: operand stages
   int32_t wide;             // every row of the epilogue's matrices starts on 32 bytes
   int32_t drop_first_arrival;       // testing aid
   int* err;
@@ -347,13 +347,13 @@ struct LinearArgs {
   uint64_t timeout_ns;
 };
 struct LinearConfig {
-  int few;      // 0, or the tokens a tile holds when the outputs lie along M
-  int bn;       // a pair's outputs (few tokens: 128)
-  int splits;   // pairs, or with few tokens CTAs, per tile
+  int few;      // 0: pairs; or the tokens of a single CTA's tile, whose outputs lie along M
+  int bn;       // outputs of a tile
+  int splits;   // single CTAs per tile
 };
-// The clusters of `splits` pairs that can be resident at once.
-cudaError_t linear_clusters(int splits, int num_sms, int* n);
 cudaError_t launch_gemm_linear(const LinearArgs& a, int num_sms, cudaStream_t stream);
+// The clusters of `splits` CTAs, tiles of nt tokens, that can be resident at once.
+cudaError_t linear_few_clusters(int nt, int splits, int num_sms, int* n);
 cudaError_t launch_gemm_linear_few(int nt, const LinearArgs& a, int num_sms, cudaStream_t stream);
 
 // The epilogue's gradient and dropout (forge_epilogue.cu).

@@ -103,33 +103,35 @@ __global__ void __launch_bounds__(256) epilogue_bwd_kernel(const EpiBwdArgs a) {
   }
 }
 
-// With dbias: a block takes 128 columns and a run of rows, 16 lanes to a row; a thread
-// adds its eight columns over its rows, and the block's 16 rows of sums are joined in
-// shared memory.  Up to eight runs of rows are the blocks of a cluster, whose first adds
-// up the others' sums through distributed shared memory: one launch.  More leave a partial
-// row each for a second one.
-constexpr int kBiasCols = 128, kBiasCluster = 8;
+// With dbias: a block takes a strip of 8 L columns and a run of rows, L lanes to a row; a
+// thread adds its eight columns over its rows, and the block's sums are joined in shared
+// memory.  Up to eight runs of rows are the blocks of a cluster, whose first adds up the
+// others' sums through distributed shared memory: one launch.  More leave a partial row
+// each for a second one.
+constexpr int kBiasCluster = 8;
 template <int ACT, bool MUL>
-__global__ void __launch_bounds__(256) epilogue_bwd_bias_kernel(const EpiBwdArgs a, int parts, int cluster) {
+__global__ void __launch_bounds__(256) epilogue_bwd_bias_kernel(const EpiBwdArgs a, int lanes,
+                                                                int parts, int cluster) {
   constexpr int U = MUL ? 2 : 4;   // rows whose loads are in flight at once
-  __shared__ float4 sums[16][kBiasCols / 4];
-  __shared__ float joined[kBiasCols];
+  __shared__ float4 sums[512];     // [row of the block][column / 4]
+  __shared__ float some[256], joined[128];
   const int64_t nv = a.cols / 8;
   const int strip = static_cast<int>(blockIdx.x) / parts, part = blockIdx.x - strip * parts;
-  const int64_t v = static_cast<int64_t>(strip) * 16 + (threadIdx.x & 15);
+  const int lane = threadIdx.x & (lanes - 1), cols = 8 * lanes, rows = 256 / lanes;
+  const int64_t v = static_cast<int64_t>(strip) * lanes + lane;
   const int64_t each = (a.rows + parts - 1) / parts;
   const int64_t r0 = each * part, r1 = min(a.rows, r0 + each);
   float sum[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
   grid_dependency_wait();
   const uint64_t offset = drop_offset(a.drop);
   if (v < nv) {
-    for (int64_t row = r0 + (threadIdx.x >> 4); row < r1; row += 16 * U) {
+    for (int64_t row = r0 + threadIdx.x / lanes; row < r1; row += rows * U) {
       uint4 dy[U], z[U], m[U];
 #pragma unroll
       for (int i = 0; i < U; ++i) {
-        const int64_t at = (row + 16 * i) * nv + v;
+        const int64_t at = (row + rows * i) * nv + v;
         dy[i] = z[i] = m[i] = make_uint4(0, 0, 0, 0);
-        if (row + 16 * i < r1) {
+        if (row + rows * i < r1) {
           dy[i] = __ldcs(reinterpret_cast<const uint4*>(a.dy) + at);
           if (ACT != kActNone || (MUL && a.dmul))
             z[i] = __ldcs(reinterpret_cast<const uint4*>(a.z) + at);
@@ -138,47 +140,66 @@ __global__ void __launch_bounds__(256) epilogue_bwd_bias_kernel(const EpiBwdArgs
       }
 #pragma unroll
       for (int i = 0; i < U; ++i)
-        if (row + 16 * i < r1) {
+        if (row + rows * i < r1) {
           float dz[8];
-          bwd8<ACT, MUL>(a, dy[i], z[i], m[i], offset, (row + 16 * i) * nv + v, dz);
+          bwd8<ACT, MUL>(a, dy[i], z[i], m[i], offset, (row + rows * i) * nv + v, dz);
 #pragma unroll
           for (int k = 0; k < 8; ++k) sum[k] += dz[k];
         }
     }
   }
   grid_dependency_trigger();
-  sums[threadIdx.x >> 4][2 * (threadIdx.x & 15)] = make_float4(sum[0], sum[1], sum[2], sum[3]);
-  sums[threadIdx.x >> 4][2 * (threadIdx.x & 15) + 1] = make_float4(sum[4], sum[5], sum[6], sum[7]);
+  sums[2 * threadIdx.x] = make_float4(sum[0], sum[1], sum[2], sum[3]);
+  sums[2 * threadIdx.x + 1] = make_float4(sum[4], sum[5], sum[6], sum[7]);
   __syncthreads();
-  const int64_t col = static_cast<int64_t>(strip) * kBiasCols + threadIdx.x;
+  // a column's sums: `runs` threads each add some, the first adds theirs
+  const int col = threadIdx.x & (cols - 1), runs = 256 / cols;
   float s = 0.0f;
-  if (threadIdx.x < kBiasCols) {
-#pragma unroll
-    for (int r = 0; r < 16; ++r) s += reinterpret_cast<const float*>(sums[r])[threadIdx.x];
-  }
+  for (int r = threadIdx.x / cols; r < rows; r += runs)
+    s += reinterpret_cast<const float*>(sums)[r * cols + col];
+  some[threadIdx.x] = s;
+  __syncthreads();
+  const bool mine = static_cast<int>(threadIdx.x) < cols;
+  if (mine)
+    for (int r = 1; r < runs; ++r) s += some[r * cols + col];
   if (cluster) {   // its rank is `part`
-    if (threadIdx.x < kBiasCols) joined[threadIdx.x] = s;
+    if (mine) joined[col] = s;
     cluster_sync_all();
-    if (part == 0 && threadIdx.x < kBiasCols) {
-      const uint32_t at = smem_u32(joined + threadIdx.x);
+    if (part == 0 && mine) {
+      const uint32_t at = smem_u32(joined + col);
       for (int r = 1; r < parts; ++r) s += ld_cluster_f32(mapa_shared(at, r));
     }
     cluster_sync_all();   // no block leaves before its sums are read
   }
-  if (threadIdx.x < kBiasCols && col < a.cols) {
-    if (!cluster && parts > 1) a.part[part * a.cols + col] = s;
-    else if (part == 0) a.dbias[col] = s;
+  const int64_t c = static_cast<int64_t>(strip) * cols + col;
+  if (mine && c < a.cols) {
+    if (!cluster && parts > 1) a.part[part * a.cols + c] = s;
+    else if (part == 0) a.dbias[c] = s;
   }
 }
 
-// Runs of rows: about six blocks an SM, each with 32 rows at least; where that makes few
-// more than a cluster holds, as many as it holds.
-int bias_parts(int64_t rows, int64_t cols, int num_sms) {
-  const int64_t strips = (cols + kBiasCols - 1) / kBiasCols, blocks = 6LL * num_sms;
-  const int64_t most = (rows + 31) / 32, want = (blocks + strips - 1) / strips;
-  const int64_t n = want < most ? want : most;
-  if (n > kBiasCluster && n <= 2 * kBiasCluster) return kBiasCluster;
-  return static_cast<int>(n < 1 ? 1 : n);
+// Strips of 128 columns and about six blocks an SM in all, with 32 rows at least; where
+// that makes few more runs of rows than a cluster holds, as many as it holds.  Where it
+// leaves SMs without a block, narrower strips (333 x 520: 4.3 us with strips of 128 and 40
+// blocks).
+struct BiasPlan {
+  int lanes, parts;
+};
+BiasPlan bias_plan(int64_t rows, int64_t cols, int num_sms) {
+  BiasPlan p{16, 1};
+  auto strips = [&] { return (cols + 8 * p.lanes - 1) / (8 * p.lanes); };
+  auto parts = [&] {
+    const int64_t most = (rows * p.lanes + 511) / 512, blocks = 6LL * num_sms;
+    const int64_t want = (blocks + strips() - 1) / strips(), n = want < most ? want : most;
+    if (n > kBiasCluster && n <= 2 * kBiasCluster) return kBiasCluster;
+    return static_cast<int>(n < 1 ? 1 : n);
+  };
+  p.parts = parts();
+  while (p.lanes > 4 && p.parts <= kBiasCluster && strips() * p.parts < num_sms) {
+    p.lanes /= 2;
+    p.parts = parts();
+  }
+  return p;
 }
 
 template <int ACT, bool MUL>
@@ -188,14 +209,14 @@ cudaError_t launch_t(const EpiBwdArgs& a, int num_sms, cudaStream_t stream) {
     return launch_chained(epilogue_bwd_kernel<ACT, MUL>, static_cast<unsigned>(blocks), 256, 0, 0,
                           stream, a);
   }
-  const int parts = bias_parts(a.rows, a.cols, num_sms);
-  const int64_t strips = (a.cols + kBiasCols - 1) / kBiasCols;
-  const bool cluster = parts > 1 && parts <= kBiasCluster;
-  const cudaError_t e =
-      launch_chained(epilogue_bwd_bias_kernel<ACT, MUL>, static_cast<unsigned>(strips * parts), 256,
-                     0, cluster ? parts : 0, stream, a, parts, static_cast<int>(cluster));
-  if (e != cudaSuccess || parts == 1 || cluster) return e;
-  return launch_join_rows(a.part, parts, static_cast<int>(a.cols), a.dbias, stream);
+  const BiasPlan p = bias_plan(a.rows, a.cols, num_sms);
+  const int64_t strips = (a.cols + 8 * p.lanes - 1) / (8 * p.lanes);
+  const bool cluster = p.parts > 1 && p.parts <= kBiasCluster;
+  const cudaError_t e = launch_chained(
+      epilogue_bwd_bias_kernel<ACT, MUL>, static_cast<unsigned>(strips * p.parts), 256, 0,
+      cluster ? p.parts : 0, stream, a, p.lanes, p.parts, static_cast<int>(cluster));
+  if (e != cudaSuccess || p.parts == 1 || cluster) return e;
+  return launch_join_rows(a.part, p.parts, static_cast<int>(a.cols), a.dbias, stream);
 }
 
 template <bool MUL>
@@ -212,7 +233,7 @@ cudaError_t launch_act(const EpiBwdArgs& a, int num_sms, cudaStream_t stream) {
 }  // namespace
 
 int epilogue_bwd_rows(int64_t rows, int64_t cols, int num_sms) {
-  const int parts = bias_parts(rows, cols, num_sms);
+  const int parts = bias_plan(rows, cols, num_sms).parts;
   return parts > kBiasCluster ? parts : 0;
 }
 

@@ -686,7 +686,8 @@ forge_status forge_linear_bf16(const void* X, const void* W, void* Y, forge_dtyp
 
 /*
  * forge_epilogue_backward: the gradients of that epilogue, in fp32 from the stored Z:
- *   dA = drop(dY),  dmul = dA * act(Z),  dZ = dA * mul * act'(Z),  dbias = sum over rows of dZ.
+ *   dA = drop(dY),  dmul = dA * act(Z),  dZ = dA * mul * act'(Z),  dbias = sum over rows of dZ
+ * (where an element was dropped: zeros, whatever Z and mul hold there).
  *   dY [rows, cols] bf16; Z [rows, cols] bf16 (may be NULL where act is FORGE_ACT_NONE and
  *   dmul is not asked for); mul [rows, cols] bf16 or NULL (1); drop as in the forward call
  *   (NULL: none).  Outputs, at least one, each written if not NULL: dZ, dmul [rows, cols]
@@ -844,8 +845,9 @@ int forge_debug_timeout_site(void);
 void forge_set_wait_limit_ns(uint64_t ns);
 
 /* Testing aid for the timeout path: when enabled, the next fused or forge_wgrad
- * launch, or the next norm, quantiser or 8-bit product (where its kernel waits on
- * copies: norms of many rows, quantisers of 128 x 128 blocks, the products), skips
+ * launch, or the next norm, quantiser, 8-bit product or forge_linear_bf16 (where its
+ * kernel waits on copies: norms of many rows, quantisers of 128 x 128 blocks, the
+ * products), skips
  * its first operand-load arrival, so its waits run out, the kernel records
  * FORGE_ERR_DEVICE_TIMEOUT and returns with its outputs unspecified.  The flag
  * clears itself after that one launch. */
@@ -867,13 +869,17 @@ typedef enum {
 typedef struct {
   int profile;     /* a forge_profile                                          */
   int cta_group;   /* 0 automatic; 1 one CTA per tile; 2 a CTA pair (256 x 256);
-                      for the 8-bit products both also set the tile for few tokens */
-  int bn;          /* 0 automatic; 128 or 256: accumulator width on one CTA     */
+                      for the 8-bit products both also set the tile for few tokens;
+                      for forge_linear_bf16 1: 128 outputs and up to 128 tokens on
+                      one CTA, 2: pairs with 256 tokens                          */
+  int bn;          /* 0 automatic; 128 or 256: accumulator width on one CTA
+                      (forge_linear_bf16: outputs of a pair's tile)              */
   int group_m;     /* 0 automatic; 1..64 tile rows per raster group             */
   int poll_store;  /* -1 automatic; 0 or 1: store lanes poll for finished slots */
   int splits;      /* 0 automatic; 1..8 k-ranges per tile for forge_dgrad; for
-                      the 8-bit products of up to 128 tokens the CTAs that share
-                      a tile (rounded down to 1, 2, 4 or 8)                     */
+                      the 8-bit products of up to 128 tokens and forge_linear_bf16
+                      on single CTAs the CTAs that share a tile (rounded down to
+                      1, 2, 4 or 8)                                             */
   int l2_hints;    /* -1 automatic; 0..3: bit 0 marks the optimizer state's
                       stores evict-first in L2, bit 1 its m, v loads whose rows
                       are whole 128-byte lines                                  */

@@ -226,6 +226,57 @@ def test_linear_special_values(bt):
             assert Y[r, 5] == (np.inf if x[r] > 0 else 0.0)
 
 
+@pytest.mark.parametrize("bt,d_out", [(3, 256), (300, 256), (300, 264), (1100, 1040)])
+@pytest.mark.parametrize("name", ["all", "all_fp32"])
+def test_linear_at_16_byte_alignment(bt, d_out, name):
+    """Matrices that start 16 bytes behind a 32-byte boundary, rows of 32 bytes or not."""
+    c = linear_case(bt, 136, d_out, **EPILOGUES[name])
+    call_linear(c)
+    want = [c["Y"].clone(), c["Z"].clone()]
+
+    def shifted(t):
+        n = 16 // t.element_size()
+        buf = torch.empty(t.numel() + 2 * n, dtype=t.dtype, device=DEV)
+        out = buf[n:n + t.numel()].view(t.shape)
+        assert out.data_ptr() % 32 == 16
+        out.copy_(t)
+        return out
+
+    for k in ("X", "W", "bias", "mul", "residual", "Z", "Y"):
+        d = dict(c, Z=torch.zeros_like(c["Z"]), Y=torch.zeros_like(c["Y"]))
+        for name_ in (k,) if k != "Y" else ("X", "W", "bias", "mul", "residual", "Z", "Y"):
+            d[name_] = shifted(d[name_])
+        call_linear(d)
+        assert torch.equal(d["Y"], want[0]) and torch.equal(d["Z"], want[1]), k
+
+
+def test_more_than_2_to_the_31_elements():
+    """Outputs and dropout blocks whose indexes pass 32 bits: the last rows."""
+    bt, d_in, d_out, last = 140000, 8, 16384, 3
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs 24 GB")
+    X, W = rand(1, (bt, d_in)), rand(2, (d_out, d_in))
+    Y = torch.empty((bt, d_out), dtype=torch.bfloat16, device=DEV)
+    F.linear_bf16(X, W, Y, p=0.5, seed=SEED, offset=OFFSET)
+    ok()
+    blocks = np.arange((bt - last) * d_out // 8, bt * d_out // 8)
+    pick = [0, 1, len(blocks) // 2, len(blocks) - 1]
+    want = np.array([[(w >> s) & 0xFFFF for w in R.philox4x32_10(
+        (int(blocks[i]) & 0xFFFFFFFF, int(blocks[i]) >> 32, OFFSET, 0),
+        (SEED & 0xFFFFFFFF, SEED >> 32)) for s in (0, 16)] for i in pick]) >= 32768
+    Z, _ = R.linear(f64(X[-last:]), f64(W))
+    kept = f64(Y[-last:]).reshape(-1, 8)
+    assert np.array_equal(kept[pick] != 0, want)
+    ref = np.where(kept != 0, 2 * Z.reshape(-1, 8), 0.0)
+    within(kept, ref, BF * np.abs(ref) + 1e-5)
+    y2 = torch.empty_like(Y)
+    F.dropout(Y, y2, p=0.5, seed=SEED, offset=OFFSET)
+    F.epilogue_backward(Y, Y, p=0.5, seed=SEED, offset=OFFSET)      # in place, the same mask
+    ok()
+    within(f64(y2[-last:]), 2 * kept.reshape(last, -1), BF * np.abs(2 * kept.reshape(last, -1)))
+    assert torch.equal(Y, y2)
+
+
 def test_linear_no_tokens():
     none = torch.empty((0, 64), dtype=torch.bfloat16, device=DEV)
     F.linear_bf16(none, rand(2, (24, 64)), torch.empty((0, 24), dtype=torch.bfloat16, device=DEV))
@@ -304,6 +355,26 @@ def test_epilogue_backward(rows, cols, kind, mul, p):
         if mul and dst != "mul":
             assert torch.equal(t["mul"], dm)
     ok()
+
+
+def test_epilogue_backward_of_dropped_elements_is_zero():
+    """Whatever Z, mul and dY hold there."""
+    rows, cols = 40, 264
+    keep = R.keep(rows, cols, 0.5, SEED, OFFSET) > 0
+    gone = torch.from_numpy(~keep).to(DEV)
+    for bad in (float("nan"), float("inf"), -float("inf")):
+        dY, Z, m = rand(1, (rows, cols)), rand(2, (rows, cols)), rand(3, (rows, cols))
+        for t in (dY, Z, m):
+            t[gone] = bad
+        for kind in KINDS:
+            dZ, dm, db = torch.empty_like(Z), torch.empty_like(Z), torch.empty(cols, device=DEV)
+            F.epilogue_backward(dY, dZ, Z=Z, act=kind, mul=m, dmul=dm, dbias=db, p=0.5, seed=SEED,
+                                offset=OFFSET,
+                                workspace=torch.empty(1 << 20, dtype=torch.uint8, device=DEV))
+            ok()
+            for t in (dZ, dm):
+                assert bool((t[gone] == 0).all()) and bool(torch.isfinite(t).all())
+            assert bool(torch.isfinite(db).all())
 
 
 def test_epilogue_backward_without_z():

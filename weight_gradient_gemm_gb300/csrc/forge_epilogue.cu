@@ -34,7 +34,7 @@ __global__ void __launch_bounds__(256) dropout_kernel(const uint4* x, const uint
     if (v < nvec) {
       float f[8];
       unpack8(xv[i], f);
-      if (d.threshold) drop8(f, d, offset, static_cast<uint64_t>(v));
+      if (d.threshold) drop8(f, d, kept8(d, offset, static_cast<uint64_t>(v)));
       if (residual) {
         float r[8];
         unpack8(rv[i], r);
@@ -48,12 +48,17 @@ __global__ void __launch_bounds__(256) dropout_kernel(const uint4* x, const uint
 
 // ---------------------------------------------------------------- backward
 //   dA = drop(dY),  dmul = dA act(Z),  dZ = dA mul act'(Z),  dbias = sum over rows of dZ
-// in fp32 (dZ rounded only where it is stored).
+// in fp32 (dZ rounded only where it is stored).  Where an element was dropped all its
+// gradients are zero, also where Z or mul is NaN or infinite there.
 template <int ACT, bool MUL>
 __device__ __forceinline__ void bwd8(const EpiBwdArgs& a, uint4 dyv, uint4 zv, uint4 mv,
                                      uint64_t offset, int64_t at, float (&dz)[8]) {
   unpack8(dyv, dz);
-  if (a.drop.threshold) drop8(dz, a.drop, offset, static_cast<uint64_t>(at));
+  uint32_t kept = 0xFFu;
+  if (a.drop.threshold) {
+    kept = kept8(a.drop, offset, static_cast<uint64_t>(at));
+    drop8(dz, a.drop, kept);
+  }
   float z[8];
   if (ACT != kActNone || MUL) unpack8(zv, z);
   if constexpr (MUL) {
@@ -62,7 +67,7 @@ __device__ __forceinline__ void bwd8(const EpiBwdArgs& a, uint4 dyv, uint4 zv, u
     if (a.dmul) {
       float dm[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) dm[k] = dz[k] * act_value<ACT>(z[k]);
+      for (int k = 0; k < 8; ++k) dm[k] = kept >> k & 1u ? dz[k] * act_value<ACT>(z[k]) : 0.0f;
       __stcs(reinterpret_cast<uint4*>(a.dmul) + at, pack8(dm));
     }
 #pragma unroll
@@ -71,6 +76,10 @@ __device__ __forceinline__ void bwd8(const EpiBwdArgs& a, uint4 dyv, uint4 zv, u
   if constexpr (ACT != kActNone) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) dz[k] *= act_slope<ACT>(z[k]);
+  }
+  if (kept != 0xFFu) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) dz[k] = kept >> k & 1u ? dz[k] : 0.0f;
   }
   if (a.dz) __stcs(reinterpret_cast<uint4*>(a.dz) + at, pack8(dz));
 }

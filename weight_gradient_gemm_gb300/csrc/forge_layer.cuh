@@ -114,19 +114,25 @@ __device__ __forceinline__ uint4 philox4x32_10(uint4 c, uint32_t k0, uint32_t k1
 __device__ __forceinline__ uint64_t drop_offset(const DropArgs& d) {
   return d.offset + (d.counter ? __ldcg(reinterpret_cast<const unsigned long long*>(d.counter)) : 0);
 }
-// v = 0 where dropped, v * scale elsewhere, for the elements of block b.
-__device__ __forceinline__ void drop8(float (&v)[8], const DropArgs& d, uint64_t offset,
-                                      uint64_t b) {
+// Which elements of block b are kept, a bit each.
+__device__ __forceinline__ uint32_t kept8(const DropArgs& d, uint64_t offset, uint64_t b) {
   const uint4 w = philox4x32_10(
       make_uint4(static_cast<uint32_t>(b), static_cast<uint32_t>(b >> 32),
                  static_cast<uint32_t>(offset), static_cast<uint32_t>(offset >> 32)),
       static_cast<uint32_t>(d.seed), static_cast<uint32_t>(d.seed >> 32));
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+  uint32_t kept = 0u;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    v[2 * j] = (u[j] & 0xFFFFu) >= d.threshold ? v[2 * j] * d.scale : 0.0f;
-    v[2 * j + 1] = (u[j] >> 16) >= d.threshold ? v[2 * j + 1] * d.scale : 0.0f;
+    if ((u[j] & 0xFFFFu) >= d.threshold) kept |= 1u << (2 * j);
+    if ((u[j] >> 16) >= d.threshold) kept |= 2u << (2 * j);
   }
+  return kept;
+}
+// v = 0 where dropped (whatever it was), v * scale elsewhere.
+__device__ __forceinline__ void drop8(float (&v)[8], const DropArgs& d, uint32_t kept) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) v[k] = kept >> k & 1u ? v[k] * d.scale : 0.0f;
 }
 
 // ---------------------------------------------------------------- the epilogue
@@ -159,7 +165,7 @@ __device__ __forceinline__ uint4 epilogue8(float (&v)[8], const EpiArgs& e, uint
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] *= m[k];
   }
-  if (e.drop.threshold) drop8(v, e.drop, offset, block);
+  if (e.drop.threshold) drop8(v, e.drop, kept8(e.drop, offset, block));
   if (e.residual) {
     float r[8];
     unpack8(residual, r);

@@ -30,9 +30,14 @@ namespace forge {
 namespace {
 
 enum RopeMode { kRope = 0, kQkNorm = 1, kQkNormBwd = 2 };
-// Steps whose loads are in flight at once, most steps of a chunk, and blocks an SM.
-constexpr int kStepsFwd = 4, kChunkFwd = 4, kBlocksFwd = 2;
-constexpr int kStepsBwd = 1, kChunkBwd = 4, kBlocksBwd = 2;
+// By mode: the steps whose loads are in flight at once, and the most steps of a chunk
+// (longer chunks form fewer sines and cosines, shorter ones leave more blocks and less to
+// wait for: norm and rotation of 1999 tokens 10.5 us with chunks of two, 11.2 of four and
+// 12.4 of eight; its backward pass 17.0, 18.0 and 20.4).
+constexpr int kSteps[] = {4, 2, 1}, kChunk[] = {4, 2, 2};
+// Two blocks of 256 threads an SM, with up to 128 registers a thread; three, with 80,
+// spill (backward pass of 8192 tokens 82 us in place of 49).
+constexpr int kBlocks = 2;
 
 // Which blocks take what: the chunks of set k, `per` steps each (a multiple of the steps
 // in flight), have `blocks` blocks each, one chunk's after the other's.
@@ -160,15 +165,17 @@ __device__ __forceinline__ void sin_cos(uint32_t turn, float& s, float& c) {
   if ((quarter + 1u) & 2u) c = -c;
 }
 // Those of all the head's pairs at a position, times the magnitude, into the warp's
-// tables.
-__device__ __forceinline__ void fill_turns(const RopeArgs& r, int64_t pos, int lane, float* cosine,
-                                           float* sine) {
+// tables: cosines, sines (back = -1: of the opposite angle) and their negatives.
+__device__ __forceinline__ void fill_turns(const RopeArgs& r, int64_t pos, int lane, float back,
+                                           float (*table)[128]) {
   for (int i = lane; i < r.rot / 2; i += 32) {
     const uint64_t at = static_cast<uint64_t>(pos) * r.freqs[i];
     float s, c;
     sin_cos(static_cast<uint32_t>(at >> 32), s, c);
-    cosine[i] = c * r.magnitude;
-    sine[i] = s * r.magnitude;
+    s *= back * r.magnitude;
+    table[0][i] = c * r.magnitude;
+    table[1][i] = s;
+    table[2][i] = -s;
   }
 }
 // Those of the lane's VEC pairs, which follow one another.
@@ -181,46 +188,55 @@ __device__ __forceinline__ void load_turns(const float* t, float2 (&v)[VEC / 2])
     v[i + 1] = make_float2(w.z, w.w);
   }
 }
-__device__ __forceinline__ float2 neg2(float2 v) { return make_float2(-v.x, -v.y); }
-// The pairs turned by the angle whose sines and cosines are c and s.
+// The pairs turned by the angle whose cosines, sines and their negatives are c, s and n.
 template <int VEC>
 __device__ __forceinline__ void turn(const LanePart& p, const float2 (&c)[VEC / 2],
-                                     const float2 (&s)[VEC / 2], float2 (&a)[VEC / 2],
-                                     float2 (&b)[VEC / 2]) {
+                                     const float2 (&s)[VEC / 2], const float2 (&n)[VEC / 2],
+                                     float2 (&a)[VEC / 2], float2 (&b)[VEC / 2]) {
 #pragma unroll
   for (int i = 0; i < VEC / 2; ++i) {
     if (i < VEC / 4 ? p.rot_a : p.rot_b) {
       const float2 x = a[i], y = b[i];
-      a[i] = fma2(neg2(s[i]), y, mul2(c[i], x));
+      a[i] = fma2(n[i], y, mul2(c[i], x));
       b[i] = fma2(s[i], x, mul2(c[i], y));
     }
   }
 }
 
-// Sum over the P lanes of a head.
+// Sum over the `lanes` lanes of a head (P of them where P is not 0).
+template <int P>
 __device__ __forceinline__ float head_sum(float v, int lanes) {
-  for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if constexpr (P > 0) {
+#pragma unroll
+    for (int o = P >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  } else {
+    for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  }
   return v;
 }
 
-template <int VEC, bool INTER, int MODE>
-__global__ void __launch_bounds__(256, MODE == kQkNormBwd ? kBlocksBwd : kBlocksFwd)
+// P: lanes of a head, 0 where the launch says them.
+template <int VEC, bool INTER, int MODE, int P>
+__global__ void __launch_bounds__(256, kBlocks)
     rope_kernel(const RopeArgs r, const RopeGrid grid) {
   using V = typename Words<VEC>::V;
   constexpr bool kBwd = MODE == kQkNormBwd;
-  constexpr int STEPS = kBwd ? kStepsBwd : kStepsFwd;
+  constexpr int STEPS = kSteps[MODE];
   constexpr int N = VEC / 2;
-  __shared__ __align__(16) float tables[8][2][128];   // [warp][cosine, sine][pair]
+  __shared__ __align__(16) float tables[8][3][128];   // [warp][table][pair]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int lanes = grid.lanes, u = lane & (lanes - 1), g = lane / lanes, groups = 32 / lanes;
+  const int lanes = P > 0 ? P : grid.lanes, u = lane & (lanes - 1), g = lane / lanes, groups = 32 / lanes;
   const LanePart p = lane_part<VEC, INTER>(u, r.dim, r.rot);
   const int of0 = grid.set[0].chunks * grid.set[0].blocks;
   const int k = static_cast<int>(blockIdx.x) >= of0;
   const int rank = static_cast<int>(blockIdx.x) - (k ? of0 : 0);
   const int chunk = rank / grid.set[k].blocks, sub = rank - chunk * grid.set[k].blocks;
   const HeadSet& set = r.set[k];
-  const int per = grid.set[k].per, head0 = chunk * per * groups + g;
-  const int end = min(set.heads, (chunk + 1) * per * groups);
+  const int per = grid.set[k].per, first = chunk * per * groups, head0 = first + g;
+  const int end = min(set.heads, first + per * groups);
+  // a step whose heads all exist has nothing to ask where the lanes fill a head
+  const bool whole = 2 * VEC * lanes == r.dim;
+  auto all_of = [&](int step) { return whole && first + (step + 1) * groups <= end; };
 
   const int64_t walk = static_cast<int64_t>(grid.set[k].blocks) * 8;   // tokens from one to the next
   int64_t t = static_cast<int64_t>(sub) * 8 + warp;
@@ -237,17 +253,27 @@ __global__ void __launch_bounds__(256, MODE == kQkNormBwd ? kBlocksBwd : kBlocks
 
   V xa[STEPS], xb[STEPS], da[kBwd ? STEPS : 1], db[kBwd ? STEPS : 1];
   auto load = [&](int j) {
-    const bool in = load_t < r.tokens && head0 + load_step * groups < end;
-    xa[j] = xb[j] = Words<VEC>::zero();
-    if (in && p.has_a) xa[j] = __ldcs(reinterpret_cast<const V*>(x));
-    if (in && p.has_b) xb[j] = __ldcs(reinterpret_cast<const V*>(x + ab));
-    x += x_step;
-    if constexpr (kBwd) {
-      da[j] = db[j] = Words<VEC>::zero();
-      if (in && p.has_a) da[j] = __ldcs(reinterpret_cast<const V*>(dy));
-      if (in && p.has_b) db[j] = __ldcs(reinterpret_cast<const V*>(dy + ab));
-      dy += dy_step;
+    const bool more = load_t < r.tokens;
+    if (more && all_of(load_step)) {
+      xa[j] = __ldcs(reinterpret_cast<const V*>(x));
+      xb[j] = __ldcs(reinterpret_cast<const V*>(x + ab));
+      if constexpr (kBwd) {
+        da[j] = __ldcs(reinterpret_cast<const V*>(dy));
+        db[j] = __ldcs(reinterpret_cast<const V*>(dy + ab));
+      }
+    } else {
+      const bool in = more && head0 + load_step * groups < end;
+      xa[j] = xb[j] = Words<VEC>::zero();
+      if (in && p.has_a) xa[j] = __ldcs(reinterpret_cast<const V*>(x));
+      if (in && p.has_b) xb[j] = __ldcs(reinterpret_cast<const V*>(x + ab));
+      if constexpr (kBwd) {
+        da[j] = db[j] = Words<VEC>::zero();
+        if (in && p.has_a) da[j] = __ldcs(reinterpret_cast<const V*>(dy));
+        if (in && p.has_b) db[j] = __ldcs(reinterpret_cast<const V*>(dy + ab));
+      }
     }
+    x += x_step;
+    if constexpr (kBwd) dy += dy_step;
     if (++load_step == per) {
       load_step = 0;
       load_t += walk;
@@ -275,24 +301,23 @@ __global__ void __launch_bounds__(256, MODE == kQkNormBwd ? kBlocksBwd : kBlocks
       gb[i] = make_float2(gain(i, 0, 1), gain(i, 1, 1));
     }
   }
-  float *cosine = tables[warp][0], *sine = tables[warp][1];
+  float(*table)[128] = tables[warp];
+  const float back = kBwd || r.inverse ? -1.0f : 1.0f;
 #pragma unroll 1
   for (; t < r.tokens; t += walk) {
     __syncwarp();
-    fill_turns(r, pos, lane, cosine, sine);
+    fill_turns(r, pos, lane, back, table);
     __syncwarp();
     if (t + walk < r.tokens) pos = r.positions ? r.positions[t + walk] : t + walk;
-    float2 c[N], s[N];
+    float2 c[N], s[N], n[N];
     auto turns = [&]() {   // the lane's pairs, VEC from VEC u on
       if (!p.rot_a) return;
-      load_turns<VEC>(cosine + VEC * u, c);
-      load_turns<VEC>(sine + VEC * u, s);
-      if (kBwd || r.inverse) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) s[i] = neg2(s[i]);
-      }
+      load_turns<VEC>(table[0] + VEC * u, c);
+      load_turns<VEC>(table[1] + VEC * u, s);
+      load_turns<VEC>(table[2] + VEC * u, n);
     };
-    if constexpr (!kBwd) turns();
+    // (with the norm again at every step: registers are short)
+    if constexpr (MODE == kRope) turns();
 #pragma unroll 1
     for (int step = 0; step < per; step += STEPS) {
 #pragma unroll
@@ -305,15 +330,15 @@ __global__ void __launch_bounds__(256, MODE == kQkNormBwd ? kBlocksBwd : kBlocks
           float2 sq = make_float2(0.0f, 0.0f);
 #pragma unroll
           for (int i = 0; i < N; ++i) sq = fma2(b[i], b[i], fma2(a[i], a[i], sq));
-          const float rstd = rsqrtf(head_sum(sq.x + sq.y, lanes) * r.inv_dim + r.eps);
+          const float rstd = rsqrtf(head_sum<P>(sq.x + sq.y, lanes) * r.inv_dim + r.eps);
 #pragma unroll
           for (int i = 0; i < N; ++i) {
             a[i] = mul2(a[i], dup2(rstd));
             b[i] = mul2(b[i], dup2(rstd));
           }
           if constexpr (kBwd) {
-            turns();                      // (again: registers are short)
-            turn<VEC>(p, c, s, na, nb);   // the gradient of the normed head
+            turns();
+            turn<VEC>(p, c, s, n, na, nb);   // the gradient of the normed head
             float2 dots = make_float2(0.0f, 0.0f);
 #pragma unroll
             for (int i = 0; i < N; ++i) {
@@ -323,7 +348,7 @@ __global__ void __launch_bounds__(256, MODE == kQkNormBwd ? kBlocksBwd : kBlocks
               nb[i] = mul2(nb[i], gb[i]);
               dots = fma2(nb[i], b[i], fma2(na[i], a[i], dots));
             }
-            const float dot = head_sum(dots.x + dots.y, lanes) * r.inv_dim;
+            const float dot = head_sum<P>(dots.x + dots.y, lanes) * r.inv_dim;
 #pragma unroll
             for (int i = 0; i < N; ++i) {
               a[i] = mul2(dup2(rstd), fma2(dup2(-dot), a[i], na[i]));
@@ -337,12 +362,18 @@ __global__ void __launch_bounds__(256, MODE == kQkNormBwd ? kBlocksBwd : kBlocks
             }
           }
         }
-        if constexpr (!kBwd) turn<VEC>(p, c, s, a, b);
+        if constexpr (MODE == kQkNorm) turns();
+        if constexpr (!kBwd) turn<VEC>(p, c, s, n, a, b);
         V va, vb;
         from_pairs<VEC, INTER>(a, b, va, vb);
-        const bool in = head0 + (step + j) * groups < end;
-        if (in && p.has_a) __stcs(reinterpret_cast<V*>(y), va);
-        if (in && p.has_b) __stcs(reinterpret_cast<V*>(y + ab), vb);
+        if (all_of(step + j)) {
+          __stcs(reinterpret_cast<V*>(y), va);
+          __stcs(reinterpret_cast<V*>(y + ab), vb);
+        } else {
+          const bool in = head0 + (step + j) * groups < end;
+          if (in && p.has_a) __stcs(reinterpret_cast<V*>(y), va);
+          if (in && p.has_b) __stcs(reinterpret_cast<V*>(y + ab), vb);
+        }
         y += y_step;
       }
     }
@@ -422,7 +453,7 @@ int round_up_pow2(int n) {
 // As many blocks as are resident at once, shared among the chunks by their steps (and
 // two for a token's sines and cosines), or one a chunk and eight tokens where there are
 // fewer.
-RopePlan rope_plan(const RopeArgs& a, bool backward, int num_sms) {
+RopePlan rope_plan(const RopeArgs& a, RopeMode mode, int num_sms) {
   RopePlan p;
   p.vec = a.interleaved || a.rot % 16 == 0 ? 8 : 4;
   const int turning = a.rot / (2 * p.vec), rest = a.dim - a.rot;
@@ -430,11 +461,11 @@ RopePlan rope_plan(const RopeArgs& a, bool backward, int num_sms) {
                                  : turning + (rest + 2 * p.vec - 1) / (2 * p.vec);
   p.grid.lanes = round_up_pow2(need);
   const int groups = 32 / p.grid.lanes;
-  const int flight = backward ? kStepsBwd : kStepsFwd;
-  const int64_t cap = static_cast<int64_t>(num_sms) * (backward ? kBlocksBwd : kBlocksFwd);
+  const int flight = kSteps[mode];
+  const int64_t cap = static_cast<int64_t>(num_sms) * kBlocks;
   const int64_t full = (a.tokens + 7) / 8;
   // few tokens: shorter chunks, for more blocks
-  int most = backward ? kChunkBwd : kChunkFwd;
+  int most = kChunk[mode];
   auto chunks_of = [&](int k) {
     const int steps = (a.set[k].heads + groups - 1) / groups;
     return (steps + most - 1) / most;
@@ -463,24 +494,35 @@ cudaError_t launch_mode(const RopeArgs& a, const RopePlan& p, cudaStream_t strea
   auto go = [&](auto kern) {
     return launch_chained(kern, p.blocks(0) + p.blocks(1), 256, 0, 0, stream, a, p.grid);
   };
-  if (a.interleaved) return go(rope_kernel<8, true, MODE>);
-  return p.vec == 8 ? go(rope_kernel<8, false, MODE>) : go(rope_kernel<4, false, MODE>);
+  // Heads of 128 (down to 65) and of 64 know their lanes; not the backward pass of
+  // neighbouring pairs, which spills more so (8192 tokens 54.5 us in place of 52).
+  if (a.interleaved) {
+    if constexpr (MODE != kQkNormBwd) {
+      if (p.grid.lanes == 8) return go(rope_kernel<8, true, MODE, 8>);
+      if (p.grid.lanes == 4) return go(rope_kernel<8, true, MODE, 4>);
+    }
+    return go(rope_kernel<8, true, MODE, 0>);
+  }
+  if (p.vec == 4) return go(rope_kernel<4, false, MODE, 0>);
+  if (p.grid.lanes == 8) return go(rope_kernel<8, false, MODE, 8>);
+  if (p.grid.lanes == 4) return go(rope_kernel<8, false, MODE, 4>);
+  return go(rope_kernel<8, false, MODE, 0>);
 }
 
 }  // namespace
 
 cudaError_t launch_rope(const RopeArgs& a, int num_sms, cudaStream_t stream) {
-  return launch_mode<kRope>(a, rope_plan(a, false, num_sms), stream);
+  return launch_mode<kRope>(a, rope_plan(a, kRope, num_sms), stream);
 }
 cudaError_t launch_qk_norm_rope(const RopeArgs& a, int num_sms, cudaStream_t stream) {
-  return launch_mode<kQkNorm>(a, rope_plan(a, false, num_sms), stream);
+  return launch_mode<kQkNorm>(a, rope_plan(a, kQkNorm, num_sms), stream);
 }
 
 // A block a chunk at least: kMaxHeads heads of each kind, one a step where they are widest.
-int qk_bwd_blocks(int num_sms) { return kBlocksBwd * num_sms + 2 * (kMaxHeads / kStepsBwd); }
+int qk_bwd_blocks(int num_sms) { return kBlocks * num_sms + 2 * (kMaxHeads / kSteps[kQkNormBwd]); }
 
 cudaError_t launch_qk_norm_rope_bwd(const RopeArgs& a, int num_sms, cudaStream_t stream) {
-  const RopePlan p = rope_plan(a, true, num_sms);
+  const RopePlan p = rope_plan(a, kQkNormBwd, num_sms);
   const cudaError_t e = launch_mode<kQkNormBwd>(a, p, stream);
   if (e != cudaSuccess) return e;
   const bool join = (a.set[0].dgain && p.blocks(0) > 1) || (a.set[1].dgain && p.blocks(1) > 1);

@@ -11,7 +11,9 @@ namespace {
 
 // ---------------------------------------------------------------- dropout
 // y = residual + drop(x), eight elements (one generator block) a thread and vector.
-// U vectors' loads are in flight at once.
+// U vectors' loads are in flight at once.  Bound by memory (the generator is 9
+// instructions an element): 8191 x 4096 with the residual 30.4 us, 29.6 at the copy rate;
+// 64 x 520 1.4 on the device, 3.2 through Python.
 template <int U>
 __global__ void __launch_bounds__(256) dropout_kernel(const uint4* x, const uint4* residual,
                                                       uint4* y, int64_t nvec, const DropArgs d) {
@@ -84,7 +86,8 @@ __device__ __forceinline__ void bwd8(const EpiBwdArgs& a, uint4 dyv, uint4 zv, u
   if (a.dz) __stcs(reinterpret_cast<uint4*>(a.dz) + at, pack8(dz));
 }
 
-// Without dbias: vectors in memory order.
+// Without dbias: vectors in memory order.  8192 x 14336 with SILU and mul, 1.17 GB, 162.5 us
+// (7.2 TB/s, three fifths of it reads).
 template <int ACT, bool MUL>
 __global__ void __launch_bounds__(256) epilogue_bwd_kernel(const EpiBwdArgs a) {
   constexpr int U = 2;

@@ -12,6 +12,20 @@
 // into registers ahead of the arithmetic, and Y and Z stored from registers, a sector
 // or more a lane: shared memory is left to the operands.  Every wait is bounded, as in
 // forge_gemm.cuh.
+//
+// What bounds it: a stage's products take 2 BN cycles and its operands, 16 KB of tokens
+// and 64 BN bytes of weight a CTA, as long at the 64 bytes a cycle that an SM takes in;
+// for BN = 256 both take 512, and 530 were measured.  Long runs meet the power limit
+// before either (the clock falls to about 1500 MHz).  8192 tokens, 4096 -> 14336: 472 us in short runs
+// (2.04 PFLOP/s; a plain library product 465), with gate and stored Z 533, and 616 to 624 without
+// a pause, where the sustained library rate would take 563 without an epilogue.  2000
+// tokens, 14336 -> 4096, 152 tiles of 224 on 76 pairs: 125 and 150 us.  4096 tokens, 4096
+// -> 4096: 73.4.
+// Measured and dropped: outputs through shared memory and TMA (605 us with the gate, on
+// five stages, where registers and seven stages took 550), pairs that split a reduction
+// over a cluster (256 tokens, 4096 -> 4096, 16.4 us, on single CTAs 14.3), 512 tokens a
+// tile with one accumulator (2000 tokens 150 -> 144, 8192 tokens 487 -> 560), pairs that
+// are not persistent (484 -> 612).
 #include <cuda_bf16.h>
 
 #include "forge_internal.h"
@@ -57,7 +71,8 @@ struct Ahead {
   uint4 res[4], mul[4];
   float bias;   // lane l: that of column l
 };
-// 32 bytes (a sector) at once where everything is aligned to them, else 16.
+// 32 bytes (a sector) at once where everything is aligned to them, else 16.  (A row a lane:
+// what a warp reads or writes at once lies in 32 rows, so whole sectors matter.)
 __device__ __forceinline__ void load32(const uint16_t* p, bool wide, bool second, uint4& x,
                                        uint4& y) {
   if (wide) {

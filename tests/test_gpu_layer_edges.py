@@ -220,6 +220,35 @@ def test_heads_leave_the_rest_alone(dim, rot):
             untouched(wse, dg[0][1], dg[1][1])
 
 
+@pytest.mark.parametrize("heads", [(0, 2), (2, 0), (0, 0)])
+def test_kinds_without_heads(heads):
+    """A kind without heads: the other is as alone, its gain's gradient is zero."""
+    dim, tokens = 64, 9
+    freqs, _ = F.rope_frequencies(dim, 10000.0)
+    x = [rand(1 + i, (tokens, h, dim)) for i, h in enumerate(heads)]
+    dy = [rand(3 + i, (tokens, h, dim)) for i, h in enumerate(heads)]
+    g = [rand(5 + i, (dim,), 1.0, torch.float32) for i in range(2)]
+    ws = torch.empty(F.qk_norm_rope_backward_workspace_bytes(dim), dtype=torch.uint8, device=DEV)
+    dg = [torch.full((dim,), 7.0, device=DEV) for _ in range(2)]
+    out = [torch.empty_like(t) for t in x]
+    F.qk_norm_rope_backward(*dy, *x, *g, freqs, eps=1e-5, dq_out=out[0], dk_out=out[1],
+                            dq_gain=dg[0], dk_gain=dg[1], workspace=ws)
+    for i, h in enumerate(heads):
+        if h == 0:
+            ok()
+            assert bool((dg[i] == 0).all())
+            continue
+        one, dg1 = torch.empty_like(x[i]), torch.empty(dim, device=DEV)
+        F.qk_norm_rope_backward(dy[i], None, x[i], None, g[i], None, freqs, eps=1e-5, dq_out=one,
+                                dq_gain=dg1, workspace=ws)
+        ok()
+        assert torch.equal(out[i], one) and torch.equal(dg[i], dg1)   # the same blocks
+    for fn in (lambda o: F.rope(*x, freqs, q_out=o[0], k_out=o[1]),
+               lambda o: F.qk_norm_rope(*x, *g, freqs, eps=1e-5, q_out=o[0], k_out=o[1])):
+        fn(out)
+        ok()
+
+
 @pytest.mark.parametrize("bt,d_in,d_out,how", [
     (3, 4104, 264, {}), (100, 1032, 520, {}), (3, 264, 40000, {}),            # few tokens
     (300, 4104, 520, dict(cg=1, splits=4)), (700, 264, 2056, dict(cg=1, splits=1)),

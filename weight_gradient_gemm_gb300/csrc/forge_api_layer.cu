@@ -501,15 +501,13 @@ forge_status forge_qk_norm_rope_backward(const forge_heads* sets, int n, forge_d
         return FORGE_ERR_ALIAS;
     }
   }
-  if (a.tokens == 0) {   // nothing to sum: the gains' gradients are zero
-    for (int i = 0; i < n; ++i)
-      if (a.set[i].dgain) {
-        const cudaError_t e =
-            cudaMemsetAsync(a.set[i].dgain, 0, static_cast<size_t>(head_dim) * 4, cs);
-        if (e != cudaSuccess) return status(e);
-      }
-    return FORGE_OK;
-  }
+  for (int i = 0; i < n; ++i)   // nothing to sum: the gain's gradient is zero
+    if (a.set[i].dgain && a.set[i].heads == 0) {
+      const cudaError_t e =
+          cudaMemsetAsync(a.set[i].dgain, 0, static_cast<size_t>(head_dim) * 4, cs);
+      if (e != cudaSuccess) return status(e);
+    }
+  if (a.tokens == 0) return FORGE_OK;
   a.part = static_cast<float*>(workspace);
   return status(launch_qk_norm_rope_bwd(a, d.num_sms, cs));
 }

@@ -697,8 +697,8 @@ forge_status forge_linear_bf16(const void* X, const void* W, void* Y, forge_dtyp
  * (device, 16-byte aligned) of at least forge_epilogue_backward_workspace_bytes(rows, cols)
  * (FORGE_ERR_SHAPE if smaller; 0 bytes: it may be NULL), not used by another call until this
  * one has run.  The rows are added in a fixed order: the same result on every run.  rows = 0
- * writes zeros to dbias.  cols is a multiple of 8, rows * cols at most 2^40.  Asynchronous
- * on `stream`.
+ * writes zeros to dbias.  cols is a multiple of 8, rows * cols at most 2^40; pointers
+ * 16-byte aligned.  Asynchronous on `stream`.
  */
 forge_status forge_epilogue_backward(const void* dY, const void* Z, const void* mul,
                                      forge_activation act, const forge_drop* drop, void* dZ,
@@ -711,8 +711,8 @@ size_t forge_epilogue_backward_workspace_bytes(int64_t rows, int64_t cols);
  * forge_dropout: y = residual + drop(x) in fp32, rounded once to bf16.  x, y [rows, cols]
  * bf16, residual [rows, cols] bf16 or NULL (0).  The gradient of x is the same call on y's
  * gradient without the residual, whose gradient is y's.  y may be the same buffer as x or
- * residual.  cols is a multiple of 8, rows * cols at most 2^40.  rows = 0 does nothing.
- * Asynchronous on `stream`.
+ * residual.  cols is a multiple of 8, rows * cols at most 2^40; pointers 16-byte aligned.
+ * rows = 0 does nothing.  Asynchronous on `stream`.
  */
 forge_status forge_dropout(const void* x, const void* residual, void* y, const forge_drop* drop,
                            int64_t rows, int64_t cols, forge_stream stream);
@@ -770,7 +770,8 @@ typedef struct {
   const void* gain;           /* forge_qk_norm_rope and its backward pass: [head_dim]      */
   const void* dy;             /* backward: the gradient of the rotated heads              */
   int64_t dy_token, dy_head;
-  float* dgain;               /* backward: [head_dim] fp32, overwritten, or NULL          */
+  float* dgain;               /* backward: [head_dim] fp32, overwritten, 16-byte aligned,
+                                 or NULL                                                  */
 } forge_heads;
 
 /*
@@ -778,11 +779,11 @@ typedef struct {
  * with the angle w = 2 pi p freqs[i] / 2^64 (formed exactly modulo a turn), pair (a, b)
  * becomes magnitude (a cos w - b sin w, b cos w + a sin w), in fp32, rounded once.  With
  * `inverse` the angle is -w: the gradient of the call without it.
- * head_dim is a multiple of 8, at most 256; at most 1024 heads of a kind.  Pointers of heads 16-byte aligned.  y may be
- * the same view as its own x; otherwise no output may overlap an input or another output
- * (interleaved views of one buffer, as queries and keys in the fused output of their
- * projections, do not), and no element of y may lie in two places.  tokens = 0 or heads = 0
- * does nothing.  Asynchronous on `stream`.
+ * head_dim is a multiple of 8, at most 256; at most 1024 heads of a kind.  Pointers of
+ * heads 16-byte aligned.  y may be the same view as its own x; otherwise no output may
+ * overlap an input or another output (interleaved views of one buffer, as queries and keys
+ * in the fused output of their projections, do not), and no element of y may lie in two
+ * places.  tokens = 0 or heads = 0 does nothing.  Asynchronous on `stream`.
  */
 forge_status forge_rope(const forge_heads* sets, int n, const forge_rotation* rot, int inverse,
                         int64_t tokens, int64_t head_dim, forge_stream stream);

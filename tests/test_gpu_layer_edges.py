@@ -220,6 +220,15 @@ def test_heads_leave_the_rest_alone(dim, rot):
             untouched(wse, dg[0][1], dg[1][1])
 
 
+@pytest.mark.parametrize("group_m", [-3, 1, 2, 64, 1000])
+def test_linear_tile_order(group_m, tune):
+    """Groups of tile rows of any size (what lies outside 1..64: automatic)."""
+    tune(cg=2, group_m=group_m)
+    c = linear_case(1100, 136, 2056, **EPILOGUES["all"])
+    call_linear(c)
+    check_linear(c)
+
+
 @pytest.mark.parametrize("heads", [(0, 2), (2, 0), (0, 0)])
 def test_kinds_without_heads(heads):
     """A kind without heads: the other is as alone, its gain's gradient is zero."""

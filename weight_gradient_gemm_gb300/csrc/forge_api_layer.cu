@@ -183,7 +183,8 @@ forge_status forge_linear_bf16(const void* X, const void* W, void* Y, forge_dtyp
   a.tiles_m = static_cast<int32_t>(tiles_m);
   a.tiles_n = static_cast<int32_t>(tiles_n);
   a.num_tiles = static_cast<int32_t>(tiles_m * tiles_n);
-  a.group_m = tune.group_m ? tune.group_m : 16;
+  a.group_m = tune.group_m >= 1 && tune.group_m <= 64 ? tune.group_m : 16;
+  if (a.group_m > a.tiles_m) a.group_m = a.tiles_m;
   a.bn = cfg.bn;
   a.wide = d_out % 16 == 0 && aligned(Y, 32) && aligned(e.mul, 32) && aligned(e.residual, 32) &&
            aligned(e.z, 32);
@@ -285,7 +286,6 @@ forge_status forge_dropout(const void* x, const void* residual, void* y, const f
 namespace {
 
 constexpr int kMaxHeadDim = 256;
-
 
 // One view [tokens, heads, dim] of a call.
 struct View {

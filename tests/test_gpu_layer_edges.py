@@ -220,6 +220,14 @@ def test_heads_leave_the_rest_alone(dim, rot):
             untouched(wse, dg[0][1], dg[1][1])
 
 
+@pytest.mark.parametrize("bt,d_in,d_out", [(65, 136, 19600), (100, 8, 20000), (128, 72, 40008)])
+def test_linear_up_to_128_tokens_and_many_outputs(bt, d_in, d_out):
+    """More tiles of 128 outputs than SMs: pairs with half of their rows empty."""
+    c = linear_case(bt, d_in, d_out, **EPILOGUES["all"])
+    call_linear(c)
+    check_linear(c)
+
+
 @pytest.mark.parametrize("group_m", [-3, 1, 2, 64, 1000])
 def test_linear_tile_order(group_m, tune):
     """Groups of tile rows of any size (what lies outside 1..64: automatic)."""

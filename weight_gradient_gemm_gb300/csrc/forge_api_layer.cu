@@ -88,8 +88,12 @@ Span counter_span(const DropArgs& d) { return Span{d.counter, 8}; }
 //   bn = 256, whose products take 512), tiles in waves, the last tile's epilogue after them.
 // 333 tokens, 1032 -> 520, 7.3 us on single CTAs and 8.1 on pairs; 300, 4096 -> 1024, 9.7
 // and 17.9; 512, 4096 -> 14336, 62 and 40; 150, 4096 -> 14336, 48.6 and 26.8.
-// Up to 128 tokens the pairs' form would leave half of its rows empty (128 tokens, 4096 ->
-// 14336, 23.5 us and 30), and the weight's bytes need every SM: the largest split there is.
+// Up to 128 tokens the pairs' form leaves half of its rows empty (128 tokens, 4096 ->
+// 14336, 24.0 us and 26.7), and the weight's bytes need every SM: the largest split there
+// is.  Tiles of 128 tokens, one an SM, do not overlap one's end with the next's start:
+// where there are more than SMs the persistent pairs take them (128 tokens, 4096 -> 20480,
+// 38.6 us and 52.7, -> 57344 81.7 and 91.4, -> 131072 173 and 221); up to 64, two an SM do
+// (64 tokens, -> 57344, 78.9 us and 80.7).
 LinearConfig choose_linear(int64_t m, int64_t n, int64_t num_kb, const forge_tuning& tune,
                            int num_sms, const int (&clusters)[4]) {
   const int nt = m <= 16 ? 16 : (m <= 32 ? 32 : (m <= 64 ? 64 : 128));
@@ -102,8 +106,9 @@ LinearConfig choose_linear(int64_t m, int64_t n, int64_t num_kb, const forge_tun
     const int64_t cost = (num_kb + splits - 1) / splits * 512 + (splits > 2 ? 4000 : 5000);
     if (tune.splits || m <= 128 || cost < least) least = cost, best.splits = splits;
   }
-  if (tune.cta_group == 1 || (m <= 128 && tune.cta_group == 0)) return best;
-  if (tune.cta_group == 2) least = INT64_MAX;
+  const bool waves_of_128 = m <= 128 && nt == 128 && tiles > num_sms;
+  if (tune.cta_group == 1 || (m <= 128 && tune.cta_group == 0 && !waves_of_128)) return best;
+  if (tune.cta_group == 2 || waves_of_128) least = INT64_MAX;
   const int64_t pairs = num_sms / 2, tiles_m = (m + 255) / 256;
   for (int bn = 256; bn >= 64; bn -= 32) {
     if (tune.bn && bn != tune.bn) continue;

@@ -672,7 +672,9 @@ typedef struct {
  * forge_linear_bf16: the forward product of a linear layer with its epilogue,
  *   Z = X W^T + bias,   Y = residual + drop(act(Z) * mul),
  * accumulated and computed in fp32 and rounded once to each output (act is taken of the
- * unrounded Z).  X [bt, d_in], W [d_out, d_in] bf16; Y [bt, d_out] bf16 or fp32.
+ * unrounded Z).  The tensor core's sums are cut off rather than rounded, about 10^-9 of a sum
+ * for each element; with Y in fp32 that ends after 512 elements, whose sums are added in
+ * fp32, so that long reductions stay within about 5 10^-7.  X [bt, d_in], W [d_out, d_in] bf16; Y [bt, d_out] bf16 or fp32.
  * `epilogue` (host memory, read before the call returns) may be NULL.
  * d_in, d_out multiples of 8; pointers 16-byte aligned.  Y in bf16 may be the same buffer
  * as mul or residual; otherwise no output may overlap an input or another output.  bt = 0

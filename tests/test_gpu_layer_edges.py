@@ -228,6 +228,25 @@ def test_linear_up_to_128_tokens_and_many_outputs(bt, d_in, d_out):
     check_linear(c)
 
 
+@pytest.mark.parametrize("bt,d_out,how", [
+    (1, 264, {}), (40, 20000, {}), (128, 264, dict(splits=1)), (300, 520, dict(cg=1, splits=2)),
+    (300, 520, dict(cg=2)), (300, 520, dict(cg=2, bn=256)), (1000, 2056, dict(cg=2, bn=128)),
+    (2000, 2600, {})])
+def test_fp32_outputs_of_long_reductions(bt, d_out, how, tune):
+    """The tensor core cuts sums off: an instruction (16 products) loses less than 2^-23 of the
+    sum so far.  Over 512 elements, whose j-th of 32 partial sums is about sqrt(j / 32) of the
+    512's, that is less than 2^-23 (2 / 3) 32 of it.  What the 32 sums of 512 lose is
+    independent (it has the sign of each, and they are random), so in the 2-norm it is that
+    share of the whole; adding them in fp32 costs 2^-24 each.  (Cut off throughout, 16384
+    elements lose 1.2 10^-9 each, 1.9 10^-5 in all.)"""
+    tune(**how)
+    c = linear_case(bt, 16384, d_out, residual=False, out=torch.float32)
+    call_linear(c)
+    want = c["X"].double() @ c["W"].double().t()
+    off = float((c["Y"].double() - want).norm() / want.norm())
+    assert off <= 2.0 ** -23 * 2 / 3 * 32 + 32 * 2.0 ** -24
+
+
 @pytest.mark.parametrize("group_m", [-3, 1, 2, 64, 1000])
 def test_linear_tile_order(group_m, tune):
     """Groups of tile rows of any size (what lies outside 1..64: automatic)."""

@@ -95,7 +95,7 @@ Span counter_span(const DropArgs& d) { return Span{d.counter, 8}; }
 // 38.6 us and 52.7, -> 57344 81.7 and 91.4, -> 131072 173 and 221); up to 64, two an SM do
 // (64 tokens, -> 57344, 78.9 us and 80.7).
 LinearConfig choose_linear(int64_t m, int64_t n, int64_t num_kb, const forge_tuning& tune,
-                           int num_sms, const int (&clusters)[4]) {
+                           int num_sms, const int (&clusters)[4], int most_bn) {
   const int nt = m <= 16 ? 16 : (m <= 32 ? 32 : (m <= 64 ? 64 : 128));
   const int64_t tiles = (n + 127) / 128 * ((m + 127) / 128);
   LinearConfig best{nt, 128, 1};
@@ -110,8 +110,8 @@ LinearConfig choose_linear(int64_t m, int64_t n, int64_t num_kb, const forge_tun
   if (tune.cta_group == 1 || (m <= 128 && tune.cta_group == 0 && !waves_of_128)) return best;
   if (tune.cta_group == 2 || waves_of_128) least = INT64_MAX;
   const int64_t pairs = num_sms / 2, tiles_m = (m + 255) / 256;
-  for (int bn = 256; bn >= 64; bn -= 32) {
-    if (tune.bn && bn != tune.bn) continue;
+  for (int bn = most_bn; bn >= 64; bn -= 32) {
+    if (tune.bn && bn != (tune.bn < most_bn ? tune.bn : most_bn)) continue;
     const int64_t waves = (tiles_m * ((n + bn - 1) / bn) + pairs - 1) / pairs;
     const int64_t cost = waves * num_kb * (370 + 5 * bn / 8) + 24 * bn + 1500;
     if (cost < least) least = cost, best = LinearConfig{0, bn, 1};
@@ -164,7 +164,8 @@ forge_status forge_linear_bf16(const void* X, const void* W, void* Y, forge_dtyp
     const cudaError_t r = linear_few_clusters(nt, 1 << i, d.num_sms, &clusters[i]);
     if (r != cudaSuccess) return status(r);
   }
-  const LinearConfig cfg = choose_linear(bt, d_out, num_kb, tune, d.num_sms, clusters);
+  const LinearConfig cfg = choose_linear(bt, d_out, num_kb, tune, d.num_sms, clusters,
+                                         es == 4 ? kMaxLinearF32 : 256);
   const int64_t rows = cfg.few ? cfg.few : 256, tiles_m = (bt + rows - 1) / rows;
   const int64_t tiles_n = (d_out + cfg.bn - 1) / cfg.bn;
   if (tiles_m * tiles_n > kMaxIndex / 8) return FORGE_ERR_SHAPE;
@@ -185,6 +186,7 @@ forge_status forge_linear_bf16(const void* X, const void* W, void* Y, forge_dtyp
   a.m = static_cast<int32_t>(bt);
   a.n = static_cast<int32_t>(d_out);
   a.num_kb = static_cast<int32_t>(num_kb);
+  a.chunk = es == 4 ? kLinearChunk : a.num_kb;
   a.tiles_m = static_cast<int32_t>(tiles_m);
   a.tiles_n = static_cast<int32_t>(tiles_n);
   a.num_tiles = static_cast<int32_t>(tiles_m * tiles_n);

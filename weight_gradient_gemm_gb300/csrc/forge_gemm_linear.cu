@@ -3,7 +3,7 @@
 // X [m, k] and W [n, k] are both K-major.  A pair of CTAs computes a tile of 256 tokens
 // x BN outputs (BN a multiple of 32 up to 256), 128 tokens each, from its own tokens and
 // half of the weight's rows each; the tile's whole reduction stays in tensor memory
-// (fp32).  Pairs are persistent and have two accumulators each, so that the epilogue
+// (fp32; with Y in fp32 in parts).  Pairs are persistent and have two accumulators each, so that the epilogue
 // works on one tile while the next tile's products run.
 //
 // Warp roles (384 threads): warp 0 loads operand stages 64 deep with TMA, warp 1 issues
@@ -16,11 +16,16 @@
 // What bounds it: a stage's products take 2 BN cycles and its operands, 16 KB of tokens
 // and 64 BN bytes of weight a CTA, as long at the 64 bytes a cycle that an SM takes in;
 // for BN = 256 both take 512, and 530 were measured.  Long runs meet the power limit
-// before either (the clock falls to about 1500 MHz).  8192 tokens, 4096 -> 14336: 472 us in short runs
-// (2.04 PFLOP/s; a plain library product 465), with gate and stored Z 533, and 616 to 624 without
-// a pause, where the sustained library rate would take 563 without an epilogue.  2000
-// tokens, 14336 -> 4096, 152 tiles of 224 on 76 pairs: 125 and 150 us.  4096 tokens, 4096
-// -> 4096: 73.4.
+// before either (the clock falls to about 1500 MHz).  8192 tokens, 4096 -> 14336: 472 us in
+// short runs (2.04 PFLOP/s; a plain library product 465), with gate and stored Z 533, and
+// 616 to 624 without a pause, where the sustained library rate would take 563 without an
+// epilogue.  2000 tokens, 14336 -> 4096, 152 tiles of 224 on 76 pairs: 125 and 150 us.  4096
+// tokens, 4096 -> 4096: 73.4.
+// With Y in fp32 the sums of 512 elements each come out of tensor memory and are added in
+// the epilogue's registers (see kLinearChunk), 96 a thread, so that a tile has at most 192
+// outputs: 8192 tokens, 4096 -> 14336, 578 us (one sum throughout: 500 in the library, 1.6
+// 10^-5 off after 14336 elements in place of 4.8 10^-7); 4096 tokens, 4096 -> 4096, 91.7.
+// Without spills: with 40 words of them 110.
 // Measured and dropped: outputs through shared memory and TMA (605 us with the gate, on
 // five stages, where registers and seven stages took 550), pairs that split a reduction
 // over a cluster (256 tokens, 4096 -> 4096, 16.4 us, on single CTAs 14.3), 512 tokens a
@@ -95,11 +100,12 @@ __device__ __forceinline__ void store32(void* p, bool wide, bool second, uint4 x
     if (second) reinterpret_cast<uint4*>(p)[1] = y;
   }
 }
+template <int FROM = 0, int TO = 4>   // eights of the 32 columns
 __device__ __forceinline__ void ask(const LinearArgs& a, int row, int col, int lane, Ahead& in) {
   if (row < a.m) {
     const int64_t at = static_cast<int64_t>(row) * a.n + col;
 #pragma unroll
-    for (int c = 0; c < 4; c += 2) {
+    for (int c = FROM; c < TO; c += 2) {
       if (col + 8 * c >= a.n) break;
       const bool second = col + 8 * c + 8 < a.n;
       if (a.e.residual)
@@ -113,7 +119,7 @@ __device__ __forceinline__ void ask(const LinearArgs& a, int row, int col, int l
                   : static_cast<const float*>(a.e.bias)[col + lane];
 }
 // The epilogue of 16 columns, from the c-th eight of the 32 on, and their stores.
-template <int ACT>
+template <int ACT, bool F32>
 __device__ __forceinline__ void finish16(float (&v)[2][8], const LinearArgs& a, const Ahead& in,
                                          int c, int row, int col, uint64_t offset) {
   uint4 z[2];
@@ -130,7 +136,7 @@ __device__ __forceinline__ void finish16(float (&v)[2][8], const LinearArgs& a, 
     const bool second = col + 8 < a.n, wide = a.wide && second;
     const int64_t at = static_cast<int64_t>(row) * a.n + col;
     if (a.e.z) store32(a.e.z + at, wide, second, z[0], z[1]);
-    if (a.e.y_fp32) {
+    if constexpr (F32) {
       float* y = static_cast<float*>(a.e.y) + at;
 #pragma unroll
       for (int i = 0; i < 2; ++i)
@@ -147,7 +153,9 @@ __device__ __forceinline__ void finish16(float (&v)[2][8], const LinearArgs& a, 
   __syncwarp();
 }
 
-template <int ACT>
+// F32: Y in fp32, whose sums are added up in registers a few steps at a time (see
+// kLinearChunk).
+template <int ACT, bool F32>
 __global__ void __launch_bounds__(kThreadsL, 1)
     gemm_linear_kernel(const __grid_constant__ LinearArgs a) {
   using T = SmemL;
@@ -263,28 +271,33 @@ __global__ void __launch_bounds__(kThreadsL, 1)
       uint32_t s = 0, ph = 0, buf = 0, bph = 1;
       bool ok = true;
       for (int t = unit0; ok && t < a.num_tiles; t += units) {
-        ok = __all_sync(0xffffffffu, wait_bounded(bar_tempty(buf), bph, wc, kSiteMmaTmemEmpty));
-        if (!ok) break;
-        tc_fence_after_sync();
-        const uint32_t d = tmem_base + buf * 256;
+        const int chunk = F32 ? a.chunk : a.num_kb;
 #pragma unroll 1
-        for (int k = 0; k < a.num_kb; ++k) {
-          ok = __all_sync(0xffffffffu, wait_bounded(bar_full(s), ph, wc, kSiteMmaFull));
+        for (int k0 = 0; ok && k0 < a.num_kb; k0 += chunk) {
+          ok = __all_sync(0xffffffffu, wait_bounded(bar_tempty(buf), bph, wc, kSiteMmaTmemEmpty));
           if (!ok) break;
           tc_fence_after_sync();
-          const uint64_t ad = ad0 + s * (T::STAGE_BYTES >> 4);
-          const uint64_t bd = bd0 + s * (T::STAGE_BYTES >> 4);
-          if (issue) {
+          const uint32_t d = tmem_base + buf * 256;
+          const int k1 = min(a.num_kb, k0 + chunk);
+#pragma unroll 1
+          for (int k = k0; k < k1; ++k) {
+            ok = __all_sync(0xffffffffu, wait_bounded(bar_full(s), ph, wc, kSiteMmaFull));
+            if (!ok) break;
+            tc_fence_after_sync();
+            const uint64_t ad = ad0 + s * (T::STAGE_BYTES >> 4);
+            const uint64_t bd = bd0 + s * (T::STAGE_BYTES >> 4);
+            if (issue) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)   // 16 of K: 32 bytes
-              umma_bf16_pair(d, ad + 2 * kk, bd + 2 * kk, idesc, (k | kk) != 0);
-            umma_commit_pair_mc(bar_empty(s), 0x3);
+              for (int kk = 0; kk < 4; ++kk)   // 16 of K: 32 bytes
+                umma_bf16_pair(d, ad + 2 * kk, bd + 2 * kk, idesc, ((k - k0) | kk) != 0);
+              umma_commit_pair_mc(bar_empty(s), 0x3);
+            }
+            if (++s == T::STAGES) { s = 0; ph ^= 1u; }
           }
-          if (++s == T::STAGES) { s = 0; ph ^= 1u; }
+          if (!ok) break;
+          if (issue) umma_commit_pair_mc(bar_tfull(buf), 0x3);
+          if (++buf == 2) { buf = 0; bph ^= 1u; }
         }
-        if (!ok) break;
-        if (issue) umma_commit_pair_mc(bar_tfull(buf), 0x3);
-        if (++buf == 2) { buf = 0; bph ^= 1u; }
       }
       // every MMA issued must complete before the tensor memory is freed
       if (issue) umma_commit_pair_mc(bar_drain, 0x1);
@@ -303,52 +316,102 @@ __global__ void __launch_bounds__(kThreadsL, 1)
     };
     uint32_t buf = 0, bph = 0;
     bool ok = true;
-    {
-      int row0, col;
-      if (unit0 < a.num_tiles) {
-        place(unit0, 0, row0, col);
-        ask(a, row0 + lane, col, lane, in);
-      }
-    }
-    for (int t = unit0; ok && t < a.num_tiles; t += units) {
-      ok = __all_sync(0xffffffffu,
-                      wait_bounded_inline(bar_tfull(buf), bph, wc, kSiteEpiTmemFull));
-      if (!ok) break;
-      tc_fence_after_sync();
-#pragma unroll 1
-      for (int b = 0; b < boxes; ++b) {
-        int row0, col;
-        place(t, b, row0, col);
-        const bool there = row0 < a.m && col < a.n;   // the same in all lanes
-        uint32_t r[32];
-        tmem_ld_x32(tmem_base + lane_addr + buf * 256 + (box0 + b) * 32, r);
-        const Ahead now = in;
-        {   // the next box's inputs
-          const bool wrap = b + 1 == boxes;
-          const int nt = wrap ? t + units : t;
-          int nrow, ncol;
-          if (nt < a.num_tiles) {
-            place(nt, wrap ? 0 : b + 1, nrow, ncol);
-            ask(a, nrow + lane, ncol, lane, in);
-          }
+    if constexpr (F32) {
+      constexpr int PARTS = kMaxLinearF32 / 32;   // of 16 columns, a warp's at most
+      for (int t = unit0; ok && t < a.num_tiles; t += units) {
+        float sum[PARTS][16];
+#pragma unroll
+        for (int p = 0; p < PARTS; ++p) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) sum[p][i] = 0.0f;
         }
-        tmem_ld_wait();
-        if (b == boxes - 1) {   // this warp has read its part of the accumulator
+#pragma unroll 1
+        for (int k0 = 0; k0 < a.num_kb; k0 += a.chunk) {
+          ok = __all_sync(0xffffffffu,
+                          wait_bounded_inline(bar_tfull(buf), bph, wc, kSiteEpiTmemFull));
+          if (!ok) break;
+          tc_fence_after_sync();
+#pragma unroll
+          for (int p = 0; p < PARTS; ++p) {
+            if (p >= 2 * boxes) break;
+            uint32_t r[16];
+            tmem_ld_x16(tmem_base + lane_addr + buf * 256 + box0 * 32 + 16 * p, r);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) sum[p][i] += __uint_as_float(r[i]);
+          }
           tc_fence_before_sync();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(bar_tempty(buf), 0));
+          if (++buf == 2) { buf = 0; bph ^= 1u; }
         }
-        if (!there) continue;
-#pragma unroll
-        for (int c = 0; c < 4; c += 2) {
+        if (!ok) break;
+        int row0, col;
+        place(t, 0, row0, col);
+        if (row0 >= a.m) continue;   // the same in all lanes, as the next
+#pragma unroll 1
+        for (int p = 0; p < 2 * boxes && col + 16 * p < a.n; ++p) {
+          Ahead now;
+          ask<0, 2>(a, row0 + lane, col + 16 * p, lane, now);
           float v[2][8];
 #pragma unroll
-          for (int k = 0; k < 16; ++k) v[k / 8][k % 8] = __uint_as_float(r[8 * c + k]);
-          finish16<ACT>(v, a, now, c, row0 + lane, col + 8 * c, offset);
+          for (int k = 0; k < 16; ++k) {   // (by selection: one epilogue in the code)
+            float x = sum[0][k];
+#pragma unroll
+            for (int o = 1; o < PARTS; ++o) x = p == o ? sum[o][k] : x;
+            v[k / 8][k % 8] = x;
+          }
+          finish16<ACT, true>(v, a, now, 0, row0 + lane, col + 16 * p, offset);
         }
       }
-      if (!ok) break;
-      if (++buf == 2) { buf = 0; bph ^= 1u; }
+    } else {
+      {
+        int row0, col;
+        if (unit0 < a.num_tiles) {
+          place(unit0, 0, row0, col);
+          ask(a, row0 + lane, col, lane, in);
+        }
+      }
+      for (int t = unit0; ok && t < a.num_tiles; t += units) {
+        ok = __all_sync(0xffffffffu,
+                        wait_bounded_inline(bar_tfull(buf), bph, wc, kSiteEpiTmemFull));
+        if (!ok) break;
+        tc_fence_after_sync();
+#pragma unroll 1
+        for (int b = 0; b < boxes; ++b) {
+          int row0, col;
+          place(t, b, row0, col);
+          const bool there = row0 < a.m && col < a.n;   // the same in all lanes
+          uint32_t r[32];
+          tmem_ld_x32(tmem_base + lane_addr + buf * 256 + (box0 + b) * 32, r);
+          const Ahead now = in;
+          {   // the next box's inputs
+            const bool wrap = b + 1 == boxes;
+            const int nt = wrap ? t + units : t;
+            int nrow, ncol;
+            if (nt < a.num_tiles) {
+              place(nt, wrap ? 0 : b + 1, nrow, ncol);
+              ask(a, nrow + lane, ncol, lane, in);
+            }
+          }
+          tmem_ld_wait();
+          if (b == boxes - 1) {   // this warp has read its part of the accumulator
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(bar_tempty(buf), 0));
+          }
+          if (!there) continue;
+#pragma unroll
+          for (int c = 0; c < 4; c += 2) {
+            float v[2][8];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) v[k / 8][k % 8] = __uint_as_float(r[8 * c + k]);
+            finish16<ACT, false>(v, a, now, c, row0 + lane, col + 8 * c, offset);
+          }
+        }
+        if (!ok) break;
+        if (++buf == 2) { buf = 0; bph ^= 1u; }
+      }
     }
     __syncwarp();
   }
@@ -369,11 +432,11 @@ __global__ void __launch_bounds__(kThreadsL, 1)
 }
 
 // The pairs that can be resident at once.
-template <int ACT>
+template <int ACT, bool F32>
 cudaError_t resident(int num_sms, int* n) {
   static PerDevice kept;
   return kept.get(n, [&](int* v) {
-    cudaError_t r = cudaFuncSetAttribute(gemm_linear_kernel<ACT>,
+    cudaError_t r = cudaFuncSetAttribute(gemm_linear_kernel<ACT, F32>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, SmemL::ALLOC);
     if (r != cudaSuccess) return r;
     cudaLaunchConfig_t lc = {};
@@ -387,20 +450,26 @@ cudaError_t resident(int num_sms, int* n) {
     attr[0].val.clusterDim.z = 1;
     lc.attrs = attr;
     lc.numAttrs = 1;
-    r = cudaOccupancyMaxActiveClusters(v, gemm_linear_kernel<ACT>, &lc);
+    r = cudaOccupancyMaxActiveClusters(v, gemm_linear_kernel<ACT, F32>, &lc);
     if (r == cudaSuccess && *v <= 0) r = cudaErrorInvalidConfiguration;
     *v = *v < num_sms / 2 ? *v : num_sms / 2;
     return r;
   });
 }
 
+template <int ACT, bool F32>
+cudaError_t launch_t(const LinearArgs& a, int num_sms, cudaStream_t stream) {
+  int units = 0;
+  const cudaError_t e = resident<ACT, F32>(num_sms, &units);
+  if (e != cudaSuccess) return e;
+  return launch_chained(gemm_linear_kernel<ACT, F32>,
+                        2 * (a.num_tiles < units ? a.num_tiles : units), kThreadsL, SmemL::ALLOC, 2,
+                        stream, a);
+}
 template <int ACT>
 cudaError_t launch_act(const LinearArgs& a, int num_sms, cudaStream_t stream) {
-  int units = 0;
-  const cudaError_t e = resident<ACT>(num_sms, &units);
-  if (e != cudaSuccess) return e;
-  return launch_chained(gemm_linear_kernel<ACT>, 2 * (a.num_tiles < units ? a.num_tiles : units),
-                        kThreadsL, SmemL::ALLOC, 2, stream, a);
+  return a.e.y_fp32 ? launch_t<ACT, true>(a, num_sms, stream)
+                    : launch_t<ACT, false>(a, num_sms, stream);
 }
 
 }  // namespace

@@ -42,11 +42,11 @@ struct FewL {
   // more than one CTA for each, as many as fit.
   static constexpr int STAGES = NT <= 16 ? 6 : (NT == 32 ? 5 : 4);
   static constexpr int DEEP = NT <= 16 ? 12 : (NT == 32 ? 11 : (NT == 64 ? 9 : 7));
-  static constexpr int TMEM_COLS = NT < 32 ? 32 : NT;
+  static constexpr int ACC_COLS = NT < 32 ? 32 : NT;
   // Shared memory from a 1024-aligned base: barriers (the most there can be), abort
   // flag, stages.  The shares, one tile of fp32 sums, take the stages' place once the
   // products of all the cluster's CTAs have run.
-  static constexpr int NUM_BARS = 2 * DEEP + 1;
+  static constexpr int NUM_BARS = 2 * DEEP + 5;
   static constexpr int OFF_TMEM = 8 * NUM_BARS;
   static constexpr int OFF_STAGES = 1024;
   static constexpr int smem(int stages) { return OFF_STAGES + stages * STAGE_BYTES + 1024; }
@@ -56,10 +56,14 @@ struct FewL {
   static_assert(smem(DEEP) <= 232448, "shared memory budget");
 };
 
-template <int NT>
+// F32: Y in fp32, whose sums are added up in registers a few steps at a time (see
+// kLinearChunk), from two accumulators in turn.  (128 tokens, 4096 -> 14336, 25.1 us as
+// 24.3 in one sum.  A kernel of its own: as a loop of one turn it cost Y in bf16 3 to 6 %.)
+template <int NT, bool F32>
 __global__ void __launch_bounds__(FewL<NT>::THREADS, NT <= 64 ? 2 : 1)
     gemm_linear_few_kernel(const __grid_constant__ LinearArgs a) {
   using T = FewL<NT>;
+  constexpr int TMEM_COLS = (F32 ? 2 : 1) * T::ACC_COLS;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   // the same offset in every CTA of the cluster: remote stores use it
@@ -80,6 +84,8 @@ __global__ void __launch_bounds__(FewL<NT>::THREADS, NT <= 64 ? 2 : 1)
   auto bar_full = [&](int s) { return bars + 8u * s; };
   auto bar_empty = [&](int s) { return bars + 8u * (T::DEEP + s); };
   const uint32_t bar_done = bars + 8u * (2 * T::DEEP);   // all products have run
+  auto bar_acc = [&](int b) { return bars + 8u * (2 * T::DEEP + 1 + b); };    // an accumulator's
+  auto bar_free = [&](int b) { return bars + 8u * (2 * T::DEEP + 3 + b); };   // has been read
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(gbase + T::OFF_TMEM + 4);
   const WaitCtx wc{abort_flag, a.err, a.err_site, a.timeout_ns};
   // A weight that is read once passes through L2 as the first to leave it (one token,
@@ -90,13 +96,14 @@ __global__ void __launch_bounds__(FewL<NT>::THREADS, NT <= 64 ? 2 : 1)
   // Warp 0 sets up the barriers while warp 1 takes the tensor memory; one block
   // barrier covers both.
   if (warp == 0) {
-    for (int i = lane; i < T::NUM_BARS; i += 32) mbar_init(bars + 8u * i, 1);
+    for (int i = lane; i < T::NUM_BARS; i += 32)
+      mbar_init(bars + 8u * i, i >= 2 * T::DEEP + 3 ? T::EPI : 1);
     if (lane == 0) *abort_flag = 0u;
     fence_mbarrier_init();
     __syncwarp();
     if (lane == 0) drop_first_arrival(a.drop_first_arrival, bar_full(0));
   } else if (warp == 1) {
-    tmem_alloc(base + T::OFF_TMEM, T::TMEM_COLS);
+    tmem_alloc(base + T::OFF_TMEM, TMEM_COLS);
     tmem_relinquish();
     tc_fence_before_sync();
   }
@@ -159,19 +166,32 @@ __global__ void __launch_bounds__(FewL<NT>::THREADS, NT <= 64 ? 2 : 1)
     const uint64_t ad0 = make_sdesc_k_sw128(stage0, 1024);
     const uint64_t bd0 = make_sdesc_k_sw128(stage0 + T::A_BYTES, 1024);
     const bool issue = elect_one();
-    uint32_t s = 0, ph = 0;
+    uint32_t s = 0, ph = 0, buf = 0, bph = 1;
+    for (int k0 = kb, k1; k0 < ke; k0 = k1) {
+      k1 = F32 ? min(ke, k0 + a.chunk) : ke;
+      if (F32 && !__all_sync(0xffffffffu, wait_bounded(bar_free(buf), bph, wc, kSiteMmaTmemEmpty)))
+        break;
+      if (F32) tc_fence_after_sync();
+      bool ok = true;
 #pragma unroll 1
-    for (int k = kb; k < ke; ++k) {
-      if (!__all_sync(0xffffffffu, wait_bounded(bar_full(s), ph, wc, kSiteMmaFull))) break;
-      tc_fence_after_sync();
-      const uint64_t ad = ad0 + s * (T::STAGE_BYTES >> 4), bd = bd0 + s * (T::STAGE_BYTES >> 4);
-      if (issue) {
+      for (int k = k0; k < k1; ++k) {
+        ok = __all_sync(0xffffffffu, wait_bounded(bar_full(s), ph, wc, kSiteMmaFull));
+        if (!ok) break;
+        tc_fence_after_sync();
+        const uint64_t ad = ad0 + s * (T::STAGE_BYTES >> 4), bd = bd0 + s * (T::STAGE_BYTES >> 4);
+        if (issue) {
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          umma_bf16(tmem_base, ad + 2 * kk, bd + 2 * kk, idesc, (k - kb) | kk);
-        umma_commit(bar_empty(s));
+          for (int kk = 0; kk < 4; ++kk)
+            umma_bf16(tmem_base + buf * T::ACC_COLS, ad + 2 * kk, bd + 2 * kk, idesc, (k - k0) | kk);
+          umma_commit(bar_empty(s));
+        }
+        if (++s == stages) { s = 0; ph ^= 1u; }
       }
-      if (++s == stages) { s = 0; ph ^= 1u; }
+      if (!ok) break;
+      if (F32) {
+        if (issue) umma_commit(bar_acc(buf));
+        if (++buf == 2) { buf = 0; bph ^= 1u; }
+      }
     }
     if (issue) umma_commit(bar_done);
     wait_bounded(bar_done, 0u, wc, kSiteDrainMma, false);
@@ -179,20 +199,33 @@ __global__ void __launch_bounds__(FewL<NT>::THREADS, NT <= 64 ? 2 : 1)
   } else if (warp >= 4) {
     const int q = warp & 3, h = (warp - 4) >> 2;
     const uint32_t tcol = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + h * T::NC;
-    const bool ok = __all_sync(0xffffffffu, wait_bounded(bar_done, 0u, wc, kSiteEpiTmemFull));
-    if (ok && ke > kb) {   // (a CTA without steps adds nothing)
+    auto sums = [&](uint32_t from, auto&& take) {   // take(i, the i-th token's)
       tc_fence_after_sync();
 #pragma unroll
       for (int c = 0; c < T::NC / 16; ++c) {
         uint32_t r[16];
-        tmem_ld_x16(tcol + 16 * c, r);
+        tmem_ld_x16(from + 16 * c, r);
         tmem_ld_wait();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) acc[16 * c + i] = __uint_as_float(r[i]);
+        for (int i = 0; i < 16; ++i) take(16 * c + i, __uint_as_float(r[i]));
       }
-    } else {
+    };
 #pragma unroll
-      for (int i = 0; i < T::NC; ++i) acc[i] = 0.0f;
+    for (int i = 0; i < T::NC; ++i) acc[i] = 0.0f;   // (a CTA without steps adds nothing)
+    if constexpr (F32) {
+      uint32_t buf = 0, bph = 0;
+#pragma unroll 1
+      for (int k0 = kb; k0 < ke; k0 += a.chunk) {
+        if (!__all_sync(0xffffffffu, wait_bounded(bar_acc(buf), bph, wc, kSiteEpiTmemFull))) break;
+        sums(tcol + buf * T::ACC_COLS, [&](int i, float v) { acc[i] += v; });
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_free(buf));
+        if (++buf == 2) { buf = 0; bph ^= 1u; }
+      }
+    } else if (__all_sync(0xffffffffu, wait_bounded(bar_done, 0u, wc, kSiteEpiTmemFull)) &&
+               ke > kb) {
+      sums(tcol, [&](int i, float v) { acc[i] = v; });
     }
   }
   tc_fence_before_sync();
@@ -247,7 +280,7 @@ __global__ void __launch_bounds__(FewL<NT>::THREADS, NT <= 64 ? 2 : 1)
         z = epilogue8<decltype(act)::value>(v, a.e, mul0, res0, offset, static_cast<uint64_t>(at));
       });
       if (a.e.z) reinterpret_cast<uint4*>(a.e.z)[at] = z;
-      if (a.e.y_fp32) {
+      if constexpr (F32) {
         float4* y = reinterpret_cast<float4*>(a.e.y) + 2 * at;
         y[0] = make_float4(v[0], v[1], v[2], v[3]);
         y[1] = make_float4(v[4], v[5], v[6], v[7]);
@@ -258,16 +291,16 @@ __global__ void __launch_bounds__(FewL<NT>::THREADS, NT <= 64 ? 2 : 1)
   }
   if (warp == 1) {
     tc_fence_after_sync();
-    tmem_dealloc(tmem_base, T::TMEM_COLS);
+    tmem_dealloc(tmem_base, TMEM_COLS);
   }
 }
 
 // The clusters of `splits` CTAs that can be resident at once with as many stages as fit.
-template <int NT>
+template <int NT, bool F32>
 cudaError_t resident(int splits, int num_sms, int* n) {
   using T = FewL<NT>;
   static PerDevice kept[4];
-  auto kern = gemm_linear_few_kernel<NT>;
+  auto kern = gemm_linear_few_kernel<NT, F32>;
   return kept[splits == 1 ? 0 : (splits == 2 ? 1 : (splits == 4 ? 2 : 3))].get(n, [&](int* v) {
     cudaError_t r =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
@@ -290,39 +323,44 @@ cudaError_t resident(int splits, int num_sms, int* n) {
   });
 }
 
-template <int NT>
+template <int NT, bool F32>
 cudaError_t launch_t(LinearArgs a, int num_sms, cudaStream_t stream) {
   using T = FewL<NT>;
   int clusters = 0;
-  const cudaError_t e = resident<NT>(a.splits, num_sms, &clusters);
+  const cudaError_t e = resident<NT, F32>(a.splits, num_sms, &clusters);
   if (e != cudaSuccess) return e;
   const int steps = (a.num_kb + a.splits - 1) / a.splits;
   a.stages = a.num_tiles <= clusters ? T::DEEP : T::STAGES;
   if (steps < a.stages) a.stages = steps < 2 ? 2 : steps;
   // (the shares take the stages' place)
   while (a.stages * T::STAGE_BYTES < NT * kBM * 4) ++a.stages;
-  return launch_chained(gemm_linear_few_kernel<NT>, a.num_tiles * a.splits, T::THREADS,
+  return launch_chained(gemm_linear_few_kernel<NT, F32>, a.num_tiles * a.splits, T::THREADS,
                         T::smem(a.stages), a.splits > 1 ? a.splits : 0, stream, a);
+}
+
+template <int NT>
+cudaError_t launch_nt(const LinearArgs& a, int num_sms, cudaStream_t stream) {
+  return a.e.y_fp32 ? launch_t<NT, true>(a, num_sms, stream) : launch_t<NT, false>(a, num_sms, stream);
 }
 
 }  // namespace
 
 cudaError_t linear_few_clusters(int nt, int splits, int num_sms, int* n) {
   switch (nt) {
-    case 16: return resident<16>(splits, num_sms, n);
-    case 32: return resident<32>(splits, num_sms, n);
-    case 64: return resident<64>(splits, num_sms, n);
-    case 128: return resident<128>(splits, num_sms, n);
+    case 16: return resident<16, false>(splits, num_sms, n);
+    case 32: return resident<32, false>(splits, num_sms, n);
+    case 64: return resident<64, false>(splits, num_sms, n);
+    case 128: return resident<128, false>(splits, num_sms, n);
   }
   return cudaErrorInvalidValue;
 }
 
 cudaError_t launch_gemm_linear_few(int nt, const LinearArgs& a, int num_sms, cudaStream_t stream) {
   switch (nt) {
-    case 16: return launch_t<16>(a, num_sms, stream);
-    case 32: return launch_t<32>(a, num_sms, stream);
-    case 64: return launch_t<64>(a, num_sms, stream);
-    case 128: return launch_t<128>(a, num_sms, stream);
+    case 16: return launch_nt<16>(a, num_sms, stream);
+    case 32: return launch_nt<32>(a, num_sms, stream);
+    case 64: return launch_nt<64>(a, num_sms, stream);
+    case 128: return launch_nt<128>(a, num_sms, stream);
   }
   return cudaErrorInvalidValue;
 }

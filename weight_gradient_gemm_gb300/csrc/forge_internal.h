@@ -332,10 +332,18 @@ struct EpiArgs {
 };
 
 // The 16-bit product of a linear layer (forge_gemm_linear.cu).
+// The tensor core cuts its fp32 sums off at every product instead of rounding them, so a sum
+// falls short by about 10^-9 of itself for every element of the reduction (measured: 4.4
+// 10^-6 after 4096), as much as fp32 addition in any order loses after some 10^5.  A bf16
+// output does not show it; for an fp32 one the tensor core adds up this many steps of 64
+// and their sums are added in registers (512 elements: 4.7 10^-7, however many follow).
+constexpr int kLinearChunk = 8;
+constexpr int kMaxLinearF32 = 192;   // outputs of a pair's tile whose sums are in registers
 struct LinearArgs {
   CUtensorMap a, b;         // operands: tokens and weight
   EpiArgs e;
   int32_t m, n, num_kb;     // tokens, outputs, 64-deep steps of the reduction
+  int32_t chunk;            // steps that the tensor core adds up by itself (kLinearChunk)
   int32_t tiles_m, tiles_n, num_tiles, group_m;
   int32_t bn;               // outputs of a pair's tile: a multiple of 32, at most 256
   int32_t splits;           // single CTAs: those of a cluster, which share a tile's reduction

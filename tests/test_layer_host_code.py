@@ -102,7 +102,8 @@ int main() {
 
 def test_product_shapes_take_their_forms(tmp_path):
     # on 152 SMs: single CTAs for few tokens and small outputs, with every split there is,
-    # and pairs of every width; a split has two steps a CTA at least, all resident at once
+    # and pairs of every width; a split has two steps a CTA at least, all resident at once;
+    # more tiles of 65 to 128 tokens than SMs are pairs'
     out = run(tmp_path, "#include <cstdio>\n" + API + r"""
 int main() {
   const forge_tuning automatic = {FORGE_PROFILE_AUTO, 0, 0, 0, -1, 0, -1, -1};
@@ -118,8 +119,17 @@ int main() {
           int i = 0;
           while (1 << i < c.splits) ++i;
           if (c.splits > 1 && (kb < 2 * c.splits || tiles > clusters[i])) return 2;
-        } else if (m <= 128 || c.bn % 32 || c.bn < 64 || c.bn > 256 || c.splits != 1) {
+          if (m > 64 && m <= 128 && tiles > 152) return 4;
+        } else if ((m <= 128 && (m <= 64 || tiles <= 152)) || c.bn % 32 || c.bn < 64 ||
+                   c.bn > 256 || c.splits != 1) {
           return 3;
+        }
+        for (int bn : {0, 64, 256}) {   // a limit on the width holds whatever is asked for
+          forge_tuning asked = automatic;
+          asked.cta_group = 2;
+          asked.bn = bn;
+          const LinearConfig w = choose_linear(m, n, kb, asked, 152, clusters, 192);
+          if (w.few || w.bn > 192 || (bn && w.bn != (bn < 192 ? bn : 192))) return 5;
         }
         std::printf("%d %d %d\n", c.few, c.bn, c.splits);
       }

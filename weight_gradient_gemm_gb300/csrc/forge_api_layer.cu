@@ -95,7 +95,7 @@ Span counter_span(const DropArgs& d) { return Span{d.counter, 8}; }
 // 38.6 us and 52.7, -> 57344 81.7 and 91.4, -> 131072 173 and 221); up to 64, two an SM do
 // (64 tokens, -> 57344, 78.9 us and 80.7).
 LinearConfig choose_linear(int64_t m, int64_t n, int64_t num_kb, const forge_tuning& tune,
-                           int num_sms, const int (&clusters)[4], int most_bn) {
+                           int num_sms, const int (&clusters)[4], int most_bn = 256) {
   const int nt = m <= 16 ? 16 : (m <= 32 ? 32 : (m <= 64 ? 64 : 128));
   const int64_t tiles = (n + 127) / 128 * ((m + 127) / 128);
   LinearConfig best{nt, 128, 1};

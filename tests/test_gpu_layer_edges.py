@@ -314,6 +314,30 @@ def test_linear_waits_run_out(bt, d_in, d_out, how, tune):
     assert torch.equal(Y, want[0]) and torch.equal(Z, want[1])
 
 
+@pytest.mark.parametrize("bt,d_in,d_out,how", [
+    (3, 4104, 264, {}), (100, 1032, 520, dict(splits=1)), (300, 4104, 520, dict(cg=1, splits=2)),
+    (700, 1032, 2056, dict(cg=2)), (40, 1032, 20000, {})])
+def test_linear_waits_run_out_with_fp32_outputs(bt, d_in, d_out, how, tune):
+    tune(**how)
+    Y, ye = fenced(bt, d_out, torch.float32)
+    c = linear_case(bt, d_in, d_out, act=R.SILU, residual=True, out=torch.float32)
+    c["Y"] = Y
+    call_linear(c)
+    want = Y.clone()
+    F.set_wait_limit_ns(20_000_000)
+    try:
+        F.debug_drop_first_arrival(True)
+        F.linear_bf16(c["X"], c["W"], Y, act=c["act"], residual=c["residual"])
+        assert F.device_error() == TIMEOUT
+        assert F.device_error() == 0      # cleared
+    finally:
+        F.debug_drop_first_arrival(False)
+        F.set_wait_limit_ns(2_000_000_000)
+    untouched(ye)
+    call_linear(c)
+    assert torch.equal(Y, want)
+
+
 def test_python_refusals():
     x, w, y = rand(1, (4, 256)), rand(2, (8, 256)), torch.empty((4, 8), dtype=torch.bfloat16, device=DEV)
     with pytest.raises(ValueError):

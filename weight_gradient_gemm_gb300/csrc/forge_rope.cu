@@ -28,8 +28,8 @@
 // Measured and dropped: fp32 arithmetic one value at a time (it trades the packed forms'
 // moves for twice the operations: backward pass 49.6 us), four elements a vector (62),
 // a block a few tokens without a walk (31.0 rotated, 13.1 for the norm of 1999 tokens), and
-// asking for the next token's or the one after's rows in L2 ahead (rotated 28.9 to 30.5,
-// norm 31.9 to 30.1, its backward pass 48.4 to 52.3: the instructions cost what the wait is).
+// asking for the next token's rows in L2 ahead (rotated 29.0 to 29.4, norm 31.9 to 31.3 and
+// of 1999 tokens 10.4 to 10.6, its backward pass 48.4 to 52.3).
 #include <cuda_bf16.h>
 
 #include "forge_e4m3.cuh"

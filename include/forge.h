@@ -876,7 +876,8 @@ typedef struct {
                       for forge_linear_bf16 1: 128 outputs and up to 128 tokens on
                       one CTA, 2: pairs with 256 tokens                          */
   int bn;          /* 0 automatic; 128 or 256: accumulator width on one CTA
-                      (forge_linear_bf16: outputs of a pair's tile)              */
+                      (forge_linear_bf16: outputs of a pair's tile; with Y in
+                      fp32 at most 192)                                          */
   int group_m;     /* 0 automatic; 1..64 tile rows per raster group             */
   int poll_store;  /* -1 automatic; 0 or 1: store lanes poll for finished slots */
   int splits;      /* 0 automatic; 1..8 k-ranges per tile for forge_dgrad; for

@@ -77,10 +77,11 @@ struct Words {
     if constexpr (VEC == 8) return make_uint4(w[0], w[1], w[2], w[3]);
     else return make_uint2(w[0], w[1]);
   }
-  static __device__ __forceinline__ V zero() {
-    if constexpr (VEC == 8) return make_uint4(0, 0, 0, 0);
-    else return make_uint2(0, 0);
+  static __device__ __forceinline__ V all(uint32_t v) {
+    if constexpr (VEC == 8) return make_uint4(v, v, v, v);
+    else return make_uint2(v, v);
   }
+  static __device__ __forceinline__ V zero() { return all(0u); }
 };
 
 // What a lane's two vectors are: their first elements in the head, whether they exist
@@ -274,7 +275,9 @@ __global__ void __launch_bounds__(256, kBlocks)
       }
     } else {
       const bool in = more && head0 + load_step * groups < end;
-      xa[j] = xb[j] = Words<VEC>::zero();
+      // Backward, an absent head is of ones with gradients of zero: finite whatever eps is
+      // (zeros with eps = 0 are not), so that it adds nothing to the gain's gradient.
+      xa[j] = xb[j] = Words<VEC>::all(kBwd && !in ? 0x3F803F80u : 0u);
       if (in && p.has_a) xa[j] = __ldcs(reinterpret_cast<const V*>(x));
       if (in && p.has_b) xb[j] = __ldcs(reinterpret_cast<const V*>(x + ab));
       if constexpr (kBwd) {

@@ -1,5 +1,5 @@
-"""The norm of queries and keys with eps = 0, against the fp64 definitions: a head count that
-leaves lanes without a head must not reach the gains' gradients."""
+"""Heads where the other tests do not go, against the fp64 definitions: eps = 0 with head counts
+that leave lanes without a head, and queries, keys and values side by side within a head."""
 import numpy as np
 import pytest
 import torch
@@ -54,3 +54,28 @@ def test_without_eps(tokens, hq, hk, dim, rot, layout):
         within(f64(gotx), dx64, BF * np.abs(dx64) + 1.01 * noise)
         adds = min(tokens * x.shape[1], 200) + 100
         within(f64(gotg), dg64, ((terr + rel + adds * U) * d * xh).sum((0, 1)) + 1e-30)
+
+
+@pytest.mark.parametrize("tokens", [1, 37])
+def test_queries_keys_and_values_of_a_head_side_by_side(tokens):
+    """[tokens, heads, 3, dim]: in place on the views is as apart; the values stay."""
+    h, dim = 5, 64
+    qkv, grad = rand(81, (tokens, h, 3, dim)), rand(82, (tokens, h, 3, dim))
+    freqs, _ = F.rope_frequencies(dim, 10000.0)
+    gains = [1 + rand(83 + i, (dim,), 0.2, torch.float32) for i in range(2)]
+    ws = torch.empty(F.qk_norm_rope_backward_workspace_bytes(dim), dtype=torch.uint8, device=DEV)
+    dg = torch.empty(4, dim, device=DEV)
+    calls = [lambda x, d, g: F.rope(*x, freqs),
+             lambda x, d, g: F.qk_norm_rope(*x, *gains, freqs, eps=1e-5),
+             lambda x, d, g: F.qk_norm_rope_backward(*d, *x, *gains, freqs, eps=1e-5, dq_gain=g[0],
+                                                     dk_gain=g[1], workspace=ws)]
+    for call in calls:
+        views = qkv.clone(), grad.clone()
+        call(*[(t[:, :, 0], t[:, :, 1]) for t in views], dg[:2])
+        apart = [[t[:, :, i].contiguous() for i in range(2)] for t in (qkv, grad)]
+        call(*apart, dg[2:])
+        ok()
+        for got, want, start in zip(views, apart, (qkv, grad)):
+            assert torch.equal(got[:, :, 0], want[0]) and torch.equal(got[:, :, 1], want[1])
+            assert torch.equal(got[:, :, 2], start[:, :, 2])
+    assert torch.equal(dg[:2], dg[2:])

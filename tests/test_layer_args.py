@@ -210,6 +210,25 @@ def test_qk_norm_rope_backward_refusals(L):
         assert qkb(L, [heads(**base)]) in REACHED, kw
 
 
+def test_heads_side_by_side_within_a_projection(L):
+    # [tokens, heads, 3, dim]: queries, keys and values of a head next to each other
+    row, size = (3 * 3 * 64, 3 * 64), 2 * 64
+    q, k, v = (heads(A + i * size, A + i * size, xs=row) for i in range(3))
+    assert rope(L, [q, k]) in REACHED and rope(L, [k, v]) in REACHED and rope(L, [v, q]) in REACHED
+    assert rope(L, [heads(A, A + size, xs=row), heads(A + 2 * size, B, xs=row, ys=(192, 64))]) in REACHED
+    # [tokens, heads, keys and values, dim] beside queries of another buffer
+    assert rope(L, [heads(B, B), heads(A, A, xs=(2 * 3 * 64, 2 * 64))]) in REACHED
+    # one that reaches into its neighbour, and two in one place
+    assert rope(L, [q, heads(A + size // 2, A + size // 2, xs=row)]) == ALIAS
+    assert rope(L, [q, heads(B, A, xs=row)]) == ALIAS
+    assert rope(L, [q, heads(A + 2 * size + 64, A + 2 * size + 64, xs=row)]) == ALIAS
+    qs = [heads(A + i * size, A + i * size, xs=row, gain=C) for i in range(2)]
+    assert qk(L, qs) in REACHED
+    grads = [heads(A + i * size, D + i * size, xs=row, gain=C, dy=D + i * size, dg=E + 1024 * i)
+             for i in range(2)]
+    assert qkb(L, grads) in REACHED
+
+
 def test_frequencies_refusals(L):
     table, mag = (ctypes.c_uint64 * 128)(), ctypes.c_float()
 

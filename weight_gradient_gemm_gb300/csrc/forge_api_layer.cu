@@ -5,6 +5,7 @@
 #include <cmath>
 #include <cstring>
 #include <initializer_list>
+#include <numeric>
 
 #include "forge.h"
 #include "forge_internal.h"
@@ -334,7 +335,9 @@ forge_status check_view(const View& v, bool output) {
   return FORGE_OK;
 }
 // Whether two views share an element: their bounds meet, and they are not interleaved
-// rows of one buffer (as queries and keys in the projections' fused output are).
+// rows of one buffer (as queries and keys in the projections' fused output are), token by
+// token, head by head or, where all strides are multiples of one step ([tokens, heads, 3,
+// dim]), within that step.
 bool views_meet(const View& a, const View& b) {
   if (!a.p || !b.p || !meet(a.span(), b.span())) return false;
   auto interleaved = [&](int64_t step_a, int64_t step_b, uint64_t row_a, uint64_t row_b) {
@@ -346,7 +349,9 @@ bool views_meet(const View& a, const View& b) {
   };
   const uint64_t ta = (a.heads - 1) * a.head + a.dim, tb = (b.heads - 1) * b.head + b.dim;
   const uint64_t ha = (a.tokens - 1) * a.token + a.dim, hb = (b.tokens - 1) * b.token + b.dim;
-  return !interleaved(a.token, b.token, ta, tb) && !interleaved(a.head, b.head, ha, hb);
+  const int64_t step = std::gcd(std::gcd(a.token, a.head), std::gcd(b.token, b.head));
+  return !interleaved(a.token, b.token, ta, tb) && !interleaved(a.head, b.head, ha, hb) &&
+         !interleaved(step, step, a.dim, b.dim);
 }
 
 struct HeadCall {

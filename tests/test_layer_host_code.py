@@ -142,6 +142,33 @@ int main() {
     assert len({p[1] for p in plans if not p[0]}) >= 4
 
 
+def test_columns_of_the_last_tile_stay_in_32_bits(tmp_path):
+    # outputs are counted in 32-bit numbers: a width of which no whole number of tiles ends at
+    # 2^31 must not be taken where the last tile would reach behind it
+    run(tmp_path, "#include <cstdio>\n" + API + r"""
+int main() {
+  const int clusters[4] = {152, 76, 36, 16};
+  int pairs = 0;
+  for (int64_t m : {1, 16, 100, 128, 300, 40000})
+    for (int64_t less = 8; less <= 512; less += 8)
+      for (int cg : {0, 1, 2})
+        for (int bn : {0, 128, 256})
+          for (int most : {192, 256})
+            for (int64_t kb : {1, 3, 64}) {
+              const forge_tuning tune = {FORGE_PROFILE_AUTO, cg, bn, 0, -1, 0, -1, -1};
+              const int64_t n = (1LL << 31) - less;
+              const LinearConfig c = choose_linear(m, n, kb, tune, 152, clusters, most);
+              if ((n + c.bn - 1) / c.bn * c.bn > 1LL << 31) {
+                std::printf("%lld outputs in tiles of %d\n", static_cast<long long>(n), c.bn);
+                return 1;
+              }
+              pairs += c.few == 0;
+            }
+  return pairs > 1000 ? 0 : 2;
+}
+""", "")
+
+
 @pytest.mark.parametrize("source,call", [
     ("forge_gemm_linear.cu", "forge::LinearArgs a = {}; a.num_tiles = 100; a.e.act = 1; "
      "forge::launch_gemm_linear(a, 152, nullptr);"),

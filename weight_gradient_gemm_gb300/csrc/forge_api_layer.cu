@@ -113,6 +113,8 @@ LinearConfig choose_linear(int64_t m, int64_t n, int64_t num_kb, const forge_tun
   const int64_t pairs = num_sms / 2, tiles_m = (m + 255) / 256;
   for (int bn = most_bn; bn >= 64; bn -= 32) {
     if (tune.bn && bn != (tune.bn < most_bn ? tune.bn : most_bn)) continue;
+    // (a kernel counts columns in 32 bits: the last tile has to end there)
+    if ((n + bn - 1) / bn * bn > kMaxIndex + 1) continue;
     const int64_t waves = (tiles_m * ((n + bn - 1) / bn) + pairs - 1) / pairs;
     const int64_t cost = waves * num_kb * (370 + 5 * bn / 8) + 24 * bn + 1500;
     if (cost < least) least = cost, best = LinearConfig{0, bn, 1};

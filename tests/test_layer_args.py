@@ -266,6 +266,22 @@ def test_frequencies_against_the_definition(scale, dim):
         assert abs(mag - mag64) <= 2.0 ** -24 * mag64
 
 
+@pytest.mark.parametrize("kind,name,high", [(F.ROPE_SCALE_LLAMA3, "llama3", 4.0),
+                                            (F.ROPE_SCALE_YARN, "yarn", 32.0)])
+def test_frequencies_are_mixed_up_to_the_usual_turns(kind, name, high):
+    kw = dict(factor=16.0, context=4096.0)
+    table, mag = F.rope_frequencies(128, 10000.0, scaling=kind, device="cpu", **kw)
+    given, mag2 = F.rope_frequencies(128, 10000.0, scaling=kind, high=high, device="cpu", **kw)
+    assert torch.equal(table, given) and mag == mag2
+    rad, mag64 = R.frequencies(128, 10000.0, name, low=1.0, high=high, **kw)
+    turns = table.numpy().view(np.uint64).astype(np.float64) / 2.0 ** 64
+    # doubles on both sides, as above
+    assert np.abs(turns - rad / (2 * np.pi)).max() <= 2.0 ** -52
+    assert abs(mag - mag64) <= 2.0 ** -24 * mag64
+    other, _ = F.rope_frequencies(128, 10000.0, scaling=kind, high=36.0 - high, device="cpu", **kw)
+    assert not torch.equal(table, other)
+
+
 def test_python_checks_without_a_gpu():
     x = torch.zeros((4, 256), dtype=torch.bfloat16)
     w = torch.zeros((8, 256), dtype=torch.bfloat16)

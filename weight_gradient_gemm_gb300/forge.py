@@ -1234,12 +1234,14 @@ def dropout(x: torch.Tensor, y: torch.Tensor, *, p: float, seed: int, offset: in
 
 def rope_frequencies(dim: int, theta: float, *, scaling: int = ROPE_SCALE_NONE,
                      factor: float = 1.0, context: float = 0.0, low: float = 1.0,
-                     high: float = 4.0, device="cuda"):
+                     high: Optional[float] = None, device="cuda"):
     """The table that rope and qk_norm_rope take for a rotation of `dim` elements (int64
     [dim / 2] on the device: turns per position as fractions of 2^64, modulo 2^64) and the
     rotated values' magnitude.  scaling: one of ROPE_SCALE_*, with its factor and, for
     LLAMA3 and YARN, the context trained on and the turns low and high between which
-    frequencies are mixed (usual: 1 and 4; YARN 1 and 32)."""
+    frequencies are mixed (high=None: the usual 4 of LLAMA3 and 32 of YARN)."""
+    if high is None:
+        high = 32.0 if scaling == ROPE_SCALE_YARN else 4.0
     s = ForgeRopeScaling(scaling, factor, context, low, high)
     table = (ctypes.c_uint64 * max(dim // 2, 1))()
     magnitude = ctypes.c_float()

@@ -247,6 +247,28 @@ def test_fp32_outputs_of_long_reductions(bt, d_out, how, tune):
     assert off <= 2.0 ** -23 * 2 / 3 * 32 + 32 * 2.0 ** -24
 
 
+@pytest.mark.parametrize("bt,d_out,how", [
+    (1, 264, {}), (40, 20000, {}), (128, 264, dict(splits=1)), (300, 520, dict(cg=1, splits=2)),
+    (300, 520, dict(cg=2)), (1000, 2056, dict(cg=2, bn=128))])
+@pytest.mark.parametrize("d_in", [512, 16384])
+def test_fp32_outputs_of_operands_of_one_sign(bt, d_out, how, d_in, tune):
+    """Products of one sign: what is cut off adds up instead of averaging out.  An instruction
+    loses between nothing and one unit in the last place of the sum so far, on average half of
+    at most 2^-23 of it; the i-th of 32 partial sums is i / 32 of the 512's, so that 512
+    elements lose 2^-24 (1 + ... + 32) / 32 = 16.5 2^-24 of their sum.  Adding the 32 sums of
+    512 in fp32 rounds the i-th time by at most 2^-24 i / 32, either way: the root of the
+    squares is 3.4 2^-24.  (1024 elements in one sum would lose twice 16.5 2^-24 less the
+    seventh part by which half a unit is below 2^-24 on average: 28.)"""
+    tune(**how)
+    g = torch.Generator().manual_seed(7)
+    X, W = (torch.randn(s, generator=g).abs().bfloat16().to(DEV) for s in ((bt, d_in), (d_out, d_in)))
+    Y = torch.empty((bt, d_out), device=DEV)
+    F.linear_bf16(X, W, Y)
+    ok()
+    want = X.double() @ W.double().t()
+    assert float((Y.double() - want).norm() / want.norm()) <= (16.5 + 3.4) * 2.0 ** -24
+
+
 @pytest.mark.parametrize("group_m", [-3, 1, 2, 64, 1000])
 def test_linear_tile_order(group_m, tune):
     """Groups of tile rows of any size (what lies outside 1..64: automatic)."""

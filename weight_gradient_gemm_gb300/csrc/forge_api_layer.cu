@@ -82,7 +82,7 @@ Span counter_span(const DropArgs& d) { return Span{d.counter, 8}; }
 //   Single CTAs with 128 outputs along M and up to 128 tokens (forge_gemm_linear_few.cu):
 //   a step of 64 of the reduction takes 512 cycles with 128 tokens, what its operands need
 //   at the 64 bytes a cycle that an SM loads.  The reduction is split over a cluster as
-//   long as its CTAs are all resident at once (`clusters`: of 1, 2, 4 and 8) and have two
+//   long as its CTAs are all resident at once (`clusters`: [i] of 2^i, i from 1) and have two
 //   steps each.  What follows takes 6000 cycles on one CTA, 5000 on two that share the
 //   epilogue, 4000 on more.
 //   Pairs with 256 tokens and bn outputs: 370 + 5 bn / 8 cycles a step (measured; 530 for
@@ -161,9 +161,9 @@ forge_status forge_linear_bf16(const void* X, const void* W, void* Y, forge_dtyp
   forge_tuning tune;
   forge_get_tuning(&tune);
   const int64_t num_kb = (d_in + 63) / 64;
-  int clusters[4];
+  int clusters[4] = {};
   const int nt = bt <= 16 ? 16 : (bt <= 32 ? 32 : (bt <= 64 ? 64 : 128));
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 1; i < 4; ++i) {
     const cudaError_t r = linear_few_clusters(nt, 1 << i, d.num_sms, &clusters[i]);
     if (r != cudaSuccess) return status(r);
   }
@@ -435,7 +435,6 @@ forge_status rope_args(const forge_heads* sets, int n, const forge_rotation* rot
     h.y_token = c.y[i].token; h.y_head = c.y[i].head;
     h.heads = tokens > 0 ? static_cast<int32_t>(s.heads) : 0;
   }
-  a->sets = n;
   a->dim = static_cast<int32_t>(head_dim);
   a->rot = rot->dim;
   a->interleaved = rot->layout == FORGE_ROPE_INTERLEAVED;
@@ -541,7 +540,6 @@ forge_status forge_rope_frequencies(int dim, double theta, const forge_rope_scal
   if (by_turns && !(s.context > 0.0 && std::isfinite(s.context) && s.low > 0.0 && s.high > s.low &&
                     std::isfinite(s.high)))
     return FORGE_ERR_HYPER;
-  if (s.kind == FORGE_ROPE_SCALE_NTK && dim <= 2) return FORGE_ERR_SHAPE;
   const double two_pi = 6.283185307179586476925286766559;
   double base = theta;
   if (s.kind == FORGE_ROPE_SCALE_NTK) base *= std::pow(s.factor, dim / (dim - 2.0));

@@ -399,7 +399,6 @@ struct HeadSet {
 };
 struct RopeArgs {
   HeadSet set[2];
-  int32_t sets;
   int32_t dim, rot, interleaved;
   int32_t gain_bf16, inverse;
   const uint64_t* freqs;         // [rot / 2] turns per position as fractions of 2^64

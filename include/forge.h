@@ -672,9 +672,13 @@ typedef struct {
  * forge_linear_bf16: the forward product of a linear layer with its epilogue,
  *   Z = X W^T + bias,   Y = residual + drop(act(Z) * mul),
  * accumulated and computed in fp32 and rounded once to each output (act is taken of the
- * unrounded Z).  The tensor core's sums are cut off rather than rounded, about 10^-9 of a sum
- * for each element; with Y in fp32 that ends after 512 elements, whose sums are added in
- * fp32, so that long reductions stay within about 5 10^-7.  X [bt, d_in], W [d_out, d_in] bf16; Y [bt, d_out] bf16 or fp32.
+ * unrounded Z).  X [bt, d_in], W [d_out, d_in] bf16; Y [bt, d_out] bf16 or fp32.
+ * The tensor core's sums are cut off rather than rounded, about 10^-9 of a sum for each
+ * element.  With Y in fp32 that ends after 512 elements, whose sums are added in fp32:
+ * measured over all outputs (the 2-norm) 5 10^-7 for random operands and 9 10^-7 where all
+ * products have one sign.  A single sum can be off by more: an instruction of 16 products
+ * loses up to one unit in the last place of the sum so far, so 2^-23 32 of its products'
+ * magnitudes, and 2^-24 of them for each 512 elements added.
  * `epilogue` (host memory, read before the call returns) may be NULL.
  * d_in, d_out multiples of 8; pointers 16-byte aligned.  Y in bf16 may be the same buffer
  * as mul or residual; otherwise no output may overlap an input or another output.  bt = 0
@@ -784,7 +788,8 @@ typedef struct {
  * head_dim is a multiple of 8, at most 256; at most 1024 heads of a kind.  Pointers of
  * heads 16-byte aligned.  y may be the same view as its own x; otherwise no output may
  * overlap an input or another output (interleaved views of one buffer, as queries and keys
- * in the fused output of their projections, do not), and no element of y may lie in two
+ * in the fused output of their projections, do not: [tokens, q and k and v heads, head_dim] or
+ * [tokens, heads, 3, head_dim]), and no element of y may lie in two
  * places.  tokens = 0 or heads = 0 does nothing.  Asynchronous on `stream`.
  */
 forge_status forge_rope(const forge_heads* sets, int n, const forge_rotation* rot, int inverse,
@@ -793,8 +798,10 @@ forge_status forge_rope(const forge_heads* sets, int n, const forge_rotation* ro
 /*
  * forge_qk_norm_rope: the RMS norm of each head, then the rotation, in one pass:
  *   m = x gain / sqrt(mean(x^2) + eps) over head_dim,   y = rotation of m,
- * in fp32, rounded once.  gain [head_dim] fp32 or bf16 (16-byte aligned), one for the
- * queries and one for the keys.  Otherwise as forge_rope; eps >= 0.
+ * in fp32, rounded once (a head whose mean square leaves fp32's range, entries above about
+ * 10^19, comes out as zeros).  gain [head_dim] fp32 or bf16 (16-byte aligned), one for the
+ * queries and one for the keys.  Otherwise as forge_rope; eps >= 0 (with 0 a head of zeros
+ * gives NaN, as the formula does).
  */
 forge_status forge_qk_norm_rope(const forge_heads* sets, int n, forge_dtype gain_dtype, float eps,
                                 const forge_rotation* rot, int64_t tokens, int64_t head_dim,

@@ -88,9 +88,9 @@ Span counter_span(const DropArgs& d) { return Span{d.counter, 8}; }
 //   Pairs with 256 tokens and bn outputs: 370 + 5 bn / 8 cycles a step (measured; 530 for
 //   bn = 256, whose products take 512), tiles in waves, the last tile's epilogue after them.
 // 333 tokens, 1032 -> 520, 7.3 us on single CTAs and 8.1 on pairs; 300, 4096 -> 1024, 9.7
-// and 17.9; 512, 4096 -> 14336, 62 and 40; 150, 4096 -> 14336, 48.6 and 26.8.
+// and 18.0; 512, 4096 -> 14336, 74 and 40; 150, 4096 -> 14336, 48.7 and 25.4.
 // Up to 128 tokens the pairs' form leaves half of its rows empty (128 tokens, 4096 ->
-// 14336, 24.0 us and 26.7), and the weight's bytes need every SM: the largest split there
+// 14336, 23.1 us and 26.0), and the weight's bytes need every SM: the largest split there
 // is.  Tiles of 128 tokens, one an SM, do not overlap one's end with the next's start:
 // where there are more than SMs the persistent pairs take them (128 tokens, 4096 -> 20480,
 // 38.6 us and 52.7, -> 57344 81.7 and 91.4, -> 131072 173 and 221); up to 64, two an SM do

@@ -86,8 +86,8 @@ __device__ __forceinline__ void bwd8(const EpiBwdArgs& a, uint4 dyv, uint4 zv, u
   if (a.dz) __stcs(reinterpret_cast<uint4*>(a.dz) + at, pack8(dz));
 }
 
-// Without dbias: vectors in memory order.  8192 x 14336 with SILU and mul, 1.17 GB, 162.5 us
-// (7.2 TB/s, three fifths of it reads).
+// Without dbias: vectors in memory order.  8192 x 14336 with SILU and mul, 1.17 GB, 171.5 us
+// (6.8 TB/s, the copy rate; three fifths of it reads).
 template <int ACT, bool MUL>
 __global__ void __launch_bounds__(256) epilogue_bwd_kernel(const EpiBwdArgs a) {
   constexpr int U = 2;
@@ -119,7 +119,10 @@ __global__ void __launch_bounds__(256) epilogue_bwd_kernel(const EpiBwdArgs a) {
 // thread adds its eight columns over its rows, and the block's sums are joined in shared
 // memory.  Up to eight runs of rows are the blocks of a cluster, whose first adds up the
 // others' sums through distributed shared memory: one launch.  More leave a partial row
-// each for a second one.
+// each for a second one.  333 x 520 with GELU and dropout 4.4 us; 2000 x 4096 with dropout
+// 18.8, 8192 x 4096 46.3 (its bytes 19.8), dbias alone 24.1 (9.9); 8192 x 14336 with SILU and
+// mul 314 (173), with GELU 225 (104): twice what the bytes take, for reasons not looked into
+// (121 registers a thread leave two blocks an SM).
 constexpr int kBiasCluster = 8;
 template <int ACT, bool MUL>
 __global__ void __launch_bounds__(256) epilogue_bwd_bias_kernel(const EpiBwdArgs a, int lanes,

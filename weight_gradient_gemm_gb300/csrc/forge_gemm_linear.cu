@@ -3,8 +3,8 @@
 // X [m, k] and W [n, k] are both K-major.  A pair of CTAs computes a tile of 256 tokens
 // x BN outputs (BN a multiple of 32 up to 256), 128 tokens each, from its own tokens and
 // half of the weight's rows each; the tile's whole reduction stays in tensor memory
-// (fp32; with Y in fp32 in parts).  Pairs are persistent and have two accumulators each, so that the epilogue
-// works on one tile while the next tile's products run.
+// (fp32; with Y in fp32 in parts).  Pairs are persistent and have two accumulators each, so
+// that the epilogue works on one tile while the next tile's products run.
 //
 // Warp roles (384 threads): warp 0 loads operand stages 64 deep with TMA, warp 1 issues
 // the MMAs, warps 4-11 are the epilogue (two per TMEM lane quadrant): a lane holds a
@@ -16,16 +16,16 @@
 // What bounds it: a stage's products take 2 BN cycles and its operands, 16 KB of tokens
 // and 64 BN bytes of weight a CTA, as long at the 64 bytes a cycle that an SM takes in;
 // for BN = 256 both take 512, and 530 were measured.  Long runs meet the power limit
-// before either (the clock falls to about 1500 MHz).  8192 tokens, 4096 -> 14336: 472 us in
-// short runs (2.04 PFLOP/s; a plain library product 465), with gate and stored Z 533, and
-// 616 to 624 without a pause, where the sustained library rate would take 563 without an
-// epilogue.  2000 tokens, 14336 -> 4096, 152 tiles of 224 on 76 pairs: 125 and 150 us.  4096
+// before either (the clock falls to about 1500 MHz).  8192 tokens, 4096 -> 14336: 472 to 483
+// us in short runs (2.0 PFLOP/s; a plain library product 465 to 472), with gate and stored Z
+// 522, and 608 to 620 without a pause, where the sustained library rate would take 563 without
+// an epilogue.  2000 tokens, 14336 -> 4096, 152 tiles of 224 on 76 pairs: 126 and 149 us.  4096
 // tokens, 4096 -> 4096: 73.4.
 // With Y in fp32 the sums of 512 elements each come out of tensor memory and are added in
 // the epilogue's registers (see kLinearChunk), 96 a thread, so that a tile has at most 192
-// outputs: 8192 tokens, 4096 -> 14336, 578 us (one sum throughout: 500 in the library, 1.6
-// 10^-5 off after 14336 elements in place of 4.8 10^-7); 4096 tokens, 4096 -> 4096, 91.7.
-// Without spills: with 40 words of them 110.
+// outputs: 8192 tokens, 4096 -> 14336, 562 to 578 us (one sum throughout: 483 to 500 in the
+// library, 1.6 10^-5 off after 14336 random elements in place of 4.8 10^-7); 4096 tokens, 4096
+// -> 4096, 90 to 92.  Without spills: with 40 words of them 110.
 // Measured and dropped: outputs through shared memory and TMA (605 us with the gate, on
 // five stages, where registers and seven stages took 550), pairs that split a reduction
 // over a cluster (256 tokens, 4096 -> 4096, 16.4 us, on single CTAs 14.3), 512 tokens a
@@ -223,10 +223,10 @@ __global__ void __launch_bounds__(kThreadsL, 1)
   if (warp == 0) {
     // -------------------------------------------------------------- producer
     if (lane == 0) {
-      // Last to leave L2: other pairs read the same operands.  (8192 tokens, 4096 ->
-      // 14336, 472 us, as evict-normal 484; 4096 tokens, 4096 -> 4096, 73.4 and 78.6.)
-      // A weight that is read once leaves first (256 tokens, 4096 -> 14336, 26.8 us, as
-      // the last 28.3).
+      // Last to leave L2: other pairs read the same operands.  (When only that was
+      // changed: 8192 tokens, 4096 -> 14336, 484 -> 472 us; 4096 tokens, 4096 -> 4096, 78.6 ->
+      // 73.4.)
+      // A weight that is read once leaves first (256 tokens, 4096 -> 14336, 28.3 -> 26.8 us).
       const uint64_t pol = l2_policy_evict_last();
       const uint64_t wpol = a.tiles_m > 1 ? pol : l2_policy_evict_first();
       uint32_t s = 0, ph = 0;   // next stage, and its phase

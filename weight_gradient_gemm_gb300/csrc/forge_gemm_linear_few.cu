@@ -3,23 +3,23 @@
 //
 // As in the 8-bit form (forge_gemm_b128_few.cu) the operands change places: 128
 // outputs lie along the MMA's M and the tokens along its N, 16 to 128 of them (more
-// tokens: several tiles of 128), and the reduction is split over the CTAs of a cluster (up to 8), which send slices of their
-// fp32 sums to the CTAs that own them through distributed shared memory; the owners
-// add them in a fixed order, apply the epilogue and store.  One launch, no workspace,
-// the same result on every run.
+// tokens: several tiles of 128), and the reduction is split over the CTAs of a cluster (up
+// to 8), which send slices of their fp32 sums to the CTAs that own them through distributed
+// shared memory; the owners add them in a fixed order, apply the epilogue and store.  One
+// launch, no workspace, the same result on every run.
 //
 // Warp roles: 0 loads (TMA), 1 issues the MMAs, from 4 on a warp takes the 32 outputs
 // of a TMEM lane quadrant and up to 32 tokens; all threads join in the end.  Every
 // wait is bounded.
 //
-// Bound by the weight's bytes: 4096 -> 14336 (117 MB, 17.3 us at 6.79 TB/s) 19.1 us for
-// one token, 20.2 for 16, 22.1 for 64, 23.5 for 128; 4096 -> 4096 (4.9) 8.5, 9.0, 10.2 and
-// 11.7, of which about 3.5 are a launch from its first load to its last store.  More
+// Bound by the weight's bytes: 4096 -> 14336 (117 MB, 17.3 us at 6.79 TB/s) 18.8 us for
+// one token (19.1 gated), 19.2 for 16, 21.3 for 64, 23.1 for 128; 4096 -> 4096 (4.9) 8.6, 9.1,
+// 10.3 and 11.8, of which about 3.5 are a launch from its first load to its last store.  More
 // tokens: by the operands at 64 bytes a cycle an SM (512 cycles a step of 128 x 128) and
-// the exchange of shares: 300 tokens, 4096 -> 1024, 9.6 us; 200, 14336 -> 4096, 31.2.  The
+// the exchange of shares: 300 tokens, 4096 -> 1024, 9.7 us; 200, 14336 -> 4096, 31.1.  The
 // shares go out as [token][output], 128 bytes a warp and store; as [output][token] in
-// stores of 16 bytes a lane the exchange cost more (333 tokens, 1032 -> 520, 9.3 us, 7.8
-// so).
+// stores of 16 bytes a lane the exchange cost more (333 tokens, 1032 -> 520, with everything,
+// 9.3 us, 7.9 so).
 #include <cuda_bf16.h>
 
 #include "forge_internal.h"
@@ -57,8 +57,8 @@ struct FewL {
 };
 
 // F32: Y in fp32, whose sums are added up in registers a few steps at a time (see
-// kLinearChunk), from two accumulators in turn.  (128 tokens, 4096 -> 14336, 25.1 us as
-// 24.3 in one sum.  A kernel of its own: as a loop of one turn it cost Y in bf16 3 to 6 %.)
+// kLinearChunk), from two accumulators in turn.  (128 tokens, 4096 -> 14336, 24.4 us; Y in
+// bf16, one sum, 23.1.  A kernel of its own: as a loop of one turn it cost Y in bf16 3 to 6 %.)
 template <int NT, bool F32>
 __global__ void __launch_bounds__(FewL<NT>::THREADS, NT <= 64 ? 2 : 1)
     gemm_linear_few_kernel(const __grid_constant__ LinearArgs a) {
@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(FewL<NT>::THREADS, NT <= 64 ? 2 : 1)
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(gbase + T::OFF_TMEM + 4);
   const WaitCtx wc{abort_flag, a.err, a.err_site, a.timeout_ns};
   // A weight that is read once passes through L2 as the first to leave it (one token,
-  // 4096 -> 14336, 19.9 us; as evict-normal 22.7).
+  // 4096 -> 14336, when only that was changed: 22.7 -> 19.9 us).
   const uint64_t wpol = a.tiles_m > 1 ? l2_policy_evict_last() : l2_policy_evict_first();
   const uint64_t xpol = l2_policy_evict_last();
 
@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(FewL<NT>::THREADS, NT <= 64 ? 2 : 1)
   tc_fence_after_sync();
   // While the kernel before still runs, the weight's first steps are asked for as far
   // as L2, where all writes meet (see forge_gemm_b128_few.cu): calls back to back on one
-  // token, 4096 -> 14336, 19.2 us with 16 steps ahead, 20.7 with eight, 21.6 with none.
+  // token, 4096 -> 14336, gated, 19.1 us with 16 steps ahead, 20.7 with eight, 21.6 with none.
   if (warp == 0 && lane == 0) {
     for (int k = kb; k < min(ke, kb + 16); ++k) tma_prefetch_l2_2d(&a.b, k * 64, tile * 128);
   }

@@ -336,7 +336,9 @@ struct EpiArgs {
 // falls short by about 10^-9 of itself for every element of the reduction (measured: 4.4
 // 10^-6 after 4096), as much as fp32 addition in any order loses after some 10^5.  A bf16
 // output does not show it; for an fp32 one the tensor core adds up this many steps of 64
-// and their sums are added in registers (512 elements: 4.7 10^-7, however many follow).
+// and their sums are added in registers.  Measured on 512 to 16384 elements, in the 2-norm:
+// 4.8 10^-7 for random products, 9.0 10^-7 where all have one sign, as much as a sum of 512
+// loses.
 constexpr int kLinearChunk = 8;
 constexpr int kMaxLinearF32 = 192;   // outputs of a pair's tile whose sums are in registers
 struct LinearArgs {

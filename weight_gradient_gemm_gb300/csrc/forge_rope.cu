@@ -21,10 +21,11 @@
 // some of them, and shared through memory of the warp's own.
 //
 // Bound by memory, and by how many loads 16 warps an SM keep in flight beside about 200
-// instructions a step (the backward pass 350).  32 + 8 heads of 128, with the time of the
-// bytes at 6.79 TB/s: 8192 tokens rotated 28.3 us (24.7), with the norm 32.2 (24.7), its
-// backward pass 48.7 (37.1; 2.2 of them the second launch); 1999 tokens 9.3, 10.5 and 16.7
-// (6.0 and 9.0); one token 2 on the device.
+// instructions a step (the backward pass 350).  32 + 8 heads of 128 that turn whole, halves,
+// with the time of the bytes at 6.79 TB/s: 8192 tokens rotated 28.4 to 29.1 us (24.7), with the
+// norm 32.1 (24.7), its backward pass 48.3 to 49.2 (37.1; 2.2 of them the second launch); 1999
+// tokens 9.3, 10.5 and 16.8 to 17.1 (6.0 and 9.0; the norm with half a head turning,
+// neighbouring pairs, 9.8); one token 2 on the device.
 // Measured and dropped: fp32 arithmetic one value at a time (it trades the packed forms'
 // moves for twice the operations: backward pass 49.6 us), four elements a vector (62),
 // a block a few tokens without a walk (31.0 rotated, 13.1 for the norm of 1999 tokens), and
@@ -43,8 +44,8 @@ namespace {
 enum RopeMode { kRope = 0, kQkNorm = 1, kQkNormBwd = 2 };
 // By mode: the steps whose loads are in flight at once, and the most steps of a chunk
 // (longer chunks form fewer sines and cosines, shorter ones leave more blocks and less to
-// wait for: norm and rotation of 1999 tokens 10.5 us with chunks of two, 11.2 of four and
-// 12.4 of eight; its backward pass 17.0, 18.0 and 20.4).
+// wait for: norm and rotation of 1999 tokens, whole heads, 10.5 us with chunks of two, 11.2 of
+// four and 12.4 of eight; its backward pass 17.0, 18.0 and 20.4).
 constexpr int kSteps[] = {4, 2, 1}, kChunk[] = {4, 2, 2};
 // Two blocks of 256 threads an SM, with up to 128 registers a thread; three, with 80,
 // spill (backward pass of 8192 tokens 82 us in place of 49).
@@ -160,7 +161,8 @@ __device__ __forceinline__ bool exists(const LanePart& p, int i, int s) {
 
 // Sine and cosine of 2 pi turn / 2^32.  The nearest quarter turn comes off exactly; for
 // the rest, |x| <= pi / 4, the Taylor series to x^9 and x^10 leave less than 2^-28 and
-// 2^-30.  (sincospi does the same for any argument: the backward pass of 8192 tokens
+// 2^-30; rounding the angle and the last operations of the series to fp32 costs more, about
+// 2^-24 in all.  (sincospi does the same for any argument: the backward pass of 8192 tokens
 // 53.9 us with it.)
 __device__ __forceinline__ void sin_cos(uint32_t turn, float& s, float& c) {
   const uint32_t quarter = (turn + 0x20000000u) >> 30;
